@@ -214,6 +214,23 @@ int tc_auto_splits_for(int64_t B, int64_t T, int64_t H, int64_t Dk, int64_t Dv) 
     p.B = B; p.T = T; p.H = H; p.Dk = Dk; p.Dv = Dv;
     return tc_auto_splits(p, sms);
 }
+int device_info(int *num_sms, unsigned int **err_word) {
+    DeviceState *st = nullptr;
+    const gla_status rc = current_device(&st);
+    *num_sms = rc == GLA_OK ? st->num_sms : 152;
+    *err_word = rc == GLA_OK ? st->err_word : nullptr;
+    return (int)rc;
+}
+int stream_workspace(cudaStream_t stream, size_t need, void **out) {
+    DeviceState *st = nullptr;
+    const gla_status rc = current_device(&st);
+    return rc == GLA_OK ? (int)library_workspace(st, stream, need, out) : (int)rc;
+}
+int launch_failed(const char *where, cudaError_t e) {
+    cudaGetLastError();
+    set_detail(where, e);
+    return (int)GLA_ERR_LAUNCH;
+}
 void set_error_detail(const char *text) { snprintf(g_detail, sizeof(g_detail), "%s", text); }
 }  // namespace gla
 
@@ -241,6 +258,7 @@ const char *gla_status_string(gla_status s) {
         case GLA_ERR_WORKSPACE: return "GLA_ERR_WORKSPACE";
         case GLA_ERR_BAD_OPTION: return "GLA_ERR_BAD_OPTION";
         case GLA_ERR_BAD_SEQLENS: return "GLA_ERR_BAD_SEQLENS";
+        case GLA_ERR_BAD_PAGES: return "GLA_ERR_BAD_PAGES";
     }
     return "GLA_ERR_UNKNOWN";
 }
@@ -519,7 +537,8 @@ gla_status gla_last_device_status(gla_stream_t stream) {
             cudaGetLastError();
             return GLA_ERR_LAUNCH;
         }
-        return (word & gla::kDevErrTimeout) ? GLA_ERR_DEVICE_TIMEOUT : GLA_ERR_BAD_SEQLENS;
+        if (word & gla::kDevErrTimeout) return GLA_ERR_DEVICE_TIMEOUT;
+        return (word & gla::kDevErrInternal) ? GLA_ERR_BAD_SEQLENS : GLA_ERR_BAD_PAGES;
     }
     return GLA_OK;
 }

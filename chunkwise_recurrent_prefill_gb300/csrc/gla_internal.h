@@ -36,11 +36,23 @@ enum : unsigned int {
     kDevErrTimeout = 1u,     // a bounded mbarrier / flag wait ran out
     kDevErrInternal = 2u,    // an input the host could not check was inconsistent (packed-
                              // sequence offsets not non-decreasing from 0 to T)
+    kDevErrPages = 4u,       // a page, slot or row number was out of range or used twice, or
+                             // no page was free
 };
 
 // Status (a gla_status value) of the current device: GLA_OK for an sm_103 device, else the
 // error gla_fwd_ex would return; probes the device once.
 int current_device_status();
+
+// The current device for the other ABI layers: its SM count and error word, with the status
+// above as the result.
+int device_info(int *num_sms, unsigned int **err_word);
+
+// The library's own workspace of `stream` on the current device (a gla_status value).
+int stream_workspace(cudaStream_t stream, size_t need, void **out);
+
+// gla_status of a failed CUDA call: clears the error and keeps its text for this thread.
+int launch_failed(const char *where, cudaError_t e);
 
 // Host-side count of kernel launches issued by the library (gla_launch_counter).
 void count_launches(unsigned n);

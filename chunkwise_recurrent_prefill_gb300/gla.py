@@ -22,7 +22,7 @@ STATUS = {
     0: "GLA_OK", 1: "GLA_ERR_NULL_ARG", 2: "GLA_ERR_BAD_SHAPE", 3: "GLA_ERR_UNSUPPORTED_DIM",
     4: "GLA_ERR_MISALIGNED", 5: "GLA_ERR_ALIAS", 6: "GLA_ERR_LAUNCH",
     7: "GLA_ERR_DEVICE_TIMEOUT", 8: "GLA_ERR_UNSUPPORTED_DEVICE", 9: "GLA_ERR_WORKSPACE",
-    10: "GLA_ERR_BAD_OPTION", 11: "GLA_ERR_BAD_SEQLENS",
+    10: "GLA_ERR_BAD_OPTION", 11: "GLA_ERR_BAD_SEQLENS", 12: "GLA_ERR_BAD_PAGES",
 }
 PATHS = {"auto": 0, "exact": 1, "tc": 2}
 GATES = {"key": 0, "scalar": 1}
@@ -40,6 +40,21 @@ class _Options(ctypes.Structure):
     _fields_ = [("path", ctypes.c_int), ("seq_splits", ctypes.c_int),
                 ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
                 ("gate", ctypes.c_int)]
+
+
+class _Strides(ctypes.Structure):
+    _fields_ = [("b", ctypes.c_int64), ("t", ctypes.c_int64), ("h", ctypes.c_int64)]
+
+
+class _HdaShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("B", "T", "H", "Hq", "Hk", "Hv", "Dk", "Dv")] + \
+        [(n, _Strides) for n in ("q", "k", "v", "d_o")] + [("io", ctypes.c_int)]
+
+
+class _NormShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("N", "L", "C", "G", "x_n", "x_l", "gate_n", "gate_l",
+                                              "dy_n", "dy_l")] + \
+        [("eps", ctypes.c_float), ("act", ctypes.c_int), ("io", ctypes.c_int)]
 
 
 _lock = threading.Lock()
@@ -92,6 +107,28 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
             lib.gdn_fwd.restype = ctypes.c_int
             lib.gdn_fwd_workspace_size.argtypes = [i64, i64, i64, i64, i64]
             lib.gdn_fwd_workspace_size.restype = ctypes.c_size_t
+            hs, ns = ctypes.POINTER(_HdaShape), ctypes.POINTER(_NormShape)
+            opt = ctypes.POINTER(_Options)
+            lib.hda_fwd.argtypes = [vp, vp, vp, vp, f32, vp, vp, vp, hs, opt, vp]
+            lib.hda_bwd.argtypes = [vp, vp, vp, vp, vp, f32] + [vp] * 6 + [hs, opt, vp]
+            lib.hda_step.argtypes = [vp, vp, vp, vp, f32, vp, vp, vp, i64, hs, vp]
+            lib.hda_path_for.argtypes = [hs, opt]
+            lib.gla_group_norm_fwd.argtypes = [vp] * 7 + [ns, vp, ctypes.c_size_t, vp]
+            lib.gla_group_norm_bwd.argtypes = [vp] * 11 + [ns, vp, ctypes.c_size_t, vp]
+            lib.gla_pages_copy.argtypes = [vp, i64, i64, vp, vp, i64, vp]
+            lib.gla_pages_fork.argtypes = [vp, i64, i64, vp, i64, i64, vp, vp, vp, vp, i64, vp]
+            lib.gla_pages_free.argtypes = [i64, vp, i64, i64, vp, vp, vp, i64, vp]
+            lib.gla_pages_compact.argtypes = [vp, i64, i64, vp, i64, i64, vp, vp, vp]
+            for f in (lib.hda_fwd, lib.hda_bwd, lib.hda_step, lib.hda_path_for,
+                      lib.gla_group_norm_fwd, lib.gla_group_norm_bwd, lib.gla_pages_copy,
+                      lib.gla_pages_fork, lib.gla_pages_free, lib.gla_pages_compact):
+                f.restype = ctypes.c_int
+            lib.hda_fwd_workspace_size.argtypes = [hs, opt]
+            lib.hda_bwd_workspace_size.argtypes = [hs, opt]
+            lib.gla_group_norm_workspace_size.argtypes = [ns, ctypes.c_int]
+            for f in (lib.hda_fwd_workspace_size, lib.hda_bwd_workspace_size,
+                      lib.gla_group_norm_workspace_size):
+                f.restype = ctypes.c_size_t
             _lib = lib
     return _lib
 

@@ -1,0 +1,93 @@
+"""Pages of a pool of states: Python binding of ``gla_pages_*`` (``include/gla.h`` has the
+contracts). All bookkeeping is int32 on the device; nothing is read back by these calls.
+
+    pool  [P, ...]  P pages (any dtype; a page is a multiple of 16 bytes)
+    table [R, M]    the pages of each row, negative where there is none
+    free  [P]       stack of free pages, ``count`` [1] of them, the top last
+"""
+from __future__ import annotations
+
+import torch
+
+from .gla import _check, _ptr, _stream_handle, load_library
+from .hda import _fail
+
+
+def _pool(pool):
+    if not isinstance(pool, torch.Tensor):
+        raise TypeError("pool must be a torch.Tensor")
+    if pool.device.type != "cuda":
+        raise ValueError("tensors must be on a CUDA device")
+    if pool.dim() < 1 or not pool.is_contiguous():
+        raise ValueError("pool must be contiguous, [P, ...]")
+    P = pool.shape[0]
+    per = 1
+    for n in pool.shape[1:]:
+        per *= n
+    return P, per * pool.element_size()
+
+
+def _ints(t, name, dev, shape=None):
+    _check(t, name, torch.int32, (t.numel(),) if shape is None else shape, dev)
+    return t
+
+
+def _book(table, free, count, P, dev):
+    if table.dim() != 2:
+        raise ValueError("table must be [R, M]")
+    _ints(table, "table", dev, tuple(table.shape))
+    _ints(free, "free", dev, (P,))
+    _ints(count, "count", dev, (1,))
+    return table.shape
+
+
+def pages_copy(pool, src, dst, *, stream=None):
+    """pool[dst[i]] = pool[src[i]] for every i whose two numbers are not negative."""
+    lib = load_library()
+    P, nb = _pool(pool)
+    n = src.numel()
+    _ints(src, "src", pool.device)
+    _ints(dst, "dst", pool.device, (n,))
+    with torch.cuda.device(pool.device):
+        rc = lib.gla_pages_copy(_ptr(pool), P, nb, _ptr(src), _ptr(dst), n, _stream_handle(stream))
+    _fail(lib, rc, "gla_pages_copy")
+
+
+def pages_fork(pool, table, free, count, parents, children, *, stream=None):
+    """Rows ``children`` become copies of rows ``parents`` on pages taken from the stack."""
+    lib = load_library()
+    P, nb = _pool(pool)
+    R, M = _book(table, free, count, P, pool.device)
+    n = parents.numel()
+    _ints(parents, "parents", pool.device)
+    _ints(children, "children", pool.device, (n,))
+    with torch.cuda.device(pool.device):
+        rc = lib.gla_pages_fork(_ptr(pool), P, nb, _ptr(table), R, M, _ptr(free), _ptr(count),
+                                _ptr(parents), _ptr(children), n, _stream_handle(stream))
+    _fail(lib, rc, "gla_pages_fork")
+
+
+def pages_free(table, free, count, rows, *, stream=None):
+    """The pages of ``rows`` go back on the stack; the rows have none afterwards."""
+    lib = load_library()
+    dev = table.device
+    if dev.type != "cuda":
+        raise ValueError("tensors must be on a CUDA device")
+    P = free.numel()
+    R, M = _book(table, free, count, P, dev)
+    _ints(rows, "rows", dev)
+    with torch.cuda.device(dev):
+        rc = lib.gla_pages_free(P, _ptr(table), R, M, _ptr(free), _ptr(count), _ptr(rows),
+                                rows.numel(), _stream_handle(stream))
+    _fail(lib, rc, "gla_pages_free")
+
+
+def pages_compact(pool, table, free, count, *, stream=None):
+    """The live pages move down to 0 .. n-1; the table follows, the stack is rebuilt."""
+    lib = load_library()
+    P, nb = _pool(pool)
+    R, M = _book(table, free, count, P, pool.device)
+    with torch.cuda.device(pool.device):
+        rc = lib.gla_pages_compact(_ptr(pool), P, nb, _ptr(table), R, M, _ptr(free), _ptr(count),
+                                   _stream_handle(stream))
+    _fail(lib, rc, "gla_pages_compact")

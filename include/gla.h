@@ -68,8 +68,11 @@ typedef enum {
     GLA_ERR_UNSUPPORTED_DEVICE = 8,/* the current device is not sm_103                */
     GLA_ERR_WORKSPACE = 9,         /* caller workspace too small or misaligned        */
     GLA_ERR_BAD_OPTION = 10,       /* an option value is out of range                 */
-    GLA_ERR_BAD_SEQLENS = 11       /* packed-sequence offsets were found inconsistent on
+    GLA_ERR_BAD_SEQLENS = 11,      /* packed-sequence offsets were found inconsistent on
                                       the device (reported by gla_last_device_status)   */
+    GLA_ERR_BAD_PAGES = 12         /* a page, slot or row number read on the device was out
+                                      of range or used twice, or no page was free (reported
+                                      by gla_last_device_status)                         */
 } gla_status;
 
 /* Which arithmetic path runs. */
@@ -190,8 +193,10 @@ int gla_path_for(int64_t B, int64_t T, int64_t H, int64_t Dk, int64_t Dv, int io
  * device error word on the current device. Returns GLA_OK, GLA_ERR_DEVICE_TIMEOUT when
  * a kernel abandoned a bounded pipeline wait (its outputs are then undefined, the
  * context stays usable), GLA_ERR_BAD_SEQLENS when gla_fwd_varlen found offsets that are
- * not non-decreasing within [0, T] (the affected sequences are left unwritten), or
- * GLA_ERR_LAUNCH when the synchronisation itself failed.
+ * not non-decreasing within [0, T] (the affected sequences are left unwritten),
+ * GLA_ERR_BAD_PAGES when hda_step or a gla_pages_ call met a number it could not use (that
+ * row or page was skipped, the others were done), or GLA_ERR_LAUNCH when the
+ * synchronisation itself failed.
  */
 gla_status gla_last_device_status(gla_stream_t stream);
 
@@ -283,6 +288,155 @@ gla_status gdn_fwd(const void *q, const void *k, const void *v, const float *g_l
                    const float *beta, float scale, const float *h0, void *o, float *hT,
                    int64_t B, int64_t T, int64_t H, int64_t Dk, int64_t Dv, int io,
                    void *workspace, size_t workspace_bytes, gla_stream_t stream);
+
+/*
+ * hda_fwd, hda_bwd, hda_step — linear attention with one fixed decay per head: the recurrence
+ * of gla_fwd with a gate that is a constant of the head instead of an input per token,
+ *     S_t = e^decay S_{t-1} + k_t^T v_t,    o_t = scale . q_t . S_t,    hT = S_T
+ * for prompts (chunkwise, forward), for training (the gradients) and for single tokens.
+ *
+ * Heads may be shared: there are H states per batch entry, and q, k, v have Hq, Hk, Hv heads,
+ * each a divisor of H; state head h reads q head h / (H / Hq), and so on. decay is [H] float32
+ * log-decays: any value <= 0, -inf among them (the state then holds the current token alone);
+ * a positive value is computed as given. It is a constant: no gradient is returned for it.
+ *
+ * q [B, T, Hq, Dk], k [B, T, Hk, Dk], v [B, T, Hv, Dv] (and d_o, shaped as o) may be strided:
+ * the last dimension is contiguous, the strides of the others are given in elements and are
+ * positive multiples of 16 bytes (so slices of one fused projection need no copy). o, the
+ * gradients and the states are contiguous: o [B, T, H, Dv]; h0, hT, dhT, dh0 [B, H, Dk, Dv]
+ * float32. bf16 or fp32 q, k, v, o, d_o and gradients, by shape->io.
+ *
+ * Dk and Dv: multiples of 8 in [8, 256]. bf16 with Dk, Dv in {64, 128} and at least 64 tokens
+ * runs on the tensor cores (GLA_PATH_TC: bf16 products, fp32 accumulation and state; the
+ * operand of the state update carries its decay in two bf16 parts, so hT and dh0 keep fp32-like
+ * accuracy); everything else runs token by token in fp32 (GLA_PATH_EXACT). Deterministic: no
+ * atomics. T = 0 gives hT = h0 (dh0 = dhT), or zero.
+ */
+typedef struct {
+    int64_t b, t, h;        /* element strides of the batch, token and head dimension   */
+} gla_strides;
+
+typedef struct {
+    int64_t B, T, H;        /* batch entries, tokens, states (and o heads) per entry    */
+    int64_t Hq, Hk, Hv;     /* heads of q, k, v: divisors of H                          */
+    int64_t Dk, Dv;
+    gla_strides q, k, v;    /* all three members zero = contiguous                      */
+    gla_strides d_o;        /* hda_bwd only                                             */
+    int io;                 /* gla_io                                                   */
+} hda_shape;
+
+/* opt: path, seq_splits (tensor cores: sequence segments per head; 0 = auto) and the workspace,
+ * as in gla_fwd_ex; its gate must be GLA_GATE_KEY (0). opt may be NULL. */
+gla_status hda_fwd(const void *q, const void *k, const void *v, const float *decay, float scale,
+                   const float *h0, void *o, float *hT, const hda_shape *shape,
+                   const gla_options *opt, gla_stream_t stream);
+
+/*
+ * hda_bwd — gradients of hda_fwd. d_o [B, T, H, Dv] is the gradient of o, dhT that of hT (NULL:
+ * none); h0 is the forward's initial state (NULL: zero). With dS the gradient of the state,
+ *     dq_t = scale . S_t . d_o_t,   dS_t = e^decay dS_{t+1} + scale . q_t^T d_o_t (dhT enters at T)
+ *     dk_t = dS_t . v_t,   dv_t = k_t . dS_t,   dh0 = e^decay dS_1
+ * Writes dq [B, T, Hq, Dk], dk [B, T, Hk, Dk], dv [B, T, Hv, Dv] (each summed in fp32 over the
+ * heads that share it) and dh0 (may be NULL). Nothing of the forward is kept: the states are
+ * computed again from q, k, v.
+ */
+gla_status hda_bwd(const void *d_o, const void *q, const void *k, const void *v,
+                   const float *decay, float scale, const float *h0, const float *dhT, void *dq,
+                   void *dk, void *dv, float *dh0, const hda_shape *shape, const gla_options *opt,
+                   gla_stream_t stream);
+
+/* Bytes of workspace hda_fwd / hda_bwd need (0 if none, or if they would reject the shape). */
+size_t hda_fwd_workspace_size(const hda_shape *shape, const gla_options *opt);
+size_t hda_bwd_workspace_size(const hda_shape *shape, const gla_options *opt);
+
+/* The path hda_fwd and hda_bwd would run: GLA_PATH_EXACT, GLA_PATH_TC, or -1 (rejected). */
+int hda_path_for(const hda_shape *shape, const gla_options *opt);
+
+/*
+ * hda_step — one token for each of shape->B rows on a pool of states, S [P, H, Dk, Dv] float32,
+ * updated in place: row r uses page slots[r] (int32 on the device; NULL: page r, P >= B). A
+ * negative slot is an empty row: its o is zero and no page is touched. A slot >= P is reported
+ * as GLA_ERR_BAD_PAGES and treated as an empty row. No page may be listed twice: its state
+ * would be undefined. q, k, v are [B, heads, D] with the strides b and h of shape (T and the t
+ * strides are ignored); o [B, H, Dv]. Dk in [1, 1024], Dv a multiple of 4 in [4, 1024]; no
+ * strides but multiples of 16 bytes.
+ */
+gla_status hda_step(const void *q, const void *k, const void *v, const float *decay, float scale,
+                    float *S, const int32_t *slots, void *o, int64_t P, const hda_shape *shape,
+                    gla_stream_t stream);
+
+/*
+ * gla_group_norm_fwd, gla_group_norm_bwd — group norm, channels last, with an activation: the
+ * norm over each head that follows the attention (L = 1: one token per entry, G = heads), and
+ * the norm over whole feature maps (L positions). x [N, L, C] in G groups of C / G channels:
+ *     mean, var over the L positions and the group's channels;  rstd = (var + eps)^-1/2
+ *     u = (x - mean) rstd w + b
+ *     y = act(u)                       without a gate
+ *     y = u act(gate)                  with one (gate [N, L, C])
+ * act: identity, silu(u) = u / (1 + e^-u), or gelu(u) = u Phi(u). w, b: [C] float32 or NULL
+ * (1 and 0). mean, rstd [N, G] float32. x, gate, dy may be strided: contiguous channels, the
+ * strides of N and L in elements; y, dx, dgate are contiguous. Any C that G divides. bf16 or
+ * fp32 tensors (io); fp32 statistics and sums, combined in a fixed order (deterministic).
+ * The variance is taken from deviations from the mean of each part (never as a difference
+ * of squares). dw, db [C] float32 (may be NULL); dgate with a gate only.
+ */
+typedef enum { GLA_ACT_NONE = 0, GLA_ACT_SILU = 1, GLA_ACT_GELU = 2 } gla_act;
+
+typedef struct {
+    int64_t N, L, C, G;
+    int64_t x_n, x_l;          /* element strides of x, gate, dy: both zero = contiguous  */
+    int64_t gate_n, gate_l;
+    int64_t dy_n, dy_l;
+    float eps;
+    int act;                   /* gla_act */
+    int io;                    /* gla_io  */
+} gla_norm_shape;
+
+/* y, mean, rstd are written; mean and rstd may be NULL when no backward pass follows. */
+gla_status gla_group_norm_fwd(const void *x, const float *w, const float *b, const void *gate,
+                              void *y, float *mean, float *rstd, const gla_norm_shape *shape,
+                              void *workspace, size_t workspace_bytes, gla_stream_t stream);
+gla_status gla_group_norm_bwd(const void *dy, const void *x, const float *mean, const float *rstd,
+                              const float *w, const float *b, const void *gate, void *dx,
+                              float *dw, float *db, void *dgate, const gla_norm_shape *shape,
+                              void *workspace, size_t workspace_bytes, gla_stream_t stream);
+/* Bytes of workspace the two calls need; NULL uses the library's workspace of the stream. */
+size_t gla_group_norm_workspace_size(const gla_norm_shape *shape, int backward);
+
+/*
+ * gla_pages_* — the pages of a cache whose pages are owned by one row each (recurrent states:
+ * every step rewrites the whole page, so rows cannot share one).
+ *     pool  : P pages of page_bytes bytes (a multiple of 16)
+ *     table : int32 [R, M], the M pages of each of R rows (one per layer, say); negative = none
+ *     free  : int32 [P], a stack of free pages; free[0 .. count-1] are valid, the top is last
+ *     count : int32 [1], pages on the stack
+ * All of it lives on the device and nothing is read back: calls may follow one another on a
+ * stream, or in a CUDA graph, without a host round trip. Results are those of going through the
+ * requests in order, one at a time. A number out of range, and what is said below, raises
+ * GLA_ERR_BAD_PAGES (gla_last_device_status) and skips that request; the others are done.
+ *
+ * copy    : page src[i] to page dst[i], i < n; a negative number in either skips i. No dst may
+ *           be listed twice, nor as a src of another i.
+ * fork    : row children[i] becomes a copy of row parents[i] on pages taken from the stack, in
+ *           the order of (i, m); negative numbers skip i. A child must have no pages, and of the
+ *           requests that name the same child the first counts and the others are in error.
+ *           Parents are read as they were before the call. When the stack runs out, the remaining entries become -1 and the error is raised.
+ * free    : the pages of rows[i] go back on the stack and the rows' entries become -1; a row
+ *           listed again has none left. Pages are pushed last to first, so that freeing what
+ *           a fork took, in the same order, restores the stack.
+ * compact : the live pages (those in the table) at or above their count n move down into the
+ *           holes below n, the i-th such page into the i-th hole; the table follows, and the
+ *           stack becomes P-1, ..., n (top last; the rest of free is set to -1).
+ */
+gla_status gla_pages_copy(void *pool, int64_t P, int64_t page_bytes, const int32_t *src,
+                          const int32_t *dst, int64_t n, gla_stream_t stream);
+gla_status gla_pages_fork(void *pool, int64_t P, int64_t page_bytes, int32_t *table, int64_t R,
+                          int64_t M, int32_t *free_stack, int32_t *count, const int32_t *parents,
+                          const int32_t *children, int64_t n, gla_stream_t stream);
+gla_status gla_pages_free(int64_t P, int32_t *table, int64_t R, int64_t M, int32_t *free_stack,
+                          int32_t *count, const int32_t *rows, int64_t n, gla_stream_t stream);
+gla_status gla_pages_compact(void *pool, int64_t P, int64_t page_bytes, int32_t *table, int64_t R,
+                             int64_t M, int32_t *free_stack, int32_t *count, gla_stream_t stream);
 
 /* Library ABI version: major * 10000 + minor * 100 + patch. */
 int gla_version(void);
