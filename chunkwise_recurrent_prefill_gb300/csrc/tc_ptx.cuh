@@ -168,6 +168,12 @@ __device__ __forceinline__ uint64_t l2_policy_evict_first() {
     return p;
 }
 
+__device__ __forceinline__ uint64_t l2_policy_evict_normal() {
+    uint64_t p;
+    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+
 // tma_load_4d with an L2 cache policy.
 __device__ __forceinline__ void tma_load_4d_hint(void *dst, const void *tmap, uint64_t *bar,
                                                  int c0, int c1, int c2, int c3, uint64_t pol) {
