@@ -2,19 +2,25 @@
 // tcgen05 MMAs with TMEM accumulators, fp32 state in TMEM, warp-specialised roles.
 //
 // One map serves the forward and the three gradients (hda_internal.h). Per chunk of n = 64
-// tokens (fewer at the end), with l = e^decay and the state S before the chunk:
+// tokens (fewer at the end of the walk), with l = e^decay and the state S before the chunk:
 //     P   = (X Y^T) . M,                  M_ij = l^|i-j| for j <= i (j >= i reversed), else 0
-//     out = P Z + diag(f) X S,            f_i = l^(i+1)      (reversed: l^(n-1-i))
-//     S  <- l^n S + Y^T diag(u) Z,        u_j = l^(n-1-j)    (reversed: l^(j+1))
-// Every factor is a power with an exponent >= 0, so for decays <= 0 none overflows, whatever
-// their strength; a constant decay makes M, f and u the same in every chunk. The kernels work
-// on the transposes (out^T = Z^T P^T + S^T X^T diag(f), S^T += (diag(u) Z)^T Y): the state and
-// the output then have M = 128 lanes, and S^T is an A operand straight from TMEM.
+//     out = P Z + diag(f) X S,            f_i = l^(i+1)      (reversed: l^(63-i))
+//     S  <- l^n S + Y^T diag(u) Z,        u_j = l^(n-1-j)    (reversed: l^(j+1), less the rows
+//                                                             that a short chunk lacks)
+// A constant decay makes M, f and u the same in every chunk. The kernels work on the transposes
+// (out^T = Z^T P^T + S^T X^T diag(f), S^T += (diag(u) Z)^T Y): the state and the output then have
+// M = 128 lanes, and S^T is an A operand straight from TMEM.
+//
+// Both terms of the output share one accumulator: out = diag(F) ((P / F) Z + X S) with
+// F_i = max(f_i, 2^-60). The scores' factors M_ij / F_i stay below 2^60 (every other factor is a
+// power with an exponent >= 0), so no decay overflows; where F_i is not f_i, X S counts 2^-60
+// instead of less, which no output's 2^-9 can tell.
 //
 // Roundings to bf16: the operands themselves are bf16. P is rounded once after the mask, S once
-// per chunk for its product with X (both end in an output that is bf16 itself). diag(u) Z is
-// carried as a sum of two bf16 parts (2^-16 of a value is lost), because it goes into the fp32
-// state that the caller gets back: with one part hT would be off by 2^-9.
+// per chunk for its product with X, and diag(u) Z once for the update of a state that only such
+// outputs read (they are bf16 themselves). A state that the caller gets back in fp32 is updated
+// with diag(u) Z as a sum of three bf16 parts, which leaves nothing out of 24 bits: one part
+// would leave hT off by 2^-9 of a term, two by 2^-18 (3e-6 of hT, measured, against 3e-7).
 //
 // When there are fewer heads than SMs, each head's chunks are split into segments:
 //   hda_tc_state_kernel : pieces of the segments but the last -> their end state from zero, E
@@ -37,6 +43,7 @@ namespace {
 using namespace tc;
 
 constexpr int kC = 64;              // tokens of a chunk
+constexpr float kLeastF = 0x1p-60f; // least output factor
 constexpr int kMaxSplits = 256;
 constexpr int kMaxPieces = 8;
 
@@ -74,7 +81,8 @@ struct TcArgs {
 };
 
 struct TcMaps {
-    CUtensorMap x[3], y[3], z[3];
+    CUtensorMap x[3], y[3], z[3];   // loads: boxes of 64 columns, 64 tokens
+    CUtensorMap o[3];               // stores: boxes of 32 columns (make_out_map)
 };
 
 // Chunks of segment `seg`, in the order of the walk.
@@ -82,13 +90,20 @@ __host__ __device__ __forceinline__ int seg_bound(int seg, int nchunks, int spli
     return (int)((int64_t)seg * nchunks / splits);
 }
 
-// Chunk at position p of the walk, and its tokens.
-__device__ __forceinline__ int walk_chunk(int p, int nchunks, int rev) {
-    return rev ? nchunks - 1 - p : p;
+// Chunk p of the walk: its first token and how many it has. A reversed walk counts its chunks from
+// the end, so that here too only the last one is short; its first rows, before token 0, are read
+// as zeros.
+__device__ __forceinline__ int chunk_start(int p, const TcArgs &a, int rev) {
+    return rev ? (int)a.T - kC * (p + 1) : kC * p;
 }
-__device__ __forceinline__ int chunk_tokens(int c, int64_t T) {
-    const int64_t left = T - (int64_t)c * kC;
-    return left < kC ? (int)left : kC;
+__device__ __forceinline__ int chunk_tokens(int p, const TcArgs &a) {
+    const int left = (int)a.T - kC * p;
+    return left < kC ? left : kC;
+}
+// u_j of a chunk of nt tokens, from the powers pw.
+__device__ __forceinline__ float state_factor(const float *pw, int row, int nt, int rev) {
+    const int e = rev ? row - (kC - nt) + 1 : nt - 1 - row;
+    return (rev ? e > 0 : e >= 0) ? pw[e] : 0.f;
 }
 
 __device__ __forceinline__ uint8_t *align1024(uint8_t *p) {
@@ -96,7 +111,83 @@ __device__ __forceinline__ uint8_t *align1024(uint8_t *p) {
 }
 __device__ __forceinline__ uint32_t par(int use) { return (uint32_t)use & 1u; }
 
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&out)[32]) {
+// mbar_wait (bounded) that does not look at the clock until it has tried for a while: reading the
+// global timer at every wait that does not succeed at once cost the roles here hundreds of cycles.
+__device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity) {
+#pragma unroll 1
+    for (int i = 0; i < 128; ++i)
+        if (mbar_try_wait(bar, parity)) return true;
+    return mbar_wait(bar, parity);
+}
+
+// The tile [64 tokens][D] of one head: one or two 128B-swizzled boxes of 64 columns, 8 KB each.
+__device__ __forceinline__ void load_tile(uint8_t *dst, const CUtensorMap *m, uint64_t *bar, int D,
+                                          int h, int t, int b, uint64_t pol) {
+    tma_load_4d_hint(dst, m, bar, 0, h, t, b, pol);
+    if (D > 64) tma_load_4d_hint(dst + 8192, m, bar, 64, h, t, b, pol);
+}
+
+// 16 bytes of Z (8 values of one token) times the token's factor, as kParts bf16 parts 16 KB
+// apart.
+template <int kParts>
+__device__ __forceinline__ void put_scaled(uint4 v, float u, uint4 *dst) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    float2 p[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p[i] = mul2(unpack_bf16(w[i]), make_float2(u, u));
+#pragma unroll
+    for (int part = 0; part < kParts; ++part) {
+        uint32_t o[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            o[i] = pack_bf16(p[i].x, p[i].y);
+            const float2 r = unpack_bf16(o[i]);
+            p[i] = make_float2(p[i].x - r.x, p[i].y - r.y);
+        }
+        dst[part * 1024] = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+}
+
+// ======================================================================= output kernel
+namespace om {
+constexpr int NQ = 3;                            // stages of x, y, z tiles
+constexpr uint32_t X = 0, Y = 16384, Z = 32768, STAGE = 49152;
+constexpr uint32_t ZP = NQ * STAGE;              // diag(u) Z: three buffers, or one of three parts
+constexpr uint32_t P = ZP + 3 * 16384;           // two [64 x 64] bf16 tiles, 128B swizzle
+constexpr uint32_t OUT = P + 2 * 8192;           // a [64 x 32] bf16 (or [32 x 32] f32) tile per warp
+constexpr uint32_t PW = OUT + 4 * 4096;          // [65] f32 powers l^0 .. l^64
+constexpr uint32_t FA = PW + 320;                // [64] f32 output factors a_out F_i
+constexpr uint32_t FU = FA + 256;                // [64] f32 state factors a_in u_j of a full chunk
+constexpr uint32_t FUL = FU + 256;               // the same of the last chunk of the walk
+constexpr uint32_t BAR = FUL + 256;
+constexpr uint32_t NBAR = 26;
+constexpr uint32_t TSLOT = BAR + NBAR * 8;
+constexpr uint32_t ALLOC = TSLOT + 16 + 1024;
+static_assert(ALLOC <= 232448, "output kernel shared memory");
+constexpr uint32_t COL_S = 0;                    // S^T fp32: lane z, column x
+constexpr uint32_t COL_D = 128;                  // a chunk's (diag(u) Z)^T Y, the same way
+constexpr uint32_t COL_P = 256;                  // X Y^T (M = 64 layout)
+constexpr uint32_t COL_O = 320;                  // S^T X^T + Z^T P^T: two of 64 columns
+constexpr uint32_t COL_SB = 448;                 // bf16 snapshot of S^T
+}  // namespace om
+
+// Barriers. Where a producer may run two phases ahead of a waiter, the phases alternate between
+// the barriers of the buffers (ZDONE, ZFREE, PBF, OFULL, OFREE); elsewhere the next phase needs the
+// waiter's own arrival.
+enum {
+    QFULL = 0, QEMPTY = 3, ZDONE = 6, ZFREE = 9, PBF = 12, OFULL = 14, OFREE = 16, PFULL = 18,
+    PFREE = 19, SREADY = 20, SBFREE = 21, UDONE = 22, FIN = 23,
+};
+static_assert(FIN < (int)om::NBAR, "output kernel barrier map");
+// Warps: 0 TMA, 1 MMA, 2-5 output, 6-9 state, 10-13 P, 14-17 diag(u) Z. Every role has a loop of its
+// own, since what it does in a chunk is mostly waiting for barriers, TMEM and fences one after
+// another; and the loops are kept short, since five different ones share the instruction cache of
+// each quarter of the SM (28 warps with the state in registers, and unrolled loops, both ran slower).
+constexpr int kOutWarps = 18;
+constexpr int kOutThreads = kOutWarps * 32;
+
+// 32 lanes x 32 columns of fp32 accumulators -> 32 floats.
+__device__ __forceinline__ void tmem_ld32f(uint32_t taddr, float (&out)[32]) {
     uint32_t r0[16], r1[16];
     tmem_ld16(taddr, r0);
     tmem_ld16(taddr + 16, r1);
@@ -109,59 +200,6 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&out)[32]) {
         out[16 + x] = __uint_as_float(r1[x]);
     }
 }
-
-// The tile [64 tokens][D] of one head: one or two 128B-swizzled boxes of 64 columns, 8 KB each.
-__device__ __forceinline__ void load_tile(uint8_t *dst, const CUtensorMap *m, uint64_t *bar, int D,
-                                          int h, int t, int b, uint64_t pol) {
-    tma_load_4d_hint(dst, m, bar, 0, h, t, b, pol);
-    if (D > 64) tma_load_4d_hint(dst + 8192, m, bar, 64, h, t, b, pol);
-}
-
-// 16 bytes of Z (8 values of one token) times the token's factor, as two bf16 parts.
-__device__ __forceinline__ void split8(uint4 v, float u, uint4 &hi, uint4 &lo) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    uint32_t h[4], l[4];
-    const float2 uu = make_float2(u, u);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 p = mul2(unpack_bf16(w[i]), uu);
-        h[i] = pack_bf16(p.x, p.y);
-        const float2 r = unpack_bf16(h[i]);
-        l[i] = pack_bf16(p.x - r.x, p.y - r.y);
-    }
-    hi = make_uint4(h[0], h[1], h[2], h[3]);
-    lo = make_uint4(l[0], l[1], l[2], l[3]);
-}
-
-// ======================================================================= output kernel
-namespace om {
-constexpr int NQ = 3;                            // stages of x, y, z tiles
-constexpr uint32_t X = 0, Y = 16384, Z = 32768, STAGE = 49152;
-constexpr uint32_t ZP = NQ * STAGE;              // two buffers of diag(u) Z: high, low part
-constexpr uint32_t ZPSTAGE = 32768;
-constexpr uint32_t P = ZP + 2 * ZPSTAGE;         // [64 x 64] bf16, 128B swizzle
-constexpr uint32_t PW = P + 8192;                // [65] f32 powers l^0 .. l^64
-constexpr uint32_t FA = PW + 320;                // [128] f32 output factors a_out f_i
-constexpr uint32_t BAR = FA + 512;
-constexpr uint32_t NBAR = 24;
-constexpr uint32_t TSLOT = BAR + NBAR * 8;
-constexpr uint32_t ALLOC = TSLOT + 16 + 1024;
-static_assert(ALLOC <= 232448, "output kernel shared memory");
-constexpr uint32_t COL_S = 0;                    // S^T fp32, 128 columns (lane z, column x)
-constexpr uint32_t COL_SB = 128;                 // its bf16 snapshots, 2 x 64
-constexpr uint32_t COL_P = 256;                  // X Y^T (M = 64 layout)
-constexpr uint32_t COL_OI = 320;                 // S^T X^T
-constexpr uint32_t COL_OA = 384;                 // Z^T P^T
-}  // namespace om
-
-// Barriers. Where a producer may run two phases ahead of a waiter, the phases alternate between
-// two barriers (ZDONE, ZFREE, SBFREE); elsewhere the next phase needs the waiter's own arrival.
-enum {
-    QFULL = 0, QEMPTY = 3, ZDONE = 6, ZFREE = 8, SBFREE = 10, PFULL = 12, PFREE = 13, PBF = 14,
-    SREADY = 15, UDONE = 16, OFULL = 17, OFREE = 18, FIN = 19,
-};
-constexpr int kOutWarps = 14;   // 0 TMA, 1 MMA, 2-5 output, 6-9 state, 10-13 P and diag(u) Z
-constexpr int kOutThreads = kOutWarps * 32;
 
 __global__ void __launch_bounds__(kOutThreads, 1)
 hda_tc_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ TcArgs a) {
@@ -183,32 +221,36 @@ hda_tc_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ T
     const int rev = m.rev, Dx = m.Dx, Dz = m.Dz;
     const int cb = seg_bound(seg, a.nchunks, a.splits);
     const int n = seg_bound(seg + 1, a.nchunks, a.splits) - cb;
-    auto chunk = [&](int c) { return walk_chunk(cb + c, a.nchunks, rev); };
     const float g = a.decay[h];
+    // the segment that returns the state updates it in three parts, through one buffer
+    const bool exact = m.fin && seg == a.splits - 1;
+    const int nzb = exact ? 1 : 3;      // buffers of diag(u) Z
 
     if (threadIdx.x < 128) {
         const int i = threadIdx.x;
         if (i <= kC) pw[i] = decay_pow(g, (float)i);
-        // forwards f_i = l^(i+1); reversed f_i = l^(n-1-i) = entry i + 64 - n of l^63 .. l^0
-        fa[i] = i >= kC ? 0.f : m.a_out * decay_pow(g, (float)(rev ? kC - 1 - i : i + 1));
+        if (i < kC)
+            fa[i] = m.a_out * fmaxf(decay_pow(g, (float)(rev ? kC - 1 - i : i + 1)), kLeastF);
     }
     if (threadIdx.x == 0) {
         for (int i = 0; i < NQ; ++i) {
             mbar_init(&bars[QFULL + i], 1);
             mbar_init(&bars[QEMPTY + i], 1);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < 3; ++i) {
             mbar_init(&bars[ZDONE + i], 4);
             mbar_init(&bars[ZFREE + i], 1);
-            mbar_init(&bars[SBFREE + i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bars[PBF + i], 4);
+            mbar_init(&bars[OFULL + i], 1);
+            mbar_init(&bars[OFREE + i], 4);
         }
         mbar_init(&bars[PFULL], 1);
         mbar_init(&bars[PFREE], 4);
-        mbar_init(&bars[PBF], 4);
         mbar_init(&bars[SREADY], 4);
+        mbar_init(&bars[SBFREE], 1);
         mbar_init(&bars[UDONE], 1);
-        mbar_init(&bars[OFULL], 1);
-        mbar_init(&bars[OFREE], 4);
         mbar_init(&bars[FIN], 1);
         fence_mbar_init();
     }
@@ -216,29 +258,37 @@ hda_tc_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ T
         tma_prefetch_desc(&maps.x[li]);
         tma_prefetch_desc(&maps.y[li]);
         tma_prefetch_desc(&maps.z[li]);
+        tma_prefetch_desc(&maps.o[li]);
     }
     if (warp == 1) tmem_alloc(tslot, 512);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    if (threadIdx.x < 2 * kC) {     // the factors of a full chunk, then those of the last one
+        const int i = threadIdx.x & (kC - 1);
+        const int nt = threadIdx.x < kC ? kC : chunk_tokens(a.nchunks - 1, a);
+        reinterpret_cast<float *>(sm + FU)[threadIdx.x] = m.a_in * state_factor(pw, i, nt, rev);
+    }
+    __syncthreads();
     const uint32_t tm = *tslot;
     bool ok = true;
+    const int j = warp & 3;     // the warp's quarter of the TMEM lanes
 
     if (warp == 0) {
-        // ------------------------------------------------------------ TMA producer
         if (lane == 0) {
+        // ------------------------------------------------------------ TMA producer
             const uint64_t pol = a.hint ? l2_policy_evict_first() : l2_policy_evict_normal();
             const uint32_t bytes = (uint32_t)(2 * Dx + Dz) * 2 * kC;
             int c = 0;
             for (; c < n; ++c) {
                 const int s = c % NQ;
-                if (c >= NQ && !mbar_wait(&bars[QEMPTY + s], par(c / NQ - 1))) {
+                if (c >= NQ && !wait_bar(&bars[QEMPTY + s], par(c / NQ - 1))) {
                     ok = false;
                     break;
                 }
                 uint8_t *base = sm + s * STAGE;
                 uint64_t *fb = &bars[QFULL + s];
-                const int t = chunk(c) * kC;
+                const int t = chunk_start(cb + c, a, rev);
                 mbar_arrive_expect_tx(fb, bytes);
                 load_tile(base + X, &maps.x[li], fb, Dx, h / m.hx, t, b, pol);
                 load_tile(base + Y, &maps.y[li], fb, Dx, h / m.hy, t, b, pol);
@@ -247,300 +297,390 @@ hda_tc_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ T
             // never leave with a copy still landing in this CTA's shared memory
             for (int i = 0; i < NQ; ++i) {
                 const int uses = c > i ? (c - 1 - i) / NQ + 1 : 0;
-                if (uses > 0 && !mbar_wait(&bars[QFULL + i], par(uses - 1))) ok = false;
+                if (uses > 0 && !wait_bar(&bars[QFULL + i], par(uses - 1))) ok = false;
             }
         }
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
-        // Three groups per chunk, each issued once its inputs are ready:
-        //   U(c): snapshot of S taken, S decayed, diag(u) Z written  -> S^T += (diag(u) Z)^T Y
-        //   P(c): tiles landed, P(c - 1) read                        -> X Y^T
-        //   O(c): P tile written, O(c - 1) read                      -> S^T X^T, Z^T P^T
-        // Lane 0's view of the barriers decides for the warp; one elected lane issues.
+        // Four groups per chunk, in a fixed order that the other roles keep up with:
+        //   U(c)    : D(c - 1) read, diag(u) Z written -> D = (diag(u) Z)^T Y
+        //   I(c)    : snapshot of S taken, out(c - 2) read -> O = S^T X^T
+        //   P(c + 1): tiles landed, P(c) read -> X Y^T
+        //   A(c)    : P tile written -> O += Z^T P^T; the stage has no reader left
+        // The warp waits converged, then one elected lane issues. Issuing is what this warp's
+        // time goes to, so the operand descriptors are made once: a tile further on is an
+        // addition to the address field (in 16-byte units; the field does not overflow).
         const uint32_t idP = idesc_bf16(64, 64, 0, 0);
         const uint32_t idU = idesc_bf16(128, Dx, 1, 1);
         const uint32_t idOa = idesc_bf16(128, 64, 1, 0);
         const uint32_t idOi = idesc_bf16(128, 64, 0, 0);
-        const int kx = Dx / 16;
-        int np = 0, nu = 0, no = 0;
-        uint32_t idle = 0;
-        uint64_t t_idle = 0;
-        while (no < n) {
-            bool prog = false;
-            if (__shfl_sync(0xffffffffu, nu < n && mbar_test(&bars[SREADY], par(nu)) &&
-                                             mbar_test(&bars[ZDONE + (nu & 1)], par(nu >> 1)), 0)) {
-                tc_fence_after();
-                const uint32_t y = smem_u32(sm + (nu % NQ) * STAGE + Y);
-                const uint32_t zp = smem_u32(sm + ZP + (nu & 1) * ZPSTAGE);
-                if (elect_one()) {
+        const uint32_t s0 = smem_u32(sm);
+        const uint64_t dX = smem_desc(s0 + X, 16, 1024), dY = smem_desc(s0 + Y, 16, 1024);
+        const uint64_t dYt = smem_desc(s0 + Y, 8192, 1024), dZt = smem_desc(s0 + Z, 8192, 1024);
+        const uint64_t dZP = smem_desc(s0 + ZP, 8192, 1024), dP = smem_desc(s0 + P, 16, 1024);
+        // K-major operands: 16 columns of a 64-column box are 32 bytes, the boxes 8 KB apart
+        auto koff = [](int x) { return (uint64_t)((x >> 2) * (8192 >> 4) + (x & 3) * (32 >> 4)); };
+        const bool wide = Dx > 64;
+        auto issue_P = [&](int s) {
+            const uint64_t x0 = dX + (uint64_t)(s * (STAGE >> 4)), y0 = dY + (uint64_t)(s * (STAGE >> 4));
 #pragma unroll
-                    for (int part = 0; part < 2; ++part)
+            for (int x = 0; x < 4; ++x) mma_ss(tm + COL_P, x0 + koff(x), y0 + koff(x), idP, x > 0);
+            if (wide) {
 #pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            mma_ss(tm + COL_S, smem_desc(zp + part * 16384 + kk * 2048, 8192, 1024),
-                                   smem_desc(y + kk * 2048, 8192, 1024), idU, 1);
-                    mma_commit(&bars[UDONE]);
-                    mma_commit(&bars[ZFREE + (nu & 1)]);
-                }
-                __syncwarp();
-                ++nu;
-                prog = true;
+                for (int x = 4; x < 8; ++x) mma_ss(tm + COL_P, x0 + koff(x), y0 + koff(x), idP, 1);
             }
-            if (__shfl_sync(0xffffffffu, np < n && mbar_test(&bars[QFULL + np % NQ], par(np / NQ)) &&
-                                             (np == 0 || mbar_test(&bars[PFREE], par(np - 1))), 0)) {
-                tc_fence_after();
-                const uint32_t base = smem_u32(sm + (np % NQ) * STAGE);
-                if (elect_one()) {
-                    for (int x = 0; x < kx; ++x) {
-                        const uint32_t off = (x >> 2) * 8192 + (x & 3) * 32;
-                        mma_ss(tm + COL_P, smem_desc(base + X + off, 16, 1024),
-                               smem_desc(base + Y + off, 16, 1024), idP, x > 0);
-                    }
-                    mma_commit(&bars[PFULL]);
-                }
-                __syncwarp();
-                ++np;
-                prog = true;
-            }
-            if (__shfl_sync(0xffffffffu, no < nu && mbar_test(&bars[PBF], par(no)) &&
-                                             (no == 0 || mbar_test(&bars[OFREE], par(no - 1))), 0)) {
-                tc_fence_after();
-                const uint32_t base = smem_u32(sm + (no % NQ) * STAGE);
-                const uint32_t pt = smem_u32(sm + P);
-                if (elect_one()) {
-                    for (int x = 0; x < kx; ++x)
-                        mma_ts(tm + COL_OI, tm + COL_SB + (no & 1) * 64 + x * 8,
-                               smem_desc(base + X + (x >> 2) * 8192 + (x & 3) * 32, 16, 1024), idOi,
-                               x > 0);
+            mma_commit(&bars[PFULL]);
+        };
+        bool w = wait_bar(&bars[QFULL], 0);
+        ok = __all_sync(0xffffffffu, w);
+        if (ok) {
+            tc_fence_after();
+            if (elect_one()) issue_P(0);
+            __syncwarp();
+        }
+        int zb = 0, zuse = 0;       // buffer of diag(u) Z of chunk c, and how often it was used before
+        for (int c = 0, s = 0; ok && c < n; ++c) {
+            const uint64_t so = (uint64_t)(s * (STAGE >> 4));
+            w = wait_bar(&bars[SREADY], par(c)) && wait_bar(&bars[ZDONE + zb], par(zuse));
+            if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
+            tc_fence_after();
+            if (elect_one()) {
+                const uint64_t y0 = dYt + so, z0 = dZP + (uint64_t)(zb * (16384 >> 4));
+                // the small parts first: the accumulator drops the bits below its own last one
+                // at every step, so the fewer steps it is large in, the better
+                if (exact) {
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        mma_ss(tm + COL_OA, smem_desc(base + Z + kk * 2048, 8192, 1024),
-                               smem_desc(pt + kk * 32, 16, 1024), idOa, kk > 0);
-                    mma_commit(&bars[OFULL]);
-                    mma_commit(&bars[SBFREE + (no & 1)]);
-                    // U(no) and P(no) were issued before: the stage has no reader left
-                    mma_commit(&bars[QEMPTY + no % NQ]);
+                    for (int kk = 0; kk < 8; ++kk)
+                        mma_ss(tm + COL_D, z0 + (2 - (kk >> 2)) * (16384 >> 4) + (kk & 3) * (2048 >> 4),
+                               y0 + (kk & 3) * (2048 >> 4), idU, kk > 0);
                 }
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    mma_ss(tm + COL_D, z0 + kk * (2048 >> 4), y0 + kk * (2048 >> 4), idU, exact || kk > 0);
+                mma_commit(&bars[UDONE]);
+                mma_commit(&bars[ZFREE + zb]);
+            }
+            __syncwarp();
+            if (++zb == nzb) {
+                zb = 0;
+                ++zuse;
+            }
+            const uint32_t o = tm + COL_O + (c & 1) * 64;
+            w = c < 2 || wait_bar(&bars[OFREE + (c & 1)], par((c >> 1) - 1));
+            if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
+            tc_fence_after();
+            if (elect_one()) {
+                const uint64_t x0 = dX + so;
+                const uint32_t sb = tm + COL_SB;
+#pragma unroll
+                for (int x = 0; x < 4; ++x) mma_ts(o, sb + x * 8, x0 + koff(x), idOi, x > 0);
+                if (wide) {
+#pragma unroll
+                    for (int x = 4; x < 8; ++x) mma_ts(o, sb + x * 8, x0 + koff(x), idOi, 1);
+                }
+                mma_commit(&bars[SBFREE]);
+            }
+            __syncwarp();
+            const int s1 = s + 1 == NQ ? 0 : s + 1;
+            if (c + 1 < n) {
+                w = wait_bar(&bars[QFULL + s1], par((c + 1) / NQ)) && wait_bar(&bars[PFREE], par(c));
+                if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
+                tc_fence_after();
+                if (elect_one()) issue_P(s1);
                 __syncwarp();
-                ++no;
-                prog = true;
             }
-            if (prog) {
-                idle = 0;
-            } else {
-                __nanosleep(32);    // leave the issue slots to the other warps
-                if (++idle == 256) {
-                    t_idle = global_ns();
-                } else if ((idle & 1023) == 0 &&
-                           __shfl_sync(0xffffffffu, global_ns() - t_idle > kWaitLimitNs, 0)) {
-                    ok = false;
-                    break;
-                }
+            if (!__all_sync(0xffffffffu, wait_bar(&bars[PBF + (c & 1)], par(c >> 1)))) { ok = false; break; }
+            tc_fence_after();
+            if (elect_one()) {
+                const uint64_t z0 = dZt + so, p0 = dP + (uint64_t)((c & 1) * (8192 >> 4));
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    mma_ss(o, z0 + kk * (2048 >> 4), p0 + kk * (32 >> 4), idOa, 1);
+                mma_commit(&bars[OFULL + (c & 1)]);
+                mma_commit(&bars[QEMPTY + s]);
             }
+            __syncwarp();
+            s = s1;
         }
         // all issued MMAs complete before the CTA gives up its TMEM
         if (elect_one()) mma_commit(&bars[FIN]);
         __syncwarp();
-        if (!mbar_wait(&bars[FIN], 0)) ok = false;
+        if (!wait_bar(&bars[FIN], 0)) ok = false;
         __syncwarp();
     } else if (warp < 6) {
         // ------------------------------------------------------------ output
-        // Lane z of the accumulators, tokens in columns. A warp stores 32 neighbouring values
-        // of one token at a time.
-        const int j = warp & 3, z = j * 32 + lane;
+        // out^T = O diag(F): lane z, tokens in columns. A warp stages its 32 value columns as
+        // [token][32] rows (64 bytes, 16-byte chunks XORed with (row / 2) % 4), which one bulk
+        // store then takes to global memory. (Loads in the mma fragment layout, whose transposing
+        // stores need fewer instructions, took 2.5 times as long.)
+        const int z = j * 32 + lane;
         const uint64_t pol = l2_policy_evict_first();
-        const int64_t rs = (int64_t)a.H * Dz;
+        uint8_t *tile = sm + OUT + j * 4096;
+        const bool mine = 32 * j < Dz;      // this warp's columns exist
+        uint32_t at[4];                     // of this lane in rows 2 r, 2 r + 1 modulo 8
+#pragma unroll
+        for (int r = 0; r < 4; ++r) at[r] = smem_u32(tile) + (((lane >> 3) ^ r) << 4) + (lane & 7) * 2;
         for (int c = 0; c < n; ++c) {
-            if (!__all_sync(0xffffffffu, mbar_wait(&bars[OFULL], par(c)))) { ok = false; break; }
+            if (!__all_sync(0xffffffffu, wait_bar(&bars[OFULL + (c & 1)], par(c >> 1)))) { ok = false; break; }
             tc_fence_after();
-            const int ch = chunk(c), nt = chunk_tokens(ch, a.T);
-            const float *f = fa + (rev ? kC - nt : 0);
-            float ov[64];
+            const int t0 = chunk_start(cb + c, a, rev), nt = chunk_tokens(cb + c, a);
+            const uint32_t ta = tmem_addr(tm, j, COL_O + (c & 1) * 64);
+            const bool bulk = nt == kC;     // else row by row, straight from here
+            if (mine && bulk) {
+#pragma unroll 1
+                for (int q = 0; q < kC; q += 16) {
+                    // the staging tile has been read (it takes 64 tokens of bf16, 32 of float)
+                    if (q == 0 || (m.out_f32 && q == 32)) {
+                        if (lane == 0) bulk_wait_read_all();
+                        __syncwarp();
+                    }
+                    uint32_t r[16];
+                    tmem_ld16(ta + q, r);
+                    float4 f[4];
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                float oi[32], oa[32];
-                tmem_ld32(tmem_addr(tm, j, COL_OI + 32 * half), oi);
-                tmem_ld32(tmem_addr(tm, j, COL_OA + 32 * half), oa);
+                    for (int x = 0; x < 4; ++x) f[x] = *reinterpret_cast<const float4 *>(fa + q + 4 * x);
+                    tmem_wait_ld();
+                    reg_fence(r);
+                    float2 v[8];
 #pragma unroll
-                for (int x = 0; x < 32; ++x) ov[32 * half + x] = fmaf(f[32 * half + x], oi[x], oa[x]);
-            }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars[OFREE]);
-            if (z >= Dz) continue;
-            const int64_t at = (((int64_t)b * a.T + (int64_t)ch * kC) * a.H + h) * Dz + z;
-            if (m.out_f32) {
-                float *op = static_cast<float *>(m.out) + at;
+                    for (int x = 0; x < 8; ++x)
+                        v[x] = mul2(make_float2(__uint_as_float(r[2 * x]), __uint_as_float(r[2 * x + 1])),
+                                    x & 1 ? make_float2(f[x >> 1].z, f[x >> 1].w)
+                                          : make_float2(f[x >> 1].x, f[x >> 1].y));
+                    if (m.out_f32) {
+                        float *to = reinterpret_cast<float *>(tile) + (q & 31) * 32 + lane;
 #pragma unroll
-                for (int x = 0; x < kC; ++x)
-                    if (x < nt) op[x * rs] = ov[x];
-            } else {
-                __nv_bfloat16 *op = static_cast<__nv_bfloat16 *>(m.out) + at;
-                if (nt == kC) {
+                        for (int x = 0; x < 8; ++x) {
+                            to[2 * x * 32] = v[x].x;
+                            to[(2 * x + 1) * 32] = v[x].y;
+                        }
+                        if (q & 16) {
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                            if (lane == 0) {
+                                tma_store_4d_hint(&maps.o[li], tile, 32 * j, h, t0 + q - 16, b, pol);
+                                bulk_commit();
+                            }
+                        }
+                    } else {
 #pragma unroll
-                    for (int x = 0; x < kC; ++x)
-                        st_global_bf16_hint(op + x * rs, __float2bfloat16_rn(ov[x]), pol);
-                } else {
-#pragma unroll
-                    for (int x = 0; x < kC; ++x)
-                        if (x < nt) st_global_bf16_hint(op + x * rs, __float2bfloat16_rn(ov[x]), pol);
+                        for (int x = 0; x < 8; ++x)
+                            asm volatile("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %0;\n\t"
+                                         "st.shared.b16 [%1], lo;\n\tst.shared.b16 [%1 + 64], hi;\n\t}" ::"r"(
+                                             pack_bf16(v[x].x, v[x].y)),
+                                         "r"(at[x & 3] + (q + 2 * x) * 64)
+                                         : "memory");
+                    }
                 }
-            }
-        }
-        __syncwarp();
-    } else if (warp < 10) {
-        // ------------------------------------------------------------ state
-        // Per chunk: the bf16 snapshot of S for X S, and S <- l^n S before the update is added.
-        const int j = warp & 3, z = j * 32 + lane;
-        const float *init = nullptr;
-        int tr = 0;
-        if (seg > 0) {
-            // the start states come from the scan kernel, which may still be running
-            pdl_wait_prerequisites();
-            init = m.start + ((size_t)bh * (a.splits - 1) + (seg - 1)) * (Dx * Dz);
-            tr = m.start_t;
-        } else if (m.init) {
-            init = m.init + (size_t)bh * Dx * Dz;
-            tr = m.init_t;
-        }
-        const int sx = tr ? 1 : Dz, sz = tr ? Dx : 1;   // strides of the state as stored
+            } else if (mine) {
+                const int64_t rs = (int64_t)a.H * Dz;
+                const int64_t base = ((int64_t)b * a.T + t0) * rs + (int64_t)h * Dz + z;
+                const int lo = rev ? kC - nt : 0, hi = rev ? kC : nt;    // the rows there are
 #pragma unroll 1
-        for (int x0 = 0; x0 < Dx; x0 += 16) {
-            uint32_t r[16];
+                for (int q = 0; q < kC; q += 16) {
+                    uint32_t r[16];
+                    tmem_ld16(ta + q, r);
+                    tmem_wait_ld();
+                    reg_fence(r);
 #pragma unroll
-            for (int x = 0; x < 16; ++x)
-                r[x] = (init && z < Dz) ? __float_as_uint(init[(x0 + x) * sx + z * sz]) : 0u;
-            tmem_st16(tmem_addr(tm, j, COL_S + x0), r);
-        }
-        tmem_wait_st();
-        for (int c = 0; c < n; ++c) {
-            const bool w = (c == 0 || mbar_wait(&bars[UDONE], par(c - 1))) &&
-                           (c < 2 || mbar_wait(&bars[SBFREE + (c & 1)], par((c >> 1) - 1)));
-            if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
-            tc_fence_after();
-            const float carry = pw[chunk_tokens(chunk(c), a.T)];
-            const float2 cc = make_float2(carry, carry);
-#pragma unroll 1
-            for (int q = 0; q < Dx / 32; ++q) {
-                float sv[32];
-                tmem_ld32(tmem_addr(tm, j, COL_S + 32 * q), sv);
-                uint32_t pk[16], r0[16], r1[16];
-#pragma unroll
-                for (int x = 0; x < 16; ++x) pk[x] = pack_bf16(sv[2 * x], sv[2 * x + 1]);
-                tmem_st16(tmem_addr(tm, j, COL_SB + (c & 1) * 64 + 16 * q), pk);
-#pragma unroll
-                for (int x = 0; x < 8; ++x) {
-                    const float2 lo = mul2(make_float2(sv[2 * x], sv[2 * x + 1]), cc);
-                    const float2 hi = mul2(make_float2(sv[16 + 2 * x], sv[17 + 2 * x]), cc);
-                    r0[2 * x] = __float_as_uint(lo.x);
-                    r0[2 * x + 1] = __float_as_uint(lo.y);
-                    r1[2 * x] = __float_as_uint(hi.x);
-                    r1[2 * x + 1] = __float_as_uint(hi.y);
-                }
-                tmem_st16(tmem_addr(tm, j, COL_S + 32 * q), r0);
-                tmem_st16(tmem_addr(tm, j, COL_S + 32 * q + 16), r1);
-            }
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars[SREADY]);
-        }
-        if (ok && m.fin && seg == a.splits - 1) {
-            if (!__all_sync(0xffffffffu, mbar_wait(&bars[UDONE], par(n - 1)))) {
-                ok = false;
-            } else {
-                tc_fence_after();
-                float *fp = m.fin + (size_t)bh * Dx * Dz + z;
-#pragma unroll 1
-                for (int q = 0; q < Dx / 32; ++q) {
-                    float sv[32];
-                    tmem_ld32(tmem_addr(tm, j, COL_S + 32 * q), sv);
-                    if (z < Dz) {
-#pragma unroll
-                        for (int x = 0; x < 32; ++x) fp[(32 * q + x) * Dz] = sv[x];
+                    for (int x = 0; x < 16; ++x) {
+                        const int row = q + x;
+                        if (row < lo || row >= hi) continue;
+                        const float v = fa[row] * __uint_as_float(r[x]);
+                        if (m.out_f32) static_cast<float *>(m.out)[base + row * rs] = v;
+                        else static_cast<__nv_bfloat16 *>(m.out)[base + row * rs] = __float2bfloat16_rn(v);
                     }
                 }
             }
+            tc_fence_before();
+            const bool store = mine && bulk && !m.out_f32;
+            if (store) fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&bars[OFREE + (c & 1)]);
+                if (store) {
+                    tma_store_4d_hint(&maps.o[li], tile, 32 * j, h, t0, b, pol);
+                    bulk_commit();
+                }
+            }
         }
+        if (lane == 0) bulk_wait_all();
         __syncwarp();
-    } else {
-        // ------------------------------------------------------------ diag(u) Z, then P
-        const int j = warp & 3, ct = (warp - 10) * 32 + lane;
-        // The warp's 16 rows of P over all 32 threads: rows ia and ia + 8, column pairs
-        // 8 k + 2 (lane % 4). Their mask is the same in every chunk and stays in registers.
+    } else if (warp >= 10 && warp < 14) {
+        // ------------------------------------------------------------ P
+        // X Y^T of chunk c -> its masked bf16 tile. The tile's buffer was last read by A(c - 2),
+        // which PFULL(c), whose MMAs were issued later, has seen complete. A warp has 16 rows: ia
+        // and ia + 8 of a thread, column pairs 8 k + 2 (lane % 4). The factors are the same in every
+        // chunk and stay in registers.
         const int ia = 16 * j + (lane >> 2), c0 = 2 * (lane & 3);
         float mask[32];
 #pragma unroll
         for (int e = 0; e < 32; ++e) {
-            const int i = ia + (e & 2 ? 8 : 0), col = 8 * (e >> 2) + c0 + (e & 1);
-            const int d = rev ? col - i : i - col;
-            mask[e] = d >= 0 ? m.a_in * m.a_out * pw[d] : 0.f;
+            const int i = ia + (e & 2 ? 8 : 0), col = 8 * (e >> 2) + c0 + (e & 1), d = rev ? col - i : i - col;
+            // M_ij / F_i (a_out is in F, a_in here)
+            mask[e] = d >= 0 ? pw[d] * (m.a_in / fmaxf(pw[rev ? kC - 1 - i : i + 1], kLeastF)) : 0.f;
         }
-        // 16-byte vectors ct + 128 x of the Z tile: token (ct / 8 + 16 x) % 64
-        const int row = ct >> 3;
         for (int c = 0; c < n; ++c) {
-            const int s = c % NQ, nt = chunk_tokens(chunk(c), a.T);
-            bool w = mbar_wait(&bars[QFULL + s], par(c / NQ)) &&
-                     (c < 2 || mbar_wait(&bars[ZFREE + (c & 1)], par((c >> 1) - 1)));
-            if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
-            const uint4 *zs = reinterpret_cast<const uint4 *>(sm + s * STAGE + Z) + ct;
-            uint4 *zh = reinterpret_cast<uint4 *>(sm + ZP + (c & 1) * ZPSTAGE) + ct;
-            float u[4];
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                const int t = row + 16 * x, e = rev ? t + 1 : nt - 1 - t;
-                u[x] = t < nt ? m.a_in * pw[e] : 0.f;
-            }
-#pragma unroll 1
-            for (int box = 0; box < Dz / 64; ++box) {
-                uint4 v[4];
-#pragma unroll
-                for (int x = 0; x < 4; ++x) v[x] = zs[box * 512 + 128 * x];
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    uint4 hi, lo;
-                    split8(v[x], u[x], hi, lo);
-                    zh[box * 512 + 128 * x] = hi;
-                    zh[1024 + box * 512 + 128 * x] = lo;
-                }
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars[ZDONE + (c & 1)]);
-
-            w = mbar_wait(&bars[PFULL], par(c)) && (c == 0 || mbar_wait(&bars[OFULL], par(c - 1)));
-            if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
+            if (!__all_sync(0xffffffffu, wait_bar(&bars[PFULL], par(c)))) { ok = false; break; }
             tc_fence_after();
+            uint8_t *pt = sm + P + (c & 1) * 8192;
             uint32_t r0[16], r1[16];
-            const uint32_t ta = tmem_addr(tm, j, COL_P);
-            tmem_ld16x256b_x4(ta, r0);
-            tmem_ld16x256b_x4(ta + 32, r1);
+            tmem_ld16x256b_x4(tmem_addr(tm, j, COL_P), r0);
+            tmem_ld16x256b_x4(tmem_addr(tm, j, COL_P + 32), r1);
             tmem_wait_ld();
             reg_fence(r0);
             reg_fence(r1);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars[PFREE]);
-            uint8_t *pt = sm + P;
 #pragma unroll
-            for (int k8 = 0; k8 < 8; ++k8) {
-                const uint32_t *r = k8 < 4 ? r0 + 4 * k8 : r1 + 4 * (k8 - 4);
-                float f[4];
+            for (int k = 0; k < 8; ++k) {
+                const uint32_t *r = k < 4 ? r0 + 4 * k : r1 + 4 * (k - 4);
+                float2 f[2];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float mk = mask[4 * k8 + e];
-                    // a score outside the mask is dropped, not multiplied by zero: it may be
-                    // infinite
-                    f[e] = mk != 0.f ? mk * __uint_as_float(r[e]) : 0.f;
-                }
-                const int col = 8 * k8 + c0;
-                *reinterpret_cast<uint32_t *>(pt + sw128_offset(ia, col)) = pack_bf16(f[0], f[1]);
-                *reinterpret_cast<uint32_t *>(pt + sw128_offset(ia + 8, col)) = pack_bf16(f[2], f[3]);
+                for (int e = 0; e < 2; ++e)
+                    f[e] = mul2(make_float2(mask[4 * k + 2 * e], mask[4 * k + 2 * e + 1]),
+                                make_float2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1])));
+                const int col = c0 + 8 * k;
+                *reinterpret_cast<uint32_t *>(pt + sw128_offset(ia, col)) = pack_bf16(f[0].x, f[0].y);
+                *reinterpret_cast<uint32_t *>(pt + sw128_offset(ia + 8, col)) = pack_bf16(f[1].x, f[1].y);
             }
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bars[PBF]);
+            if (lane == 0) mbar_arrive(&bars[PBF + (c & 1)]);
+        }
+        __syncwarp();
+    } else if (warp >= 14) {
+        // ------------------------------------------------------------ diag(u) Z
+        // 16-byte vectors ct + 128 x of the Z tile: token (ct / 8 + 16 x) % 64. The product keeps
+        // the tile's layout, so the swizzle does not matter here.
+        const int ct = (warp - 14) * 32 + lane;
+        int zb = 0, zuse = 0;
+        for (int c = 0, s = 0, use = 0; c < n; ++c) {
+            const bool w = wait_bar(&bars[QFULL + s], par(use)) &&
+                           (zuse == 0 || wait_bar(&bars[ZFREE + zb], par(zuse - 1)));
+            if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
+            const float *u = reinterpret_cast<const float *>(sm + (cb + c == a.nchunks - 1 ? FUL : FU)) + (ct >> 3);
+            const uint4 *zs = reinterpret_cast<const uint4 *>(sm + s * STAGE + Z) + ct;
+            uint4 *zp = reinterpret_cast<uint4 *>(sm + ZP + zb * 16384) + ct;
+#pragma unroll 1
+            for (int box = 0; box < Dz / 64; ++box) {
+                uint4 v[4];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) v[x] = zs[box * 512 + 128 * x];
+                if (exact) {
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) put_scaled<3>(v[x], u[16 * x], zp + box * 512 + 128 * x);
+                } else {
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) put_scaled<1>(v[x], u[16 * x], zp + box * 512 + 128 * x);
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[ZDONE + zb]);
+            if (++zb == nzb) {
+                zb = 0;
+                ++zuse;
+            }
+            if (++s == NQ) {
+                s = 0;
+                ++use;
+            }
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------------ state
+        // Lane z, key rows x. Per chunk S <- l^n S + D, rounded to nearest (a sum kept in the
+        // accumulator over many chunks is cut off at every step: 3e-6 of hT at a memory of 1024
+        // tokens), and its bf16 snapshot for X S.
+        const int z = j * 32 + lane;
+        {
+            const float *init = nullptr;
+            int tr = 0;
+            if (seg > 0) {
+                // the start states come from the scan kernel, which may still be running
+                pdl_wait_prerequisites();
+                init = m.start + ((size_t)bh * (a.splits - 1) + (seg - 1)) * (Dx * Dz);
+                tr = m.start_t;
+            } else if (m.init) {
+                init = m.init + (size_t)bh * Dx * Dz;
+                tr = m.init_t;
+            }
+            const int sx = tr ? 1 : Dz, sz = tr ? Dx : 1;   // strides of the state as stored
+#pragma unroll 1
+            for (int x0 = 0; x0 < Dx; x0 += 16) {
+                uint32_t r[16];
+#pragma unroll
+                for (int x = 0; x < 16; ++x)
+                    r[x] = init && z < Dz ? __float_as_uint(init[(x0 + x) * sx + z * sz]) : 0u;
+                tmem_st16(tmem_addr(tm, j, COL_S + x0), r);
+            }
+            tmem_wait_st();
+        }
+        // The state before chunk c (after the last one for c = n, which goes to fin).
+        for (int c = 0; c <= n; ++c) {
+            const bool last = c == n;
+            if (last && !exact) break;
+            bool w = c == 0 || wait_bar(&bars[UDONE], par(c - 1));
+            w = w && (c == 0 || last || wait_bar(&bars[SBFREE], par(c - 1)));
+            if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
+            tc_fence_after();
+            const float carry = c > 0 ? pw[chunk_tokens(cb + c - 1, a)] : 1.f;
+            const float2 cc = make_float2(carry, carry);
+            float *fp = m.fin + (size_t)bh * Dx * Dz + z;
+#pragma unroll 1
+            for (int q = 0; q < Dx; q += 32) {
+                float sv[32];
+                if (c > 0) {
+                    uint32_t d0[16], d1[16], s0[16], s1[16];
+                    tmem_ld16(tmem_addr(tm, j, COL_D + q), d0);
+                    tmem_ld16(tmem_addr(tm, j, COL_D + q + 16), d1);
+                    tmem_ld16(tmem_addr(tm, j, COL_S + q), s0);
+                    tmem_ld16(tmem_addr(tm, j, COL_S + q + 16), s1);
+                    tmem_wait_ld();
+                    reg_fence(d0);
+                    reg_fence(d1);
+                    reg_fence(s0);
+                    reg_fence(s1);
+#pragma unroll
+                    for (int x = 0; x < 16; x += 2) {
+                        const float2 lo = fma2(make_float2(__uint_as_float(s0[x]), __uint_as_float(s0[x + 1])), cc,
+                                               make_float2(__uint_as_float(d0[x]), __uint_as_float(d0[x + 1])));
+                        const float2 hi = fma2(make_float2(__uint_as_float(s1[x]), __uint_as_float(s1[x + 1])), cc,
+                                               make_float2(__uint_as_float(d1[x]), __uint_as_float(d1[x + 1])));
+                        sv[x] = lo.x;
+                        sv[x + 1] = lo.y;
+                        sv[16 + x] = hi.x;
+                        sv[17 + x] = hi.y;
+                    }
+                    if (!last) {
+#pragma unroll
+                        for (int x = 0; x < 16; ++x) {
+                            s0[x] = __float_as_uint(sv[x]);
+                            s1[x] = __float_as_uint(sv[16 + x]);
+                        }
+                        tmem_st16(tmem_addr(tm, j, COL_S + q), s0);
+                        tmem_st16(tmem_addr(tm, j, COL_S + q + 16), s1);
+                    }
+                } else {
+                    tmem_ld32f(tmem_addr(tm, j, COL_S + q), sv);
+                }
+                if (!last) {
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int x = 0; x < 16; ++x) pk[x] = pack_bf16(sv[2 * x], sv[2 * x + 1]);
+                    tmem_st16(tmem_addr(tm, j, COL_SB + q / 2), pk);
+                } else if (z < Dz) {
+#pragma unroll
+                    for (int x = 0; x < 32; ++x) fp[(q + x) * Dz] = sv[x];
+                }
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0 && !last) mbar_arrive(&bars[SREADY]);
         }
         __syncwarp();
     }
@@ -555,17 +695,16 @@ hda_tc_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ T
 }
 
 // ======================================================================= state kernel
+// Stages of y, z and, over z and behind it, the parts of diag(u) Z.
 namespace st {
-constexpr int NS = 4;
-constexpr uint32_t Y = 0, Z = 16384, L = 32768, STAGE = 49152;   // L: low part of diag(u) Z
-constexpr uint32_t PW = NS * STAGE;
+constexpr uint32_t Y = 0, Z = 16384;
+constexpr uint32_t BYTES = 6 * 32768;            // 6 stages of one part, or 3 of three
+constexpr uint32_t PW = BYTES;
 constexpr uint32_t BAR = PW + 320;
-constexpr uint32_t NBAR = 3 * NS + 1;
-constexpr uint32_t TSLOT = BAR + NBAR * 8;
+constexpr uint32_t TSLOT = BAR + 19 * 8;
 constexpr uint32_t ALLOC = TSLOT + 24 + 1024;
 static_assert(ALLOC <= 232448, "state kernel shared memory");
 }  // namespace st
-enum { SFULL = 0, SEMPTY = st::NS, SZDONE = 2 * st::NS, SEND = 3 * st::NS };
 constexpr int kStateThreads = 320;   // 0 TMA, 1 MMA, 2-9 diag(u) Z
 
 struct StateProblem {
@@ -588,10 +727,17 @@ __device__ __forceinline__ void piece_range(const TcArgs &a, int seg, int sub, i
     ce = s0 + (int)((int64_t)(sub + 1) * len / pieces);
 }
 
+template <int kParts>
 __global__ void __launch_bounds__(kStateThreads, 1)
 hda_tc_state_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ TcArgs a,
                     const __grid_constant__ StateArgs sa) {
     using namespace st;
+    constexpr int NS = kParts == 1 ? 6 : 3;
+    constexpr uint32_t STAGE = 16384 + kParts * 16384;
+    // With three parts every chunk has an accumulator of its own (two take turns), added up in
+    // registers: a sum over many chunks in the accumulator would be cut off at each step.
+    constexpr bool kDrain = kParts == 3;
+    enum { SFULL = 0, SEMPTY = NS, SZDONE = 2 * NS, SEND = 3 * NS, SDONE = SEND + 1, SREAD = SDONE + 2 };
     extern __shared__ uint8_t smraw[];
     uint8_t *sm = align1024(smraw);
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + BAR);
@@ -608,7 +754,8 @@ hda_tc_state_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__
     piece_range(a, pi / sa.pieces, pi % sa.pieces, sa.pieces, cb, ce);
     const int n = ce - cb;
     // the chunks run last to first: what is read last is what the out kernel reads first
-    auto chunk = [&](int c) { return walk_chunk(ce - 1 - c, a.nchunks, rev); };
+    // (never the last chunk of the walk: all are full)
+    auto start = [&](int c) { return chunk_start(ce - 1 - c, a, rev); };
     const float g = a.decay[h];
     if (threadIdx.x <= kC) pw[threadIdx.x] = decay_pow(g, (float)threadIdx.x);
     if (threadIdx.x == 0) {
@@ -617,6 +764,10 @@ hda_tc_state_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__
             mbar_init(&bars[SEMPTY + i], 1);
             mbar_init(&bars[SZDONE + i], 8);
         }
+        for (int i = 0; kDrain && i < 2; ++i) {
+            mbar_init(&bars[SDONE + i], 1);
+            mbar_init(&bars[SREAD + i], 8);
+        }
         mbar_init(&bars[SEND], 1);
         fence_mbar_init();
     }
@@ -624,7 +775,7 @@ hda_tc_state_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__
         tma_prefetch_desc(&maps.y[sp.li]);
         tma_prefetch_desc(&maps.z[sp.li]);
     }
-    if (warp == 1) tmem_alloc(tslot, 128);
+    if (warp == 1) tmem_alloc(tslot, 256);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -637,90 +788,109 @@ hda_tc_state_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__
             int c = 0;
             for (; c < n; ++c) {
                 const int s = c % NS;
-                if (c >= NS && !mbar_wait(&bars[SEMPTY + s], par(c / NS - 1))) { ok = false; break; }
+                if (c >= NS && !wait_bar(&bars[SEMPTY + s], par(c / NS - 1))) { ok = false; break; }
                 uint8_t *base = sm + s * STAGE;
                 const uint64_t pol = c >= n - sa.retain ? keep : drop;
                 mbar_arrive_expect_tx(&bars[SFULL + s], (uint32_t)(Dx + Dz) * 2 * kC);
-                load_tile(base + Y, &maps.y[sp.li], &bars[SFULL + s], Dx, h / m.hy, chunk(c) * kC, b, pol);
-                load_tile(base + Z, &maps.z[sp.li], &bars[SFULL + s], Dz, h / m.hz, chunk(c) * kC, b, pol);
+                load_tile(base + Y, &maps.y[sp.li], &bars[SFULL + s], Dx, h / m.hy, start(c), b, pol);
+                load_tile(base + Z, &maps.z[sp.li], &bars[SFULL + s], Dz, h / m.hz, start(c), b, pol);
             }
             for (int i = 0; i < NS; ++i) {
                 const int uses = c > i ? (c - 1 - i) / NS + 1 : 0;
-                if (uses > 0 && !mbar_wait(&bars[SFULL + i], par(uses - 1))) ok = false;
+                if (uses > 0 && !wait_bar(&bars[SFULL + i], par(uses - 1))) ok = false;
             }
         }
         __syncwarp();
     } else if (warp == 1) {
         const uint32_t idU = idesc_bf16(128, Dx, 1, 1);
+        const uint64_t dY = smem_desc(smem_u32(sm) + Y, 8192, 1024);
+        const uint64_t dZ = smem_desc(smem_u32(sm) + Z, 8192, 1024);
         for (int c = 0; c < n; ++c) {
-            const bool w = mbar_wait(&bars[SZDONE + c % NS], par(c / NS));
+            const bool w = wait_bar(&bars[SZDONE + c % NS], par(c / NS)) &&
+                           (!kDrain || c < 2 || wait_bar(&bars[SREAD + (c & 1)], par((c >> 1) - 1)));
             if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
             tc_fence_after();
-            const uint32_t base = smem_u32(sm + (c % NS) * STAGE);
+            const uint64_t so = (uint64_t)((c % NS) * (STAGE >> 4));
+            const uint32_t acc = tm + (kDrain ? (c & 1) * 128 : 0);
             if (elect_one()) {
+                // the small parts first
 #pragma unroll
-                for (int part = 0; part < 2; ++part)
+                for (int part = kParts - 1; part >= 0; --part)
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        mma_ss(tm, smem_desc(base + (part ? L : Z) + kk * 2048, 8192, 1024),
-                               smem_desc(base + Y + kk * 2048, 8192, 1024), idU,
-                               (c > 0 || part > 0 || kk > 0) ? 1u : 0u);
+                        mma_ss(acc, dZ + so + part * (16384 >> 4) + kk * (2048 >> 4),
+                               dY + so + kk * (2048 >> 4), idU,
+                               ((!kDrain && c > 0) || part < kParts - 1 || kk > 0) ? 1u : 0u);
                 mma_commit(&bars[SEMPTY + c % NS]);
+                if (kDrain) mma_commit(&bars[SDONE + (c & 1)]);
             }
             __syncwarp();
         }
         if (elect_one()) mma_commit(&bars[SEND]);
         __syncwarp();
-        if (!mbar_wait(&bars[SEND], 0)) ok = false;
+        if (!wait_bar(&bars[SEND], 0)) ok = false;
         __syncwarp();
     } else {
         const int ct = (warp - 2) * 32 + lane;      // 0..255
         const int row = ct >> 3;                    // tokens row and row + 32
+        // E^T: lanes z (quarter j), columns x (half) in registers
+        const int j = warp & 3, half = (warp - 2) >> 2, z = j * 32 + lane;
+        const bool mine = 64 * half < Dx;
+        float S[64];
+#pragma unroll
+        for (int x = 0; x < 64; ++x) S[x] = 0.f;
+        auto add_D = [&](uint32_t col) {
+            tc_fence_after();
+            if (mine) {
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    float d[32];
+                    tmem_ld32f(tmem_addr(tm, j, col + 64 * half + 32 * q), d);
+#pragma unroll
+                    for (int x = 0; x < 32; ++x) S[32 * q + x] += d[x];
+                }
+            }
+        };
+        auto drain = [&](int c) -> bool {
+            if (!__all_sync(0xffffffffu, wait_bar(&bars[SDONE + (c & 1)], par(c >> 1)))) return false;
+            add_D((c & 1) * 128);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[SREAD + (c & 1)]);
+            return true;
+        };
         for (int c = 0; c < n; ++c) {
             const int s = c % NS;
-            if (!__all_sync(0xffffffffu, mbar_wait(&bars[SFULL + s], par(c / NS)))) { ok = false; break; }
+            if (!__all_sync(0xffffffffu, wait_bar(&bars[SFULL + s], par(c / NS)))) { ok = false; break; }
             // c chunks of 64 tokens follow this one in the piece
             const float after = m.a_in * decay_pow(g, (float)(kC * c));
-            const int nt = chunk_tokens(chunk(c), a.T);
             float u[2];
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const int t = row + 32 * x;
-                u[x] = t < nt ? after * pw[rev ? t + 1 : nt - 1 - t] : 0.f;
-            }
+            for (int x = 0; x < 2; ++x) u[x] = after * state_factor(pw, row + 32 * x, kC, rev);
             uint4 *zs = reinterpret_cast<uint4 *>(sm + s * STAGE + Z) + ct;
-#pragma unroll 1
-            for (int box = 0; box < Dz / 64; ++box) {
-                const uint4 v0 = zs[box * 512], v1 = zs[box * 512 + 256];
-                uint4 hi, lo;
-                split8(v0, u[0], hi, lo);
-                zs[box * 512] = hi;
-                zs[1024 + box * 512] = lo;
-                split8(v1, u[1], hi, lo);
-                zs[box * 512 + 256] = hi;
-                zs[1024 + box * 512 + 256] = lo;
-            }
+            const int vecs = Dz / 64 * 2;
+            uint4 v[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+                if (x < vecs) v[x] = zs[256 * x];
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+                if (x < vecs) put_scaled<kParts>(v[x], u[x & 1], zs + 256 * x);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars[SZDONE + s]);
+            if (kDrain && c > 0 && !drain(c - 1)) { ok = false; break; }
         }
-        if (warp < 6) {     // E^T (lane z, column x) -> E[x][z]
-            const int j = warp & 3, z = j * 32 + lane;
-            if (!ok || !__all_sync(0xffffffffu, mbar_wait(&bars[SEND], 0))) {
-                ok = false;
-            } else {
-                tc_fence_after();
-                float *ep = sp.E + ((size_t)bh * npc + pi) * (Dx * Dz) + z;
-#pragma unroll 1
-                for (int q = 0; q < Dx / 32; ++q) {
-                    float sv[32];
-                    tmem_ld32(tmem_addr(tm, j, 32 * q), sv);
-                    if (z < Dz) {
+        if (kDrain) {
+            ok = ok && (n == 0 || drain(n - 1));
+        } else if (ok && n > 0) {
+            ok = __all_sync(0xffffffffu, wait_bar(&bars[SEND], 0));
+            if (ok) add_D(0);
+        }
+        if (ok && mine && z < Dz) {
+            float *ep = sp.E + ((size_t)bh * npc + pi) * (Dx * Dz) + z;
 #pragma unroll
-                        for (int x = 0; x < 32; ++x) ep[(32 * q + x) * Dz] = sv[x];
-                    }
-                }
-            }
+            for (int x = 0; x < 64; ++x) ep[(64 * half + x) * Dz] = S[x];
         }
         __syncwarp();
     }
@@ -729,7 +899,7 @@ hda_tc_state_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__
     __syncthreads();
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tm, 128);
+        tmem_dealloc(tm, 256);
     }
 }
 
@@ -771,10 +941,7 @@ hda_tc_scan_kernel(const __grid_constant__ TcArgs a, const __grid_constant__ Sta
             const int r = r0 + j;
             int cb, ce;
             piece_range(a, r / sa.pieces, r % sa.pieces, sa.pieces, cb, ce);
-            // only the first chunk of a reversed walk can be short
-            int64_t tokens = (int64_t)(ce - cb) * kC;
-            if (m.rev && cb == 0 && ce > 0) tokens -= kC - chunk_tokens(a.nchunks - 1, a.T);
-            const float f = decay_pow(g, (float)tokens);
+            const float f = decay_pow(g, (float)(ce - cb) * kC);   // (all chunks are full)
             const bool end = (r + 1) % sa.pieces == 0;
 #pragma unroll
             for (int i = 0; i < kScanPer; ++i) {
@@ -800,9 +967,10 @@ cudaError_t set_attrs() {
     e = cudaFuncSetAttribute((const void *)hda_tc_out_kernel,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, om::ALLOC);
     if (e != cudaSuccess) return e;
-    e = cudaFuncSetAttribute((const void *)hda_tc_state_kernel,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, st::ALLOC);
-    if (e != cudaSuccess) return e;
+    for (const void *k : {(const void *)hda_tc_state_kernel<1>, (const void *)hda_tc_state_kernel<3>}) {
+        e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, st::ALLOC);
+        if (e != cudaSuccess) return e;
+    }
     g_attr_done[dev] = true;
     return cudaSuccess;
 }
@@ -815,6 +983,21 @@ bool make_map(CUtensorMap *m, const HdaTensor &t, int64_t B, int64_t T, int D) {
     cuuint32_t box[4] = {64, 1, kC, 1}, estr[4] = {1, 1, 1, 1};
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(t.p), dims, strides, box, estr,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The store of a warp's 32 columns of a contiguous [B, T, H, D] output: 64 tokens of bf16 (rows of 64
+// bytes, swizzled), or 32 of float.
+bool make_out_map(CUtensorMap *m, void *out, bool f32, int64_t B, int64_t T, int64_t H, int64_t D) {
+    EncodeTiledFn fn = encode_tiled_fn();
+    if (!fn) return false;
+    const cuuint64_t es = f32 ? 4 : 2;
+    cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)T, (cuuint64_t)B};
+    cuuint64_t strides[3] = {D * es, H * D * es, T * H * D * es};
+    cuuint32_t box[4] = {32, 1, f32 ? 32u : kC, 1}, estr[4] = {1, 1, 1, 1};
+    return fn(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, out, dims,
+              strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              f32 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_64B,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -867,6 +1050,7 @@ bool hda_tc_supported(const HdaProblem &p) {
         for (const HdaTensor *t : {&m.x, &m.y, &m.z})     // limits of a tensor map
             for (int64_t s : {t->b, t->t, t->h})
                 if (s * 2 >= (int64_t(1) << 40)) return false;
+        if (p.T * p.H * m.Dz * 4 >= (int64_t(1) << 40)) return false;
     }
     return true;
 }
@@ -898,7 +1082,8 @@ cudaError_t launch_hda_tc(const HdaProblem &p, int splits, int num_sms, void *ws
     for (int i = 0; i < p.n; ++i) {
         const HdaLin &m = p.lin[i];
         if (!make_map(&maps.x[i], m.x, p.B, p.T, m.Dx) || !make_map(&maps.y[i], m.y, p.B, p.T, m.Dx) ||
-            !make_map(&maps.z[i], m.z, p.B, p.T, m.Dz))
+            !make_map(&maps.z[i], m.z, p.B, p.T, m.Dz) ||
+            !make_out_map(&maps.o[i], m.out, m.out_f32, p.B, p.T, p.H, m.Dz))
             return cudaErrorInvalidResourceHandle;   // a tensor map could not be encoded
         const auto rep = [&](const HdaTensor &t) { return (int)(p.H / t.heads); };
         a.lin[i] = TcLin{m.init, nullptr, m.fin, m.out, m.init_t, 0, m.out_f32, m.Dx, m.Dz,
@@ -925,8 +1110,8 @@ cudaError_t launch_hda_tc(const HdaProblem &p, int splits, int num_sms, void *ws
             a.lin[1].start = a.lin[2].start;
             a.lin[1].start_t = 1;
         }
-        hda_tc_state_kernel<<<(unsigned)(bh * (s - 1) * pieces * ns), kStateThreads, st::ALLOC, stream>>>(
-            maps, a, sa);
+        const auto kernel = p.lin[p.n - 1].fin ? hda_tc_state_kernel<3> : hda_tc_state_kernel<1>;
+        kernel<<<(unsigned)(bh * (s - 1) * pieces * ns), kStateThreads, st::ALLOC, stream>>>(maps, a, sa);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
         // the scan and the output may be scheduled while their predecessor still runs, and wait
         // for it before they read what it wrote
