@@ -127,10 +127,11 @@ __device__ __forceinline__ void load_tile(uint8_t *dst, const CUtensorMap *m, ui
     if (D > 64) tma_load_4d_hint(dst + 8192, m, bar, 64, h, t, b, pol);
 }
 
-// 16 bytes of Z (8 values of one token) times the token's factor, as kParts bf16 parts 16 KB
-// apart.
+// 16 bytes of Z (8 values of one token) times the token's factor, as kParts bf16 parts (the first
+// to dst, the others to rest, 16 KB apart): one, rounded, or three that hold 8 bits of the product's 24 each (cut off, not rounded:
+// the upper half of a float is a bf16, so a part is a byte permutation and the rest a subtraction).
 template <int kParts>
-__device__ __forceinline__ void put_scaled(uint4 v, float u, uint4 *dst) {
+__device__ __forceinline__ void put_scaled(uint4 v, float u, uint4 *dst, uint4 *rest) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
     float2 p[4];
 #pragma unroll
@@ -140,11 +141,13 @@ __device__ __forceinline__ void put_scaled(uint4 v, float u, uint4 *dst) {
         uint32_t o[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            o[i] = pack_bf16(p[i].x, p[i].y);
-            const float2 r = unpack_bf16(o[i]);
-            p[i] = make_float2(p[i].x - r.x, p[i].y - r.y);
+            const uint32_t x = __float_as_uint(p[i].x), y = __float_as_uint(p[i].y);
+            o[i] = kParts == 1 ? pack_bf16(p[i].x, p[i].y) : __byte_perm(x, y, 0x7632);
+            if (part + 1 < kParts)
+                p[i] = add2(p[i], make_float2(__uint_as_float((x & 0xffff0000u) ^ 0x80000000u),
+                                              __uint_as_float((y & 0xffff0000u) ^ 0x80000000u)));
         }
-        dst[part * 1024] = make_uint4(o[0], o[1], o[2], o[3]);
+        (part == 0 ? dst : rest + (part - 1) * 1024)[0] = make_uint4(o[0], o[1], o[2], o[3]);
     }
 }
 
@@ -238,7 +241,7 @@ hda_tc_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ T
             mbar_init(&bars[QEMPTY + i], 1);
         }
         for (int i = 0; i < 3; ++i) {
-            mbar_init(&bars[ZDONE + i], 4);
+            mbar_init(&bars[ZDONE + i], exact ? 8 : 4);
             mbar_init(&bars[ZFREE + i], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -273,6 +276,38 @@ hda_tc_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ T
     const uint32_t tm = *tslot;
     bool ok = true;
     const int j = warp & 3;     // the warp's quarter of the TMEM lanes
+
+    // diag(u) Z of chunk c, boxes b0 .. b1 - 1 of 64 value columns, by four warps (ct: the thread).
+    // 16-byte vectors ct + 128 x of a box: token (ct / 8 + 16 x) % 64. The product keeps the tile's
+    // layout, so the swizzle does not matter here.
+    auto scale_Z = [&](int c, int ct, int b0, int b1) -> bool {
+        const int s = c % NQ, zb = exact ? 0 : c % 3, zuse = exact ? c : c / 3;
+        const bool w = wait_bar(&bars[QFULL + s], par(c / NQ)) &&
+                       (zuse == 0 || wait_bar(&bars[ZFREE + zb], par(zuse - 1)));
+        if (!__all_sync(0xffffffffu, w)) return false;
+        const float *u = reinterpret_cast<const float *>(sm + (cb + c == a.nchunks - 1 ? FUL : FU)) + (ct >> 3);
+        const uint4 *zs = reinterpret_cast<const uint4 *>(sm + s * STAGE + Z) + ct;
+        uint4 *zp = reinterpret_cast<uint4 *>(sm + ZP + zb * 16384) + ct;
+#pragma unroll 1
+        for (int box = b0; box < b1; ++box) {
+            uint4 v[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) v[x] = zs[box * 512 + 128 * x];
+            if (exact) {
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    put_scaled<3>(v[x], u[16 * x], zp + box * 512 + 128 * x, zp + 1024 + box * 512 + 128 * x);
+            } else {
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    put_scaled<1>(v[x], u[16 * x], zp + box * 512 + 128 * x, nullptr);
+            }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[ZDONE + zb]);
+        return true;
+    };
 
     if (warp == 0) {
         if (lane == 0) {
@@ -522,6 +557,7 @@ hda_tc_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ T
             mask[e] = d >= 0 ? pw[d] * (m.a_in / fmaxf(pw[rev ? kC - 1 - i : i + 1], kLeastF)) : 0.f;
         }
         for (int c = 0; c < n; ++c) {
+            if (exact && !scale_Z(c, (warp - 10) * 32 + lane, 1, Dz / 64)) { ok = false; break; }
             if (!__all_sync(0xffffffffu, wait_bar(&bars[PFULL], par(c)))) { ok = false; break; }
             tc_fence_after();
             uint8_t *pt = sm + P + (c & 1) * 8192;
@@ -553,42 +589,9 @@ hda_tc_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ T
         __syncwarp();
     } else if (warp >= 14) {
         // ------------------------------------------------------------ diag(u) Z
-        // 16-byte vectors ct + 128 x of the Z tile: token (ct / 8 + 16 x) % 64. The product keeps
-        // the tile's layout, so the swizzle does not matter here.
-        const int ct = (warp - 14) * 32 + lane;
-        int zb = 0, zuse = 0;
-        for (int c = 0, s = 0, use = 0; c < n; ++c) {
-            const bool w = wait_bar(&bars[QFULL + s], par(use)) &&
-                           (zuse == 0 || wait_bar(&bars[ZFREE + zb], par(zuse - 1)));
-            if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
-            const float *u = reinterpret_cast<const float *>(sm + (cb + c == a.nchunks - 1 ? FUL : FU)) + (ct >> 3);
-            const uint4 *zs = reinterpret_cast<const uint4 *>(sm + s * STAGE + Z) + ct;
-            uint4 *zp = reinterpret_cast<uint4 *>(sm + ZP + zb * 16384) + ct;
-#pragma unroll 1
-            for (int box = 0; box < Dz / 64; ++box) {
-                uint4 v[4];
-#pragma unroll
-                for (int x = 0; x < 4; ++x) v[x] = zs[box * 512 + 128 * x];
-                if (exact) {
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) put_scaled<3>(v[x], u[16 * x], zp + box * 512 + 128 * x);
-                } else {
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) put_scaled<1>(v[x], u[16 * x], zp + box * 512 + 128 * x);
-                }
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars[ZDONE + zb]);
-            if (++zb == nzb) {
-                zb = 0;
-                ++zuse;
-            }
-            if (++s == NQ) {
-                s = 0;
-                ++use;
-            }
-        }
+        // (in three parts, the second box is the P warps')
+        for (int c = 0; ok && c < n; ++c)
+            ok = scale_Z(c, (warp - 14) * 32 + lane, 0, exact ? 1 : Dz / 64);
         __syncwarp();
     } else {
         // ------------------------------------------------------------ state
@@ -623,8 +626,7 @@ hda_tc_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ T
         for (int c = 0; c <= n; ++c) {
             const bool last = c == n;
             if (last && !exact) break;
-            bool w = c == 0 || wait_bar(&bars[UDONE], par(c - 1));
-            w = w && (c == 0 || last || wait_bar(&bars[SBFREE], par(c - 1)));
+            const bool w = c == 0 || wait_bar(&bars[UDONE], par(c - 1));
             if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
             tc_fence_after();
             const float carry = c > 0 ? pw[chunk_tokens(cb + c - 1, a)] : 1.f;
@@ -668,6 +670,11 @@ hda_tc_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ T
                     tmem_ld32f(tmem_addr(tm, j, COL_S + q), sv);
                 }
                 if (!last) {
+                    // the snapshot was last read by I(c - 1)
+                    if (q == 0 && c > 0) {
+                        if (!__all_sync(0xffffffffu, wait_bar(&bars[SBFREE], par(c - 1)))) ok = false;
+                        tc_fence_after();
+                    }
                     uint32_t pk[16];
 #pragma unroll
                     for (int x = 0; x < 16; ++x) pk[x] = pack_bf16(sv[2 * x], sv[2 * x + 1]);
@@ -677,6 +684,7 @@ hda_tc_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ T
                     for (int x = 0; x < 32; ++x) fp[(q + x) * Dz] = sv[x];
                 }
             }
+            if (!ok) break;
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
@@ -695,17 +703,21 @@ hda_tc_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ T
 }
 
 // ======================================================================= state kernel
-// Stages of y, z and, over z and behind it, the parts of diag(u) Z.
+// Stages of y and z, the latter overwritten with the first part of diag(u) Z. Their number is even:
+// each stage then belongs to one of the two groups of scaling warps, which sees every use of it
+// (a parity tells a use from the last one, not from the one before).
 namespace st {
-constexpr uint32_t Y = 0, Z = 16384;
-constexpr uint32_t BYTES = 6 * 32768;            // 6 stages of one part, or 3 of three
-constexpr uint32_t PW = BYTES;
+constexpr uint32_t Y = 0, Z = 16384, STAGE = 32768;
+constexpr uint32_t REST = 4 * STAGE;             // three parts: the others, a buffer for each group
+constexpr uint32_t PW = 6 * STAGE;               // (6 stages of one part, or 4 and the buffers)
 constexpr uint32_t BAR = PW + 320;
-constexpr uint32_t TSLOT = BAR + 19 * 8;
-constexpr uint32_t ALLOC = TSLOT + 24 + 1024;
+constexpr uint32_t NBAR = 26;
+constexpr uint32_t TSLOT = BAR + NBAR * 8;
+constexpr uint32_t ALLOC = TSLOT + 16 + 1024;
 static_assert(ALLOC <= 232448, "state kernel shared memory");
 }  // namespace st
-constexpr int kStateThreads = 320;   // 0 TMA, 1 MMA, 2-9 diag(u) Z
+// 0 TMA, 1 MMA, 2-5 and 6-9 diag(u) Z of every other chunk, 10-17 the sum of the accumulators
+constexpr int kStateThreads = 576;
 
 struct StateProblem {
     float *E;               // [BH][(splits - 1) pieces][Dx][Dz]
@@ -732,12 +744,14 @@ __global__ void __launch_bounds__(kStateThreads, 1)
 hda_tc_state_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ TcArgs a,
                     const __grid_constant__ StateArgs sa) {
     using namespace st;
-    constexpr int NS = kParts == 1 ? 6 : 3;
-    constexpr uint32_t STAGE = 16384 + kParts * 16384;
-    // With three parts every chunk has an accumulator of its own (two take turns), added up in
-    // registers: a sum over many chunks in the accumulator would be cut off at each step.
-    constexpr bool kDrain = kParts == 3;
-    enum { SFULL = 0, SEMPTY = NS, SZDONE = 2 * NS, SEND = 3 * NS, SDONE = SEND + 1, SREAD = SDONE + 2 };
+    constexpr int NS = kParts == 1 ? 6 : 4;
+    static_assert(NS % 2 == 0 && (kParts == 1 || kParts == 3), "stages of the state kernel");
+    // Three parts: an accumulator takes kRun chunks, two take turns, and their sums are added in
+    // registers (a sum over many chunks in the accumulator would be cut off at each step).
+    constexpr int kRun = kParts == 3 ? 2 : 1 << 30;
+    enum { SFULL = 0, SEMPTY = NS, SZDONE = 2 * NS, SDONE = 3 * NS, SREAD = SDONE + 2, SZFREE = SREAD + 2,
+           SEND = SZFREE + 2 };
+    static_assert(SEND < (int)NBAR, "state kernel barrier map");
     extern __shared__ uint8_t smraw[];
     uint8_t *sm = align1024(smraw);
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + BAR);
@@ -762,11 +776,12 @@ hda_tc_state_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__
         for (int i = 0; i < NS; ++i) {
             mbar_init(&bars[SFULL + i], 1);
             mbar_init(&bars[SEMPTY + i], 1);
-            mbar_init(&bars[SZDONE + i], 8);
+            mbar_init(&bars[SZDONE + i], 4);
         }
-        for (int i = 0; kDrain && i < 2; ++i) {
+        for (int i = 0; i < 2; ++i) {
             mbar_init(&bars[SDONE + i], 1);
             mbar_init(&bars[SREAD + i], 8);
+            mbar_init(&bars[SZFREE + i], 1);
         }
         mbar_init(&bars[SEND], 1);
         fence_mbar_init();
@@ -805,24 +820,28 @@ hda_tc_state_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__
         const uint32_t idU = idesc_bf16(128, Dx, 1, 1);
         const uint64_t dY = smem_desc(smem_u32(sm) + Y, 8192, 1024);
         const uint64_t dZ = smem_desc(smem_u32(sm) + Z, 8192, 1024);
+        const uint64_t dRest = smem_desc(smem_u32(sm) + REST, 8192, 1024);
         for (int c = 0; c < n; ++c) {
-            const bool w = wait_bar(&bars[SZDONE + c % NS], par(c / NS)) &&
-                           (!kDrain || c < 2 || wait_bar(&bars[SREAD + (c & 1)], par((c >> 1) - 1)));
+            const int run = c / kRun, buf = run & 1;    // (run 0 alone with one part)
+            const bool first = c % kRun == 0, w = wait_bar(&bars[SZDONE + c % NS], par(c / NS)) &&
+                               (!first || run < 2 || wait_bar(&bars[SREAD + buf], par((run >> 1) - 1)));
             if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
             tc_fence_after();
             const uint64_t so = (uint64_t)((c % NS) * (STAGE >> 4));
-            const uint32_t acc = tm + (kDrain ? (c & 1) * 128 : 0);
+            const uint64_t rest = dRest + (uint64_t)((c & 1) * (STAGE >> 4));
             if (elect_one()) {
                 // the small parts first
 #pragma unroll
                 for (int part = kParts - 1; part >= 0; --part)
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        mma_ss(acc, dZ + so + part * (16384 >> 4) + kk * (2048 >> 4),
+                        mma_ss(tm + buf * 128,
+                               (part ? rest + (part - 1) * (16384 >> 4) : dZ + so) + kk * (2048 >> 4),
                                dY + so + kk * (2048 >> 4), idU,
-                               ((!kDrain && c > 0) || part < kParts - 1 || kk > 0) ? 1u : 0u);
+                               (!first || part < kParts - 1 || kk > 0) ? 1u : 0u);
                 mma_commit(&bars[SEMPTY + c % NS]);
-                if (kDrain) mma_commit(&bars[SDONE + (c & 1)]);
+                if (kParts == 3) mma_commit(&bars[SZFREE + (c & 1)]);
+                if ((c + 1) % kRun == 0 || c + 1 == n) mma_commit(&bars[SDONE + buf]);
             }
             __syncwarp();
         }
@@ -830,62 +849,57 @@ hda_tc_state_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__
         __syncwarp();
         if (!wait_bar(&bars[SEND], 0)) ok = false;
         __syncwarp();
+    } else if (warp < 10) {
+        const int ct = ((warp - 2) & 3) * 32 + lane;    // 16-byte vectors ct + 128 x: tokens row + 16 x
+        for (int c = (warp - 2) >> 2; c < n; c += 2) {
+            const int s = c % NS;
+            // c chunks of 64 tokens follow this one in the piece
+            const float after = m.a_in * decay_pow(g, (float)(kC * c));
+            float u[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) u[x] = after * state_factor(pw, (ct >> 3) + 16 * x, kC, rev);
+            const bool w = wait_bar(&bars[SFULL + s], par(c / NS)) &&
+                           (kParts == 1 || c < 2 || wait_bar(&bars[SZFREE + (c & 1)], par((c >> 1) - 1)));
+            if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
+            uint4 *rest = reinterpret_cast<uint4 *>(sm + REST + (c & 1) * STAGE) + ct;
+            uint4 *zs = reinterpret_cast<uint4 *>(sm + s * STAGE + Z) + ct;
+#pragma unroll 1
+            for (int box = 0; box < Dz / 64; ++box) {
+                uint4 v[4];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) v[x] = zs[box * 512 + 128 * x];
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    put_scaled<kParts>(v[x], u[x], zs + box * 512 + 128 * x, rest + box * 512 + 128 * x);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[SZDONE + s]);
+        }
+        __syncwarp();
     } else {
-        const int ct = (warp - 2) * 32 + lane;      // 0..255
-        const int row = ct >> 3;                    // tokens row and row + 32
         // E^T: lanes z (quarter j), columns x (half) in registers
-        const int j = warp & 3, half = (warp - 2) >> 2, z = j * 32 + lane;
+        const int j = warp & 3, half = (warp - 10) >> 2, z = j * 32 + lane;
         const bool mine = 64 * half < Dx;
         float S[64];
 #pragma unroll
         for (int x = 0; x < 64; ++x) S[x] = 0.f;
-        auto add_D = [&](uint32_t col) {
+        const int runs = (n - 1) / kRun + 1;
+        for (int r = 0; r < runs; ++r) {
+            if (!__all_sync(0xffffffffu, wait_bar(&bars[SDONE + (r & 1)], par(r >> 1)))) { ok = false; break; }
             tc_fence_after();
             if (mine) {
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
                     float d[32];
-                    tmem_ld32f(tmem_addr(tm, j, col + 64 * half + 32 * q), d);
+                    tmem_ld32f(tmem_addr(tm, j, (r & 1) * 128 + 64 * half + 32 * q), d);
 #pragma unroll
                     for (int x = 0; x < 32; ++x) S[32 * q + x] += d[x];
                 }
             }
-        };
-        auto drain = [&](int c) -> bool {
-            if (!__all_sync(0xffffffffu, wait_bar(&bars[SDONE + (c & 1)], par(c >> 1)))) return false;
-            add_D((c & 1) * 128);
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bars[SREAD + (c & 1)]);
-            return true;
-        };
-        for (int c = 0; c < n; ++c) {
-            const int s = c % NS;
-            if (!__all_sync(0xffffffffu, wait_bar(&bars[SFULL + s], par(c / NS)))) { ok = false; break; }
-            // c chunks of 64 tokens follow this one in the piece
-            const float after = m.a_in * decay_pow(g, (float)(kC * c));
-            float u[2];
-#pragma unroll
-            for (int x = 0; x < 2; ++x) u[x] = after * state_factor(pw, row + 32 * x, kC, rev);
-            uint4 *zs = reinterpret_cast<uint4 *>(sm + s * STAGE + Z) + ct;
-            const int vecs = Dz / 64 * 2;
-            uint4 v[4];
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-                if (x < vecs) v[x] = zs[256 * x];
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-                if (x < vecs) put_scaled<kParts>(v[x], u[x & 1], zs + 256 * x);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars[SZDONE + s]);
-            if (kDrain && c > 0 && !drain(c - 1)) { ok = false; break; }
-        }
-        if (kDrain) {
-            ok = ok && (n == 0 || drain(n - 1));
-        } else if (ok && n > 0) {
-            ok = __all_sync(0xffffffffu, wait_bar(&bars[SEND], 0));
-            if (ok) add_D(0);
+            if (lane == 0) mbar_arrive(&bars[SREAD + (r & 1)]);
         }
         if (ok && mine && z < Dz) {
             float *ep = sp.E + ((size_t)bh * npc + pi) * (Dx * Dz) + z;
