@@ -1,27 +1,87 @@
-// Group norm with an activation, channels last (forward and backward).
+// Group norm with an activation, channels last (forward and backward), and an optional gate:
+//     u = (x - mean) rstd w + b;   y = act(u), or u act(gate)
+//     du = dy act'(u), or dy act(gate);  dgate = dy u act'(gate)
+//     dx = rstd (du w - mean(du w) - xhat mean(du w xhat));  dw = sum du xhat;  db = sum du
+//
+// Every element is read once or twice and written once, so HBM bandwidth bounds all of it. Three
+// routes, by shape:
+//   rows : L = 1 and a group's channels fit the registers of a warp's lanes: one pass. A segment
+//          of W lanes (a power of two) owns one group and walks over entries, so weights and the
+//          channel sums of the backward pass stay in registers.
+//   maps : L > 1 (or wide groups): the positions of an entry are cut into parts, one CTA each;
+//          a first kernel leaves each part's statistics, a second one combines them and writes.
+//          The second reading of x comes from L2 when the tensor fits there.
+//   plain: whatever does not come in whole 16-byte vectors of one group: a CTA per group.
+// Means and variances: each thread takes the exact mean and squared deviations of a few values at a
+// time and merges them with what it has (count, mean, M2), threads and parts are merged the same
+// way, in a fixed order; no variance is a difference of squares.
 #include <cuda_bf16.h>
 
 #include "gla_internal.h"
 #include "norm.h"
+#include "tc_ptx.cuh"
 
 namespace gla {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
 
 __device__ __forceinline__ float get(const float *p) { return *p; }
 __device__ __forceinline__ float get(const __nv_bfloat16 *p) { return __bfloat162float(*p); }
 __device__ __forceinline__ void put(float *p, float x) { *p = x; }
 __device__ __forceinline__ void put(__nv_bfloat16 *p, float x) { *p = __float2bfloat16_rn(x); }
 
+// 16 bytes as floats.
+template <typename T>
+struct Vec;
+template <>
+struct Vec<float> {
+    static constexpr int n = 4;
+    static __device__ __forceinline__ void unpack(uint4 v, float (&f)[4]) {
+        f[0] = __uint_as_float(v.x);
+        f[1] = __uint_as_float(v.y);
+        f[2] = __uint_as_float(v.z);
+        f[3] = __uint_as_float(v.w);
+    }
+    static __device__ __forceinline__ uint4 pack(const float (&f)[4]) {
+        return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                          __float_as_uint(f[3]));
+    }
+};
+template <>
+struct Vec<__nv_bfloat16> {
+    static constexpr int n = 8;
+    static __device__ __forceinline__ void unpack(uint4 v, float (&f)[8]) {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[2 * i] = __uint_as_float(w[i] << 16);
+            f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    }
+    static __device__ __forceinline__ uint4 pack(const float (&f)[8]) {
+        return make_uint4(tc::pack_bf16(f[0], f[1]), tc::pack_bf16(f[2], f[3]), tc::pack_bf16(f[4], f[5]),
+                          tc::pack_bf16(f[6], f[7]));
+    }
+};
+
+// The logistic function. Results that are rounded to bf16 take the fast exponential and division
+// (a few 2^-22 of the value); the exact ones would make the kernels bound by arithmetic.
+template <typename T>
+__device__ __forceinline__ float logistic(float u) {
+    return sizeof(T) == 2 ? __fdividef(1.f, 1.f + __expf(-u)) : 1.f / (1.f + expf(-u));
+}
+template <typename T>
 __device__ __forceinline__ float act_of(float u, int act) {
-    if (act == 1) return u / (1.f + expf(-u));
+    if (act == 1) return u * logistic<T>(u);
     if (act == 2) return 0.5f * u * (1.f + erff(u * 0.70710678f));
     return u;
 }
+template <typename T>
 __device__ __forceinline__ float act_grad(float u, int act) {
     if (act == 1) {
-        const float s = 1.f / (1.f + expf(-u));
+        const float s = logistic<T>(u);
         return s * (1.f + u * (1.f - s));
     }
     if (act == 2)
@@ -29,22 +89,521 @@ __device__ __forceinline__ float act_grad(float u, int act) {
     return 1.f;
 }
 
+// Count, mean and sum of squared deviations of some values.
+struct Stat {
+    float n, mean, m2;
+};
+__device__ __forceinline__ Stat merge(const Stat &a, const Stat &b) {
+    const float n = a.n + b.n;
+    if (n == 0.f) return a;
+    const float d = b.mean - a.mean, f = b.n / n;
+    return Stat{n, fmaf(d, f, a.mean), a.m2 + b.m2 + d * d * a.n * f};
+}
+__device__ __forceinline__ Stat merge_lanes(Stat s, int width) {
+    for (int o = width >> 1; o > 0; o >>= 1) {
+        // both partners form the same sum: the lower lane's part first
+        const Stat t{__shfl_xor_sync(0xffffffffu, s.n, o), __shfl_xor_sync(0xffffffffu, s.mean, o),
+                     __shfl_xor_sync(0xffffffffu, s.m2, o)};
+        s = (threadIdx.x & o) ? merge(t, s) : merge(s, t);
+    }
+    return s;
+}
+__device__ __forceinline__ float sum_lanes(float v, int width) {
+    for (int o = width >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+template <int N>
+__device__ __forceinline__ Stat stat_of(const float (&f)[N]) {
+    float s = 0.f, q = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) s += f[i];
+    const float mean = s * (1.f / N);
+#pragma unroll
+    for (int i = 0; i < N; ++i) q = fmaf(f[i] - mean, f[i] - mean, q);
+    return Stat{(float)N, mean, q};
+}
+
+// 8 (or 4) weights from memory, or their default.
+template <int N>
+__device__ __forceinline__ void load_param(const float *p, int64_t c, float otherwise, float (&f)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) f[i] = p ? p[c + i] : otherwise;
+}
+
+// What the backward pass makes of one vector: xhat, du, and dgate in place of z.
+template <typename T, bool kGate, int V>
+__device__ __forceinline__ void grad_vec(float (&x)[V], float (&dy)[V], float (&z)[V], const float (&w)[V],
+                                         const float (&b)[V], float mean, float rstd, int act) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        x[i] = (x[i] - mean) * rstd;
+        const float u = fmaf(x[i], w[i], b[i]);
+        if (kGate) {
+            float a, g;
+            if (act == 1) {     // both of silu's from one logistic
+                const float s = logistic<T>(z[i]);
+                a = z[i] * s;
+                g = s * (1.f + z[i] * (1.f - s));
+            } else {
+                a = act_of<T>(z[i], act);
+                g = act_grad<T>(z[i], act);
+            }
+            z[i] = dy[i] * u * g;
+            dy[i] *= a;
+        } else {
+            dy[i] *= act_grad<T>(u, act);
+        }
+    }
+}
+
+// ======================================================================= rows
+// Lanes of a segment, vectors of a lane, and how segments share the work of a CTA.
+struct RowPlan {
+    int W;          // lanes per group
+    int gpc;        // groups of a CTA (grid y covers all)
+    int rp;         // entries a CTA handles at a time
+};
+
+template <typename T, int VPL, bool kGate>
+__global__ void __launch_bounds__(kThreads)
+norm_rows_fwd(const __grid_constant__ NormProblem p, const RowPlan r) {
+    constexpr int V = Vec<T>::n;
+    const int cg = (int)(p.C / p.G), nv = cg / V;
+    const int seg = threadIdx.x / r.W, lane = threadIdx.x % r.W;
+    const int64_t g = (int64_t)blockIdx.y * r.gpc + seg % r.gpc;
+    const int64_t n0 = (int64_t)blockIdx.x * r.rp + seg / r.gpc, step = (int64_t)gridDim.x * r.rp;
+    const bool live = g < p.G && seg / r.gpc < r.rp;
+    const int64_t c0 = (live ? g : 0) * cg;
+    float w[VPL][V], b[VPL][V];
+#pragma unroll
+    for (int k = 0; k < VPL; ++k) {
+        const int v = lane + k * r.W;
+        const int64_t c = c0 + (v < nv ? v : 0) * V;
+        load_param(p.w, c, 1.f, w[k]);
+        load_param(p.b, c, 0.f, b[k]);
+    }
+    // the whole warp walks together (the shuffles need every lane): rows past the end do nothing
+    const int64_t rounds = (p.N - (int64_t)blockIdx.x * r.rp + step - 1) / step;
+    for (int64_t it = 0; it < rounds; ++it) {
+        const int64_t n = n0 + it * step;
+        const bool in = live && n < p.N;
+        const T *xp = static_cast<const T *>(p.x) + n * p.x_n + c0;
+        const T *zp = static_cast<const T *>(p.gate) + (kGate ? n * p.gate_n + c0 : 0);
+        float x[VPL][V];
+        uint4 zv[VPL];
+        Stat s{0.f, 0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < VPL; ++k) {
+            const int v = lane + k * r.W;
+            uint4 xv = make_uint4(0, 0, 0, 0);
+            zv[k] = xv;
+            if (in && v < nv) {
+                xv = *reinterpret_cast<const uint4 *>(xp + v * V);
+                if (kGate) zv[k] = *reinterpret_cast<const uint4 *>(zp + v * V);
+            }
+            Vec<T>::unpack(xv, x[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < VPL; ++k)
+            if (lane + k * r.W < nv) s = merge(s, stat_of(x[k]));
+        s = merge_lanes(s, r.W);
+        const float rstd = 1.f / sqrtf(s.m2 / (float)cg + p.eps);
+        if (!in) continue;
+        if (lane == 0) {
+            if (p.mean) p.mean[n * p.G + g] = s.mean;
+            if (p.rstd) p.rstd[n * p.G + g] = rstd;
+        }
+        T *yp = static_cast<T *>(p.y) + n * p.C + c0;
+#pragma unroll
+        for (int k = 0; k < VPL; ++k) {
+            const int v = lane + k * r.W;
+            if (v >= nv) continue;
+            float z[V];
+            if (kGate) Vec<T>::unpack(zv[k], z);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const float u = fmaf((x[k][i] - s.mean) * rstd, w[k][i], b[k][i]);
+                x[k][i] = kGate ? u * act_of<T>(z[i], p.act) : act_of<T>(u, p.act);
+            }
+            *reinterpret_cast<uint4 *>(yp + v * V) = Vec<T>::pack(x[k]);
+        }
+    }
+}
+
+// Partial channel sums: sums[part][0: dw, 1: db][C], part = blockIdx.x * rp + the entry slot.
+template <typename T, int VPL, bool kGate>
+__global__ void __launch_bounds__(kThreads)
+norm_rows_bwd(const __grid_constant__ NormProblem p, const RowPlan r, float *sums) {
+    constexpr int V = Vec<T>::n;
+    const int cg = (int)(p.C / p.G), nv = cg / V;
+    const int seg = threadIdx.x / r.W, lane = threadIdx.x % r.W;
+    const int64_t g = (int64_t)blockIdx.y * r.gpc + seg % r.gpc;
+    const int64_t n0 = (int64_t)blockIdx.x * r.rp + seg / r.gpc, step = (int64_t)gridDim.x * r.rp;
+    const bool live = g < p.G && seg / r.gpc < r.rp;
+    const int64_t c0 = (live ? g : 0) * cg;
+    float w[VPL][V], b[VPL][V], dw[VPL][V], db[VPL][V];
+#pragma unroll
+    for (int k = 0; k < VPL; ++k) {
+        const int v = lane + k * r.W;
+        const int64_t c = c0 + (v < nv ? v : 0) * V;
+        load_param(p.w, c, 1.f, w[k]);
+        load_param(p.b, c, 0.f, b[k]);
+#pragma unroll
+        for (int i = 0; i < V; ++i) dw[k][i] = db[k][i] = 0.f;
+    }
+    const float inv = 1.f / (float)cg;
+    const int64_t rounds = (p.N - (int64_t)blockIdx.x * r.rp + step - 1) / step;
+    for (int64_t it = 0; it < rounds; ++it) {
+        const int64_t n = n0 + it * step;
+        const bool in = live && n < p.N;
+        const T *xp = static_cast<const T *>(p.x) + n * p.x_n + c0;
+        const T *dp = static_cast<const T *>(p.dy) + n * p.dy_n + c0;
+        const T *zp = static_cast<const T *>(p.gate) + (kGate ? n * p.gate_n + c0 : 0);
+        uint4 xv[VPL], dv[VPL], zv[VPL];
+#pragma unroll
+        for (int k = 0; k < VPL; ++k) {
+            const int v = lane + k * r.W;
+            xv[k] = dv[k] = zv[k] = make_uint4(0, 0, 0, 0);
+            if (in && v < nv) {
+                xv[k] = *reinterpret_cast<const uint4 *>(xp + v * V);
+                dv[k] = *reinterpret_cast<const uint4 *>(dp + v * V);
+                if (kGate) zv[k] = *reinterpret_cast<const uint4 *>(zp + v * V);
+            }
+        }
+        const float mean = in ? p.mean[n * p.G + g] : 0.f, rstd = in ? p.rstd[n * p.G + g] : 0.f;
+        float x[VPL][V], d[VPL][V], z[V];
+        float s1 = 0.f, s2 = 0.f;
+        T *gp = static_cast<T *>(p.dgate) + (kGate ? n * p.C + c0 : 0);
+#pragma unroll
+        for (int k = 0; k < VPL; ++k) {
+            const int v = lane + k * r.W;
+            Vec<T>::unpack(xv[k], x[k]);
+            Vec<T>::unpack(dv[k], d[k]);
+            Vec<T>::unpack(zv[k], z);
+            grad_vec<T, kGate>(x[k], d[k], z, w[k], b[k], mean, rstd, p.act);
+            if (!in || v >= nv) continue;
+            if (kGate) *reinterpret_cast<uint4 *>(gp + v * V) = Vec<T>::pack(z);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                dw[k][i] = fmaf(d[k][i], x[k][i], dw[k][i]);
+                db[k][i] += d[k][i];
+                d[k][i] *= w[k][i];
+                s1 += d[k][i];
+                s2 = fmaf(d[k][i], x[k][i], s2);
+            }
+        }
+        s1 = sum_lanes(s1, r.W) * inv;
+        s2 = sum_lanes(s2, r.W) * inv;
+        if (!in) continue;
+        T *op = static_cast<T *>(p.dx) + n * p.C + c0;
+#pragma unroll
+        for (int k = 0; k < VPL; ++k) {
+            const int v = lane + k * r.W;
+            if (v >= nv) continue;
+#pragma unroll
+            for (int i = 0; i < V; ++i) x[k][i] = rstd * (d[k][i] - s1 - x[k][i] * s2);
+            *reinterpret_cast<uint4 *>(op + v * V) = Vec<T>::pack(x[k]);
+        }
+    }
+    if (!sums || !live) return;
+    float *sp = sums + ((int64_t)blockIdx.x * r.rp + seg / r.gpc) * 2 * p.C;
+#pragma unroll
+    for (int k = 0; k < VPL; ++k) {
+        const int v = lane + k * r.W;
+        if (v >= nv) continue;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            sp[c0 + v * V + i] = dw[k][i];
+            sp[p.C + c0 + v * V + i] = db[k][i];
+        }
+    }
+}
+
+// ======================================================================= maps
+// CTA = (part of the positions, block of whole groups, entry). Thread (tx, ty) owns one vector column
+// and every ry-th position.
+struct MapPlan {
+    int parts;      // of an entry's positions
+    int nvb;        // vector columns of a block (a multiple of a group's)
+    int ry;         // positions at a time
+};
+struct MapPos {
+    int tx, ty;
+    int64_t n, l0, l1, v;   // v: vector column in the row
+    bool live;
+};
+__device__ __forceinline__ MapPos map_pos(const NormProblem &p, const MapPlan &m, int V) {
+    MapPos q;
+    q.tx = threadIdx.x % m.nvb;
+    q.ty = threadIdx.x / m.nvb;
+    q.n = blockIdx.z;
+    q.l0 = p.L * blockIdx.x / m.parts;
+    q.l1 = p.L * (blockIdx.x + 1) / m.parts;
+    q.v = (int64_t)blockIdx.y * m.nvb + q.tx;
+    q.live = q.ty < m.ry && q.v < p.C / V;
+    return q;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads)
+norm_maps_stats(const __grid_constant__ NormProblem p, const MapPlan m, Stat *part) {
+    constexpr int V = Vec<T>::n, kAhead = 4;
+    tc::pdl_launch_dependents();
+    __shared__ Stat sh[kThreads];
+    const MapPos q = map_pos(p, m, V);
+    Stat s{0.f, 0.f, 0.f};
+    if (q.live) {
+        const T *xp = static_cast<const T *>(p.x) + q.n * p.x_n + q.v * V;
+        for (int64_t l = q.l0 + q.ty; l < q.l1; l += (int64_t)m.ry * kAhead) {
+            uint4 xv[kAhead];
+#pragma unroll
+            for (int a = 0; a < kAhead; ++a)
+                if (l + a * m.ry < q.l1) xv[a] = *reinterpret_cast<const uint4 *>(xp + (l + a * m.ry) * p.x_l);
+#pragma unroll
+            for (int a = 0; a < kAhead; ++a)
+                if (l + a * m.ry < q.l1) {
+                    float f[V];
+                    Vec<T>::unpack(xv[a], f);
+                    s = merge(s, stat_of(f));
+                }
+        }
+    }
+    sh[threadIdx.x] = s;
+    __syncthreads();
+    // a warp per group: its columns and position slots
+    const int nv = (int)(p.C / p.G) / V, groups = m.nvb / nv, lane = threadIdx.x & 31;
+    for (int g = threadIdx.x >> 5; g < groups; g += kWarps) {
+        Stat t{0.f, 0.f, 0.f};
+        for (int e = lane; e < nv * m.ry; e += 32) t = merge(t, sh[e / nv * m.nvb + g * nv + e % nv]);
+        t = merge_lanes(t, 32);
+        const int64_t gg = (int64_t)blockIdx.y * groups + g;
+        if (lane == 0 && gg < p.G) part[((int64_t)q.n * m.parts + blockIdx.x) * p.G + gg] = t;
+    }
+}
+
+// Statistics of the block's groups from those of the parts -> shared memory.
+__device__ __forceinline__ void load_stats(const NormProblem &p, const MapPlan &m, const Stat *part, int groups,
+                                           float *mean, float *rstd) {
+    const int lane = threadIdx.x & 31;
+    for (int g = threadIdx.x >> 5; g < groups; g += kWarps) {
+        const int64_t gg = (int64_t)blockIdx.y * groups + g;
+        if (gg >= p.G) break;
+        Stat t{0.f, 0.f, 0.f};
+        for (int e = lane; e < m.parts; e += 32)
+            t = merge(t, part[((int64_t)blockIdx.z * m.parts + e) * p.G + gg]);
+        t = merge_lanes(t, 32);
+        if (lane == 0) {
+            mean[g] = t.mean;
+            rstd[g] = 1.f / sqrtf(t.m2 / t.n + p.eps);
+            if (blockIdx.x == 0) {
+                if (p.mean) p.mean[blockIdx.z * p.G + gg] = mean[g];
+                if (p.rstd) p.rstd[blockIdx.z * p.G + gg] = rstd[g];
+            }
+        }
+    }
+    __syncthreads();
+}
+
+template <typename T, bool kGate>
+__global__ void __launch_bounds__(kThreads)
+norm_maps_apply(const __grid_constant__ NormProblem p, const MapPlan m, const Stat *part) {
+    constexpr int V = Vec<T>::n, kAhead = 2;
+    __shared__ float sm[kThreads], sr[kThreads];
+    const MapPos q = map_pos(p, m, V);
+    float w[V], b[V];
+    const int64_t c = (q.live ? q.v : 0) * V;
+    load_param(p.w, c, 1.f, w);
+    load_param(p.b, c, 0.f, b);
+    tc::pdl_wait_prerequisites();
+    const int nv = (int)(p.C / p.G) / V;
+    load_stats(p, m, part, m.nvb / nv, sm, sr);
+    if (!q.live) return;
+    const float mean = sm[q.tx / nv], rstd = sr[q.tx / nv];
+    const T *xp = static_cast<const T *>(p.x) + q.n * p.x_n + c;
+    const T *zp = static_cast<const T *>(p.gate) + (kGate ? q.n * p.gate_n + c : 0);
+    T *yp = static_cast<T *>(p.y) + q.n * p.L * p.C + c;
+    for (int64_t l = q.l0 + q.ty; l < q.l1; l += (int64_t)m.ry * kAhead) {
+        uint4 xv[kAhead], zv[kAhead];
+#pragma unroll
+        for (int a = 0; a < kAhead; ++a)
+            if (l + a * m.ry < q.l1) {
+                xv[a] = *reinterpret_cast<const uint4 *>(xp + (l + a * m.ry) * p.x_l);
+                if (kGate) zv[a] = *reinterpret_cast<const uint4 *>(zp + (l + a * m.ry) * p.gate_l);
+            }
+#pragma unroll
+        for (int a = 0; a < kAhead; ++a)
+            if (l + a * m.ry < q.l1) {
+                float f[V], z[V];
+                Vec<T>::unpack(xv[a], f);
+                if (kGate) Vec<T>::unpack(zv[a], z);
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const float u = fmaf((f[i] - mean) * rstd, w[i], b[i]);
+                    f[i] = kGate ? u * act_of<T>(z[i], p.act) : act_of<T>(u, p.act);
+                }
+                *reinterpret_cast<uint4 *>(yp + (l + a * m.ry) * p.C) = Vec<T>::pack(f);
+            }
+    }
+}
+
+// Sums of du w and du w xhat of each part and group -> part; channel sums -> sums[entry, part][2][C].
+template <typename T, bool kGate>
+__global__ void __launch_bounds__(kThreads)
+norm_maps_bwd_stats(const __grid_constant__ NormProblem p, const MapPlan m, float2 *part, float *sums) {
+    constexpr int V = Vec<T>::n;
+    tc::pdl_launch_dependents();
+    __shared__ float2 sh[kThreads];
+    extern __shared__ float ch[];      // [threads][2 V] channel sums of the position slots
+    const MapPos q = map_pos(p, m, V);
+    const int nv = (int)(p.C / p.G) / V;
+    float dw[V], db[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) dw[i] = db[i] = 0.f;
+    float s1 = 0.f, s2 = 0.f;
+    if (q.live) {
+        const int64_t c = q.v * V, at = q.n * p.G + q.v / nv;
+        float w[V], b[V];
+        load_param(p.w, c, 1.f, w);
+        load_param(p.b, c, 0.f, b);
+        const float mean = p.mean[at], rstd = p.rstd[at];
+        const T *xp = static_cast<const T *>(p.x) + q.n * p.x_n + c;
+        const T *dp = static_cast<const T *>(p.dy) + q.n * p.dy_n + c;
+        const T *zp = static_cast<const T *>(p.gate) + (kGate ? q.n * p.gate_n + c : 0);
+#pragma unroll 2
+        for (int64_t l = q.l0 + q.ty; l < q.l1; l += m.ry) {
+            float x[V], d[V], z[V];
+            Vec<T>::unpack(*reinterpret_cast<const uint4 *>(xp + l * p.x_l), x);
+            Vec<T>::unpack(*reinterpret_cast<const uint4 *>(dp + l * p.dy_l), d);
+            if (kGate) Vec<T>::unpack(*reinterpret_cast<const uint4 *>(zp + l * p.gate_l), z);
+            grad_vec<T, kGate>(x, d, z, w, b, mean, rstd, p.act);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                dw[i] = fmaf(d[i], x[i], dw[i]);
+                db[i] += d[i];
+                s1 = fmaf(d[i], w[i], s1);
+                s2 = fmaf(d[i] * w[i], x[i], s2);
+            }
+        }
+    }
+    sh[threadIdx.x] = make_float2(s1, s2);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        ch[threadIdx.x * 2 * V + i] = dw[i];
+        ch[threadIdx.x * 2 * V + V + i] = db[i];
+    }
+    __syncthreads();
+    const int groups = m.nvb / nv, lane = threadIdx.x & 31;
+    for (int g = threadIdx.x >> 5; g < groups; g += kWarps) {
+        float a = 0.f, b = 0.f;
+        for (int e = lane; e < nv * m.ry; e += 32) {
+            const float2 t = sh[e / nv * m.nvb + g * nv + e % nv];
+            a += t.x;
+            b += t.y;
+        }
+        a = sum_lanes(a, 32);
+        b = sum_lanes(b, 32);
+        const int64_t gg = (int64_t)blockIdx.y * groups + g;
+        if (lane == 0 && gg < p.G) part[((int64_t)q.n * m.parts + blockIdx.x) * p.G + gg] = make_float2(a, b);
+    }
+    if (!sums) return;
+    float *sp = sums + ((int64_t)q.n * m.parts + blockIdx.x) * 2 * p.C;
+    for (int e = threadIdx.x; e < m.nvb * 2 * V; e += kThreads) {
+        const int tx = e / (2 * V), i = e % (2 * V);
+        const int64_t c = ((int64_t)blockIdx.y * m.nvb + tx) * V + i % V;
+        if (c >= p.C) continue;
+        float t = 0.f;
+        for (int y = 0; y < m.ry; ++y) t += ch[(y * m.nvb + tx) * 2 * V + i];
+        sp[(i < V ? 0 : p.C) + c] = t;
+    }
+}
+
+template <typename T, bool kGate>
+__global__ void __launch_bounds__(kThreads)
+norm_maps_bwd_apply(const __grid_constant__ NormProblem p, const MapPlan m, const float2 *part) {
+    constexpr int V = Vec<T>::n;
+    tc::pdl_launch_dependents();
+    __shared__ float sh1[kThreads], sh2[kThreads];
+    const MapPos q = map_pos(p, m, V);
+    const int nv = (int)(p.C / p.G) / V, groups = m.nvb / nv, lane = threadIdx.x & 31;
+    const float inv = 1.f / ((float)p.L * (float)(p.C / p.G));
+    tc::pdl_wait_prerequisites();
+    for (int g = threadIdx.x >> 5; g < groups; g += kWarps) {
+        const int64_t gg = (int64_t)blockIdx.y * groups + g;
+        if (gg >= p.G) break;
+        float a = 0.f, b = 0.f;
+        for (int e = lane; e < m.parts; e += 32) {
+            const float2 t = part[((int64_t)q.n * m.parts + e) * p.G + gg];
+            a += t.x;
+            b += t.y;
+        }
+        a = sum_lanes(a, 32);
+        b = sum_lanes(b, 32);
+        if (lane == 0) {
+            sh1[g] = a * inv;
+            sh2[g] = b * inv;
+        }
+    }
+    __syncthreads();
+    if (!q.live) return;
+    const int64_t c = q.v * V, at = q.n * p.G + q.v / nv;
+    float w[V], b[V];
+    load_param(p.w, c, 1.f, w);
+    load_param(p.b, c, 0.f, b);
+    const float mean = p.mean[at], rstd = p.rstd[at], s1 = sh1[q.tx / nv], s2 = sh2[q.tx / nv];
+    const T *xp = static_cast<const T *>(p.x) + q.n * p.x_n + c;
+    const T *dp = static_cast<const T *>(p.dy) + q.n * p.dy_n + c;
+    const T *zp = static_cast<const T *>(p.gate) + (kGate ? q.n * p.gate_n + c : 0);
+    T *op = static_cast<T *>(p.dx) + q.n * p.L * p.C + c;
+    T *gp = static_cast<T *>(p.dgate) + (kGate ? q.n * p.L * p.C + c : 0);
+#pragma unroll 2
+    for (int64_t l = q.l0 + q.ty; l < q.l1; l += m.ry) {
+        float x[V], d[V], z[V];
+        Vec<T>::unpack(*reinterpret_cast<const uint4 *>(xp + l * p.x_l), x);
+        Vec<T>::unpack(*reinterpret_cast<const uint4 *>(dp + l * p.dy_l), d);
+        if (kGate) Vec<T>::unpack(*reinterpret_cast<const uint4 *>(zp + l * p.gate_l), z);
+        grad_vec<T, kGate>(x, d, z, w, b, mean, rstd, p.act);
+#pragma unroll
+        for (int i = 0; i < V; ++i) x[i] = rstd * (d[i] * w[i] - s1 - x[i] * s2);
+        *reinterpret_cast<uint4 *>(op + l * p.C) = Vec<T>::pack(x);
+        if (kGate) *reinterpret_cast<uint4 *>(gp + l * p.C) = Vec<T>::pack(z);
+    }
+}
+
+// dw, db: the partial sums added in order. Thread (channel, slice): 32 channels, 8 slices of parts.
+__global__ void __launch_bounds__(kThreads)
+norm_sum_parts(const float *sums, int64_t parts, int64_t C, float *dw, float *db) {
+    __shared__ float sh[8][32];
+    tc::pdl_wait_prerequisites();
+    const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+    const int64_t e = (int64_t)blockIdx.x * 32 + tx;      // 0 .. 2 C - 1
+    float t = 0.f;
+    if (e < 2 * C)
+        for (int64_t i = ty; i < parts; i += 8) t += sums[i * 2 * C + e];
+    sh[ty][tx] = t;
+    __syncthreads();
+    if (ty != 0 || e >= 2 * C) return;
+    for (int i = 1; i < 8; ++i) t += sh[i][tx];
+    float *to = e < C ? dw : db;
+    if (to) to[e % C] = t;
+}
+
+// ======================================================================= plain
 // Sum over the block, the same on every thread (a fixed order).
 __device__ __forceinline__ float block_sum(float v, float *sh) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    v = sum_lanes(v, 32);
     __syncthreads();
     if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
     __syncthreads();
     float s = 0.f;
-    for (int i = 0; i < kThreads / 32; ++i) s += sh[i];
+    for (int i = 0; i < kWarps; ++i) s += sh[i];
     return s;
 }
 
 // One CTA per (entry, group): mean, then the squared deviations from it, then the output.
 template <typename T>
-__global__ void norm_fwd_kernel(const __grid_constant__ NormProblem p) {
-    __shared__ float sh[kThreads / 32];
+__global__ void __launch_bounds__(kThreads)
+norm_plain_fwd(const __grid_constant__ NormProblem p) {
+    __shared__ float sh[kWarps];
     const int64_t n = blockIdx.x / p.G, g = blockIdx.x % p.G, cg = p.C / p.G, m = p.L * cg;
     const T *x = static_cast<const T *>(p.x) + n * p.x_n + g * cg;
     float s = 0.f;
@@ -65,8 +624,10 @@ __global__ void norm_fwd_kernel(const __grid_constant__ NormProblem p) {
         float u = (get(x + l * p.x_l + e % cg) - mean) * rstd;
         u = fmaf(u, p.w ? p.w[c] : 1.f, p.b ? p.b[c] : 0.f);
         float y;
-        if (p.gate) y = u * act_of(get(static_cast<const T *>(p.gate) + n * p.gate_n + l * p.gate_l + c), p.act);
-        else y = act_of(u, p.act);
+        if (p.gate)
+            y = u * act_of<T>(get(static_cast<const T *>(p.gate) + n * p.gate_n + l * p.gate_l + c), p.act);
+        else
+            y = act_of<T>(u, p.act);
         put(static_cast<T *>(p.y) + (n * p.L + l) * p.C + c, y);
     }
 }
@@ -75,26 +636,27 @@ struct Grad {
     float xh, du, dz;
 };
 template <typename T>
-__device__ __forceinline__ Grad grad_at(const NormProblem &p, int64_t n, int64_t l, int64_t c,
-                                        float mean, float rstd) {
+__device__ __forceinline__ Grad grad_at(const NormProblem &p, int64_t n, int64_t l, int64_t c, float mean,
+                                        float rstd) {
     Grad r;
     r.xh = (get(static_cast<const T *>(p.x) + n * p.x_n + l * p.x_l + c) - mean) * rstd;
     const float u = fmaf(r.xh, p.w ? p.w[c] : 1.f, p.b ? p.b[c] : 0.f);
     const float dy = get(static_cast<const T *>(p.dy) + n * p.dy_n + l * p.dy_l + c);
     if (p.gate) {
         const float z = get(static_cast<const T *>(p.gate) + n * p.gate_n + l * p.gate_l + c);
-        r.du = dy * act_of(z, p.act);
-        r.dz = dy * u * act_grad(z, p.act);
+        r.du = dy * act_of<T>(z, p.act);
+        r.dz = dy * u * act_grad<T>(z, p.act);
     } else {
-        r.du = dy * act_grad(u, p.act);
+        r.du = dy * act_grad<T>(u, p.act);
         r.dz = 0.f;
     }
     return r;
 }
 
 template <typename T>
-__global__ void norm_bwd_kernel(const __grid_constant__ NormProblem p) {
-    __shared__ float sh[kThreads / 32];
+__global__ void __launch_bounds__(kThreads)
+norm_plain_bwd(const __grid_constant__ NormProblem p) {
+    __shared__ float sh[kWarps];
     const int64_t n = blockIdx.x / p.G, g = blockIdx.x % p.G, cg = p.C / p.G, m = p.L * cg;
     const float mean = p.mean[blockIdx.x], rstd = p.rstd[blockIdx.x];
     float s1 = 0.f, s2 = 0.f;
@@ -118,8 +680,9 @@ __global__ void norm_bwd_kernel(const __grid_constant__ NormProblem p) {
 
 // One CTA per channel: dw and db.
 template <typename T>
-__global__ void norm_dw_kernel(const __grid_constant__ NormProblem p) {
-    __shared__ float sh[kThreads / 32];
+__global__ void __launch_bounds__(kThreads)
+norm_plain_dw(const __grid_constant__ NormProblem p) {
+    __shared__ float sh[kWarps];
     const int64_t c = blockIdx.x, g = c / (p.C / p.G);
     float sw = 0.f, sb = 0.f;
     for (int64_t e = threadIdx.x; e < p.N * p.L; e += kThreads) {
@@ -136,37 +699,170 @@ __global__ void norm_dw_kernel(const __grid_constant__ NormProblem p) {
     }
 }
 
-template <typename T>
-cudaError_t run_fwd(const NormProblem &p, cudaStream_t s) {
-    norm_fwd_kernel<T><<<(unsigned)(p.N * p.G), kThreads, 0, s>>>(p);
-    const cudaError_t e = cudaGetLastError();
+// ======================================================================= host
+enum Route { kRows, kMaps, kPlain };
+constexpr int kMostVpl = 4;
+
+int64_t vec_of(const NormProblem &p) { return p.io == 0 ? 8 : 4; }
+
+// The route depends on the shape and strides, so that the workspace's size can be told before
+// the pointers are known; pointers that are not on 16 bytes fall back to plain at the launch.
+Route route(const NormProblem &p, bool backward) {
+    const int64_t V = vec_of(p), cg = p.C / p.G;
+    if (cg % V != 0) return kPlain;
+    int64_t strides = p.x_n | p.x_l;
+    if (p.gate) strides |= p.gate_n | p.gate_l;
+    if (backward) strides |= p.dy_n | p.dy_l;
+    if (strides % V != 0) return kPlain;
+    if (p.L == 1 && cg / V <= 32 * kMostVpl) return kRows;
+    if (cg / V <= kThreads && p.N <= 65535) return kMaps;
+    return kPlain;
+}
+bool aligned(const NormProblem &p) {
+    return !((reinterpret_cast<uintptr_t>(p.x) | reinterpret_cast<uintptr_t>(p.gate) |
+              reinterpret_cast<uintptr_t>(p.dy)) & 15u);
+}
+
+RowPlan row_plan(const NormProblem &p) {
+    const int nv = (int)(p.C / p.G / vec_of(p));
+    RowPlan r;
+    r.W = 1;
+    while (r.W < nv && r.W < 32) r.W <<= 1;
+    const int segs = kThreads / r.W;
+    r.gpc = (int)min(p.G, (int64_t)segs);
+    r.rp = segs / r.gpc;
+    return r;
+}
+// About `per_sm` CTAs on every SM, each with at least one entry.
+dim3 row_grid(const NormProblem &p, const RowPlan &r, int sms, int per_sm) {
+    const int64_t gy = (p.G + r.gpc - 1) / r.gpc, most = (p.N + r.rp - 1) / r.rp;
+    const int64_t gx = min(most, max((int64_t)1, (int64_t)sms * per_sm / gy));
+    return dim3((unsigned)gx, (unsigned)gy);
+}
+
+MapPlan map_plan(const NormProblem &p, int sms) {
+    const int64_t V = vec_of(p), nv = p.C / p.G / V;
+    MapPlan m;
+    m.nvb = (int)min(p.C / V, kThreads / nv * nv);
+    m.ry = kThreads / m.nvb;
+    // parts: about four CTAs an SM, of at least four rounds of positions
+    const int64_t blocks = (p.C / V + m.nvb - 1) / m.nvb * p.N;
+    m.parts = (int)max((int64_t)1, min((int64_t)sms * 4 / blocks, p.L / (4 * m.ry)));
+    return m;
+}
+dim3 map_grid(const NormProblem &p, const MapPlan &m) {
+    return dim3((unsigned)m.parts, (unsigned)((p.C / vec_of(p) + m.nvb - 1) / m.nvb), (unsigned)p.N);
+}
+
+size_t round256(size_t n) { return (n + 255) & ~size_t(255); }
+constexpr int kFwdPerSm = 8, kBwdPerSm = 3;
+
+// Bytes of the parts' statistics, and parts of the channel sums.
+size_t stat_bytes(const NormProblem &p, const MapPlan &m, bool backward) {
+    return round256((size_t)(p.N * m.parts * p.G) * (backward ? sizeof(float2) : sizeof(Stat)));
+}
+
+template <typename... A>
+cudaError_t launch(void (*kernel)(A...), dim3 grid, size_t smem, bool dependent, cudaStream_t s, A... args) {
+    cudaLaunchAttribute pdl[1];
+    pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    pdl[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = pdl;
+    cfg.numAttrs = dependent ? 1 : 0;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
     if (e == cudaSuccess) count_launches(1);
     return e;
 }
 
-template <typename T>
-cudaError_t run_bwd(const NormProblem &p, cudaStream_t s) {
-    norm_bwd_kernel<T><<<(unsigned)(p.N * p.G), kThreads, 0, s>>>(p);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    count_launches(1);
-    if (!p.dw && !p.db) return e;
-    norm_dw_kernel<T><<<(unsigned)p.C, kThreads, 0, s>>>(p);
-    e = cudaGetLastError();
-    if (e == cudaSuccess) count_launches(1);
-    return e;
+template <typename T, bool kGate>
+cudaError_t run_fwd(const NormProblem &p, void *ws, int sms, cudaStream_t s) {
+    const Route rt = aligned(p) ? route(p, false) : kPlain;
+    if (rt == kRows) {
+        const RowPlan r = row_plan(p);
+        const int vpl = (int)((p.C / p.G / Vec<T>::n + r.W - 1) / r.W);
+        const dim3 grid = row_grid(p, r, sms, kFwdPerSm);
+        if (vpl == 1) return launch(norm_rows_fwd<T, 1, kGate>, grid, 0, false, s, p, r);
+        if (vpl == 2) return launch(norm_rows_fwd<T, 2, kGate>, grid, 0, false, s, p, r);
+        return launch(norm_rows_fwd<T, 4, kGate>, grid, 0, false, s, p, r);
+    }
+    if (rt == kMaps) {
+        const MapPlan m = map_plan(p, sms);
+        Stat *part = static_cast<Stat *>(ws);
+        const cudaError_t e = launch(norm_maps_stats<T>, map_grid(p, m), 0, false, s, p, m, part);
+        if (e != cudaSuccess) return e;
+        return launch(norm_maps_apply<T, kGate>, map_grid(p, m), 0, true, s, p, m, (const Stat *)part);
+    }
+    return launch(norm_plain_fwd<T>, dim3((unsigned)(p.N * p.G)), 0, false, s, p);
+}
+
+template <typename T, bool kGate>
+cudaError_t run_bwd(const NormProblem &p, void *ws, int sms, cudaStream_t s) {
+    const Route rt = aligned(p) ? route(p, true) : kPlain;
+    const bool want = p.dw || p.db;
+    cudaError_t e;
+    if (rt == kPlain) {
+        e = launch(norm_plain_bwd<T>, dim3((unsigned)(p.N * p.G)), 0, false, s, p);
+        if (e != cudaSuccess || !want) return e;
+        return launch(norm_plain_dw<T>, dim3((unsigned)p.C), 0, false, s, p);
+    }
+    float *sums = nullptr;
+    int64_t parts;
+    bool dependent = false;
+    if (rt == kRows) {
+        const RowPlan r = row_plan(p);
+        const int vpl = (int)((p.C / p.G / Vec<T>::n + r.W - 1) / r.W);
+        const dim3 grid = row_grid(p, r, sms, kBwdPerSm);
+        parts = (int64_t)grid.x * r.rp;
+        if (want) sums = static_cast<float *>(ws);
+        if (vpl == 1) e = launch(norm_rows_bwd<T, 1, kGate>, grid, 0, false, s, p, r, sums);
+        else if (vpl == 2) e = launch(norm_rows_bwd<T, 2, kGate>, grid, 0, false, s, p, r, sums);
+        else e = launch(norm_rows_bwd<T, 4, kGate>, grid, 0, false, s, p, r, sums);
+    } else {
+        const MapPlan m = map_plan(p, sms);
+        float2 *part = static_cast<float2 *>(ws);
+        parts = p.N * m.parts;
+        if (want) sums = reinterpret_cast<float *>(static_cast<char *>(ws) + stat_bytes(p, m, true));
+        const size_t smem = (size_t)kThreads * 2 * Vec<T>::n * sizeof(float);
+        e = launch(norm_maps_bwd_stats<T, kGate>, map_grid(p, m), smem, false, s, p, m, part, sums);
+        if (e != cudaSuccess) return e;
+        e = launch(norm_maps_bwd_apply<T, kGate>, map_grid(p, m), 0, true, s, p, m, (const float2 *)part);
+    }
+    if (e != cudaSuccess || !want) return e;
+    return launch(norm_sum_parts, dim3((unsigned)((2 * p.C + 31) / 32)), 0, dependent, s,
+                  (const float *)sums, parts, p.C, p.dw, p.db);
 }
 
 }  // namespace
 
-size_t norm_workspace_bytes(const NormProblem &, bool, int) { return 0; }
-
-cudaError_t launch_norm_fwd(const NormProblem &p, void *, int, cudaStream_t s) {
-    return p.io == 0 ? run_fwd<__nv_bfloat16>(p, s) : run_fwd<float>(p, s);
+size_t norm_workspace_bytes(const NormProblem &p, bool backward, int num_sms) {
+    // (a gate can only take the route to plain, which needs none)
+    const Route rt = route(p, backward);
+    if (rt == kPlain || (rt == kRows && !backward)) return 0;
+    if (rt == kRows) {
+        const RowPlan r = row_plan(p);
+        return (size_t)row_grid(p, r, num_sms, kBwdPerSm).x * r.rp * 2 * p.C * sizeof(float);
+    }
+    const MapPlan m = map_plan(p, num_sms);
+    return stat_bytes(p, m, backward) + (backward ? (size_t)(p.N * m.parts) * 2 * p.C * sizeof(float) : 0);
 }
 
-cudaError_t launch_norm_bwd(const NormProblem &p, void *, int, cudaStream_t s) {
-    return p.io == 0 ? run_bwd<__nv_bfloat16>(p, s) : run_bwd<float>(p, s);
+cudaError_t launch_norm_fwd(const NormProblem &p, void *ws, int num_sms, cudaStream_t s) {
+    if (p.io == 0)
+        return p.gate ? run_fwd<__nv_bfloat16, true>(p, ws, num_sms, s)
+                      : run_fwd<__nv_bfloat16, false>(p, ws, num_sms, s);
+    return p.gate ? run_fwd<float, true>(p, ws, num_sms, s) : run_fwd<float, false>(p, ws, num_sms, s);
+}
+
+cudaError_t launch_norm_bwd(const NormProblem &p, void *ws, int num_sms, cudaStream_t s) {
+    if (p.io == 0)
+        return p.gate ? run_bwd<__nv_bfloat16, true>(p, ws, num_sms, s)
+                      : run_bwd<__nv_bfloat16, false>(p, ws, num_sms, s);
+    return p.gate ? run_bwd<float, true>(p, ws, num_sms, s) : run_bwd<float, false>(p, ws, num_sms, s);
 }
 
 }  // namespace gla

@@ -143,6 +143,15 @@ def _stream_handle(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _launch(f, device, stream, *args):
+    """f(*args, stream handle) with ``device`` current: switching costs as much as a small call,
+    so it is only done when another device is."""
+    if device.index == torch.cuda.current_device():
+        return f(*args, _stream_handle(stream))
+    with torch.cuda.device(device):
+        return f(*args, _stream_handle(stream))
+
+
 def _check(t, name, dtype, shape, device):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")

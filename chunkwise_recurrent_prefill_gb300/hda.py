@@ -10,63 +10,80 @@ contiguous, such as slices of one projection. As in ``gla.py`` nothing is comput
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
-from .gla import (GLA_OK, GLAError, IO_BF16, IO_F32, _HdaShape, _check, _ptr, _stream_handle,
+from .gla import (GLA_OK, GLAError, IO_BF16, IO_F32, _HdaShape, _check, _launch, _ptr,
                   load_library, options)
 
 
-def _check_rows(t, name, dtype, shape, device, align):
-    """A tensor whose last dimension is contiguous and whose other strides are positive and
-    multiples of ``align`` bytes (those of dimensions with more than one element)."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.device != device:
-        raise ValueError(f"{name}: on {t.device}, expected {device}")
-    if t.numel() == 0:
+def _check_rows(name, dtype, shape, strides, want_dtype, want_shape, align):
+    """The last dimension is contiguous and the strides of the others (those with more than one
+    element) are positive multiples of ``align`` bytes."""
+    if dtype != want_dtype:
+        raise TypeError(f"{name}: dtype {dtype}, expected {want_dtype}")
+    if shape != want_shape:
+        raise ValueError(f"{name}: shape {tuple(shape)}, expected {tuple(want_shape)}")
+    if 0 in shape:
         return
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+    if shape[-1] > 1 and strides[-1] != 1:
         raise ValueError(f"{name}: the last dimension must be contiguous")
-    for n, s in zip(t.shape[:-1], t.stride()[:-1]):
-        if n > 1 and (s <= 0 or s * t.element_size() % align):
-            raise ValueError(f"{name}: strides {t.stride()} must be positive multiples of "
+    es = 2 if dtype == torch.bfloat16 else 4
+    for n, s in zip(shape[:-1], strides[:-1]):
+        if n > 1 and (s <= 0 or s * es % align):
+            raise ValueError(f"{name}: strides {tuple(strides)} must be positive multiples of "
                              f"{align} bytes")
 
 
-def _strides(dst, t, dims):
-    for n, s in zip(dims, t.stride()):
-        setattr(dst, n, s if t.numel() else 0)
-
-
-def _shape(q, k, v, H, step=False) -> _HdaShape:
-    if q.dtype not in (torch.bfloat16, torch.float32):
+# The C shape of a call depends on the tensors' types, shapes and strides alone: it is checked and
+# made once for each combination.
+@functools.lru_cache(maxsize=512)
+def _plan(step, H, dtype, tensors) -> _HdaShape:
+    (qs, qt, _), (ks, kt, kd), (vs, vt, vd) = tensors[:3]
+    if dtype not in (torch.bfloat16, torch.float32):
         raise TypeError("q/k/v must be bfloat16 or float32")
-    if q.dim() != (3 if step else 4) or k.dim() != q.dim() or v.dim() != q.dim():
+    dims = 3 if step else 4
+    if len(qs) != dims or len(ks) != dims or len(vs) != dims:
         raise ValueError("q, k, v must be " + ("[B, heads, D]" if step else "[B, T, heads, D]"))
+    align = (2 if dtype == torch.bfloat16 else 4) if step else 16
+    lead = qs[:-2]
+    _check_rows("q", dtype, qs, qt, dtype, qs, align)
+    _check_rows("k", kd, ks, kt, dtype, torch.Size(lead + (ks[-2], qs[-1])), align)
+    _check_rows("v", vd, vs, vt, dtype, torch.Size(lead + (vs[-2], vs[-1])), align)
     sh = _HdaShape()
-    sh.B, sh.T = q.shape[0], 1 if step else q.shape[1]
-    sh.H, sh.Hq, sh.Hk, sh.Hv = H, q.shape[-2], k.shape[-2], v.shape[-2]
-    sh.Dk, sh.Dv = q.shape[-1], v.shape[-1]
-    sh.io = IO_BF16 if q.dtype == torch.bfloat16 else IO_F32
-    for n, t in (("q", q), ("k", k), ("v", v)):
-        _strides(getattr(sh, n), t, "bh" if step else "bth")
+    sh.B, sh.T = qs[0], 1 if step else qs[1]
+    sh.H, sh.Hq, sh.Hk, sh.Hv = H, qs[-2], ks[-2], vs[-2]
+    sh.Dk, sh.Dv = qs[-1], vs[-1]
+    sh.io = IO_BF16 if dtype == torch.bfloat16 else IO_F32
+    rows = [("q", qs, qt), ("k", ks, kt), ("v", vs, vt)]
+    if len(tensors) > 3:
+        os, ot, od = tensors[3]
+        _check_rows("do", od, os, ot, dtype, torch.Size((sh.B, sh.T, H, sh.Dv)), align)
+        rows.append(("d_o", os, ot))
+    for n, shape, strides in rows:
+        for d, s in zip("bh" if step else "bth", strides):
+            setattr(getattr(sh, n), d, 0 if 0 in shape else s)
     return sh
 
 
-def _check_inputs(q, k, v, decay, step=False):
+def _shape(q, k, v, decay, do=None, step=False):
+    for t, n in ((q, "q"), (k, "k"), (v, "v"), (decay, "decay")):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{n} must be a torch.Tensor")
+    ts = ((q.shape, q.stride(), q.dtype), (k.shape, k.stride(), k.dtype), (v.shape, v.stride(), v.dtype))
+    if do is not None:
+        ts += ((do.shape, do.stride(), do.dtype),)
+    return _plan(step, decay.numel(), q.dtype, ts)
+
+
+def _check_inputs(q, k, v, decay):
     dev = q.device
     if dev.type != "cuda":
         raise ValueError("tensors must be on a CUDA device")
-    align = q.element_size() if step else 16
-    lead = tuple(q.shape[:-2])
-    _check_rows(q, "q", q.dtype, q.shape, dev, align)
-    _check_rows(k, "k", q.dtype, lead + (k.shape[-2], q.shape[-1]), dev, align)
-    _check_rows(v, "v", q.dtype, lead + (v.shape[-2], v.shape[-1]), dev, align)
+    for t, n in ((k, "k"), (v, "v")):
+        if t.device != dev:
+            raise ValueError(f"{n}: on {t.device}, expected {dev}")
     _check(decay, "decay", torch.float32, (decay.numel(),), dev)
     return dev
 
@@ -91,7 +108,7 @@ def hda_fwd(q, k, v, decay, scale: float, h0=None, *, o=None, hT=None, return_st
     ``stream`` (default: torch's current stream)."""
     lib = load_library()
     H = decay.numel()
-    sh = _shape(q, k, v, H)
+    sh = _shape(q, k, v, decay)
     dev = _check_inputs(q, k, v, decay)
     B, T, Dk, Dv = sh.B, sh.T, sh.Dk, sh.Dv
     _state(h0, "h0", (B, H, Dk, Dv), dev)
@@ -103,10 +120,8 @@ def hda_fwd(q, k, v, decay, scale: float, h0=None, *, o=None, hT=None, return_st
         hT = torch.empty((B, H, Dk, Dv), dtype=torch.float32, device=dev)
     _state(hT, "hT", (B, H, Dk, Dv), dev)
     opt = options(path, seq_splits, workspace)
-    with torch.cuda.device(dev):
-        rc = lib.hda_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(decay), ctypes.c_float(scale), _ptr(h0),
-                         _ptr(o), _ptr(hT), ctypes.byref(sh), ctypes.byref(opt),
-                         _stream_handle(stream))
+    rc = _launch(lib.hda_fwd, dev, stream, _ptr(q), _ptr(k), _ptr(v), _ptr(decay), scale, _ptr(h0),
+                 _ptr(o), _ptr(hT), ctypes.byref(sh), ctypes.byref(opt))
     _fail(lib, rc, "hda_fwd")
     return o, hT
 
@@ -118,20 +133,19 @@ def hda_bwd(do, q, k, v, decay, scale: float, h0=None, dhT=None, *, path: str = 
     gradients of shared heads are summed in fp32."""
     lib = load_library()
     H = decay.numel()
-    sh = _shape(q, k, v, H)
+    sh = _shape(q, k, v, decay, do)
     dev = _check_inputs(q, k, v, decay)
-    B, T, Dk, Dv = sh.B, sh.T, sh.Dk, sh.Dv
-    _check_rows(do, "do", q.dtype, (B, T, H, Dv), dev, 16)
-    _strides(sh.d_o, do, "bth")
+    if do.device != dev:
+        raise ValueError(f"do: on {do.device}, expected {dev}")
+    B, Dk, Dv = sh.B, sh.Dk, sh.Dv
     _state(h0, "h0", (B, H, Dk, Dv), dev)
     _state(dhT, "dhT", (B, H, Dk, Dv), dev)
     dq, dk, dv = (torch.empty(t.shape, dtype=t.dtype, device=dev) for t in (q, k, v))
     dh0 = None if h0 is None else torch.empty_like(h0)
     opt = options(path, seq_splits, workspace)
-    with torch.cuda.device(dev):
-        rc = lib.hda_bwd(_ptr(do), _ptr(q), _ptr(k), _ptr(v), _ptr(decay), ctypes.c_float(scale),
-                         _ptr(h0), _ptr(dhT), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dh0),
-                         ctypes.byref(sh), ctypes.byref(opt), _stream_handle(stream))
+    rc = _launch(lib.hda_bwd, dev, stream, _ptr(do), _ptr(q), _ptr(k), _ptr(v), _ptr(decay), scale,
+                 _ptr(h0), _ptr(dhT), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dh0), ctypes.byref(sh),
+                 ctypes.byref(opt))
     _fail(lib, rc, "hda_bwd")
     return dq, dk, dv, dh0
 
@@ -141,13 +155,13 @@ def hda_workspace_size(q, k, v, decay, backward: bool = False, path: str = "auto
     """Bytes of workspace ``hda_fwd`` (or ``hda_bwd``) needs for these tensors' shapes."""
     lib = load_library()
     f = lib.hda_bwd_workspace_size if backward else lib.hda_fwd_workspace_size
-    return int(f(ctypes.byref(_shape(q, k, v, decay.numel())),
+    return int(f(ctypes.byref(_shape(q, k, v, decay)),
                  ctypes.byref(options(path, seq_splits))))
 
 
 def hda_path_for(q, k, v, decay, path: str = "auto") -> str | None:
     """The path ``hda_fwd`` and ``hda_bwd`` run for these shapes ("exact" / "tc"), or None."""
-    r = load_library().hda_path_for(ctypes.byref(_shape(q, k, v, decay.numel())),
+    r = load_library().hda_path_for(ctypes.byref(_shape(q, k, v, decay)),
                                     ctypes.byref(options(path)))
     return {1: "exact", 2: "tc"}.get(int(r))
 
@@ -159,8 +173,8 @@ def hda_step(q, k, v, decay, scale: float, S, slots=None, *, o=None, stream=None
     when ``slots`` is None. Returns o [R,H,Dv] in q's dtype."""
     lib = load_library()
     H = decay.numel()
-    sh = _shape(q, k, v, H, step=True)
-    dev = _check_inputs(q, k, v, decay, step=True)
+    sh = _shape(q, k, v, decay, step=True)
+    dev = _check_inputs(q, k, v, decay)
     R, Dk, Dv = sh.B, sh.Dk, sh.Dv
     P = S.shape[0]
     _check(S, "S", torch.float32, (P, H, Dk, Dv), dev)
@@ -170,8 +184,7 @@ def hda_step(q, k, v, decay, scale: float, S, slots=None, *, o=None, stream=None
         o = torch.empty((R, H, Dv), dtype=q.dtype, device=dev)
     else:
         _check(o, "o", q.dtype, (R, H, Dv), dev)
-    with torch.cuda.device(dev):
-        rc = lib.hda_step(_ptr(q), _ptr(k), _ptr(v), _ptr(decay), ctypes.c_float(scale), _ptr(S),
-                          _ptr(slots), _ptr(o), P, ctypes.byref(sh), _stream_handle(stream))
+    rc = _launch(lib.hda_step, dev, stream, _ptr(q), _ptr(k), _ptr(v), _ptr(decay), scale, _ptr(S),
+                 _ptr(slots), _ptr(o), P, ctypes.byref(sh))
     _fail(lib, rc, "hda_step")
     return o

@@ -7,64 +7,76 @@ of each group. The norm over each head of a token is x [B T, C] with one group p
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
-from .gla import IO_BF16, IO_F32, _NormShape, _check, _ptr, _stream_handle, load_library
+from .gla import IO_BF16, IO_F32, _NormShape, _check, _launch, _ptr, load_library
 from .hda import _fail
 
 ACTS = {"none": 0, "silu": 1, "gelu": 2}
 
 
-def _rows(t, name, dtype, shape, dev):
+def _rows(name, dtype, shape, strides, want_dtype, want_shape):
     """(stride of N, stride of a position) of [N, ..., C]; the positions must be evenly spaced."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.device != dev:
-        raise ValueError(f"{name}: on {t.device}, expected {dev}")
-    if t.numel() == 0:
+    if dtype != want_dtype:
+        raise TypeError(f"{name}: dtype {dtype}, expected {want_dtype}")
+    if shape != want_shape:
+        raise ValueError(f"{name}: shape {tuple(shape)}, expected {tuple(want_shape)}")
+    if 0 in shape:
         return 0, 0
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+    if shape[-1] > 1 and strides[-1] != 1:
         raise ValueError(f"{name}: the channels must be contiguous")
     step, run = 0, 1      # stride of one position, positions covered so far
-    for n, s in zip(reversed(t.shape[1:-1]), reversed(t.stride()[1:-1])):
+    for n, s in zip(reversed(shape[1:-1]), reversed(strides[1:-1])):
         if n == 1:
             continue
         if step and s != step * run:
             raise ValueError(f"{name}: the positions must be evenly spaced in memory")
         step = step or s
         run *= n
-    sn = t.stride(0) if t.shape[0] > 1 else max(step, t.shape[-1]) * run
-    sl = step or t.shape[-1]
+    sn = strides[0] if shape[0] > 1 else max(step, shape[-1]) * run
+    sl = step or shape[-1]
     if sn <= 0 or sl <= 0:
-        raise ValueError(f"{name}: strides {t.stride()} must be positive")
+        raise ValueError(f"{name}: strides {tuple(strides)} must be positive")
     return sn, sl
 
 
-def _shape(x, groups, eps, act, gate, dy=None) -> _NormShape:
-    if x.dtype not in (torch.bfloat16, torch.float32):
+# The C shape of a call depends on the tensors' types, shapes and strides alone: it is checked and
+# made once for each combination.
+@functools.lru_cache(maxsize=512)
+def _plan(groups, eps, act, x, gate, dy) -> _NormShape:
+    shape, strides, dtype = x
+    if dtype not in (torch.bfloat16, torch.float32):
         raise TypeError("x must be bfloat16 or float32")
-    if x.dim() < 2:
+    if len(shape) < 2:
         raise ValueError("x must be [N, ..., C]")
     if act not in ACTS:
         raise ValueError(f"act must be one of {sorted(ACTS)}")
     sh = _NormShape()
-    sh.N, sh.C, sh.G = x.shape[0], x.shape[-1], int(groups)
+    sh.N, sh.C, sh.G = shape[0], shape[-1], int(groups)
     sh.L = 1
-    for n in x.shape[1:-1]:
+    for n in shape[1:-1]:
         sh.L *= n
-    sh.x_n, sh.x_l = _rows(x, "x", x.dtype, x.shape, x.device)
+    sh.x_n, sh.x_l = _rows("x", dtype, shape, strides, dtype, shape)
     if gate is not None:
-        sh.gate_n, sh.gate_l = _rows(gate, "gate", x.dtype, x.shape, x.device)
+        sh.gate_n, sh.gate_l = _rows("gate", gate[2], gate[0], gate[1], dtype, shape)
     if dy is not None:
-        sh.dy_n, sh.dy_l = _rows(dy, "dy", x.dtype, x.shape, x.device)
+        sh.dy_n, sh.dy_l = _rows("dy", dy[2], dy[0], dy[1], dtype, shape)
     sh.eps, sh.act = eps, ACTS[act]
-    sh.io = IO_BF16 if x.dtype == torch.bfloat16 else IO_F32
+    sh.io = IO_BF16 if dtype == torch.bfloat16 else IO_F32
     return sh
+
+
+def _shape(x, groups, eps, act, gate, dy=None) -> _NormShape:
+    key = []
+    for t, n in ((x, "x"), (gate, "gate"), (dy, "dy")):
+        if t is not None and not isinstance(t, torch.Tensor):
+            raise TypeError(f"{n} must be a torch.Tensor")
+        if t is not None and t.device != x.device:
+            raise ValueError(f"{n}: on {t.device}, expected {x.device}")
+        key.append(None if t is None else (t.shape, t.stride(), t.dtype))
+    return _plan(groups, eps, act, *key)
 
 
 def _affine(x, weight, bias):
@@ -104,10 +116,8 @@ def group_norm_fwd(x, groups: int, weight=None, bias=None, *, eps: float = 1e-5,
     mean = torch.empty((sh.N, max(sh.G, 0)), dtype=torch.float32, device=dev)
     rstd = torch.empty_like(mean)
     ws, nws = _workspace(workspace, dev)
-    with torch.cuda.device(dev):
-        rc = lib.gla_group_norm_fwd(_ptr(x), _ptr(weight), _ptr(bias), _ptr(gate), _ptr(y),
-                                    _ptr(mean), _ptr(rstd), ctypes.byref(sh), ws, nws,
-                                    _stream_handle(stream))
+    rc = _launch(lib.gla_group_norm_fwd, dev, stream, _ptr(x), _ptr(weight), _ptr(bias), _ptr(gate),
+                 _ptr(y), _ptr(mean), _ptr(rstd), ctypes.byref(sh), ws, nws)
     _fail(lib, rc, "gla_group_norm_fwd")
     return y, mean, rstd
 
@@ -127,9 +137,8 @@ def group_norm_bwd(dy, x, mean, rstd, groups: int, weight=None, bias=None, *, ac
     dw = None if weight is None else torch.empty_like(weight)
     db = None if bias is None else torch.empty_like(bias)
     ws, nws = _workspace(workspace, dev)
-    with torch.cuda.device(dev):
-        rc = lib.gla_group_norm_bwd(_ptr(dy), _ptr(x), _ptr(mean), _ptr(rstd), _ptr(weight),
-                                    _ptr(bias), _ptr(gate), _ptr(dx), _ptr(dw), _ptr(db), _ptr(dz),
-                                    ctypes.byref(sh), ws, nws, _stream_handle(stream))
+    rc = _launch(lib.gla_group_norm_bwd, dev, stream, _ptr(dy), _ptr(x), _ptr(mean), _ptr(rstd),
+                 _ptr(weight), _ptr(bias), _ptr(gate), _ptr(dx), _ptr(dw), _ptr(db), _ptr(dz),
+                 ctypes.byref(sh), ws, nws)
     _fail(lib, rc, "gla_group_norm_bwd")
     return dx, dw, db, dz

@@ -9,7 +9,7 @@ from __future__ import annotations
 
 import torch
 
-from .gla import _check, _ptr, _stream_handle, load_library
+from .gla import _check, _launch, _ptr, load_library
 from .hda import _fail
 
 
@@ -48,8 +48,7 @@ def pages_copy(pool, src, dst, *, stream=None):
     n = src.numel()
     _ints(src, "src", pool.device)
     _ints(dst, "dst", pool.device, (n,))
-    with torch.cuda.device(pool.device):
-        rc = lib.gla_pages_copy(_ptr(pool), P, nb, _ptr(src), _ptr(dst), n, _stream_handle(stream))
+    rc = _launch(lib.gla_pages_copy, pool.device, stream, _ptr(pool), P, nb, _ptr(src), _ptr(dst), n)
     _fail(lib, rc, "gla_pages_copy")
 
 
@@ -61,9 +60,8 @@ def pages_fork(pool, table, free, count, parents, children, *, stream=None):
     n = parents.numel()
     _ints(parents, "parents", pool.device)
     _ints(children, "children", pool.device, (n,))
-    with torch.cuda.device(pool.device):
-        rc = lib.gla_pages_fork(_ptr(pool), P, nb, _ptr(table), R, M, _ptr(free), _ptr(count),
-                                _ptr(parents), _ptr(children), n, _stream_handle(stream))
+    rc = _launch(lib.gla_pages_fork, pool.device, stream, _ptr(pool), P, nb, _ptr(table), R, M,
+                 _ptr(free), _ptr(count), _ptr(parents), _ptr(children), n)
     _fail(lib, rc, "gla_pages_fork")
 
 
@@ -76,9 +74,8 @@ def pages_free(table, free, count, rows, *, stream=None):
     P = free.numel()
     R, M = _book(table, free, count, P, dev)
     _ints(rows, "rows", dev)
-    with torch.cuda.device(dev):
-        rc = lib.gla_pages_free(P, _ptr(table), R, M, _ptr(free), _ptr(count), _ptr(rows),
-                                rows.numel(), _stream_handle(stream))
+    rc = _launch(lib.gla_pages_free, dev, stream, P, _ptr(table), R, M, _ptr(free), _ptr(count),
+                 _ptr(rows), rows.numel())
     _fail(lib, rc, "gla_pages_free")
 
 
@@ -87,7 +84,6 @@ def pages_compact(pool, table, free, count, *, stream=None):
     lib = load_library()
     P, nb = _pool(pool)
     R, M = _book(table, free, count, P, pool.device)
-    with torch.cuda.device(pool.device):
-        rc = lib.gla_pages_compact(_ptr(pool), P, nb, _ptr(table), R, M, _ptr(free), _ptr(count),
-                                   _stream_handle(stream))
+    rc = _launch(lib.gla_pages_compact, pool.device, stream, _ptr(pool), P, nb, _ptr(table), R, M,
+                 _ptr(free), _ptr(count))
     _fail(lib, rc, "gla_pages_compact")
