@@ -4,9 +4,9 @@
 // The columns of the state are independent (out_t[z] needs S[:, z] alone), so a CTA owns 16 of
 // them for one head and walks the tokens with its part of S in registers: thread (column, row
 // group) holds RPT rows of one column. A token costs it RPT multiply-adds for the update and
-// RPT for the read; nothing but the state's own multiply-add chain is serial, and the sums over
-// the 8 row groups of a column (3 shuffles) overlap with the next tokens. x, y and z are staged
-// as fp32 in shared memory TB tokens at a time, the next tile being loaded meanwhile.
+// RPT for the read; nothing but the state's own multiply-add chain is serial, so eight tokens are
+// unrolled, and their sums over the 8 row groups of a column take 7 shuffles together. x, y and z
+// are staged as fp32 in shared memory TB tokens at a time, the next tile being loaded meanwhile.
 #include <cuda_bf16.h>
 
 #include "gla_internal.h"
@@ -137,28 +137,53 @@ hda_exact_kernel(const __grid_constant__ HdaProblem p) {
         }
         const int nt = (int)min((int64_t)TB, p.T - i0);
         auto walk = [&](auto is_slow) {
-#pragma unroll 2
-            for (int i = 0; i < nt; ++i) {
-                const float zt = m.a_in * zs[buf][i * kCols + col];
-                const bool first = rev && i0 == 0 && i == 0;
-                const float f = first ? (is_slow ? 0.f : 1.f) : (is_slow ? lm1 : lam);
-                float acc = 0.f;
+#pragma unroll 1
+            for (int i8 = 0; i8 < nt; i8 += 8) {
+                float acc[8];
 #pragma unroll
-                for (int k4 = 0; k4 < RPT / 4; ++k4) {
-                    const float4 y4 = *reinterpret_cast<const float4 *>(&ys[buf][i * W + row_of(4 * k4)]);
-                    const float4 x4 = *reinterpret_cast<const float4 *>(&xs[buf][i * W + row_of(4 * k4)]);
-                    const float yv[4] = {y4.x, y4.y, y4.z, y4.w}, xv[4] = {x4.x, x4.y, x4.z, x4.w};
+                for (int i = 0; i < 8; ++i) {
+                    acc[i] = 0.f;
+                    if (i8 + i >= nt) continue;
+                    const float zt = m.a_in * zs[buf][(i8 + i) * kCols + col];
+                    const bool first = rev && i0 == 0 && i8 + i == 0;
+                    const float f = first ? (is_slow ? 0.f : 1.f) : (is_slow ? lm1 : lam);
+                    float part[2] = {0.f, 0.f};
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float &sk = s[4 * k4 + e];
-                        sk = is_slow ? fmaf(f, sk, fmaf(yv[e], zt, sk)) : fmaf(f, sk, yv[e] * zt);
-                        acc = fmaf(xv[e], sk, acc);
+                    for (int k4 = 0; k4 < RPT / 4; ++k4) {
+                        const float4 y4 =
+                            *reinterpret_cast<const float4 *>(&ys[buf][(i8 + i) * W + row_of(4 * k4)]);
+                        const float4 x4 =
+                            *reinterpret_cast<const float4 *>(&xs[buf][(i8 + i) * W + row_of(4 * k4)]);
+                        const float yv[4] = {y4.x, y4.y, y4.z, y4.w}, xv[4] = {x4.x, x4.y, x4.z, x4.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            float &sk = s[4 * k4 + e];
+                            sk = is_slow ? fmaf(f, sk, fmaf(yv[e], zt, sk)) : fmaf(f, sk, yv[e] * zt);
+                            part[e & 1] = fmaf(xv[e], sk, part[e & 1]);
+                        }
                     }
+                    acc[i] = part[0] + part[1];
                 }
-                acc += __shfl_xor_sync(0xffffffffu, acc, 1);
-                acc += __shfl_xor_sync(0xffffffffu, acc, 2);
-                acc += __shfl_xor_sync(0xffffffffu, acc, 4);
-                if (rg == (i & 7)) os[i][col] = m.a_out * acc;
+                // sums over the 8 row groups, of 8 tokens at once: each step halves the tokens a lane
+                // holds, and lane rg is left with token rg
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const bool up = rg & 4;
+                    const float keep = up ? acc[i + 4] : acc[i], give = up ? acc[i] : acc[i + 4];
+                    acc[i] = keep + __shfl_xor_sync(0xffffffffu, give, 4);
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const bool up = rg & 2;
+                    const float keep = up ? acc[i + 2] : acc[i], give = up ? acc[i] : acc[i + 2];
+                    acc[i] = keep + __shfl_xor_sync(0xffffffffu, give, 2);
+                }
+                {
+                    const bool up = rg & 1;
+                    const float keep = up ? acc[1] : acc[0], give = up ? acc[0] : acc[1];
+                    acc[0] = keep + __shfl_xor_sync(0xffffffffu, give, 1);
+                }
+                os[i8 + rg][col] = m.a_out * acc[0];
             }
         };
         if (slow) walk(std::true_type{});

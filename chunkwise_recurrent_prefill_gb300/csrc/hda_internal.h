@@ -63,7 +63,7 @@ struct HdaStep {
     int64_t R, P, H;
     int Dk, Dv, io;
 };
-cudaError_t launch_hda_step(const HdaStep &p, unsigned int *dev_err, cudaStream_t s);
+cudaError_t launch_hda_step(const HdaStep &p, int num_sms, unsigned int *dev_err, cudaStream_t s);
 
 // Tensor-core path (bf16, Dx and Dz of every map in {64, 128}).
 bool hda_tc_supported(const HdaProblem &p);

@@ -9,36 +9,39 @@
 namespace gla {
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kBatch = 16;  // state rows a warp loads before it stores them
+constexpr int kThreads = 256;
+constexpr int kBatch = 16;  // state rows a thread loads before it stores them
 
 __device__ __forceinline__ float get(const float *p) { return *p; }
 __device__ __forceinline__ float get(const __nv_bfloat16 *p) { return __bfloat162float(*p); }
 __device__ __forceinline__ void put(float *p, float x) { *p = x; }
 __device__ __forceinline__ void put(__nv_bfloat16 *p, float x) { *p = __float2bfloat16_rn(x); }
 
-// CTA = (row, head, 128 value columns). Warp w updates key rows w, w + 8, ...; lane l owns four
-// columns and moves them with 16-byte accesses. The per-column sums of the warps are added in
-// shared memory in a fixed order.
-template <typename T>
-__global__ void __launch_bounds__(kWarps * 32, 2)
+// CTA = (row, head, kCols value columns). A thread owns four columns of every kRows-th key row and
+// moves them with 16-byte accesses; the sums over the key rows are added in shared memory in a
+// fixed order. Columns of 128 keep whole rows of 512 bytes together; a call of few rows and heads
+// takes 32, so that four times as many SMs share it (16 states of 128 x 128: 5.1 us against 6.7).
+template <typename T, int kCols>
+__global__ void __launch_bounds__(kThreads, 2)
 hda_step_kernel(const __grid_constant__ HdaStep p, unsigned int *err) {
-    __shared__ float4 part[kWarps][32];
+    constexpr int kQuads = kCols / 4, kRows = kThreads / kQuads;
+    constexpr int kLoad = kCols == 128 ? kBatch : 4;
+    __shared__ float4 part[kRows][kQuads];
     extern __shared__ float rows[];   // [2][Dk]: k and q
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t r = blockIdx.x / p.H, h = blockIdx.x % p.H;
-    const int col = blockIdx.y * 128 + 4 * lane;
+    const int row0 = threadIdx.x / kQuads, quad = threadIdx.x % kQuads;
+    const int r = blockIdx.x / (unsigned)p.H, h = blockIdx.x % (unsigned)p.H;
+    const int col = blockIdx.y * kCols + 4 * quad;
     const bool in = col < p.Dv;
-    T *op = static_cast<T *>(p.o) + (r * p.H + h) * p.Dv + col;
+    T *op = static_cast<T *>(p.o) + ((int64_t)r * p.H + h) * p.Dv + col;
     const int64_t slot = p.slots ? p.slots[r] : r;
     if (slot < 0 || slot >= p.P) {   // an empty row (uniform over the CTA)
         if (slot >= p.P && threadIdx.x == 0) atomicOr(err, kDevErrPages);
-        if (warp == 0 && in)
+        if (row0 == 0 && in)
             for (int j = 0; j < 4; ++j) put(op + j, 0.f);
         return;
     }
     auto head = [&](const HdaTensor &t) {
-        return static_cast<const T *>(t.p) + r * t.b + (h / (p.H / t.heads)) * t.h;
+        return static_cast<const T *>(t.p) + r * t.b + (h * t.heads / (int)p.H) * t.h;
     };
     const T *kp = head(p.k), *qp = head(p.q), *vp = head(p.v) + col;
     for (int d = threadIdx.x; d < p.Dk; d += blockDim.x) {
@@ -51,17 +54,17 @@ hda_step_kernel(const __grid_constant__ HdaStep p, unsigned int *err) {
     if (in)
         for (int j = 0; j < 4; ++j) v[j] = get(vp + j);
     float *Sp = p.S + (slot * p.H + h) * p.Dk * (int64_t)p.Dv + col;
-    for (int d0 = warp; d0 < p.Dk; d0 += kWarps * kBatch) {
-        float4 sv[kBatch];
+    for (int d0 = row0; d0 < p.Dk; d0 += kRows * kLoad) {
+        float4 sv[kLoad];
 #pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
-            const int d = d0 + j * kWarps;
+        for (int j = 0; j < kLoad; ++j) {
+            const int d = d0 + j * kRows;
             sv[j] = (d < p.Dk && in) ? *reinterpret_cast<const float4 *>(Sp + (int64_t)d * p.Dv)
                                      : make_float4(0.f, 0.f, 0.f, 0.f);
         }
 #pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
-            const int d = d0 + j * kWarps;
+        for (int j = 0; j < kLoad; ++j) {
+            const int d = d0 + j * kRows;
             if (d < p.Dk && in) {
                 const float kd = rows[d], qd = rows[p.Dk + d];
                 float4 s4;
@@ -77,16 +80,16 @@ hda_step_kernel(const __grid_constant__ HdaStep p, unsigned int *err) {
             }
         }
     }
-    part[warp][lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+    part[row0][quad] = make_float4(acc[0], acc[1], acc[2], acc[3]);
     __syncthreads();
-    if (warp == 0 && in) {
-        float4 sum = part[0][lane];
-#pragma unroll
-        for (int w = 1; w < kWarps; ++w) {
-            sum.x += part[w][lane].x;
-            sum.y += part[w][lane].y;
-            sum.z += part[w][lane].z;
-            sum.w += part[w][lane].w;
+    if (row0 == 0 && in) {
+        float4 sum = part[0][quad];
+#pragma unroll 8
+        for (int w = 1; w < kRows; ++w) {
+            sum.x += part[w][quad].x;
+            sum.y += part[w][quad].y;
+            sum.z += part[w][quad].z;
+            sum.w += part[w][quad].w;
         }
         put(op, p.scale * sum.x);
         put(op + 1, p.scale * sum.y);
@@ -97,11 +100,21 @@ hda_step_kernel(const __grid_constant__ HdaStep p, unsigned int *err) {
 
 }  // namespace
 
-cudaError_t launch_hda_step(const HdaStep &p, unsigned int *dev_err, cudaStream_t s) {
-    const dim3 grid((unsigned)(p.R * p.H), (unsigned)((p.Dv + 127) / 128));
+template <typename T>
+static void run_step(const HdaStep &p, int num_sms, unsigned int *dev_err, cudaStream_t s) {
     const size_t smem = 2 * (size_t)p.Dk * sizeof(float);
-    if (p.io == 0) hda_step_kernel<__nv_bfloat16><<<grid, kWarps * 32, smem, s>>>(p, dev_err);
-    else hda_step_kernel<float><<<grid, kWarps * 32, smem, s>>>(p, dev_err);
+    const int64_t ctas = p.R * p.H * ((p.Dv + 127) / 128);
+    if (ctas >= num_sms)
+        hda_step_kernel<T, 128><<<dim3((unsigned)(p.R * p.H), (unsigned)((p.Dv + 127) / 128)), kThreads, smem, s>>>(
+            p, dev_err);
+    else
+        hda_step_kernel<T, 32><<<dim3((unsigned)(p.R * p.H), (unsigned)((p.Dv + 31) / 32)), kThreads, smem, s>>>(
+            p, dev_err);
+}
+
+cudaError_t launch_hda_step(const HdaStep &p, int num_sms, unsigned int *dev_err, cudaStream_t s) {
+    if (p.io == 0) run_step<__nv_bfloat16>(p, num_sms, dev_err, s);
+    else run_step<float>(p, num_sms, dev_err, s);
     const cudaError_t e = cudaGetLastError();
     if (e == cudaSuccess) count_launches(1);
     return e;

@@ -12,9 +12,11 @@
 //          a first kernel leaves each part's statistics, a second one combines them and writes.
 //          The second reading of x comes from L2 when the tensor fits there.
 //   plain: whatever does not come in whole 16-byte vectors of one group: a CTA per group.
-// Means and variances: each thread takes the exact mean and squared deviations of a few values at a
-// time and merges them with what it has (count, mean, M2), threads and parts are merged the same
-// way, in a fixed order; no variance is a difference of squares.
+// Means and variances: where a group is in registers, the mean and then the squared deviations from
+// it. Else each thread takes the mean of its first vector as a pivot and sums the deviations from
+// it and their squares; threads and parts are then merged as (count, mean, M2), in a fixed order.
+// (M2 = sum of squares - (sum)^2 / n loses digits only if the pivot is many standard deviations of
+// the thread's own values away from their mean, which a value among them cannot be.)
 #include <cuda_bf16.h>
 
 #include "gla_internal.h"
@@ -112,22 +114,18 @@ __device__ __forceinline__ float sum_lanes(float v, int width) {
     for (int o = width >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
 }
-template <int N>
-__device__ __forceinline__ Stat stat_of(const float (&f)[N]) {
-    float s = 0.f, q = 0.f;
-#pragma unroll
-    for (int i = 0; i < N; ++i) s += f[i];
-    const float mean = s * (1.f / N);
-#pragma unroll
-    for (int i = 0; i < N; ++i) q = fmaf(f[i] - mean, f[i] - mean, q);
-    return Stat{(float)N, mean, q};
-}
-
 // 8 (or 4) weights from memory, or their default.
 template <int N>
 __device__ __forceinline__ void load_param(const float *p, int64_t c, float otherwise, float (&f)[N]) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) f[i] = p ? p[c + i] : otherwise;
+    for (int i = 0; i < N; i += 4) {
+        const float4 v = p ? *reinterpret_cast<const float4 *>(p + c + i)
+                           : make_float4(otherwise, otherwise, otherwise, otherwise);
+        f[i] = v.x;
+        f[i + 1] = v.y;
+        f[i + 2] = v.z;
+        f[i + 3] = v.w;
+    }
 }
 
 // What the backward pass makes of one vector: xhat, du, and dgate in place of z.
@@ -162,13 +160,14 @@ struct RowPlan {
     int W;          // lanes per group
     int gpc;        // groups of a CTA (grid y covers all)
     int rp;         // entries a CTA handles at a time
+    int cg;         // channels of a group
 };
 
 template <typename T, int VPL, bool kGate>
 __global__ void __launch_bounds__(kThreads)
 norm_rows_fwd(const __grid_constant__ NormProblem p, const RowPlan r) {
     constexpr int V = Vec<T>::n;
-    const int cg = (int)(p.C / p.G), nv = cg / V;
+    const int cg = r.cg, nv = cg / V;
     const int seg = threadIdx.x / r.W, lane = threadIdx.x % r.W;
     const int64_t g = (int64_t)blockIdx.y * r.gpc + seg % r.gpc;
     const int64_t n0 = (int64_t)blockIdx.x * r.rp + seg / r.gpc, step = (int64_t)gridDim.x * r.rp;
@@ -182,35 +181,49 @@ norm_rows_fwd(const __grid_constant__ NormProblem p, const RowPlan r) {
         load_param(p.w, c, 1.f, w[k]);
         load_param(p.b, c, 0.f, b[k]);
     }
-    // the whole warp walks together (the shuffles need every lane): rows past the end do nothing
-    const int64_t rounds = (p.N - (int64_t)blockIdx.x * r.rp + step - 1) / step;
-    for (int64_t it = 0; it < rounds; ++it) {
-        const int64_t n = n0 + it * step;
-        const bool in = live && n < p.N;
-        const T *xp = static_cast<const T *>(p.x) + n * p.x_n + c0;
-        const T *zp = static_cast<const T *>(p.gate) + (kGate ? n * p.gate_n + c0 : 0);
-        float x[VPL][V];
-        uint4 zv[VPL];
-        Stat s{0.f, 0.f, 0.f};
+    const float inv = 1.f / (float)cg;
+    uint4 xv[VPL], zv[VPL];
+    auto load = [&](int64_t n) {
 #pragma unroll
         for (int k = 0; k < VPL; ++k) {
             const int v = lane + k * r.W;
-            uint4 xv = make_uint4(0, 0, 0, 0);
-            zv[k] = xv;
-            if (in && v < nv) {
-                xv = *reinterpret_cast<const uint4 *>(xp + v * V);
-                if (kGate) zv[k] = *reinterpret_cast<const uint4 *>(zp + v * V);
+            xv[k] = zv[k] = make_uint4(0, 0, 0, 0);
+            if (live && n < p.N && v < nv) {
+                xv[k] = *reinterpret_cast<const uint4 *>(static_cast<const T *>(p.x) + n * p.x_n + c0 + v * V);
+                if (kGate)
+                    zv[k] = *reinterpret_cast<const uint4 *>(static_cast<const T *>(p.gate) + n * p.gate_n + c0 + v * V);
             }
-            Vec<T>::unpack(xv, x[k]);
         }
+    };
+    load(n0);
+    // the whole warp walks together (the shuffles need every lane): rows past the end do nothing.
+    // The next entry is loaded while this one is worked on.
+    for (int64_t base = (int64_t)blockIdx.x * r.rp, n = n0; base < p.N; base += step, n += step) {
+        float x[VPL][V];
+        uint4 zc[VPL];
+#pragma unroll
+        for (int k = 0; k < VPL; ++k) {
+            Vec<T>::unpack(xv[k], x[k]);
+            zc[k] = zv[k];
+        }
+        load(n + step);
+        float sum = 0.f, sq = 0.f;      // (vectors past the group's are zeros)
 #pragma unroll
         for (int k = 0; k < VPL; ++k)
-            if (lane + k * r.W < nv) s = merge(s, stat_of(x[k]));
-        s = merge_lanes(s, r.W);
-        const float rstd = 1.f / sqrtf(s.m2 / (float)cg + p.eps);
-        if (!in) continue;
+#pragma unroll
+            for (int i = 0; i < V; ++i) sum += x[k][i];
+        const float mean = sum_lanes(sum, r.W) * inv;
+#pragma unroll
+        for (int k = 0; k < VPL; ++k)
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                x[k][i] -= mean;
+                if (lane + k * r.W < nv) sq = fmaf(x[k][i], x[k][i], sq);
+            }
+        const float rstd = 1.f / sqrtf(fmaf(sum_lanes(sq, r.W), inv, p.eps));
+        if (!live || n >= p.N) continue;
         if (lane == 0) {
-            if (p.mean) p.mean[n * p.G + g] = s.mean;
+            if (p.mean) p.mean[n * p.G + g] = mean;
             if (p.rstd) p.rstd[n * p.G + g] = rstd;
         }
         T *yp = static_cast<T *>(p.y) + n * p.C + c0;
@@ -219,10 +232,10 @@ norm_rows_fwd(const __grid_constant__ NormProblem p, const RowPlan r) {
             const int v = lane + k * r.W;
             if (v >= nv) continue;
             float z[V];
-            if (kGate) Vec<T>::unpack(zv[k], z);
+            if (kGate) Vec<T>::unpack(zc[k], z);
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                const float u = fmaf((x[k][i] - s.mean) * rstd, w[k][i], b[k][i]);
+                const float u = fmaf(x[k][i] * rstd, w[k][i], b[k][i]);
                 x[k][i] = kGate ? u * act_of<T>(z[i], p.act) : act_of<T>(u, p.act);
             }
             *reinterpret_cast<uint4 *>(yp + v * V) = Vec<T>::pack(x[k]);
@@ -235,7 +248,7 @@ template <typename T, int VPL, bool kGate>
 __global__ void __launch_bounds__(kThreads)
 norm_rows_bwd(const __grid_constant__ NormProblem p, const RowPlan r, float *sums) {
     constexpr int V = Vec<T>::n;
-    const int cg = (int)(p.C / p.G), nv = cg / V;
+    const int cg = r.cg, nv = cg / V;
     const int seg = threadIdx.x / r.W, lane = threadIdx.x % r.W;
     const int64_t g = (int64_t)blockIdx.y * r.gpc + seg % r.gpc;
     const int64_t n0 = (int64_t)blockIdx.x * r.rp + seg / r.gpc, step = (int64_t)gridDim.x * r.rp;
@@ -252,35 +265,49 @@ norm_rows_bwd(const __grid_constant__ NormProblem p, const RowPlan r, float *sum
         for (int i = 0; i < V; ++i) dw[k][i] = db[k][i] = 0.f;
     }
     const float inv = 1.f / (float)cg;
-    const int64_t rounds = (p.N - (int64_t)blockIdx.x * r.rp + step - 1) / step;
-    for (int64_t it = 0; it < rounds; ++it) {
-        const int64_t n = n0 + it * step;
+    uint4 xv[VPL], dv[VPL], zv[VPL];
+    float mean, rstd;
+    auto load = [&](int64_t n) {
         const bool in = live && n < p.N;
-        const T *xp = static_cast<const T *>(p.x) + n * p.x_n + c0;
-        const T *dp = static_cast<const T *>(p.dy) + n * p.dy_n + c0;
-        const T *zp = static_cast<const T *>(p.gate) + (kGate ? n * p.gate_n + c0 : 0);
-        uint4 xv[VPL], dv[VPL], zv[VPL];
 #pragma unroll
         for (int k = 0; k < VPL; ++k) {
             const int v = lane + k * r.W;
             xv[k] = dv[k] = zv[k] = make_uint4(0, 0, 0, 0);
             if (in && v < nv) {
-                xv[k] = *reinterpret_cast<const uint4 *>(xp + v * V);
-                dv[k] = *reinterpret_cast<const uint4 *>(dp + v * V);
-                if (kGate) zv[k] = *reinterpret_cast<const uint4 *>(zp + v * V);
+                xv[k] = *reinterpret_cast<const uint4 *>(static_cast<const T *>(p.x) + n * p.x_n + c0 + v * V);
+                dv[k] = *reinterpret_cast<const uint4 *>(static_cast<const T *>(p.dy) + n * p.dy_n + c0 + v * V);
+                if (kGate)
+                    zv[k] = *reinterpret_cast<const uint4 *>(static_cast<const T *>(p.gate) + n * p.gate_n + c0 + v * V);
             }
         }
-        const float mean = in ? p.mean[n * p.G + g] : 0.f, rstd = in ? p.rstd[n * p.G + g] : 0.f;
+        mean = in ? p.mean[n * p.G + g] : 0.f;
+        rstd = in ? p.rstd[n * p.G + g] : 0.f;
+    };
+    // (a lane with more than one vector has no registers for the next entry's)
+    constexpr bool kAhead = VPL == 1;
+    if (kAhead) load(n0);
+    for (int64_t base = (int64_t)blockIdx.x * r.rp, n = n0; base < p.N; base += step, n += step) {
+        const bool in = live && n < p.N;
+        if (!kAhead) load(n);
+        uint4 xc[VPL], dc[VPL], zc[VPL];
+#pragma unroll
+        for (int k = 0; k < VPL; ++k) {
+            xc[k] = xv[k];
+            dc[k] = dv[k];
+            zc[k] = zv[k];
+        }
+        const float mu = mean, rs = rstd;
+        if (kAhead) load(n + step);
         float x[VPL][V], d[VPL][V], z[V];
         float s1 = 0.f, s2 = 0.f;
         T *gp = static_cast<T *>(p.dgate) + (kGate ? n * p.C + c0 : 0);
 #pragma unroll
         for (int k = 0; k < VPL; ++k) {
             const int v = lane + k * r.W;
-            Vec<T>::unpack(xv[k], x[k]);
-            Vec<T>::unpack(dv[k], d[k]);
-            Vec<T>::unpack(zv[k], z);
-            grad_vec<T, kGate>(x[k], d[k], z, w[k], b[k], mean, rstd, p.act);
+            Vec<T>::unpack(xc[k], x[k]);
+            Vec<T>::unpack(dc[k], d[k]);
+            Vec<T>::unpack(zc[k], z);
+            grad_vec<T, kGate>(x[k], d[k], z, w[k], b[k], mu, rs, p.act);
             if (!in || v >= nv) continue;
             if (kGate) *reinterpret_cast<uint4 *>(gp + v * V) = Vec<T>::pack(z);
 #pragma unroll
@@ -301,7 +328,7 @@ norm_rows_bwd(const __grid_constant__ NormProblem p, const RowPlan r, float *sum
             const int v = lane + k * r.W;
             if (v >= nv) continue;
 #pragma unroll
-            for (int i = 0; i < V; ++i) x[k][i] = rstd * (d[k][i] - s1 - x[k][i] * s2);
+            for (int i = 0; i < V; ++i) x[k][i] = rs * (d[k][i] - s1 - x[k][i] * s2);
             *reinterpret_cast<uint4 *>(op + v * V) = Vec<T>::pack(x[k]);
         }
     }
@@ -326,21 +353,24 @@ struct MapPlan {
     int parts;      // of an entry's positions
     int nvb;        // vector columns of a block (a multiple of a group's)
     int ry;         // positions at a time
+    int nv, groups; // vector columns of a group, groups of a block
+    int cols;       // vector columns of a row
+    int len;        // positions of a part
 };
 struct MapPos {
     int tx, ty;
     int64_t n, l0, l1, v;   // v: vector column in the row
     bool live;
 };
-__device__ __forceinline__ MapPos map_pos(const NormProblem &p, const MapPlan &m, int V) {
+__device__ __forceinline__ MapPos map_pos(const NormProblem &p, const MapPlan &m) {
     MapPos q;
     q.tx = threadIdx.x % m.nvb;
     q.ty = threadIdx.x / m.nvb;
     q.n = blockIdx.z;
-    q.l0 = p.L * blockIdx.x / m.parts;
-    q.l1 = p.L * (blockIdx.x + 1) / m.parts;
+    q.l0 = (int64_t)m.len * blockIdx.x;
+    q.l1 = min(q.l0 + m.len, p.L);
     q.v = (int64_t)blockIdx.y * m.nvb + q.tx;
-    q.live = q.ty < m.ry && q.v < p.C / V;
+    q.live = q.ty < m.ry && q.v < m.cols;
     return q;
 }
 
@@ -350,10 +380,11 @@ norm_maps_stats(const __grid_constant__ NormProblem p, const MapPlan m, Stat *pa
     constexpr int V = Vec<T>::n, kAhead = 4;
     tc::pdl_launch_dependents();
     __shared__ Stat sh[kThreads];
-    const MapPos q = map_pos(p, m, V);
+    const MapPos q = map_pos(p, m);
     Stat s{0.f, 0.f, 0.f};
-    if (q.live) {
+    if (q.live && q.l0 + q.ty < q.l1) {
         const T *xp = static_cast<const T *>(p.x) + q.n * p.x_n + q.v * V;
+        float pivot = 0.f, s1 = 0.f, s2 = 0.f, n = 0.f;
         for (int64_t l = q.l0 + q.ty; l < q.l1; l += (int64_t)m.ry * kAhead) {
             uint4 xv[kAhead];
 #pragma unroll
@@ -364,61 +395,71 @@ norm_maps_stats(const __grid_constant__ NormProblem p, const MapPlan m, Stat *pa
                 if (l + a * m.ry < q.l1) {
                     float f[V];
                     Vec<T>::unpack(xv[a], f);
-                    s = merge(s, stat_of(f));
+                    if (n == 0.f) {
+                        float t = 0.f;
+#pragma unroll
+                        for (int i = 0; i < V; ++i) t += f[i];
+                        pivot = t * (1.f / V);
+                    }
+                    n += (float)V;
+#pragma unroll
+                    for (int i = 0; i < V; ++i) {
+                        const float d = f[i] - pivot;
+                        s1 += d;
+                        s2 = fmaf(d, d, s2);
+                    }
                 }
         }
+        const float d = s1 / n;
+        s = Stat{n, pivot + d, fmaxf(fmaf(-s1, d, s2), 0.f)};
+        if (!(s2 < INFINITY)) s.m2 = s2;    // infinity or NaN (which fmaxf would drop)
     }
     sh[threadIdx.x] = s;
     __syncthreads();
     // a warp per group: its columns and position slots
-    const int nv = (int)(p.C / p.G) / V, groups = m.nvb / nv, lane = threadIdx.x & 31;
-    for (int g = threadIdx.x >> 5; g < groups; g += kWarps) {
+    const int lane = threadIdx.x & 31, entries = m.nv * m.ry;
+    for (int g = threadIdx.x >> 5; g < m.groups; g += kWarps) {
         Stat t{0.f, 0.f, 0.f};
-        for (int e = lane; e < nv * m.ry; e += 32) t = merge(t, sh[e / nv * m.nvb + g * nv + e % nv]);
+        for (int e = lane; e < entries; e += 32) t = merge(t, sh[e / m.nv * m.nvb + g * m.nv + e % m.nv]);
         t = merge_lanes(t, 32);
-        const int64_t gg = (int64_t)blockIdx.y * groups + g;
-        if (lane == 0 && gg < p.G) part[((int64_t)q.n * m.parts + blockIdx.x) * p.G + gg] = t;
+        const int64_t gg = (int64_t)blockIdx.y * m.groups + g;
+        if (lane == 0 && gg < p.G) part[((int64_t)q.n * p.G + gg) * m.parts + blockIdx.x] = t;
     }
 }
 
-// Statistics of the block's groups from those of the parts -> shared memory.
-__device__ __forceinline__ void load_stats(const NormProblem &p, const MapPlan &m, const Stat *part, int groups,
-                                           float *mean, float *rstd) {
+// The parts' statistics of one group of one entry, a warp each -> mean and rstd (stat [N, G] for the
+// next kernel, and the caller's). Combined here once: done by every CTA of the next kernel, it
+// cost more than the whole of its other work (3 maps of 4095 x 512: 50 us).
+__global__ void __launch_bounds__(kThreads)
+norm_maps_combine(const __grid_constant__ NormProblem p, const MapPlan m, const Stat *part, float2 *stat) {
+    tc::pdl_launch_dependents();
+    const int64_t i = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
-    for (int g = threadIdx.x >> 5; g < groups; g += kWarps) {
-        const int64_t gg = (int64_t)blockIdx.y * groups + g;
-        if (gg >= p.G) break;
-        Stat t{0.f, 0.f, 0.f};
-        for (int e = lane; e < m.parts; e += 32)
-            t = merge(t, part[((int64_t)blockIdx.z * m.parts + e) * p.G + gg]);
-        t = merge_lanes(t, 32);
-        if (lane == 0) {
-            mean[g] = t.mean;
-            rstd[g] = 1.f / sqrtf(t.m2 / t.n + p.eps);
-            if (blockIdx.x == 0) {
-                if (p.mean) p.mean[blockIdx.z * p.G + gg] = mean[g];
-                if (p.rstd) p.rstd[blockIdx.z * p.G + gg] = rstd[g];
-            }
-        }
-    }
-    __syncthreads();
+    tc::pdl_wait_prerequisites();
+    if (i >= p.N * p.G) return;
+    Stat t{0.f, 0.f, 0.f};
+    for (int e = lane; e < m.parts; e += 32) t = merge(t, part[i * m.parts + e]);
+    t = merge_lanes(t, 32);
+    if (lane != 0) return;
+    const float rstd = 1.f / sqrtf(t.m2 / t.n + p.eps);
+    stat[i] = make_float2(t.mean, rstd);
+    if (p.mean) p.mean[i] = t.mean;
+    if (p.rstd) p.rstd[i] = rstd;
 }
 
 template <typename T, bool kGate>
 __global__ void __launch_bounds__(kThreads)
-norm_maps_apply(const __grid_constant__ NormProblem p, const MapPlan m, const Stat *part) {
+norm_maps_apply(const __grid_constant__ NormProblem p, const MapPlan m, const float2 *stat) {
     constexpr int V = Vec<T>::n, kAhead = 2;
-    __shared__ float sm[kThreads], sr[kThreads];
-    const MapPos q = map_pos(p, m, V);
+    const MapPos q = map_pos(p, m);
     float w[V], b[V];
     const int64_t c = (q.live ? q.v : 0) * V;
     load_param(p.w, c, 1.f, w);
     load_param(p.b, c, 0.f, b);
     tc::pdl_wait_prerequisites();
-    const int nv = (int)(p.C / p.G) / V;
-    load_stats(p, m, part, m.nvb / nv, sm, sr);
     if (!q.live) return;
-    const float mean = sm[q.tx / nv], rstd = sr[q.tx / nv];
+    const float2 st = stat[q.n * p.G + q.v / m.nv];
+    const float mean = st.x, rstd = st.y;
     const T *xp = static_cast<const T *>(p.x) + q.n * p.x_n + c;
     const T *zp = static_cast<const T *>(p.gate) + (kGate ? q.n * p.gate_n + c : 0);
     T *yp = static_cast<T *>(p.y) + q.n * p.L * p.C + c;
@@ -454,8 +495,8 @@ norm_maps_bwd_stats(const __grid_constant__ NormProblem p, const MapPlan m, floa
     tc::pdl_launch_dependents();
     __shared__ float2 sh[kThreads];
     extern __shared__ float ch[];      // [threads][2 V] channel sums of the position slots
-    const MapPos q = map_pos(p, m, V);
-    const int nv = (int)(p.C / p.G) / V;
+    const MapPos q = map_pos(p, m);
+    const int nv = m.nv;
     float dw[V], db[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) dw[i] = db[i] = 0.f;
@@ -492,7 +533,7 @@ norm_maps_bwd_stats(const __grid_constant__ NormProblem p, const MapPlan m, floa
         ch[threadIdx.x * 2 * V + V + i] = db[i];
     }
     __syncthreads();
-    const int groups = m.nvb / nv, lane = threadIdx.x & 31;
+    const int groups = m.groups, lane = threadIdx.x & 31;
     for (int g = threadIdx.x >> 5; g < groups; g += kWarps) {
         float a = 0.f, b = 0.f;
         for (int e = lane; e < nv * m.ry; e += 32) {
@@ -503,7 +544,7 @@ norm_maps_bwd_stats(const __grid_constant__ NormProblem p, const MapPlan m, floa
         a = sum_lanes(a, 32);
         b = sum_lanes(b, 32);
         const int64_t gg = (int64_t)blockIdx.y * groups + g;
-        if (lane == 0 && gg < p.G) part[((int64_t)q.n * m.parts + blockIdx.x) * p.G + gg] = make_float2(a, b);
+        if (lane == 0 && gg < p.G) part[((int64_t)q.n * p.G + gg) * m.parts + blockIdx.x] = make_float2(a, b);
     }
     if (!sums) return;
     float *sp = sums + ((int64_t)q.n * m.parts + blockIdx.x) * 2 * p.C;
@@ -517,39 +558,39 @@ norm_maps_bwd_stats(const __grid_constant__ NormProblem p, const MapPlan m, floa
     }
 }
 
+// The parts' sums of one group of one entry, a warp each -> their means.
+__global__ void __launch_bounds__(kThreads)
+norm_maps_bwd_combine(const __grid_constant__ NormProblem p, const MapPlan m, const float2 *part, float2 *mean) {
+    tc::pdl_launch_dependents();
+    const int64_t i = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    tc::pdl_wait_prerequisites();
+    if (i >= p.N * p.G) return;
+    float a = 0.f, b = 0.f;
+    for (int e = lane; e < m.parts; e += 32) {
+        const float2 t = part[i * m.parts + e];
+        a += t.x;
+        b += t.y;
+    }
+    a = sum_lanes(a, 32);
+    b = sum_lanes(b, 32);
+    const float inv = 1.f / ((float)p.L * (float)(m.nv * (p.io == 0 ? 8 : 4)));
+    if (lane == 0) mean[i] = make_float2(a * inv, b * inv);
+}
+
 template <typename T, bool kGate>
 __global__ void __launch_bounds__(kThreads)
-norm_maps_bwd_apply(const __grid_constant__ NormProblem p, const MapPlan m, const float2 *part) {
+norm_maps_bwd_apply(const __grid_constant__ NormProblem p, const MapPlan m, const float2 *means) {
     constexpr int V = Vec<T>::n;
-    tc::pdl_launch_dependents();
-    __shared__ float sh1[kThreads], sh2[kThreads];
-    const MapPos q = map_pos(p, m, V);
-    const int nv = (int)(p.C / p.G) / V, groups = m.nvb / nv, lane = threadIdx.x & 31;
-    const float inv = 1.f / ((float)p.L * (float)(p.C / p.G));
+    const MapPos q = map_pos(p, m);
+    const int nv = m.nv;
     tc::pdl_wait_prerequisites();
-    for (int g = threadIdx.x >> 5; g < groups; g += kWarps) {
-        const int64_t gg = (int64_t)blockIdx.y * groups + g;
-        if (gg >= p.G) break;
-        float a = 0.f, b = 0.f;
-        for (int e = lane; e < m.parts; e += 32) {
-            const float2 t = part[((int64_t)q.n * m.parts + e) * p.G + gg];
-            a += t.x;
-            b += t.y;
-        }
-        a = sum_lanes(a, 32);
-        b = sum_lanes(b, 32);
-        if (lane == 0) {
-            sh1[g] = a * inv;
-            sh2[g] = b * inv;
-        }
-    }
-    __syncthreads();
     if (!q.live) return;
     const int64_t c = q.v * V, at = q.n * p.G + q.v / nv;
     float w[V], b[V];
     load_param(p.w, c, 1.f, w);
     load_param(p.b, c, 0.f, b);
-    const float mean = p.mean[at], rstd = p.rstd[at], s1 = sh1[q.tx / nv], s2 = sh2[q.tx / nv];
+    const float mean = p.mean[at], rstd = p.rstd[at], s1 = means[at].x, s2 = means[at].y;
     const T *xp = static_cast<const T *>(p.x) + q.n * p.x_n + c;
     const T *dp = static_cast<const T *>(p.dy) + q.n * p.dy_n + c;
     const T *zp = static_cast<const T *>(p.gate) + (kGate ? q.n * p.gate_n + c : 0);
@@ -569,22 +610,25 @@ norm_maps_bwd_apply(const __grid_constant__ NormProblem p, const MapPlan m, cons
     }
 }
 
-// dw, db: the partial sums added in order. Thread (channel, slice): 32 channels, 8 slices of parts.
-__global__ void __launch_bounds__(kThreads)
-norm_sum_parts(const float *sums, int64_t parts, int64_t C, float *dw, float *db) {
-    __shared__ float sh[8][32];
-    tc::pdl_wait_prerequisites();
+// dw, db: the partial sums added in order. Thread (channel, slice): 32 channels, 32 slices of parts.
+constexpr int kSumThreads = 1024;
+__global__ void __launch_bounds__(kSumThreads)
+norm_sum_parts(const float *__restrict__ sums, int parts, int64_t C, float *dw, float *db) {
+    __shared__ float sh[32][33];
     const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
     const int64_t e = (int64_t)blockIdx.x * 32 + tx;      // 0 .. 2 C - 1
     float t = 0.f;
-    if (e < 2 * C)
-        for (int64_t i = ty; i < parts; i += 8) t += sums[i * 2 * C + e];
+    if (e < 2 * C) {
+#pragma unroll 8
+        for (int i = ty; i < parts; i += 32) t += sums[i * 2 * C + e];
+    }
     sh[ty][tx] = t;
     __syncthreads();
-    if (ty != 0 || e >= 2 * C) return;
-    for (int i = 1; i < 8; ++i) t += sh[i][tx];
-    float *to = e < C ? dw : db;
-    if (to) to[e % C] = t;
+    t = sum_lanes(sh[tx][ty], 32);      // channel ty of this block, over the slices
+    const int64_t c = (int64_t)blockIdx.x * 32 + ty;
+    if (tx != 0 || c >= 2 * C) return;
+    float *to = c < C ? dw : db;
+    if (to) to[c < C ? c : c - C] = t;
 }
 
 // ======================================================================= plain
@@ -720,12 +764,14 @@ Route route(const NormProblem &p, bool backward) {
 }
 bool aligned(const NormProblem &p) {
     return !((reinterpret_cast<uintptr_t>(p.x) | reinterpret_cast<uintptr_t>(p.gate) |
-              reinterpret_cast<uintptr_t>(p.dy)) & 15u);
+              reinterpret_cast<uintptr_t>(p.dy) | reinterpret_cast<uintptr_t>(p.w) |
+              reinterpret_cast<uintptr_t>(p.b)) & 15u);
 }
 
 RowPlan row_plan(const NormProblem &p) {
     const int nv = (int)(p.C / p.G / vec_of(p));
     RowPlan r;
+    r.cg = (int)(p.C / p.G);
     r.W = 1;
     while (r.W < nv && r.W < 32) r.W <<= 1;
     const int segs = kThreads / r.W;
@@ -743,11 +789,16 @@ dim3 row_grid(const NormProblem &p, const RowPlan &r, int sms, int per_sm) {
 MapPlan map_plan(const NormProblem &p, int sms) {
     const int64_t V = vec_of(p), nv = p.C / p.G / V;
     MapPlan m;
-    m.nvb = (int)min(p.C / V, kThreads / nv * nv);
+    m.nv = (int)nv;
+    m.cols = (int)(p.C / V);
+    m.nvb = (int)min((int64_t)m.cols, kThreads / nv * nv);
+    m.groups = m.nvb / m.nv;
     m.ry = kThreads / m.nvb;
     // parts: about four CTAs an SM, of at least four rounds of positions
     const int64_t blocks = (p.C / V + m.nvb - 1) / m.nvb * p.N;
-    m.parts = (int)max((int64_t)1, min((int64_t)sms * 4 / blocks, p.L / (4 * m.ry)));
+    const int64_t parts = max((int64_t)1, min((int64_t)sms * 4 / blocks, p.L / (4 * m.ry)));
+    m.len = (int)((p.L + parts - 1) / parts);
+    m.parts = (int)((p.L + m.len - 1) / m.len);
     return m;
 }
 dim3 map_grid(const NormProblem &p, const MapPlan &m) {
@@ -755,7 +806,9 @@ dim3 map_grid(const NormProblem &p, const MapPlan &m) {
 }
 
 size_t round256(size_t n) { return (n + 255) & ~size_t(255); }
-constexpr int kFwdPerSm = 8, kBwdPerSm = 3;
+constexpr int kFwdPerSm = 5, kBwdPerSm = 2;
+dim3 combine_grid(const NormProblem &p) { return dim3((unsigned)((p.N * p.G + kWarps - 1) / kWarps)); }
+size_t mean_bytes(const NormProblem &p) { return round256((size_t)(p.N * p.G) * sizeof(float2)); }
 
 // Bytes of the parts' statistics, and parts of the channel sums.
 size_t stat_bytes(const NormProblem &p, const MapPlan &m, bool backward) {
@@ -763,13 +816,14 @@ size_t stat_bytes(const NormProblem &p, const MapPlan &m, bool backward) {
 }
 
 template <typename... A>
-cudaError_t launch(void (*kernel)(A...), dim3 grid, size_t smem, bool dependent, cudaStream_t s, A... args) {
+cudaError_t launch_n(void (*kernel)(A...), dim3 grid, int threads, size_t smem, bool dependent, cudaStream_t s,
+                     A... args) {
     cudaLaunchAttribute pdl[1];
     pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     pdl[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = grid;
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cfg.attrs = pdl;
@@ -777,6 +831,10 @@ cudaError_t launch(void (*kernel)(A...), dim3 grid, size_t smem, bool dependent,
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
     if (e == cudaSuccess) count_launches(1);
     return e;
+}
+template <typename... A>
+cudaError_t launch(void (*kernel)(A...), dim3 grid, size_t smem, bool dependent, cudaStream_t s, A... args) {
+    return launch_n(kernel, grid, kThreads, smem, dependent, s, args...);
 }
 
 template <typename T, bool kGate>
@@ -793,9 +851,12 @@ cudaError_t run_fwd(const NormProblem &p, void *ws, int sms, cudaStream_t s) {
     if (rt == kMaps) {
         const MapPlan m = map_plan(p, sms);
         Stat *part = static_cast<Stat *>(ws);
-        const cudaError_t e = launch(norm_maps_stats<T>, map_grid(p, m), 0, false, s, p, m, part);
+        float2 *stat = reinterpret_cast<float2 *>(static_cast<char *>(ws) + stat_bytes(p, m, false));
+        cudaError_t e = launch(norm_maps_stats<T>, map_grid(p, m), 0, false, s, p, m, part);
         if (e != cudaSuccess) return e;
-        return launch(norm_maps_apply<T, kGate>, map_grid(p, m), 0, true, s, p, m, (const Stat *)part);
+        e = launch(norm_maps_combine, combine_grid(p), 0, true, s, p, m, (const Stat *)part, stat);
+        if (e != cudaSuccess) return e;
+        return launch(norm_maps_apply<T, kGate>, map_grid(p, m), 0, true, s, p, m, (const float2 *)stat);
     }
     return launch(norm_plain_fwd<T>, dim3((unsigned)(p.N * p.G)), 0, false, s, p);
 }
@@ -812,7 +873,6 @@ cudaError_t run_bwd(const NormProblem &p, void *ws, int sms, cudaStream_t s) {
     }
     float *sums = nullptr;
     int64_t parts;
-    bool dependent = false;
     if (rt == kRows) {
         const RowPlan r = row_plan(p);
         const int vpl = (int)((p.C / p.G / Vec<T>::n + r.W - 1) / r.W);
@@ -826,15 +886,18 @@ cudaError_t run_bwd(const NormProblem &p, void *ws, int sms, cudaStream_t s) {
         const MapPlan m = map_plan(p, sms);
         float2 *part = static_cast<float2 *>(ws);
         parts = p.N * m.parts;
-        if (want) sums = reinterpret_cast<float *>(static_cast<char *>(ws) + stat_bytes(p, m, true));
+        float2 *means = reinterpret_cast<float2 *>(static_cast<char *>(ws) + stat_bytes(p, m, true));
+        if (want) sums = reinterpret_cast<float *>(static_cast<char *>(ws) + stat_bytes(p, m, true) + mean_bytes(p));
         const size_t smem = (size_t)kThreads * 2 * Vec<T>::n * sizeof(float);
         e = launch(norm_maps_bwd_stats<T, kGate>, map_grid(p, m), smem, false, s, p, m, part, sums);
         if (e != cudaSuccess) return e;
-        e = launch(norm_maps_bwd_apply<T, kGate>, map_grid(p, m), 0, true, s, p, m, (const float2 *)part);
+        e = launch(norm_maps_bwd_combine, combine_grid(p), 0, true, s, p, m, (const float2 *)part, means);
+        if (e != cudaSuccess) return e;
+        e = launch(norm_maps_bwd_apply<T, kGate>, map_grid(p, m), 0, true, s, p, m, (const float2 *)means);
     }
     if (e != cudaSuccess || !want) return e;
-    return launch(norm_sum_parts, dim3((unsigned)((2 * p.C + 31) / 32)), 0, dependent, s,
-                  (const float *)sums, parts, p.C, p.dw, p.db);
+    return launch_n(norm_sum_parts, dim3((unsigned)((2 * p.C + 31) / 32)), kSumThreads, 0, false, s,
+                    (const float *)sums, (int)parts, p.C, p.dw, p.db);
 }
 
 }  // namespace
@@ -848,7 +911,7 @@ size_t norm_workspace_bytes(const NormProblem &p, bool backward, int num_sms) {
         return (size_t)row_grid(p, r, num_sms, kBwdPerSm).x * r.rp * 2 * p.C * sizeof(float);
     }
     const MapPlan m = map_plan(p, num_sms);
-    return stat_bytes(p, m, backward) + (backward ? (size_t)(p.N * m.parts) * 2 * p.C * sizeof(float) : 0);
+    return stat_bytes(p, m, backward) + mean_bytes(p) + (backward ? (size_t)(p.N * m.parts) * 2 * p.C * sizeof(float) : 0);
 }
 
 cudaError_t launch_norm_fwd(const NormProblem &p, void *ws, int num_sms, cudaStream_t s) {

@@ -492,7 +492,7 @@ gla_status hda_step(const void *q, const void *k, const void *v, const float *de
     p.Dk = (int)sh.Dk;
     p.Dv = (int)sh.Dv;
     p.io = sh.io;
-    const cudaError_t e = gla::launch_hda_step(p, err, reinterpret_cast<cudaStream_t>(stream));
+    const cudaError_t e = gla::launch_hda_step(p, sms, err, reinterpret_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? GLA_OK : (gla_status)gla::launch_failed("decay step launch", e);
 }
 

@@ -64,6 +64,8 @@ _lib = None
 def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     """Load libgla.so (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(path):
@@ -137,6 +139,11 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+def _addr(t):
+    """A tensor's address as ctypes takes it for a declared pointer argument (None: NULL)."""
+    return None if t is None else t.data_ptr()
+
+
 def _stream_handle(stream) -> ctypes.c_void_p:
     if stream is None:
         stream = torch.cuda.current_stream()
@@ -145,11 +152,14 @@ def _stream_handle(stream) -> ctypes.c_void_p:
 
 def _launch(f, device, stream, *args):
     """f(*args, stream handle) with ``device`` current: switching costs as much as a small call,
-    so it is only done when another device is."""
-    if device.index == torch.cuda.current_device():
-        return f(*args, _stream_handle(stream))
-    with torch.cuda.device(device):
-        return f(*args, _stream_handle(stream))
+    so it is only done when another device is. (The raw handle of torch's current stream, without
+    a Stream object around it, for the same reason.)"""
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return _launch(f, device, stream, *args)
+    if stream is None:
+        return f(*args, torch._C._cuda_getCurrentRawStream(device.index))
+    return f(*args, stream.cuda_stream)
 
 
 def _check(t, name, dtype, shape, device):
@@ -157,7 +167,7 @@ def _check(t, name, dtype, shape, device):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.device != device:
         raise ValueError(f"{name}: on {t.device}, expected {device}")

@@ -14,7 +14,7 @@ import functools
 
 import torch
 
-from .gla import (GLA_OK, GLAError, IO_BF16, IO_F32, _HdaShape, _check, _launch, _ptr,
+from .gla import (GLA_OK, GLAError, IO_BF16, IO_F32, _HdaShape, _check, _addr, _launch,
                   load_library, options)
 
 
@@ -120,8 +120,8 @@ def hda_fwd(q, k, v, decay, scale: float, h0=None, *, o=None, hT=None, return_st
         hT = torch.empty((B, H, Dk, Dv), dtype=torch.float32, device=dev)
     _state(hT, "hT", (B, H, Dk, Dv), dev)
     opt = options(path, seq_splits, workspace)
-    rc = _launch(lib.hda_fwd, dev, stream, _ptr(q), _ptr(k), _ptr(v), _ptr(decay), scale, _ptr(h0),
-                 _ptr(o), _ptr(hT), ctypes.byref(sh), ctypes.byref(opt))
+    rc = _launch(lib.hda_fwd, dev, stream, _addr(q), _addr(k), _addr(v), _addr(decay), scale, _addr(h0),
+                 _addr(o), _addr(hT), ctypes.byref(sh), ctypes.byref(opt))
     _fail(lib, rc, "hda_fwd")
     return o, hT
 
@@ -143,8 +143,8 @@ def hda_bwd(do, q, k, v, decay, scale: float, h0=None, dhT=None, *, path: str = 
     dq, dk, dv = (torch.empty(t.shape, dtype=t.dtype, device=dev) for t in (q, k, v))
     dh0 = None if h0 is None else torch.empty_like(h0)
     opt = options(path, seq_splits, workspace)
-    rc = _launch(lib.hda_bwd, dev, stream, _ptr(do), _ptr(q), _ptr(k), _ptr(v), _ptr(decay), scale,
-                 _ptr(h0), _ptr(dhT), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dh0), ctypes.byref(sh),
+    rc = _launch(lib.hda_bwd, dev, stream, _addr(do), _addr(q), _addr(k), _addr(v), _addr(decay), scale,
+                 _addr(h0), _addr(dhT), _addr(dq), _addr(dk), _addr(dv), _addr(dh0), ctypes.byref(sh),
                  ctypes.byref(opt))
     _fail(lib, rc, "hda_bwd")
     return dq, dk, dv, dh0
@@ -184,7 +184,7 @@ def hda_step(q, k, v, decay, scale: float, S, slots=None, *, o=None, stream=None
         o = torch.empty((R, H, Dv), dtype=q.dtype, device=dev)
     else:
         _check(o, "o", q.dtype, (R, H, Dv), dev)
-    rc = _launch(lib.hda_step, dev, stream, _ptr(q), _ptr(k), _ptr(v), _ptr(decay), scale, _ptr(S),
-                 _ptr(slots), _ptr(o), P, ctypes.byref(sh))
+    rc = _launch(lib.hda_step, dev, stream, _addr(q), _addr(k), _addr(v), _addr(decay), scale, _addr(S),
+                 _addr(slots), _addr(o), P, ctypes.byref(sh))
     _fail(lib, rc, "hda_step")
     return o

@@ -11,7 +11,7 @@ import functools
 
 import torch
 
-from .gla import IO_BF16, IO_F32, _NormShape, _check, _launch, _ptr, load_library
+from .gla import IO_BF16, IO_F32, _NormShape, _check, _addr, _launch, load_library
 from .hda import _fail
 
 ACTS = {"none": 0, "silu": 1, "gelu": 2}
@@ -92,7 +92,7 @@ def _workspace(workspace, dev):
         return None, 0
     if workspace.device != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the inputs' device")
-    return _ptr(workspace), workspace.numel() * workspace.element_size()
+    return _addr(workspace), workspace.numel() * workspace.element_size()
 
 
 def group_norm_workspace_size(x, groups: int, backward: bool = False, gate=None) -> int:
@@ -116,8 +116,8 @@ def group_norm_fwd(x, groups: int, weight=None, bias=None, *, eps: float = 1e-5,
     mean = torch.empty((sh.N, max(sh.G, 0)), dtype=torch.float32, device=dev)
     rstd = torch.empty_like(mean)
     ws, nws = _workspace(workspace, dev)
-    rc = _launch(lib.gla_group_norm_fwd, dev, stream, _ptr(x), _ptr(weight), _ptr(bias), _ptr(gate),
-                 _ptr(y), _ptr(mean), _ptr(rstd), ctypes.byref(sh), ws, nws)
+    rc = _launch(lib.gla_group_norm_fwd, dev, stream, _addr(x), _addr(weight), _addr(bias), _addr(gate),
+                 _addr(y), _addr(mean), _addr(rstd), ctypes.byref(sh), ws, nws)
     _fail(lib, rc, "gla_group_norm_fwd")
     return y, mean, rstd
 
@@ -137,8 +137,8 @@ def group_norm_bwd(dy, x, mean, rstd, groups: int, weight=None, bias=None, *, ac
     dw = None if weight is None else torch.empty_like(weight)
     db = None if bias is None else torch.empty_like(bias)
     ws, nws = _workspace(workspace, dev)
-    rc = _launch(lib.gla_group_norm_bwd, dev, stream, _ptr(dy), _ptr(x), _ptr(mean), _ptr(rstd),
-                 _ptr(weight), _ptr(bias), _ptr(gate), _ptr(dx), _ptr(dw), _ptr(db), _ptr(dz),
+    rc = _launch(lib.gla_group_norm_bwd, dev, stream, _addr(dy), _addr(x), _addr(mean), _addr(rstd),
+                 _addr(weight), _addr(bias), _addr(gate), _addr(dx), _addr(dw), _addr(db), _addr(dz),
                  ctypes.byref(sh), ws, nws)
     _fail(lib, rc, "gla_group_norm_bwd")
     return dx, dw, db, dz

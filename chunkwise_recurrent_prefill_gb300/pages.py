@@ -9,7 +9,7 @@ from __future__ import annotations
 
 import torch
 
-from .gla import _check, _launch, _ptr, load_library
+from .gla import _check, _addr, _launch, load_library
 from .hda import _fail
 
 
@@ -35,7 +35,7 @@ def _ints(t, name, dev, shape=None):
 def _book(table, free, count, P, dev):
     if table.dim() != 2:
         raise ValueError("table must be [R, M]")
-    _ints(table, "table", dev, tuple(table.shape))
+    _ints(table, "table", dev, table.shape)
     _ints(free, "free", dev, (P,))
     _ints(count, "count", dev, (1,))
     return table.shape
@@ -48,7 +48,7 @@ def pages_copy(pool, src, dst, *, stream=None):
     n = src.numel()
     _ints(src, "src", pool.device)
     _ints(dst, "dst", pool.device, (n,))
-    rc = _launch(lib.gla_pages_copy, pool.device, stream, _ptr(pool), P, nb, _ptr(src), _ptr(dst), n)
+    rc = _launch(lib.gla_pages_copy, pool.device, stream, _addr(pool), P, nb, _addr(src), _addr(dst), n)
     _fail(lib, rc, "gla_pages_copy")
 
 
@@ -60,8 +60,8 @@ def pages_fork(pool, table, free, count, parents, children, *, stream=None):
     n = parents.numel()
     _ints(parents, "parents", pool.device)
     _ints(children, "children", pool.device, (n,))
-    rc = _launch(lib.gla_pages_fork, pool.device, stream, _ptr(pool), P, nb, _ptr(table), R, M,
-                 _ptr(free), _ptr(count), _ptr(parents), _ptr(children), n)
+    rc = _launch(lib.gla_pages_fork, pool.device, stream, _addr(pool), P, nb, _addr(table), R, M,
+                 _addr(free), _addr(count), _addr(parents), _addr(children), n)
     _fail(lib, rc, "gla_pages_fork")
 
 
@@ -74,8 +74,8 @@ def pages_free(table, free, count, rows, *, stream=None):
     P = free.numel()
     R, M = _book(table, free, count, P, dev)
     _ints(rows, "rows", dev)
-    rc = _launch(lib.gla_pages_free, dev, stream, P, _ptr(table), R, M, _ptr(free), _ptr(count),
-                 _ptr(rows), rows.numel())
+    rc = _launch(lib.gla_pages_free, dev, stream, P, _addr(table), R, M, _addr(free), _addr(count),
+                 _addr(rows), rows.numel())
     _fail(lib, rc, "gla_pages_free")
 
 
@@ -84,6 +84,6 @@ def pages_compact(pool, table, free, count, *, stream=None):
     lib = load_library()
     P, nb = _pool(pool)
     R, M = _book(table, free, count, P, pool.device)
-    rc = _launch(lib.gla_pages_compact, pool.device, stream, _ptr(pool), P, nb, _ptr(table), R, M,
-                 _ptr(free), _ptr(count))
+    rc = _launch(lib.gla_pages_compact, pool.device, stream, _addr(pool), P, nb, _addr(table), R, M,
+                 _addr(free), _addr(count))
     _fail(lib, rc, "gla_pages_compact")
