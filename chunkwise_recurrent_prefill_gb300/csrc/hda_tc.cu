@@ -23,9 +23,10 @@
 // would leave hT off by 2^-9 of a term, two by 2^-18 (3e-6 of hT, measured, against 3e-7).
 //
 // When there are fewer heads than SMs, each head's chunks are split into segments:
-//   hda_tc_state_kernel : pieces of the segments but the last -> their end state from zero, E
-//   hda_tc_scan_kernel  : S_start(s + 1) = l^tokens(s) S_start(s) + E(s)
-//   hda_tc_out_kernel   : each segment from its start state; the last one gives the final state
+//   hda_tc_state_kernel : pieces of the segments -> their end state from zero, E (of the last
+//                         segment only where the final state is wanted)
+//   hda_tc_scan_kernel  : S_start(s + 1) = l^tokens(s) S_start(s) + E(s), and the final state
+//   hda_tc_out_kernel   : each segment from its start state (unsplit, it gives the final state too)
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -46,6 +47,7 @@ constexpr int kC = 64;              // tokens of a chunk
 constexpr float kLeastF = 0x1p-60f; // least output factor
 constexpr int kMaxSplits = 256;
 constexpr int kMaxPieces = 8;
+constexpr int64_t kL2Keep = 64ll << 20;
 
 // l^n = e^(n g): the product is formed in two parts, so that the result is good to a few 2^-24
 // of itself (the rounding of n g alone would cost 2^-24 |n g|). 1 for n = 0, whatever g is.
@@ -168,10 +170,11 @@ constexpr uint32_t TSLOT = BAR + NBAR * 8;
 constexpr uint32_t ALLOC = TSLOT + 16 + 1024;
 static_assert(ALLOC <= 232448, "output kernel shared memory");
 constexpr uint32_t COL_S = 0;                    // S^T fp32: lane z, column x
-constexpr uint32_t COL_D = 128;                  // a chunk's (diag(u) Z)^T Y, the same way
 constexpr uint32_t COL_P = 256;                  // X Y^T (M = 64 layout)
 constexpr uint32_t COL_O = 320;                  // S^T X^T + Z^T P^T: two of 64 columns
-constexpr uint32_t COL_SB = 448;                 // bf16 snapshot of S^T
+// the state's bf16 snapshots: two of 64 columns; with a returned state (kExact) one, further on,
+// and a chunk's (diag(u) Z)^T Y apart from S
+constexpr uint32_t COL_SB = 128, COL_SB_EXACT = 448, COL_D = 128;
 }  // namespace om
 
 // Barriers. Where a producer may run two phases ahead of a waiter, the phases alternate between
@@ -183,9 +186,10 @@ enum {
 };
 static_assert(FIN < (int)om::NBAR, "output kernel barrier map");
 // Warps: 0 TMA, 1 MMA, 2-5 output, 6-9 state, 10-13 P, 14-17 diag(u) Z. Every role has a loop of its
-// own, since what it does in a chunk is mostly waiting for barriers, TMEM and fences one after
-// another; and the loops are kept short, since five different ones share the instruction cache of
-// each quarter of the SM (28 warps with the state in registers, and unrolled loops, both ran slower).
+// own, since what it does in a chunk is mostly waiting: for barriers, fences, TMEM, and for shared
+// memory, which the tiles' copies and the MMAs keep busy for 60 % of a chunk's time (240 KB of it).
+// The loops are kept short, since different ones share the instruction cache of each quarter of the
+// SM. 14 warps (roles joined), 22 and 28 warps (state and scaling spread out) were slower.
 constexpr int kOutWarps = 18;
 constexpr int kOutThreads = kOutWarps * 32;
 
@@ -204,8 +208,10 @@ __device__ __forceinline__ void tmem_ld32f(uint32_t taddr, float (&out)[32]) {
     }
 }
 
-__global__ void __launch_bounds__(kOutThreads, 1)
-hda_tc_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ TcArgs a) {
+// kExact: the state is returned from here (a sequence that is not split), so its updates take
+// three parts of diag(u) Z, and each chunk's is accumulated by itself.
+template <bool kExact>
+__device__ __forceinline__ void out_segment(const TcMaps &maps, const TcArgs &a) {
     using namespace om;
     extern __shared__ uint8_t smraw[];
     uint8_t *sm = align1024(smraw);
@@ -225,9 +231,8 @@ hda_tc_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ T
     const int cb = seg_bound(seg, a.nchunks, a.splits);
     const int n = seg_bound(seg + 1, a.nchunks, a.splits) - cb;
     const float g = a.decay[h];
-    // the segment that returns the state updates it in three parts, through one buffer
-    const bool exact = m.fin && seg == a.splits - 1;
-    const int nzb = exact ? 1 : 3;      // buffers of diag(u) Z
+    constexpr int nzb = kExact ? 1 : 3;     // buffers of diag(u) Z
+    constexpr uint32_t kColU = kExact ? COL_D : COL_S;
 
     if (threadIdx.x < 128) {
         const int i = threadIdx.x;
@@ -241,7 +246,7 @@ hda_tc_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ T
             mbar_init(&bars[QEMPTY + i], 1);
         }
         for (int i = 0; i < 3; ++i) {
-            mbar_init(&bars[ZDONE + i], exact ? 8 : 4);
+            mbar_init(&bars[ZDONE + i], kExact ? 8 : 4);
             mbar_init(&bars[ZFREE + i], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -281,7 +286,7 @@ hda_tc_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ T
     // 16-byte vectors ct + 128 x of a box: token (ct / 8 + 16 x) % 64. The product keeps the tile's
     // layout, so the swizzle does not matter here.
     auto scale_Z = [&](int c, int ct, int b0, int b1) -> bool {
-        const int s = c % NQ, zb = exact ? 0 : c % 3, zuse = exact ? c : c / 3;
+        const int s = c % NQ, zb = c % nzb, zuse = c / nzb;
         const bool w = wait_bar(&bars[QFULL + s], par(c / NQ)) &&
                        (zuse == 0 || wait_bar(&bars[ZFREE + zb], par(zuse - 1)));
         if (!__all_sync(0xffffffffu, w)) return false;
@@ -293,15 +298,10 @@ hda_tc_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ T
             uint4 v[4];
 #pragma unroll
             for (int x = 0; x < 4; ++x) v[x] = zs[box * 512 + 128 * x];
-            if (exact) {
 #pragma unroll
-                for (int x = 0; x < 4; ++x)
-                    put_scaled<3>(v[x], u[16 * x], zp + box * 512 + 128 * x, zp + 1024 + box * 512 + 128 * x);
-            } else {
-#pragma unroll
-                for (int x = 0; x < 4; ++x)
-                    put_scaled<1>(v[x], u[16 * x], zp + box * 512 + 128 * x, nullptr);
-            }
+            for (int x = 0; x < 4; ++x)
+                put_scaled<kExact ? 3 : 1>(v[x], u[16 * x], zp + box * 512 + 128 * x,
+                                           zp + 1024 + box * 512 + 128 * x);
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -339,7 +339,8 @@ hda_tc_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ T
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
         // Four groups per chunk, in a fixed order that the other roles keep up with:
-        //   U(c)    : D(c - 1) read, diag(u) Z written -> D = (diag(u) Z)^T Y
+        //   U(c)    : S decayed, diag(u) Z written -> S += (diag(u) Z)^T Y
+        //             (kExact: D(c - 1) read -> D = (diag(u) Z)^T Y, which the state warps add)
         //   I(c)    : snapshot of S taken, out(c - 2) read -> O = S^T X^T
         //   P(c + 1): tiles landed, P(c) read -> X Y^T
         //   A(c)    : P tile written -> O += Z^T P^T; the stage has no reader left
@@ -384,15 +385,15 @@ hda_tc_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ T
                 const uint64_t y0 = dYt + so, z0 = dZP + (uint64_t)(zb * (16384 >> 4));
                 // the small parts first: the accumulator drops the bits below its own last one
                 // at every step, so the fewer steps it is large in, the better
-                if (exact) {
+                if (kExact) {
 #pragma unroll
                     for (int kk = 0; kk < 8; ++kk)
-                        mma_ss(tm + COL_D, z0 + (2 - (kk >> 2)) * (16384 >> 4) + (kk & 3) * (2048 >> 4),
+                        mma_ss(tm + kColU, z0 + (2 - (kk >> 2)) * (16384 >> 4) + (kk & 3) * (2048 >> 4),
                                y0 + (kk & 3) * (2048 >> 4), idU, kk > 0);
                 }
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
-                    mma_ss(tm + COL_D, z0 + kk * (2048 >> 4), y0 + kk * (2048 >> 4), idU, exact || kk > 0);
+                    mma_ss(tm + kColU, z0 + kk * (2048 >> 4), y0 + kk * (2048 >> 4), idU, 1);
                 mma_commit(&bars[UDONE]);
                 mma_commit(&bars[ZFREE + zb]);
             }
@@ -407,14 +408,14 @@ hda_tc_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ T
             tc_fence_after();
             if (elect_one()) {
                 const uint64_t x0 = dX + so;
-                const uint32_t sb = tm + COL_SB;
+                const uint32_t sb = tm + (kExact ? COL_SB_EXACT : COL_SB + (c & 1) * 64);
 #pragma unroll
                 for (int x = 0; x < 4; ++x) mma_ts(o, sb + x * 8, x0 + koff(x), idOi, x > 0);
                 if (wide) {
 #pragma unroll
                     for (int x = 4; x < 8; ++x) mma_ts(o, sb + x * 8, x0 + koff(x), idOi, 1);
                 }
-                mma_commit(&bars[SBFREE]);
+                if (kExact) mma_commit(&bars[SBFREE]);
             }
             __syncwarp();
             const int s1 = s + 1 == NQ ? 0 : s + 1;
@@ -557,30 +558,35 @@ hda_tc_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ T
             mask[e] = d >= 0 ? pw[d] * (m.a_in / fmaxf(pw[rev ? kC - 1 - i : i + 1], kLeastF)) : 0.f;
         }
         for (int c = 0; c < n; ++c) {
-            if (exact && !scale_Z(c, (warp - 10) * 32 + lane, 1, Dz / 64)) { ok = false; break; }
+            if (kExact && !scale_Z(c, (warp - 10) * 32 + lane, 1, Dz / 64)) { ok = false; break; }
             if (!__all_sync(0xffffffffu, wait_bar(&bars[PFULL], par(c)))) { ok = false; break; }
             tc_fence_after();
             uint8_t *pt = sm + P + (c & 1) * 8192;
-            uint32_t r0[16], r1[16];
-            tmem_ld16x256b_x4(tmem_addr(tm, j, COL_P), r0);
-            tmem_ld16x256b_x4(tmem_addr(tm, j, COL_P + 32), r1);
-            tmem_wait_ld();
-            reg_fence(r0);
-            reg_fence(r1);
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars[PFREE]);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const uint32_t *r = k < 4 ? r0 + 4 * k : r1 + 4 * (k - 4);
-                float2 f[2];
+            for (int half = 0; half < 2; ++half) {
+                uint32_t r[16];
+                tmem_ld16x256b_x4(tmem_addr(tm, j, COL_P + 32 * half), r);
+                tmem_wait_ld();
+                reg_fence(r);
+                if (half == 1) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars[PFREE]);
+                }
 #pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    f[e] = mul2(make_float2(mask[4 * k + 2 * e], mask[4 * k + 2 * e + 1]),
-                                make_float2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1])));
-                const int col = c0 + 8 * k;
-                *reinterpret_cast<uint32_t *>(pt + sw128_offset(ia, col)) = pack_bf16(f[0].x, f[0].y);
-                *reinterpret_cast<uint32_t *>(pt + sw128_offset(ia + 8, col)) = pack_bf16(f[1].x, f[1].y);
+                for (int k = 0; k < 4; ++k) {
+                    float2 f[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int at = 16 * half + 4 * k + 2 * e;
+                        f[e] = mul2(make_float2(mask[at], mask[at + 1]),
+                                    make_float2(__uint_as_float(r[4 * k + 2 * e]),
+                                                __uint_as_float(r[4 * k + 2 * e + 1])));
+                    }
+                    const int col = c0 + 32 * half + 8 * k;
+                    *reinterpret_cast<uint32_t *>(pt + sw128_offset(ia, col)) = pack_bf16(f[0].x, f[0].y);
+                    *reinterpret_cast<uint32_t *>(pt + sw128_offset(ia + 8, col)) = pack_bf16(f[1].x, f[1].y);
+                }
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -591,13 +597,11 @@ hda_tc_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ T
         // ------------------------------------------------------------ diag(u) Z
         // (in three parts, the second box is the P warps')
         for (int c = 0; ok && c < n; ++c)
-            ok = scale_Z(c, (warp - 14) * 32 + lane, 0, exact ? 1 : Dz / 64);
+            ok = scale_Z(c, (warp - 14) * 32 + lane, 0, kExact ? 1 : Dz / 64);
         __syncwarp();
     } else {
         // ------------------------------------------------------------ state
-        // Lane z, key rows x. Per chunk S <- l^n S + D, rounded to nearest (a sum kept in the
-        // accumulator over many chunks is cut off at every step: 3e-6 of hT at a memory of 1024
-        // tokens), and its bf16 snapshot for X S.
+        // Lane z, key rows x. Per chunk: the bf16 snapshot of S for X S, and S <- l^n S.
         const int z = j * 32 + lane;
         {
             const float *init = nullptr;
@@ -622,73 +626,101 @@ hda_tc_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ T
             }
             tmem_wait_st();
         }
-        // The state before chunk c (after the last one for c = n, which goes to fin).
-        for (int c = 0; c <= n; ++c) {
+        // The state before chunk c (with kExact: after the last one for c = n, which goes to fin).
+        for (int c = 0; c < n + (kExact ? 1 : 0); ++c) {
             const bool last = c == n;
-            if (last && !exact) break;
-            const bool w = c == 0 || wait_bar(&bars[UDONE], par(c - 1));
-            if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
+            // (U(c - 1) was issued after I(c - 2), so that snapshot's buffer is free, too)
+            if (!__all_sync(0xffffffffu, c == 0 || wait_bar(&bars[UDONE], par(c - 1)))) { ok = false; break; }
             tc_fence_after();
-            const float carry = c > 0 ? pw[chunk_tokens(cb + c - 1, a)] : 1.f;
-            const float2 cc = make_float2(carry, carry);
-            float *fp = m.fin + (size_t)bh * Dx * Dz + z;
+            if (!kExact) {
+                const float carry = pw[chunk_tokens(cb + c, a)];
+                const float2 cc = make_float2(carry, carry);
 #pragma unroll 1
-            for (int q = 0; q < Dx; q += 32) {
-                float sv[32];
-                if (c > 0) {
-                    uint32_t d0[16], d1[16], s0[16], s1[16];
-                    tmem_ld16(tmem_addr(tm, j, COL_D + q), d0);
-                    tmem_ld16(tmem_addr(tm, j, COL_D + q + 16), d1);
-                    tmem_ld16(tmem_addr(tm, j, COL_S + q), s0);
-                    tmem_ld16(tmem_addr(tm, j, COL_S + q + 16), s1);
-                    tmem_wait_ld();
-                    reg_fence(d0);
-                    reg_fence(d1);
-                    reg_fence(s0);
-                    reg_fence(s1);
+                for (int q = 0; q < Dx; q += 32) {
+                    float sv[32];
+                    tmem_ld32f(tmem_addr(tm, j, COL_S + q), sv);
+                    uint32_t pk[16], s0[16], s1[16];
+#pragma unroll
+                    for (int x = 0; x < 16; ++x) pk[x] = pack_bf16(sv[2 * x], sv[2 * x + 1]);
+                    tmem_st16(tmem_addr(tm, j, COL_SB + (c & 1) * 64 + q / 2), pk);
 #pragma unroll
                     for (int x = 0; x < 16; x += 2) {
-                        const float2 lo = fma2(make_float2(__uint_as_float(s0[x]), __uint_as_float(s0[x + 1])), cc,
-                                               make_float2(__uint_as_float(d0[x]), __uint_as_float(d0[x + 1])));
-                        const float2 hi = fma2(make_float2(__uint_as_float(s1[x]), __uint_as_float(s1[x + 1])), cc,
-                                               make_float2(__uint_as_float(d1[x]), __uint_as_float(d1[x + 1])));
-                        sv[x] = lo.x;
-                        sv[x + 1] = lo.y;
-                        sv[16 + x] = hi.x;
-                        sv[17 + x] = hi.y;
+                        const float2 lo = mul2(make_float2(sv[x], sv[x + 1]), cc);
+                        const float2 hi = mul2(make_float2(sv[16 + x], sv[17 + x]), cc);
+                        s0[x] = __float_as_uint(lo.x);
+                        s0[x + 1] = __float_as_uint(lo.y);
+                        s1[x] = __float_as_uint(hi.x);
+                        s1[x + 1] = __float_as_uint(hi.y);
                     }
-                    if (!last) {
+                    tmem_st16(tmem_addr(tm, j, COL_S + q), s0);
+                    tmem_st16(tmem_addr(tm, j, COL_S + q + 16), s1);
+                }
+            } else {
+                // S <- l^n S + D, rounded to nearest (a sum kept in the accumulator over many chunks
+                // is cut off at every step: 3e-6 of hT at a memory of 1024 tokens)
+                const float carry = c > 0 ? pw[chunk_tokens(cb + c - 1, a)] : 1.f;
+                const float2 cc = make_float2(carry, carry);
+                float *fp = m.fin + (size_t)bh * Dx * Dz + z;
+#pragma unroll 1
+                for (int q = 0; q < Dx; q += 32) {
+                    uint32_t d0[16], d1[16], s0[16], s1[16];
+                    tmem_ld16(tmem_addr(tm, j, COL_S + q), s0);
+                    tmem_ld16(tmem_addr(tm, j, COL_S + q + 16), s1);
+                    if (c > 0) {
+                        tmem_ld16(tmem_addr(tm, j, COL_D + q), d0);
+                        tmem_ld16(tmem_addr(tm, j, COL_D + q + 16), d1);
+                    }
+                    tmem_wait_ld();
+                    reg_fence(s0);
+                    reg_fence(s1);
+                    if (c > 0) {
+                        reg_fence(d0);
+                        reg_fence(d1);
 #pragma unroll
-                        for (int x = 0; x < 16; ++x) {
-                            s0[x] = __float_as_uint(sv[x]);
-                            s1[x] = __float_as_uint(sv[16 + x]);
+                        for (int x = 0; x < 16; x += 2) {
+                            const float2 lo = fma2(make_float2(__uint_as_float(s0[x]), __uint_as_float(s0[x + 1])), cc,
+                                                   make_float2(__uint_as_float(d0[x]), __uint_as_float(d0[x + 1])));
+                            const float2 hi = fma2(make_float2(__uint_as_float(s1[x]), __uint_as_float(s1[x + 1])), cc,
+                                                   make_float2(__uint_as_float(d1[x]), __uint_as_float(d1[x + 1])));
+                            s0[x] = __float_as_uint(lo.x);
+                            s0[x + 1] = __float_as_uint(lo.y);
+                            s1[x] = __float_as_uint(hi.x);
+                            s1[x + 1] = __float_as_uint(hi.y);
                         }
+                    }
+                    if (last) {
+                        if (z < Dz) {
+#pragma unroll
+                            for (int x = 0; x < 16; ++x) {
+                                fp[(q + x) * Dz] = __uint_as_float(s0[x]);
+                                fp[(q + 16 + x) * Dz] = __uint_as_float(s1[x]);
+                            }
+                        }
+                        continue;
+                    }
+                    if (c > 0) {
                         tmem_st16(tmem_addr(tm, j, COL_S + q), s0);
                         tmem_st16(tmem_addr(tm, j, COL_S + q + 16), s1);
-                    }
-                } else {
-                    tmem_ld32f(tmem_addr(tm, j, COL_S + q), sv);
-                }
-                if (!last) {
-                    // the snapshot was last read by I(c - 1)
-                    if (q == 0 && c > 0) {
-                        if (!__all_sync(0xffffffffu, wait_bar(&bars[SBFREE], par(c - 1)))) ok = false;
-                        tc_fence_after();
+                        // the snapshot was last read by I(c - 1)
+                        if (q == 0) {
+                            if (!__all_sync(0xffffffffu, wait_bar(&bars[SBFREE], par(c - 1)))) ok = false;
+                            tc_fence_after();
+                        }
                     }
                     uint32_t pk[16];
 #pragma unroll
-                    for (int x = 0; x < 16; ++x) pk[x] = pack_bf16(sv[2 * x], sv[2 * x + 1]);
-                    tmem_st16(tmem_addr(tm, j, COL_SB + q / 2), pk);
-                } else if (z < Dz) {
-#pragma unroll
-                    for (int x = 0; x < 32; ++x) fp[(q + x) * Dz] = sv[x];
+                    for (int x = 0; x < 8; ++x) {
+                        pk[x] = pack_bf16(__uint_as_float(s0[2 * x]), __uint_as_float(s0[2 * x + 1]));
+                        pk[8 + x] = pack_bf16(__uint_as_float(s1[2 * x]), __uint_as_float(s1[2 * x + 1]));
+                    }
+                    tmem_st16(tmem_addr(tm, j, COL_SB_EXACT + q / 2), pk);
                 }
+                if (!ok || last) break;
             }
-            if (!ok) break;
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0 && !last) mbar_arrive(&bars[SREADY]);
+            if (lane == 0) mbar_arrive(&bars[SREADY]);
         }
         __syncwarp();
     }
@@ -700,6 +732,14 @@ hda_tc_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ T
         tc_fence_after();
         tmem_dealloc(tm, 512);
     }
+}
+
+// CTA = one segment of one head and map (the maps of one segment are neighbours: they read the
+// same tiles).
+__global__ void __launch_bounds__(kOutThreads, 1)
+hda_tc_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ TcArgs a) {
+    if (a.splits == 1 && a.lin[blockIdx.x % a.n].fin) out_segment<true>(maps, a);
+    else out_segment<false>(maps, a);
 }
 
 // ======================================================================= state kernel
@@ -720,9 +760,10 @@ static_assert(ALLOC <= 232448, "state kernel shared memory");
 constexpr int kStateThreads = 576;
 
 struct StateProblem {
-    float *E;               // [BH][(splits - 1) pieces][Dx][Dz]
+    float *E;               // [BH][segs pieces][Dx][Dz]
     float *start;           // [BH][splits - 1][Dx][Dz]
     int li;                 // the map whose y and z it reads
+    int segs;               // splits - 1, or splits where the final state is wanted
 };
 struct StateArgs {
     StateProblem s[2];
@@ -740,9 +781,8 @@ __device__ __forceinline__ void piece_range(const TcArgs &a, int seg, int sub, i
 }
 
 template <int kParts>
-__global__ void __launch_bounds__(kStateThreads, 1)
-hda_tc_state_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ TcArgs a,
-                    const __grid_constant__ StateArgs sa) {
+__device__ __forceinline__ void state_piece(const TcMaps &maps, const TcArgs &a, const StateArgs &sa,
+                                            const StateProblem &sp, int bh, int pi) {
     using namespace st;
     constexpr int NS = kParts == 1 ? 6 : 4;
     static_assert(NS % 2 == 0 && (kParts == 1 || kParts == 3), "stages of the state kernel");
@@ -759,16 +799,13 @@ hda_tc_state_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__
     float *pw = reinterpret_cast<float *>(sm + PW);
     pdl_launch_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int npc = (a.splits - 1) * sa.pieces;
-    const int si = blockIdx.x % sa.n, pi = (blockIdx.x / sa.n) % npc, bh = blockIdx.x / sa.n / npc;
-    const StateProblem &sp = sa.s[si];
+    const int npc = sp.segs * sa.pieces;
     const TcLin &m = a.lin[sp.li];
     const int b = bh / a.H, h = bh % a.H, rev = m.rev, Dx = m.Dx, Dz = m.Dz;
     int cb, ce;
     piece_range(a, pi / sa.pieces, pi % sa.pieces, sa.pieces, cb, ce);
     const int n = ce - cb;
     // the chunks run last to first: what is read last is what the out kernel reads first
-    // (never the last chunk of the walk: all are full)
     auto start = [&](int c) { return chunk_start(ce - 1 - c, a, rev); };
     const float g = a.decay[h];
     if (threadIdx.x <= kC) pw[threadIdx.x] = decay_pow(g, (float)threadIdx.x);
@@ -853,11 +890,13 @@ hda_tc_state_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__
         const int ct = ((warp - 2) & 3) * 32 + lane;    // 16-byte vectors ct + 128 x: tokens row + 16 x
         for (int c = (warp - 2) >> 2; c < n; c += 2) {
             const int s = c % NS;
-            // c chunks of 64 tokens follow this one in the piece
-            const float after = m.a_in * decay_pow(g, (float)(kC * c));
+            // tokens that follow this chunk in the piece
+            const int p = ce - 1 - c, nt = chunk_tokens(p, a);
+            const int rest_tokens = min((int)a.T, ce * kC) - p * kC - nt;
+            const float after = m.a_in * decay_pow(g, (float)rest_tokens);
             float u[4];
 #pragma unroll
-            for (int x = 0; x < 4; ++x) u[x] = after * state_factor(pw, (ct >> 3) + 16 * x, kC, rev);
+            for (int x = 0; x < 4; ++x) u[x] = after * state_factor(pw, (ct >> 3) + 16 * x, nt, rev);
             const bool w = wait_bar(&bars[SFULL + s], par(c / NS)) &&
                            (kParts == 1 || c < 2 || wait_bar(&bars[SZFREE + (c & 1)], par((c >> 1) - 1)));
             if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
@@ -917,8 +956,20 @@ hda_tc_state_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__
     }
 }
 
+// CTA = one piece of one problem and head.
+__global__ void __launch_bounds__(kStateThreads, 1)
+hda_tc_state_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ TcArgs a,
+                    const __grid_constant__ StateArgs sa) {
+    const int n0 = sa.s[0].segs * sa.pieces, all = n0 + (sa.n > 1 ? sa.s[1].segs * sa.pieces : 0);
+    const int bh = blockIdx.x / all, i = blockIdx.x % all;
+    const StateProblem &sp = sa.s[i < n0 ? 0 : 1];
+    const int pi = i < n0 ? i : i - n0;
+    if (sp.segs == a.splits) state_piece<3>(maps, a, sa, sp, bh, pi);
+    else state_piece<1>(maps, a, sa, sp, bh, pi);
+}
+
 // ======================================================================= scan kernel
-// Start states of segments 1 .. splits - 1. A thread carries kScanPer elements of one head; the
+// Start states of segments 1 .. splits - 1, and the final state. A thread carries kScanPer elements of one head; the
 // loads of a batch of pieces are issued together, so the chain costs one round trip per batch.
 constexpr int kScanThreads = 256, kScanPer = 4, kScanBatch = 4;
 
@@ -932,7 +983,7 @@ hda_tc_scan_kernel(const __grid_constant__ TcArgs a, const __grid_constant__ Sta
     if (e0 >= dd) return;       // (dd is a multiple of a block's elements)
     const size_t bh = blockIdx.x;
     const float g = a.decay[bh % a.H];
-    const int nseg = a.splits - 1, npc = nseg * sa.pieces;
+    const int nseg = a.splits - 1, npc = sp.segs * sa.pieces;
     float s[kScanPer];
 #pragma unroll
     for (int i = 0; i < kScanPer; ++i) {
@@ -955,12 +1006,15 @@ hda_tc_scan_kernel(const __grid_constant__ TcArgs a, const __grid_constant__ Sta
             const int r = r0 + j;
             int cb, ce;
             piece_range(a, r / sa.pieces, r % sa.pieces, sa.pieces, cb, ce);
-            const float f = decay_pow(g, (float)(ce - cb) * kC);   // (all chunks are full)
+            const float f = decay_pow(g, (float)(min((int)a.T, ce * kC) - cb * kC));
             const bool end = (r + 1) % sa.pieces == 0;
+            const int seg = r / sa.pieces;
 #pragma unroll
             for (int i = 0; i < kScanPer; ++i) {
                 s[i] = fmaf(f, s[i], ev[j][i]);
-                if (end) ob[(size_t)((r + 1) / sa.pieces - 1) * dd + i * kScanThreads] = s[i];
+                if (!end) continue;
+                if (seg < nseg) ob[(size_t)seg * dd + i * kScanThreads] = s[i];
+                else m.fin[bh * dd + e0 + i * kScanThreads] = s[i];
             }
         }
     }
@@ -981,10 +1035,9 @@ cudaError_t set_attrs() {
     e = cudaFuncSetAttribute((const void *)hda_tc_out_kernel,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, om::ALLOC);
     if (e != cudaSuccess) return e;
-    for (const void *k : {(const void *)hda_tc_state_kernel<1>, (const void *)hda_tc_state_kernel<3>}) {
-        e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, st::ALLOC);
-        if (e != cudaSuccess) return e;
-    }
+    e = cudaFuncSetAttribute((const void *)hda_tc_state_kernel,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, st::ALLOC);
+    if (e != cudaSuccess) return e;
     g_attr_done[dev] = true;
     return cudaSuccess;
 }
@@ -1045,10 +1098,11 @@ int clamp_splits(const HdaProblem &p, int splits, int sms) {
     const int64_t nchunks = (p.T + kC - 1) / kC;
     return (int)std::max<int64_t>(1, std::min<int64_t>({(int64_t)splits, nchunks, kMaxSplits}));
 }
-int state_pieces(const HdaProblem &p, int splits, int sms) {
+// `segs`: segments of all problems together.
+int state_pieces(const HdaProblem &p, int splits, int segs, int sms) {
     if (splits <= 1) return 1;
     const int64_t nchunks = (p.T + kC - 1) / kC;
-    int64_t k = sms / (p.B * p.H * state_problems(p) * (splits - 1));
+    int64_t k = sms / (p.B * p.H * segs);
     k = std::min<int64_t>(k, nchunks / (4 * (int64_t)splits));
     return (int)std::max<int64_t>(1, std::min<int64_t>(k, kMaxPieces));
 }
@@ -1072,8 +1126,11 @@ bool hda_tc_supported(const HdaProblem &p) {
 size_t hda_tc_workspace_bytes(const HdaProblem &p, int splits, int num_sms) {
     const int s = clamp_splits(p, splits, num_sms);
     if (s <= 1) return 0;
-    const size_t per = (size_t)(p.B * p.H) * (s - 1) * p.lin[0].Dx * p.lin[0].Dz * sizeof(float);
-    return state_problems(p) * per * (1 + state_pieces(p, s, num_sms));
+    // E of every piece (one segment more where the final state is wanted: room for it always, since
+    // the size must not depend on it) and the start states
+    const size_t per = (size_t)(p.B * p.H) * p.lin[0].Dx * p.lin[0].Dz * sizeof(float);
+    const int pieces = state_pieces(p, s, state_problems(p) * (s - 1), num_sms);
+    return state_problems(p) * per * ((size_t)s * pieces + (s - 1));
 }
 
 cudaError_t launch_hda_tc(const HdaProblem &p, int splits, int num_sms, void *ws,
@@ -1081,7 +1138,9 @@ cudaError_t launch_hda_tc(const HdaProblem &p, int splits, int num_sms, void *ws
     cudaError_t e = set_attrs();
     if (e != cudaSuccess) return e;
     const int s = clamp_splits(p, splits, num_sms), ns = state_problems(p);
-    const int pieces = state_pieces(p, s, num_sms);
+    int segs = 0;
+    for (int i = 0; i < ns; ++i) segs += p.lin[2 * i].fin ? s : s - 1;
+    const int pieces = state_pieces(p, s, segs, num_sms);
     const int64_t bh = p.B * p.H;
     TcMaps maps{};
     TcArgs a{};
@@ -1107,25 +1166,29 @@ cudaError_t launch_hda_tc(const HdaProblem &p, int splits, int num_sms, void *ws
     pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     pdl[0].val.programmaticStreamSerializationAllowed = 1;
     if (s > 1) {
-        const size_t per = (size_t)bh * (s - 1) * p.lin[0].Dx * p.lin[0].Dz;
+        const size_t per = (size_t)bh * p.lin[0].Dx * p.lin[0].Dz;
         StateArgs sa{};
         sa.n = ns;
         sa.pieces = pieces;
-        sa.retain = 0;
         float *w = static_cast<float *>(ws);
+        const int64_t all = (int64_t)segs * pieces;
         for (int i = 0; i < ns; ++i) {
-            sa.s[i].li = 2 * i;
-            sa.s[i].E = w;
-            sa.s[i].start = w + per * pieces;
-            w += per * (pieces + 1);
-            a.lin[2 * i].start = sa.s[i].start;
+            StateProblem &sp = sa.s[i];
+            sp.li = 2 * i;
+            sp.segs = p.lin[2 * i].fin ? s : s - 1;
+            sp.E = w;
+            sp.start = w + per * s * pieces;
+            w += per * (s * pieces + s - 1);
+            a.lin[2 * i].start = sp.start;
         }
         if (p.n == 3) {
             a.lin[1].start = a.lin[2].start;
             a.lin[1].start_t = 1;
         }
-        const auto kernel = p.lin[p.n - 1].fin ? hda_tc_state_kernel<3> : hda_tc_state_kernel<1>;
-        kernel<<<(unsigned)(bh * (s - 1) * pieces * ns), kStateThreads, st::ALLOC, stream>>>(maps, a, sa);
+        // keep about kL2Keep bytes of what the state pass reads last for the out kernel
+        sa.retain = (int)std::min<int64_t>((a.nchunks / s + pieces - 1) / pieces,
+                                           kL2Keep / (bh * all * (p.lin[0].Dx + p.lin[0].Dz) * kC * 2));
+        hda_tc_state_kernel<<<(unsigned)(bh * all), kStateThreads, st::ALLOC, stream>>>(maps, a, sa);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
         // the scan and the output may be scheduled while their predecessor still runs, and wait
         // for it before they read what it wrote
