@@ -165,7 +165,7 @@ constexpr uint32_t FA = PW + 320;                // [64] f32 output factors a_ou
 constexpr uint32_t FU = FA + 256;                // [64] f32 state factors a_in u_j of a full chunk
 constexpr uint32_t FUL = FU + 256;               // the same of the last chunk of the walk
 constexpr uint32_t BAR = FUL + 256;
-constexpr uint32_t NBAR = 26;
+constexpr uint32_t NBAR = 28;
 constexpr uint32_t TSLOT = BAR + NBAR * 8;
 constexpr uint32_t ALLOC = TSLOT + 16 + 1024;
 static_assert(ALLOC <= 232448, "output kernel shared memory");
@@ -182,15 +182,15 @@ constexpr uint32_t COL_SB = 128, COL_SB_EXACT = 448, COL_D = 128;
 // waiter's own arrival.
 enum {
     QFULL = 0, QEMPTY = 3, ZDONE = 6, ZFREE = 9, PBF = 12, OFULL = 14, OFREE = 16, PFULL = 18,
-    PFREE = 19, SREADY = 20, SBFREE = 21, UDONE = 22, FIN = 23,
+    PFREE = 19, SREADY = 20, SBFREE = 21, UDONE = 22, IDONE = 23, FIN = 25,
 };
 static_assert(FIN < (int)om::NBAR, "output kernel barrier map");
-// Warps: 0 TMA, 1 MMA, 2-5 output, 6-9 state, 10-13 P, 14-17 diag(u) Z. Every role has a loop of its
+// Warps: 0 TMA, 1 and 19 MMA, 2-5 output, 6-9 state, 10-13 P, 14-17 diag(u) Z (18: none). Every role has a loop of its
 // own, since what it does in a chunk is mostly waiting: for barriers, fences, TMEM, and for shared
 // memory, which the tiles' copies and the MMAs keep busy for 60 % of a chunk's time (240 KB of it).
 // The loops are kept short, since different ones share the instruction cache of each quarter of the
 // SM. 14 warps (roles joined), 22 and 28 warps (state and scaling spread out) were slower.
-constexpr int kOutWarps = 18;
+constexpr int kOutWarps = 20;
 constexpr int kOutThreads = kOutWarps * 32;
 
 // 32 lanes x 32 columns of fp32 accumulators -> 32 floats.
@@ -243,7 +243,7 @@ __device__ __forceinline__ void out_segment(const TcMaps &maps, const TcArgs &a)
     if (threadIdx.x == 0) {
         for (int i = 0; i < NQ; ++i) {
             mbar_init(&bars[QFULL + i], 1);
-            mbar_init(&bars[QEMPTY + i], 1);
+            mbar_init(&bars[QEMPTY + i], 2);
         }
         for (int i = 0; i < 3; ++i) {
             mbar_init(&bars[ZDONE + i], kExact ? 8 : 4);
@@ -253,13 +253,14 @@ __device__ __forceinline__ void out_segment(const TcMaps &maps, const TcArgs &a)
             mbar_init(&bars[PBF + i], 4);
             mbar_init(&bars[OFULL + i], 1);
             mbar_init(&bars[OFREE + i], 4);
+            mbar_init(&bars[IDONE + i], 1);
         }
         mbar_init(&bars[PFULL], 1);
         mbar_init(&bars[PFREE], 4);
         mbar_init(&bars[SREADY], 4);
         mbar_init(&bars[SBFREE], 1);
         mbar_init(&bars[UDONE], 1);
-        mbar_init(&bars[FIN], 1);
+        mbar_init(&bars[FIN], 2);
         fence_mbar_init();
     }
     if (warp == 0 && lane == 0) {
@@ -336,108 +337,113 @@ __device__ __forceinline__ void out_segment(const TcMaps &maps, const TcArgs &a)
             }
         }
         __syncwarp();
-    } else if (warp == 1) {
-        // ------------------------------------------------------------ MMA issuer
-        // Four groups per chunk, in a fixed order that the other roles keep up with:
-        //   U(c)    : S decayed, diag(u) Z written -> S += (diag(u) Z)^T Y
-        //             (kExact: D(c - 1) read -> D = (diag(u) Z)^T Y, which the state warps add)
-        //   I(c)    : snapshot of S taken, out(c - 2) read -> O = S^T X^T
-        //   P(c + 1): tiles landed, P(c) read -> X Y^T
-        //   A(c)    : P tile written -> O += Z^T P^T; the stage has no reader left
-        // The warp waits converged, then one elected lane issues. Issuing is what this warp's
-        // time goes to, so the operand descriptors are made once: a tile further on is an
-        // addition to the address field (in 16-byte units; the field does not overflow).
-        const uint32_t idP = idesc_bf16(64, 64, 0, 0);
-        const uint32_t idU = idesc_bf16(128, Dx, 1, 1);
-        const uint32_t idOa = idesc_bf16(128, 64, 1, 0);
-        const uint32_t idOi = idesc_bf16(128, 64, 0, 0);
+    } else if (warp == 1 || warp == 19) {
+        // ------------------------------------------------------------ MMA issuers
+        // Two warps, each with two groups per chunk in a fixed order that the other roles keep up
+        // with (one warp that issued all four spent 2600 cycles a chunk on it, 1000 of them on
+        // waits and commits one after another):
+        //   1 : U(c)     S decayed, diag(u) Z written -> S += (diag(u) Z)^T Y
+        //                (kExact: D(c - 1) read -> D = (diag(u) Z)^T Y, which the state warps add)
+        //       I(c)     snapshot of S taken, out(c - 2) read -> O = S^T X^T
+        //   19: P(c + 1) tiles landed, P(c) read -> X Y^T
+        //       A(c)     I(c) complete, P tile written -> O += Z^T P^T
+        // A stage is free once both have committed their last reads of it. A warp waits converged,
+        // then one elected lane issues. The operand descriptors are made once: a tile further on
+        // is an addition to the address field (in 16-byte units; the field does not overflow).
         const uint32_t s0 = smem_u32(sm);
         const uint64_t dX = smem_desc(s0 + X, 16, 1024), dY = smem_desc(s0 + Y, 16, 1024);
-        const uint64_t dYt = smem_desc(s0 + Y, 8192, 1024), dZt = smem_desc(s0 + Z, 8192, 1024);
-        const uint64_t dZP = smem_desc(s0 + ZP, 8192, 1024), dP = smem_desc(s0 + P, 16, 1024);
         // K-major operands: 16 columns of a 64-column box are 32 bytes, the boxes 8 KB apart
         auto koff = [](int x) { return (uint64_t)((x >> 2) * (8192 >> 4) + (x & 3) * (32 >> 4)); };
         const bool wide = Dx > 64;
-        auto issue_P = [&](int s) {
-            const uint64_t x0 = dX + (uint64_t)(s * (STAGE >> 4)), y0 = dY + (uint64_t)(s * (STAGE >> 4));
-#pragma unroll
-            for (int x = 0; x < 4; ++x) mma_ss(tm + COL_P, x0 + koff(x), y0 + koff(x), idP, x > 0);
-            if (wide) {
-#pragma unroll
-                for (int x = 4; x < 8; ++x) mma_ss(tm + COL_P, x0 + koff(x), y0 + koff(x), idP, 1);
-            }
-            mma_commit(&bars[PFULL]);
-        };
-        bool w = wait_bar(&bars[QFULL], 0);
-        ok = __all_sync(0xffffffffu, w);
-        if (ok) {
-            tc_fence_after();
-            if (elect_one()) issue_P(0);
-            __syncwarp();
-        }
-        int zb = 0, zuse = 0;       // buffer of diag(u) Z of chunk c, and how often it was used before
-        for (int c = 0, s = 0; ok && c < n; ++c) {
-            const uint64_t so = (uint64_t)(s * (STAGE >> 4));
-            w = wait_bar(&bars[SREADY], par(c)) && wait_bar(&bars[ZDONE + zb], par(zuse));
-            if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
-            tc_fence_after();
-            if (elect_one()) {
-                const uint64_t y0 = dYt + so, z0 = dZP + (uint64_t)(zb * (16384 >> 4));
-                // the small parts first: the accumulator drops the bits below its own last one
-                // at every step, so the fewer steps it is large in, the better
-                if (kExact) {
-#pragma unroll
-                    for (int kk = 0; kk < 8; ++kk)
-                        mma_ss(tm + kColU, z0 + (2 - (kk >> 2)) * (16384 >> 4) + (kk & 3) * (2048 >> 4),
-                               y0 + (kk & 3) * (2048 >> 4), idU, kk > 0);
-                }
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                    mma_ss(tm + kColU, z0 + kk * (2048 >> 4), y0 + kk * (2048 >> 4), idU, 1);
-                mma_commit(&bars[UDONE]);
-                mma_commit(&bars[ZFREE + zb]);
-            }
-            __syncwarp();
-            if (++zb == nzb) {
-                zb = 0;
-                ++zuse;
-            }
-            const uint32_t o = tm + COL_O + (c & 1) * 64;
-            w = c < 2 || wait_bar(&bars[OFREE + (c & 1)], par((c >> 1) - 1));
-            if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
-            tc_fence_after();
-            if (elect_one()) {
-                const uint64_t x0 = dX + so;
-                const uint32_t sb = tm + (kExact ? COL_SB_EXACT : COL_SB + (c & 1) * 64);
-#pragma unroll
-                for (int x = 0; x < 4; ++x) mma_ts(o, sb + x * 8, x0 + koff(x), idOi, x > 0);
-                if (wide) {
-#pragma unroll
-                    for (int x = 4; x < 8; ++x) mma_ts(o, sb + x * 8, x0 + koff(x), idOi, 1);
-                }
-                if (kExact) mma_commit(&bars[SBFREE]);
-            }
-            __syncwarp();
-            const int s1 = s + 1 == NQ ? 0 : s + 1;
-            if (c + 1 < n) {
-                w = wait_bar(&bars[QFULL + s1], par((c + 1) / NQ)) && wait_bar(&bars[PFREE], par(c));
+        bool w;
+        if (warp == 1) {
+            const uint32_t idU = idesc_bf16(128, Dx, 1, 1), idOi = idesc_bf16(128, 64, 0, 0);
+            const uint64_t dYt = smem_desc(s0 + Y, 8192, 1024), dZP = smem_desc(s0 + ZP, 8192, 1024);
+            int zb = 0, zuse = 0;   // buffer of diag(u) Z of chunk c, and how often it was used before
+            for (int c = 0, s = 0; c < n; ++c) {
+                const uint64_t so = (uint64_t)(s * (STAGE >> 4));
+                w = wait_bar(&bars[SREADY], par(c)) && wait_bar(&bars[ZDONE + zb], par(zuse));
                 if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
                 tc_fence_after();
-                if (elect_one()) issue_P(s1);
-                __syncwarp();
-            }
-            if (!__all_sync(0xffffffffu, wait_bar(&bars[PBF + (c & 1)], par(c >> 1)))) { ok = false; break; }
-            tc_fence_after();
-            if (elect_one()) {
-                const uint64_t z0 = dZt + so, p0 = dP + (uint64_t)((c & 1) * (8192 >> 4));
+                if (elect_one()) {
+                    const uint64_t y0 = dYt + so, z0 = dZP + (uint64_t)(zb * (16384 >> 4));
+                    // the small parts first: the accumulator drops the bits below its own last one
+                    // at every step, so the fewer steps it is large in, the better
+                    if (kExact) {
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                    mma_ss(o, z0 + kk * (2048 >> 4), p0 + kk * (32 >> 4), idOa, 1);
-                mma_commit(&bars[OFULL + (c & 1)]);
-                mma_commit(&bars[QEMPTY + s]);
+                        for (int kk = 0; kk < 8; ++kk)
+                            mma_ss(tm + kColU, z0 + (2 - (kk >> 2)) * (16384 >> 4) + (kk & 3) * (2048 >> 4),
+                                   y0 + (kk & 3) * (2048 >> 4), idU, kk > 0);
+                    }
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        mma_ss(tm + kColU, z0 + kk * (2048 >> 4), y0 + kk * (2048 >> 4), idU, 1);
+                    mma_commit(&bars[UDONE]);
+                    mma_commit(&bars[ZFREE + zb]);
+                }
+                __syncwarp();
+                if (++zb == nzb) {
+                    zb = 0;
+                    ++zuse;
+                }
+                w = c < 2 || wait_bar(&bars[OFREE + (c & 1)], par((c >> 1) - 1));
+                if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
+                tc_fence_after();
+                if (elect_one()) {
+                    const uint64_t x0 = dX + so;
+                    const uint32_t sb = tm + (kExact ? COL_SB_EXACT : COL_SB + (c & 1) * 64);
+                    const uint32_t o = tm + COL_O + (c & 1) * 64;
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) mma_ts(o, sb + x * 8, x0 + koff(x), idOi, x > 0);
+                    if (wide) {
+#pragma unroll
+                        for (int x = 4; x < 8; ++x) mma_ts(o, sb + x * 8, x0 + koff(x), idOi, 1);
+                    }
+                    if (kExact) mma_commit(&bars[SBFREE]);
+                    mma_commit(&bars[IDONE + (c & 1)]);
+                    mma_commit(&bars[QEMPTY + s]);
+                }
+                __syncwarp();
+                s = s + 1 == NQ ? 0 : s + 1;
             }
-            __syncwarp();
-            s = s1;
+        } else {
+            const uint32_t idP = idesc_bf16(64, 64, 0, 0), idOa = idesc_bf16(128, 64, 1, 0);
+            const uint64_t dZt = smem_desc(s0 + Z, 8192, 1024), dP = smem_desc(s0 + P, 16, 1024);
+            for (int c = -1, s = 0; c < n; ++c) {       // s: the stage of chunk c (0 for c = -1)
+                const int s1 = c < 0 ? 0 : s + 1 == NQ ? 0 : s + 1;
+                if (c + 1 < n) {
+                    w = wait_bar(&bars[QFULL + s1], par((c + 1) / NQ)) && (c < 0 || wait_bar(&bars[PFREE], par(c)));
+                    if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
+                    tc_fence_after();
+                    if (elect_one()) {
+                        const uint64_t x0 = dX + (uint64_t)(s1 * (STAGE >> 4)), y0 = dY + (uint64_t)(s1 * (STAGE >> 4));
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) mma_ss(tm + COL_P, x0 + koff(x), y0 + koff(x), idP, x > 0);
+                        if (wide) {
+#pragma unroll
+                            for (int x = 4; x < 8; ++x) mma_ss(tm + COL_P, x0 + koff(x), y0 + koff(x), idP, 1);
+                        }
+                        mma_commit(&bars[PFULL]);
+                    }
+                    __syncwarp();
+                }
+                if (c >= 0) {
+                    w = wait_bar(&bars[PBF + (c & 1)], par(c >> 1)) && wait_bar(&bars[IDONE + (c & 1)], par(c >> 1));
+                    if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
+                    tc_fence_after();
+                    if (elect_one()) {
+                        const uint64_t z0 = dZt + (uint64_t)(s * (STAGE >> 4)), p0 = dP + (uint64_t)((c & 1) * (8192 >> 4));
+                        const uint32_t o = tm + COL_O + (c & 1) * 64;
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            mma_ss(o, z0 + kk * (2048 >> 4), p0 + kk * (32 >> 4), idOa, 1);
+                        mma_commit(&bars[OFULL + (c & 1)]);
+                        mma_commit(&bars[QEMPTY + s]);
+                    }
+                    __syncwarp();
+                }
+                s = s1;
+            }
         }
         // all issued MMAs complete before the CTA gives up its TMEM
         if (elect_one()) mma_commit(&bars[FIN]);
@@ -593,13 +599,13 @@ __device__ __forceinline__ void out_segment(const TcMaps &maps, const TcArgs &a)
             if (lane == 0) mbar_arrive(&bars[PBF + (c & 1)]);
         }
         __syncwarp();
-    } else if (warp >= 14) {
+    } else if (warp >= 14 && warp < 18) {
         // ------------------------------------------------------------ diag(u) Z
         // (in three parts, the second box is the P warps')
         for (int c = 0; ok && c < n; ++c)
             ok = scale_Z(c, (warp - 14) * 32 + lane, 0, kExact ? 1 : Dz / 64);
         __syncwarp();
-    } else {
+    } else if (warp < 10) {
         // ------------------------------------------------------------ state
         // Lane z, key rows x. Per chunk: the bf16 snapshot of S for X S, and S <- l^n S.
         const int z = j * 32 + lane;
@@ -617,12 +623,13 @@ __device__ __forceinline__ void out_segment(const TcMaps &maps, const TcArgs &a)
             }
             const int sx = tr ? 1 : Dz, sz = tr ? Dx : 1;   // strides of the state as stored
 #pragma unroll 1
-            for (int x0 = 0; x0 < Dx; x0 += 16) {
-                uint32_t r[16];
+            for (int x0 = 0; x0 < Dx; x0 += 64) {       // 64 loads on their way at a time
+                uint32_t r[4][16];
 #pragma unroll
-                for (int x = 0; x < 16; ++x)
-                    r[x] = init && z < Dz ? __float_as_uint(init[(x0 + x) * sx + z * sz]) : 0u;
-                tmem_st16(tmem_addr(tm, j, COL_S + x0), r);
+                for (int x = 0; x < 64; ++x)
+                    r[x >> 4][x & 15] = init && z < Dz ? __float_as_uint(init[(x0 + x) * sx + z * sz]) : 0u;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) tmem_st16(tmem_addr(tm, j, COL_S + x0 + 16 * q), r[q]);
             }
             tmem_wait_st();
         }
