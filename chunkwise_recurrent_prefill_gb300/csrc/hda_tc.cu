@@ -78,6 +78,7 @@ struct TcArgs {
     const float *decay;
     int64_t T;
     int n, H, nchunks, splits;
+    int seg_len, seg_more;  // chunks of a segment; the first seg_more have one more
     int hint;               // L2: what the out kernel reads is not read again
     unsigned *err;
 };
@@ -87,9 +88,9 @@ struct TcMaps {
     CUtensorMap o[3];               // stores: boxes of 32 columns (make_out_map)
 };
 
-// Chunks of segment `seg`, in the order of the walk.
-__host__ __device__ __forceinline__ int seg_bound(int seg, int nchunks, int splits) {
-    return (int)((int64_t)seg * nchunks / splits);
+// First chunk of segment `seg`, in the order of the walk.
+__device__ __forceinline__ int seg_bound(int seg, const TcArgs &a) {
+    return seg * a.seg_len + min(seg, a.seg_more);
 }
 
 // Chunk p of the walk: its first token and how many it has. A reversed walk counts its chunks from
@@ -113,13 +114,20 @@ __device__ __forceinline__ uint8_t *align1024(uint8_t *p) {
 }
 __device__ __forceinline__ uint32_t par(int use) { return (uint32_t)use & 1u; }
 
-// mbar_wait (bounded) that does not look at the clock until it has tried for a while: reading the
-// global timer at every wait that does not succeed at once cost the roles here hundreds of cycles.
+// Bounded wait (false after kWaitLimitNs). One short loop that looks at the clock every 256th try:
+// it is inlined at forty places, and with mbar_wait's two loops and timer the output kernel had 150 KB
+// of code, more than an SM's instruction cache; reading the timer at every wait that does not
+// succeed at once cost the roles hundreds of cycles, too.
 __device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity) {
+    uint64_t t0 = 0;
 #pragma unroll 1
-    for (int i = 0; i < 128; ++i)
-        if (mbar_try_wait(bar, parity)) return true;
-    return mbar_wait(bar, parity);
+    for (uint32_t i = 1; !mbar_try_wait(bar, parity); ++i) {
+        if ((i & 255u) != 0) continue;
+        const uint64_t t = global_ns();
+        if (t0 == 0) t0 = t;
+        else if (t - t0 > kWaitLimitNs) return false;
+    }
+    return true;
 }
 
 // The tile [64 tokens][D] of one head: one or two 128B-swizzled boxes of 64 columns, 8 KB each.
@@ -228,8 +236,8 @@ __device__ __forceinline__ void out_segment(const TcMaps &maps, const TcArgs &a)
     const int b = bh / a.H, h = bh % a.H;
     const TcLin &m = a.lin[li];
     const int rev = m.rev, Dx = m.Dx, Dz = m.Dz;
-    const int cb = seg_bound(seg, a.nchunks, a.splits);
-    const int n = seg_bound(seg + 1, a.nchunks, a.splits) - cb;
+    const int cb = seg_bound(seg, a);
+    const int n = seg_bound(seg + 1, a) - cb;
     const float g = a.decay[h];
     constexpr int nzb = kExact ? 1 : 3;     // buffers of diag(u) Z
     constexpr uint32_t kColU = kExact ? COL_D : COL_S;
@@ -556,12 +564,14 @@ __device__ __forceinline__ void out_segment(const TcMaps &maps, const TcArgs &a)
         // and ia + 8 of a thread, column pairs 8 k + 2 (lane % 4). The factors are the same in every
         // chunk and stay in registers.
         const int ia = 16 * j + (lane >> 2), c0 = 2 * (lane & 3);
-        float mask[32];
+        float mask[32], rf[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+            rf[e] = m.a_in / fmaxf(pw[rev ? kC - 1 - ia - 8 * e : ia + 8 * e + 1], kLeastF);
 #pragma unroll
         for (int e = 0; e < 32; ++e) {
             const int i = ia + (e & 2 ? 8 : 0), col = 8 * (e >> 2) + c0 + (e & 1), d = rev ? col - i : i - col;
-            // M_ij / F_i (a_out is in F, a_in here)
-            mask[e] = d >= 0 ? pw[d] * (m.a_in / fmaxf(pw[rev ? kC - 1 - i : i + 1], kLeastF)) : 0.f;
+            mask[e] = d >= 0 ? pw[d] * rf[(e >> 1) & 1] : 0.f;     // M_ij / F_i (a_out is in F, a_in here)
         }
         for (int c = 0; c < n; ++c) {
             if (kExact && !scale_Z(c, (warp - 10) * 32 + lane, 1, Dz / 64)) { ok = false; break; }
@@ -781,10 +791,10 @@ struct StateArgs {
 // Chunks of piece `sub` of segment `seg`, in the order of the walk.
 __device__ __forceinline__ void piece_range(const TcArgs &a, int seg, int sub, int pieces, int &cb,
                                             int &ce) {
-    const int s0 = seg_bound(seg, a.nchunks, a.splits);
-    const int len = seg_bound(seg + 1, a.nchunks, a.splits) - s0;
-    cb = s0 + (int)((int64_t)sub * len / pieces);
-    ce = s0 + (int)((int64_t)(sub + 1) * len / pieces);
+    const int s0 = seg_bound(seg, a);
+    const int len = seg_bound(seg + 1, a) - s0;
+    cb = s0 + sub * len / pieces;       // (len < 2^24, pieces <= 8)
+    ce = s0 + (sub + 1) * len / pieces;
 }
 
 template <int kParts>
@@ -1157,6 +1167,8 @@ cudaError_t launch_hda_tc(const HdaProblem &p, int splits, int num_sms, void *ws
     a.H = (int)p.H;
     a.nchunks = (int)((p.T + kC - 1) / kC);
     a.splits = s;
+    a.seg_len = a.nchunks / s;
+    a.seg_more = a.nchunks % s;
     a.hint = p.n == 1;
     a.err = dev_err;
     for (int i = 0; i < p.n; ++i) {
