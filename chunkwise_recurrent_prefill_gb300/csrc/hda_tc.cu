@@ -172,7 +172,8 @@ constexpr uint32_t PW = OUT + 4 * 4096;          // [65] f32 powers l^0 .. l^64
 constexpr uint32_t FA = PW + 320;                // [64] f32 output factors a_out F_i
 constexpr uint32_t FU = FA + 256;                // [64] f32 state factors a_in u_j of a full chunk
 constexpr uint32_t FUL = FU + 256;               // the same of the last chunk of the walk
-constexpr uint32_t BAR = FUL + 256;
+constexpr uint32_t MASK = FUL + 256;             // [128] f32 M_ij by i - j + 64
+constexpr uint32_t BAR = MASK + 512;
 constexpr uint32_t NBAR = 28;
 constexpr uint32_t TSLOT = BAR + NBAR * 8;
 constexpr uint32_t ALLOC = TSLOT + 16 + 1024;
@@ -201,6 +202,12 @@ static_assert(FIN < (int)om::NBAR, "output kernel barrier map");
 constexpr int kOutWarps = 20;
 constexpr int kOutThreads = kOutWarps * 32;
 
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+}
+
 // 32 lanes x 32 columns of fp32 accumulators -> 32 floats.
 __device__ __forceinline__ void tmem_ld32f(uint32_t taddr, float (&out)[32]) {
     uint32_t r0[16], r1[16];
@@ -218,8 +225,13 @@ __device__ __forceinline__ void tmem_ld32f(uint32_t taddr, float (&out)[32]) {
 
 // kExact: the state is returned from here (a sequence that is not split), so its updates take
 // three parts of diag(u) Z, and each chunk's is accumulated by itself.
+// CTA = one segment of one head and map (the maps of one segment are neighbours: they read the
+// same tiles). The maps are lin[first] .. lin[first + count - 1].
+// (Two kernels, not two branches of one: an SM's instruction cache does not hold both.)
 template <bool kExact>
-__device__ __forceinline__ void out_segment(const TcMaps &maps, const TcArgs &a) {
+__global__ void __launch_bounds__(kOutThreads, 1)
+hda_tc_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ TcArgs a, const int first,
+                  const int count) {
     using namespace om;
     extern __shared__ uint8_t smraw[];
     uint8_t *sm = align1024(smraw);
@@ -229,10 +241,10 @@ __device__ __forceinline__ void out_segment(const TcMaps &maps, const TcArgs &a)
     float *fa = reinterpret_cast<float *>(sm + FA);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    // the maps of one segment are neighbours: they read the same tiles
-    const int li = blockIdx.x % a.n;
-    const int seg = (blockIdx.x / a.n) % a.splits;
-    const int bh = blockIdx.x / a.n / a.splits;
+    pdl_launch_dependents();
+    const int li = first + blockIdx.x % count;
+    const int seg = (blockIdx.x / count) % a.splits;
+    const int bh = blockIdx.x / count / a.splits;
     const int b = bh / a.H, h = bh % a.H;
     const TcLin &m = a.lin[li];
     const int rev = m.rev, Dx = m.Dx, Dz = m.Dz;
@@ -285,6 +297,8 @@ __device__ __forceinline__ void out_segment(const TcMaps &maps, const TcArgs &a)
         const int i = threadIdx.x & (kC - 1);
         const int nt = threadIdx.x < kC ? kC : chunk_tokens(a.nchunks - 1, a);
         reinterpret_cast<float *>(sm + FU)[threadIdx.x] = m.a_in * state_factor(pw, i, nt, rev);
+        const int d = rev ? kC - (int)threadIdx.x : (int)threadIdx.x - kC;
+        reinterpret_cast<float *>(sm + MASK)[threadIdx.x] = d >= 0 ? pw[d] : 0.f;
     }
     __syncthreads();
     const uint32_t tm = *tslot;
@@ -304,13 +318,19 @@ __device__ __forceinline__ void out_segment(const TcMaps &maps, const TcArgs &a)
         uint4 *zp = reinterpret_cast<uint4 *>(sm + ZP + zb * 16384) + ct;
 #pragma unroll 1
         for (int box = b0; box < b1; ++box) {
-            uint4 v[4];
+            // (three parts: two vectors at a time, for want of registers)
+            constexpr int kAtOnce = kExact ? 2 : 4;
+#pragma unroll 1
+            for (int x0 = 0; x0 < 4; x0 += kAtOnce) {
+                uint4 v[kAtOnce];
 #pragma unroll
-            for (int x = 0; x < 4; ++x) v[x] = zs[box * 512 + 128 * x];
+                for (int x = 0; x < kAtOnce; ++x) v[x] = zs[box * 512 + 128 * (x0 + x)];
 #pragma unroll
-            for (int x = 0; x < 4; ++x)
-                put_scaled<kExact ? 3 : 1>(v[x], u[16 * x], zp + box * 512 + 128 * x,
-                                           zp + 1024 + box * 512 + 128 * x);
+                for (int x = 0; x < kAtOnce; ++x) {
+                    const int at = box * 512 + 128 * (x0 + x);
+                    put_scaled<kExact ? 3 : 1>(v[x], u[16 * (x0 + x)], zp + at, zp + 1024 + at);
+                }
+            }
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -528,13 +548,13 @@ __device__ __forceinline__ void out_segment(const TcMaps &maps, const TcArgs &a)
                 const int64_t base = ((int64_t)b * a.T + t0) * rs + (int64_t)h * Dz + z;
                 const int lo = rev ? kC - nt : 0, hi = rev ? kC : nt;    // the rows there are
 #pragma unroll 1
-                for (int q = 0; q < kC; q += 16) {
-                    uint32_t r[16];
-                    tmem_ld16(ta + q, r);
+                for (int q = 0; q < kC; q += 8) {
+                    uint32_t r[8];
+                    tmem_ld8(ta + q, r);
                     tmem_wait_ld();
                     reg_fence(r);
 #pragma unroll
-                    for (int x = 0; x < 16; ++x) {
+                    for (int x = 0; x < 8; ++x) {
                         const int row = q + x;
                         if (row < lo || row >= hi) continue;
                         const float v = fa[row] * __uint_as_float(r[x]);
@@ -568,11 +588,10 @@ __device__ __forceinline__ void out_segment(const TcMaps &maps, const TcArgs &a)
 #pragma unroll
         for (int e = 0; e < 2; ++e)
             rf[e] = m.a_in / fmaxf(pw[rev ? kC - 1 - ia - 8 * e : ia + 8 * e + 1], kLeastF);
+        const float *mk = reinterpret_cast<const float *>(sm + MASK) + kC + ia - c0;
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-            const int i = ia + (e & 2 ? 8 : 0), col = 8 * (e >> 2) + c0 + (e & 1), d = rev ? col - i : i - col;
-            mask[e] = d >= 0 ? pw[d] * rf[(e >> 1) & 1] : 0.f;     // M_ij / F_i (a_out is in F, a_in here)
-        }
+        for (int e = 0; e < 32; ++e)        // M_ij / F_i (a_out is in F, a_in here)
+            mask[e] = mk[(e & 2 ? 8 : 0) - 8 * (e >> 2) - (e & 1)] * rf[(e >> 1) & 1];
         for (int c = 0; c < n; ++c) {
             if (kExact && !scale_Z(c, (warp - 10) * 32 + lane, 1, Dz / 64)) { ok = false; break; }
             if (!__all_sync(0xffffffffu, wait_bar(&bars[PFULL], par(c)))) { ok = false; break; }
@@ -743,20 +762,14 @@ __device__ __forceinline__ void out_segment(const TcMaps &maps, const TcArgs &a)
     }
 
     if (!ok) atomicOr(a.err, kDevErrTimeout);
+    // launched beside the other maps' kernel: what follows this one must find that complete, too
+    if (kExact) pdl_wait_prerequisites();
     tc_fence_before();
     __syncthreads();
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tm, 512);
     }
-}
-
-// CTA = one segment of one head and map (the maps of one segment are neighbours: they read the
-// same tiles).
-__global__ void __launch_bounds__(kOutThreads, 1)
-hda_tc_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ TcArgs a) {
-    if (a.splits == 1 && a.lin[blockIdx.x % a.n].fin) out_segment<true>(maps, a);
-    else out_segment<false>(maps, a);
 }
 
 // ======================================================================= state kernel
@@ -1049,9 +1062,10 @@ cudaError_t set_attrs() {
     if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
     std::lock_guard<std::mutex> lock(g_attr_mu);
     if (g_attr_done[dev]) return cudaSuccess;
-    e = cudaFuncSetAttribute((const void *)hda_tc_out_kernel,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, om::ALLOC);
-    if (e != cudaSuccess) return e;
+    for (const void *k : {(const void *)hda_tc_out_kernel<false>, (const void *)hda_tc_out_kernel<true>}) {
+        e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, om::ALLOC);
+        if (e != cudaSuccess) return e;
+    }
     e = cudaFuncSetAttribute((const void *)hda_tc_state_kernel,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, st::ALLOC);
     if (e != cudaSuccess) return e;
@@ -1221,16 +1235,27 @@ cudaError_t launch_hda_tc(const HdaProblem &p, int splits, int num_sms, void *ws
         if ((e = cudaLaunchKernelEx(&cfg, hda_tc_scan_kernel, a, sa)) != cudaSuccess) return e;
         count_launches(2);
     }
+    // the last map may return a state: if nothing is split, from the output kernel
+    const int exact = s == 1 && p.lin[p.n - 1].fin ? 1 : 0, plain = p.n - exact;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(bh * s * p.n));
     cfg.blockDim = dim3(kOutThreads);
     cfg.dynamicSmemBytes = om::ALLOC;
     cfg.stream = stream;
     cfg.attrs = pdl;
-    cfg.numAttrs = s > 1 ? 1 : 0;
-    e = cudaLaunchKernelEx(&cfg, hda_tc_out_kernel, maps, a);
-    if (e == cudaSuccess) count_launches(1);
-    return e;
+    if (plain > 0) {
+        cfg.gridDim = dim3((unsigned)(bh * s * plain));
+        cfg.numAttrs = s > 1 ? 1 : 0;
+        if ((e = cudaLaunchKernelEx(&cfg, hda_tc_out_kernel<false>, maps, a, 0, plain)) != cudaSuccess) return e;
+        count_launches(1);
+    }
+    if (exact > 0) {
+        // depends on nothing the other kernel writes: its CTAs fill the SMs as that one's end
+        cfg.gridDim = dim3((unsigned)(bh * s));
+        cfg.numAttrs = plain > 0 ? 1 : 0;
+        if ((e = cudaLaunchKernelEx(&cfg, hda_tc_out_kernel<true>, maps, a, plain, 1)) != cudaSuccess) return e;
+        count_launches(1);
+    }
+    return cudaSuccess;
 }
 
 }  // namespace gla
