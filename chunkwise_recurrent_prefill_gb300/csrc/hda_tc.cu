@@ -16,11 +16,12 @@
 // power with an exponent >= 0), so no decay overflows; where F_i is not f_i, X S counts 2^-60
 // instead of less, which no output's 2^-9 can tell.
 //
-// Roundings to bf16: the operands themselves are bf16. P is rounded once after the mask, S once
-// per chunk for its product with X, and diag(u) Z once for the update of a state that only such
-// outputs read (they are bf16 themselves). A state that the caller gets back in fp32 is updated
-// with diag(u) Z as a sum of three bf16 parts, which leaves nothing out of 24 bits: one part
-// would leave hT off by 2^-9 of a term, two by 2^-18 (3e-6 of hT, measured, against 3e-7).
+// Roundings to bf16: the operands themselves are bf16. P is rounded once after the mask, and S once
+// per chunk for its product with X; both end in an output that is bf16 itself. diag(u) Z goes into
+// the state as a sum of bf16 parts of 8 bits each: two where only outputs read the state (2^-16 of a
+// term is lost; one part, 2^-9, raised the outputs' rms error from 0.0023 to 0.0028 of them, where
+// their own rounding is 0.0017), three where the state is returned in fp32 (nothing of 24 bits is
+// lost; with two parts hT was off by 3e-6, with three by 3e-7).
 //
 // When there are fewer heads than SMs, each head's chunks are split into segments:
 //   hda_tc_state_kernel : pieces of the segments -> their end state from zero, E (of the last
@@ -138,8 +139,9 @@ __device__ __forceinline__ void load_tile(uint8_t *dst, const CUtensorMap *m, ui
 }
 
 // 16 bytes of Z (8 values of one token) times the token's factor, as kParts bf16 parts (the first
-// to dst, the others to rest, 16 KB apart): one, rounded, or three that hold 8 bits of the product's 24 each (cut off, not rounded:
-// the upper half of a float is a bf16, so a part is a byte permutation and the rest a subtraction).
+// to dst, the others to rest, 16 KB apart) that hold 8 of the product's 24 bits each. (Cut off, not
+// rounded: the upper half of a float is a bf16, so a part is a byte permutation and what remains a
+// subtraction.)
 template <int kParts>
 __device__ __forceinline__ void put_scaled(uint4 v, float u, uint4 *dst, uint4 *rest) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -152,7 +154,7 @@ __device__ __forceinline__ void put_scaled(uint4 v, float u, uint4 *dst, uint4 *
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const uint32_t x = __float_as_uint(p[i].x), y = __float_as_uint(p[i].y);
-            o[i] = kParts == 1 ? pack_bf16(p[i].x, p[i].y) : __byte_perm(x, y, 0x7632);
+            o[i] = __byte_perm(x, y, 0x7632);
             if (part + 1 < kParts)
                 p[i] = add2(p[i], make_float2(__uint_as_float((x & 0xffff0000u) ^ 0x80000000u),
                                               __uint_as_float((y & 0xffff0000u) ^ 0x80000000u)));
@@ -165,7 +167,7 @@ __device__ __forceinline__ void put_scaled(uint4 v, float u, uint4 *dst, uint4 *
 namespace om {
 constexpr int NQ = 3;                            // stages of x, y, z tiles
 constexpr uint32_t X = 0, Y = 16384, Z = 32768, STAGE = 49152;
-constexpr uint32_t ZP = NQ * STAGE;              // diag(u) Z: three buffers, or one of three parts
+constexpr uint32_t ZP = NQ * STAGE;              // diag(u) Z, two or three parts
 constexpr uint32_t P = ZP + 3 * 16384;           // two [64 x 64] bf16 tiles, 128B swizzle
 constexpr uint32_t OUT = P + 2 * 8192;           // a [64 x 32] bf16 (or [32 x 32] f32) tile per warp
 constexpr uint32_t PW = OUT + 4 * 4096;          // [65] f32 powers l^0 .. l^64
@@ -187,11 +189,11 @@ constexpr uint32_t COL_SB = 128, COL_SB_EXACT = 448, COL_D = 128;
 }  // namespace om
 
 // Barriers. Where a producer may run two phases ahead of a waiter, the phases alternate between
-// the barriers of the buffers (ZDONE, ZFREE, PBF, OFULL, OFREE); elsewhere the next phase needs the
-// waiter's own arrival.
+// the barriers of the buffers (PBF, OFULL, OFREE, IDONE); elsewhere the next phase needs the waiter's
+// own arrival.
 enum {
-    QFULL = 0, QEMPTY = 3, ZDONE = 6, ZFREE = 9, PBF = 12, OFULL = 14, OFREE = 16, PFULL = 18,
-    PFREE = 19, SREADY = 20, SBFREE = 21, UDONE = 22, IDONE = 23, FIN = 25,
+    QFULL = 0, QEMPTY = 3, PBF = 6, OFULL = 8, OFREE = 10, IDONE = 12, ZDONE = 14, ZFREE = 15, PFULL = 16,
+    PFREE = 17, SREADY = 18, SBFREE = 19, UDONE = 20, FIN = 21,
 };
 static_assert(FIN < (int)om::NBAR, "output kernel barrier map");
 // Warps: 0 TMA, 1 and 19 MMA, 2-5 output, 6-9 state, 10-13 P, 14-17 diag(u) Z (18: none). Every role has a loop of its
@@ -251,7 +253,7 @@ hda_tc_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ T
     const int cb = seg_bound(seg, a);
     const int n = seg_bound(seg + 1, a) - cb;
     const float g = a.decay[h];
-    constexpr int nzb = kExact ? 1 : 3;     // buffers of diag(u) Z
+    constexpr int kParts = kExact ? 3 : 2;
     constexpr uint32_t kColU = kExact ? COL_D : COL_S;
 
     if (threadIdx.x < 128) {
@@ -265,16 +267,14 @@ hda_tc_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ T
             mbar_init(&bars[QFULL + i], 1);
             mbar_init(&bars[QEMPTY + i], 2);
         }
-        for (int i = 0; i < 3; ++i) {
-            mbar_init(&bars[ZDONE + i], kExact ? 8 : 4);
-            mbar_init(&bars[ZFREE + i], 1);
-        }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bars[PBF + i], 4);
             mbar_init(&bars[OFULL + i], 1);
             mbar_init(&bars[OFREE + i], 4);
             mbar_init(&bars[IDONE + i], 1);
         }
+        mbar_init(&bars[ZDONE], 8);
+        mbar_init(&bars[ZFREE], 1);
         mbar_init(&bars[PFULL], 1);
         mbar_init(&bars[PFREE], 4);
         mbar_init(&bars[SREADY], 4);
@@ -309,32 +309,30 @@ hda_tc_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ T
     // 16-byte vectors ct + 128 x of a box: token (ct / 8 + 16 x) % 64. The product keeps the tile's
     // layout, so the swizzle does not matter here.
     auto scale_Z = [&](int c, int ct, int b0, int b1) -> bool {
-        const int s = c % NQ, zb = c % nzb, zuse = c / nzb;
+        const int s = c % NQ;
         const bool w = wait_bar(&bars[QFULL + s], par(c / NQ)) &&
-                       (zuse == 0 || wait_bar(&bars[ZFREE + zb], par(zuse - 1)));
+                       (c == 0 || wait_bar(&bars[ZFREE], par(c - 1)));
         if (!__all_sync(0xffffffffu, w)) return false;
         const float *u = reinterpret_cast<const float *>(sm + (cb + c == a.nchunks - 1 ? FUL : FU)) + (ct >> 3);
         const uint4 *zs = reinterpret_cast<const uint4 *>(sm + s * STAGE + Z) + ct;
-        uint4 *zp = reinterpret_cast<uint4 *>(sm + ZP + zb * 16384) + ct;
+        uint4 *zp = reinterpret_cast<uint4 *>(sm + ZP) + ct;
 #pragma unroll 1
         for (int box = b0; box < b1; ++box) {
-            // (three parts: two vectors at a time, for want of registers)
-            constexpr int kAtOnce = kExact ? 2 : 4;
 #pragma unroll 1
-            for (int x0 = 0; x0 < 4; x0 += kAtOnce) {
-                uint4 v[kAtOnce];
+            for (int x0 = 0; x0 < 4; x0 += 2) {     // (two vectors at a time, for want of registers)
+                uint4 v[2];
 #pragma unroll
-                for (int x = 0; x < kAtOnce; ++x) v[x] = zs[box * 512 + 128 * (x0 + x)];
+                for (int x = 0; x < 2; ++x) v[x] = zs[box * 512 + 128 * (x0 + x)];
 #pragma unroll
-                for (int x = 0; x < kAtOnce; ++x) {
+                for (int x = 0; x < 2; ++x) {
                     const int at = box * 512 + 128 * (x0 + x);
-                    put_scaled<kExact ? 3 : 1>(v[x], u[16 * (x0 + x)], zp + at, zp + 1024 + at);
+                    put_scaled<kParts>(v[x], u[16 * (x0 + x)], zp + at, zp + 1024 + at);
                 }
             }
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars[ZDONE + zb]);
+        if (lane == 0) mbar_arrive(&bars[ZDONE]);
         return true;
     };
 
@@ -387,33 +385,25 @@ hda_tc_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ T
         if (warp == 1) {
             const uint32_t idU = idesc_bf16(128, Dx, 1, 1), idOi = idesc_bf16(128, 64, 0, 0);
             const uint64_t dYt = smem_desc(s0 + Y, 8192, 1024), dZP = smem_desc(s0 + ZP, 8192, 1024);
-            int zb = 0, zuse = 0;   // buffer of diag(u) Z of chunk c, and how often it was used before
             for (int c = 0, s = 0; c < n; ++c) {
                 const uint64_t so = (uint64_t)(s * (STAGE >> 4));
-                w = wait_bar(&bars[SREADY], par(c)) && wait_bar(&bars[ZDONE + zb], par(zuse));
+                w = wait_bar(&bars[SREADY], par(c)) && wait_bar(&bars[ZDONE], par(c));
                 if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
                 tc_fence_after();
                 if (elect_one()) {
-                    const uint64_t y0 = dYt + so, z0 = dZP + (uint64_t)(zb * (16384 >> 4));
+                    const uint64_t y0 = dYt + so;
                     // the small parts first: the accumulator drops the bits below its own last one
                     // at every step, so the fewer steps it is large in, the better
-                    if (kExact) {
 #pragma unroll
-                        for (int kk = 0; kk < 8; ++kk)
-                            mma_ss(tm + kColU, z0 + (2 - (kk >> 2)) * (16384 >> 4) + (kk & 3) * (2048 >> 4),
-                                   y0 + (kk & 3) * (2048 >> 4), idU, kk > 0);
-                    }
+                    for (int part = kParts - 1; part >= 0; --part)
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        mma_ss(tm + kColU, z0 + kk * (2048 >> 4), y0 + kk * (2048 >> 4), idU, 1);
+                        for (int kk = 0; kk < 4; ++kk)
+                            mma_ss(tm + kColU, dZP + part * (16384 >> 4) + kk * (2048 >> 4),
+                                   y0 + kk * (2048 >> 4), idU, !kExact || part < kParts - 1 || kk > 0);
                     mma_commit(&bars[UDONE]);
-                    mma_commit(&bars[ZFREE + zb]);
+                    mma_commit(&bars[ZFREE]);
                 }
                 __syncwarp();
-                if (++zb == nzb) {
-                    zb = 0;
-                    ++zuse;
-                }
                 w = c < 2 || wait_bar(&bars[OFREE + (c & 1)], par((c >> 1) - 1));
                 if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
                 tc_fence_after();
@@ -593,7 +583,8 @@ hda_tc_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ T
         for (int e = 0; e < 32; ++e)        // M_ij / F_i (a_out is in F, a_in here)
             mask[e] = mk[(e & 2 ? 8 : 0) - 8 * (e >> 2) - (e & 1)] * rf[(e >> 1) & 1];
         for (int c = 0; c < n; ++c) {
-            if (kExact && !scale_Z(c, (warp - 10) * 32 + lane, 1, Dz / 64)) { ok = false; break; }
+            // (the second box of diag(u) Z is these warps')
+            if (!scale_Z(c, (warp - 10) * 32 + lane, 1, Dz / 64)) { ok = false; break; }
             if (!__all_sync(0xffffffffu, wait_bar(&bars[PFULL], par(c)))) { ok = false; break; }
             tc_fence_after();
             uint8_t *pt = sm + P + (c & 1) * 8192;
@@ -630,9 +621,7 @@ hda_tc_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ T
         __syncwarp();
     } else if (warp >= 14 && warp < 18) {
         // ------------------------------------------------------------ diag(u) Z
-        // (in three parts, the second box is the P warps')
-        for (int c = 0; ok && c < n; ++c)
-            ok = scale_Z(c, (warp - 14) * 32 + lane, 0, kExact ? 1 : Dz / 64);
+        for (int c = 0; ok && c < n; ++c) ok = scale_Z(c, (warp - 14) * 32 + lane, 0, 1);
         __syncwarp();
     } else if (warp < 10) {
         // ------------------------------------------------------------ state
@@ -778,8 +767,8 @@ hda_tc_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ T
 // (a parity tells a use from the last one, not from the one before).
 namespace st {
 constexpr uint32_t Y = 0, Z = 16384, STAGE = 32768;
-constexpr uint32_t REST = 4 * STAGE;             // three parts: the others, a buffer for each group
-constexpr uint32_t PW = 6 * STAGE;               // (6 stages of one part, or 4 and the buffers)
+constexpr uint32_t REST = 4 * STAGE;             // the other parts, a buffer for each group
+constexpr uint32_t PW = 6 * STAGE;
 constexpr uint32_t BAR = PW + 320;
 constexpr uint32_t NBAR = 26;
 constexpr uint32_t TSLOT = BAR + NBAR * 8;
@@ -814,8 +803,7 @@ template <int kParts>
 __device__ __forceinline__ void state_piece(const TcMaps &maps, const TcArgs &a, const StateArgs &sa,
                                             const StateProblem &sp, int bh, int pi) {
     using namespace st;
-    constexpr int NS = kParts == 1 ? 6 : 4;
-    static_assert(NS % 2 == 0 && (kParts == 1 || kParts == 3), "stages of the state kernel");
+    constexpr int NS = 4;
     // Three parts: an accumulator takes kRun chunks, two take turns, and their sums are added in
     // registers (a sum over many chunks in the accumulator would be cut off at each step).
     constexpr int kRun = kParts == 3 ? 2 : 1 << 30;
@@ -889,7 +877,7 @@ __device__ __forceinline__ void state_piece(const TcMaps &maps, const TcArgs &a,
         const uint64_t dZ = smem_desc(smem_u32(sm) + Z, 8192, 1024);
         const uint64_t dRest = smem_desc(smem_u32(sm) + REST, 8192, 1024);
         for (int c = 0; c < n; ++c) {
-            const int run = c / kRun, buf = run & 1;    // (run 0 alone with one part)
+            const int run = c / kRun, buf = run & 1;    // (run 0 alone with two parts)
             const bool first = c % kRun == 0, w = wait_bar(&bars[SZDONE + c % NS], par(c / NS)) &&
                                (!first || run < 2 || wait_bar(&bars[SREAD + buf], par((run >> 1) - 1)));
             if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
@@ -907,7 +895,7 @@ __device__ __forceinline__ void state_piece(const TcMaps &maps, const TcArgs &a,
                                dY + so + kk * (2048 >> 4), idU,
                                (!first || part < kParts - 1 || kk > 0) ? 1u : 0u);
                 mma_commit(&bars[SEMPTY + c % NS]);
-                if (kParts == 3) mma_commit(&bars[SZFREE + (c & 1)]);
+                mma_commit(&bars[SZFREE + (c & 1)]);
                 if ((c + 1) % kRun == 0 || c + 1 == n) mma_commit(&bars[SDONE + buf]);
             }
             __syncwarp();
@@ -928,7 +916,7 @@ __device__ __forceinline__ void state_piece(const TcMaps &maps, const TcArgs &a,
 #pragma unroll
             for (int x = 0; x < 4; ++x) u[x] = after * state_factor(pw, (ct >> 3) + 16 * x, nt, rev);
             const bool w = wait_bar(&bars[SFULL + s], par(c / NS)) &&
-                           (kParts == 1 || c < 2 || wait_bar(&bars[SZFREE + (c & 1)], par((c >> 1) - 1)));
+                           (c < 2 || wait_bar(&bars[SZFREE + (c & 1)], par((c >> 1) - 1)));
             if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
             uint4 *rest = reinterpret_cast<uint4 *>(sm + REST + (c & 1) * STAGE) + ct;
             uint4 *zs = reinterpret_cast<uint4 *>(sm + s * STAGE + Z) + ct;
@@ -995,7 +983,7 @@ hda_tc_state_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__
     const StateProblem &sp = sa.s[i < n0 ? 0 : 1];
     const int pi = i < n0 ? i : i - n0;
     if (sp.segs == a.splits) state_piece<3>(maps, a, sa, sp, bh, pi);
-    else state_piece<1>(maps, a, sa, sp, bh, pi);
+    else state_piece<2>(maps, a, sa, sp, bh, pi);
 }
 
 // ======================================================================= scan kernel
