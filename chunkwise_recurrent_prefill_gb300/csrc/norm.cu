@@ -34,45 +34,51 @@ __device__ __forceinline__ float get(const __nv_bfloat16 *p) { return __bfloat16
 __device__ __forceinline__ void put(float *p, float x) { *p = x; }
 __device__ __forceinline__ void put(__nv_bfloat16 *p, float x) { *p = __float2bfloat16_rn(x); }
 
-// 16 bytes as floats.
+// 16 bytes as pairs of floats (the arithmetic is in packed pairs throughout: with scalar
+// instructions the rows kernels were bound by issue, at 40 instructions an element).
 template <typename T>
 struct Vec;
 template <>
 struct Vec<float> {
     static constexpr int n = 4;
-    static __device__ __forceinline__ void unpack(uint4 v, float (&f)[4]) {
-        f[0] = __uint_as_float(v.x);
-        f[1] = __uint_as_float(v.y);
-        f[2] = __uint_as_float(v.z);
-        f[3] = __uint_as_float(v.w);
+    static __device__ __forceinline__ void unpack(uint4 v, float2 (&f)[2]) {
+        f[0] = make_float2(__uint_as_float(v.x), __uint_as_float(v.y));
+        f[1] = make_float2(__uint_as_float(v.z), __uint_as_float(v.w));
     }
-    static __device__ __forceinline__ uint4 pack(const float (&f)[4]) {
-        return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
-                          __float_as_uint(f[3]));
+    static __device__ __forceinline__ uint4 pack(const float2 (&f)[2]) {
+        return make_uint4(__float_as_uint(f[0].x), __float_as_uint(f[0].y), __float_as_uint(f[1].x),
+                          __float_as_uint(f[1].y));
     }
 };
 template <>
 struct Vec<__nv_bfloat16> {
     static constexpr int n = 8;
-    static __device__ __forceinline__ void unpack(uint4 v, float (&f)[8]) {
+    static __device__ __forceinline__ void unpack(uint4 v, float2 (&f)[4]) {
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            f[2 * i] = __uint_as_float(w[i] << 16);
-            f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-        }
+        for (int i = 0; i < 4; ++i)
+            f[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
     }
-    static __device__ __forceinline__ uint4 pack(const float (&f)[8]) {
-        return make_uint4(tc::pack_bf16(f[0], f[1]), tc::pack_bf16(f[2], f[3]), tc::pack_bf16(f[4], f[5]),
-                          tc::pack_bf16(f[6], f[7]));
+    static __device__ __forceinline__ uint4 pack(const float2 (&f)[4]) {
+        return make_uint4(tc::pack_bf16(f[0].x, f[0].y), tc::pack_bf16(f[1].x, f[1].y),
+                          tc::pack_bf16(f[2].x, f[2].y), tc::pack_bf16(f[3].x, f[3].y));
     }
 };
+using tc::add2;
+using tc::fma2;
+using tc::mul2;
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
-// The logistic function. Results that are rounded to bf16 take the fast exponential and division
-// (a few 2^-22 of the value); the exact ones would make the kernels bound by arithmetic.
+// The logistic function 1 / (1 + 2^(-u log2 e)). Results that are rounded to bf16 take the hardware's
+// approximate exponential and reciprocal (a few 2^-22 of the value), flushing denormals: the exact
+// functions, and even the fast ones with their care for denormals, made the kernels bound by issue.
 template <typename T>
 __device__ __forceinline__ float logistic(float u) {
-    return sizeof(T) == 2 ? __fdividef(1.f, 1.f + __expf(-u)) : 1.f / (1.f + expf(-u));
+    if (sizeof(T) == 4) return 1.f / (1.f + expf(-u));
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(u * -1.4426950408889634f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+    return r;
 }
 template <typename T>
 __device__ __forceinline__ float act_of(float u, int act) {
@@ -89,6 +95,25 @@ __device__ __forceinline__ float act_grad(float u, int act) {
     if (act == 2)
         return 0.5f * (1.f + erff(u * 0.70710678f)) + u * expf(-0.5f * u * u) * 0.39894228f;
     return 1.f;
+}
+
+// Of pairs; kSilu: the activation is known at compile time, else it is act.
+template <typename T, bool kSilu>
+__device__ __forceinline__ float2 act_of2(float2 u, int act) {
+    if (kSilu) return mul2(u, make_float2(logistic<T>(u.x), logistic<T>(u.y)));
+    return make_float2(act_of<T>(u.x, act), act_of<T>(u.y, act));
+}
+// The activation and its derivative, from one logistic if it is silu.
+template <typename T, bool kSilu>
+__device__ __forceinline__ void act_and_grad2(float2 u, int act, float2 &a, float2 &g) {
+    if (kSilu) {
+        const float2 s = make_float2(logistic<T>(u.x), logistic<T>(u.y));
+        a = mul2(u, s);
+        g = fma2(a, fma2(s, both(-1.f), both(1.f)), s);     // s (1 + u (1 - s))
+    } else {
+        a = make_float2(act_of<T>(u.x, act), act_of<T>(u.y, act));
+        g = make_float2(act_grad<T>(u.x, act), act_grad<T>(u.y, act));
+    }
 }
 
 // Count, mean and sum of squared deviations of some values.
@@ -111,45 +136,38 @@ __device__ __forceinline__ Stat merge_lanes(Stat s, int width) {
     return s;
 }
 __device__ __forceinline__ float sum_lanes(float v, int width) {
-    for (int o = width >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        if (o < width) v += __shfl_xor_sync(0xffffffffu, v, o);     // (width is the same in the warp)
     return v;
 }
 // 8 (or 4) weights from memory, or their default.
 template <int N>
-__device__ __forceinline__ void load_param(const float *p, int64_t c, float otherwise, float (&f)[N]) {
+__device__ __forceinline__ void load_param(const float *p, int64_t c, float otherwise, float2 (&f)[N]) {
 #pragma unroll
-    for (int i = 0; i < N; i += 4) {
-        const float4 v = p ? *reinterpret_cast<const float4 *>(p + c + i)
+    for (int i = 0; i < N; i += 2) {
+        const float4 v = p ? *reinterpret_cast<const float4 *>(p + c + 2 * i)
                            : make_float4(otherwise, otherwise, otherwise, otherwise);
-        f[i] = v.x;
-        f[i + 1] = v.y;
-        f[i + 2] = v.z;
-        f[i + 3] = v.w;
+        f[i] = make_float2(v.x, v.y);
+        f[i + 1] = make_float2(v.z, v.w);
     }
 }
 
 // What the backward pass makes of one vector: xhat, du, and dgate in place of z.
-template <typename T, bool kGate, int V>
-__device__ __forceinline__ void grad_vec(float (&x)[V], float (&dy)[V], float (&z)[V], const float (&w)[V],
-                                         const float (&b)[V], float mean, float rstd, int act) {
+template <typename T, bool kGate, bool kSilu, int N>
+__device__ __forceinline__ void grad_vec(float2 (&x)[N], float2 (&dy)[N], float2 (&z)[N], const float2 (&w)[N],
+                                         const float2 (&b)[N], float mean, float rstd, int act) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        x[i] = (x[i] - mean) * rstd;
-        const float u = fmaf(x[i], w[i], b[i]);
+    for (int i = 0; i < N; ++i) {
+        x[i] = mul2(add2(x[i], both(-mean)), both(rstd));
+        const float2 u = fma2(x[i], w[i], b[i]);
+        float2 a, g;
+        act_and_grad2<T, kSilu>(kGate ? z[i] : u, act, a, g);
         if (kGate) {
-            float a, g;
-            if (act == 1) {     // both of silu's from one logistic
-                const float s = logistic<T>(z[i]);
-                a = z[i] * s;
-                g = s * (1.f + z[i] * (1.f - s));
-            } else {
-                a = act_of<T>(z[i], act);
-                g = act_grad<T>(z[i], act);
-            }
-            z[i] = dy[i] * u * g;
-            dy[i] *= a;
+            z[i] = mul2(mul2(dy[i], u), g);
+            dy[i] = mul2(dy[i], a);
         } else {
-            dy[i] *= act_grad<T>(u, act);
+            dy[i] = mul2(dy[i], g);
         }
     }
 }
@@ -163,7 +181,7 @@ struct RowPlan {
     int cg;         // channels of a group
 };
 
-template <typename T, int VPL, bool kGate>
+template <typename T, int VPL, bool kGate, bool kSilu>
 __global__ void __launch_bounds__(kThreads)
 norm_rows_fwd(const __grid_constant__ NormProblem p, const RowPlan r) {
     constexpr int V = Vec<T>::n;
@@ -173,7 +191,7 @@ norm_rows_fwd(const __grid_constant__ NormProblem p, const RowPlan r) {
     const int64_t n0 = (int64_t)blockIdx.x * r.rp + seg / r.gpc, step = (int64_t)gridDim.x * r.rp;
     const bool live = g < p.G && seg / r.gpc < r.rp;
     const int64_t c0 = (live ? g : 0) * cg;
-    float w[VPL][V], b[VPL][V];
+    float2 w[VPL][V / 2], b[VPL][V / 2];
 #pragma unroll
     for (int k = 0; k < VPL; ++k) {
         const int v = lane + k * r.W;
@@ -183,23 +201,28 @@ norm_rows_fwd(const __grid_constant__ NormProblem p, const RowPlan r) {
     }
     const float inv = 1.f / (float)cg;
     uint4 xv[VPL], zv[VPL];
+    const T *xp = static_cast<const T *>(p.x) + n0 * p.x_n + c0 + lane * V;
+    const T *zp = static_cast<const T *>(p.gate) + (kGate ? n0 * p.gate_n + c0 + lane * V : 0);
+    T *yp = static_cast<T *>(p.y) + n0 * p.C + c0 + lane * V;
+    const int64_t xs = step * p.x_n, zs = step * p.gate_n, ys = step * p.C;
     auto load = [&](int64_t n) {
+        const bool in = live && n < p.N;
 #pragma unroll
         for (int k = 0; k < VPL; ++k) {
-            const int v = lane + k * r.W;
             xv[k] = zv[k] = make_uint4(0, 0, 0, 0);
-            if (live && n < p.N && v < nv) {
-                xv[k] = *reinterpret_cast<const uint4 *>(static_cast<const T *>(p.x) + n * p.x_n + c0 + v * V);
-                if (kGate)
-                    zv[k] = *reinterpret_cast<const uint4 *>(static_cast<const T *>(p.gate) + n * p.gate_n + c0 + v * V);
+            if (in && lane + k * r.W < nv) {
+                xv[k] = *reinterpret_cast<const uint4 *>(xp + k * r.W * V);
+                if (kGate) zv[k] = *reinterpret_cast<const uint4 *>(zp + k * r.W * V);
             }
         }
+        xp += xs;
+        if (kGate) zp += zs;
     };
     load(n0);
     // the whole warp walks together (the shuffles need every lane): rows past the end do nothing.
     // The next entry is loaded while this one is worked on.
-    for (int64_t base = (int64_t)blockIdx.x * r.rp, n = n0; base < p.N; base += step, n += step) {
-        float x[VPL][V];
+    for (int64_t base = (int64_t)blockIdx.x * r.rp, n = n0; base < p.N; base += step, n += step, yp += ys) {
+        float2 x[VPL][V / 2];
         uint4 zc[VPL];
 #pragma unroll
         for (int k = 0; k < VPL; ++k) {
@@ -207,44 +230,45 @@ norm_rows_fwd(const __grid_constant__ NormProblem p, const RowPlan r) {
             zc[k] = zv[k];
         }
         load(n + step);
-        float sum = 0.f, sq = 0.f;      // (vectors past the group's are zeros)
+        float2 sum = both(0.f), sq = both(0.f);     // (vectors past the group's are zeros)
 #pragma unroll
         for (int k = 0; k < VPL; ++k)
 #pragma unroll
-            for (int i = 0; i < V; ++i) sum += x[k][i];
-        const float mean = sum_lanes(sum, r.W) * inv;
+            for (int i = 0; i < V / 2; ++i) sum = add2(sum, x[k][i]);
+        const float mean = sum_lanes(sum.x + sum.y, r.W) * inv;
 #pragma unroll
-        for (int k = 0; k < VPL; ++k)
+        for (int k = 0; k < VPL; ++k) {
+            float2 t = both(0.f);
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                x[k][i] -= mean;
-                if (lane + k * r.W < nv) sq = fmaf(x[k][i], x[k][i], sq);
+            for (int i = 0; i < V / 2; ++i) {
+                x[k][i] = add2(x[k][i], both(-mean));
+                t = fma2(x[k][i], x[k][i], t);
             }
-        const float rstd = 1.f / sqrtf(fmaf(sum_lanes(sq, r.W), inv, p.eps));
+            if (lane + k * r.W < nv) sq = add2(sq, t);
+        }
+        const float rstd = rsqrtf(fmaf(sum_lanes(sq.x + sq.y, r.W), inv, p.eps));
         if (!live || n >= p.N) continue;
         if (lane == 0) {
             if (p.mean) p.mean[n * p.G + g] = mean;
             if (p.rstd) p.rstd[n * p.G + g] = rstd;
         }
-        T *yp = static_cast<T *>(p.y) + n * p.C + c0;
 #pragma unroll
         for (int k = 0; k < VPL; ++k) {
-            const int v = lane + k * r.W;
-            if (v >= nv) continue;
-            float z[V];
+            if (lane + k * r.W >= nv) continue;
+            float2 z[V / 2];
             if (kGate) Vec<T>::unpack(zc[k], z);
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const float u = fmaf(x[k][i] * rstd, w[k][i], b[k][i]);
-                x[k][i] = kGate ? u * act_of<T>(z[i], p.act) : act_of<T>(u, p.act);
+            for (int i = 0; i < V / 2; ++i) {
+                const float2 u = fma2(mul2(x[k][i], both(rstd)), w[k][i], b[k][i]);
+                x[k][i] = kGate ? mul2(u, act_of2<T, kSilu>(z[i], p.act)) : act_of2<T, kSilu>(u, p.act);
             }
-            *reinterpret_cast<uint4 *>(yp + v * V) = Vec<T>::pack(x[k]);
+            *reinterpret_cast<uint4 *>(yp + k * r.W * V) = Vec<T>::pack(x[k]);
         }
     }
 }
 
 // Partial channel sums: sums[part][0: dw, 1: db][C], part = blockIdx.x * rp + the entry slot.
-template <typename T, int VPL, bool kGate>
+template <typename T, int VPL, bool kGate, bool kSilu>
 __global__ void __launch_bounds__(kThreads)
 norm_rows_bwd(const __grid_constant__ NormProblem p, const RowPlan r, float *sums) {
     constexpr int V = Vec<T>::n;
@@ -254,7 +278,7 @@ norm_rows_bwd(const __grid_constant__ NormProblem p, const RowPlan r, float *sum
     const int64_t n0 = (int64_t)blockIdx.x * r.rp + seg / r.gpc, step = (int64_t)gridDim.x * r.rp;
     const bool live = g < p.G && seg / r.gpc < r.rp;
     const int64_t c0 = (live ? g : 0) * cg;
-    float w[VPL][V], b[VPL][V], dw[VPL][V], db[VPL][V];
+    float2 w[VPL][V / 2], b[VPL][V / 2], dw[VPL][V / 2], db[VPL][V / 2];
 #pragma unroll
     for (int k = 0; k < VPL; ++k) {
         const int v = lane + k * r.W;
@@ -262,31 +286,43 @@ norm_rows_bwd(const __grid_constant__ NormProblem p, const RowPlan r, float *sum
         load_param(p.w, c, 1.f, w[k]);
         load_param(p.b, c, 0.f, b[k]);
 #pragma unroll
-        for (int i = 0; i < V; ++i) dw[k][i] = db[k][i] = 0.f;
+        for (int i = 0; i < V / 2; ++i) dw[k][i] = db[k][i] = both(0.f);
     }
     const float inv = 1.f / (float)cg;
     uint4 xv[VPL], dv[VPL], zv[VPL];
     float mean, rstd;
+    const int64_t at0 = c0 + lane * V;
+    const T *xp = static_cast<const T *>(p.x) + n0 * p.x_n + at0;
+    const T *dp = static_cast<const T *>(p.dy) + n0 * p.dy_n + at0;
+    const T *zp = static_cast<const T *>(p.gate) + (kGate ? n0 * p.gate_n + at0 : 0);
+    const float *mp = p.mean + n0 * p.G + g, *rp = p.rstd + n0 * p.G + g;
+    T *op = static_cast<T *>(p.dx) + n0 * p.C + at0;
+    T *gp = static_cast<T *>(p.dgate) + (kGate ? n0 * p.C + at0 : 0);
+    const int64_t xs = step * p.x_n, ds = step * p.dy_n, zs = step * p.gate_n, ms = step * p.G, os = step * p.C;
     auto load = [&](int64_t n) {
         const bool in = live && n < p.N;
 #pragma unroll
         for (int k = 0; k < VPL; ++k) {
-            const int v = lane + k * r.W;
             xv[k] = dv[k] = zv[k] = make_uint4(0, 0, 0, 0);
-            if (in && v < nv) {
-                xv[k] = *reinterpret_cast<const uint4 *>(static_cast<const T *>(p.x) + n * p.x_n + c0 + v * V);
-                dv[k] = *reinterpret_cast<const uint4 *>(static_cast<const T *>(p.dy) + n * p.dy_n + c0 + v * V);
-                if (kGate)
-                    zv[k] = *reinterpret_cast<const uint4 *>(static_cast<const T *>(p.gate) + n * p.gate_n + c0 + v * V);
+            if (in && lane + k * r.W < nv) {
+                xv[k] = *reinterpret_cast<const uint4 *>(xp + k * r.W * V);
+                dv[k] = *reinterpret_cast<const uint4 *>(dp + k * r.W * V);
+                if (kGate) zv[k] = *reinterpret_cast<const uint4 *>(zp + k * r.W * V);
             }
         }
-        mean = in ? p.mean[n * p.G + g] : 0.f;
-        rstd = in ? p.rstd[n * p.G + g] : 0.f;
+        mean = in ? *mp : 0.f;
+        rstd = in ? *rp : 0.f;
+        xp += xs;
+        dp += ds;
+        if (kGate) zp += zs;
+        mp += ms;
+        rp += ms;
     };
     // (a lane with more than one vector has no registers for the next entry's)
     constexpr bool kAhead = VPL == 1;
     if (kAhead) load(n0);
-    for (int64_t base = (int64_t)blockIdx.x * r.rp, n = n0; base < p.N; base += step, n += step) {
+    for (int64_t base = (int64_t)blockIdx.x * r.rp, n = n0; base < p.N;
+         base += step, n += step, op += os, gp += kGate ? os : 0) {
         const bool in = live && n < p.N;
         if (!kAhead) load(n);
         uint4 xc[VPL], dc[VPL], zc[VPL];
@@ -298,38 +334,36 @@ norm_rows_bwd(const __grid_constant__ NormProblem p, const RowPlan r, float *sum
         }
         const float mu = mean, rs = rstd;
         if (kAhead) load(n + step);
-        float x[VPL][V], d[VPL][V], z[V];
-        float s1 = 0.f, s2 = 0.f;
-        T *gp = static_cast<T *>(p.dgate) + (kGate ? n * p.C + c0 : 0);
+        float2 x[VPL][V / 2], d[VPL][V / 2], z[V / 2];
+        float2 t1 = both(0.f), t2 = both(0.f);
 #pragma unroll
         for (int k = 0; k < VPL; ++k) {
             const int v = lane + k * r.W;
             Vec<T>::unpack(xc[k], x[k]);
             Vec<T>::unpack(dc[k], d[k]);
             Vec<T>::unpack(zc[k], z);
-            grad_vec<T, kGate>(x[k], d[k], z, w[k], b[k], mu, rs, p.act);
+            grad_vec<T, kGate, kSilu>(x[k], d[k], z, w[k], b[k], mu, rs, p.act);
             if (!in || v >= nv) continue;
-            if (kGate) *reinterpret_cast<uint4 *>(gp + v * V) = Vec<T>::pack(z);
+            if (kGate) *reinterpret_cast<uint4 *>(gp + k * r.W * V) = Vec<T>::pack(z);
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                dw[k][i] = fmaf(d[k][i], x[k][i], dw[k][i]);
-                db[k][i] += d[k][i];
-                d[k][i] *= w[k][i];
-                s1 += d[k][i];
-                s2 = fmaf(d[k][i], x[k][i], s2);
+            for (int i = 0; i < V / 2; ++i) {
+                dw[k][i] = fma2(d[k][i], x[k][i], dw[k][i]);
+                db[k][i] = add2(db[k][i], d[k][i]);
+                d[k][i] = mul2(d[k][i], w[k][i]);
+                t1 = add2(t1, d[k][i]);
+                t2 = fma2(d[k][i], x[k][i], t2);
             }
         }
-        s1 = sum_lanes(s1, r.W) * inv;
-        s2 = sum_lanes(s2, r.W) * inv;
+        const float s1 = sum_lanes(t1.x + t1.y, r.W) * inv;
+        const float s2 = sum_lanes(t2.x + t2.y, r.W) * inv;
         if (!in) continue;
-        T *op = static_cast<T *>(p.dx) + n * p.C + c0;
 #pragma unroll
         for (int k = 0; k < VPL; ++k) {
-            const int v = lane + k * r.W;
-            if (v >= nv) continue;
+            if (lane + k * r.W >= nv) continue;
 #pragma unroll
-            for (int i = 0; i < V; ++i) x[k][i] = rs * (d[k][i] - s1 - x[k][i] * s2);
-            *reinterpret_cast<uint4 *>(op + v * V) = Vec<T>::pack(x[k]);
+            for (int i = 0; i < V / 2; ++i)
+                x[k][i] = mul2(both(rs), fma2(x[k][i], both(-s2), add2(d[k][i], both(-s1))));
+            *reinterpret_cast<uint4 *>(op + k * r.W * V) = Vec<T>::pack(x[k]);
         }
     }
     if (!sums || !live) return;
@@ -339,9 +373,9 @@ norm_rows_bwd(const __grid_constant__ NormProblem p, const RowPlan r, float *sum
         const int v = lane + k * r.W;
         if (v >= nv) continue;
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            sp[c0 + v * V + i] = dw[k][i];
-            sp[p.C + c0 + v * V + i] = db[k][i];
+        for (int i = 0; i < V / 2; ++i) {
+            *reinterpret_cast<float2 *>(sp + c0 + v * V + 2 * i) = dw[k][i];
+            *reinterpret_cast<float2 *>(sp + p.C + c0 + v * V + 2 * i) = db[k][i];
         }
     }
 }
@@ -384,32 +418,38 @@ norm_maps_stats(const __grid_constant__ NormProblem p, const MapPlan m, Stat *pa
     Stat s{0.f, 0.f, 0.f};
     if (q.live && q.l0 + q.ty < q.l1) {
         const T *xp = static_cast<const T *>(p.x) + q.n * p.x_n + q.v * V;
-        float pivot = 0.f, s1 = 0.f, s2 = 0.f, n = 0.f;
-        for (int64_t l = q.l0 + q.ty; l < q.l1; l += (int64_t)m.ry * kAhead) {
+        float pivot = 0.f;
+        float2 t1 = both(0.f), t2 = both(0.f);
+        const int64_t xs = m.ry * p.x_l;
+        xp += (q.l0 + q.ty) * p.x_l;
+        const int count = (int)((q.l1 - q.l0 - q.ty + m.ry - 1) / m.ry);
+        for (int i0 = 0; i0 < count; i0 += kAhead) {
             uint4 xv[kAhead];
 #pragma unroll
-            for (int a = 0; a < kAhead; ++a)
-                if (l + a * m.ry < q.l1) xv[a] = *reinterpret_cast<const uint4 *>(xp + (l + a * m.ry) * p.x_l);
+            for (int a = 0; a < kAhead; ++a) {
+                if (i0 + a < count) xv[a] = *reinterpret_cast<const uint4 *>(xp);
+                xp += xs;
+            }
 #pragma unroll
             for (int a = 0; a < kAhead; ++a)
-                if (l + a * m.ry < q.l1) {
-                    float f[V];
+                if (i0 + a < count) {
+                    float2 f[V / 2];
                     Vec<T>::unpack(xv[a], f);
-                    if (n == 0.f) {
-                        float t = 0.f;
+                    if (a == 0 && i0 == 0) {
+                        float2 t = f[0];
 #pragma unroll
-                        for (int i = 0; i < V; ++i) t += f[i];
-                        pivot = t * (1.f / V);
+                        for (int i = 1; i < V / 2; ++i) t = add2(t, f[i]);
+                        pivot = (t.x + t.y) * (1.f / V);
                     }
-                    n += (float)V;
 #pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        const float d = f[i] - pivot;
-                        s1 += d;
-                        s2 = fmaf(d, d, s2);
+                    for (int i = 0; i < V / 2; ++i) {
+                        const float2 d = add2(f[i], both(-pivot));
+                        t1 = add2(t1, d);
+                        t2 = fma2(d, d, t2);
                     }
                 }
         }
+        const float s1 = t1.x + t1.y, s2 = t2.x + t2.y, n = (float)count * V;
         const float d = s1 / n;
         s = Stat{n, pivot + d, fmaxf(fmaf(-s1, d, s2), 0.f)};
         if (!(s2 < INFINITY)) s.m2 = s2;    // infinity or NaN (which fmaxf would drop)
@@ -447,12 +487,12 @@ norm_maps_combine(const __grid_constant__ NormProblem p, const MapPlan m, const 
     if (p.rstd) p.rstd[i] = rstd;
 }
 
-template <typename T, bool kGate>
+template <typename T, bool kGate, bool kSilu>
 __global__ void __launch_bounds__(kThreads)
 norm_maps_apply(const __grid_constant__ NormProblem p, const MapPlan m, const float2 *stat) {
     constexpr int V = Vec<T>::n, kAhead = 2;
     const MapPos q = map_pos(p, m);
-    float w[V], b[V];
+    float2 w[V / 2], b[V / 2];
     const int64_t c = (q.live ? q.v : 0) * V;
     load_param(p.w, c, 1.f, w);
     load_param(p.b, c, 0.f, b);
@@ -474,13 +514,13 @@ norm_maps_apply(const __grid_constant__ NormProblem p, const MapPlan m, const fl
 #pragma unroll
         for (int a = 0; a < kAhead; ++a)
             if (l + a * m.ry < q.l1) {
-                float f[V], z[V];
+                float2 f[V / 2], z[V / 2];
                 Vec<T>::unpack(xv[a], f);
                 if (kGate) Vec<T>::unpack(zv[a], z);
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const float u = fmaf((f[i] - mean) * rstd, w[i], b[i]);
-                    f[i] = kGate ? u * act_of<T>(z[i], p.act) : act_of<T>(u, p.act);
+                for (int i = 0; i < V / 2; ++i) {
+                    const float2 u = fma2(mul2(add2(f[i], both(-mean)), both(rstd)), w[i], b[i]);
+                    f[i] = kGate ? mul2(u, act_of2<T, kSilu>(z[i], p.act)) : act_of2<T, kSilu>(u, p.act);
                 }
                 *reinterpret_cast<uint4 *>(yp + (l + a * m.ry) * p.C) = Vec<T>::pack(f);
             }
@@ -488,22 +528,21 @@ norm_maps_apply(const __grid_constant__ NormProblem p, const MapPlan m, const fl
 }
 
 // Sums of du w and du w xhat of each part and group -> part; channel sums -> sums[entry, part][2][C].
-template <typename T, bool kGate>
+template <typename T, bool kGate, bool kSilu>
 __global__ void __launch_bounds__(kThreads)
 norm_maps_bwd_stats(const __grid_constant__ NormProblem p, const MapPlan m, float2 *part, float *sums) {
     constexpr int V = Vec<T>::n;
     tc::pdl_launch_dependents();
     __shared__ float2 sh[kThreads];
-    extern __shared__ float ch[];      // [threads][2 V] channel sums of the position slots
+    extern __shared__ __align__(16) float ch[];     // [threads][2 V + 4] channel sums of the position slots
     const MapPos q = map_pos(p, m);
     const int nv = m.nv;
-    float dw[V], db[V];
+    float2 dw[V / 2], db[V / 2], t1 = both(0.f), t2 = both(0.f);
 #pragma unroll
-    for (int i = 0; i < V; ++i) dw[i] = db[i] = 0.f;
-    float s1 = 0.f, s2 = 0.f;
+    for (int i = 0; i < V / 2; ++i) dw[i] = db[i] = both(0.f);
     if (q.live) {
         const int64_t c = q.v * V, at = q.n * p.G + q.v / nv;
-        float w[V], b[V];
+        float2 w[V / 2], b[V / 2];
         load_param(p.w, c, 1.f, w);
         load_param(p.b, c, 0.f, b);
         const float mean = p.mean[at], rstd = p.rstd[at];
@@ -512,25 +551,28 @@ norm_maps_bwd_stats(const __grid_constant__ NormProblem p, const MapPlan m, floa
         const T *zp = static_cast<const T *>(p.gate) + (kGate ? q.n * p.gate_n + c : 0);
 #pragma unroll 2
         for (int64_t l = q.l0 + q.ty; l < q.l1; l += m.ry) {
-            float x[V], d[V], z[V];
+            float2 x[V / 2], d[V / 2], z[V / 2];
             Vec<T>::unpack(*reinterpret_cast<const uint4 *>(xp + l * p.x_l), x);
             Vec<T>::unpack(*reinterpret_cast<const uint4 *>(dp + l * p.dy_l), d);
             if (kGate) Vec<T>::unpack(*reinterpret_cast<const uint4 *>(zp + l * p.gate_l), z);
-            grad_vec<T, kGate>(x, d, z, w, b, mean, rstd, p.act);
+            grad_vec<T, kGate, kSilu>(x, d, z, w, b, mean, rstd, p.act);
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                dw[i] = fmaf(d[i], x[i], dw[i]);
-                db[i] += d[i];
-                s1 = fmaf(d[i], w[i], s1);
-                s2 = fmaf(d[i] * w[i], x[i], s2);
+            for (int i = 0; i < V / 2; ++i) {
+                dw[i] = fma2(d[i], x[i], dw[i]);
+                db[i] = add2(db[i], d[i]);
+                d[i] = mul2(d[i], w[i]);
+                t1 = add2(t1, d[i]);
+                t2 = fma2(d[i], x[i], t2);
             }
         }
     }
-    sh[threadIdx.x] = make_float2(s1, s2);
+    sh[threadIdx.x] = make_float2(t1.x + t1.y, t2.x + t2.y);
+    // (16 bytes more a thread, so that neighbours' sums do not share banks)
+    float2 *mine = reinterpret_cast<float2 *>(ch + threadIdx.x * (2 * V + 4));
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        ch[threadIdx.x * 2 * V + i] = dw[i];
-        ch[threadIdx.x * 2 * V + V + i] = db[i];
+    for (int i = 0; i < V / 2; ++i) {
+        mine[i] = dw[i];
+        mine[V / 2 + i] = db[i];
     }
     __syncthreads();
     const int groups = m.groups, lane = threadIdx.x & 31;
@@ -553,7 +595,7 @@ norm_maps_bwd_stats(const __grid_constant__ NormProblem p, const MapPlan m, floa
         const int64_t c = ((int64_t)blockIdx.y * m.nvb + tx) * V + i % V;
         if (c >= p.C) continue;
         float t = 0.f;
-        for (int y = 0; y < m.ry; ++y) t += ch[(y * m.nvb + tx) * 2 * V + i];
+        for (int y = 0; y < m.ry; ++y) t += ch[(y * m.nvb + tx) * (2 * V + 4) + i];
         sp[(i < V ? 0 : p.C) + c] = t;
     }
 }
@@ -578,7 +620,7 @@ norm_maps_bwd_combine(const __grid_constant__ NormProblem p, const MapPlan m, co
     if (lane == 0) mean[i] = make_float2(a * inv, b * inv);
 }
 
-template <typename T, bool kGate>
+template <typename T, bool kGate, bool kSilu>
 __global__ void __launch_bounds__(kThreads)
 norm_maps_bwd_apply(const __grid_constant__ NormProblem p, const MapPlan m, const float2 *means) {
     constexpr int V = Vec<T>::n;
@@ -587,7 +629,7 @@ norm_maps_bwd_apply(const __grid_constant__ NormProblem p, const MapPlan m, cons
     tc::pdl_wait_prerequisites();
     if (!q.live) return;
     const int64_t c = q.v * V, at = q.n * p.G + q.v / nv;
-    float w[V], b[V];
+    float2 w[V / 2], b[V / 2];
     load_param(p.w, c, 1.f, w);
     load_param(p.b, c, 0.f, b);
     const float mean = p.mean[at], rstd = p.rstd[at], s1 = means[at].x, s2 = means[at].y;
@@ -598,13 +640,14 @@ norm_maps_bwd_apply(const __grid_constant__ NormProblem p, const MapPlan m, cons
     T *gp = static_cast<T *>(p.dgate) + (kGate ? q.n * p.L * p.C + c : 0);
 #pragma unroll 2
     for (int64_t l = q.l0 + q.ty; l < q.l1; l += m.ry) {
-        float x[V], d[V], z[V];
+        float2 x[V / 2], d[V / 2], z[V / 2];
         Vec<T>::unpack(*reinterpret_cast<const uint4 *>(xp + l * p.x_l), x);
         Vec<T>::unpack(*reinterpret_cast<const uint4 *>(dp + l * p.dy_l), d);
         if (kGate) Vec<T>::unpack(*reinterpret_cast<const uint4 *>(zp + l * p.gate_l), z);
-        grad_vec<T, kGate>(x, d, z, w, b, mean, rstd, p.act);
+        grad_vec<T, kGate, kSilu>(x, d, z, w, b, mean, rstd, p.act);
 #pragma unroll
-        for (int i = 0; i < V; ++i) x[i] = rstd * (d[i] * w[i] - s1 - x[i] * s2);
+        for (int i = 0; i < V / 2; ++i)
+            x[i] = mul2(both(rstd), fma2(x[i], both(-s2), fma2(d[i], w[i], both(-s1))));
         *reinterpret_cast<uint4 *>(op + l * p.C) = Vec<T>::pack(x);
         if (kGate) *reinterpret_cast<uint4 *>(gp + l * p.C) = Vec<T>::pack(z);
     }
@@ -837,16 +880,16 @@ cudaError_t launch(void (*kernel)(A...), dim3 grid, size_t smem, bool dependent,
     return launch_n(kernel, grid, kThreads, smem, dependent, s, args...);
 }
 
-template <typename T, bool kGate>
+template <typename T, bool kGate, bool kSilu>
 cudaError_t run_fwd(const NormProblem &p, void *ws, int sms, cudaStream_t s) {
     const Route rt = aligned(p) ? route(p, false) : kPlain;
     if (rt == kRows) {
         const RowPlan r = row_plan(p);
         const int vpl = (int)((p.C / p.G / Vec<T>::n + r.W - 1) / r.W);
         const dim3 grid = row_grid(p, r, sms, kFwdPerSm);
-        if (vpl == 1) return launch(norm_rows_fwd<T, 1, kGate>, grid, 0, false, s, p, r);
-        if (vpl == 2) return launch(norm_rows_fwd<T, 2, kGate>, grid, 0, false, s, p, r);
-        return launch(norm_rows_fwd<T, 4, kGate>, grid, 0, false, s, p, r);
+        if (vpl == 1) return launch(norm_rows_fwd<T, 1, kGate, kSilu>, grid, 0, false, s, p, r);
+        if (vpl == 2) return launch(norm_rows_fwd<T, 2, kGate, kSilu>, grid, 0, false, s, p, r);
+        return launch(norm_rows_fwd<T, 4, kGate, kSilu>, grid, 0, false, s, p, r);
     }
     if (rt == kMaps) {
         const MapPlan m = map_plan(p, sms);
@@ -856,12 +899,12 @@ cudaError_t run_fwd(const NormProblem &p, void *ws, int sms, cudaStream_t s) {
         if (e != cudaSuccess) return e;
         e = launch(norm_maps_combine, combine_grid(p), 0, true, s, p, m, (const Stat *)part, stat);
         if (e != cudaSuccess) return e;
-        return launch(norm_maps_apply<T, kGate>, map_grid(p, m), 0, true, s, p, m, (const float2 *)stat);
+        return launch(norm_maps_apply<T, kGate, kSilu>, map_grid(p, m), 0, true, s, p, m, (const float2 *)stat);
     }
     return launch(norm_plain_fwd<T>, dim3((unsigned)(p.N * p.G)), 0, false, s, p);
 }
 
-template <typename T, bool kGate>
+template <typename T, bool kGate, bool kSilu>
 cudaError_t run_bwd(const NormProblem &p, void *ws, int sms, cudaStream_t s) {
     const Route rt = aligned(p) ? route(p, true) : kPlain;
     const bool want = p.dw || p.db;
@@ -879,21 +922,21 @@ cudaError_t run_bwd(const NormProblem &p, void *ws, int sms, cudaStream_t s) {
         const dim3 grid = row_grid(p, r, sms, kBwdPerSm);
         parts = (int64_t)grid.x * r.rp;
         if (want) sums = static_cast<float *>(ws);
-        if (vpl == 1) e = launch(norm_rows_bwd<T, 1, kGate>, grid, 0, false, s, p, r, sums);
-        else if (vpl == 2) e = launch(norm_rows_bwd<T, 2, kGate>, grid, 0, false, s, p, r, sums);
-        else e = launch(norm_rows_bwd<T, 4, kGate>, grid, 0, false, s, p, r, sums);
+        if (vpl == 1) e = launch(norm_rows_bwd<T, 1, kGate, kSilu>, grid, 0, false, s, p, r, sums);
+        else if (vpl == 2) e = launch(norm_rows_bwd<T, 2, kGate, kSilu>, grid, 0, false, s, p, r, sums);
+        else e = launch(norm_rows_bwd<T, 4, kGate, kSilu>, grid, 0, false, s, p, r, sums);
     } else {
         const MapPlan m = map_plan(p, sms);
         float2 *part = static_cast<float2 *>(ws);
         parts = p.N * m.parts;
         float2 *means = reinterpret_cast<float2 *>(static_cast<char *>(ws) + stat_bytes(p, m, true));
         if (want) sums = reinterpret_cast<float *>(static_cast<char *>(ws) + stat_bytes(p, m, true) + mean_bytes(p));
-        const size_t smem = (size_t)kThreads * 2 * Vec<T>::n * sizeof(float);
-        e = launch(norm_maps_bwd_stats<T, kGate>, map_grid(p, m), smem, false, s, p, m, part, sums);
+        const size_t smem = (size_t)kThreads * (2 * Vec<T>::n + 4) * sizeof(float);
+        e = launch(norm_maps_bwd_stats<T, kGate, kSilu>, map_grid(p, m), smem, false, s, p, m, part, sums);
         if (e != cudaSuccess) return e;
         e = launch(norm_maps_bwd_combine, combine_grid(p), 0, true, s, p, m, (const float2 *)part, means);
         if (e != cudaSuccess) return e;
-        e = launch(norm_maps_bwd_apply<T, kGate>, map_grid(p, m), 0, true, s, p, m, (const float2 *)means);
+        e = launch(norm_maps_bwd_apply<T, kGate, kSilu>, map_grid(p, m), 0, true, s, p, m, (const float2 *)means);
     }
     if (e != cudaSuccess || !want) return e;
     return launch_n(norm_sum_parts, dim3((unsigned)((2 * p.C + 31) / 32)), kSumThreads, 0, false, s,
@@ -915,17 +958,23 @@ size_t norm_workspace_bytes(const NormProblem &p, bool backward, int num_sms) {
 }
 
 cudaError_t launch_norm_fwd(const NormProblem &p, void *ws, int num_sms, cudaStream_t s) {
-    if (p.io == 0)
-        return p.gate ? run_fwd<__nv_bfloat16, true>(p, ws, num_sms, s)
-                      : run_fwd<__nv_bfloat16, false>(p, ws, num_sms, s);
-    return p.gate ? run_fwd<float, true>(p, ws, num_sms, s) : run_fwd<float, false>(p, ws, num_sms, s);
+    using bf16 = __nv_bfloat16;
+    if (p.act == 1) {
+        if (p.io == 0) return p.gate ? run_fwd<bf16, true, true>(p, ws, num_sms, s) : run_fwd<bf16, false, true>(p, ws, num_sms, s);
+        return p.gate ? run_fwd<float, true, true>(p, ws, num_sms, s) : run_fwd<float, false, true>(p, ws, num_sms, s);
+    }
+    if (p.io == 0) return p.gate ? run_fwd<bf16, true, false>(p, ws, num_sms, s) : run_fwd<bf16, false, false>(p, ws, num_sms, s);
+    return p.gate ? run_fwd<float, true, false>(p, ws, num_sms, s) : run_fwd<float, false, false>(p, ws, num_sms, s);
 }
 
 cudaError_t launch_norm_bwd(const NormProblem &p, void *ws, int num_sms, cudaStream_t s) {
-    if (p.io == 0)
-        return p.gate ? run_bwd<__nv_bfloat16, true>(p, ws, num_sms, s)
-                      : run_bwd<__nv_bfloat16, false>(p, ws, num_sms, s);
-    return p.gate ? run_bwd<float, true>(p, ws, num_sms, s) : run_bwd<float, false>(p, ws, num_sms, s);
+    using bf16 = __nv_bfloat16;
+    if (p.act == 1) {
+        if (p.io == 0) return p.gate ? run_bwd<bf16, true, true>(p, ws, num_sms, s) : run_bwd<bf16, false, true>(p, ws, num_sms, s);
+        return p.gate ? run_bwd<float, true, true>(p, ws, num_sms, s) : run_bwd<float, false, true>(p, ws, num_sms, s);
+    }
+    if (p.io == 0) return p.gate ? run_bwd<bf16, true, false>(p, ws, num_sms, s) : run_bwd<bf16, false, false>(p, ws, num_sms, s);
+    return p.gate ? run_bwd<float, true, false>(p, ws, num_sms, s) : run_bwd<float, false, false>(p, ws, num_sms, s);
 }
 
 }  // namespace gla
