@@ -8,9 +8,10 @@
 //   rows : L = 1 and a group's channels fit the registers of a warp's lanes: one pass. A segment
 //          of W lanes (a power of two) owns one group and walks over entries, so weights and the
 //          channel sums of the backward pass stay in registers.
-//   maps : L > 1 (or wide groups): the positions of an entry are cut into parts, one CTA each;
-//          a first kernel leaves each part's statistics, a second one combines them and writes.
-//          The second reading of x comes from L2 when the tensor fits there.
+//   maps : L > 1 (or wide groups): the positions of an entry are cut into parts, one CTA each. Where
+//          they are few (cluster_plan), the parts are a cluster and one kernel does it all; else a
+//          first kernel leaves each part's statistics, a second one combines them and a third one
+//          writes. The second reading of x comes from registers or from L2 when the tensor fits there.
 //   plain: whatever does not come in whole 16-byte vectors of one group: a CTA per group.
 // Means and variances: where a group is in registers, the mean and then the squared deviations from
 // it. Else each thread takes the mean of its first vector as a pivot and sums the deviations from
@@ -18,6 +19,8 @@
 // (M2 = sum of squares - (sum)^2 / n loses digits only if the pivot is many standard deviations of
 // the thread's own values away from their mean, which a value among them cannot be.)
 #include <cuda_bf16.h>
+
+#include <atomic>
 
 #include "gla_internal.h"
 #include "norm.h"
@@ -653,6 +656,234 @@ norm_maps_bwd_apply(const __grid_constant__ NormProblem p, const MapPlan m, cons
     }
 }
 
+// ======================================================================= maps of a cluster
+// One kernel for maps that a cluster can hold: the CTAs of a cluster are the parts of one entry and
+// block of groups, and read each other's statistics from shared memory. Blocks are as narrow as a
+// 128-byte row allows, so that there are many; the last read of a peer is followed by an arrival
+// that every CTA awaits before it leaves.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+__device__ __forceinline__ float peer(const float *p, int rank) {
+    uint32_t at;
+    float v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(tc::smem_u32(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+    return v;
+}
+constexpr int kMostGroups = 8;      // of a cluster's block
+
+// The first kKeep vectors of a thread stay in registers from the statistics to the output; the rest
+// is read again (from L2).
+template <typename T, bool kGate, bool kSilu>
+__global__ void __launch_bounds__(kThreads, 3)
+norm_cluster_fwd(const __grid_constant__ NormProblem p, const MapPlan m) {
+    constexpr int V = Vec<T>::n, kKeep = 8;
+    __shared__ Stat sh[kThreads];
+    __shared__ Stat part[kMostGroups];
+    __shared__ float2 stat[kMostGroups];
+    const MapPos q = map_pos(p, m);
+    const int64_t c = (q.live ? q.v : 0) * V, first = q.l0 + q.ty;
+    const int count = q.live && first < q.l1 ? (int)((q.l1 - first + m.ry - 1) / m.ry) : 0;
+    const int64_t xs = m.ry * p.x_l, zs = m.ry * p.gate_l, ys = m.ry * p.C;
+    const T *xp = static_cast<const T *>(p.x) + (count ? q.n * p.x_n + first * p.x_l + c : 0);
+    uint4 xv[kKeep];
+#pragma unroll
+    for (int a = 0; a < kKeep; ++a) xv[a] = a < count ? *reinterpret_cast<const uint4 *>(xp + a * xs) : make_uint4(0, 0, 0, 0);
+    Stat s{0.f, 0.f, 0.f};
+    if (count) {
+        float2 f[V / 2], t1 = both(0.f), t2 = both(0.f);
+        Vec<T>::unpack(xv[0], f);
+        float2 t = f[0];
+#pragma unroll
+        for (int i = 1; i < V / 2; ++i) t = add2(t, f[i]);
+        const float pivot = (t.x + t.y) * (1.f / V);
+        auto add = [&](uint4 v) {
+            Vec<T>::unpack(v, f);
+#pragma unroll
+            for (int i = 0; i < V / 2; ++i) {
+                const float2 d = add2(f[i], both(-pivot));
+                t1 = add2(t1, d);
+                t2 = fma2(d, d, t2);
+            }
+        };
+#pragma unroll
+        for (int a = 0; a < kKeep; ++a)
+            if (a < count) add(xv[a]);
+#pragma unroll 4
+        for (int a = kKeep; a < count; ++a) add(*reinterpret_cast<const uint4 *>(xp + a * xs));
+        const float s1 = t1.x + t1.y, s2 = t2.x + t2.y, n = (float)count * V;
+        const float d = s1 / n;
+        s = Stat{n, pivot + d, fmaxf(fmaf(-s1, d, s2), 0.f)};
+        if (!(s2 < INFINITY)) s.m2 = s2;    // infinity or NaN (which fmaxf would drop)
+    }
+    sh[threadIdx.x] = s;
+    __syncthreads();
+    const int lane = threadIdx.x & 31, entries = m.nv * m.ry;
+    for (int g = threadIdx.x >> 5; g < m.groups; g += kWarps) {
+        Stat t{0.f, 0.f, 0.f};
+        for (int e = lane; e < entries; e += 32) t = merge(t, sh[e / m.nv * m.nvb + g * m.nv + e % m.nv]);
+        t = merge_lanes(t, 32);
+        if (lane == 0) part[g] = t;
+    }
+    cluster_arrive();
+    float2 w[V / 2], b[V / 2];
+    load_param(p.w, c, 1.f, w);
+    load_param(p.b, c, 0.f, b);
+    cluster_wait();
+    for (int g = threadIdx.x >> 5; g < m.groups; g += kWarps) {
+        Stat t{0.f, 0.f, 0.f};
+        if (lane < m.parts) t = Stat{peer(&part[g].n, lane), peer(&part[g].mean, lane), peer(&part[g].m2, lane)};
+        t = merge_lanes(t, 16);
+        const float rstd = 1.f / sqrtf(t.m2 / t.n + p.eps);
+        const int64_t gg = (int64_t)blockIdx.y * m.groups + g;
+        if (lane != 0) continue;
+        stat[g] = make_float2(t.mean, rstd);
+        if (blockIdx.x != 0 || gg >= p.G) continue;
+        if (p.mean) p.mean[q.n * p.G + gg] = t.mean;
+        if (p.rstd) p.rstd[q.n * p.G + gg] = rstd;
+    }
+    cluster_arrive();
+    __syncthreads();
+    if (count) {
+        const float2 st = stat[q.tx / m.nv];
+        const T *zp = static_cast<const T *>(p.gate) + (kGate ? q.n * p.gate_n + first * p.gate_l + c : 0);
+        T *yp = static_cast<T *>(p.y) + (q.n * p.L + first) * p.C + c;
+        auto write = [&](uint4 v, int a) {
+            float2 f[V / 2], z[V / 2];
+            Vec<T>::unpack(v, f);
+            if (kGate) Vec<T>::unpack(*reinterpret_cast<const uint4 *>(zp + a * zs), z);
+#pragma unroll
+            for (int i = 0; i < V / 2; ++i) {
+                const float2 u = fma2(mul2(add2(f[i], both(-st.x)), both(st.y)), w[i], b[i]);
+                f[i] = kGate ? mul2(u, act_of2<T, kSilu>(z[i], p.act)) : act_of2<T, kSilu>(u, p.act);
+            }
+            *reinterpret_cast<uint4 *>(yp + a * ys) = Vec<T>::pack(f);
+        };
+#pragma unroll
+        for (int a = 0; a < kKeep; ++a)
+            if (a < count) write(xv[a], a);
+#pragma unroll 2
+        for (int a = kKeep; a < count; ++a) write(*reinterpret_cast<const uint4 *>(xp + a * xs), a);
+    }
+    cluster_wait();
+}
+
+// sums: [N][2][C] where there are several entries; for one, dw and db come from here.
+template <typename T, bool kGate, bool kSilu>
+__global__ void __launch_bounds__(kThreads)
+norm_cluster_bwd(const __grid_constant__ NormProblem p, const MapPlan m, float *sums) {
+    constexpr int V = Vec<T>::n;
+    __shared__ float2 sh[kThreads];
+    __shared__ float2 part[kMostGroups], means[kMostGroups];
+    extern __shared__ __align__(16) float ch[];     // [threads][2 V + 4] channel sums of the position slots
+    float *cta = ch + kThreads * (2 * V + 4);       // [nvb][2 V], those of the CTA
+    const MapPos q = map_pos(p, m);
+    const int nv = m.nv, lane = threadIdx.x & 31;
+    const int64_t c = (q.live ? q.v : 0) * V, first = q.l0 + q.ty;
+    const int count = q.live && first < q.l1 ? (int)((q.l1 - first + m.ry - 1) / m.ry) : 0;
+    const T *xp = static_cast<const T *>(p.x) + (count ? q.n * p.x_n + first * p.x_l + c : 0);
+    const T *dp = static_cast<const T *>(p.dy) + (count ? q.n * p.dy_n + first * p.dy_l + c : 0);
+    const T *zp = static_cast<const T *>(p.gate) + (kGate && count ? q.n * p.gate_n + first * p.gate_l + c : 0);
+    const int64_t xs = m.ry * p.x_l, ds = m.ry * p.dy_l, zs = m.ry * p.gate_l, os = m.ry * p.C;
+    float2 w[V / 2], b[V / 2];
+    load_param(p.w, c, 1.f, w);
+    load_param(p.b, c, 0.f, b);
+    const int64_t at = q.n * p.G + (q.live ? q.v / nv : 0);
+    const float mean = p.mean[at], rstd = p.rstd[at];
+    {
+        float2 dw[V / 2], db[V / 2], t1 = both(0.f), t2 = both(0.f);
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) dw[i] = db[i] = both(0.f);
+#pragma unroll 2
+        for (int a = 0; a < count; ++a) {
+            float2 x[V / 2], d[V / 2], z[V / 2];
+            Vec<T>::unpack(*reinterpret_cast<const uint4 *>(xp + a * xs), x);
+            Vec<T>::unpack(*reinterpret_cast<const uint4 *>(dp + a * ds), d);
+            if (kGate) Vec<T>::unpack(*reinterpret_cast<const uint4 *>(zp + a * zs), z);
+            grad_vec<T, kGate, kSilu>(x, d, z, w, b, mean, rstd, p.act);
+#pragma unroll
+            for (int i = 0; i < V / 2; ++i) {
+                dw[i] = fma2(d[i], x[i], dw[i]);
+                db[i] = add2(db[i], d[i]);
+                d[i] = mul2(d[i], w[i]);
+                t1 = add2(t1, d[i]);
+                t2 = fma2(d[i], x[i], t2);
+            }
+        }
+        sh[threadIdx.x] = make_float2(t1.x + t1.y, t2.x + t2.y);
+        float2 *mine = reinterpret_cast<float2 *>(ch + threadIdx.x * (2 * V + 4));
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) {
+            mine[i] = dw[i];
+            mine[V / 2 + i] = db[i];
+        }
+    }
+    __syncthreads();
+    for (int g = threadIdx.x >> 5; g < m.groups; g += kWarps) {
+        float u = 0.f, v = 0.f;
+        for (int e = lane; e < nv * m.ry; e += 32) {
+            const float2 t = sh[e / nv * m.nvb + g * nv + e % nv];
+            u += t.x;
+            v += t.y;
+        }
+        u = sum_lanes(u, 32);
+        v = sum_lanes(v, 32);
+        if (lane == 0) part[g] = make_float2(u, v);
+    }
+    const bool want = p.dw || p.db;
+    if (want)
+        for (int e = threadIdx.x; e < m.nvb * 2 * V; e += kThreads) {
+            const int tx = e / (2 * V), i = e % (2 * V);
+            float t = 0.f;
+            for (int y = 0; y < m.ry; ++y) t += ch[(y * m.nvb + tx) * (2 * V + 4) + i];
+            cta[e] = t;
+        }
+    cluster_arrive();
+    cluster_wait();
+    const float inv = 1.f / ((float)p.L * (float)(nv * V));
+    for (int g = threadIdx.x >> 5; g < m.groups; g += kWarps) {
+        float u = 0.f, v = 0.f;
+        if (lane < m.parts) {
+            u = peer(&part[g].x, lane);
+            v = peer(&part[g].y, lane);
+        }
+        u = sum_lanes(u, 16);
+        v = sum_lanes(v, 16);
+        if (lane == 0) means[g] = make_float2(u * inv, v * inv);
+    }
+    if (want)       // the channels are shared out among the CTAs
+        for (int e = blockIdx.x * kThreads + threadIdx.x; e < m.nvb * 2 * V; e += m.parts * kThreads) {
+            const int i = e % (2 * V);
+            const int64_t k = ((int64_t)blockIdx.y * m.nvb + e / (2 * V)) * V + i % V;
+            if (k >= p.C) continue;
+            float t = 0.f;
+            for (int r = 0; r < m.parts; ++r) t += peer(&cta[e], r);
+            float *to = sums ? sums + (q.n * 2 + (i >= V)) * p.C : i < V ? p.dw : p.db;
+            if (to) to[k] = t;
+        }
+    cluster_arrive();
+    __syncthreads();
+    if (count) {
+        const float2 mm = means[q.tx / nv];
+        T *op = static_cast<T *>(p.dx) + (q.n * p.L + first) * p.C + c;
+        T *gp = static_cast<T *>(p.dgate) + (kGate ? (q.n * p.L + first) * p.C + c : 0);
+#pragma unroll 2
+        for (int a = 0; a < count; ++a) {
+            float2 x[V / 2], d[V / 2], z[V / 2];
+            Vec<T>::unpack(*reinterpret_cast<const uint4 *>(xp + a * xs), x);
+            Vec<T>::unpack(*reinterpret_cast<const uint4 *>(dp + a * ds), d);
+            if (kGate) Vec<T>::unpack(*reinterpret_cast<const uint4 *>(zp + a * zs), z);
+            grad_vec<T, kGate, kSilu>(x, d, z, w, b, mean, rstd, p.act);
+#pragma unroll
+            for (int i = 0; i < V / 2; ++i)
+                x[i] = mul2(both(rstd), fma2(x[i], both(-mm.y), fma2(d[i], w[i], both(-mm.x))));
+            *reinterpret_cast<uint4 *>(op + a * os) = Vec<T>::pack(x);
+            if (kGate) *reinterpret_cast<uint4 *>(gp + a * os) = Vec<T>::pack(z);
+        }
+    }
+    cluster_wait();
+}
+
 // dw, db: the partial sums added in order. Thread (channel, slice): 32 channels, 32 slices of parts.
 constexpr int kSumThreads = 1024;
 __global__ void __launch_bounds__(kSumThreads)
@@ -848,6 +1079,58 @@ dim3 map_grid(const NormProblem &p, const MapPlan &m) {
     return dim3((unsigned)m.parts, (unsigned)((p.C / vec_of(p) + m.nvb - 1) / m.nvb), (unsigned)p.N);
 }
 
+// The plan of a cluster of up to 16 CTAs, each thread with at least four rounds of positions if it
+// is larger than one, and all clusters on the GPU at once; false where that leaves a thread more
+// than kMostRounds (half of them backward). Measured, clusters against three kernels, per call:
+// 3 x 4095 x 512 21 us against 28, 1 x 16384 x 512 22 against 37, backward of 4 x 4096 x 512 26
+// against 33; beyond the rule 64 x 300 x 512 37 against 27, 1 x 262144 x 64 211 against 31, backward
+// of 1 x 16384 x 1024 79 against 59.
+constexpr int kMostCluster = 16, kMostRounds = 32;
+bool cluster_plan(const NormProblem &p, int sms, bool backward, MapPlan *out) {
+    const int64_t V = vec_of(p), nv = p.C / p.G / V;
+    MapPlan m;
+    m.nv = (int)nv;
+    m.cols = (int)(p.C / V);
+    m.groups = (int)min(max((int64_t)1, 8 / nv), p.G);
+    m.nvb = m.groups * m.nv;
+    m.ry = kThreads / m.nvb;
+    m.parts = 1;
+    const int64_t blocks = (m.cols + m.nvb - 1) / m.nvb * p.N, most = 3 * (int64_t)sms;
+    while (m.parts < kMostCluster && (int64_t)m.parts * m.ry * 4 < p.L && blocks * m.parts * 2 <= most) m.parts *= 2;
+    const int64_t len = (p.L + m.parts - 1) / m.parts;
+    m.len = (int)len;
+    *out = m;
+    return blocks <= most && (len + m.ry - 1) / m.ry <= (backward ? kMostRounds / 2 : kMostRounds);
+}
+// Not the portable cluster size: asked for once for each kernel.
+template <typename... A>
+cudaError_t launch_cluster(void (*kernel)(A...), std::atomic<uint64_t> &done, dim3 grid, size_t smem, cudaStream_t s,
+                           A... args) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = uint64_t(1) << (dev & 63);
+    if (!(done.load(std::memory_order_acquire) & bit)) {
+        e = cudaFuncSetAttribute((const void *)kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+        done.fetch_or(bit, std::memory_order_release);
+    }
+    cudaLaunchAttribute cl[1];
+    cl[0].id = cudaLaunchAttributeClusterDimension;
+    cl[0].val.clusterDim.x = grid.x;
+    cl[0].val.clusterDim.y = cl[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = cl;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, kernel, args...);
+    if (e == cudaSuccess) count_launches(1);
+    return e;
+}
+
 size_t round256(size_t n) { return (n + 255) & ~size_t(255); }
 constexpr int kFwdPerSm = 5, kBwdPerSm = 2;
 dim3 combine_grid(const NormProblem &p) { return dim3((unsigned)((p.N * p.G + kWarps - 1) / kWarps)); }
@@ -892,7 +1175,12 @@ cudaError_t run_fwd(const NormProblem &p, void *ws, int sms, cudaStream_t s) {
         return launch(norm_rows_fwd<T, 4, kGate, kSilu>, grid, 0, false, s, p, r);
     }
     if (rt == kMaps) {
-        const MapPlan m = map_plan(p, sms);
+        MapPlan m;
+        if (cluster_plan(p, sms, false, &m)) {
+            static std::atomic<uint64_t> done{0};
+            return launch_cluster(norm_cluster_fwd<T, kGate, kSilu>, done, map_grid(p, m), 0, s, p, m);
+        }
+        m = map_plan(p, sms);
         Stat *part = static_cast<Stat *>(ws);
         float2 *stat = reinterpret_cast<float2 *>(static_cast<char *>(ws) + stat_bytes(p, m, false));
         cudaError_t e = launch(norm_maps_stats<T>, map_grid(p, m), 0, false, s, p, m, part);
@@ -926,7 +1214,17 @@ cudaError_t run_bwd(const NormProblem &p, void *ws, int sms, cudaStream_t s) {
         else if (vpl == 2) e = launch(norm_rows_bwd<T, 2, kGate, kSilu>, grid, 0, false, s, p, r, sums);
         else e = launch(norm_rows_bwd<T, 4, kGate, kSilu>, grid, 0, false, s, p, r, sums);
     } else {
-        const MapPlan m = map_plan(p, sms);
+        MapPlan m;
+        if (cluster_plan(p, sms, true, &m)) {
+            static std::atomic<uint64_t> done{0};
+            if (want && p.N > 1) sums = static_cast<float *>(ws);
+            const size_t smem = (size_t)(kThreads * (2 * Vec<T>::n + 4) + m.nvb * 2 * Vec<T>::n) * sizeof(float);
+            e = launch_cluster(norm_cluster_bwd<T, kGate, kSilu>, done, map_grid(p, m), smem, s, p, m, sums);
+            if (e != cudaSuccess || !sums) return e;
+            return launch_n(norm_sum_parts, dim3((unsigned)((2 * p.C + 31) / 32)), kSumThreads, 0, false, s,
+                            (const float *)sums, (int)p.N, p.C, p.dw, p.db);
+        }
+        m = map_plan(p, sms);
         float2 *part = static_cast<float2 *>(ws);
         parts = p.N * m.parts;
         float2 *means = reinterpret_cast<float2 *>(static_cast<char *>(ws) + stat_bytes(p, m, true));
@@ -953,7 +1251,9 @@ size_t norm_workspace_bytes(const NormProblem &p, bool backward, int num_sms) {
         const RowPlan r = row_plan(p);
         return (size_t)row_grid(p, r, num_sms, kBwdPerSm).x * r.rp * 2 * p.C * sizeof(float);
     }
-    const MapPlan m = map_plan(p, num_sms);
+    MapPlan m;
+    if (cluster_plan(p, num_sms, backward, &m)) return backward && p.N > 1 ? (size_t)p.N * 2 * p.C * sizeof(float) : 0;
+    m = map_plan(p, num_sms);
     return stat_bytes(p, m, backward) + mean_bytes(p) + (backward ? (size_t)(p.N * m.parts) * 2 * p.C * sizeof(float) : 0);
 }
 
