@@ -1,22 +1,29 @@
 // Linear attention with one decay per head, token by token in fp32 on CUDA cores: every dtype,
 // head dimension and length, and the route of short bf16 sequences.
 //
-// The columns of the state are independent (out_t[z] needs S[:, z] alone), so a CTA owns 16 of
-// them for one head and walks the tokens with its part of S in registers: thread (column, row
-// group) holds RPT rows of one column. A token costs it RPT multiply-adds for the update and
-// RPT for the read; nothing but the state's own multiply-add chain is serial, so eight tokens are
-// unrolled, and their sums over the 8 row groups of a column take 7 shuffles together. x, y and z
-// are staged as fp32 in shared memory TB tokens at a time, the next tile being loaded meanwhile.
+// The columns of the state are independent (out_t[z] needs S[:, z] alone), so a CTA owns 16 NC of
+// them for one head and walks the tokens with its part of S in registers: a thread holds RPT rows of
+// NC columns (packed in pairs of rows), 8 threads the rows of a column. A token costs it three
+// multiply-adds per element of S; with one column per thread the reads of x and y from shared memory
+// took three times as long as these. Nothing but the state's own multiply-add chain is serial. The
+// sums over the 8 row groups are formed for 8 (token, column) pairs at once, in 7 shuffles. x, y and
+// z are staged as fp32 in shared memory TB tokens at a time, the next tile being loaded meanwhile.
+//
+// A walk is serial, so where long sequences give the SMs few CTAs it is cut into segments: one kernel
+// walks all but the last for their end states alone (from zero, but the first), a second one makes
+// start states of them,
+//     S(1) = E(0),  S(j + 1) = l^len S(j) + E(j),
+// and a third one walks all segments for the outputs (one head of 16384 tokens: 2050 us -> 122).
 #include <cuda_bf16.h>
 
 #include "gla_internal.h"
 #include "hda_internal.h"
+#include "tc_ptx.cuh"
 
 namespace gla {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kCols = 16;          // state columns of a CTA
 constexpr float kSlow = -0.5f;     // log-decays above it use l - 1 (see below)
 
 template <typename T>
@@ -57,15 +64,15 @@ struct Tile {
     static constexpr int kPer = (kVecs + kThreads - 1) / kThreads;
     uint4 r[kPer];
     // base: this head's first element; row i of the walk is token (rev ? T - 1 - i : i)
-    __device__ __forceinline__ void load(const T *base, int64_t ts, int64_t i0, int64_t Tn, bool rev,
-                                         int width) {
+    __device__ __forceinline__ void load(const T *base, int64_t ts, int64_t i0, int64_t end, int64_t Tn,
+                                         bool rev, int width) {
 #pragma unroll
         for (int a = 0; a < kPer; ++a) {
             const int e = threadIdx.x + a * kThreads;
             const int row = e / (W / V), col = (e % (W / V)) * V;
             const int64_t i = i0 + row;
             r[a] = make_uint4(0, 0, 0, 0);
-            if (e < kVecs && i < Tn && col < width)
+            if (e < kVecs && i < end && col < width)
                 r[a] = *reinterpret_cast<const uint4 *>(base + (rev ? Tn - 1 - i : i) * ts + col);
         }
     }
@@ -78,22 +85,31 @@ struct Tile {
     }
 };
 
-template <typename T, int RPT, int TB>
+struct Segs {
+    int n, len;             // segments and their tokens
+    int zblocks;            // CTAs of a segment
+    float2 *E;              // end states: [map][head][segment 0 .. n - 2][CTA][pair][thread]
+};
+
+// kState: the segments' end states only.
+template <typename T, int RPT, int NC, int TB, bool kState>
 __global__ void __launch_bounds__(kThreads)
-hda_exact_kernel(const __grid_constant__ HdaProblem p) {
+hda_exact_kernel(const __grid_constant__ HdaProblem p, const Segs sg) {
     constexpr int W = 8 * RPT;                 // rows of the state, padded
-    __shared__ __align__(16) float xs[2][TB * W], ys[2][TB * W], zs[2][TB * kCols];
-    __shared__ float os[TB][kCols];
+    constexpr int kCols = 16 * NC, G = 8 / NC; // columns of the CTA; tokens at a time
+    __shared__ __align__(16) float xs[kState ? 1 : 2][kState ? 4 : TB * W], ys[2][TB * W], zs[2][TB * kCols];
+    __shared__ float os[kState ? 1 : TB][kCols];
+    if (kState) tc::pdl_launch_dependents();
     const HdaLin &m = p.lin[blockIdx.z];
-    const int z0 = blockIdx.x * kCols;
+    const int zb = blockIdx.x % sg.zblocks, seg = blockIdx.x / sg.zblocks, z0 = zb * kCols;
     if (z0 >= m.Dz) return;
+    const int64_t begin = (int64_t)seg * sg.len, end = min(begin + sg.len, p.T);
     const int64_t bh = blockIdx.y, b = bh / p.H, h = bh % p.H;
     const int lane = threadIdx.x & 31;
-    // lanes 8 c .. 8 c + 7 of a warp are the row groups of one column; a row group's rows come
+    // lanes 8 c .. 8 c + 7 of a warp are the row groups of NC columns; a row group's rows come
     // in fours, interleaved with the other groups', so that 16-byte reads of x and y meet no
     // bank twice
-    const int rg = lane & 7, col = (threadIdx.x >> 5) * 4 + (lane >> 3);
-    const bool in = z0 + col < m.Dz;
+    const int rg = lane & 7, col = ((threadIdx.x >> 5) * 4 + (lane >> 3)) * NC;
     auto row_of = [&](int k) { return (k >> 2) * 32 + rg * 4 + (k & 3); };
     auto head = [&](const HdaTensor &t) {
         return static_cast<const T *>(t.p) + b * t.b + (h / (p.H / t.heads)) * t.h;
@@ -102,14 +118,24 @@ hda_exact_kernel(const __grid_constant__ HdaProblem p) {
     const float g = p.decay[h];
     const bool rev = m.rev != 0;
 
-    float s[RPT];
+    float2 s[NC][RPT / 2];      // rows 2 k, 2 k + 1 of the thread's
 #pragma unroll
-    for (int k = 0; k < RPT; ++k) {
-        const int r = row_of(k), c = z0 + col;
-        s[k] = 0.f;
-        if (m.init && in && r < m.Dx)
-            s[k] = m.init[bh * m.Dx * m.Dz + (m.init_t ? (int64_t)c * m.Dx + r
-                                                       : (int64_t)r * m.Dz + c)];
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int k = 0; k < RPT; ++k) {
+            const int r = row_of(k), z = z0 + col + c;
+            float v = 0.f;
+            if (m.init && seg == 0 && z < m.Dz && r < m.Dx)
+                v = m.init[bh * m.Dx * m.Dz + (m.init_t ? (int64_t)z * m.Dx + r : (int64_t)r * m.Dz + z)];
+            (k & 1 ? s[c][k / 2].y : s[c][k / 2].x) = v;
+        }
+    constexpr int kPer = NC * RPT / 2;      // pairs of a thread
+    float2 *E = sg.E + (((blockIdx.z * p.B * p.H + bh) * (sg.n - 1)) * sg.zblocks + zb) * (kPer * kThreads) + threadIdx.x;
+    const int64_t e_seg = (int64_t)sg.zblocks * (kPer * kThreads);
+    if (!kState && seg > 0) {
+        tc::pdl_wait_prerequisites();
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) s[k / (RPT / 2)][k % (RPT / 2)] = E[(seg - 1) * e_seg + k * kThreads];
     }
 
     // Reversed passes start from a state that already carries the step's decay: their first
@@ -121,73 +147,78 @@ hda_exact_kernel(const __grid_constant__ HdaProblem p) {
     Tile<T, TB, W> tx, ty;
     Tile<T, TB, kCols> tz;
     const int zw = min(kCols, m.Dz - z0);
-    tx.load(xp, m.x.t, 0, p.T, rev, m.Dx);
-    ty.load(yp, m.y.t, 0, p.T, rev, m.Dx);
-    tz.load(zp, m.z.t, 0, p.T, rev, zw);
+    if (!kState) tx.load(xp, m.x.t, begin, end, p.T, rev, m.Dx);
+    ty.load(yp, m.y.t, begin, end, p.T, rev, m.Dx);
+    tz.load(zp, m.z.t, begin, end, p.T, rev, zw);
     int buf = 0;
-    for (int64_t i0 = 0; i0 < p.T; i0 += TB, buf ^= 1) {
-        tx.store(xs[buf]);
+    for (int64_t i0 = begin; i0 < end; i0 += TB, buf ^= 1) {
+        if (!kState) tx.store(xs[buf]);
         ty.store(ys[buf]);
         tz.store(zs[buf]);
         __syncthreads();
-        if (i0 + TB < p.T) {
-            tx.load(xp, m.x.t, i0 + TB, p.T, rev, m.Dx);
-            ty.load(yp, m.y.t, i0 + TB, p.T, rev, m.Dx);
-            tz.load(zp, m.z.t, i0 + TB, p.T, rev, zw);
+        if (i0 + TB < end) {
+            if (!kState) tx.load(xp, m.x.t, i0 + TB, end, p.T, rev, m.Dx);
+            ty.load(yp, m.y.t, i0 + TB, end, p.T, rev, m.Dx);
+            tz.load(zp, m.z.t, i0 + TB, end, p.T, rev, zw);
         }
-        const int nt = (int)min((int64_t)TB, p.T - i0);
+        const int nt = (int)min((int64_t)TB, end - i0);
         auto walk = [&](auto is_slow) {
 #pragma unroll 1
-            for (int i8 = 0; i8 < nt; i8 += 8) {
+            for (int i8 = 0; i8 < nt; i8 += G) {
                 float acc[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    acc[i] = 0.f;
-                    if (i8 + i >= nt) continue;
-                    const float zt = m.a_in * zs[buf][(i8 + i) * kCols + col];
-                    const bool first = rev && i0 == 0 && i8 + i == 0;
-                    const float f = first ? (is_slow ? 0.f : 1.f) : (is_slow ? lm1 : lam);
-                    float part[2] = {0.f, 0.f};
+                for (int i = 0; i < G; ++i) {
+                    // (no branch: the loads of later tokens are to be issued ahead. A token past the
+                    // end is all zeros and applies no decay.)
+                    float zt[NC];
+#pragma unroll
+                    for (int c = 0; c < NC; ++c) zt[c] = m.a_in * zs[buf][(i8 + i) * kCols + col + c];
+                    const bool none = i8 + i >= nt || (rev && i0 + i8 + i == 0);
+                    const float f = none ? (is_slow ? 0.f : 1.f) : (is_slow ? lm1 : lam);
+                    const float2 ff = make_float2(f, f);
+                    float2 part[NC];
+#pragma unroll
+                    for (int c = 0; c < NC; ++c) part[c] = make_float2(0.f, 0.f);
 #pragma unroll
                     for (int k4 = 0; k4 < RPT / 4; ++k4) {
                         const float4 y4 =
                             *reinterpret_cast<const float4 *>(&ys[buf][(i8 + i) * W + row_of(4 * k4)]);
-                        const float4 x4 =
-                            *reinterpret_cast<const float4 *>(&xs[buf][(i8 + i) * W + row_of(4 * k4)]);
-                        const float yv[4] = {y4.x, y4.y, y4.z, y4.w}, xv[4] = {x4.x, x4.y, x4.z, x4.w};
+                        const float4 x4 = kState ? y4 : *reinterpret_cast<const float4 *>(
+                                                            &xs[buf][(i8 + i) * W + row_of(4 * k4)]);
+                        const float2 yv[2] = {make_float2(y4.x, y4.y), make_float2(y4.z, y4.w)};
+                        const float2 xv[2] = {make_float2(x4.x, x4.y), make_float2(x4.z, x4.w)};
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            float &sk = s[4 * k4 + e];
-                            sk = is_slow ? fmaf(f, sk, fmaf(yv[e], zt, sk)) : fmaf(f, sk, yv[e] * zt);
-                            part[e & 1] = fmaf(xv[e], sk, part[e & 1]);
-                        }
+                        for (int e = 0; e < 2; ++e)
+#pragma unroll
+                            for (int c = 0; c < NC; ++c) {
+                                float2 &sk = s[c][2 * k4 + e];
+                                const float2 zz = make_float2(zt[c], zt[c]);
+                                sk = is_slow ? tc::fma2(ff, sk, tc::fma2(yv[e], zz, sk))
+                                             : tc::fma2(ff, sk, tc::mul2(yv[e], zz));
+                                if (!kState) part[c] = tc::fma2(xv[e], sk, part[c]);
+                            }
                     }
-                    acc[i] = part[0] + part[1];
-                }
-                // sums over the 8 row groups, of 8 tokens at once: each step halves the tokens a lane
-                // holds, and lane rg is left with token rg
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const bool up = rg & 4;
-                    const float keep = up ? acc[i + 4] : acc[i], give = up ? acc[i] : acc[i + 4];
-                    acc[i] = keep + __shfl_xor_sync(0xffffffffu, give, 4);
+                    for (int c = 0; c < NC; ++c) acc[i * NC + c] = part[c].x + part[c].y;
                 }
+                // sums over the 8 row groups, of 8 values at once: each step halves the values a lane
+                // holds, and lane rg is left with value rg
+                if constexpr (!kState) {
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const bool up = rg & 2;
-                    const float keep = up ? acc[i + 2] : acc[i], give = up ? acc[i] : acc[i + 2];
-                    acc[i] = keep + __shfl_xor_sync(0xffffffffu, give, 2);
+                    for (int n = 4; n > 0; n >>= 1)
+#pragma unroll
+                        for (int i = 0; i < n; ++i) {
+                            const bool up = rg & n;
+                            const float keep = up ? acc[i + n] : acc[i], give = up ? acc[i] : acc[i + n];
+                            acc[i] = keep + __shfl_xor_sync(0xffffffffu, give, n);
+                        }
+                    os[i8 + rg / NC][col + rg % NC] = m.a_out * acc[0];
                 }
-                {
-                    const bool up = rg & 1;
-                    const float keep = up ? acc[1] : acc[0], give = up ? acc[0] : acc[1];
-                    acc[0] = keep + __shfl_xor_sync(0xffffffffu, give, 1);
-                }
-                os[i8 + rg][col] = m.a_out * acc[0];
             }
         };
         if (slow) walk(std::true_type{});
         else walk(std::false_type{});
+        if (kState) continue;       // (the next tile goes to the other buffer)
         __syncthreads();
         for (int e = threadIdx.x; e < nt * kCols; e += kThreads) {
             const int i = e / kCols, c = e % kCols;
@@ -198,15 +229,46 @@ hda_exact_kernel(const __grid_constant__ HdaProblem p) {
             else put(static_cast<T *>(m.out) + at, os[i][c]);
         }
     }
-    if (m.fin && in) {
+    if (kState) {
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) E[seg * e_seg + k * kThreads] = s[k / (RPT / 2)][k % (RPT / 2)];
+        return;
+    }
+    if (!m.fin || seg != sg.n - 1) return;
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
 #pragma unroll
         for (int k = 0; k < RPT; ++k) {
-            const int r = row_of(k), c = z0 + col;
-            float v = s[k];
+            const int r = row_of(k), z = z0 + col + c;
+            float v = k & 1 ? s[c][k / 2].y : s[c][k / 2].x;
             if (rev && p.T > 0) v = slow ? fmaf(lm1, v, v) : lam * v;
-            if (r < m.Dx)
-                m.fin[bh * m.Dx * m.Dz + (m.fin_t ? (int64_t)c * m.Dx + r
-                                                  : (int64_t)r * m.Dz + c)] = v;
+            if (z < m.Dz && r < m.Dx)
+                m.fin[bh * m.Dx * m.Dz + (m.fin_t ? (int64_t)z * m.Dx + r : (int64_t)r * m.Dz + z)] = v;
+        }
+}
+
+// E(j) -> S(j + 1), in place: a thread takes one pair of values through all segments.
+constexpr int kScanBatch = 8;
+__global__ void __launch_bounds__(kThreads)
+hda_exact_scan_kernel(const float *__restrict__ decay, int64_t H, const Segs sg, int64_t per_seg, int64_t pairs) {
+    tc::pdl_launch_dependents();
+    const int64_t e = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    if (e >= pairs) return;
+    const int64_t mbh = e / per_seg;        // map and head
+    const float f = decay_pow(decay[mbh % H], (float)sg.len);
+    float2 *E = sg.E + mbh * (sg.n - 1) * per_seg + e % per_seg;
+    tc::pdl_wait_prerequisites();
+    float2 s = make_float2(0.f, 0.f);
+    for (int j0 = 0; j0 < sg.n - 1; j0 += kScanBatch) {
+        float2 v[kScanBatch];
+#pragma unroll
+        for (int j = 0; j < kScanBatch; ++j)
+            if (j0 + j < sg.n - 1) v[j] = E[(j0 + j) * per_seg];
+#pragma unroll
+        for (int j = 0; j < kScanBatch; ++j) {
+            if (j0 + j >= sg.n - 1) break;
+            s = j0 + j == 0 ? v[j] : tc::fma2(make_float2(f, f), s, v[j]);
+            E[(j0 + j) * per_seg] = s;
         }
     }
 }
@@ -238,13 +300,87 @@ __global__ void hda_share_kernel(HdaShare a, HdaShare b, HdaShare c, int64_t BT,
     }
 }
 
-template <typename T>
-cudaError_t run_exact(const HdaProblem &p, cudaStream_t s) {
-    int dx = 0, dz = 0;
+constexpr int kTile = 16, kMostSegs = 128;
+
+void exact_dims(const HdaProblem &p, int &dx, int &dz) {
+    dx = dz = 0;
     for (int i = 0; i < p.n; ++i) {
         dx = max(dx, p.lin[i].Dx);
         dz = max(dz, p.lin[i].Dz);
     }
+}
+
+struct ExactPlan {
+    int rows, cols;         // of S in a thread
+    Segs g;
+};
+
+// Segments of a sequence, and one column of S per thread or kWide (4; with more than 128 rows, 2): one
+// is faster for a CTA by itself, four read x and y once for four times the columns. The cost of each
+// in ns, as measured at 128 rows (one column and four): the token of a lone CTA 122 and 270; as long
+// as an SM's CTAs are fewer than 1.2 and 1.9, it does not depend on them, then it grows in
+// proportion; the first kernel's tokens 0.7 of that; 6 us for the two kernels more.
+ExactPlan exact_plan(const HdaProblem &p, int splits, int sms) {
+    int dx, dz;
+    exact_dims(p, dx, dz);
+    ExactPlan best{};
+    best.rows = dx <= 64 ? 8 : dx <= 128 ? 16 : 32;
+    double least = 0;
+    for (int wide = 0; wide < 2; ++wide) {
+        const int cols = wide ? (dx <= 128 ? 4 : 2) : 1, zblocks = (dz + 16 * cols - 1) / (16 * cols);
+        const double ctas = (double)(p.B * p.H * p.n) * zblocks, token = wide ? 270 : 122, share = wide ? 1.9 : 1.2;
+        int most = (int)min(p.T / (2 * kTile), (int64_t)kMostSegs);
+        if (p.B * p.H > 65535 || p.T > (int64_t)1 << 30) most = 1;
+        if (splits > 0) most = min(splits, kMostSegs);
+        for (int n = splits > 0 ? most : 1; n <= max(most, 1); ++n) {
+            const double walk = token * (double)p.T / n * max(1.0, ctas * n / (share * sms));
+            const double cost = n == 1 ? walk : 1.7 * walk + 6000.0;
+            if (least > 0 && cost >= least) continue;
+            least = cost;
+            best.cols = cols;
+            best.g.n = n;
+            best.g.zblocks = zblocks;
+        }
+    }
+    const int64_t len = (p.T + best.g.n - 1) / best.g.n;
+    best.g.len = best.g.n == 1 ? (int)min(len, (int64_t)1 << 30) : (int)((len + kTile - 1) / kTile * kTile);
+    if (best.g.n > 1) best.g.n = (int)max((int64_t)1, (p.T + best.g.len - 1) / best.g.len);
+    return best;
+}
+int64_t pairs_per_segment(const ExactPlan &e) { return (int64_t)e.g.zblocks * e.rows * e.cols / 2 * kThreads; }
+
+template <typename T, int RPT, int NC, int TB>
+cudaError_t launch_walk(const HdaProblem &p, const Segs &g, cudaStream_t s) {
+    dim3 grid(g.zblocks * g.n, (unsigned)(p.B * p.H), p.n);
+    cudaLaunchAttribute pdl[1];
+    pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    pdl[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = s;
+    cfg.attrs = pdl;
+    if (g.n > 1) {
+        cfg.gridDim = dim3(g.zblocks * (g.n - 1), grid.y, grid.z);
+        cudaError_t e = cudaLaunchKernelEx(&cfg, hda_exact_kernel<T, RPT, NC, TB, true>, p, g);
+        if (e != cudaSuccess) return e;
+        cfg.numAttrs = 1;
+        const int64_t per_seg = (int64_t)g.zblocks * (RPT * NC / 2) * kThreads, pairs = p.n * p.B * p.H * per_seg;
+        cfg.gridDim = dim3((unsigned)((pairs + kThreads - 1) / kThreads));
+        e = cudaLaunchKernelEx(&cfg, hda_exact_scan_kernel, p.decay, p.H, g, per_seg, pairs);
+        if (e != cudaSuccess) return e;
+        count_launches(2);
+    }
+    cfg.gridDim = grid;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, hda_exact_kernel<T, RPT, NC, TB, false>, p, g);
+    if (e == cudaSuccess) count_launches(1);
+    return e;
+}
+
+template <typename T>
+cudaError_t run_exact(const HdaProblem &p, int splits, int sms, void *ws, cudaStream_t s) {
+    ExactPlan plan = exact_plan(p, splits, sms);
+    const Segs &g = plan.g;
+    plan.g.E = static_cast<float2 *>(ws);
     // the batch entries are cut so that the grid's y dimension stays within its limit
     const int64_t most = 65535 / p.H > 0 ? 65535 / p.H : 1;
     for (int64_t b0 = 0; b0 < p.B; b0 += most) {
@@ -258,21 +394,26 @@ cudaError_t run_exact(const HdaProblem &p, cudaStream_t s) {
             if (m.fin) m.fin += st;
             m.out = static_cast<char *>(m.out) + ot * (m.out_f32 ? 4 : (int64_t)sizeof(T));
         }
-        const dim3 grid((dz + kCols - 1) / kCols, (unsigned)(c.B * p.H), p.n);
-        if (dx <= 64) hda_exact_kernel<T, 8, 16><<<grid, kThreads, 0, s>>>(c);
-        else if (dx <= 128) hda_exact_kernel<T, 16, 16><<<grid, kThreads, 0, s>>>(c);
-        else hda_exact_kernel<T, 32, 8><<<grid, kThreads, 0, s>>>(c);
-        const cudaError_t e = cudaGetLastError();
+        const bool one = plan.cols == 1;
+        cudaError_t e;
+        if (plan.rows == 8) e = one ? launch_walk<T, 8, 1, kTile>(c, g, s) : launch_walk<T, 8, 4, kTile>(c, g, s);
+        else if (plan.rows == 16) e = one ? launch_walk<T, 16, 1, kTile>(c, g, s) : launch_walk<T, 16, 4, kTile>(c, g, s);
+        else e = one ? launch_walk<T, 32, 1, kTile / 2>(c, g, s) : launch_walk<T, 32, 2, kTile / 2>(c, g, s);
         if (e != cudaSuccess) return e;
-        count_launches(1);
     }
     return cudaSuccess;
 }
 
 }  // namespace
 
-cudaError_t launch_hda_exact(const HdaProblem &p, cudaStream_t s) {
-    return p.io == 0 ? run_exact<__nv_bfloat16>(p, s) : run_exact<float>(p, s);
+size_t hda_exact_workspace_bytes(const HdaProblem &p, int splits, int num_sms) {
+    const ExactPlan plan = exact_plan(p, splits, num_sms);
+    return (size_t)(plan.g.n - 1) * p.n * p.B * p.H * pairs_per_segment(plan) * sizeof(float2);
+}
+
+cudaError_t launch_hda_exact(const HdaProblem &p, int splits, int num_sms, void *ws, cudaStream_t s) {
+    return p.io == 0 ? run_exact<__nv_bfloat16>(p, splits, num_sms, ws, s)
+                     : run_exact<float>(p, splits, num_sms, ws, s);
 }
 
 cudaError_t launch_hda_share(const HdaShare *parts, int n, int64_t BT, int64_t H, int io,

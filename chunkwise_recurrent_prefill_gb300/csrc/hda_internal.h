@@ -50,7 +50,18 @@ struct HdaShare {
     int heads, D;
 };
 
-cudaError_t launch_hda_exact(const HdaProblem &p, cudaStream_t s);
+// l^n = e^(n g): the product is formed in two parts, so that the result is good to a few 2^-24
+// of itself (the rounding of n g alone would cost 2^-24 |n g|). 1 for n = 0, whatever g is.
+__device__ __forceinline__ float decay_pow(float g, float n) {
+    if (n == 0.f) return 1.f;
+    const float p = n * g;
+    if (!(p > -100.f)) return expf(p);      // below (or NaN): the correction has no meaning
+    return expf(p) * (1.f + fmaf(n, g, -p));
+}
+
+// splits: segments of a sequence, 0 = by the rule beside exact_plan.
+size_t hda_exact_workspace_bytes(const HdaProblem &p, int splits, int num_sms);
+cudaError_t launch_hda_exact(const HdaProblem &p, int splits, int num_sms, void *ws, cudaStream_t s);
 cudaError_t launch_hda_share(const HdaShare *parts, int n, int64_t BT, int64_t H, int io,
                              cudaStream_t s);
 struct HdaStep {

@@ -50,15 +50,6 @@ constexpr int kMaxSplits = 256;
 constexpr int kMaxPieces = 8;
 constexpr int64_t kL2Keep = 64ll << 20;
 
-// l^n = e^(n g): the product is formed in two parts, so that the result is good to a few 2^-24
-// of itself (the rounding of n g alone would cost 2^-24 |n g|). 1 for n = 0, whatever g is.
-__device__ __forceinline__ float decay_pow(float g, float n) {
-    if (n == 0.f) return 1.f;
-    const float p = n * g;
-    if (!(p > -100.f)) return expf(p);      // below (or NaN): the correction has no meaning
-    return expf(p) * (1.f + fmaf(n, g, -p));
-}
-
 // One map as the kernels see it.
 struct TcLin {
     const float *init;      // state before the first token (seg 0), or null

@@ -201,14 +201,14 @@ gla::HdaProblem hda_problem(const hda_shape &sh, const HdaDims &d, bool backward
 
 size_t round256(size_t n) { return (n + 255) & ~size_t(255); }
 
-// Workspace of a call: the tensor-core path's states, then one fp32 buffer per gradient of a
+// Workspace of a call: the segments' states of either path, then one fp32 buffer per gradient of a
 // shared head ([B, T, H, D]).
 size_t hda_workspace(const hda_shape &sh, const gla::HdaProblem &p, const gla_options *opt,
-                     int path, int sms, size_t *tc_bytes) {
-    size_t need = path == GLA_PATH_TC
-                      ? round256(gla::hda_tc_workspace_bytes(p, opt ? opt->seq_splits : 0, sms))
-                      : 0;
-    *tc_bytes = need;
+                     int path, int sms, size_t *state_bytes) {
+    const int splits = opt ? opt->seq_splits : 0;
+    size_t need = round256(path == GLA_PATH_TC ? gla::hda_tc_workspace_bytes(p, splits, sms)
+                                               : gla::hda_exact_workspace_bytes(p, splits, sms));
+    *state_bytes = need;
     if (p.n == 3) {
         const int64_t heads[3] = {sh.Hq, sh.Hk, sh.Hv};
         for (int i = 0; i < 3; ++i)
@@ -227,8 +227,8 @@ size_t workspace_size(const hda_shape *sh, const gla_options *opt, bool backward
     int sms;
     unsigned *err;
     gla::device_info(&sms, &err);
-    size_t tc;
-    return hda_workspace(*sh, p, opt, path, sms, &tc);
+    size_t states;
+    return hda_workspace(*sh, p, opt, path, sms, &states);
 }
 
 // State at the end of no tokens: the one at the start, or zero.
@@ -241,11 +241,11 @@ gla_status empty_state(float *dst, const float *src, int64_t bytes, cudaStream_t
 }
 
 gla_status run_hda(gla::HdaProblem &p, const hda_shape &sh, const gla_options *opt, void *ws,
-                   size_t tc_bytes, int path, int sms, unsigned *err, cudaStream_t s) {
+                   size_t state_bytes, int path, int sms, unsigned *err, cudaStream_t s) {
     // gradients of shared heads go to fp32 buffers first
     gla::HdaShare parts[3];
     int np = 0;
-    char *at = static_cast<char *>(ws) + tc_bytes;
+    char *at = static_cast<char *>(ws) + state_bytes;
     if (p.n == 3) {
         const int64_t heads[3] = {sh.Hq, sh.Hk, sh.Hv};
         for (int i = 0; i < 3; ++i) {
@@ -259,7 +259,7 @@ gla_status run_hda(gla::HdaProblem &p, const hda_shape &sh, const gla_options *o
     }
     cudaError_t e = path == GLA_PATH_TC
                         ? gla::launch_hda_tc(p, opt ? opt->seq_splits : 0, sms, ws, err, s)
-                        : gla::launch_hda_exact(p, s);
+                        : gla::launch_hda_exact(p, opt ? opt->seq_splits : 0, sms, ws, s);
     if (e == cudaSuccess) e = gla::launch_hda_share(parts, np, sh.B * sh.T, sh.H, sh.io, s);
     return e == cudaSuccess ? GLA_OK : (gla_status)gla::launch_failed("decay attention launch", e);
 }
@@ -382,8 +382,8 @@ gla_status hda_fwd(const void *q, const void *k, const void *v, const float *dec
     int sms;
     unsigned *err;
     const int dev = gla::device_info(&sms, &err);
-    size_t tc;
-    const size_t need = empty ? 0 : hda_workspace(sh, p, opt, path, sms, &tc);
+    size_t states;
+    const size_t need = empty ? 0 : hda_workspace(sh, p, opt, path, sms, &states);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (dev != GLA_OK && !(opt && opt->workspace)) return (gla_status)dev;
     void *ws = nullptr;
@@ -393,7 +393,7 @@ gla_status hda_fwd(const void *q, const void *k, const void *v, const float *dec
     if (dev != GLA_OK) return (gla_status)dev;
     if (none) return GLA_OK;
     if (empty) return empty_state(hT, h0, d.bs, s);
-    return run_hda(p, sh, opt, ws, tc, path, sms, err, s);
+    return run_hda(p, sh, opt, ws, states, path, sms, err, s);
 }
 
 gla_status hda_bwd(const void *d_o, const void *q, const void *k, const void *v,
@@ -434,8 +434,8 @@ gla_status hda_bwd(const void *d_o, const void *q, const void *k, const void *v,
     int sms;
     unsigned *err;
     const int dev = gla::device_info(&sms, &err);
-    size_t tc;
-    const size_t need = empty ? 0 : hda_workspace(sh, p, opt, path, sms, &tc);
+    size_t states;
+    const size_t need = empty ? 0 : hda_workspace(sh, p, opt, path, sms, &states);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (dev != GLA_OK && !(opt && opt->workspace)) return (gla_status)dev;
     void *ws = nullptr;
@@ -445,7 +445,7 @@ gla_status hda_bwd(const void *d_o, const void *q, const void *k, const void *v,
     if (dev != GLA_OK) return (gla_status)dev;
     if (none) return GLA_OK;
     if (empty) return empty_state(dh0, dhT, d.bs, s);
-    return run_hda(p, sh, opt, ws, tc, path, sms, err, s);
+    return run_hda(p, sh, opt, ws, states, path, sms, err, s);
 }
 
 gla_status hda_step(const void *q, const void *k, const void *v, const float *decay, float scale,

@@ -325,7 +325,7 @@ typedef struct {
     int io;                 /* gla_io                                                   */
 } hda_shape;
 
-/* opt: path, seq_splits (tensor cores: sequence segments per head; 0 = auto) and the workspace,
+/* opt: path, seq_splits (sequence segments per head, on either path; 0 = auto) and the workspace,
  * as in gla_fwd_ex; its gate must be GLA_GATE_KEY (0). opt may be NULL. */
 gla_status hda_fwd(const void *q, const void *k, const void *v, const float *decay, float scale,
                    const float *h0, void *o, float *hT, const hda_shape *shape,

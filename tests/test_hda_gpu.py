@@ -111,6 +111,16 @@ def test_infinite_decay_keeps_the_token_alone():
     assert torch.equal(hT[0, 0], x["k"][0, 4, 0][:, None] * x["v"][0, 4, 0][None, :])
 
 
+@pytest.mark.parametrize("splits", [0, 1, 2, 5, 200])
+@pytest.mark.parametrize("dims", [(64, 64), (128, 40), (24, 200), (200, 64)])
+def test_sequence_splits_token_by_token(splits, dims):
+    """Segments of whole tiles of 16 tokens, the last one shorter; 0: by the rule, which gives one
+    head's 777 tokens several."""
+    x = ref.inputs(1, 777, 2, 2, 1, 1, dims[0], dims[1], io="f32", seed=splits, decay=[-0.02, -3.0])
+    _check_forward(x, "exact", splits)
+    _check_backward(x, "exact", splits)
+
+
 @pytest.mark.parametrize("splits", [1, 2, 3, 7])
 def test_sequence_splits(splits):
     x = ref.inputs(1, 64 * 7 + 5, 2, 1, 2, 2, 128, 64, "bf16", seed=10)
