@@ -54,6 +54,11 @@ struct Vec<float> {
 __device__ __forceinline__ void put(float *p, float x) { *p = x; }
 __device__ __forceinline__ void put(__nv_bfloat16 *p, float x) { *p = __float2bfloat16_rn(x); }
 
+__device__ __forceinline__ void put4(float *p, float4 v) { *reinterpret_cast<float4 *>(p) = v; }
+__device__ __forceinline__ void put4(__nv_bfloat16 *p, float4 v) {
+    *reinterpret_cast<uint2 *>(p) = make_uint2(tc::pack_bf16(v.x, v.y), tc::pack_bf16(v.z, v.w));
+}
+
 // One tile of TB tokens on its way from global memory to shared memory: rows of W floats, of
 // which the first `width` (a multiple of 8) exist. Rows past the end and columns past the width
 // become zero.
@@ -277,6 +282,7 @@ hda_exact_scan_kernel(const float *__restrict__ decay, int64_t H, const Segs sg,
 // heads, and rounded once.
 template <typename T>
 __global__ void hda_share_kernel(HdaShare a, HdaShare b, HdaShare c, int64_t BT, int64_t H) {
+    tc::pdl_wait_prerequisites();
     const HdaShare s = blockIdx.y == 0 ? a : blockIdx.y == 1 ? b : c;
     const int64_t n = BT * s.heads * (s.D / 4);
     const int rep = (int)(H / s.heads);
@@ -284,19 +290,22 @@ __global__ void hda_share_kernel(HdaShare a, HdaShare b, HdaShare c, int64_t BT,
          e += (int64_t)gridDim.x * blockDim.x) {
         const int64_t d4 = e % (s.D / 4), th = e / (s.D / 4);   // th = token * heads + head
         const float *ip = s.in + th * rep * s.D + d4 * 4;
-        float4 v = *reinterpret_cast<const float4 *>(ip);
-        for (int r = 1; r < rep; ++r) {
-            const float4 w = *reinterpret_cast<const float4 *>(ip + (int64_t)r * s.D);
-            v.x += w.x;
-            v.y += w.y;
-            v.z += w.z;
-            v.w += w.w;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int r0 = 0; r0 < rep; r0 += 4) {       // (four loads on their way at a time)
+            float4 w[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                if (r0 + r < rep) w[r] = __ldcs(reinterpret_cast<const float4 *>(ip + (int64_t)(r0 + r) * s.D));
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                if (r0 + r < rep) {
+                    v.x += w[r].x;
+                    v.y += w[r].y;
+                    v.z += w[r].z;
+                    v.w += w[r].w;
+                }
         }
-        T *op = static_cast<T *>(s.out) + e * 4;
-        put(op, v.x);
-        put(op + 1, v.y);
-        put(op + 2, v.z);
-        put(op + 3, v.w);
+        put4(static_cast<T *>(s.out) + e * 4, v);
     }
 }
 
@@ -421,11 +430,20 @@ cudaError_t launch_hda_share(const HdaShare *parts, int n, int64_t BT, int64_t H
     if (n == 0 || BT == 0) return cudaSuccess;
     int64_t most = 0;
     for (int i = 0; i < n; ++i) most = max(most, BT * parts[i].heads * (parts[i].D / 4));
-    const dim3 grid((unsigned)min((most + 255) / 256, (int64_t)152 * 8), n);
+    const dim3 grid((unsigned)min((most + 255) / 256, (int64_t)1 << 16), n);
     const HdaShare b = parts[n > 1 ? 1 : 0], c = parts[n > 2 ? 2 : 0];
-    if (io == 0) hda_share_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(parts[0], b, c, BT, H);
-    else hda_share_kernel<float><<<grid, 256, 0, s>>>(parts[0], b, c, BT, H);
-    const cudaError_t e = cudaGetLastError();
+    cudaLaunchAttribute pdl[1];
+    pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    pdl[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(256);
+    cfg.stream = s;
+    cfg.attrs = pdl;
+    cfg.numAttrs = 1;
+    const cudaError_t e =
+        io == 0 ? cudaLaunchKernelEx(&cfg, hda_share_kernel<__nv_bfloat16>, parts[0], b, c, BT, H)
+                : cudaLaunchKernelEx(&cfg, hda_share_kernel<float>, parts[0], b, c, BT, H);
     if (e == cudaSuccess) count_launches(1);
     return e;
 }
