@@ -675,9 +675,9 @@ constexpr int kMostGroups = 8;      // of a cluster's block
 // The first kKeep vectors of a thread stay in registers from the statistics to the output; the rest
 // is read again (from L2).
 template <typename T, bool kGate, bool kSilu>
-__global__ void __launch_bounds__(kThreads, 3)
+__global__ void __launch_bounds__(kThreads, 2)
 norm_cluster_fwd(const __grid_constant__ NormProblem p, const MapPlan m) {
-    constexpr int V = Vec<T>::n, kKeep = 8;
+    constexpr int V = Vec<T>::n, kKeep = 16;
     __shared__ Stat sh[kThreads];
     __shared__ Stat part[kMostGroups];
     __shared__ float2 stat[kMostGroups];
@@ -1081,10 +1081,12 @@ dim3 map_grid(const NormProblem &p, const MapPlan &m) {
 
 // The plan of a cluster of up to 16 CTAs, each thread with at least four rounds of positions if it
 // is larger than one, and all clusters on the GPU at once; false where that leaves a thread more
-// than kMostRounds (half of them backward). Measured, clusters against three kernels, per call:
-// 3 x 4095 x 512 21 us against 28, 1 x 16384 x 512 22 against 37, backward of 4 x 4096 x 512 26
-// against 33; beyond the rule 64 x 300 x 512 37 against 27, 1 x 262144 x 64 211 against 31, backward
-// of 1 x 16384 x 1024 79 against 59.
+// than kMostRounds (half of them backward). With two CTAs to an SM (the registers of 16 vectors), a
+// cluster's placement within a GPC leaves room for 14 clusters of 16 or 36 of 8 (occupancy query on
+// 152 SMs): 24 of 16 ran in two waves, 23 us against 19 for 24 of 8. Measured, clusters against three
+// kernels, per call: 3 x 4095 x 512 20 us against 28, 1 x 16384 x 512 21 against 37, backward of
+// 4 x 4096 x 512 26 against 33; beyond the rule 64 x 300 x 512 37 against 27, 1 x 262144 x 64 211
+// against 31, backward of 1 x 16384 x 1024 79 against 59.
 constexpr int kMostCluster = 16, kMostRounds = 32;
 bool cluster_plan(const NormProblem &p, int sms, bool backward, MapPlan *out) {
     const int64_t V = vec_of(p), nv = p.C / p.G / V;
@@ -1095,12 +1097,13 @@ bool cluster_plan(const NormProblem &p, int sms, bool backward, MapPlan *out) {
     m.nvb = m.groups * m.nv;
     m.ry = kThreads / m.nvb;
     m.parts = 1;
-    const int64_t blocks = (m.cols + m.nvb - 1) / m.nvb * p.N, most = 3 * (int64_t)sms;
-    while (m.parts < kMostCluster && (int64_t)m.parts * m.ry * 4 < p.L && blocks * m.parts * 2 <= most) m.parts *= 2;
+    const int64_t blocks = (m.cols + m.nvb - 1) / m.nvb * p.N;
+    auto fits = [&](int parts) { return blocks * parts * 10 <= (int64_t)sms * (parts > 8 ? 14 : 18); };
+    while (m.parts < kMostCluster && (int64_t)m.parts * m.ry * 4 < p.L && fits(m.parts * 2)) m.parts *= 2;
     const int64_t len = (p.L + m.parts - 1) / m.parts;
     m.len = (int)len;
     *out = m;
-    return blocks <= most && (len + m.ry - 1) / m.ry <= (backward ? kMostRounds / 2 : kMostRounds);
+    return fits(m.parts) && (len + m.ry - 1) / m.ry <= (backward ? kMostRounds / 2 : kMostRounds);
 }
 // Not the portable cluster size: asked for once for each kernel.
 template <typename... A>
