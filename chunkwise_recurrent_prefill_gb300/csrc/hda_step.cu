@@ -20,7 +20,9 @@ __device__ __forceinline__ void put(__nv_bfloat16 *p, float x) { *p = __float2bf
 // CTA = (row, head, kCols value columns). A thread owns four columns of every kRows-th key row and
 // moves them with 16-byte accesses; the sums over the key rows are added in shared memory in a
 // fixed order. Columns of 128 keep whole rows of 512 bytes together; a call of few rows and heads
-// takes 32, so that four times as many SMs share it (16 states of 128 x 128: 5.1 us against 6.7).
+// takes 32, so that four times as many SMs share it (16 states of 128 x 128: 5.2 us against 6.7).
+// Measured: 240 rows of 16 heads of 128 x 128 (512 MB of states and vectors) 79 us in the kernel, 84
+// per call, 6.0 TB/s or 89 % of a plain copy's rate.
 template <typename T, int kCols>
 __global__ void __launch_bounds__(kThreads, 2)
 hda_step_kernel(const __grid_constant__ HdaStep p, unsigned int *err) {

@@ -184,6 +184,9 @@ struct RowPlan {
     int cg;         // channels of a group
 };
 
+// A lane keeps VPL vectors of an entry (and those of the next one, on their way). Measured: 16384
+// entries of 2048 gated bf16 channels in 16 groups (201 MB) 41 us in the kernel, 4.9 TB/s, bound by
+// instruction issue as much as by memory (28 instructions an element, 2.65 of 4 a cycle).
 template <typename T, int VPL, bool kGate, bool kSilu>
 __global__ void __launch_bounds__(kThreads)
 norm_rows_fwd(const __grid_constant__ NormProblem p, const RowPlan r) {
@@ -271,6 +274,8 @@ norm_rows_fwd(const __grid_constant__ NormProblem p, const RowPlan r) {
 }
 
 // Partial channel sums: sums[part][0: dw, 1: db][C], part = blockIdx.x * rp + the entry slot.
+// Measured: 8191 entries of 2048 gated bf16 channels (168 MB) 30 us, 5.6 TB/s, and 6 us for the sums
+// of the channels' parts.
 template <typename T, int VPL, bool kGate, bool kSilu>
 __global__ void __launch_bounds__(kThreads)
 norm_rows_bwd(const __grid_constant__ NormProblem p, const RowPlan r, float *sums) {

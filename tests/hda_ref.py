@@ -10,7 +10,7 @@ most K u A (to first order):
   Dx / 8 rows and three shuffles: K = 4 T + Dx / 8 + 16.
 * tensor cores: the same fp32 work, and roundings to bf16 (2^-8 of a term at most): one of the
   masked score or of the state's snapshot for an output. The state's update carries its operand
-  in two bf16 parts, which leaves 2^-16 of a term.
+  in two bf16 parts or more, which leaves 2^-16 of a term at most.
 
 bf16 outputs add their own rounding, 2^-8 of the value. The roundings of a bf16 output are
 independent, so their joint effect over a tensor is much smaller than A says: each has a

@@ -96,3 +96,47 @@ def test_training_lowers_the_loss(ex):
     x = torch.randn(2, 300, 256, device="cuda", dtype=torch.bfloat16)
     losses = ex.train(layer, x, torch.randn(2, 300, 256, device="cuda"))
     assert losses[-1] < losses[0]
+
+
+def test_steps_in_a_graph(ex):
+    """One decode step's own kernels (fork, step, norm, free, compact), captured and replayed,
+    against the same calls one by one."""
+    from chunkwise_recurrent_prefill_gb300 import group_norm_fwd, hda_step, last_device_status
+    torch.manual_seed(4)
+    layer = ex.DecayLayer(64, 4, 2, 2, 64, 64)
+    R = 4
+    q, k, v, z = layer.split(torch.randn(R, 64, device="cuda", dtype=torch.bfloat16))
+    q, k, v, z = (t.detach() for t in (q, k, v, z))
+    norm = layer.norm.detach()
+    rows = torch.arange(2, dtype=torch.int32, device="cuda")
+
+    def fresh():
+        pool = ex.StatePool(layer, 6, R)
+        pool.admit(2).copy_(states)
+        return pool
+
+    def step(pool):
+        pool.fork(rows, rows + 2)
+        o = hda_step(q, k, v, layer.decay, layer.scale, pool.pages, pool.slots())
+        y, _, _ = group_norm_fwd(o.view(R, -1), layer.H, norm, act="silu", gate=z)
+        pool.drop(rows)
+        pool.compact()
+        return y
+
+    states = torch.randn(2, 4, 64, 64, device="cuda")
+    plain = fresh()
+    want = step(plain)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):       # the stream's workspace exists before the capture
+        step(fresh())
+    torch.cuda.current_stream().wait_stream(side)
+    pool = fresh()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        got = step(pool)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert last_device_status() == 0
+    assert torch.equal(got, want) and torch.equal(pool.table, plain.table)
+    assert torch.equal(pool.pages[:2], plain.pages[:2]) and torch.equal(pool.count, plain.count)
