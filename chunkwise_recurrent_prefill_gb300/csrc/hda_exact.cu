@@ -91,8 +91,8 @@ struct Tile {
 };
 
 struct Segs {
-    int n, len;             // segments and their tokens
-    int zblocks;            // CTAs of a segment
+    int n, zblocks;         // segments, CTAs of a segment
+    int64_t len;            // tokens of a segment
     float2 *E;              // end states: [map][head][segment 0 .. n - 2][CTA][pair][thread]
 };
 
@@ -108,7 +108,7 @@ hda_exact_kernel(const __grid_constant__ HdaProblem p, const Segs sg) {
     const HdaLin &m = p.lin[blockIdx.z];
     const int zb = blockIdx.x % sg.zblocks, seg = blockIdx.x / sg.zblocks, z0 = zb * kCols;
     if (z0 >= m.Dz) return;
-    const int64_t begin = (int64_t)seg * sg.len, end = min(begin + sg.len, p.T);
+    const int64_t begin = seg * sg.len, end = min(begin + sg.len, p.T);
     const int64_t bh = blockIdx.y, b = bh / p.H, h = bh % p.H;
     const int lane = threadIdx.x & 31;
     // lanes 8 c .. 8 c + 7 of a warp are the row groups of NC columns; a row group's rows come
@@ -135,7 +135,8 @@ hda_exact_kernel(const __grid_constant__ HdaProblem p, const Segs sg) {
             (k & 1 ? s[c][k / 2].y : s[c][k / 2].x) = v;
         }
     constexpr int kPer = NC * RPT / 2;      // pairs of a thread
-    float2 *E = sg.E + (((blockIdx.z * p.B * p.H + bh) * (sg.n - 1)) * sg.zblocks + zb) * (kPer * kThreads) + threadIdx.x;
+    float2 *E = sg.E + (((blockIdx.z * p.B * p.H + bh) * (sg.n - 1)) * sg.zblocks + zb) * (kPer * kThreads) +
+                threadIdx.x;
     const int64_t e_seg = (int64_t)sg.zblocks * (kPer * kThreads);
     if (!kState && seg > 0) {
         tc::pdl_wait_prerequisites();
@@ -339,7 +340,7 @@ ExactPlan exact_plan(const HdaProblem &p, int splits, int sms) {
         const int cols = wide ? (dx <= 128 ? 4 : 2) : 1, zblocks = (dz + 16 * cols - 1) / (16 * cols);
         const double ctas = (double)(p.B * p.H * p.n) * zblocks, token = wide ? 270 : 122, share = wide ? 1.9 : 1.2;
         int most = (int)min(p.T / (2 * kTile), (int64_t)kMostSegs);
-        if (p.B * p.H > 65535 || p.T > (int64_t)1 << 30) most = 1;
+        if (p.B * p.H > 65535) most = 1;
         if (splits > 0) most = min(splits, kMostSegs);
         for (int n = splits > 0 ? most : 1; n <= max(most, 1); ++n) {
             const double walk = token * (double)p.T / n * max(1.0, ctas * n / (share * sms));
@@ -352,8 +353,8 @@ ExactPlan exact_plan(const HdaProblem &p, int splits, int sms) {
         }
     }
     const int64_t len = (p.T + best.g.n - 1) / best.g.n;
-    best.g.len = best.g.n == 1 ? (int)min(len, (int64_t)1 << 30) : (int)((len + kTile - 1) / kTile * kTile);
-    if (best.g.n > 1) best.g.n = (int)max((int64_t)1, (p.T + best.g.len - 1) / best.g.len);
+    best.g.len = (len + kTile - 1) / kTile * kTile;
+    best.g.n = (int)max((int64_t)1, (p.T + best.g.len - 1) / best.g.len);
     return best;
 }
 int64_t pairs_per_segment(const ExactPlan &e) { return (int64_t)e.g.zblocks * e.rows * e.cols / 2 * kThreads; }
@@ -405,9 +406,12 @@ cudaError_t run_exact(const HdaProblem &p, int splits, int sms, void *ws, cudaSt
         }
         const bool one = plan.cols == 1;
         cudaError_t e;
-        if (plan.rows == 8) e = one ? launch_walk<T, 8, 1, kTile>(c, g, s) : launch_walk<T, 8, 4, kTile>(c, g, s);
-        else if (plan.rows == 16) e = one ? launch_walk<T, 16, 1, kTile>(c, g, s) : launch_walk<T, 16, 4, kTile>(c, g, s);
-        else e = one ? launch_walk<T, 32, 1, kTile / 2>(c, g, s) : launch_walk<T, 32, 2, kTile / 2>(c, g, s);
+        if (plan.rows == 8)
+            e = one ? launch_walk<T, 8, 1, kTile>(c, g, s) : launch_walk<T, 8, 4, kTile>(c, g, s);
+        else if (plan.rows == 16)
+            e = one ? launch_walk<T, 16, 1, kTile>(c, g, s) : launch_walk<T, 16, 4, kTile>(c, g, s);
+        else
+            e = one ? launch_walk<T, 32, 1, kTile / 2>(c, g, s) : launch_walk<T, 32, 2, kTile / 2>(c, g, s);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;

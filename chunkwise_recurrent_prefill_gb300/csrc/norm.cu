@@ -185,8 +185,8 @@ struct RowPlan {
 };
 
 // A lane keeps VPL vectors of an entry (and those of the next one, on their way). Measured: 16384
-// entries of 2048 gated bf16 channels in 16 groups (201 MB) 41 us in the kernel, 4.9 TB/s, bound by
-// instruction issue as much as by memory (28 instructions an element, 2.65 of 4 a cycle).
+// entries of 2048 gated bf16 channels in 16 groups (201 MB) 38 us a call, 5.3 TB/s; with one vector
+// to a lane (28 instructions an element) 47.
 template <typename T, int VPL, bool kGate, bool kSilu>
 __global__ void __launch_bounds__(kThreads)
 norm_rows_fwd(const __grid_constant__ NormProblem p, const RowPlan r) {
@@ -676,13 +676,14 @@ __device__ __forceinline__ float peer(const float *p, int rank) {
     return v;
 }
 constexpr int kMostGroups = 8;      // of a cluster's block
+constexpr int kKeep = 16;
 
 // The first kKeep vectors of a thread stay in registers from the statistics to the output; the rest
 // is read again (from L2).
 template <typename T, bool kGate, bool kSilu>
 __global__ void __launch_bounds__(kThreads, 2)
 norm_cluster_fwd(const __grid_constant__ NormProblem p, const MapPlan m) {
-    constexpr int V = Vec<T>::n, kKeep = 16;
+    constexpr int V = Vec<T>::n;
     __shared__ Stat sh[kThreads];
     __shared__ Stat part[kMostGroups];
     __shared__ float2 stat[kMostGroups];
@@ -1047,12 +1048,15 @@ bool aligned(const NormProblem &p) {
               reinterpret_cast<uintptr_t>(p.b)) & 15u);
 }
 
-RowPlan row_plan(const NormProblem &p) {
+// `per`: vectors of a lane, if the group has as many. Two forward (half the shuffles, and half of what
+// a vector costs besides its arithmetic: 16384 x 2048 gated 47.8 -> 43.2 us), one backward, where the
+// registers of two leave too few warps (8191 x 2048: 40 against 54 us).
+RowPlan row_plan(const NormProblem &p, int per) {
     const int nv = (int)(p.C / p.G / vec_of(p));
     RowPlan r;
     r.cg = (int)(p.C / p.G);
     r.W = 1;
-    while (r.W < nv && r.W < 32) r.W <<= 1;
+    while (r.W * per < nv && r.W < 32) r.W <<= 1;
     const int segs = kThreads / r.W;
     r.gpc = (int)min(p.G, (int64_t)segs);
     r.rp = segs / r.gpc;
@@ -1090,8 +1094,9 @@ dim3 map_grid(const NormProblem &p, const MapPlan &m) {
 // cluster's placement within a GPC leaves room for 14 clusters of 16 or 36 of 8 (occupancy query on
 // 152 SMs): 24 of 16 ran in two waves, 23 us against 19 for 24 of 8. Measured, clusters against three
 // kernels, per call: 3 x 4095 x 512 20 us against 28, 1 x 16384 x 512 21 against 37, backward of
-// 4 x 4096 x 512 26 against 33; beyond the rule 64 x 300 x 512 37 against 27, 1 x 262144 x 64 211
-// against 31, backward of 1 x 16384 x 1024 79 against 59.
+// 4 x 4096 x 512 26 against 33, 64 x 300 x 512 (single CTAs) 20.5 against 27; beyond the rule
+// 300 x 64 x 512 (2400 CTAs) 68 against 26, 1 x 262144 x 64 211 against 31, backward of
+// 1 x 16384 x 1024 79 against 59.
 constexpr int kMostCluster = 16, kMostRounds = 32;
 bool cluster_plan(const NormProblem &p, int sms, bool backward, MapPlan *out) {
     const int64_t V = vec_of(p), nv = p.C / p.G / V;
@@ -1104,11 +1109,13 @@ bool cluster_plan(const NormProblem &p, int sms, bool backward, MapPlan *out) {
     m.parts = 1;
     const int64_t blocks = (m.cols + m.nvb - 1) / m.nvb * p.N;
     auto fits = [&](int parts) { return blocks * parts * 10 <= (int64_t)sms * (parts > 8 ? 14 : 18); };
-    while (m.parts < kMostCluster && (int64_t)m.parts * m.ry * 4 < p.L && fits(m.parts * 2)) m.parts *= 2;
+    // one CTA that keeps all its positions, if such CTAs fill the GPU once or twice over
+    const bool one = blocks >= sms && blocks <= 4 * (int64_t)sms && p.L <= (int64_t)kKeep * m.ry;
+    while (!one && m.parts < kMostCluster && (int64_t)m.parts * m.ry * 4 < p.L && fits(m.parts * 2)) m.parts *= 2;
     const int64_t len = (p.L + m.parts - 1) / m.parts;
     m.len = (int)len;
     *out = m;
-    return fits(m.parts) && (len + m.ry - 1) / m.ry <= (backward ? kMostRounds / 2 : kMostRounds);
+    return (one || fits(m.parts)) && (len + m.ry - 1) / m.ry <= (backward ? kMostRounds / 2 : kMostRounds);
 }
 // Not the portable cluster size: asked for once for each kernel.
 template <typename... A>
@@ -1140,7 +1147,7 @@ cudaError_t launch_cluster(void (*kernel)(A...), std::atomic<uint64_t> &done, di
 }
 
 size_t round256(size_t n) { return (n + 255) & ~size_t(255); }
-constexpr int kFwdPerSm = 5, kBwdPerSm = 2;
+constexpr int kBwdPerSm = 2;
 dim3 combine_grid(const NormProblem &p) { return dim3((unsigned)((p.N * p.G + kWarps - 1) / kWarps)); }
 size_t mean_bytes(const NormProblem &p) { return round256((size_t)(p.N * p.G) * sizeof(float2)); }
 
@@ -1171,16 +1178,31 @@ cudaError_t launch(void (*kernel)(A...), dim3 grid, size_t smem, bool dependent,
     return launch_n(kernel, grid, kThreads, smem, dependent, s, args...);
 }
 
+// As many CTAs as are resident at once: each walks over its entries with the next one on its way, and
+// a second, partial round of CTAs costs up to a fifth (16384 x 2048 gated bf16, 2 to an SM: 38 us;
+// with 3 to 8 to an SM 40 to 45).
+template <auto kKernel>
+cudaError_t launch_rows(const NormProblem &p, const RowPlan &r, int sms, cudaStream_t s) {
+    static std::atomic<int> resident{0};
+    int per_sm = resident.load(std::memory_order_relaxed);
+    if (per_sm == 0) {
+        const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kKernel, kThreads, 0);
+        if (e != cudaSuccess) return e;
+        per_sm = max(per_sm, 1);
+        resident.store(per_sm, std::memory_order_relaxed);
+    }
+    return launch(kKernel, row_grid(p, r, sms, per_sm), 0, false, s, p, r);
+}
+
 template <typename T, bool kGate, bool kSilu>
 cudaError_t run_fwd(const NormProblem &p, void *ws, int sms, cudaStream_t s) {
     const Route rt = aligned(p) ? route(p, false) : kPlain;
     if (rt == kRows) {
-        const RowPlan r = row_plan(p);
+        const RowPlan r = row_plan(p, 2);
         const int vpl = (int)((p.C / p.G / Vec<T>::n + r.W - 1) / r.W);
-        const dim3 grid = row_grid(p, r, sms, kFwdPerSm);
-        if (vpl == 1) return launch(norm_rows_fwd<T, 1, kGate, kSilu>, grid, 0, false, s, p, r);
-        if (vpl == 2) return launch(norm_rows_fwd<T, 2, kGate, kSilu>, grid, 0, false, s, p, r);
-        return launch(norm_rows_fwd<T, 4, kGate, kSilu>, grid, 0, false, s, p, r);
+        if (vpl == 1) return launch_rows<norm_rows_fwd<T, 1, kGate, kSilu>>(p, r, sms, s);
+        if (vpl == 2) return launch_rows<norm_rows_fwd<T, 2, kGate, kSilu>>(p, r, sms, s);
+        return launch_rows<norm_rows_fwd<T, 4, kGate, kSilu>>(p, r, sms, s);
     }
     if (rt == kMaps) {
         MapPlan m;
@@ -1213,7 +1235,7 @@ cudaError_t run_bwd(const NormProblem &p, void *ws, int sms, cudaStream_t s) {
     float *sums = nullptr;
     int64_t parts;
     if (rt == kRows) {
-        const RowPlan r = row_plan(p);
+        const RowPlan r = row_plan(p, 1);
         const int vpl = (int)((p.C / p.G / Vec<T>::n + r.W - 1) / r.W);
         const dim3 grid = row_grid(p, r, sms, kBwdPerSm);
         parts = (int64_t)grid.x * r.rp;
@@ -1256,7 +1278,7 @@ size_t norm_workspace_bytes(const NormProblem &p, bool backward, int num_sms) {
     const Route rt = route(p, backward);
     if (rt == kPlain || (rt == kRows && !backward)) return 0;
     if (rt == kRows) {
-        const RowPlan r = row_plan(p);
+        const RowPlan r = row_plan(p, 1);
         return (size_t)row_grid(p, r, num_sms, kBwdPerSm).x * r.rp * 2 * p.C * sizeof(float);
     }
     MapPlan m;

@@ -139,7 +139,7 @@ def test_sizes(shape, G, io):
     ((1, 3000, 72), 9), ((2, 4100, 128), 1),        # clusters of several CTAs in both directions
     ((70, 130, 256), 4), ((3, 2, 16), 1),           # of one
     ((1, 9000, 64), 8), ((1, 20000, 64), 8),        # too long for them: backward, then in both
-    ((130, 40, 512), 8)])                           # too many for them
+    ((200, 70, 64), 2), ((500, 40, 512), 8)])       # single CTAs; too many for them
 def test_maps_in_clusters_and_in_parts(shape, G, io):
     check_all(make(shape, io, seed=shape[1], gate=shape[0] % 2 == 0), G, "gelu")
 
