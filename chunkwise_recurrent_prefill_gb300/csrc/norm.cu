@@ -279,6 +279,7 @@ norm_rows_fwd(const __grid_constant__ NormProblem p, const RowPlan r) {
 template <typename T, int VPL, bool kGate, bool kSilu>
 __global__ void __launch_bounds__(kThreads)
 norm_rows_bwd(const __grid_constant__ NormProblem p, const RowPlan r, float *sums) {
+    tc::pdl_launch_dependents();
     constexpr int V = Vec<T>::n;
     const int cg = r.cg, nv = cg / V;
     const int seg = threadIdx.x / r.W, lane = threadIdx.x % r.W;
@@ -631,6 +632,7 @@ norm_maps_bwd_combine(const __grid_constant__ NormProblem p, const MapPlan m, co
 template <typename T, bool kGate, bool kSilu>
 __global__ void __launch_bounds__(kThreads)
 norm_maps_bwd_apply(const __grid_constant__ NormProblem p, const MapPlan m, const float2 *means) {
+    tc::pdl_launch_dependents();
     constexpr int V = Vec<T>::n;
     const MapPos q = map_pos(p, m);
     const int nv = m.nv;
@@ -778,6 +780,7 @@ norm_cluster_fwd(const __grid_constant__ NormProblem p, const MapPlan m) {
 template <typename T, bool kGate, bool kSilu>
 __global__ void __launch_bounds__(kThreads)
 norm_cluster_bwd(const __grid_constant__ NormProblem p, const MapPlan m, float *sums) {
+    tc::pdl_launch_dependents();
     constexpr int V = Vec<T>::n;
     __shared__ float2 sh[kThreads];
     __shared__ float2 part[kMostGroups], means[kMostGroups];
@@ -898,6 +901,7 @@ norm_sum_parts(const float *__restrict__ sums, int parts, int64_t C, float *dw, 
     const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
     const int64_t e = (int64_t)blockIdx.x * 32 + tx;      // 0 .. 2 C - 1
     float t = 0.f;
+    tc::pdl_wait_prerequisites();
     if (e < 2 * C) {
 #pragma unroll 8
         for (int i = ty; i < parts; i += 32) t += sums[i * 2 * C + e];
@@ -1251,7 +1255,7 @@ cudaError_t run_bwd(const NormProblem &p, void *ws, int sms, cudaStream_t s) {
             const size_t smem = (size_t)(kThreads * (2 * Vec<T>::n + 4) + m.nvb * 2 * Vec<T>::n) * sizeof(float);
             e = launch_cluster(norm_cluster_bwd<T, kGate, kSilu>, done, map_grid(p, m), smem, s, p, m, sums);
             if (e != cudaSuccess || !sums) return e;
-            return launch_n(norm_sum_parts, dim3((unsigned)((2 * p.C + 31) / 32)), kSumThreads, 0, false, s,
+            return launch_n(norm_sum_parts, dim3((unsigned)((2 * p.C + 31) / 32)), kSumThreads, 0, true, s,
                             (const float *)sums, (int)p.N, p.C, p.dw, p.db);
         }
         m = map_plan(p, sms);
@@ -1267,7 +1271,7 @@ cudaError_t run_bwd(const NormProblem &p, void *ws, int sms, cudaStream_t s) {
         e = launch(norm_maps_bwd_apply<T, kGate, kSilu>, map_grid(p, m), 0, true, s, p, m, (const float2 *)means);
     }
     if (e != cudaSuccess || !want) return e;
-    return launch_n(norm_sum_parts, dim3((unsigned)((2 * p.C + 31) / 32)), kSumThreads, 0, false, s,
+    return launch_n(norm_sum_parts, dim3((unsigned)((2 * p.C + 31) / 32)), kSumThreads, 0, true, s,
                     (const float *)sums, (int)parts, p.C, p.dw, p.db);
 }
 
