@@ -986,7 +986,7 @@ hda_tc_state_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__
 // Start states of segments 1 .. splits - 1, and the final state. A thread carries kScanPer elements of
 // one head; the loads of a batch of pieces are issued together, so the chain costs one round trip
 // per batch (16 heads of 8 segments: 8 us from cold caches).
-constexpr int kScanThreads = 256, kScanPer = 4, kScanBatch = 4;
+constexpr int kScanThreads = 256, kScanPer = 4, kScanBatch = 12;
 
 __global__ void __launch_bounds__(kScanThreads)
 hda_tc_scan_kernel(const __grid_constant__ TcArgs a, const __grid_constant__ StateArgs sa) {
