@@ -150,16 +150,21 @@ def _stream_handle(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(stream.cuda_stream)
 
 
-def _launch(f, device, stream, *args):
-    """f(*args, stream handle) with ``device`` current: switching costs as much as a small call,
-    so it is only done when another device is. (The raw handle of torch's current stream, without
-    a Stream object around it, for the same reason.)"""
+def _launch(f, device, *args):
+    """f(*args, stream handle) on torch's current stream, with ``device`` current: switching costs
+    as much as a small call, so it is only done when another device is. (The raw handle of the
+    stream, without a Stream object around it, for the same reason.)"""
     if device.index != torch.cuda.current_device():
         with torch.cuda.device(device):
-            return _launch(f, device, stream, *args)
-    if stream is None:
-        return f(*args, torch._C._cuda_getCurrentRawStream(device.index))
-    return f(*args, stream.cuda_stream)
+            return _launch(f, device, *args)
+    return f(*args, torch._C._cuda_getCurrentRawStream(device.index))
+
+
+def _on_stream(stream, f, *args, **kwargs):
+    """f with ``stream`` current: outputs allocated while another stream is current may come from
+    memory that work still pending there uses."""
+    with torch.cuda.stream(stream):
+        return f(*args, **kwargs)
 
 
 def _check(t, name, dtype, shape, device):

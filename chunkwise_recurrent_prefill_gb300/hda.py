@@ -15,7 +15,7 @@ import functools
 import torch
 
 from .gla import (GLA_OK, GLAError, IO_BF16, IO_F32, _HdaShape, _check, _addr, _launch,
-                  load_library, options)
+                  _on_stream, load_library, options)
 
 
 def _check_rows(name, dtype, shape, strides, want_dtype, want_shape, align):
@@ -105,7 +105,11 @@ def hda_fwd(q, k, v, decay, scale: float, h0=None, *, o=None, hT=None, return_st
     """Forward pass over whole sequences. decay: float32 [H] log-decays (a constant of the
     layer); h0: [B,H,Dk,Dv] float32 or None. Returns (o [B,T,H,Dv], hT | None), o in q's dtype,
     the final state hT (float32) when ``return_state`` or ``hT`` is given. Asynchronous on
-    ``stream`` (default: torch's current stream)."""
+    ``stream`` (default: torch's current stream), which the new outputs belong to."""
+    if stream is not None:
+        return _on_stream(stream, hda_fwd, q, k, v, decay, scale, h0, o=o, hT=hT,
+                          return_state=return_state, path=path, seq_splits=seq_splits,
+                          workspace=workspace)
     lib = load_library()
     H = decay.numel()
     sh = _shape(q, k, v, decay)
@@ -120,7 +124,7 @@ def hda_fwd(q, k, v, decay, scale: float, h0=None, *, o=None, hT=None, return_st
         hT = torch.empty((B, H, Dk, Dv), dtype=torch.float32, device=dev)
     _state(hT, "hT", (B, H, Dk, Dv), dev)
     opt = options(path, seq_splits, workspace)
-    rc = _launch(lib.hda_fwd, dev, stream, _addr(q), _addr(k), _addr(v), _addr(decay), scale, _addr(h0),
+    rc = _launch(lib.hda_fwd, dev, _addr(q), _addr(k), _addr(v), _addr(decay), scale, _addr(h0),
                  _addr(o), _addr(hT), ctypes.byref(sh), ctypes.byref(opt))
     _fail(lib, rc, "hda_fwd")
     return o, hT
@@ -131,6 +135,9 @@ def hda_bwd(do, q, k, v, decay, scale: float, h0=None, dhT=None, *, path: str = 
     """Gradients of ``hda_fwd``: do is that of o, dhT that of hT (None: zero), h0 what the
     forward started from. Returns (dq, dk, dv, dh0), dh0 only when h0 is given (else None). The
     gradients of shared heads are summed in fp32."""
+    if stream is not None:
+        return _on_stream(stream, hda_bwd, do, q, k, v, decay, scale, h0, dhT, path=path,
+                          seq_splits=seq_splits, workspace=workspace)
     lib = load_library()
     H = decay.numel()
     sh = _shape(q, k, v, decay, do)
@@ -143,7 +150,7 @@ def hda_bwd(do, q, k, v, decay, scale: float, h0=None, dhT=None, *, path: str = 
     dq, dk, dv = (torch.empty(t.shape, dtype=t.dtype, device=dev) for t in (q, k, v))
     dh0 = None if h0 is None else torch.empty_like(h0)
     opt = options(path, seq_splits, workspace)
-    rc = _launch(lib.hda_bwd, dev, stream, _addr(do), _addr(q), _addr(k), _addr(v), _addr(decay), scale,
+    rc = _launch(lib.hda_bwd, dev, _addr(do), _addr(q), _addr(k), _addr(v), _addr(decay), scale,
                  _addr(h0), _addr(dhT), _addr(dq), _addr(dk), _addr(dv), _addr(dh0), ctypes.byref(sh),
                  ctypes.byref(opt))
     _fail(lib, rc, "hda_bwd")
@@ -171,6 +178,8 @@ def hda_step(q, k, v, decay, scale: float, S, slots=None, *, o=None, stream=None
     float32 is a pool of states, updated in place; row r uses page ``slots[r]`` (int32 on the
     device, each page at most once; negative: an empty row, whose output is zero), or page r
     when ``slots`` is None. Returns o [R,H,Dv] in q's dtype."""
+    if stream is not None:
+        return _on_stream(stream, hda_step, q, k, v, decay, scale, S, slots, o=o)
     lib = load_library()
     H = decay.numel()
     sh = _shape(q, k, v, decay, step=True)
@@ -184,7 +193,7 @@ def hda_step(q, k, v, decay, scale: float, S, slots=None, *, o=None, stream=None
         o = torch.empty((R, H, Dv), dtype=q.dtype, device=dev)
     else:
         _check(o, "o", q.dtype, (R, H, Dv), dev)
-    rc = _launch(lib.hda_step, dev, stream, _addr(q), _addr(k), _addr(v), _addr(decay), scale, _addr(S),
+    rc = _launch(lib.hda_step, dev, _addr(q), _addr(k), _addr(v), _addr(decay), scale, _addr(S),
                  _addr(slots), _addr(o), P, ctypes.byref(sh))
     _fail(lib, rc, "hda_step")
     return o

@@ -11,7 +11,7 @@ import functools
 
 import torch
 
-from .gla import IO_BF16, IO_F32, _NormShape, _check, _addr, _launch, load_library
+from .gla import IO_BF16, IO_F32, _NormShape, _check, _addr, _launch, _on_stream, load_library
 from .hda import _fail
 
 ACTS = {"none": 0, "silu": 1, "gelu": 2}
@@ -105,6 +105,9 @@ def group_norm_fwd(x, groups: int, weight=None, bias=None, *, eps: float = 1e-5,
                    gate=None, y=None, workspace=None, stream=None):
     """y = act(u), or u act(gate) with a gate, of u = (x - mean) rstd weight + bias. weight, bias:
     float32 [C] or None. Returns (y, mean [N, groups], rstd [N, groups])."""
+    if stream is not None:
+        return _on_stream(stream, group_norm_fwd, x, groups, weight, bias, eps=eps, act=act,
+                          gate=gate, y=y, workspace=workspace)
     lib = load_library()
     sh = _shape(x, groups, eps, act, gate)
     _affine(x, weight, bias)
@@ -116,7 +119,7 @@ def group_norm_fwd(x, groups: int, weight=None, bias=None, *, eps: float = 1e-5,
     mean = torch.empty((sh.N, max(sh.G, 0)), dtype=torch.float32, device=dev)
     rstd = torch.empty_like(mean)
     ws, nws = _workspace(workspace, dev)
-    rc = _launch(lib.gla_group_norm_fwd, dev, stream, _addr(x), _addr(weight), _addr(bias), _addr(gate),
+    rc = _launch(lib.gla_group_norm_fwd, dev, _addr(x), _addr(weight), _addr(bias), _addr(gate),
                  _addr(y), _addr(mean), _addr(rstd), ctypes.byref(sh), ws, nws)
     _fail(lib, rc, "gla_group_norm_fwd")
     return y, mean, rstd
@@ -126,6 +129,9 @@ def group_norm_bwd(dy, x, mean, rstd, groups: int, weight=None, bias=None, *, ac
                    gate=None, workspace=None, stream=None):
     """Gradients of ``group_norm_fwd`` from its mean and rstd. Returns (dx, dweight | None,
     dbias | None, dgate | None): float32 [C] sums for the parameters that are given."""
+    if stream is not None:
+        return _on_stream(stream, group_norm_bwd, dy, x, mean, rstd, groups, weight, bias, act=act,
+                          gate=gate, workspace=workspace)
     lib = load_library()
     sh = _shape(x, groups, 0.0, act, gate, dy)
     _affine(x, weight, bias)
@@ -137,7 +143,7 @@ def group_norm_bwd(dy, x, mean, rstd, groups: int, weight=None, bias=None, *, ac
     dw = None if weight is None else torch.empty_like(weight)
     db = None if bias is None else torch.empty_like(bias)
     ws, nws = _workspace(workspace, dev)
-    rc = _launch(lib.gla_group_norm_bwd, dev, stream, _addr(dy), _addr(x), _addr(mean), _addr(rstd),
+    rc = _launch(lib.gla_group_norm_bwd, dev, _addr(dy), _addr(x), _addr(mean), _addr(rstd),
                  _addr(weight), _addr(bias), _addr(gate), _addr(dx), _addr(dw), _addr(db), _addr(dz),
                  ctypes.byref(sh), ws, nws)
     _fail(lib, rc, "gla_group_norm_bwd")

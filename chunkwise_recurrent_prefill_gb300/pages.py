@@ -9,7 +9,7 @@ from __future__ import annotations
 
 import torch
 
-from .gla import _check, _addr, _launch, load_library
+from .gla import _check, _addr, _launch, _on_stream, load_library
 from .hda import _fail
 
 
@@ -43,30 +43,36 @@ def _book(table, free, count, P, dev):
 
 def pages_copy(pool, src, dst, *, stream=None):
     """pool[dst[i]] = pool[src[i]] for every i whose two numbers are not negative."""
+    if stream is not None:
+        return _on_stream(stream, pages_copy, pool, src, dst)
     lib = load_library()
     P, nb = _pool(pool)
     n = src.numel()
     _ints(src, "src", pool.device)
     _ints(dst, "dst", pool.device, (n,))
-    rc = _launch(lib.gla_pages_copy, pool.device, stream, _addr(pool), P, nb, _addr(src), _addr(dst), n)
+    rc = _launch(lib.gla_pages_copy, pool.device, _addr(pool), P, nb, _addr(src), _addr(dst), n)
     _fail(lib, rc, "gla_pages_copy")
 
 
 def pages_fork(pool, table, free, count, parents, children, *, stream=None):
     """Rows ``children`` become copies of rows ``parents`` on pages taken from the stack."""
+    if stream is not None:
+        return _on_stream(stream, pages_fork, pool, table, free, count, parents, children)
     lib = load_library()
     P, nb = _pool(pool)
     R, M = _book(table, free, count, P, pool.device)
     n = parents.numel()
     _ints(parents, "parents", pool.device)
     _ints(children, "children", pool.device, (n,))
-    rc = _launch(lib.gla_pages_fork, pool.device, stream, _addr(pool), P, nb, _addr(table), R, M,
+    rc = _launch(lib.gla_pages_fork, pool.device, _addr(pool), P, nb, _addr(table), R, M,
                  _addr(free), _addr(count), _addr(parents), _addr(children), n)
     _fail(lib, rc, "gla_pages_fork")
 
 
 def pages_free(table, free, count, rows, *, stream=None):
     """The pages of ``rows`` go back on the stack; the rows have none afterwards."""
+    if stream is not None:
+        return _on_stream(stream, pages_free, table, free, count, rows)
     lib = load_library()
     dev = table.device
     if dev.type != "cuda":
@@ -74,16 +80,18 @@ def pages_free(table, free, count, rows, *, stream=None):
     P = free.numel()
     R, M = _book(table, free, count, P, dev)
     _ints(rows, "rows", dev)
-    rc = _launch(lib.gla_pages_free, dev, stream, P, _addr(table), R, M, _addr(free), _addr(count),
+    rc = _launch(lib.gla_pages_free, dev, P, _addr(table), R, M, _addr(free), _addr(count),
                  _addr(rows), rows.numel())
     _fail(lib, rc, "gla_pages_free")
 
 
 def pages_compact(pool, table, free, count, *, stream=None):
     """The live pages move down to 0 .. n-1; the table follows, the stack is rebuilt."""
+    if stream is not None:
+        return _on_stream(stream, pages_compact, pool, table, free, count)
     lib = load_library()
     P, nb = _pool(pool)
     R, M = _book(table, free, count, P, pool.device)
-    rc = _launch(lib.gla_pages_compact, pool.device, stream, _addr(pool), P, nb, _addr(table), R, M,
+    rc = _launch(lib.gla_pages_compact, pool.device, _addr(pool), P, nb, _addr(table), R, M,
                  _addr(free), _addr(count))
     _fail(lib, rc, "gla_pages_compact")

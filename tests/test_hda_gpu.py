@@ -256,6 +256,28 @@ def test_other_stream_and_caller_workspace():
     assert all(torch.equal(p, r) for p, r in zip(grads, want_g))
 
 
+def test_outputs_on_a_given_stream():
+    """A call with ``stream=`` does not take memory for its outputs that work still pending on the
+    current stream writes to."""
+    from chunkwise_recurrent_prefill_gb300 import group_norm_fwd, hda_fwd
+    g = _gpu(ref.inputs(1, 700, 2, 2, 2, 2, 128, 128, "bf16", seed=19))
+    a = (g["q"], g["k"], g["v"], g["decay"], 0.1)
+    want, want_h = hda_fwd(*a, return_state=True)
+    want_y = group_norm_fwd(want.view(700, 256), 2)[0]
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    held = [torch.empty_like(t) for t in (want, want_h, want_y) for _ in range(4)]
+    torch.cuda._sleep(20_000_000)
+    for t in held:
+        t.fill_(float("nan"))
+    del held, t
+    o, hT = hda_fwd(*a, return_state=True, stream=s)
+    y = group_norm_fwd(o.view(700, 256), 2, stream=s)[0]
+    torch.cuda.synchronize()
+    _status_ok()
+    assert torch.equal(o, want) and torch.equal(hT, want_h) and torch.equal(y, want_y)
+
+
 # ---------------------------------------------------------------- single tokens
 @pytest.mark.parametrize("io", ["bf16", "f32"])
 @pytest.mark.parametrize("R,P,H,Hq,Hk,Hv,Dk,Dv", [
