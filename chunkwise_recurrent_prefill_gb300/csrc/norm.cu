@@ -12,7 +12,7 @@
 //          they are few (cluster_plan), the parts are a cluster and one kernel does it all; else a
 //          first kernel leaves each part's statistics, a second one combines them and a third one
 //          writes. The second reading of x comes from registers or from L2 when the tensor fits there.
-//   plain: whatever does not come in whole 16-byte vectors of one group: a CTA per group.
+//   plain: groups of an odd number of channels, odd strides or pointers: a CTA per group.
 // Means and variances: where a group is in registers, the mean and then the squared deviations from
 // it. Else each thread takes the mean of its first vector as a pivot and sums the deviations from
 // it and their squares; threads and parts are then merged as (count, mean, M2), in a fixed order.
@@ -39,11 +39,41 @@ __device__ __forceinline__ void put(__nv_bfloat16 *p, float x) { *p = __float2bf
 
 // 16 bytes as pairs of floats (the arithmetic is in packed pairs throughout: with scalar
 // instructions the rows kernels were bound by issue, at 40 instructions an element).
+// Where a group's channels are not whole vectors of 16 bytes but an even number, a vector is two
+// channels (a type of its own of the same size, so that pointers to it count elements).
+struct BF16Pair {
+    __nv_bfloat16 v;
+};
+struct F32Pair {
+    float v;
+};
 template <typename T>
 struct Vec;
 template <>
+struct Vec<F32Pair> {
+    static constexpr int n = 2;
+    using raw = uint2;
+    using elem = float;
+    static __device__ __forceinline__ void unpack(uint2 v, float2 (&f)[1]) {
+        f[0] = make_float2(__uint_as_float(v.x), __uint_as_float(v.y));
+    }
+    static __device__ __forceinline__ uint2 pack(const float2 (&f)[1]) {
+        return make_uint2(__float_as_uint(f[0].x), __float_as_uint(f[0].y));
+    }
+};
+template <>
+struct Vec<BF16Pair> {
+    static constexpr int n = 2;
+    using raw = uint32_t;
+    using elem = __nv_bfloat16;
+    static __device__ __forceinline__ void unpack(uint32_t v, float2 (&f)[1]) { f[0] = tc::unpack_bf16(v); }
+    static __device__ __forceinline__ uint32_t pack(const float2 (&f)[1]) { return tc::pack_bf16(f[0].x, f[0].y); }
+};
+template <>
 struct Vec<float> {
     static constexpr int n = 4;
+    using raw = uint4;
+    using elem = float;
     static __device__ __forceinline__ void unpack(uint4 v, float2 (&f)[2]) {
         f[0] = make_float2(__uint_as_float(v.x), __uint_as_float(v.y));
         f[1] = make_float2(__uint_as_float(v.z), __uint_as_float(v.w));
@@ -56,6 +86,8 @@ struct Vec<float> {
 template <>
 struct Vec<__nv_bfloat16> {
     static constexpr int n = 8;
+    using raw = uint4;
+    using elem = __nv_bfloat16;
     static __device__ __forceinline__ void unpack(uint4 v, float2 (&f)[4]) {
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -67,6 +99,8 @@ struct Vec<__nv_bfloat16> {
                           tc::pack_bf16(f[2].x, f[2].y), tc::pack_bf16(f[3].x, f[3].y));
     }
 };
+template <typename T>
+using Raw = typename Vec<T>::raw;
 using tc::add2;
 using tc::fma2;
 using tc::mul2;
@@ -144,15 +178,19 @@ __device__ __forceinline__ float sum_lanes(float v, int width) {
         if (o < width) v += __shfl_xor_sync(0xffffffffu, v, o);     // (width is the same in the warp)
     return v;
 }
-// 8 (or 4) weights from memory, or their default.
+// A vector's weights from memory, or their default.
 template <int N>
 __device__ __forceinline__ void load_param(const float *p, int64_t c, float otherwise, float2 (&f)[N]) {
+    if constexpr (N == 1) {
+        f[0] = p ? *reinterpret_cast<const float2 *>(p + c) : make_float2(otherwise, otherwise);
+    } else {
 #pragma unroll
-    for (int i = 0; i < N; i += 2) {
-        const float4 v = p ? *reinterpret_cast<const float4 *>(p + c + 2 * i)
-                           : make_float4(otherwise, otherwise, otherwise, otherwise);
-        f[i] = make_float2(v.x, v.y);
-        f[i + 1] = make_float2(v.z, v.w);
+        for (int i = 0; i < N; i += 2) {
+            const float4 v = p ? *reinterpret_cast<const float4 *>(p + c + 2 * i)
+                               : make_float4(otherwise, otherwise, otherwise, otherwise);
+            f[i] = make_float2(v.x, v.y);
+            f[i + 1] = make_float2(v.z, v.w);
+        }
     }
 }
 
@@ -206,7 +244,7 @@ norm_rows_fwd(const __grid_constant__ NormProblem p, const RowPlan r) {
         load_param(p.b, c, 0.f, b[k]);
     }
     const float inv = 1.f / (float)cg;
-    uint4 xv[VPL], zv[VPL];
+    Raw<T> xv[VPL], zv[VPL];
     const T *xp = static_cast<const T *>(p.x) + n0 * p.x_n + c0 + lane * V;
     const T *zp = static_cast<const T *>(p.gate) + (kGate ? n0 * p.gate_n + c0 + lane * V : 0);
     T *yp = static_cast<T *>(p.y) + n0 * p.C + c0 + lane * V;
@@ -215,10 +253,10 @@ norm_rows_fwd(const __grid_constant__ NormProblem p, const RowPlan r) {
         const bool in = live && n < p.N;
 #pragma unroll
         for (int k = 0; k < VPL; ++k) {
-            xv[k] = zv[k] = make_uint4(0, 0, 0, 0);
+            xv[k] = zv[k] = Raw<T>{};
             if (in && lane + k * r.W < nv) {
-                xv[k] = *reinterpret_cast<const uint4 *>(xp + k * r.W * V);
-                if (kGate) zv[k] = *reinterpret_cast<const uint4 *>(zp + k * r.W * V);
+                xv[k] = *reinterpret_cast<const Raw<T> *>(xp + k * r.W * V);
+                if (kGate) zv[k] = *reinterpret_cast<const Raw<T> *>(zp + k * r.W * V);
             }
         }
         xp += xs;
@@ -229,7 +267,7 @@ norm_rows_fwd(const __grid_constant__ NormProblem p, const RowPlan r) {
     // The next entry is loaded while this one is worked on.
     for (int64_t base = (int64_t)blockIdx.x * r.rp, n = n0; base < p.N; base += step, n += step, yp += ys) {
         float2 x[VPL][V / 2];
-        uint4 zc[VPL];
+        Raw<T> zc[VPL];
 #pragma unroll
         for (int k = 0; k < VPL; ++k) {
             Vec<T>::unpack(xv[k], x[k]);
@@ -268,7 +306,7 @@ norm_rows_fwd(const __grid_constant__ NormProblem p, const RowPlan r) {
                 const float2 u = fma2(mul2(x[k][i], both(rstd)), w[k][i], b[k][i]);
                 x[k][i] = kGate ? mul2(u, act_of2<T, kSilu>(z[i], p.act)) : act_of2<T, kSilu>(u, p.act);
             }
-            *reinterpret_cast<uint4 *>(yp + k * r.W * V) = Vec<T>::pack(x[k]);
+            *reinterpret_cast<Raw<T> *>(yp + k * r.W * V) = Vec<T>::pack(x[k]);
         }
     }
 }
@@ -298,7 +336,7 @@ norm_rows_bwd(const __grid_constant__ NormProblem p, const RowPlan r, float *sum
         for (int i = 0; i < V / 2; ++i) dw[k][i] = db[k][i] = both(0.f);
     }
     const float inv = 1.f / (float)cg;
-    uint4 xv[VPL], dv[VPL], zv[VPL];
+    Raw<T> xv[VPL], dv[VPL], zv[VPL];
     float mean, rstd;
     const int64_t at0 = c0 + lane * V;
     const T *xp = static_cast<const T *>(p.x) + n0 * p.x_n + at0;
@@ -312,11 +350,11 @@ norm_rows_bwd(const __grid_constant__ NormProblem p, const RowPlan r, float *sum
         const bool in = live && n < p.N;
 #pragma unroll
         for (int k = 0; k < VPL; ++k) {
-            xv[k] = dv[k] = zv[k] = make_uint4(0, 0, 0, 0);
+            xv[k] = dv[k] = zv[k] = Raw<T>{};
             if (in && lane + k * r.W < nv) {
-                xv[k] = *reinterpret_cast<const uint4 *>(xp + k * r.W * V);
-                dv[k] = *reinterpret_cast<const uint4 *>(dp + k * r.W * V);
-                if (kGate) zv[k] = *reinterpret_cast<const uint4 *>(zp + k * r.W * V);
+                xv[k] = *reinterpret_cast<const Raw<T> *>(xp + k * r.W * V);
+                dv[k] = *reinterpret_cast<const Raw<T> *>(dp + k * r.W * V);
+                if (kGate) zv[k] = *reinterpret_cast<const Raw<T> *>(zp + k * r.W * V);
             }
         }
         mean = in ? *mp : 0.f;
@@ -334,7 +372,7 @@ norm_rows_bwd(const __grid_constant__ NormProblem p, const RowPlan r, float *sum
          base += step, n += step, op += os, gp += kGate ? os : 0) {
         const bool in = live && n < p.N;
         if (!kAhead) load(n);
-        uint4 xc[VPL], dc[VPL], zc[VPL];
+        Raw<T> xc[VPL], dc[VPL], zc[VPL];
 #pragma unroll
         for (int k = 0; k < VPL; ++k) {
             xc[k] = xv[k];
@@ -353,7 +391,7 @@ norm_rows_bwd(const __grid_constant__ NormProblem p, const RowPlan r, float *sum
             Vec<T>::unpack(zc[k], z);
             grad_vec<T, kGate, kSilu>(x[k], d[k], z, w[k], b[k], mu, rs, p.act);
             if (!in || v >= nv) continue;
-            if (kGate) *reinterpret_cast<uint4 *>(gp + k * r.W * V) = Vec<T>::pack(z);
+            if (kGate) *reinterpret_cast<Raw<T> *>(gp + k * r.W * V) = Vec<T>::pack(z);
 #pragma unroll
             for (int i = 0; i < V / 2; ++i) {
                 dw[k][i] = fma2(d[k][i], x[k][i], dw[k][i]);
@@ -372,7 +410,7 @@ norm_rows_bwd(const __grid_constant__ NormProblem p, const RowPlan r, float *sum
 #pragma unroll
             for (int i = 0; i < V / 2; ++i)
                 x[k][i] = mul2(both(rs), fma2(x[k][i], both(-s2), add2(d[k][i], both(-s1))));
-            *reinterpret_cast<uint4 *>(op + k * r.W * V) = Vec<T>::pack(x[k]);
+            *reinterpret_cast<Raw<T> *>(op + k * r.W * V) = Vec<T>::pack(x[k]);
         }
     }
     if (!sums || !live) return;
@@ -433,10 +471,10 @@ norm_maps_stats(const __grid_constant__ NormProblem p, const MapPlan m, Stat *pa
         xp += (q.l0 + q.ty) * p.x_l;
         const int count = (int)((q.l1 - q.l0 - q.ty + m.ry - 1) / m.ry);
         for (int i0 = 0; i0 < count; i0 += kAhead) {
-            uint4 xv[kAhead];
+            Raw<T> xv[kAhead];
 #pragma unroll
             for (int a = 0; a < kAhead; ++a) {
-                if (i0 + a < count) xv[a] = *reinterpret_cast<const uint4 *>(xp);
+                if (i0 + a < count) xv[a] = *reinterpret_cast<const Raw<T> *>(xp);
                 xp += xs;
             }
 #pragma unroll
@@ -513,12 +551,12 @@ norm_maps_apply(const __grid_constant__ NormProblem p, const MapPlan m, const fl
     const T *zp = static_cast<const T *>(p.gate) + (kGate ? q.n * p.gate_n + c : 0);
     T *yp = static_cast<T *>(p.y) + q.n * p.L * p.C + c;
     for (int64_t l = q.l0 + q.ty; l < q.l1; l += (int64_t)m.ry * kAhead) {
-        uint4 xv[kAhead], zv[kAhead];
+        Raw<T> xv[kAhead], zv[kAhead];
 #pragma unroll
         for (int a = 0; a < kAhead; ++a)
             if (l + a * m.ry < q.l1) {
-                xv[a] = *reinterpret_cast<const uint4 *>(xp + (l + a * m.ry) * p.x_l);
-                if (kGate) zv[a] = *reinterpret_cast<const uint4 *>(zp + (l + a * m.ry) * p.gate_l);
+                xv[a] = *reinterpret_cast<const Raw<T> *>(xp + (l + a * m.ry) * p.x_l);
+                if (kGate) zv[a] = *reinterpret_cast<const Raw<T> *>(zp + (l + a * m.ry) * p.gate_l);
             }
 #pragma unroll
         for (int a = 0; a < kAhead; ++a)
@@ -531,7 +569,7 @@ norm_maps_apply(const __grid_constant__ NormProblem p, const MapPlan m, const fl
                     const float2 u = fma2(mul2(add2(f[i], both(-mean)), both(rstd)), w[i], b[i]);
                     f[i] = kGate ? mul2(u, act_of2<T, kSilu>(z[i], p.act)) : act_of2<T, kSilu>(u, p.act);
                 }
-                *reinterpret_cast<uint4 *>(yp + (l + a * m.ry) * p.C) = Vec<T>::pack(f);
+                *reinterpret_cast<Raw<T> *>(yp + (l + a * m.ry) * p.C) = Vec<T>::pack(f);
             }
     }
 }
@@ -561,9 +599,9 @@ norm_maps_bwd_stats(const __grid_constant__ NormProblem p, const MapPlan m, floa
 #pragma unroll 2
         for (int64_t l = q.l0 + q.ty; l < q.l1; l += m.ry) {
             float2 x[V / 2], d[V / 2], z[V / 2];
-            Vec<T>::unpack(*reinterpret_cast<const uint4 *>(xp + l * p.x_l), x);
-            Vec<T>::unpack(*reinterpret_cast<const uint4 *>(dp + l * p.dy_l), d);
-            if (kGate) Vec<T>::unpack(*reinterpret_cast<const uint4 *>(zp + l * p.gate_l), z);
+            Vec<T>::unpack(*reinterpret_cast<const Raw<T> *>(xp + l * p.x_l), x);
+            Vec<T>::unpack(*reinterpret_cast<const Raw<T> *>(dp + l * p.dy_l), d);
+            if (kGate) Vec<T>::unpack(*reinterpret_cast<const Raw<T> *>(zp + l * p.gate_l), z);
             grad_vec<T, kGate, kSilu>(x, d, z, w, b, mean, rstd, p.act);
 #pragma unroll
             for (int i = 0; i < V / 2; ++i) {
@@ -625,7 +663,7 @@ norm_maps_bwd_combine(const __grid_constant__ NormProblem p, const MapPlan m, co
     }
     a = sum_lanes(a, 32);
     b = sum_lanes(b, 32);
-    const float inv = 1.f / ((float)p.L * (float)(m.nv * (p.io == 0 ? 8 : 4)));
+    const float inv = 1.f / ((float)p.L * (float)(p.C / p.G));
     if (lane == 0) mean[i] = make_float2(a * inv, b * inv);
 }
 
@@ -651,15 +689,15 @@ norm_maps_bwd_apply(const __grid_constant__ NormProblem p, const MapPlan m, cons
 #pragma unroll 2
     for (int64_t l = q.l0 + q.ty; l < q.l1; l += m.ry) {
         float2 x[V / 2], d[V / 2], z[V / 2];
-        Vec<T>::unpack(*reinterpret_cast<const uint4 *>(xp + l * p.x_l), x);
-        Vec<T>::unpack(*reinterpret_cast<const uint4 *>(dp + l * p.dy_l), d);
-        if (kGate) Vec<T>::unpack(*reinterpret_cast<const uint4 *>(zp + l * p.gate_l), z);
+        Vec<T>::unpack(*reinterpret_cast<const Raw<T> *>(xp + l * p.x_l), x);
+        Vec<T>::unpack(*reinterpret_cast<const Raw<T> *>(dp + l * p.dy_l), d);
+        if (kGate) Vec<T>::unpack(*reinterpret_cast<const Raw<T> *>(zp + l * p.gate_l), z);
         grad_vec<T, kGate, kSilu>(x, d, z, w, b, mean, rstd, p.act);
 #pragma unroll
         for (int i = 0; i < V / 2; ++i)
             x[i] = mul2(both(rstd), fma2(x[i], both(-s2), fma2(d[i], w[i], both(-s1))));
-        *reinterpret_cast<uint4 *>(op + l * p.C) = Vec<T>::pack(x);
-        if (kGate) *reinterpret_cast<uint4 *>(gp + l * p.C) = Vec<T>::pack(z);
+        *reinterpret_cast<Raw<T> *>(op + l * p.C) = Vec<T>::pack(x);
+        if (kGate) *reinterpret_cast<Raw<T> *>(gp + l * p.C) = Vec<T>::pack(z);
     }
 }
 
@@ -677,7 +715,7 @@ __device__ __forceinline__ float peer(const float *p, int rank) {
     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
     return v;
 }
-constexpr int kMostGroups = 8;      // of a cluster's block
+constexpr int kMostGroups = 32;      // of a cluster's block
 constexpr int kKeep = 16;
 
 // The first kKeep vectors of a thread stay in registers from the statistics to the output; the rest
@@ -694,9 +732,10 @@ norm_cluster_fwd(const __grid_constant__ NormProblem p, const MapPlan m) {
     const int count = q.live && first < q.l1 ? (int)((q.l1 - first + m.ry - 1) / m.ry) : 0;
     const int64_t xs = m.ry * p.x_l, zs = m.ry * p.gate_l, ys = m.ry * p.C;
     const T *xp = static_cast<const T *>(p.x) + (count ? q.n * p.x_n + first * p.x_l + c : 0);
-    uint4 xv[kKeep];
+    Raw<T> xv[kKeep];
 #pragma unroll
-    for (int a = 0; a < kKeep; ++a) xv[a] = a < count ? *reinterpret_cast<const uint4 *>(xp + a * xs) : make_uint4(0, 0, 0, 0);
+    for (int a = 0; a < kKeep; ++a)
+        xv[a] = a < count ? *reinterpret_cast<const Raw<T> *>(xp + a * xs) : Raw<T>{};
     Stat s{0.f, 0.f, 0.f};
     if (count) {
         float2 f[V / 2], t1 = both(0.f), t2 = both(0.f);
@@ -705,7 +744,7 @@ norm_cluster_fwd(const __grid_constant__ NormProblem p, const MapPlan m) {
 #pragma unroll
         for (int i = 1; i < V / 2; ++i) t = add2(t, f[i]);
         const float pivot = (t.x + t.y) * (1.f / V);
-        auto add = [&](uint4 v) {
+        auto add = [&](Raw<T> v) {
             Vec<T>::unpack(v, f);
 #pragma unroll
             for (int i = 0; i < V / 2; ++i) {
@@ -718,7 +757,7 @@ norm_cluster_fwd(const __grid_constant__ NormProblem p, const MapPlan m) {
         for (int a = 0; a < kKeep; ++a)
             if (a < count) add(xv[a]);
 #pragma unroll 4
-        for (int a = kKeep; a < count; ++a) add(*reinterpret_cast<const uint4 *>(xp + a * xs));
+        for (int a = kKeep; a < count; ++a) add(*reinterpret_cast<const Raw<T> *>(xp + a * xs));
         const float s1 = t1.x + t1.y, s2 = t2.x + t2.y, n = (float)count * V;
         const float d = s1 / n;
         s = Stat{n, pivot + d, fmaxf(fmaf(-s1, d, s2), 0.f)};
@@ -756,22 +795,22 @@ norm_cluster_fwd(const __grid_constant__ NormProblem p, const MapPlan m) {
         const float2 st = stat[q.tx / m.nv];
         const T *zp = static_cast<const T *>(p.gate) + (kGate ? q.n * p.gate_n + first * p.gate_l + c : 0);
         T *yp = static_cast<T *>(p.y) + (q.n * p.L + first) * p.C + c;
-        auto write = [&](uint4 v, int a) {
+        auto write = [&](Raw<T> v, int a) {
             float2 f[V / 2], z[V / 2];
             Vec<T>::unpack(v, f);
-            if (kGate) Vec<T>::unpack(*reinterpret_cast<const uint4 *>(zp + a * zs), z);
+            if (kGate) Vec<T>::unpack(*reinterpret_cast<const Raw<T> *>(zp + a * zs), z);
 #pragma unroll
             for (int i = 0; i < V / 2; ++i) {
                 const float2 u = fma2(mul2(add2(f[i], both(-st.x)), both(st.y)), w[i], b[i]);
                 f[i] = kGate ? mul2(u, act_of2<T, kSilu>(z[i], p.act)) : act_of2<T, kSilu>(u, p.act);
             }
-            *reinterpret_cast<uint4 *>(yp + a * ys) = Vec<T>::pack(f);
+            *reinterpret_cast<Raw<T> *>(yp + a * ys) = Vec<T>::pack(f);
         };
 #pragma unroll
         for (int a = 0; a < kKeep; ++a)
             if (a < count) write(xv[a], a);
 #pragma unroll 2
-        for (int a = kKeep; a < count; ++a) write(*reinterpret_cast<const uint4 *>(xp + a * xs), a);
+        for (int a = kKeep; a < count; ++a) write(*reinterpret_cast<const Raw<T> *>(xp + a * xs), a);
     }
     cluster_wait();
 }
@@ -806,9 +845,9 @@ norm_cluster_bwd(const __grid_constant__ NormProblem p, const MapPlan m, float *
 #pragma unroll 2
         for (int a = 0; a < count; ++a) {
             float2 x[V / 2], d[V / 2], z[V / 2];
-            Vec<T>::unpack(*reinterpret_cast<const uint4 *>(xp + a * xs), x);
-            Vec<T>::unpack(*reinterpret_cast<const uint4 *>(dp + a * ds), d);
-            if (kGate) Vec<T>::unpack(*reinterpret_cast<const uint4 *>(zp + a * zs), z);
+            Vec<T>::unpack(*reinterpret_cast<const Raw<T> *>(xp + a * xs), x);
+            Vec<T>::unpack(*reinterpret_cast<const Raw<T> *>(dp + a * ds), d);
+            if (kGate) Vec<T>::unpack(*reinterpret_cast<const Raw<T> *>(zp + a * zs), z);
             grad_vec<T, kGate, kSilu>(x, d, z, w, b, mean, rstd, p.act);
 #pragma unroll
             for (int i = 0; i < V / 2; ++i) {
@@ -879,15 +918,15 @@ norm_cluster_bwd(const __grid_constant__ NormProblem p, const MapPlan m, float *
 #pragma unroll 2
         for (int a = 0; a < count; ++a) {
             float2 x[V / 2], d[V / 2], z[V / 2];
-            Vec<T>::unpack(*reinterpret_cast<const uint4 *>(xp + a * xs), x);
-            Vec<T>::unpack(*reinterpret_cast<const uint4 *>(dp + a * ds), d);
-            if (kGate) Vec<T>::unpack(*reinterpret_cast<const uint4 *>(zp + a * zs), z);
+            Vec<T>::unpack(*reinterpret_cast<const Raw<T> *>(xp + a * xs), x);
+            Vec<T>::unpack(*reinterpret_cast<const Raw<T> *>(dp + a * ds), d);
+            if (kGate) Vec<T>::unpack(*reinterpret_cast<const Raw<T> *>(zp + a * zs), z);
             grad_vec<T, kGate, kSilu>(x, d, z, w, b, mean, rstd, p.act);
 #pragma unroll
             for (int i = 0; i < V / 2; ++i)
                 x[i] = mul2(both(rstd), fma2(x[i], both(-mm.y), fma2(d[i], w[i], both(-mm.x))));
-            *reinterpret_cast<uint4 *>(op + a * os) = Vec<T>::pack(x);
-            if (kGate) *reinterpret_cast<uint4 *>(gp + a * os) = Vec<T>::pack(z);
+            *reinterpret_cast<Raw<T> *>(op + a * os) = Vec<T>::pack(x);
+            if (kGate) *reinterpret_cast<Raw<T> *>(gp + a * os) = Vec<T>::pack(z);
         }
     }
     cluster_wait();
@@ -1031,10 +1070,15 @@ norm_plain_dw(const __grid_constant__ NormProblem p) {
 enum Route { kRows, kMaps, kPlain };
 constexpr int kMostVpl = 4;
 
-int64_t vec_of(const NormProblem &p) { return p.io == 0 ? 8 : 4; }
+// Channels of a vector: 16 bytes, or two where a group is not whole vectors of 16 bytes.
+int64_t vec_of(const NormProblem &p) {
+    const int64_t full = p.io == 0 ? 8 : 4;
+    return p.C / p.G % full == 0 ? full : 2;
+}
+int64_t elem_bytes(const NormProblem &p) { return p.io == 0 ? 2 : 4; }
 
 // The route depends on the shape and strides, so that the workspace's size can be told before
-// the pointers are known; pointers that are not on 16 bytes fall back to plain at the launch.
+// the pointers are known; pointers that are not on a vector's bytes fall back to plain at the launch.
 Route route(const NormProblem &p, bool backward) {
     const int64_t V = vec_of(p), cg = p.C / p.G;
     if (cg % V != 0) return kPlain;
@@ -1047,9 +1091,10 @@ Route route(const NormProblem &p, bool backward) {
     return kPlain;
 }
 bool aligned(const NormProblem &p) {
+    const uintptr_t bytes = (uintptr_t)(vec_of(p) * elem_bytes(p)), params = vec_of(p) == 2 ? 8 : 16;
     return !((reinterpret_cast<uintptr_t>(p.x) | reinterpret_cast<uintptr_t>(p.gate) |
-              reinterpret_cast<uintptr_t>(p.dy) | reinterpret_cast<uintptr_t>(p.w) |
-              reinterpret_cast<uintptr_t>(p.b)) & 15u);
+              reinterpret_cast<uintptr_t>(p.dy)) & (bytes - 1)) &&
+           !((reinterpret_cast<uintptr_t>(p.w) | reinterpret_cast<uintptr_t>(p.b)) & (params - 1));
 }
 
 // `per`: vectors of a lane, if the group has as many. Two forward (half the shuffles, and half of what
@@ -1107,7 +1152,7 @@ bool cluster_plan(const NormProblem &p, int sms, bool backward, MapPlan *out) {
     MapPlan m;
     m.nv = (int)nv;
     m.cols = (int)(p.C / V);
-    m.groups = (int)min(max((int64_t)1, 8 / nv), p.G);
+    m.groups = (int)min(max((int64_t)1, 128 / (V * elem_bytes(p)) / nv), p.G);    // (128 bytes of a row)
     m.nvb = m.groups * m.nv;
     m.ry = kThreads / m.nvb;
     m.parts = 1;
@@ -1223,7 +1268,7 @@ cudaError_t run_fwd(const NormProblem &p, void *ws, int sms, cudaStream_t s) {
         if (e != cudaSuccess) return e;
         return launch(norm_maps_apply<T, kGate, kSilu>, map_grid(p, m), 0, true, s, p, m, (const float2 *)stat);
     }
-    return launch(norm_plain_fwd<T>, dim3((unsigned)(p.N * p.G)), 0, false, s, p);
+    return launch(norm_plain_fwd<typename Vec<T>::elem>, dim3((unsigned)(p.N * p.G)), 0, false, s, p);
 }
 
 template <typename T, bool kGate, bool kSilu>
@@ -1232,9 +1277,9 @@ cudaError_t run_bwd(const NormProblem &p, void *ws, int sms, cudaStream_t s) {
     const bool want = p.dw || p.db;
     cudaError_t e;
     if (rt == kPlain) {
-        e = launch(norm_plain_bwd<T>, dim3((unsigned)(p.N * p.G)), 0, false, s, p);
+        e = launch(norm_plain_bwd<typename Vec<T>::elem>, dim3((unsigned)(p.N * p.G)), 0, false, s, p);
         if (e != cudaSuccess || !want) return e;
-        return launch(norm_plain_dw<T>, dim3((unsigned)p.C), 0, false, s, p);
+        return launch(norm_plain_dw<typename Vec<T>::elem>, dim3((unsigned)p.C), 0, false, s, p);
     }
     float *sums = nullptr;
     int64_t parts;
@@ -1293,6 +1338,13 @@ size_t norm_workspace_bytes(const NormProblem &p, bool backward, int num_sms) {
 
 cudaError_t launch_norm_fwd(const NormProblem &p, void *ws, int num_sms, cudaStream_t s) {
     using bf16 = __nv_bfloat16;
+    if (vec_of(p) == 2) {
+        if (p.io == 0)
+            return p.gate ? run_fwd<BF16Pair, true, false>(p, ws, num_sms, s)
+                          : run_fwd<BF16Pair, false, false>(p, ws, num_sms, s);
+        return p.gate ? run_fwd<F32Pair, true, false>(p, ws, num_sms, s)
+                      : run_fwd<F32Pair, false, false>(p, ws, num_sms, s);
+    }
     if (p.act == 1) {
         if (p.io == 0) return p.gate ? run_fwd<bf16, true, true>(p, ws, num_sms, s) : run_fwd<bf16, false, true>(p, ws, num_sms, s);
         return p.gate ? run_fwd<float, true, true>(p, ws, num_sms, s) : run_fwd<float, false, true>(p, ws, num_sms, s);
@@ -1303,6 +1355,13 @@ cudaError_t launch_norm_fwd(const NormProblem &p, void *ws, int num_sms, cudaStr
 
 cudaError_t launch_norm_bwd(const NormProblem &p, void *ws, int num_sms, cudaStream_t s) {
     using bf16 = __nv_bfloat16;
+    if (vec_of(p) == 2) {
+        if (p.io == 0)
+            return p.gate ? run_bwd<BF16Pair, true, false>(p, ws, num_sms, s)
+                          : run_bwd<BF16Pair, false, false>(p, ws, num_sms, s);
+        return p.gate ? run_bwd<F32Pair, true, false>(p, ws, num_sms, s)
+                      : run_bwd<F32Pair, false, false>(p, ws, num_sms, s);
+    }
     if (p.act == 1) {
         if (p.io == 0) return p.gate ? run_bwd<bf16, true, true>(p, ws, num_sms, s) : run_bwd<bf16, false, true>(p, ws, num_sms, s);
         return p.gate ? run_bwd<float, true, true>(p, ws, num_sms, s) : run_bwd<float, false, true>(p, ws, num_sms, s);

@@ -144,6 +144,17 @@ def test_maps_in_clusters_and_in_parts(shape, G, io):
     check_all(make(shape, io, seed=shape[1], gate=shape[0] % 2 == 0), G, "gelu")
 
 
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("gate", [False, True])
+@pytest.mark.parametrize("shape,G", [
+    ((900, 320), 32), ((200, 644), 7), ((77, 12), 6),      # per token
+    ((3, 2000, 100), 5), ((1, 700, 1284), 3), ((40, 30, 12), 6), ((1, 9000, 60), 6), ((2, 9, 2004), 1)])
+def test_groups_that_are_not_whole_vectors(shape, G, gate, io):
+    """An even number of channels that is not a multiple of 16 bytes; (2, 9, 2004): too wide for
+    anything but the plain kernels."""
+    check_all(make(shape, io, seed=shape[-1], gate=gate, strided=True), G, "silu")
+
+
 @pytest.mark.parametrize("shape,G", [((2, 700, 32), 4), ((50, 256), 2)])
 def test_a_mean_far_from_zero(shape, G):
     """The variance of values that all lie near 1000: as a difference of squares it would have no
