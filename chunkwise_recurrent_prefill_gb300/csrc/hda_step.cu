@@ -43,7 +43,7 @@ hda_step_kernel(const __grid_constant__ HdaStep p, unsigned int *err) {
         return;
     }
     auto head = [&](const HdaTensor &t) {
-        return static_cast<const T *>(t.p) + r * t.b + (h / (p.H / t.heads)) * t.h;
+        return static_cast<const T *>(t.p) + r * t.b + (h / ((int)p.H / t.heads)) * t.h;
     };
     const T *kp = head(p.k), *qp = head(p.q), *vp = head(p.v) + col;
     for (int d = threadIdx.x; d < p.Dk; d += blockDim.x) {
