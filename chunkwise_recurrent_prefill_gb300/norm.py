@@ -31,13 +31,15 @@ def _rows(name, dtype, shape, strides, want_dtype, want_shape):
     for n, s in zip(reversed(shape[1:-1]), reversed(strides[1:-1])):
         if n == 1:
             continue
+        if s <= 0:
+            raise ValueError(f"{name}: strides {tuple(strides)} must be positive")
         if step and s != step * run:
             raise ValueError(f"{name}: the positions must be evenly spaced in memory")
         step = step or s
         run *= n
     sn = strides[0] if shape[0] > 1 else max(step, shape[-1]) * run
     sl = step or shape[-1]
-    if sn <= 0 or sl <= 0:
+    if sn <= 0:
         raise ValueError(f"{name}: strides {tuple(strides)} must be positive")
     return sn, sl
 
