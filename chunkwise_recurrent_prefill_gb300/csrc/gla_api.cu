@@ -16,16 +16,22 @@ constexpr int kMaxDevices = 64;
 // Error word raised by kernels (bounded waits that ran out); one per device.
 __device__ unsigned int g_dev_err;
 
-// A workspace the library keeps for one stream of one device.
+// What the library keeps for one stream of one device: a workspace for its calls, and the one
+// that calls captured from it were given. A graph holds the latter's address for as long as it
+// may be replayed, which the library cannot know: it is never freed, and no other call gets it.
 struct StreamWorkspace {
     cudaStream_t stream = nullptr;
     void *ptr = nullptr;
     size_t bytes = 0;
+    void *graph_ptr = nullptr;
+    size_t graph_bytes = 0;
     uint64_t last_use = 0;
+    bool taken() const { return ptr || graph_ptr; }
 };
 
 // At most this many streams per device keep a library workspace; the least recently used
-// one is freed (cudaFree synchronises the device, so nothing still uses it) to make room.
+// one makes room: its own is freed (cudaFree synchronises the device, so nothing still uses it),
+// that of its graphs stays where it is.
 constexpr int kMaxStreamWorkspaces = 16;
 
 struct DeviceState {
@@ -144,24 +150,42 @@ gla_status validate(const void *q, const void *k, const void *v, const float *g,
 // The library-owned workspace of `stream` on the current device. Each stream has its own, so
 // calls on different streams never share scratch; a stream's buffer is allocated on its first
 // call that needs one and replaced only when a call needs more (sizes are rounded up to a power
-// of two), so repeated calls allocate nothing.
+// of two), so repeated calls allocate nothing. A call that is being captured takes the buffer over
+// for the stream's graphs (allocating is not allowed then), and the stream's next call outside of
+// a capture gets a new one.
 gla_status library_workspace(DeviceState *st, cudaStream_t stream, size_t need, void **out) {
+    cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(stream, &capture) != cudaSuccess) cudaGetLastError();   // (a launch will tell)
     std::lock_guard<std::mutex> lock(g_mu);
     StreamWorkspace *slot = nullptr;
     for (auto &w : st->ws)
-        if (w.ptr && w.stream == stream) slot = &w;
+        if (w.taken() && w.stream == stream) slot = &w;
+    if (capture != cudaStreamCaptureStatusNone) {
+        if (!slot || (slot->graph_bytes < need && slot->bytes < need)) {
+            snprintf(g_detail, sizeof(g_detail),
+                     "the stream is being captured and has no workspace of %zu bytes: pass one, or make the "
+                     "call once on this stream before", need);
+            return GLA_ERR_WORKSPACE;
+        }
+        if (slot->graph_bytes < need) {
+            slot->graph_ptr = slot->ptr;
+            slot->graph_bytes = slot->bytes;
+            slot->ptr = nullptr;
+            slot->bytes = 0;
+        }
+        slot->last_use = ++st->ws_clock;
+        *out = slot->graph_ptr;
+        return GLA_OK;
+    }
     if (!slot) {
         for (auto &w : st->ws)
-            if (!w.ptr) { slot = &w; break; }
+            if (!w.taken()) { slot = &w; break; }
         if (!slot) {   // every slot taken: reuse the least recently used one
             slot = &st->ws[0];
             for (auto &w : st->ws)
                 if (w.last_use < slot->last_use) slot = &w;
-        }
-        if (slot->stream != stream && slot->ptr) {
-            cudaFree(slot->ptr);   // synchronises the device: no call still uses it
-            slot->ptr = nullptr;
-            slot->bytes = 0;
+            if (slot->ptr) cudaFree(slot->ptr);   // synchronises the device: no call still uses it
+            *slot = StreamWorkspace{};
         }
         slot->stream = stream;
     }

@@ -36,9 +36,13 @@
  * Execution: every call is asynchronous and ordered on `stream` (NULL = the legacy
  * default stream). No call synchronises the host, except gla_last_device_status().
  * Calls may be captured into a CUDA graph (stream capture) once their scratch exists: pass a
- * caller workspace, or make one call on the capturing stream first (the library's own
- * workspace is allocated with cudaMalloc, which cannot happen during capture). A replay
- * reads whatever the captured buffers then hold.
+ * caller workspace, or make the call once on the capturing stream first (the library's own
+ * workspace is allocated with cudaMalloc, which cannot happen during capture; a captured call
+ * that needs more than there is returns GLA_ERR_WORKSPACE). A replay reads whatever the captured
+ * buffers then hold. Library workspace that a captured call was given stays allocated until the
+ * process ends and serves the graphs captured from that stream alone, so other calls may come
+ * between the capture and a replay, on any stream. Graphs captured from one stream share it:
+ * they must not run at the same time, unless their calls pass workspaces of the caller's.
  *
  * Errors: every entry point returns a gla_status and never aborts, traps or throws.
  * Argument errors are detected on the host before any launch; nothing is written then.
