@@ -34,6 +34,7 @@ from .pages import (  # noqa: F401
     pages_copy,
     pages_fork,
     pages_free,
+    pages_workspace_size,
 )
 from .workloads import (  # noqa: F401
     BENCH_WORKLOAD,

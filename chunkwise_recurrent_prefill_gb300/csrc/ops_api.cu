@@ -610,17 +610,28 @@ gla_status gla_pages_copy(void *pool, int64_t P, int64_t page_bytes, const int32
     return e == cudaSuccess ? GLA_OK : (gla_status)gla::launch_failed("page copy launch", e);
 }
 
-gla_status gla_pages_fork(void *pool, int64_t P, int64_t page_bytes, int32_t *table, int64_t R,
-                          int64_t M, int32_t *free_stack, int32_t *count, const int32_t *parents,
-                          const int32_t *children, int64_t n, gla_stream_t stream) {
+size_t gla_pages_workspace_size(int64_t P, int64_t R, int64_t M, int64_t n) {
+    int64_t e;
+    if (P < 0 || P > (int64_t(1) << 30) || R < 0 || R > (int64_t(1) << 30) || !mul_ok(n, M, &e) ||
+        e > (int64_t(1) << 30) || n > (int64_t(1) << 30))
+        return 0;
+    const gla::PagePool p{nullptr, P, 0, nullptr, R, M, nullptr, nullptr};
+    return std::max({n > 0 ? gla::pages_fork_workspace(p, n) : 0, n > 0 ? gla::pages_free_workspace(p) : 0,
+                     P > 0 ? gla::pages_compact_workspace(p) : 0});
+}
+
+gla_status gla_pages_fork_ex(void *pool, int64_t P, int64_t page_bytes, int32_t *table, int64_t R,
+                             int64_t M, int32_t *free_stack, int32_t *count, const int32_t *parents,
+                             const int32_t *children, int64_t n, void *workspace,
+                             size_t workspace_bytes, gla_stream_t stream) {
     gla_status rc = check_pool(pool, P, page_bytes);
     if (rc == GLA_OK) rc = check_table(P, table, R, M, free_stack, count, n);
     if (rc != GLA_OK) return rc;
     if (n > 0 && (!parents || !children)) return GLA_ERR_NULL_ARG;
     if (bad_int(parents) || bad_int(children)) return GLA_ERR_MISALIGNED;
-    const Range outs[4] = {{pool, P * page_bytes}, {table, R * M * 4}, {free_stack, P * 4}, {count, 4}};
-    const Range ins[2] = {{parents, n * 4}, {children, n * 4}};
-    if ((rc = check_alias(outs, 4, ins, 2)) != GLA_OK) return rc;
+    const Range used[6] = {{parents, n * 4}, {children, n * 4}, {pool, P * page_bytes}, {table, R * M * 4},
+                           {free_stack, P * 4}, {count, 4}};
+    if ((rc = check_alias(used + 2, 4, used, 2)) != GLA_OK) return rc;
     int sms;
     unsigned *err;
     const int dev = gla::device_info(&sms, &err);
@@ -629,21 +640,28 @@ gla_status gla_pages_fork(void *pool, int64_t P, int64_t page_bytes, int32_t *ta
     gla::PagePool p{pool, P, page_bytes, table, R, M, free_stack, count};
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     void *ws;
-    rc = (gla_status)gla::stream_workspace(s, gla::pages_fork_workspace(p, n), &ws);
+    rc = get_workspace(workspace, workspace_bytes, gla::pages_fork_workspace(p, n), s, used, 6, &ws);
     if (rc != GLA_OK) return rc;
     const cudaError_t e = gla::launch_pages_fork(p, parents, children, n, ws, sms, err, s);
     return e == cudaSuccess ? GLA_OK : (gla_status)gla::launch_failed("page fork launch", e);
 }
 
-gla_status gla_pages_free(int64_t P, int32_t *table, int64_t R, int64_t M, int32_t *free_stack,
-                          int32_t *count, const int32_t *rows, int64_t n, gla_stream_t stream) {
+gla_status gla_pages_fork(void *pool, int64_t P, int64_t page_bytes, int32_t *table, int64_t R,
+                          int64_t M, int32_t *free_stack, int32_t *count, const int32_t *parents,
+                          const int32_t *children, int64_t n, gla_stream_t stream) {
+    return gla_pages_fork_ex(pool, P, page_bytes, table, R, M, free_stack, count, parents, children, n,
+                             nullptr, 0, stream);
+}
+
+gla_status gla_pages_free_ex(int64_t P, int32_t *table, int64_t R, int64_t M, int32_t *free_stack,
+                             int32_t *count, const int32_t *rows, int64_t n, void *workspace,
+                             size_t workspace_bytes, gla_stream_t stream) {
     gla_status rc = check_table(P, table, R, M, free_stack, count, n);
     if (rc != GLA_OK) return rc;
     if (n > 0 && !rows) return GLA_ERR_NULL_ARG;
     if (bad_int(rows)) return GLA_ERR_MISALIGNED;
-    const Range outs[3] = {{table, R * M * 4}, {free_stack, P * 4}, {count, 4}};
-    const Range in{rows, n * 4};
-    if ((rc = check_alias(outs, 3, &in, 1)) != GLA_OK) return rc;
+    const Range used[4] = {{rows, n * 4}, {table, R * M * 4}, {free_stack, P * 4}, {count, 4}};
+    if ((rc = check_alias(used + 1, 3, used, 1)) != GLA_OK) return rc;
     int sms;
     unsigned *err;
     const int dev = gla::device_info(&sms, &err);
@@ -652,14 +670,20 @@ gla_status gla_pages_free(int64_t P, int32_t *table, int64_t R, int64_t M, int32
     gla::PagePool p{nullptr, P, 0, table, R, M, free_stack, count};
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     void *ws;
-    rc = (gla_status)gla::stream_workspace(s, std::max<size_t>((size_t)R * 4, 16), &ws);
+    rc = get_workspace(workspace, workspace_bytes, gla::pages_free_workspace(p), s, used, 4, &ws);
     if (rc != GLA_OK) return rc;
     const cudaError_t e = gla::launch_pages_free(p, rows, n, ws, err, s);
     return e == cudaSuccess ? GLA_OK : (gla_status)gla::launch_failed("page free launch", e);
 }
 
-gla_status gla_pages_compact(void *pool, int64_t P, int64_t page_bytes, int32_t *table, int64_t R,
-                             int64_t M, int32_t *free_stack, int32_t *count, gla_stream_t stream) {
+gla_status gla_pages_free(int64_t P, int32_t *table, int64_t R, int64_t M, int32_t *free_stack,
+                          int32_t *count, const int32_t *rows, int64_t n, gla_stream_t stream) {
+    return gla_pages_free_ex(P, table, R, M, free_stack, count, rows, n, nullptr, 0, stream);
+}
+
+gla_status gla_pages_compact_ex(void *pool, int64_t P, int64_t page_bytes, int32_t *table, int64_t R,
+                                int64_t M, int32_t *free_stack, int32_t *count, void *workspace,
+                                size_t workspace_bytes, gla_stream_t stream) {
     gla_status rc = check_pool(pool, P, page_bytes);
     if (rc == GLA_OK) rc = check_table(P, table, R, M, free_stack, count, 0);
     if (rc != GLA_OK) return rc;
@@ -673,10 +697,15 @@ gla_status gla_pages_compact(void *pool, int64_t P, int64_t page_bytes, int32_t 
     gla::PagePool p{pool, P, page_bytes, table, R, M, free_stack, count};
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     void *ws;
-    rc = (gla_status)gla::stream_workspace(s, gla::pages_compact_workspace(p), &ws);
+    rc = get_workspace(workspace, workspace_bytes, gla::pages_compact_workspace(p), s, outs, 4, &ws);
     if (rc != GLA_OK) return rc;
     const cudaError_t e = gla::launch_pages_compact(p, ws, sms, err, s);
     return e == cudaSuccess ? GLA_OK : (gla_status)gla::launch_failed("page compaction launch", e);
+}
+
+gla_status gla_pages_compact(void *pool, int64_t P, int64_t page_bytes, int32_t *table, int64_t R,
+                             int64_t M, int32_t *free_stack, int32_t *count, gla_stream_t stream) {
+    return gla_pages_compact_ex(pool, P, page_bytes, table, R, M, free_stack, count, nullptr, 0, stream);
 }
 
 }  // extern "C"

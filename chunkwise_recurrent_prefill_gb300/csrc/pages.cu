@@ -297,6 +297,7 @@ cudaError_t launch_moves(const PagePool &p, const int *n_moves, const Move *move
 size_t pages_fork_workspace(const PagePool &p, int64_t n) {
     return (size_t)(2 + p.R + n + 2 * n * p.M + 2) * 4;
 }
+size_t pages_free_workspace(const PagePool &p) { return (size_t)(p.R > 4 ? p.R : 4) * 4; }
 size_t pages_compact_workspace(const PagePool &p) { return (size_t)(2 + 4 * p.P) * 4; }
 
 cudaError_t launch_pages_copy(const PagePool &p, const int *src, const int *dst, int64_t n,

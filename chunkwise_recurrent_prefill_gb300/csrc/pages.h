@@ -15,8 +15,9 @@ struct PagePool {
     int *free_stack, *count;
 };
 
-// ws: pages_workspace_bytes() bytes (the moves planned on the device, and marks).
+// ws: so many bytes, 16-byte aligned (the moves planned on the device, and marks).
 size_t pages_fork_workspace(const PagePool &p, int64_t n);
+size_t pages_free_workspace(const PagePool &p);
 size_t pages_compact_workspace(const PagePool &p);
 cudaError_t launch_pages_copy(const PagePool &p, const int *src, const int *dst, int64_t n,
                               int num_sms, unsigned int *dev_err, cudaStream_t s);

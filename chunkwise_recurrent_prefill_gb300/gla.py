@@ -118,18 +118,25 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
             lib.gla_group_norm_fwd.argtypes = [vp] * 7 + [ns, vp, ctypes.c_size_t, vp]
             lib.gla_group_norm_bwd.argtypes = [vp] * 11 + [ns, vp, ctypes.c_size_t, vp]
             lib.gla_pages_copy.argtypes = [vp, i64, i64, vp, vp, i64, vp]
-            lib.gla_pages_fork.argtypes = [vp, i64, i64, vp, i64, i64, vp, vp, vp, vp, i64, vp]
-            lib.gla_pages_free.argtypes = [i64, vp, i64, i64, vp, vp, vp, i64, vp]
-            lib.gla_pages_compact.argtypes = [vp, i64, i64, vp, i64, i64, vp, vp, vp]
+            fork = [vp, i64, i64, vp, i64, i64, vp, vp, vp, vp, i64]
+            free = [i64, vp, i64, i64, vp, vp, vp, i64]
+            compact = [vp, i64, i64, vp, i64, i64, vp, vp]
+            ws = [vp, ctypes.c_size_t]
+            lib.gla_pages_fork.argtypes, lib.gla_pages_fork_ex.argtypes = fork + [vp], fork + ws + [vp]
+            lib.gla_pages_free.argtypes, lib.gla_pages_free_ex.argtypes = free + [vp], free + ws + [vp]
+            lib.gla_pages_compact.argtypes = compact + [vp]
+            lib.gla_pages_compact_ex.argtypes = compact + ws + [vp]
             for f in (lib.hda_fwd, lib.hda_bwd, lib.hda_step, lib.hda_path_for,
                       lib.gla_group_norm_fwd, lib.gla_group_norm_bwd, lib.gla_pages_copy,
-                      lib.gla_pages_fork, lib.gla_pages_free, lib.gla_pages_compact):
+                      lib.gla_pages_fork, lib.gla_pages_free, lib.gla_pages_compact,
+                      lib.gla_pages_fork_ex, lib.gla_pages_free_ex, lib.gla_pages_compact_ex):
                 f.restype = ctypes.c_int
             lib.hda_fwd_workspace_size.argtypes = [hs, opt]
             lib.hda_bwd_workspace_size.argtypes = [hs, opt]
             lib.gla_group_norm_workspace_size.argtypes = [ns, ctypes.c_int]
+            lib.gla_pages_workspace_size.argtypes = [i64, i64, i64, i64]
             for f in (lib.hda_fwd_workspace_size, lib.hda_bwd_workspace_size,
-                      lib.gla_group_norm_workspace_size):
+                      lib.gla_group_norm_workspace_size, lib.gla_pages_workspace_size):
                 f.restype = ctypes.c_size_t
             _lib = lib
     return _lib

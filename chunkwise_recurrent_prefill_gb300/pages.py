@@ -4,6 +4,9 @@ contracts). All bookkeeping is int32 on the device; nothing is read back by thes
     pool  [P, ...]  P pages (any dtype; a page is a multiple of 16 bytes)
     table [R, M]    the pages of each row, negative where there is none
     free  [P]       stack of free pages, ``count`` [1] of them, the top last
+
+Planning needs a little scratch: a ``workspace`` of the caller's (any type, at least
+``pages_workspace_size`` bytes), or the library's own of the stream.
 """
 from __future__ import annotations
 
@@ -11,6 +14,7 @@ import torch
 
 from .gla import _check, _addr, _launch, _on_stream, load_library
 from .hda import _fail
+from .norm import _workspace
 
 
 def _pool(pool):
@@ -54,25 +58,36 @@ def pages_copy(pool, src, dst, *, stream=None):
     _fail(lib, rc, "gla_pages_copy")
 
 
-def pages_fork(pool, table, free, count, parents, children, *, stream=None):
+def pages_workspace_size(table, free, requests: int = 0) -> int:
+    """Bytes of workspace that are enough for each of the calls below, with up to ``requests`` parents
+    or rows."""
+    if table.dim() != 2:
+        raise ValueError("table must be [R, M]")
+    R, M = table.shape
+    return int(load_library().gla_pages_workspace_size(free.numel(), R, M, requests))
+
+
+def pages_fork(pool, table, free, count, parents, children, *, workspace=None, stream=None):
     """Rows ``children`` become copies of rows ``parents`` on pages taken from the stack."""
     if stream is not None:
-        return _on_stream(stream, pages_fork, pool, table, free, count, parents, children)
+        return _on_stream(stream, pages_fork, pool, table, free, count, parents, children,
+                          workspace=workspace)
     lib = load_library()
     P, nb = _pool(pool)
     R, M = _book(table, free, count, P, pool.device)
     n = parents.numel()
     _ints(parents, "parents", pool.device)
     _ints(children, "children", pool.device, (n,))
-    rc = _launch(lib.gla_pages_fork, pool.device, _addr(pool), P, nb, _addr(table), R, M,
-                 _addr(free), _addr(count), _addr(parents), _addr(children), n)
+    rc = _launch(lib.gla_pages_fork_ex, pool.device, _addr(pool), P, nb, _addr(table), R, M,
+                 _addr(free), _addr(count), _addr(parents), _addr(children), n,
+                 *_workspace(workspace, pool.device))
     _fail(lib, rc, "gla_pages_fork")
 
 
-def pages_free(table, free, count, rows, *, stream=None):
+def pages_free(table, free, count, rows, *, workspace=None, stream=None):
     """The pages of ``rows`` go back on the stack; the rows have none afterwards."""
     if stream is not None:
-        return _on_stream(stream, pages_free, table, free, count, rows)
+        return _on_stream(stream, pages_free, table, free, count, rows, workspace=workspace)
     lib = load_library()
     dev = table.device
     if dev.type != "cuda":
@@ -80,18 +95,18 @@ def pages_free(table, free, count, rows, *, stream=None):
     P = free.numel()
     R, M = _book(table, free, count, P, dev)
     _ints(rows, "rows", dev)
-    rc = _launch(lib.gla_pages_free, dev, P, _addr(table), R, M, _addr(free), _addr(count),
-                 _addr(rows), rows.numel())
+    rc = _launch(lib.gla_pages_free_ex, dev, P, _addr(table), R, M, _addr(free), _addr(count),
+                 _addr(rows), rows.numel(), *_workspace(workspace, dev))
     _fail(lib, rc, "gla_pages_free")
 
 
-def pages_compact(pool, table, free, count, *, stream=None):
+def pages_compact(pool, table, free, count, *, workspace=None, stream=None):
     """The live pages move down to 0 .. n-1; the table follows, the stack is rebuilt."""
     if stream is not None:
-        return _on_stream(stream, pages_compact, pool, table, free, count)
+        return _on_stream(stream, pages_compact, pool, table, free, count, workspace=workspace)
     lib = load_library()
     P, nb = _pool(pool)
     R, M = _book(table, free, count, P, pool.device)
-    rc = _launch(lib.gla_pages_compact, pool.device, _addr(pool), P, nb, _addr(table), R, M,
-                 _addr(free), _addr(count))
+    rc = _launch(lib.gla_pages_compact_ex, pool.device, _addr(pool), P, nb, _addr(table), R, M,
+                 _addr(free), _addr(count), *_workspace(workspace, pool.device))
     _fail(lib, rc, "gla_pages_compact")

@@ -443,6 +443,20 @@ gla_status gla_pages_free(int64_t P, int32_t *table, int64_t R, int64_t M, int32
 gla_status gla_pages_compact(void *pool, int64_t P, int64_t page_bytes, int32_t *table, int64_t R,
                              int64_t M, int32_t *free_stack, int32_t *count, gla_stream_t stream);
 
+/* The same with a workspace of the caller's (16-byte aligned; NULL: the library's, of the stream). */
+gla_status gla_pages_fork_ex(void *pool, int64_t P, int64_t page_bytes, int32_t *table, int64_t R,
+                             int64_t M, int32_t *free_stack, int32_t *count, const int32_t *parents,
+                             const int32_t *children, int64_t n, void *workspace,
+                             size_t workspace_bytes, gla_stream_t stream);
+gla_status gla_pages_free_ex(int64_t P, int32_t *table, int64_t R, int64_t M, int32_t *free_stack,
+                             int32_t *count, const int32_t *rows, int64_t n, void *workspace,
+                             size_t workspace_bytes, gla_stream_t stream);
+gla_status gla_pages_compact_ex(void *pool, int64_t P, int64_t page_bytes, int32_t *table, int64_t R,
+                                int64_t M, int32_t *free_stack, int32_t *count, void *workspace,
+                                size_t workspace_bytes, gla_stream_t stream);
+/* Bytes that are enough for each of the three, with up to n requests (0 for sizes they refuse). */
+size_t gla_pages_workspace_size(int64_t P, int64_t R, int64_t M, int64_t n);
+
 /* Library ABI version: major * 10000 + minor * 100 + patch. */
 int gla_version(void);
 
