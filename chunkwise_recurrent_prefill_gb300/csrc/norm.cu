@@ -160,8 +160,9 @@ struct Stat {
 __device__ __forceinline__ Stat merge(const Stat &a, const Stat &b) {
     const float n = a.n + b.n;
     if (n == 0.f) return a;
-    const float d = b.mean - a.mean, f = b.n / n;
-    return Stat{n, fmaf(d, f, a.mean), a.m2 + b.m2 + d * d * a.n * f};
+    const float d = b.mean - a.mean, f = b.n / n, w = a.n * f;
+    // (d w before d d: with an empty part w is zero, where d d may be infinite and 0 d d NaN)
+    return Stat{n, fmaf(d, f, a.mean), fmaf(d * w, d, a.m2 + b.m2)};
 }
 __device__ __forceinline__ Stat merge_lanes(Stat s, int width) {
     for (int o = width >> 1; o > 0; o >>= 1) {
