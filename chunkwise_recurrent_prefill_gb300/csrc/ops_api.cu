@@ -524,7 +524,15 @@ gla_status gla_group_norm_fwd(const void *x, const float *w, const float *b, con
     unsigned *err;
     const int dev = gla::device_info(&sms, &err);
     if (dev != GLA_OK) return (gla_status)dev;
-    if (by == 0) return GLA_OK;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (by == 0) {   // statistics of nothing: 0 / 0 (all bits set is a NaN)
+        for (float *d : {mean, rstd}) {
+            if (!d || p.N * p.G == 0) continue;
+            const cudaError_t e = cudaMemsetAsync(d, 0xff, (size_t)(p.N * p.G) * 4, s);
+            if (e != cudaSuccess) return (gla_status)gla::launch_failed("group norm launch", e);
+        }
+        return GLA_OK;
+    }
     p.x = x;
     p.w = w;
     p.b = b;
@@ -532,7 +540,6 @@ gla_status gla_group_norm_fwd(const void *x, const float *w, const float *b, con
     p.y = y;
     p.mean = mean;
     p.rstd = rstd;
-    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     void *ws;
     rc = get_workspace(workspace, workspace_bytes, gla::norm_workspace_bytes(p, false, sms), s, used,
                        7, &ws);

@@ -397,7 +397,8 @@ typedef struct {
     int io;                    /* gla_io  */
 } gla_norm_shape;
 
-/* y, mean, rstd are written; mean and rstd may be NULL when no backward pass follows. */
+/* y, mean, rstd are written; mean and rstd may be NULL when no backward pass follows. Where there are
+ * no values (L = 0) they are NaN. */
 gla_status gla_group_norm_fwd(const void *x, const float *w, const float *b, const void *gate,
                               void *y, float *mean, float *rstd, const gla_norm_shape *shape,
                               void *workspace, size_t workspace_bytes, gla_stream_t stream);

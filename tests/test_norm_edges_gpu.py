@@ -1,4 +1,5 @@
-"""Group norm at the edges of its range: means whose square is beyond the largest float."""
+"""Group norm at the edges of its range: means whose square is beyond the largest float, and no values
+at all."""
 import pytest
 import torch
 
@@ -38,3 +39,14 @@ def test_equal_values_beyond_the_root_of_the_range(shape, G, io, value):
     # the mean of up to 10^5 terms and three roundings of terms of 5 or so, and bf16's own
     tol = 1e-5 + (2.0 ** -8 * want.abs() if io == torch.bfloat16 else 0)
     assert ((dx.double() - want).abs() <= tol).all()
+
+
+def test_statistics_of_no_values():
+    """mean and rstd of no positions are the formula's 0 / 0, not what the memory held."""
+    from chunkwise_recurrent_prefill_gb300 import group_norm_fwd
+    for shape in ((2, 0, 32), (3, 4, 0, 8)):
+        held = [torch.full((shape[0], 4), 7.0, device="cuda") for _ in range(4)]
+        del held        # (what the allocator hands out again)
+        _, mean, rstd = group_norm_fwd(torch.zeros(*shape, device="cuda"), 4)
+        assert mean.shape == rstd.shape == (shape[0], 4)
+        assert mean.isnan().all() and rstd.isnan().all()
