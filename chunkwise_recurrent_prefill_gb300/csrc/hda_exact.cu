@@ -105,11 +105,12 @@ hda_exact_kernel(const __grid_constant__ HdaProblem p, const Segs sg) {
     __shared__ __align__(16) float xs[kState ? 1 : 2][kState ? 4 : TB * W], ys[2][TB * W], zs[2][TB * kCols];
     __shared__ float os[kState ? 1 : TB][kCols];
     if (kState) tc::pdl_launch_dependents();
-    const HdaLin &m = p.lin[blockIdx.z];
+    const int li = blockIdx.z % p.n;
+    const int64_t bh = (int64_t)(blockIdx.z / p.n) * gridDim.y + blockIdx.y, b = bh / p.H, h = bh % p.H;
+    const HdaLin &m = p.lin[li];
     const int zb = blockIdx.x % sg.zblocks, seg = blockIdx.x / sg.zblocks, z0 = zb * kCols;
-    if (z0 >= m.Dz) return;
+    if (z0 >= m.Dz || b >= p.B) return;
     const int64_t begin = seg * sg.len, end = min(begin + sg.len, p.T);
-    const int64_t bh = blockIdx.y, b = bh / p.H, h = bh % p.H;
     const int lane = threadIdx.x & 31;
     // lanes 8 c .. 8 c + 7 of a warp are the row groups of NC columns; a row group's rows come
     // in fours, interleaved with the other groups', so that 16-byte reads of x and y meet no
@@ -135,7 +136,7 @@ hda_exact_kernel(const __grid_constant__ HdaProblem p, const Segs sg) {
             (k & 1 ? s[c][k / 2].y : s[c][k / 2].x) = v;
         }
     constexpr int kPer = NC * RPT / 2;      // pairs of a thread
-    float2 *E = sg.E + (((blockIdx.z * p.B * p.H + bh) * (sg.n - 1)) * sg.zblocks + zb) * (kPer * kThreads) +
+    float2 *E = sg.E + (((li * p.B * p.H + bh) * (sg.n - 1)) * sg.zblocks + zb) * (kPer * kThreads) +
                 threadIdx.x;
     const int64_t e_seg = (int64_t)sg.zblocks * (kPer * kThreads);
     if (!kState && seg > 0) {
@@ -340,7 +341,6 @@ ExactPlan exact_plan(const HdaProblem &p, int splits, int sms) {
         const int cols = wide ? (dx <= 128 ? 4 : 2) : 1, zblocks = (dz + 16 * cols - 1) / (16 * cols);
         const double ctas = (double)(p.B * p.H * p.n) * zblocks, token = wide ? 270 : 122, share = wide ? 1.9 : 1.2;
         int most = (int)min(p.T / (2 * kTile), (int64_t)kMostSegs);
-        if (p.B * p.H > 65535) most = 1;
         if (splits > 0) most = min(splits, kMostSegs);
         for (int n = splits > 0 ? most : 1; n <= max(most, 1); ++n) {
             const double walk = token * (double)p.T / n * max(1.0, ctas * n / (share * sms));
@@ -361,7 +361,9 @@ int64_t pairs_per_segment(const ExactPlan &e) { return (int64_t)e.g.zblocks * e.
 
 template <typename T, int RPT, int NC, int TB>
 cudaError_t launch_walk(const HdaProblem &p, const Segs &g, cudaStream_t s) {
-    dim3 grid(g.zblocks * g.n, (unsigned)(p.B * p.H), p.n);
+    // heads of all entries in y, what exceeds its limit in z beside the maps
+    const int64_t bh = p.B * p.H, rows = min(bh, (int64_t)65535);
+    dim3 grid(g.zblocks * g.n, (unsigned)rows, (unsigned)((bh + rows - 1) / rows * p.n));
     cudaLaunchAttribute pdl[1];
     pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     pdl[0].val.programmaticStreamSerializationAllowed = 1;
@@ -391,30 +393,10 @@ cudaError_t run_exact(const HdaProblem &p, int splits, int sms, void *ws, cudaSt
     ExactPlan plan = exact_plan(p, splits, sms);
     const Segs &g = plan.g;
     plan.g.E = static_cast<float2 *>(ws);
-    // the batch entries are cut so that the grid's y dimension stays within its limit
-    const int64_t most = 65535 / p.H > 0 ? 65535 / p.H : 1;
-    for (int64_t b0 = 0; b0 < p.B; b0 += most) {
-        HdaProblem c = p;
-        c.B = min(most, p.B - b0);
-        for (int i = 0; i < p.n; ++i) {
-            HdaLin &m = c.lin[i];
-            for (HdaTensor *t : {&m.x, &m.y, &m.z}) t->p = static_cast<const T *>(t->p) + b0 * t->b;
-            const int64_t st = b0 * p.H * m.Dx * m.Dz, ot = b0 * p.T * p.H * m.Dz;
-            if (m.init) m.init += st;
-            if (m.fin) m.fin += st;
-            m.out = static_cast<char *>(m.out) + ot * (m.out_f32 ? 4 : (int64_t)sizeof(T));
-        }
-        const bool one = plan.cols == 1;
-        cudaError_t e;
-        if (plan.rows == 8)
-            e = one ? launch_walk<T, 8, 1, kTile>(c, g, s) : launch_walk<T, 8, 4, kTile>(c, g, s);
-        else if (plan.rows == 16)
-            e = one ? launch_walk<T, 16, 1, kTile>(c, g, s) : launch_walk<T, 16, 4, kTile>(c, g, s);
-        else
-            e = one ? launch_walk<T, 32, 1, kTile / 2>(c, g, s) : launch_walk<T, 32, 2, kTile / 2>(c, g, s);
-        if (e != cudaSuccess) return e;
-    }
-    return cudaSuccess;
+    const bool one = plan.cols == 1;
+    if (plan.rows == 8) return one ? launch_walk<T, 8, 1, kTile>(p, g, s) : launch_walk<T, 8, 4, kTile>(p, g, s);
+    if (plan.rows == 16) return one ? launch_walk<T, 16, 1, kTile>(p, g, s) : launch_walk<T, 16, 4, kTile>(p, g, s);
+    return one ? launch_walk<T, 32, 1, kTile / 2>(p, g, s) : launch_walk<T, 32, 2, kTile / 2>(p, g, s);
 }
 
 }  // namespace
