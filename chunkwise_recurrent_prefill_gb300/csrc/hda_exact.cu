@@ -3,9 +3,9 @@
 //
 // The columns of the state are independent (out_t[z] needs S[:, z] alone), so a CTA owns 16 NC of
 // them for one head and walks the tokens with its part of S in registers: a thread holds RPT rows of
-// NC columns (packed in pairs of rows), 8 threads the rows of a column. A token costs it three
-// multiply-adds per element of S; with one column per thread the reads of x and y from shared memory
-// took three times as long as these. Nothing but the state's own multiply-add chain is serial. The
+// NC columns (packed in pairs of rows), 8 threads the rows of a column. A token costs it two
+// multiply-adds per element of S, or three where the decay is fast; with one column per thread the reads of x and y from shared memory
+// took three times as long as these. Nothing but the state's own addition chain is serial. The
 // sums over the 8 row groups are formed for 8 (token, column) pairs at once, in 7 shuffles. x, y and
 // z are staged as fp32 in shared memory TB tokens at a time, the next tile being loaded meanwhile.
 //
@@ -24,20 +24,20 @@ namespace gla {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr float kSlow = -0.5f;     // log-decays above it use l - 1 (see below)
+constexpr float kSlow = 0.5f;      // log-decays below it, of either sign, are applied by the tile (see below)
 
 template <typename T>
 struct Vec;
 template <>
 struct Vec<__nv_bfloat16> {
     static constexpr int n = 8;
-    static __device__ __forceinline__ void store(float *dst, uint4 v) {
+    static __device__ __forceinline__ void store(float *dst, uint4 v, float by = 1.f) {
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
         float f[8];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            f[2 * i] = __uint_as_float(w[i] << 16);
-            f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+            f[2 * i] = by * __uint_as_float(w[i] << 16);
+            f[2 * i + 1] = by * __uint_as_float(w[i] & 0xffff0000u);
         }
         *reinterpret_cast<float4 *>(dst) = make_float4(f[0], f[1], f[2], f[3]);
         *reinterpret_cast<float4 *>(dst + 4) = make_float4(f[4], f[5], f[6], f[7]);
@@ -46,8 +46,9 @@ struct Vec<__nv_bfloat16> {
 template <>
 struct Vec<float> {
     static constexpr int n = 4;
-    static __device__ __forceinline__ void store(float *dst, uint4 v) {
-        *reinterpret_cast<uint4 *>(dst) = v;
+    static __device__ __forceinline__ void store(float *dst, uint4 v, float by = 1.f) {
+        *reinterpret_cast<float4 *>(dst) = make_float4(by * __uint_as_float(v.x), by * __uint_as_float(v.y),
+                                                       by * __uint_as_float(v.z), by * __uint_as_float(v.w));
     }
 };
 
@@ -88,6 +89,14 @@ struct Tile {
             if (e < kVecs) Vec<T>::store(dst + (e / (W / V)) * W + (e % (W / V)) * V, r[a]);
         }
     }
+    // each token times its factor
+    __device__ __forceinline__ void store(float *dst, const float *by) const {
+#pragma unroll
+        for (int a = 0; a < kPer; ++a) {
+            const int e = threadIdx.x + a * kThreads, row = e / (W / V);
+            if (e < kVecs) Vec<T>::store(dst + row * W + (e % (W / V)) * V, r[a], by[row]);
+        }
+    }
 };
 
 struct Segs {
@@ -104,6 +113,7 @@ hda_exact_kernel(const __grid_constant__ HdaProblem p, const Segs sg) {
     constexpr int kCols = 16 * NC, G = 8 / NC; // columns of the CTA; tokens at a time
     __shared__ __align__(16) float xs[kState ? 1 : 2][kState ? 4 : TB * W], ys[2][TB * W], zs[2][TB * kCols];
     __shared__ float os[kState ? 1 : TB][kCols];
+    __shared__ float pw[TB + 1], zf[2 * TB], of[TB];    // l^i; factors of z and of the outputs
     if (kState) tc::pdl_launch_dependents();
     const int li = blockIdx.z % p.n;
     const int64_t bh = (int64_t)(blockIdx.z / p.n) * gridDim.y + blockIdx.y, b = bh / p.H, h = bh % p.H;
@@ -146,11 +156,21 @@ hda_exact_kernel(const __grid_constant__ HdaProblem p, const Segs sg) {
     }
 
     // Reversed passes start from a state that already carries the step's decay: their first
-    // token applies none. l s is formed as s + (l - 1) s for slow decays: l - 1 = expm1(g) is
-    // known to 2^-24 of itself, so that a token's weight after n steps is off by 2^-24 n |g|,
-    // not by 2^-24 n. Fast decays multiply by l itself (l = 0 leaves exactly the new token).
-    const bool slow = g > kSlow;
-    const float lam = expf(g), lm1 = expm1f(g);
+    // token applies none. Slow decays are applied by the tile: within one the state is kept as it
+    // will have decayed at the tile's end, S' = l^r S with r tokens left, so that S is multiplied once
+    // in a tile, a token adds y (l^r z), and its output is l^-r (x S'). (l itself for every token would
+    // be off by 2^-25 each time, always the same way; l S as S + (l - 1) S is NaN for an infinite S.)
+    // Fast decays multiply by l itself (l = 0 leaves exactly the new token).
+    const bool slow = fabsf(g) < kSlow;
+    const float lam = expf(g);
+    // Token i of a tile of nt is row i + TB - nt of the factors (rows past its end: any number).
+    if (threadIdx.x < 2 * TB) {
+        const int r = max(TB - 1 - (int)threadIdx.x, 0);
+        zf[threadIdx.x] = m.a_in * (slow ? decay_pow(g, (float)r) : 1.f);
+        if (threadIdx.x < TB) of[threadIdx.x] = m.a_out * (slow ? decay_pow(-g, (float)r) : 1.f);
+        if (threadIdx.x <= TB) pw[threadIdx.x] = decay_pow(g, (float)threadIdx.x);
+    }
+    __syncthreads();
     Tile<T, TB, W> tx, ty;
     Tile<T, TB, kCols> tz;
     const int zw = min(kCols, m.Dz - z0);
@@ -159,16 +179,23 @@ hda_exact_kernel(const __grid_constant__ HdaProblem p, const Segs sg) {
     tz.load(zp, m.z.t, begin, end, p.T, rev, zw);
     int buf = 0;
     for (int64_t i0 = begin; i0 < end; i0 += TB, buf ^= 1) {
+        const int nt = (int)min((int64_t)TB, end - i0);
         if (!kState) tx.store(xs[buf]);
         ty.store(ys[buf]);
-        tz.store(zs[buf]);
+        tz.store(zs[buf], zf + TB - nt);
         __syncthreads();
         if (i0 + TB < end) {
             if (!kState) tx.load(xp, m.x.t, i0 + TB, end, p.T, rev, m.Dx);
             ty.load(yp, m.y.t, i0 + TB, end, p.T, rev, m.Dx);
             tz.load(zp, m.z.t, i0 + TB, end, p.T, rev, zw);
         }
-        const int nt = (int)min((int64_t)TB, end - i0);
+        if (slow) {
+            const float f = pw[rev && i0 == 0 ? nt - 1 : nt];
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+#pragma unroll
+                for (int k = 0; k < RPT / 2; ++k) s[c][k] = tc::mul2(make_float2(f, f), s[c][k]);
+        }
         auto walk = [&](auto is_slow) {
 #pragma unroll 1
             for (int i8 = 0; i8 < nt; i8 += G) {
@@ -179,9 +206,9 @@ hda_exact_kernel(const __grid_constant__ HdaProblem p, const Segs sg) {
                     // end is all zeros and applies no decay.)
                     float zt[NC];
 #pragma unroll
-                    for (int c = 0; c < NC; ++c) zt[c] = m.a_in * zs[buf][(i8 + i) * kCols + col + c];
+                    for (int c = 0; c < NC; ++c) zt[c] = zs[buf][(i8 + i) * kCols + col + c];
                     const bool none = i8 + i >= nt || (rev && i0 + i8 + i == 0);
-                    const float f = none ? (is_slow ? 0.f : 1.f) : (is_slow ? lm1 : lam);
+                    const float f = none ? 1.f : lam;
                     const float2 ff = make_float2(f, f);
                     float2 part[NC];
 #pragma unroll
@@ -200,8 +227,7 @@ hda_exact_kernel(const __grid_constant__ HdaProblem p, const Segs sg) {
                             for (int c = 0; c < NC; ++c) {
                                 float2 &sk = s[c][2 * k4 + e];
                                 const float2 zz = make_float2(zt[c], zt[c]);
-                                sk = is_slow ? tc::fma2(ff, sk, tc::fma2(yv[e], zz, sk))
-                                             : tc::fma2(ff, sk, tc::mul2(yv[e], zz));
+                                sk = is_slow ? tc::fma2(yv[e], zz, sk) : tc::fma2(ff, sk, tc::mul2(yv[e], zz));
                                 if (!kState) part[c] = tc::fma2(xv[e], sk, part[c]);
                             }
                     }
@@ -219,7 +245,7 @@ hda_exact_kernel(const __grid_constant__ HdaProblem p, const Segs sg) {
                             const float keep = up ? acc[i + n] : acc[i], give = up ? acc[i] : acc[i + n];
                             acc[i] = keep + __shfl_xor_sync(0xffffffffu, give, n);
                         }
-                    os[i8 + rg / NC][col + rg % NC] = m.a_out * acc[0];
+                    os[i8 + rg / NC][col + rg % NC] = acc[0];
                 }
             }
         };
@@ -232,8 +258,9 @@ hda_exact_kernel(const __grid_constant__ HdaProblem p, const Segs sg) {
             if (z0 + c >= m.Dz) continue;
             const int64_t t = rev ? p.T - 1 - (i0 + i) : i0 + i;
             const int64_t at = ((b * p.T + t) * p.H + h) * m.Dz + z0 + c;
-            if (m.out_f32) static_cast<float *>(m.out)[at] = os[i][c];
-            else put(static_cast<T *>(m.out) + at, os[i][c]);
+            const float v = of[i + TB - nt] * os[i][c];
+            if (m.out_f32) static_cast<float *>(m.out)[at] = v;
+            else put(static_cast<T *>(m.out) + at, v);
         }
     }
     if (kState) {
@@ -248,7 +275,7 @@ hda_exact_kernel(const __grid_constant__ HdaProblem p, const Segs sg) {
         for (int k = 0; k < RPT; ++k) {
             const int r = row_of(k), z = z0 + col + c;
             float v = k & 1 ? s[c][k / 2].y : s[c][k / 2].x;
-            if (rev && p.T > 0) v = slow ? fmaf(lm1, v, v) : lam * v;
+            if (rev) v *= lam;
             if (z < m.Dz && r < m.Dx)
                 m.fin[bh * m.Dx * m.Dz + (m.fin_t ? (int64_t)z * m.Dx + r : (int64_t)r * m.Dz + z)] = v;
         }
@@ -262,7 +289,8 @@ hda_exact_scan_kernel(const float *__restrict__ decay, int64_t H, const Segs sg,
     const int64_t e = (int64_t)blockIdx.x * kThreads + threadIdx.x;
     if (e >= pairs) return;
     const int64_t mbh = e / per_seg;        // map and head
-    const float f = decay_pow(decay[mbh % H], (float)sg.len);
+    // (not below the least positive float unless l is zero: an infinite state stays infinite)
+    const float g = decay[mbh % H], f = fmaxf(decay_pow(g, (float)sg.len), expf(g) > 0.f ? 0x1p-149f : 0.f);
     float2 *E = sg.E + mbh * (sg.n - 1) * per_seg + e % per_seg;
     tc::pdl_wait_prerequisites();
     float2 s = make_float2(0.f, 0.f);
