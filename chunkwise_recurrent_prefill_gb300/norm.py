@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import operator
 
 import torch
 
@@ -56,7 +57,7 @@ def _plan(groups, eps, act, x, gate, dy) -> _NormShape:
     if act not in ACTS:
         raise ValueError(f"act must be one of {sorted(ACTS)}")
     sh = _NormShape()
-    sh.N, sh.C, sh.G = shape[0], shape[-1], int(groups)
+    sh.N, sh.C, sh.G = shape[0], shape[-1], operator.index(groups)
     sh.L = 1
     for n in shape[1:-1]:
         sh.L *= n

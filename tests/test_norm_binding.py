@@ -35,3 +35,9 @@ def test_strides_of_views():
     assert norm._shape(one, 4, 1e-5, "none", None).L == 1
     sh = norm._shape(torch.zeros(4, 1, 16).as_strided((4, 1, 16), (16, 0, 1)), 4, 1e-5, "none", None)
     assert (sh.x_n, sh.x_l) == (16, 16)
+
+
+@pytest.mark.parametrize("groups", [2.5, 2.0, "2", None])
+def test_groups_that_are_not_whole_numbers_are_refused(groups):
+    with pytest.raises(TypeError):
+        norm._shape(torch.zeros(3, 16), groups, 1e-5, "none", None)
