@@ -57,7 +57,7 @@ def _plan(groups, eps, act, x, gate, dy) -> _NormShape:
     if act not in ACTS:
         raise ValueError(f"act must be one of {sorted(ACTS)}")
     sh = _NormShape()
-    sh.N, sh.C, sh.G = shape[0], shape[-1], operator.index(groups)
+    sh.N, sh.C, sh.G = shape[0], shape[-1], groups
     sh.L = 1
     for n in shape[1:-1]:
         sh.L *= n
@@ -79,7 +79,7 @@ def _shape(x, groups, eps, act, gate, dy=None) -> _NormShape:
         if t is not None and t.device != x.device:
             raise ValueError(f"{n}: on {t.device}, expected {x.device}")
         key.append(None if t is None else (t.shape, t.stride(), t.dtype))
-    return _plan(groups, eps, act, *key)
+    return _plan(operator.index(groups), eps, act, *key)
 
 
 def _affine(x, weight, bias):

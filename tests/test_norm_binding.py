@@ -39,5 +39,6 @@ def test_strides_of_views():
 
 @pytest.mark.parametrize("groups", [2.5, 2.0, "2", None])
 def test_groups_that_are_not_whole_numbers_are_refused(groups):
+    norm._shape(torch.zeros(3, 16), 2, 1e-5, "none", None)     # (a shape that has been seen with 2)
     with pytest.raises(TypeError):
         norm._shape(torch.zeros(3, 16), groups, 1e-5, "none", None)
