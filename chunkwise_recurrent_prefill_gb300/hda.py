@@ -67,10 +67,14 @@ def _plan(step, H, dtype, tensors) -> _HdaShape:
     return sh
 
 
+def _tensor(t, name):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+
+
 def _shape(q, k, v, decay, do=None, step=False):
     for t, n in ((q, "q"), (k, "k"), (v, "v"), (decay, "decay")):
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{n} must be a torch.Tensor")
+        _tensor(t, n)
     ts = ((q.shape, q.stride(), q.dtype), (k.shape, k.stride(), k.dtype), (v.shape, v.stride(), v.dtype))
     if do is not None:
         ts += ((do.shape, do.stride(), do.dtype),)
@@ -111,10 +115,9 @@ def hda_fwd(q, k, v, decay, scale: float, h0=None, *, o=None, hT=None, return_st
                           return_state=return_state, path=path, seq_splits=seq_splits,
                           workspace=workspace)
     lib = load_library()
-    H = decay.numel()
     sh = _shape(q, k, v, decay)
     dev = _check_inputs(q, k, v, decay)
-    B, T, Dk, Dv = sh.B, sh.T, sh.Dk, sh.Dv
+    B, T, H, Dk, Dv = sh.B, sh.T, sh.H, sh.Dk, sh.Dv
     _state(h0, "h0", (B, H, Dk, Dv), dev)
     if o is None:
         o = torch.empty((B, T, H, Dv), dtype=q.dtype, device=dev)
@@ -139,12 +142,12 @@ def hda_bwd(do, q, k, v, decay, scale: float, h0=None, dhT=None, *, path: str = 
         return _on_stream(stream, hda_bwd, do, q, k, v, decay, scale, h0, dhT, path=path,
                           seq_splits=seq_splits, workspace=workspace)
     lib = load_library()
-    H = decay.numel()
+    _tensor(do, "do")
     sh = _shape(q, k, v, decay, do)
     dev = _check_inputs(q, k, v, decay)
     if do.device != dev:
         raise ValueError(f"do: on {do.device}, expected {dev}")
-    B, Dk, Dv = sh.B, sh.Dk, sh.Dv
+    B, H, Dk, Dv = sh.B, sh.H, sh.Dk, sh.Dv
     _state(h0, "h0", (B, H, Dk, Dv), dev)
     _state(dhT, "dhT", (B, H, Dk, Dv), dev)
     dq, dk, dv = (torch.empty(t.shape, dtype=t.dtype, device=dev) for t in (q, k, v))
@@ -181,11 +184,11 @@ def hda_step(q, k, v, decay, scale: float, S, slots=None, *, o=None, stream=None
     if stream is not None:
         return _on_stream(stream, hda_step, q, k, v, decay, scale, S, slots, o=o)
     lib = load_library()
-    H = decay.numel()
     sh = _shape(q, k, v, decay, step=True)
     dev = _check_inputs(q, k, v, decay)
-    R, Dk, Dv = sh.B, sh.Dk, sh.Dv
-    P = S.shape[0]
+    R, H, Dk, Dv = sh.B, sh.H, sh.Dk, sh.Dv
+    _tensor(S, "S")
+    P = S.shape[0] if S.dim() else 0
     _check(S, "S", torch.float32, (P, H, Dk, Dv), dev)
     if slots is not None:
         _check(slots, "slots", torch.int32, (R,), dev)

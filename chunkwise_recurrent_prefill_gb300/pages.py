@@ -13,13 +13,12 @@ from __future__ import annotations
 import torch
 
 from .gla import _check, _addr, _launch, _on_stream, load_library
-from .hda import _fail
+from .hda import _fail, _tensor
 from .norm import _workspace
 
 
 def _pool(pool):
-    if not isinstance(pool, torch.Tensor):
-        raise TypeError("pool must be a torch.Tensor")
+    _tensor(pool, "pool")
     if pool.device.type != "cuda":
         raise ValueError("tensors must be on a CUDA device")
     if pool.dim() < 1 or not pool.is_contiguous():
@@ -32,11 +31,13 @@ def _pool(pool):
 
 
 def _ints(t, name, dev, shape=None):
+    _tensor(t, name)
     _check(t, name, torch.int32, (t.numel(),) if shape is None else shape, dev)
     return t
 
 
 def _book(table, free, count, P, dev):
+    _tensor(table, "table")
     if table.dim() != 2:
         raise ValueError("table must be [R, M]")
     _ints(table, "table", dev, table.shape)
@@ -51,8 +52,7 @@ def pages_copy(pool, src, dst, *, stream=None):
         return _on_stream(stream, pages_copy, pool, src, dst)
     lib = load_library()
     P, nb = _pool(pool)
-    n = src.numel()
-    _ints(src, "src", pool.device)
+    n = _ints(src, "src", pool.device).numel()
     _ints(dst, "dst", pool.device, (n,))
     rc = _launch(lib.gla_pages_copy, pool.device, _addr(pool), P, nb, _addr(src), _addr(dst), n)
     _fail(lib, rc, "gla_pages_copy")
@@ -61,6 +61,8 @@ def pages_copy(pool, src, dst, *, stream=None):
 def pages_workspace_size(table, free, requests: int = 0) -> int:
     """Bytes of workspace that are enough for each of the calls below, with up to ``requests`` parents
     or rows."""
+    for t, n in ((table, "table"), (free, "free")):
+        _tensor(t, n)
     if table.dim() != 2:
         raise ValueError("table must be [R, M]")
     R, M = table.shape
@@ -75,8 +77,7 @@ def pages_fork(pool, table, free, count, parents, children, *, workspace=None, s
     lib = load_library()
     P, nb = _pool(pool)
     R, M = _book(table, free, count, P, pool.device)
-    n = parents.numel()
-    _ints(parents, "parents", pool.device)
+    n = _ints(parents, "parents", pool.device).numel()
     _ints(children, "children", pool.device, (n,))
     rc = _launch(lib.gla_pages_fork_ex, pool.device, _addr(pool), P, nb, _addr(table), R, M,
                  _addr(free), _addr(count), _addr(parents), _addr(children), n,
@@ -89,6 +90,8 @@ def pages_free(table, free, count, rows, *, workspace=None, stream=None):
     if stream is not None:
         return _on_stream(stream, pages_free, table, free, count, rows, workspace=workspace)
     lib = load_library()
+    for t, n in ((table, "table"), (free, "free")):
+        _tensor(t, n)
     dev = table.device
     if dev.type != "cuda":
         raise ValueError("tensors must be on a CUDA device")
