@@ -1,5 +1,5 @@
-"""Group norm at the edges of its range: means whose square is beyond the largest float, and no values
-at all."""
+"""Group norm at the edges of its range: means whose square is beyond the largest float, no values at
+all, and gradients that their mean terms make up."""
 import pytest
 import torch
 
@@ -50,3 +50,88 @@ def test_statistics_of_no_values():
         _, mean, rstd = group_norm_fwd(torch.zeros(*shape, device="cuda"), 4)
         assert mean.shape == rstd.shape == (shape[0], 4)
         assert mean.isnan().all() and rstd.isnan().all()
+
+
+# ---------------------------------------------------------------- the gradient's mean terms
+def mean_terms(shape, io, seed):
+    """Inputs whose mean(du w) and mean(du w xhat) are about 1: dy is a constant, the value itself
+    and noise."""
+    g = torch.Generator("cpu").manual_seed(seed)
+    dt = torch.bfloat16 if io == "bf16" else torch.float32
+    C = shape[-1]
+    x = torch.randn(*shape, generator=g)
+    dy = 1.5 + 1.5 * x + torch.randn(*shape, generator=g)
+    return dict(x=x.to(dt), dy=dy.to(dt), w=1 + 0.1 * torch.randn(C, generator=g),
+                b=0.1 * torch.randn(C, generator=g))
+
+
+def gradients64(d, G, terms=(1, 1)):
+    """dx, dw, db by the formula in float64; terms: how often each mean is subtracted."""
+    x, dy, w = (d[n].double() for n in ("x", "dy", "w"))
+    N, C = x.shape[0], x.shape[-1]
+    xg = x.reshape(N, -1, G, C // G)
+    rstd = 1 / ((xg - xg.mean((1, 3), keepdim=True)).square().mean((1, 3), keepdim=True) + 1e-5).sqrt()
+    xh = (xg - xg.mean((1, 3), keepdim=True)) * rstd
+    u = xh.reshape(x.shape) * w + d["b"].double()
+    s = torch.sigmoid(u)
+    du = dy * s * (1 + u * (1 - s))
+    dxh = (du * w).reshape(xg.shape)
+    dx = rstd * (dxh - terms[0] * dxh.mean((1, 3), keepdim=True)
+                 - terms[1] * xh * (dxh * xh).mean((1, 3), keepdim=True))
+    rows = tuple(range(x.dim() - 1))
+    return dx.reshape(x.shape), (du * xh.reshape(x.shape)).sum(rows), du.sum(rows)
+
+
+def rms(a, b):
+    return ((a - b).square().mean() / b.square().mean()).sqrt().item()
+
+
+# 2^-8 is three times what one rounding to bf16 leaves (2^-9 / sqrt(3)). fp32: x-hat, u, silu', du w,
+# the two means and the last three steps are some 20 roundings of 2^-25 rms (2^-24 for the exponential
+# and division) of values up to four times the result: 32 x 2^-24 = 2e-6.
+BOUND = {"bf16": 2.0 ** -8, "f32": 2.0 ** -19}
+GRADIENT_SHAPES = MAPS + [((2, 4100, 128), 1), ((1, 9000, 64), 8), ((200, 70, 64), 2), ((2, 1000, 64), 32),
+                          ((2, 4099, 16), 1), ((3, 4095, 512), 32), ((700, 2048), 16), ((900, 320), 32),
+                          ((33, 33), 11), ((2, 9, 2004), 1)]
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("shape,G", GRADIENT_SHAPES)
+def test_gradient_whose_mean_terms_count(shape, G, io):
+    """Without either mean term, or with one of a cluster's parts left out, dx would be far off."""
+    from chunkwise_recurrent_prefill_gb300 import group_norm_bwd, group_norm_fwd
+    d = mean_terms(shape, io, seed=shape[-1] + G)
+    want = gradients64(d, G)
+    for without in ((0, 1), (1, 0), (0.9, 1), (1, 0.9)):
+        assert rms(gradients64(d, G, without)[0], want[0]) > 4 * BOUND[io], "the input does not tell"
+    x, dy, w, b = (d[n].cuda() for n in ("x", "dy", "w", "b"))
+    _, mean, rstd = group_norm_fwd(x, G, w, b, act="silu")
+    got = group_norm_bwd(dy, x, mean, rstd, G, w, b, act="silu")
+    for name, g, r in zip(("dx", "dw", "db"), got, want):
+        e = rms(g.cpu().double(), r)
+        # (sums of channels are fp32 whatever the tensors are)
+        assert e <= (BOUND[io] if name == "dx" else BOUND["f32"] * (1 if io == "f32" else 4)), f"{name}: {e:.3g}"
+
+
+@pytest.mark.parametrize("shape,G", [((1, 3000, 72), 9), ((1, 20000, 64), 8), ((500, 40, 512), 8)])
+def test_gradient_against_differences_over_several_ctas(shape, G):
+    """A direction with a mean and a part along x-hat. fp32 components, and a central difference in 64
+    bits (h = 1e-4 squared): 1e-5 of the norms."""
+    from chunkwise_recurrent_prefill_gb300 import group_norm_bwd, group_norm_fwd
+    d = mean_terms(shape, "f32", seed=G)
+    x, dy, w, b = (d[n].cuda() for n in ("x", "dy", "w", "b"))
+    _, mean, rstd = group_norm_fwd(x, G, w, b, act="silu")
+    dx = group_norm_bwd(dy, x, mean, rstd, G, w, b, act="silu")[0].cpu().double()
+    x64, gen = d["x"].double(), torch.Generator("cpu").manual_seed(7)
+    N, C = shape[0], shape[-1]
+
+    def loss(t):
+        xg = t.reshape(N, -1, G, C // G)
+        m = xg.mean((1, 3), keepdim=True)
+        u = ((xg - m) / ((xg - m).square().mean((1, 3), keepdim=True) + 1e-5).sqrt()).reshape(shape)
+        return (torch.nn.functional.silu(u * d["w"].double() + d["b"].double()) * d["dy"].double()).sum()
+
+    for v in (torch.ones(shape, dtype=torch.float64), x64.clone(),
+              torch.randn(shape, generator=gen, dtype=torch.float64)):
+        diff = (loss(x64 + 1e-4 * v) - loss(x64 - 1e-4 * v)) / 2e-4
+        assert abs((dx * v).sum() - diff) <= 1e-5 * dx.norm() * v.norm()
