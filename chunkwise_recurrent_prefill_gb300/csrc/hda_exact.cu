@@ -13,7 +13,7 @@
 // walks all but the last for their end states alone (from zero, but the first), a second one makes
 // start states of them,
 //     S(1) = E(0),  S(j + 1) = l^len S(j) + E(j),
-// and a third one walks all segments for the outputs (one head of 16384 tokens: 2050 us -> 122).
+// and a third one walks all segments for the outputs (one head of 16384 tokens: 2050 us -> 82).
 #include <cuda_bf16.h>
 
 #include "gla_internal.h"
@@ -163,6 +163,12 @@ hda_exact_kernel(const __grid_constant__ HdaProblem p, const Segs sg) {
     // Fast decays multiply by l itself (l = 0 leaves exactly the new token).
     const bool slow = fabsf(g) < kSlow;
     const float lam = expf(g);
+    Tile<T, TB, W> tx, ty;
+    Tile<T, TB, kCols> tz;
+    const int zw = min(kCols, m.Dz - z0);
+    if (!kState) tx.load(xp, m.x.t, begin, end, p.T, rev, m.Dx);
+    ty.load(yp, m.y.t, begin, end, p.T, rev, m.Dx);
+    tz.load(zp, m.z.t, begin, end, p.T, rev, zw);
     // Token i of a tile of nt is row i + TB - nt of the factors (rows past its end: any number).
     if (threadIdx.x < 2 * TB) {
         const int r = max(TB - 1 - (int)threadIdx.x, 0);
@@ -171,12 +177,6 @@ hda_exact_kernel(const __grid_constant__ HdaProblem p, const Segs sg) {
         if (threadIdx.x <= TB) pw[threadIdx.x] = decay_pow(g, (float)threadIdx.x);
     }
     __syncthreads();
-    Tile<T, TB, W> tx, ty;
-    Tile<T, TB, kCols> tz;
-    const int zw = min(kCols, m.Dz - z0);
-    if (!kState) tx.load(xp, m.x.t, begin, end, p.T, rev, m.Dx);
-    ty.load(yp, m.y.t, begin, end, p.T, rev, m.Dx);
-    tz.load(zp, m.z.t, begin, end, p.T, rev, zw);
     int buf = 0;
     for (int64_t i0 = begin; i0 < end; i0 += TB, buf ^= 1) {
         const int nt = (int)min((int64_t)TB, end - i0);
@@ -356,9 +356,11 @@ struct ExactPlan {
 
 // Segments of a sequence, and one column of S per thread or kWide (4; with more than 128 rows, 2): one
 // is faster for a CTA by itself, four read x and y once for four times the columns. The cost of each
-// in ns, as measured at 128 rows (one column and four): the token of a lone CTA 122 and 270; as long
-// as an SM's CTAs are fewer than 1.2 and 1.9, it does not depend on them, then it grows in
-// proportion; the first kernel's tokens 0.7 of that; 6 us for the two kernels more.
+// in ns, set where the choices came out best at 128 rows (one column and four): the token of a lone
+// CTA 122 and 270 (measured: 120 and 235); as long as an SM's CTAs are fewer than 1.2 and 1.9, it does
+// not depend on them, then it grows in proportion (16 CTAs of one column to an SM: 1330; 4 of four:
+// 650); the first kernel's tokens 0.7 of that; 6 us for the two kernels more. (With 120, 235 and 1.45
+// CTAs for both, one head of 16384 tokens takes 94 us, not 82, and 8 of 2048 90, not 66.)
 ExactPlan exact_plan(const HdaProblem &p, int splits, int sms) {
     int dx, dz;
     exact_dims(p, dx, dz);
