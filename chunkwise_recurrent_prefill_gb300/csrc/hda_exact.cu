@@ -4,10 +4,11 @@
 // The columns of the state are independent (out_t[z] needs S[:, z] alone), so a CTA owns 16 NC of
 // them for one head and walks the tokens with its part of S in registers: a thread holds RPT rows of
 // NC columns (packed in pairs of rows), 8 threads the rows of a column. A token costs it two
-// multiply-adds per element of S, or three where the decay is fast; with one column per thread the reads of x and y from shared memory
-// took three times as long as these. Nothing but the state's own addition chain is serial. The
-// sums over the 8 row groups are formed for 8 (token, column) pairs at once, in 7 shuffles. x, y and
-// z are staged as fp32 in shared memory TB tokens at a time, the next tile being loaded meanwhile.
+// multiply-adds per element of S, or three where the decay is fast; with one column per thread the
+// reads of x and y from shared memory take more than three times as long. Nothing but the state's own
+// addition chain is serial. The sums over the 8 row groups are formed for 8 (token, column) pairs at
+// once, in 7 shuffles. x, y and z are staged as fp32 in shared memory TB tokens at a time, the next
+// tile being loaded meanwhile.
 //
 // A walk is serial, so where long sequences give the SMs few CTAs it is cut into segments: one kernel
 // walks all but the last for their end states alone (from zero, but the first), a second one makes

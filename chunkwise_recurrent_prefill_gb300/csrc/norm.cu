@@ -12,12 +12,17 @@
 //          they are few (cluster_plan), the parts are a cluster and one kernel does it all; else a
 //          first kernel leaves each part's statistics, a second one combines them and a third one
 //          writes. The second reading of x comes from registers or from L2 when the tensor fits there.
-//   plain: groups of an odd number of channels, odd strides or pointers: a CTA per group.
+//   plain: a CTA per group, element by element, and a CTA per channel for dw and db: groups of an odd
+//          number of channels; strides or pointers that are not on a vector's bytes (16, or those of two
+//          channels where a group is not whole 16-byte vectors); groups of more than 256 vectors (2048
+//          bf16 or 1024 fp32 channels), or maps and groups of more than 128 vectors with more than
+//          65535 entries.
 // Means and variances: where a group is in registers, the mean and then the squared deviations from
 // it. Else each thread takes the mean of its first vector as a pivot and sums the deviations from
 // it and their squares; threads and parts are then merged as (count, mean, M2), in a fixed order.
-// (M2 = sum of squares - (sum)^2 / n loses digits only if the pivot is many standard deviations of
-// the thread's own values away from their mean, which a value among them cannot be.)
+// (M2 = sum of squares - (sum)^2 / n loses digits if the pivot is many standard deviations of the
+// thread's own n values away from their mean. A value among them is sqrt(n) away at most, so that the
+// worst case, a first value far off all others, leaves M2 good to n 2^-24.)
 #include <cuda_bf16.h>
 
 #include <atomic>

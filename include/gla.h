@@ -70,7 +70,8 @@ typedef enum {
     GLA_ERR_LAUNCH = 6,            /* a CUDA call or kernel launch failed             */
     GLA_ERR_DEVICE_TIMEOUT = 7,    /* a kernel gave up waiting on a pipeline barrier  */
     GLA_ERR_UNSUPPORTED_DEVICE = 8,/* the current device is not sm_103                */
-    GLA_ERR_WORKSPACE = 9,         /* caller workspace too small or misaligned        */
+    GLA_ERR_WORKSPACE = 9,         /* caller workspace too small or misaligned, or the
+                                      library's too small for a call being captured     */
     GLA_ERR_BAD_OPTION = 10,       /* an option value is out of range                 */
     GLA_ERR_BAD_SEQLENS = 11,      /* packed-sequence offsets were found inconsistent on
                                       the device (reported by gla_last_device_status)   */
@@ -316,6 +317,14 @@ gla_status gdn_fwd(const void *q, const void *k, const void *v, const float *g_l
  * hT and dh0 keep fp32 accuracy, two where only outputs read it); everything else runs token by
  * token in fp32 (GLA_PATH_EXACT). Deterministic: no atomics. T = 0 gives hT = h0 (dh0 = dhT), or
  * zero.
+ *
+ * Values that are not finite: GLA_PATH_EXACT gives what the recurrence gives. They reach the tokens
+ * after theirs alone (in the gradients of k and v, those before), and an infinite state stays
+ * infinite. GLA_PATH_TC multiplies whole chunks of 64 tokens, in which the masked products of a
+ * token that is not finite are NaN, too: it makes NaN of its head's outputs from the first token of
+ * its chunk on, and an infinite state may become NaN. Chunks count from the first token (in the
+ * gradients of k and v, from the last one). So the rows of padded tokens have to hold finite
+ * numbers.
  */
 typedef struct {
     int64_t b, t, h;        /* element strides of the batch, token and head dimension   */
@@ -426,7 +435,8 @@ size_t gla_group_norm_workspace_size(const gla_norm_shape *shape, int backward);
  * fork    : row children[i] becomes a copy of row parents[i] on pages taken from the stack, in
  *           the order of (i, m); negative numbers skip i. A child must have no pages, and of the
  *           requests that name the same child the first counts and the others are in error.
- *           Parents are read as they were before the call. When the stack runs out, the remaining entries become -1 and the error is raised.
+ *           Parents are read as they were before the call. When the stack runs out, the remaining
+ *           entries become -1 and the error is raised.
  * free    : the pages of rows[i] go back on the stack and the rows' entries become -1; a row
  *           listed again has none left. Pages are pushed last to first, so that freeing what
  *           a fork took, in the same order, restores the stack.
