@@ -187,6 +187,17 @@ def _check(t, name, dtype, shape, device):
         raise ValueError(f"{name} must be contiguous")
 
 
+def _workspace(workspace, device):
+    """(address, bytes) of a caller's workspace, or (None, 0)."""
+    if workspace is None:
+        return None, 0
+    if not isinstance(workspace, torch.Tensor):
+        raise TypeError("workspace must be a torch.Tensor")
+    if workspace.device != device or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the inputs' device")
+    return _addr(workspace), workspace.numel() * workspace.element_size()
+
+
 def options(path: str = "auto", seq_splits: int = 0, workspace: torch.Tensor | None = None,
             gate: str = "key"):
     opt = _Options()
@@ -246,6 +257,7 @@ def gla_fwd(q, k, v, g, scale: float, h0=None, *, o=None, hT=None, return_state:
         hT = torch.empty((B, H, Dk, Dv), dtype=torch.float32, device=dev)
     elif hT is not None:
         _check(hT, "hT", torch.float32, (B, H, Dk, Dv), dev)
+    _workspace(workspace, dev)
     opt = options(path, seq_splits, workspace, gate)
     io = IO_BF16 if q.dtype == torch.bfloat16 else IO_F32
     with torch.cuda.device(dev):
@@ -399,11 +411,7 @@ def gdn_fwd(q, k, v, g, beta, scale: float, h0=None, *, o=None, hT=None,
         hT = torch.empty((B, H, Dk, Dv), dtype=torch.float32, device=dev)
     elif hT is not None:
         _check(hT, "hT", torch.float32, (B, H, Dk, Dv), dev)
-    ws, ws_bytes = None, 0
-    if workspace is not None:
-        if workspace.device != dev or not workspace.is_contiguous():
-            raise ValueError("workspace must be a contiguous tensor on the inputs' device")
-        ws, ws_bytes = _ptr(workspace), workspace.numel() * workspace.element_size()
+    ws, ws_bytes = _workspace(workspace, dev)
     io = IO_BF16 if q.dtype == torch.bfloat16 else IO_F32
     with torch.cuda.device(dev):
         rc = lib.gdn_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), ctypes.c_float(scale),

@@ -15,7 +15,7 @@ import functools
 import torch
 
 from .gla import (GLA_OK, GLAError, IO_BF16, IO_F32, _HdaShape, _check, _addr, _launch,
-                  _on_stream, load_library, options)
+                  _on_stream, _workspace, load_library, options)
 
 
 def _check_rows(name, dtype, shape, strides, want_dtype, want_shape, align):
@@ -126,6 +126,7 @@ def hda_fwd(q, k, v, decay, scale: float, h0=None, *, o=None, hT=None, return_st
     if hT is None and return_state:
         hT = torch.empty((B, H, Dk, Dv), dtype=torch.float32, device=dev)
     _state(hT, "hT", (B, H, Dk, Dv), dev)
+    _workspace(workspace, dev)
     opt = options(path, seq_splits, workspace)
     rc = _launch(lib.hda_fwd, dev, _addr(q), _addr(k), _addr(v), _addr(decay), scale, _addr(h0),
                  _addr(o), _addr(hT), ctypes.byref(sh), ctypes.byref(opt))
@@ -152,6 +153,7 @@ def hda_bwd(do, q, k, v, decay, scale: float, h0=None, dhT=None, *, path: str = 
     _state(dhT, "dhT", (B, H, Dk, Dv), dev)
     dq, dk, dv = (torch.empty(t.shape, dtype=t.dtype, device=dev) for t in (q, k, v))
     dh0 = None if h0 is None else torch.empty_like(h0)
+    _workspace(workspace, dev)
     opt = options(path, seq_splits, workspace)
     rc = _launch(lib.hda_bwd, dev, _addr(do), _addr(q), _addr(k), _addr(v), _addr(decay), scale,
                  _addr(h0), _addr(dhT), _addr(dq), _addr(dk), _addr(dv), _addr(dh0), ctypes.byref(sh),

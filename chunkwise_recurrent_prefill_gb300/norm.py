@@ -12,7 +12,7 @@ import operator
 
 import torch
 
-from .gla import IO_BF16, IO_F32, _NormShape, _check, _addr, _launch, _on_stream, load_library
+from .gla import IO_BF16, IO_F32, _NormShape, _check, _addr, _launch, _on_stream, _workspace, load_library
 from .hda import _fail
 
 ACTS = {"none": 0, "silu": 1, "gelu": 2}
@@ -88,14 +88,6 @@ def _affine(x, weight, bias):
     for t, n in ((weight, "weight"), (bias, "bias")):
         if t is not None:
             _check(t, n, torch.float32, (x.shape[-1],), x.device)
-
-
-def _workspace(workspace, dev):
-    if workspace is None:
-        return None, 0
-    if workspace.device != dev or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous tensor on the inputs' device")
-    return _addr(workspace), workspace.numel() * workspace.element_size()
 
 
 def group_norm_workspace_size(x, groups: int, backward: bool = False, gate=None) -> int:

@@ -12,9 +12,8 @@ from __future__ import annotations
 
 import torch
 
-from .gla import _check, _addr, _launch, _on_stream, load_library
+from .gla import _check, _addr, _launch, _on_stream, _workspace, load_library
 from .hda import _fail, _tensor
-from .norm import _workspace
 
 
 def _pool(pool):

@@ -60,3 +60,42 @@ def test_pages(monkeypatch):
         pkg.pages_workspace_size([[0]], free)
     with pytest.raises(TypeError, match="free must be"):
         pkg.pages_workspace_size(table, 4)
+
+
+def test_workspaces_elsewhere(monkeypatch):
+    """A workspace that is not on the inputs' device, or that has gaps, is refused by every call (CPU
+    stands for the inputs' device here, and the check of it is taken out of the way)."""
+    from chunkwise_recurrent_prefill_gb300 import gla, hda, norm
+    launched = []
+    monkeypatch.setattr(hda, "_check_inputs", lambda q, *a: q.device)
+    monkeypatch.setattr(norm, "_affine", lambda *a: None)
+    for mod in (hda, norm):
+        monkeypatch.setattr(mod, "_launch", lambda *a: launched.append(a) or 0)
+    q = torch.zeros(1, 4, 2, 16)
+    d, do = torch.zeros(2), torch.zeros(1, 4, 2, 16)
+    calls = (lambda w: pkg.hda_fwd(q, q, q, d, 1.0, workspace=w),
+             lambda w: pkg.hda_bwd(do, q, q, q, d, 1.0, workspace=w),
+             lambda w: pkg.group_norm_fwd(do, 2, workspace=w))
+    for call in calls:
+        call(torch.zeros(64))
+        n = len(launched)
+        for bad in (torch.empty(64, device="meta"), torch.zeros(64)[::2]):
+            with pytest.raises(ValueError, match="workspace"):
+                call(bad)
+        with pytest.raises(TypeError, match="workspace"):
+            call(1 << 20)
+        assert len(launched) == n
+    with pytest.raises(ValueError, match="workspace"):
+        gla._workspace(torch.zeros(64)[::2], torch.device("cpu"))
+
+
+@pytest.mark.gpu
+def test_workspaces_on_the_host():
+    q = torch.zeros(1, 64, 2, 64, device="cuda")
+    d, g = torch.zeros(2, device="cuda"), torch.zeros(1, 64, 2, 64, device="cuda")
+    for bad in (torch.empty(1 << 20, dtype=torch.uint8), torch.empty(1 << 20, device="cuda")[::2]):
+        for call in (lambda: pkg.hda_fwd(q, q, q, d, 1.0, workspace=bad),
+                     lambda: pkg.hda_bwd(q, q, q, q, d, 1.0, workspace=bad),
+                     lambda: pkg.gla_fwd(q, q, q, g, 1.0, workspace=bad)):
+            with pytest.raises(ValueError, match="workspace"):
+                call()
