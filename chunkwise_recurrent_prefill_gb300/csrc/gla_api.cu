@@ -155,7 +155,10 @@ gla_status validate(const void *q, const void *k, const void *v, const float *g,
 // a capture gets a new one.
 gla_status library_workspace(DeviceState *st, cudaStream_t stream, size_t need, void **out) {
     cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
-    if (cudaStreamIsCapturing(stream, &capture) != cudaSuccess) cudaGetLastError();   // (a launch will tell)
+    if (cudaStreamIsCapturing(stream, &capture) != cudaSuccess) {   // (the status is then not specified)
+        cudaGetLastError();
+        capture = cudaStreamCaptureStatusNone;
+    }
     std::lock_guard<std::mutex> lock(g_mu);
     StreamWorkspace *slot = nullptr;
     for (auto &w : st->ws)
