@@ -3,6 +3,7 @@
 #include <algorithm>
 #include <stdio.h>
 
+#include "api_util.h"
 #include "gla.h"
 #include "gla_internal.h"
 #include "hda_internal.h"
@@ -11,52 +12,7 @@
 
 namespace {
 
-constexpr int64_t kMostElems = int64_t(1) << 62;
-
-bool misaligned(const void *p) { return p && (reinterpret_cast<uintptr_t>(p) & 15u); }
-
-// a * b of non-negative sizes; false past 2^62 (so byte counts still fit)
-bool mul_ok(int64_t a, int64_t b, int64_t *r) {
-    if (a < 0 || b < 0 || (a != 0 && b > kMostElems / 16 / a)) return false;
-    *r = a * b;
-    return true;
-}
-
-// A memory range an argument covers.
-struct Range {
-    const void *p;
-    int64_t bytes;
-};
-bool overlap(const Range &a, const Range &b) {
-    if (!a.p || !b.p || a.bytes <= 0 || b.bytes <= 0) return false;
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
-    return x < y + (size_t)b.bytes && y < x + (size_t)a.bytes;
-}
-// GLA_ERR_ALIAS if an output overlaps an input or another output.
-gla_status check_alias(const Range *outs, int no, const Range *ins, int ni) {
-    for (int i = 0; i < no; ++i) {
-        for (int j = 0; j < ni; ++j)
-            if (overlap(outs[i], ins[j])) return GLA_ERR_ALIAS;
-        for (int j = i + 1; j < no; ++j)
-            if (overlap(outs[i], outs[j])) return GLA_ERR_ALIAS;
-    }
-    return GLA_OK;
-}
-
-// The caller's workspace if it will do, else the stream's own.
-gla_status get_workspace(void *ws, size_t bytes, size_t need, cudaStream_t s, const Range *used,
-                         int nu, void **out) {
-    *out = nullptr;
-    if (ws) {
-        if (misaligned(ws) || bytes < need) return GLA_ERR_WORKSPACE;
-        for (int i = 0; i < nu; ++i)
-            if (overlap(Range{ws, (int64_t)need}, used[i])) return GLA_ERR_WORKSPACE;
-        *out = ws;
-        return GLA_OK;
-    }
-    if (need == 0) return GLA_OK;
-    return (gla_status)gla::stream_workspace(s, need, out);
-}
+using namespace gla::api;
 
 // Strides of a [b, t, h, D] tensor (contiguous where the caller's are all zero) and its extent
 // in bytes. Dimensions of one element take the stride they would have in a packed tensor,
@@ -308,11 +264,6 @@ gla_status norm_problem(const gla_norm_shape *sh, gla::NormProblem *p, int64_t *
     return GLA_OK;
 }
 
-// Element alignment of a strided tensor's base (rows may start anywhere).
-bool unaligned(const void *p, int io) {
-    return p && (reinterpret_cast<uintptr_t>(p) & (io == GLA_IO_BF16 ? 1u : 3u));
-}
-
 gla_status check_pool(void *pool, int64_t P, int64_t page_bytes) {
     int64_t n;
     if (P < 0 || P > (int64_t(1) << 30) || page_bytes < 0 || !mul_ok(P, page_bytes, &n))
@@ -321,7 +272,6 @@ gla_status check_pool(void *pool, int64_t P, int64_t page_bytes) {
     if (n > 0 && !pool) return GLA_ERR_NULL_ARG;
     return GLA_OK;
 }
-bool bad_int(const void *p) { return p && (reinterpret_cast<uintptr_t>(p) & 3u); }
 
 gla_status check_table(int64_t P, const int32_t *table, int64_t R, int64_t M, const int32_t *stack,
                        const int32_t *count, int64_t n) {

@@ -57,6 +57,27 @@ class _NormShape(ctypes.Structure):
         [("eps", ctypes.c_float), ("act", ctypes.c_int), ("io", ctypes.c_int)]
 
 
+class _Rows(ctypes.Structure):
+    _fields_ = [("b", ctypes.c_int64), ("t", ctypes.c_int64)]
+
+
+class _ConvShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("B", "T", "C", "W")] + \
+        [(n, _Rows) for n in ("x", "dy")] + [("act", ctypes.c_int), ("io", ctypes.c_int)]
+
+
+class _SsmShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("B", "T", "C", "G", "N")] + \
+        [(n, _Rows) for n in ("u", "dt", "z", "b", "c", "d_o")] + \
+        [("softplus", ctypes.c_int), ("io", ctypes.c_int)]
+
+
+class _QkShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("B", "T", "Hq", "Hk", "D", "R", "P")] + \
+        [(n, _Strides) for n in ("q", "k", "d_qo", "d_ko")] + \
+        [("eps", ctypes.c_float), ("norm", ctypes.c_int), ("pairs", ctypes.c_int), ("io", ctypes.c_int)]
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -137,6 +158,25 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
             lib.gla_pages_workspace_size.argtypes = [i64, i64, i64, i64]
             for f in (lib.hda_fwd_workspace_size, lib.hda_bwd_workspace_size,
                       lib.gla_group_norm_workspace_size, lib.gla_pages_workspace_size):
+                f.restype = ctypes.c_size_t
+            cs, ss, qs = ctypes.POINTER(_ConvShape), ctypes.POINTER(_SsmShape), ctypes.POINTER(_QkShape)
+            lib.gla_conv_fwd.argtypes = [vp] * 6 + [cs, vp]
+            lib.gla_conv_bwd.argtypes = [vp] * 10 + [cs] + ws + [vp]
+            lib.gla_conv_step.argtypes = [vp] * 6 + [i64, cs, vp]
+            lib.ssm_fwd.argtypes = [vp] * 11 + [ss, opt, vp]
+            lib.ssm_bwd.argtypes = [vp] * 20 + [ss, opt, vp]
+            lib.ssm_step.argtypes = [vp] * 11 + [i64, ss, vp]
+            lib.gla_qk_norm_fwd.argtypes = [vp] * 11 + [qs, vp]
+            lib.gla_qk_norm_bwd.argtypes = [vp] * 15 + [qs] + ws + [vp]
+            for f in (lib.gla_conv_fwd, lib.gla_conv_bwd, lib.gla_conv_step, lib.ssm_fwd, lib.ssm_bwd,
+                      lib.ssm_step, lib.gla_qk_norm_fwd, lib.gla_qk_norm_bwd):
+                f.restype = ctypes.c_int
+            lib.gla_conv_bwd_workspace_size.argtypes = [cs]
+            lib.gla_qk_norm_bwd_workspace_size.argtypes = [qs]
+            lib.ssm_fwd_workspace_size.argtypes = [ss, opt]
+            lib.ssm_bwd_workspace_size.argtypes = [ss, opt]
+            for f in (lib.gla_conv_bwd_workspace_size, lib.gla_qk_norm_bwd_workspace_size,
+                      lib.ssm_fwd_workspace_size, lib.ssm_bwd_workspace_size):
                 f.restype = ctypes.c_size_t
             _lib = lib
     return _lib

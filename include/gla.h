@@ -75,9 +75,9 @@ typedef enum {
     GLA_ERR_BAD_OPTION = 10,       /* an option value is out of range                 */
     GLA_ERR_BAD_SEQLENS = 11,      /* packed-sequence offsets were found inconsistent on
                                       the device (reported by gla_last_device_status)   */
-    GLA_ERR_BAD_PAGES = 12         /* a page, slot or row number read on the device was out
-                                      of range or used twice, or no page was free (reported
-                                      by gla_last_device_status)                         */
+    GLA_ERR_BAD_PAGES = 12         /* a page, slot, row number or position read on the device
+                                      was out of range or used twice, or no page was free
+                                      (reported by gla_last_device_status)               */
 } gla_status;
 
 /* Which arithmetic path runs. */
@@ -199,9 +199,9 @@ int gla_path_for(int64_t B, int64_t T, int64_t H, int64_t Dk, int64_t Dv, int io
  * a kernel abandoned a bounded pipeline wait (its outputs are then undefined, the
  * context stays usable), GLA_ERR_BAD_SEQLENS when gla_fwd_varlen found offsets that are
  * not non-decreasing within [0, T] (the affected sequences are left unwritten),
- * GLA_ERR_BAD_PAGES when hda_step or a gla_pages_ call met a number it could not use (that
- * row or page was skipped, the others were done), or GLA_ERR_LAUNCH when the
- * synchronisation itself failed.
+ * GLA_ERR_BAD_PAGES when a step or a gla_pages_ call met a number it could not use, or
+ * gla_qk_norm_ a position (that row, page or token was skipped, the others were done), or
+ * GLA_ERR_LAUNCH when the synchronisation itself failed.
  */
 gla_status gla_last_device_status(gla_stream_t stream);
 
@@ -467,6 +467,143 @@ gla_status gla_pages_compact_ex(void *pool, int64_t P, int64_t page_bytes, int32
                                 size_t workspace_bytes, gla_stream_t stream);
 /* Bytes that are enough for each of the three, with up to n requests (0 for sizes they refuse). */
 size_t gla_pages_workspace_size(int64_t P, int64_t R, int64_t M, int64_t n);
+
+/*
+ * Around the recurrences: the short convolution in front of a layer of them (gla_conv_*), the
+ * norm of queries and keys for each head with their rotation (gla_qk_norm_*), and one more recurrence
+ * (ssm_*), whose decays are inputs for each channel and state.
+ *
+ * Tensors named with a gla_rows in the shape may be strided: the last dimension (for B and C of
+ * ssm_*: the last two) is contiguous, the strides of the others are in elements and positive
+ * (those of dimensions of one element say nothing); they need no alignment but their element's.
+ * Everything else is contiguous; outputs and states are 16-byte aligned. bf16 or fp32 by io;
+ * arithmetic and sums in fp32. All of it is deterministic: no atomics. A NaN or an infinity reaches
+ * what the formulas let it reach, and nothing else.
+ */
+typedef struct {
+    int64_t b, t;           /* element strides of the batch and token dimension; both zero = contiguous */
+} gla_rows;
+
+/*
+ * gla_conv_fwd, gla_conv_bwd, gla_conv_step — depthwise causal convolution along the tokens,
+ * with an activation:
+ *     a[t, c] = bias[c] + sum_{j < W} w[c, j] x[t - (W - 1) + j, c],     y = act(a)
+ * x [B, T, C]; w [C, W] float32, 1 <= W <= 8; bias [C] float32 or NULL. The inputs before the first
+ * token are s0 [B, W - 1, C], oldest first (x's type; NULL: zeros); sT, of the same shape, receives
+ * the last W - 1 inputs (those of s0 where T < W - 1) and may be NULL.
+ *
+ * bwd: dy is the gradient of y, dsT that of sT (NULL: zero). Writes dx, dw [C, W] and dbias [C] in
+ * float32 (each may be NULL) and ds0 (may be NULL).
+ *
+ * step: one token x [B, C] (stride x.b; T and x.t are ignored) for each of B rows, on pages of a
+ * pool S [P, W - 1, C], updated in place: row r uses page slots[r] (NULL: page r), as in hda_step.
+ */
+typedef struct {
+    int64_t B, T, C, W;
+    gla_rows x, dy;
+    int act;                /* gla_act */
+    int io;                 /* gla_io  */
+} gla_conv_shape;
+
+gla_status gla_conv_fwd(const void *x, const float *w, const float *bias, const void *s0, void *y,
+                        void *sT, const gla_conv_shape *shape, gla_stream_t stream);
+gla_status gla_conv_bwd(const void *dy, const void *x, const float *w, const float *bias,
+                        const void *s0, const void *dsT, void *dx, float *dw, float *dbias, void *ds0,
+                        const gla_conv_shape *shape, void *workspace, size_t workspace_bytes,
+                        gla_stream_t stream);
+gla_status gla_conv_step(const void *x, const float *w, const float *bias, void *S,
+                         const int32_t *slots, void *y, int64_t P, const gla_conv_shape *shape,
+                         gla_stream_t stream);
+/* Bytes of workspace gla_conv_bwd needs; NULL uses the library's workspace of the stream. */
+size_t gla_conv_bwd_workspace_size(const gla_conv_shape *shape);
+
+/*
+ * ssm_fwd, ssm_bwd, ssm_step — selective state space scan. Each channel c of C has N states, whose
+ * decays and inputs are made from the token:
+ *     d_t[c] = dt_t[c] + dt_bias[c], or softplus of that (softplus(x) = log(1 + e^x))
+ *     h_t[c, n] = e^(d_t[c] A[c, n]) h_{t-1}[c, n] + d_t[c] u_t[c] B_t[g, n]
+ *     y_t[c] = sum_n C_t[g, n] h_t[c, n] + D[c] u_t[c],     o_t[c] = y_t[c] silu(z_t[c])
+ * g = c / (C / G): the G groups of channels share their B and C. u, dt, z, o [B, T, C];
+ * A [C, N] float32, finite; B, C [B, T, G, N]; D, dt_bias [C] float32. z, D and dt_bias may be NULL:
+ * no gate, 0, 0. h0 (or NULL: zero), hT (may be NULL) [B, C, N] float32. 1 <= N <= 128.
+ * T = 0 gives hT = h0, or zero.
+ *
+ * bwd: d_o is the gradient of o, dhT that of hT (NULL: zero). Writes du, ddt, dB, dC (the inputs'
+ * type), dA, dD, ddt_bias (float32), dz and dh0 (float32). dD, dz, ddt_bias, dh0 may be NULL; dz
+ * needs z. Sums over channels, tokens and batch entries are in fp32. Nothing of the forward
+ * is kept: the states are computed again.
+ *
+ * step: one token for each of B rows on pages of a pool S [P, C, N] float32, updated in place: row r
+ * uses page slots[r] (NULL: page r), as in hda_step. u, dt, z, o [B, C] and B, C [B, G, N] with the
+ * strides b; T and the t strides are ignored.
+ */
+typedef struct {
+    int64_t B, T, C, G, N;
+    gla_rows u, dt, z, b, c;
+    gla_rows d_o;           /* ssm_bwd only */
+    int softplus;           /* 0 or 1 */
+    int io;                 /* gla_io */
+} ssm_shape;
+
+/* opt: seq_splits (sequence segments, 0 = auto) and the workspace, as in gla_fwd_ex; its path must be
+ * GLA_PATH_AUTO or GLA_PATH_EXACT (the same) and its gate GLA_GATE_KEY. opt may be NULL. */
+gla_status ssm_fwd(const void *u, const void *dt, const float *A, const void *Bm, const void *Cm,
+                   const float *D, const void *z, const float *dt_bias, const float *h0, void *o,
+                   float *hT, const ssm_shape *shape, const gla_options *opt, gla_stream_t stream);
+gla_status ssm_bwd(const void *d_o, const void *u, const void *dt, const float *A, const void *Bm,
+                   const void *Cm, const float *D, const void *z, const float *dt_bias,
+                   const float *h0, const float *dhT, void *du, void *ddt, float *dA, void *dBm,
+                   void *dCm, float *dD, void *dz, float *ddt_bias, float *dh0,
+                   const ssm_shape *shape, const gla_options *opt, gla_stream_t stream);
+gla_status ssm_step(const void *u, const void *dt, const float *A, const void *Bm, const void *Cm,
+                    const float *D, const void *z, const float *dt_bias, float *S,
+                    const int32_t *slots, void *o, int64_t P, const ssm_shape *shape,
+                    gla_stream_t stream);
+/* Bytes of workspace ssm_fwd / ssm_bwd need (0 if none, or if they would reject the shape). */
+size_t ssm_fwd_workspace_size(const ssm_shape *shape, const gla_options *opt);
+size_t ssm_bwd_workspace_size(const ssm_shape *shape, const gla_options *opt);
+
+/*
+ * gla_qk_norm_fwd, gla_qk_norm_bwd — the norm of queries and keys for each head, and their rotation
+ * by position, in one pass: what makes q and k of the attention calls. For each head x of D values:
+ *     n = x r w,    r = (s sum x^2 + eps)^-1/2     s = 1 / D (GLA_NORM_RMS) or 1 (GLA_NORM_L2);
+ *     GLA_NORM_NONE: n = x
+ *     the first R values of n (R even, 0: none) turn in pairs (a, b) -> (a cos - b sin, b cos + a sin)
+ *     by cos, sin [P, R / 2] float32, row position: (i, i + R / 2) is pair i, or with pairs = 1
+ *     (2 i, 2 i + 1)
+ * q [B, T, Hq, D], k [B, T, Hk, D], strided; qo, ko contiguous. wq, wk [D] float32 or NULL (1);
+ * NULL with GLA_NORM_NONE. positions: int32 [B, T] on the device, or NULL: a token's index. A position
+ * outside of 0 .. P-1 is reported as GLA_ERR_BAD_PAGES, and that token's outputs (in the backward
+ * pass: its gradients, which no sum then counts) are zero. rq [B, T, Hq], rk [B, T, Hk] float32
+ * receive r (may be NULL). 1 <= D <= 1024.
+ *
+ * bwd: gradients of qo and ko -> dq, dk (contiguous) and dwq, dwk (float32, may be NULL), from the
+ * forward's rq and rk (NULL with GLA_NORM_NONE).
+ */
+typedef enum { GLA_NORM_NONE = 0, GLA_NORM_RMS = 1, GLA_NORM_L2 = 2 } gla_norm_kind;
+
+typedef struct {
+    int64_t B, T, Hq, Hk, D;
+    int64_t R, P;
+    gla_strides q, k;       /* all three members zero = contiguous */
+    gla_strides d_qo, d_ko; /* gla_qk_norm_bwd only */
+    float eps;
+    int norm;               /* gla_norm_kind */
+    int pairs;              /* 0 or 1 */
+    int io;                 /* gla_io */
+} gla_qk_shape;
+
+gla_status gla_qk_norm_fwd(const void *q, const void *k, const float *wq, const float *wk,
+                           const float *cos, const float *sin, const int32_t *positions, void *qo,
+                           void *ko, float *rq, float *rk, const gla_qk_shape *shape,
+                           gla_stream_t stream);
+gla_status gla_qk_norm_bwd(const void *d_qo, const void *d_ko, const void *q, const void *k,
+                           const float *rq, const float *rk, const float *wq, const float *wk,
+                           const float *cos, const float *sin, const int32_t *positions, void *dq,
+                           void *dk, float *dwq, float *dwk, const gla_qk_shape *shape,
+                           void *workspace, size_t workspace_bytes, gla_stream_t stream);
+/* Bytes of workspace gla_qk_norm_bwd needs; NULL uses the library's workspace of the stream. */
+size_t gla_qk_norm_bwd_workspace_size(const gla_qk_shape *shape);
 
 /* Library ABI version: major * 10000 + minor * 100 + patch. */
 int gla_version(void);
