@@ -6,12 +6,21 @@
 //     dd_t = sum_n w_t A + u_t sum_n G_t B_t,   du_t = d_t sum_n G_t B_t + D dy_t
 //     dA = sum_t w_t d_t,   dB_t = sum_c G_t d_t u_t,   dC_t = sum_c h_t dy_t
 //
-// A ring of warps: a CTA owns 32 channels (one per lane) of a sequence, and its warps take chunks of
-// kTok tokens in turn. All that a chunk can do without the state (loads, step sizes, the exponentials
-// and inputs of four states at a time) runs while the chunks before it are still at work; the
-// four states then come from the warp before through shared memory, walk over the chunk's tokens in
-// registers and go on to the next warp. So a sequence is walked once, and each exponential is computed
-// once, although all warps work at the same time. Backwards the ring turns the other way.
+// A ring of warps: a CTA owns 32 kCh channels of a sequence (kCh to a lane), and its warps take chunks of
+// kTok tokens in turn, four states of a lane at a time. All that a chunk can do without the state
+// (loads, step sizes, exponentials, inputs) runs while the chunks before it are still at work; the
+// states then come from the warp before through shared memory, walk over the chunk's tokens in registers
+// and go on to the next warp. So a sequence is walked once and each exponential is computed once,
+// although all warps work at the same time. Backwards the ring turns the other way, on the states
+// that a forward walk left at the start of each chunk.
+//
+// Pairs of packed arithmetic are two tokens of one state: step sizes, inputs, B, C and sums of outputs
+// then are pairs as they come, and only the walk itself is scalar. (Pairs of two states need each
+// token's d and d u twice, which cost more moves than the walk saved: 191 instructions for a
+// token and channel of 16 states.)
+//
+// Bound: 16 exponentials of a token and channel take 64 cycles of a scheduler's share of the special function
+// units, the four multiply-adds of each state 64 of its FP32 pipe; in the backward pass thirteen of them 208.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -24,9 +33,10 @@ namespace gla {
 namespace {
 
 constexpr int kTok = 8;             // tokens of a chunk
-constexpr int kLanes = 32;          // channels of a CTA
+constexpr int kPairs = kTok / 2;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
+using tc::add2;
 using tc::fma2;
 using tc::mul2;
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
@@ -36,22 +46,750 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
+// 2^(A d) of a pair of tokens. The hardware's 2^x is good to 1.2e-7 but lies low on average, by up to 2.6e-8 of
+// the value for x in (-1/8, 0): over the hundred tokens that such decays remember this adds up, to 4e-6 of
+// the state. 2e-8 on the exponent's side (which costs nothing, as the product is a multiply-add) leaves at
+// most 1.3e-8 on average, a quarter of fp32's rounding; 2^0 is still 1.
+__device__ __forceinline__ float2 decay2(float2 A, float2 d) {
+    const float2 x = fma2(A, d, both(2e-8f));
+    return make_float2(ex2(x.x), ex2(x.y));
+}
+
+// A times log2 e, with infinities brought to the largest float: a step of zero then keeps the state.
+__device__ __forceinline__ float scale_a(float a) {
+    const float x = a * kLog2e;
+    return isinf(x) ? copysignf(3.4028235e38f, x) : x;
+}
+
+// softplus(x) = max(x, 0) + log(1 + e), e = e^-|x|, of a pair. log(1 + e) is e times a polynomial
+// fitted to log(1 + e) / e on [0, 1] with the smallest relative error (5e-9, 1.4e-7 with the roundings of
+// fp32): the small steps that give a state its memory keep their digits, which log(1 + e) formed as
+// such would lose, and ten multiply-adds of pairs cost a third of the library's functions.
+__device__ __forceinline__ float2 softplus2(float2 x) {
+    const float2 e = make_float2(ex2(fabsf(x.x) * -kLog2e), ex2(fabsf(x.y) * -kLog2e));
+    float2 r = both(-0.003244024235755205f);
+    r = fma2(r, e, both(0.019851457327604294f));
+    r = fma2(r, e, both(-0.056959524750709534f));
+    r = fma2(r, e, both(0.10603654384613037f));
+    r = fma2(r, e, both(-0.15305592119693756f));
+    r = fma2(r, e, both(0.1967593878507614f));
+    r = fma2(r, e, both(-0.24954134225845337f));
+    r = fma2(r, e, both(0.3332996368408203f));
+    r = fma2(r, e, both(-0.4999990165233612f));
+    r = fma2(r, e, both(1.f));
+    return fma2(r, e, make_float2(fmaxf(x.x, 0.f), fmaxf(x.y, 0.f)));
+}
+__device__ __forceinline__ float step_size(float x, int softplus) { return softplus ? softplus2(both(x)).x : x; }
+
+__device__ __forceinline__ void copy16(void *to, const void *from, bool in) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(tc::smem_u32(to)), "l"(from),
+                 "r"(in ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft>
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
+
+// What a CTA's warps read: the sequence's rows from the tile's first channel (the group's B and C) on.
+struct Source {
+    const void *p;
+    int64_t t;          // element stride of a token
+    int width;          // elements that exist, of a row of `row` in the stage
+    int row;
+};
+
+// Brings the tokens [t0, t0 + kTok) of a source into to[kTok][row], with zeros for tokens and
+// elements that do not exist. kVec: rows are on 16 bytes, and the copies stay on their way until
+// copies_wait; else element by element.
+template <typename T, bool kVec>
+__device__ __forceinline__ void stage_rows(const Source &s, int64_t t0, int64_t T_, T *to) {
+    constexpr int V = 16 / sizeof(T);
+    const int lane = threadIdx.x % 32;
+    const T *p = static_cast<const T *>(s.p) + t0 * s.t;
+    if (kVec) {
+        const int pieces = s.row / V;
+        for (int k = lane; k < kTok * pieces; k += 32) {
+            const int i = k / pieces, v = (k - i * pieces) * V;
+            const bool in = t0 + i < T_ && v < s.width;
+            copy16(to + i * s.row + v, in ? p + i * s.t + v : s.p, in);
+        }
+    } else {
+        for (int k = lane; k < kTok * s.row; k += 32) {
+            const int i = k / s.row, v = k - i * s.row;
+            T x;
+            put(&x, 0.f);
+            to[k] = t0 + i < T_ && v < s.width ? p[i * s.t + v] : x;
+        }
+    }
+}
+
+// B and C of the chunk as floats, the values of two tokens side by side as the packed arithmetic takes
+// them: from[2][kTok][N] -> to[2][kTok / 2][NP] float2, NP = N up to a multiple of 4, zero past N.
+template <typename T, int kN>
+__device__ __forceinline__ void widen_rows(const T *from, float2 *to, int N) {
+    const int lane = threadIdx.x % 32, NP = (N + 3) / 4 * 4;
+    if (kN) {        // four states at a time
+#pragma unroll
+        for (int k = lane; k < kTok * kN / 4; k += 32) {
+            const int row = k / (kN / 4), q = k % (kN / 4);     // row: a pair of tokens of B, or of C
+            float x[4], y[4];
+            Pack<T, 4>::unpack(*reinterpret_cast<const typename Pack<T, 4>::raw *>(from + 2 * row * N + 4 * q), x);
+            Pack<T, 4>::unpack(*reinterpret_cast<const typename Pack<T, 4>::raw *>(from + (2 * row + 1) * N + 4 * q), y);
+            float4 *t = reinterpret_cast<float4 *>(to + row * NP + 4 * q);
+            t[0] = make_float4(x[0], y[0], x[1], y[1]);
+            t[1] = make_float4(x[2], y[2], x[3], y[3]);
+        }
+        return;
+    }
+    for (int k = lane; k < kTok * NP; k += 32) {
+        const int row = k / NP, n = k - row * NP;
+        to[k] = n < N ? make_float2(get(from + 2 * row * N + n), get(from + (2 * row + 1) * N + n)) : both(0.f);
+    }
+}
+
+// Waits for a hand-over. Most arrive while it polls; the clock that bounds the wait takes longer to read than
+// they do, so that it is left to mbar_wait.
+__device__ __forceinline__ bool ring_wait(uint64_t *bar, uint32_t parity) {
+#pragma unroll 1
+    for (int i = 0; i < 256; ++i)
+        if (tc::mbar_try_wait(bar, parity)) return true;
+    return tc::mbar_wait(bar, parity);
+}
+
+
+// The CTAs of a sequence: tiles of 32 kCh channels of one group.
+struct Tiles {
+    int per_group;
+    int64_t all;
+};
+__host__ __device__ inline Tiles tiles_of(int64_t C, int64_t G, int ch) {
+    const int64_t n = (C / G + 32 * ch - 1) / (32 * ch);
+    return Tiles{(int)n, n * G};
+}
+
+// Where a CTA is: a sequence, a group of channels and 32 kCh of them.
+template <int kCh>
+struct Place {
+    int64_t b, tile, g, c0;         // c0: the first channel
+    int width, mine;                // channels of the tile, of the lane
+    __device__ Place(const SsmProblem &p, const Tiles &tl) {
+        b = blockIdx.x / tl.all;
+        tile = blockIdx.x % tl.all;
+        g = tile / tl.per_group;
+        const int64_t cg = p.C / p.G, first = (tile - g * tl.per_group) * 32 * kCh;
+        width = (int)min((int64_t)32 * kCh, cg - first);
+        c0 = g * cg + first;
+        mine = max(0, min(kCh, width - kCh * (int)(threadIdx.x % 32)));
+    }
+    // Channel j of the lane; the tile's first one where there is none.
+    __device__ int64_t channel(int j) const { return c0 + (j < mine ? threadIdx.x % 32 * kCh + j : 0); }
+    template <typename T>
+    __device__ Source channels(const SsmRows &r) const {
+        return Source{static_cast<const T *>(r.p) + b * r.b + c0, r.t, width, 32 * kCh};
+    }
+    template <typename T>
+    __device__ Source rows(const SsmRows &r, int N) const {
+        return Source{static_cast<const T *>(r.p) + b * r.b + g * N, r.t, N, N};
+    }
+};
+
+// A lane works on kSt = 4 / kCh states of its channels at a time, Q = N / kSt times. Shared memory of a
+// ring of W warps:
+//   slot[W][Q][32] float4: what a warp hands on, [kCh][kSt];  A[Q][2][32] float4: A log2 e, twice each
+//   sums[W][Q][32] float4 (backward): dA;  turn[W][32][kTurn] float (backward): sums across lanes
+//   rows[W][2][kPairs][NP] float2: B and C of a warp's chunk;  bar[W][Q]
+//   stage[W][2]: a chunk as it lies in memory, on its way while the one before it is worked on:
+//     kIn tensors [kTok][32 kCh], then B and C [kTok][N]
+constexpr int kTurn = 66;           // (lanes that write pairs side by side meet no bank twice)
+template <typename T, int kCh>
+struct Ring {
+    float4 *slot, *A, *sums;
+    float *turn;
+    float2 *rows;
+    uint64_t *bar;
+    unsigned char *stage;
+    static __host__ __device__ int steps(int N) { return (N + 4 / kCh - 1) / (4 / kCh); }
+    static __host__ __device__ int padded(int N) { return (N + 3) / 4 * 4; }
+    static __host__ __device__ size_t stage_bytes(int in, int N) {
+        return ((size_t)in * kTok * 32 * kCh * sizeof(T) + 2 * kTok * (size_t)N * sizeof(T) + 15) / 16 * 16;
+    }
+    static __host__ __device__ size_t bytes(int W, int in, int N, bool backward) {
+        const size_t Q = steps(N);
+        return W * Q * 32 * 16 * (backward ? 2 : 1) + Q * 2 * 32 * 16 + (backward ? W * 32 * kTurn * 4 : 0) +
+               (size_t)W * 2 * kPairs * padded(N) * 8 + (W * Q * 8 + 15) / 16 * 16 + 2 * W * stage_bytes(in, N);
+    }
+    __device__ Ring(unsigned char *smem, int W, int N, bool backward) {
+        const int Q = steps(N);
+        slot = reinterpret_cast<float4 *>(smem);
+        A = slot + W * Q * 32;
+        sums = A + Q * 2 * 32;
+        turn = reinterpret_cast<float *>(sums + (backward ? W * Q * 32 : 0));
+        rows = reinterpret_cast<float2 *>(turn + (backward ? W * 32 * kTurn : 0));
+        bar = reinterpret_cast<uint64_t *>(rows + W * 2 * kPairs * padded(N));
+        stage = reinterpret_cast<unsigned char *>(bar) + (W * Q * 8 + 15) / 16 * 16;
+    }
+    // A and the barriers; the CTA synchronises.
+    __device__ void begin(const SsmProblem &p, const Place<kCh> &at, int W, int N) {
+        constexpr int kSt = 4 / kCh;
+        const int Q = steps(N), lane = threadIdx.x % 32;
+        for (int q = threadIdx.x / 32; q < Q; q += W) {
+            float a[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int n = kSt * q + j % kSt;
+                a[j] = n < N && j / kSt < at.mine ? scale_a(p.A[at.channel(j / kSt) * N + n]) : 0.f;
+            }
+            A[2 * q * 32 + lane] = make_float4(a[0], a[0], a[1], a[1]);
+            A[(2 * q + 1) * 32 + lane] = make_float4(a[2], a[2], a[3], a[3]);
+        }
+        if (threadIdx.x == 0) {
+            for (int i = 0; i < W * Q; ++i) tc::mbar_init(bar + i, 1);
+            tc::fence_mbar_init();
+        }
+        __syncthreads();
+    }
+    __device__ void load_a(int q, float2 (&a)[4]) const {
+        const int lane = threadIdx.x % 32;
+        const float4 x = A[2 * q * 32 + lane], y = A[(2 * q + 1) * 32 + lane];
+        a[0] = make_float2(x.x, x.y);
+        a[1] = make_float2(x.z, x.w);
+        a[2] = make_float2(y.x, y.y);
+        a[3] = make_float2(y.z, y.w);
+    }
+};
+
+// States [kCh][kSt] of step q of the lane, from and to [B, C, N].
+template <int kCh>
+__device__ __forceinline__ void load_states(const float *from, const SsmProblem &p, const Place<kCh> &at, int q,
+                                            float (&h)[4]) {
+    constexpr int kSt = 4 / kCh;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int n = kSt * q + j % kSt;
+        h[j] = from && j / kSt < at.mine && n < p.N ? from[(at.b * p.C + at.channel(j / kSt)) * p.N + n] : 0.f;
+    }
+}
+template <int kCh>
+__device__ __forceinline__ void store_states(float *to, const SsmProblem &p, const Place<kCh> &at, int q,
+                                             const float (&h)[4]) {
+    constexpr int kSt = 4 / kCh;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int n = kSt * q + j % kSt;
+        if (j / kSt < at.mine && n < p.N) to[(at.b * p.C + at.channel(j / kSt)) * p.N + n] = h[j];
+    }
+}
+
+// The lane's channels of row i of a tensor in the stage.
+template <typename T, int kCh>
+__device__ __forceinline__ void lane_row(const T *in, int i, float (&v)[kCh]) {
+    const T *r = in + (i * 32 + threadIdx.x % 32) * kCh;
+    if constexpr (kCh == 1) {
+        v[0] = get(r);
+    } else if constexpr (sizeof(T) == 2) {
+        const float2 f = tc::unpack_bf16(*reinterpret_cast<const uint32_t *>(r));
+        v[0] = f.x;
+        v[1] = f.y;
+    } else {
+        const float2 f = *reinterpret_cast<const float2 *>(r);
+        v[0] = f.x;
+        v[1] = f.y;
+    }
+}
+template <typename T, int kCh>
+__device__ __forceinline__ void put_lane_row(T *to, int i, const float (&v)[kCh]) {
+    T *r = to + (i * 32 + threadIdx.x % 32) * kCh;
+    if constexpr (kCh == 1) {
+        put(r, v[0]);
+    } else if constexpr (sizeof(T) == 2) {
+        *reinterpret_cast<uint32_t *>(r) = tc::pack_bf16(v[0], v[1]);
+    } else {
+        *reinterpret_cast<float2 *>(r) = make_float2(v[0], v[1]);
+    }
+}
+// The same for a pair of tokens: v[channel] = (token 2 ip, token 2 ip + 1).
+template <typename T, int kCh>
+__device__ __forceinline__ void lane_pair(const T *in, int ip, float2 (&v)[kCh]) {
+    float x[kCh], y[kCh];
+    lane_row<T, kCh>(in, 2 * ip, x);
+    lane_row<T, kCh>(in, 2 * ip + 1, y);
+#pragma unroll
+    for (int c = 0; c < kCh; ++c) v[c] = make_float2(x[c], y[c]);
+}
+template <typename T, int kCh>
+__device__ __forceinline__ void put_lane_pair(T *to, int ip, const float2 (&v)[kCh]) {
+    float x[kCh], y[kCh];
+#pragma unroll
+    for (int c = 0; c < kCh; ++c) {
+        x[c] = v[c].x;
+        y[c] = v[c].y;
+    }
+    put_lane_row<T, kCh>(to, 2 * ip, x);
+    put_lane_row<T, kCh>(to, 2 * ip + 1, y);
+}
+// Rows of the stage to the tile's rows of a contiguous [B, T, C] tensor.
+template <typename T, int kCh, bool kVec>
+__device__ __forceinline__ void write_rows(const T *from, void *to, const SsmProblem &p, const Place<kCh> &at, int64_t t0) {
+    const int lane = threadIdx.x % 32;
+    T *out = static_cast<T *>(to) + (at.b * p.T + t0) * p.C + at.c0;
+    if (kVec) {
+        constexpr int V = 16 / sizeof(T), pieces = 32 * kCh / V;
+#pragma unroll
+        for (int j = lane; j < kTok * pieces; j += 32) {
+            const int i = j / pieces, v = j % pieces * V;
+            if (t0 + i < p.T && v < at.width)
+                *reinterpret_cast<uint4 *>(out + i * p.C + v) = *reinterpret_cast<const uint4 *>(from + i * 32 * kCh + v);
+        }
+    } else {
+        for (int i = 0; i < kTok; ++i)
+            for (int v = lane; v < at.width; v += 32)
+                if (t0 + i < p.T) out[i * p.C + v] = from[i * 32 * kCh + v];
+    }
+}
+
+// Step sizes of the chunk from the stage (zero for tokens and channels that do not exist: they keep the state).
+template <typename T, int kCh>
+__device__ __forceinline__ void step_sizes(const T *in, const float (&bias)[kCh], int softplus, int64_t left, int mine,
+                                           float2 (&d)[kCh][kPairs]) {
+#pragma unroll
+    for (int ip = 0; ip < kPairs; ++ip) {
+        float2 r[kCh];
+        lane_pair<T, kCh>(in, ip, r);
+#pragma unroll
+        for (int c = 0; c < kCh; ++c) {
+            d[c][ip] = add2(r[c], both(bias[c]));
+            if (softplus) d[c][ip] = softplus2(d[c][ip]);
+        }
+    }
+    if (left < kTok || mine < kCh) {
+#pragma unroll
+        for (int c = 0; c < kCh; ++c)
+#pragma unroll
+            for (int ip = 0; ip < kPairs; ++ip) {
+                if (c >= mine || 2 * ip >= left) d[c][ip].x = 0.f;
+                if (c >= mine || 2 * ip + 1 >= left) d[c][ip].y = 0.f;
+            }
+    }
+}
+
+// Two states' pairs of row ip of B (or C).
+template <int kSt>
+__device__ __forceinline__ void load_bc(const float2 *row, int q, float2 (&v)[kSt]) {
+#pragma unroll
+    for (int n = 0; n < kSt; n += 2) {
+        const float4 x = *reinterpret_cast<const float4 *>(row + kSt * q + n);
+        v[n] = make_float2(x.x, x.y);
+        v[n + 1] = make_float2(x.z, x.w);
+    }
+}
+
+// kOut: outputs and the last state; else the states before each chunk go to marks
+// [B][chunks][tiles][Q][32] float4. kN: N, if known at compile time.
+template <typename T, int kCh, int kN, bool kOut, bool kVec>
+__global__ void __launch_bounds__(512, 1)
+ssm_fwd_kernel(const __grid_constant__ SsmProblem p, float4 *marks, unsigned int *err) {
+    extern __shared__ __align__(16) unsigned char smem[];
+    constexpr int kSt = 4 / kCh, kIn = kOut ? 3 : 2, kRow = kTok * 32 * kCh;
+    using R = Ring<T, kCh>;
+    const int W = blockDim.x / 32, N = kN ? kN : p.N, Q = R::steps(N), NP = R::padded(N);
+    R ring(smem, W, N, false);
+    const int w = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const Tiles tl = tiles_of(p.C, p.G, kCh);
+    const Place<kCh> at(p, tl);
+    ring.begin(p, at, W, N);
+    float bias[kCh], D[kCh];
+#pragma unroll
+    for (int c = 0; c < kCh; ++c) {
+        bias[c] = p.dt_bias ? p.dt_bias[at.channel(c)] : 0.f;
+        D[c] = p.D ? p.D[at.channel(c)] : 0.f;
+    }
+    float2 *rows = ring.rows + w * 2 * kPairs * NP;
+    const size_t stage_bytes = R::stage_bytes(kIn, N);
+    auto stage = [&](int k) { return reinterpret_cast<T *>(ring.stage + (2 * w + k) * stage_bytes); };
+    const int64_t chunks = (p.T + kTok - 1) / kTok;
+    auto fetch = [&](int64_t ch, int k) {
+        if (ch < chunks) {
+            T *to = stage(k);
+            const int64_t t0 = ch * kTok;
+            stage_rows<T, kVec>(at.template channels<T>(p.u), t0, p.T, to);
+            stage_rows<T, kVec>(at.template channels<T>(p.dt), t0, p.T, to + kRow);
+            if (kOut && p.z.p) stage_rows<T, kVec>(at.template channels<T>(p.z), t0, p.T, to + 2 * kRow);
+            to += kIn * kRow;
+            stage_rows<T, kVec>(at.template rows<T>(p.Bm, N), t0, p.T, to);
+            stage_rows<T, kVec>(at.template rows<T>(p.Cm, N), t0, p.T, to + kTok * N);
+        }
+        if (kVec) copies_commit();
+    };
+    const int prev = w == 0 ? W - 1 : w - 1;
+    bool dead = false;
+    int k = 0;
+    fetch(w, 0);
+    for (int64_t ch = w; ch < chunks; ch += W, k ^= 1) {
+        const int64_t t0 = ch * kTok;
+        fetch(ch + W, k ^ 1);
+        if (kVec) copies_wait<1>();
+        __syncwarp();
+        T *in = stage(k);
+        widen_rows<T, kN>(in + kIn * kRow, rows, N);
+        float2 d[kCh][kPairs], x[kCh][kPairs], y[kCh][kPairs];
+        step_sizes<T, kCh>(in + kRow, bias, p.softplus, p.T - t0, at.mine, d);
+#pragma unroll
+        for (int ip = 0; ip < kPairs; ++ip) {
+            float2 u[kCh];
+            lane_pair<T, kCh>(in, ip, u);
+#pragma unroll
+            for (int c = 0; c < kCh; ++c) {
+                x[c][ip] = mul2(d[c][ip], u[c]);
+                y[c][ip] = both(0.f);
+            }
+        }
+        __syncwarp();
+        const uint32_t parity = (uint32_t)((ch - 1) / W) & 1u;
+#pragma unroll 1
+        for (int q = 0; q < Q; ++q) {
+            float2 A[4], a[4][kPairs], s[4][kPairs];      // [kCh][kSt]
+            ring.load_a(q, A);
+#pragma unroll
+            for (int ip = 0; ip < kPairs; ++ip) {
+                float2 b[kSt];
+                load_bc<kSt>(rows + ip * NP, q, b);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    a[j][ip] = decay2(A[j], d[j / kSt][ip]);
+                    s[j][ip] = mul2(b[j % kSt], x[j / kSt][ip]);
+                }
+            }
+            float h[4];
+            if (ch == 0) {
+                load_states<kCh>(p.h0, p, at, q, h);
+            } else {
+                if (!dead && !ring_wait(ring.bar + prev * Q + q, parity)) {
+                    dead = true;
+                    atomicOr(err, kDevErrTimeout);
+                }
+                const float4 v = ring.slot[(prev * Q + q) * 32 + lane];
+                h[0] = v.x;
+                h[1] = v.y;
+                h[2] = v.z;
+                h[3] = v.w;
+            }
+            if (!kOut)
+                marks[(((at.b * chunks + ch) * tl.all + at.tile) * Q + q) * 32 + lane] = make_float4(h[0], h[1], h[2], h[3]);
+#pragma unroll
+            for (int ip = 0; ip < kPairs; ++ip)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    s[j][ip].x = fmaf(a[j][ip].x, h[j], s[j][ip].x);
+                    h[j] = s[j][ip].y = fmaf(a[j][ip].y, s[j][ip].x, s[j][ip].y);
+                }
+            if (ch + 1 < chunks) {
+                ring.slot[(w * Q + q) * 32 + lane] = make_float4(h[0], h[1], h[2], h[3]);
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(ring.bar + w * Q + q);
+            } else if (kOut && p.hT) {
+                store_states<kCh>(p.hT, p, at, q, h);
+            }
+            if (kOut) {
+#pragma unroll
+                for (int ip = 0; ip < kPairs; ++ip) {
+                    float2 c[kSt];
+                    load_bc<kSt>(rows + (kPairs + ip) * NP, q, c);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) y[j / kSt][ip] = fma2(c[j % kSt], s[j][ip], y[j / kSt][ip]);
+                }
+            }
+        }
+        if (kOut) {
+            // outputs take the place of u in the stage, then leave in whole rows
+#pragma unroll
+            for (int ip = 0; ip < kPairs; ++ip) {
+                float2 u[kCh], z[kCh];
+                if (p.D) lane_pair<T, kCh>(in, ip, u);
+                if (p.z.p) lane_pair<T, kCh>(in + 2 * kRow, ip, z);
+#pragma unroll
+                for (int c = 0; c < kCh; ++c) {
+                    if (p.D) y[c][ip] = fma2(both(D[c]), u[c], y[c][ip]);
+                    if (p.z.p)
+                        y[c][ip] = mul2(y[c][ip], mul2(z[c], make_float2(logistic<T>(z[c].x), logistic<T>(z[c].y))));
+                }
+                float2 o[kCh];
+#pragma unroll
+                for (int c = 0; c < kCh; ++c) o[c] = y[c][ip];
+                put_lane_pair<T, kCh>(in, ip, o);
+            }
+            __syncwarp();
+            write_rows<T, kCh, kVec>(in, p.o, p, at, t0);
+        }
+        __syncwarp();       // the stage and the rows have been read
+    }
+}
+
+// Where the backward kernel leaves what is summed later, all float:
+//   rows [tiles][B T][2][NP]: dB and dC of a tile's channels
+//   chan [B][C][N + 2]: dA, then dD and ddt_bias
+struct Parts {
+    float *rows, *chan;
+};
+
+template <typename T, int kCh, int kN, bool kVec>
+__global__ void __launch_bounds__(256, 1)
+ssm_bwd_kernel(const __grid_constant__ SsmProblem p, const float4 *marks, const Parts parts, unsigned int *err) {
+    extern __shared__ __align__(16) unsigned char smem[];
+    __shared__ float2 chan[8][32 * kCh];
+    constexpr int kSt = 4 / kCh, kIn = 4, kRow = kTok * 32 * kCh;
+    using R = Ring<T, kCh>;
+    const int W = blockDim.x / 32, N = kN ? kN : p.N, Q = R::steps(N), NP = R::padded(N);
+    R ring(smem, W, N, true);
+    const int w = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const Tiles tl = tiles_of(p.C, p.G, kCh);
+    const Place<kCh> at(p, tl);
+    for (int q = 0; q < Q; ++q) ring.sums[(w * Q + q) * 32 + lane] = make_float4(0.f, 0.f, 0.f, 0.f);
+    ring.begin(p, at, W, N);
+    float bias[kCh], D[kCh], dD[kCh], dbias[kCh];
+#pragma unroll
+    for (int c = 0; c < kCh; ++c) {
+        bias[c] = p.dt_bias ? p.dt_bias[at.channel(c)] : 0.f;
+        D[c] = p.D ? p.D[at.channel(c)] : 0.f;
+        dD[c] = dbias[c] = 0.f;
+    }
+    float2 *rows = ring.rows + w * 2 * kPairs * NP;
+    float *turn = ring.turn + w * 32 * kTurn;
+    const size_t stage_bytes = R::stage_bytes(kIn, N);
+    auto stage = [&](int k) { return reinterpret_cast<T *>(ring.stage + (2 * w + k) * stage_bytes); };
+    const int64_t chunks = (p.T + kTok - 1) / kTok;
+    auto fetch = [&](int64_t step, int k) {
+        if (step < chunks) {
+            const int64_t t0 = (chunks - 1 - step) * kTok;
+            T *to = stage(k);
+            stage_rows<T, kVec>(at.template channels<T>(p.u), t0, p.T, to);
+            stage_rows<T, kVec>(at.template channels<T>(p.dt), t0, p.T, to + kRow);
+            stage_rows<T, kVec>(at.template channels<T>(p.go), t0, p.T, to + 2 * kRow);
+            if (p.z.p) stage_rows<T, kVec>(at.template channels<T>(p.z), t0, p.T, to + 3 * kRow);
+            to += kIn * kRow;
+            stage_rows<T, kVec>(at.template rows<T>(p.Bm, N), t0, p.T, to);
+            stage_rows<T, kVec>(at.template rows<T>(p.Cm, N), t0, p.T, to + kTok * N);
+        }
+        if (kVec) copies_commit();
+    };
+    const int prev = w == 0 ? W - 1 : w - 1;
+    bool dead = false;
+    int k = 0;
+    fetch(w, 0);
+    for (int64_t step = w; step < chunks; step += W, k ^= 1) {
+        const int64_t ch = chunks - 1 - step, t0 = ch * kTok;
+        fetch(step + W, k ^ 1);
+        if (kVec) copies_wait<1>();
+        __syncwarp();
+        T *in = stage(k);
+        widen_rows<T, kN>(in + kIn * kRow, rows, N);
+        float2 d[kCh][kPairs], x[kCh][kPairs], dy[kCh][kPairs];
+        float2 y[kCh][kPairs], gB[kCh][kPairs], wA[kCh][kPairs];
+        step_sizes<T, kCh>(in + kRow, bias, p.softplus, p.T - t0, at.mine, d);
+#pragma unroll
+        for (int ip = 0; ip < kPairs; ++ip) {
+            float2 u[kCh], go[kCh], z[kCh];
+            lane_pair<T, kCh>(in, ip, u);
+            lane_pair<T, kCh>(in + 2 * kRow, ip, go);
+            if (p.z.p) lane_pair<T, kCh>(in + 3 * kRow, ip, z);
+#pragma unroll
+            for (int c = 0; c < kCh; ++c) {
+                x[c][ip] = mul2(d[c][ip], u[c]);
+                dy[c][ip] = go[c];
+                if (p.z.p)
+                    dy[c][ip] = mul2(go[c], mul2(z[c], make_float2(logistic<T>(z[c].x), logistic<T>(z[c].y))));
+                y[c][ip] = gB[c][ip] = wA[c][ip] = both(0.f);
+            }
+        }
+        __syncwarp();
+        const uint32_t parity = (uint32_t)((step - 1) / W) & 1u;
+        // Sums across the lanes: a lane leaves its values in its row of turn; a step's are dC and dB of kSt states
+        // of 8 tokens (2 tokens side by side), [2][kSt][kTok]. kCh = 2: two steps' values, 64 in all. Lane l
+        // adds the columns 2 l and 2 l + 1 and has two tokens of dC or dB of one state.
+        const float4 *mark = marks + ((at.b * chunks + ch) * tl.all + at.tile) * Q * 32 + lane;
+#pragma unroll 1
+        for (int q = 0; q < Q; ++q) {
+            float2 A[4], a[4][kPairs], s[4][kPairs];
+            float *mine = turn + lane * kTurn + (kCh == 2 ? q % 2 * 32 : 0);
+            ring.load_a(q, A);
+            const float4 mk = mark[q * 32];
+            float h[4] = {mk.x, mk.y, mk.z, mk.w};
+#pragma unroll
+            for (int ip = 0; ip < kPairs; ++ip) {
+                float2 b[kSt], c[kSt], dC[kSt];
+                load_bc<kSt>(rows + ip * NP, q, b);
+                load_bc<kSt>(rows + (kPairs + ip) * NP, q, c);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    a[j][ip] = decay2(A[j], d[j / kSt][ip]);
+                    s[j][ip] = mul2(b[j % kSt], x[j / kSt][ip]);
+                    // s: the states after the tokens
+                    s[j][ip].x = fmaf(a[j][ip].x, ip ? s[j][ip ? ip - 1 : 0].y : h[j], s[j][ip].x);
+                    s[j][ip].y = fmaf(a[j][ip].y, s[j][ip].x, s[j][ip].y);
+                    y[j / kSt][ip] = fma2(c[j % kSt], s[j][ip], y[j / kSt][ip]);
+                    dC[j % kSt] = j < kSt ? mul2(s[j][ip], dy[0][ip]) : fma2(s[j][ip], dy[j / kSt][ip], dC[j % kSt]);
+                }
+#pragma unroll
+                for (int n = 0; n < kSt; ++n) *reinterpret_cast<float2 *>(mine + n * kTok + 2 * ip) = dC[n];
+            }
+            float G[4];         // what comes from the tokens after
+            if (step == 0) {
+                load_states<kCh>(p.dhT, p, at, q, G);
+            } else {
+                if (!dead && !ring_wait(ring.bar + prev * Q + q, parity)) {
+                    dead = true;
+                    atomicOr(err, kDevErrTimeout);
+                }
+                const float4 v = ring.slot[(prev * Q + q) * 32 + lane];
+                G[0] = v.x;
+                G[1] = v.y;
+                G[2] = v.z;
+                G[3] = v.w;
+            }
+            float2 dA[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) dA[j] = both(0.f);
+#pragma unroll
+            for (int ip = kPairs - 1; ip >= 0; --ip) {
+                float2 b[kSt], c[kSt], dB[kSt];
+                load_bc<kSt>(rows + ip * NP, q, b);
+                load_bc<kSt>(rows + (kPairs + ip) * NP, q, c);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    float2 g = mul2(c[j % kSt], dy[j / kSt][ip]), wt;
+                    g.y += G[j];
+                    G[j] = a[j][ip].y * g.y;
+                    wt.y = G[j] * s[j][ip].x;
+                    g.x += G[j];
+                    G[j] = a[j][ip].x * g.x;
+                    wt.x = G[j] * (ip ? s[j][ip ? ip - 1 : 0].y : h[j]);
+                    gB[j / kSt][ip] = fma2(g, b[j % kSt], gB[j / kSt][ip]);
+                    wA[j / kSt][ip] = fma2(wt, A[j], wA[j / kSt][ip]);
+                    dA[j] = fma2(wt, d[j / kSt][ip], dA[j]);
+                    dB[j % kSt] = j < kSt ? mul2(g, x[0][ip]) : fma2(g, x[j / kSt][ip], dB[j % kSt]);
+                }
+#pragma unroll
+                for (int n = 0; n < kSt; ++n) *reinterpret_cast<float2 *>(mine + (kSt + n) * kTok + 2 * ip) = dB[n];
+            }
+            if (ch > 0) {
+                ring.slot[(w * Q + q) * 32 + lane] = make_float4(G[0], G[1], G[2], G[3]);
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(ring.bar + w * Q + q);
+            } else if (p.dh0) {
+                store_states<kCh>(p.dh0, p, at, q, G);
+            }
+            // (a chunk's sum first: those of thousands of tokens go up in two steps)
+            float4 *sum = ring.sums + (w * Q + q) * 32 + lane;
+            const float4 all = *sum;
+            *sum = make_float4(all.x + (dA[0].x + dA[0].y), all.y + (dA[1].x + dA[1].y), all.z + (dA[2].x + dA[2].y),
+                               all.w + (dA[3].x + dA[3].y));
+            if (kCh == 1 || q % 2 == 1 || q == Q - 1) {
+                __syncwarp();
+                float2 v = both(0.f);
+#pragma unroll
+                for (int l = 0; l < 32; ++l) v = add2(v, *reinterpret_cast<const float2 *>(turn + l * kTurn + 2 * lane));
+                __syncwarp();
+                const int at_q = kCh == 2 ? q / 2 * 2 + lane / 16 : q;              // the step,
+                const int col = 2 * (kCh == 2 ? lane % 16 : lane);                  // [2][kSt][kTok]
+                const int n = kSt * at_q + col / kTok % kSt, i = col % kTok, dB_ = col / (kSt * kTok);
+                if (n < N && at_q <= q) {
+                    float *out = parts.rows + (((at.tile * p.B + at.b) * p.T + t0 + i) * 2 + (1 - dB_)) * NP + n;
+                    if (t0 + i < p.T) out[0] = v.x;
+                    if (t0 + i + 1 < p.T) out[2 * NP] = v.y;
+                }
+            }
+        }
+        float2 sD[kCh], sbias[kCh];
+#pragma unroll
+        for (int c = 0; c < kCh; ++c) sD[c] = sbias[c] = both(0.f);
+#pragma unroll
+        for (int ip = 0; ip < kPairs; ++ip) {
+            float2 u[kCh], raw[kCh], go[kCh], z[kCh], du[kCh], ddt[kCh], dz[kCh];
+            lane_pair<T, kCh>(in, ip, u);
+            lane_pair<T, kCh>(in + kRow, ip, raw);
+            lane_pair<T, kCh>(in + 2 * kRow, ip, go);
+            if (p.z.p) lane_pair<T, kCh>(in + 3 * kRow, ip, z);
+#pragma unroll
+            for (int c = 0; c < kCh; ++c) {
+                ddt[c] = fma2(wA[c][ip], both(kLn2), mul2(u[c], gB[c][ip]));
+                if (p.softplus) {
+                    const float2 r = add2(raw[c], both(bias[c]));
+                    ddt[c] = mul2(ddt[c], make_float2(logistic<float>(r.x), logistic<float>(r.y)));
+                }
+                if (2 * ip >= p.T - t0) ddt[c].x = 0.f;         // tokens that do not exist
+                if (2 * ip + 1 >= p.T - t0) ddt[c].y = 0.f;
+                du[c] = fma2(both(D[c]), dy[c][ip], mul2(d[c][ip], gB[c][ip]));
+                sbias[c] = add2(sbias[c], ddt[c]);
+                sD[c] = fma2(dy[c][ip], u[c], sD[c]);
+                if (p.z.p) {
+                    const float2 yy = fma2(both(D[c]), u[c], y[c][ip]);
+                    dz[c] = mul2(mul2(go[c], yy), make_float2(act_grad<T>(z[c].x, 1), act_grad<T>(z[c].y, 1)));
+                }
+            }
+            put_lane_pair<T, kCh>(in, ip, du);
+            put_lane_pair<T, kCh>(in + kRow, ip, ddt);
+            if (p.dz) put_lane_pair<T, kCh>(in + 3 * kRow, ip, dz);
+        }
+#pragma unroll
+        for (int c = 0; c < kCh; ++c) {
+            dD[c] += sD[c].x + sD[c].y;
+            dbias[c] += sbias[c].x + sbias[c].y;
+        }
+        __syncwarp();
+        write_rows<T, kCh, kVec>(in, p.du, p, at, t0);
+        write_rows<T, kCh, kVec>(in + kRow, p.ddt, p, at, t0);
+        if (p.dz) write_rows<T, kCh, kVec>(in + 3 * kRow, p.dz, p, at, t0);
+        __syncwarp();       // the stage and the rows have been read
+    }
+#pragma unroll
+    for (int c = 0; c < kCh; ++c) chan[w][lane * kCh + c] = make_float2(dD[c], dbias[c]);
+    __syncthreads();
+    // the warps' sums in order: a thread for each channel and state (state fastest)
+    for (int k2 = threadIdx.x; k2 < at.width * (N + 2); k2 += blockDim.x) {
+        const int ci = k2 / (N + 2), n = k2 % (N + 2), l = ci / kCh, j = ci % kCh * kSt + n % kSt;
+        float s = 0.f;
+        for (int i = 0; i < W; ++i) {
+            if (n < N) s += reinterpret_cast<const float *>(ring.sums + (i * Q + n / kSt) * 32 + l)[j];
+            else s += n == N ? chan[i][ci].x : chan[i][ci].y;
+        }
+        parts.chan[(at.b * p.C + at.c0 + ci) * (N + 2) + n] = s;
+    }
+}
+
+// dB and dC from the tiles' parts, each added in order.
+template <typename T>
+__global__ void __launch_bounds__(256)
+ssm_rows_kernel(const __grid_constant__ SsmProblem p, const Parts parts, const Tiles tl) {
+    const int NP = (p.N + 3) / 4 * 4;
+    const int64_t rows = p.B * p.T, id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t n = id % NP, k = id / NP % 2, g = id / (2 * NP) % p.G, row = id / (2 * NP) / p.G;
+    if (row >= rows || n >= p.N) return;
+    float s = 0.f;
+    for (int i = 0; i < tl.per_group; ++i)
+        s += parts.rows[(((g * tl.per_group + i) * rows + row) * 2 + k) * NP + n];
+    put(static_cast<T *>(k ? p.dCm : p.dBm) + (row * p.G + g) * p.N + n, s);
+}
+// dA, dD and ddt_bias from the batch entries' parts.
+__global__ void __launch_bounds__(256)
+ssm_chan_kernel(const __grid_constant__ SsmProblem p, const Parts parts) {
+    const int64_t w = p.N + 2, id = (int64_t)blockIdx.x * 256 + threadIdx.x, c = id / w, n = id % w;
+    if (c >= p.C) return;
+    float s = 0.f;
+    for (int64_t b = 0; b < p.B; ++b) s += parts.chan[(b * p.C + c) * w + n];
+    if (n < p.N) p.dA[c * p.N + n] = s;
+    else if (n == p.N) { if (p.dD) p.dD[c] = s; }
+    else if (p.dbias) p.dbias[c] = s;
+}
 
 struct Quad {                       // four states of a channel
     float2 a, b;
 };
 __device__ __forceinline__ Quad quad(float4 v) { return Quad{make_float2(v.x, v.y), make_float2(v.z, v.w)}; }
 __device__ __forceinline__ float4 vec4(const Quad &q) { return make_float4(q.a.x, q.a.y, q.b.x, q.b.y); }
-__device__ __forceinline__ Quad operator*(const Quad &x, const Quad &y) { return Quad{mul2(x.a, y.a), mul2(x.b, y.b)}; }
 __device__ __forceinline__ Quad operator*(const Quad &x, float y) { return Quad{mul2(x.a, both(y)), mul2(x.b, both(y))}; }
 __device__ __forceinline__ Quad fmaq(const Quad &x, const Quad &y, const Quad &z) {
     return Quad{fma2(x.a, y.a, z.a), fma2(x.b, y.b, z.b)};
-}
-__device__ __forceinline__ Quad fmaq(const Quad &x, float y, const Quad &z) {
-    return Quad{fma2(x.a, both(y), z.a), fma2(x.b, both(y), z.b)};
-}
-__device__ __forceinline__ Quad exp2q(const Quad &x) {
-    return Quad{make_float2(ex2(x.a.x), ex2(x.a.y)), make_float2(ex2(x.b.x), ex2(x.b.y))};
 }
 // x . y added to a pair of sums
 __device__ __forceinline__ float2 dotq(const Quad &x, const Quad &y, float2 s) { return fma2(x.b, y.b, fma2(x.a, y.a, s)); }
@@ -72,360 +810,6 @@ __device__ __forceinline__ void store_quad(float *row, int n0, int N, float4 v) 
     if (n0 + 1 < N) row[n0 + 1] = v.y;
     if (n0 + 2 < N) row[n0 + 2] = v.z;
     if (n0 + 3 < N) row[n0 + 3] = v.w;
-}
-
-// A times log2 e, with infinities brought to the largest float: a step of zero then keeps the state.
-__device__ __forceinline__ float scale_a(float a) { return fminf(fmaxf(a * kLog2e, -3.4028235e38f), 3.4028235e38f); }
-
-__device__ __forceinline__ float step_size(float x, int softplus) {
-    return softplus ? fmaxf(x, 0.f) + log1pf(expf(-fabsf(x))) : x;
-}
-
-// Which sequence, group and channels a CTA has.
-struct Tiles {
-    int per_group;                  // CTAs of 32 channels for a group
-    int64_t all;                    // of a sequence
-};
-__host__ __device__ inline Tiles tiles_of(int64_t C, int64_t G) {
-    const int64_t cg = C / G;
-    const int64_t n = (cg + kLanes - 1) / kLanes;
-    return Tiles{(int)n, n * G};
-}
-
-// Shared memory of a ring of W warps with Q quads of states:
-//   slot[W][Q][32] float4: what a warp hands on;  A[Q][32] float4;  rows[W][2][kTok][4 Q]: B and C of
-//   a warp's chunk;  sums[W][Q][32] float4 (backward: dA);  bar[W][Q]
-struct Ring {
-    float4 *slot, *A, *sums;
-    float *rows;
-    uint64_t *bar;
-    static __host__ __device__ size_t bytes(int W, int Q, bool backward) {
-        return (size_t)W * Q * kLanes * 16 * (backward ? 2 : 1) + (size_t)Q * kLanes * 16 +
-               (size_t)W * 2 * kTok * 4 * Q * 4 + (size_t)W * Q * 8;
-    }
-    __device__ Ring(unsigned char *smem, int W, int Q, bool backward) {
-        slot = reinterpret_cast<float4 *>(smem);
-        A = slot + W * Q * kLanes;
-        sums = A + Q * kLanes;
-        rows = reinterpret_cast<float *>(sums + (backward ? W * Q * kLanes : 0));
-        bar = reinterpret_cast<uint64_t *>(rows + W * 2 * kTok * 4 * Q);
-    }
-};
-
-// B and C of the chunk's tokens as floats: to[2][kTok][4 Q], zero past the last token and state.
-template <typename T>
-__device__ __forceinline__ void load_rows(const SsmProblem &p, int64_t b, int64_t g, int64_t t0, int Q, float *to) {
-    const int lane = threadIdx.x % 32, NP = 4 * Q;
-    for (int k = lane; k < kTok * NP; k += 32) {
-        const int i = k / NP, n = k - i * NP;
-        const bool in = t0 + i < p.T && n < p.N;
-        const int64_t at = g * p.N + n;
-        to[k] = in ? get(static_cast<const T *>(p.Bm.p) + b * p.Bm.b + (t0 + i) * p.Bm.t + at) : 0.f;
-        to[kTok * NP + k] = in ? get(static_cast<const T *>(p.Cm.p) + b * p.Cm.b + (t0 + i) * p.Cm.t + at) : 0.f;
-    }
-}
-
-// kOut: outputs and the last state; else the states before each chunk go to marks
-// [B][chunks][tiles][Q][32] float4.
-template <typename T, int kQ, bool kOut>
-__global__ void __launch_bounds__(256)
-ssm_fwd_kernel(const __grid_constant__ SsmProblem p, float4 *marks, unsigned int *err) {
-    extern __shared__ __align__(16) unsigned char smem[];
-    const int W = blockDim.x / 32, Q = kQ ? kQ : (p.N + 3) / 4, NP = 4 * Q;
-    const Ring ring(smem, W, Q, false);
-    const int w = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const Tiles tl = tiles_of(p.C, p.G);
-    const int64_t b = blockIdx.x / tl.all, tile = blockIdx.x % tl.all, g = tile / tl.per_group;
-    const int64_t cg = p.C / p.G, in_group = (tile % tl.per_group) * kLanes + lane;
-    const bool live = in_group < cg;
-    const int64_t c = g * cg + (live ? in_group : 0);
-    for (int q = w; q < Q; q += W) {
-        const float4 a = load_quad(p.A + c * p.N, 4 * q, p.N);
-        ring.A[q * kLanes + lane] = make_float4(scale_a(a.x), scale_a(a.y), scale_a(a.z), scale_a(a.w));
-    }
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < W * Q; ++i) tc::mbar_init(ring.bar + i, 1);
-        tc::fence_mbar_init();
-    }
-    __syncthreads();
-    const float bias = p.dt_bias ? p.dt_bias[c] : 0.f, D = p.D ? p.D[c] : 0.f;
-    float *rows = ring.rows + w * 2 * kTok * NP;
-    const int64_t chunks = (p.T + kTok - 1) / kTok;
-    const int64_t state = (b * p.C + c) * p.N;
-    const int prev = w == 0 ? W - 1 : w - 1;
-    bool dead = false;
-    for (int64_t ch = w; ch < chunks; ch += W) {
-        const int64_t t0 = ch * kTok;
-        float u[kTok], d[kTok], du[kTok];
-#pragma unroll
-        for (int i = 0; i < kTok; ++i) {
-            const bool in = live && t0 + i < p.T;
-            u[i] = in ? get(static_cast<const T *>(p.u.p) + b * p.u.b + (t0 + i) * p.u.t + c) : 0.f;
-            d[i] = in ? step_size(get(static_cast<const T *>(p.dt.p) + b * p.dt.b + (t0 + i) * p.dt.t + c) + bias,
-                                  p.softplus)
-                      : 0.f;
-            du[i] = d[i] * u[i];
-        }
-        __syncwarp();
-        load_rows<T>(p, b, g, t0, Q, rows);
-        __syncwarp();
-        float2 y[kTok];
-#pragma unroll
-        for (int i = 0; i < kTok; ++i) y[i] = both(0.f);
-        const uint32_t parity = (uint32_t)((ch - 1) / W) & 1u;
-        for (int q = 0; q < Q; ++q) {
-            const Quad A = quad(ring.A[q * kLanes + lane]);
-            Quad a[kTok], x[kTok];
-#pragma unroll
-            for (int i = 0; i < kTok; ++i) {
-                a[i] = exp2q(A * d[i]);
-                x[i] = quad(*reinterpret_cast<const float4 *>(rows + i * NP + 4 * q)) * du[i];
-            }
-            Quad h;
-            if (ch == 0) {
-                h = quad(p.h0 && live ? load_quad(p.h0 + state, 4 * q, p.N) : make_float4(0.f, 0.f, 0.f, 0.f));
-            } else {
-                if (!dead && !tc::mbar_wait(ring.bar + prev * Q + q, parity)) {
-                    dead = true;
-                    atomicOr(err, kDevErrTimeout);
-                }
-                h = quad(ring.slot[(prev * Q + q) * kLanes + lane]);
-            }
-            if (!kOut) marks[(((b * chunks + ch) * tl.all + tile) * Q + q) * kLanes + lane] = vec4(h);
-#pragma unroll
-            for (int i = 0; i < kTok; ++i) {
-                h = fmaq(a[i], h, x[i]);
-                x[i] = h;
-            }
-            if (ch + 1 < chunks) {
-                ring.slot[(w * Q + q) * kLanes + lane] = vec4(h);
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive(ring.bar + w * Q + q);
-            } else if (kOut && p.hT && live) {
-                store_quad(p.hT + state, 4 * q, p.N, vec4(h));
-            }
-            if (kOut) {
-#pragma unroll
-                for (int i = 0; i < kTok; ++i)
-                    y[i] = dotq(x[i], quad(*reinterpret_cast<const float4 *>(rows + (kTok + i) * NP + 4 * q)), y[i]);
-            }
-        }
-        if (kOut) {
-#pragma unroll
-            for (int i = 0; i < kTok; ++i) {
-                if (!live || t0 + i >= p.T) break;
-                float o = y[i].x + y[i].y;
-                if (p.D) o = fmaf(D, u[i], o);
-                if (p.z.p) {
-                    const float z = get(static_cast<const T *>(p.z.p) + b * p.z.b + (t0 + i) * p.z.t + c);
-                    o *= z * logistic<T>(z);
-                }
-                put(static_cast<T *>(p.o) + (b * p.T + t0 + i) * p.C + c, o);
-            }
-        }
-    }
-}
-
-// Sums over the warp's lanes of 32 values each: lane i gets that of value i.
-__device__ __forceinline__ float sum_values(float (&v)[32]) {
-    const int lane = threadIdx.x % 32;
-#pragma unroll
-    for (int s = 16; s > 0; s >>= 1) {
-        const bool up = lane & s;
-#pragma unroll
-        for (int i = 0; i < s; ++i) {
-            const float send = up ? v[i] : v[i + s], keep = up ? v[i + s] : v[i];
-            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, s);
-        }
-    }
-    return v[0];
-}
-
-// Where the backward kernel leaves what is summed later, all float:
-//   rows [tiles][B T][2][4 Q]: dB and dC of a tile's channels
-//   chan [B][C][N + 2]: dA, then dD and ddt_bias
-struct Parts {
-    float *rows, *chan;
-};
-
-template <typename T, int kQ>
-__global__ void __launch_bounds__(256)
-ssm_bwd_kernel(const __grid_constant__ SsmProblem p, const float4 *marks, const Parts parts, unsigned int *err) {
-    extern __shared__ __align__(16) unsigned char smem[];
-    __shared__ float2 chan[8][kLanes];
-    const int W = blockDim.x / 32, Q = kQ ? kQ : (p.N + 3) / 4, NP = 4 * Q;
-    const Ring ring(smem, W, Q, true);
-    const int w = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const Tiles tl = tiles_of(p.C, p.G);
-    const int64_t b = blockIdx.x / tl.all, tile = blockIdx.x % tl.all, g = tile / tl.per_group;
-    const int64_t cg = p.C / p.G, in_group = (tile % tl.per_group) * kLanes + lane;
-    const bool live = in_group < cg;
-    const int64_t c = g * cg + (live ? in_group : 0);
-    for (int q = w; q < Q; q += W) {
-        const float4 a = load_quad(p.A + c * p.N, 4 * q, p.N);
-        ring.A[q * kLanes + lane] = make_float4(scale_a(a.x), scale_a(a.y), scale_a(a.z), scale_a(a.w));
-    }
-    for (int q = 0; q < Q; ++q) ring.sums[(w * Q + q) * kLanes + lane] = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < W * Q; ++i) tc::mbar_init(ring.bar + i, 1);
-        tc::fence_mbar_init();
-    }
-    __syncthreads();
-    const float bias = p.dt_bias ? p.dt_bias[c] : 0.f, D = p.D ? p.D[c] : 0.f;
-    float *rows = ring.rows + w * 2 * kTok * NP;
-    const int64_t chunks = (p.T + kTok - 1) / kTok;
-    const int64_t state = (b * p.C + c) * p.N;
-    const int prev = w == 0 ? W - 1 : w - 1;
-    float dD = 0.f, dbias = 0.f;
-    bool dead = false;
-    for (int64_t step = w; step < chunks; step += W) {
-        const int64_t ch = chunks - 1 - step, t0 = ch * kTok;
-        float u[kTok], raw[kTok], d[kTok], go[kTok], dy[kTok], z[kTok];
-#pragma unroll
-        for (int i = 0; i < kTok; ++i) {
-            const bool in = live && t0 + i < p.T;
-            const int64_t t = t0 + i;
-            u[i] = in ? get(static_cast<const T *>(p.u.p) + b * p.u.b + t * p.u.t + c) : 0.f;
-            raw[i] = in ? get(static_cast<const T *>(p.dt.p) + b * p.dt.b + t * p.dt.t + c) + bias : 0.f;
-            d[i] = in ? step_size(raw[i], p.softplus) : 0.f;
-            go[i] = in ? get(static_cast<const T *>(p.go.p) + b * p.go.b + t * p.go.t + c) : 0.f;
-            z[i] = in && p.z.p ? get(static_cast<const T *>(p.z.p) + b * p.z.b + t * p.z.t + c) : 0.f;
-            dy[i] = p.z.p ? go[i] * z[i] * logistic<T>(z[i]) : go[i];
-        }
-        __syncwarp();
-        load_rows<T>(p, b, g, t0, Q, rows);
-        __syncwarp();
-        float2 y[kTok], gB[kTok], wA[kTok];
-#pragma unroll
-        for (int i = 0; i < kTok; ++i) y[i] = gB[i] = wA[i] = both(0.f);
-        const uint32_t parity = (uint32_t)((step - 1) / W) & 1u;
-        // rows of this tile's dB and dC: lane i sums value i % 4 of token i / 4
-        float *out = parts.rows + ((tile * p.B + b) * p.T + t0 + lane / 4) * 2 * NP + lane % 4;
-        const bool row_in = t0 + lane / 4 < p.T;
-        for (int q = 0; q < Q; ++q) {
-            const Quad A = quad(ring.A[q * kLanes + lane]);
-            Quad h = quad(marks[(((b * chunks + ch) * tl.all + tile) * Q + q) * kLanes + lane]);
-            Quad a[kTok], before[kTok];
-            float v[4 * kTok];
-#pragma unroll
-            for (int i = 0; i < kTok; ++i) {
-                const Quad Bv = quad(*reinterpret_cast<const float4 *>(rows + i * NP + 4 * q));
-                const Quad Cv = quad(*reinterpret_cast<const float4 *>(rows + (kTok + i) * NP + 4 * q));
-                a[i] = exp2q(A * d[i]);
-                before[i] = h;
-                h = fmaq(a[i], h, Bv * (d[i] * u[i]));
-                y[i] = dotq(h, Cv, y[i]);
-                const Quad e = h * dy[i];
-                v[4 * i] = e.a.x;
-                v[4 * i + 1] = e.a.y;
-                v[4 * i + 2] = e.b.x;
-                v[4 * i + 3] = e.b.y;
-            }
-            const float dC = sum_values(v);
-            Quad G;
-            if (step == 0) {
-                G = quad(p.dhT && live ? load_quad(p.dhT + state, 4 * q, p.N) : make_float4(0.f, 0.f, 0.f, 0.f));
-            } else {
-                if (!dead && !tc::mbar_wait(ring.bar + prev * Q + q, parity)) {
-                    dead = true;
-                    atomicOr(err, kDevErrTimeout);
-                }
-                G = quad(ring.slot[(prev * Q + q) * kLanes + lane]);
-            }
-            Quad dA = quad(ring.sums[(w * Q + q) * kLanes + lane]);
-#pragma unroll
-            for (int i = kTok - 1; i >= 0; --i) {
-                const Quad Bv = quad(*reinterpret_cast<const float4 *>(rows + i * NP + 4 * q));
-                const Quad Cv = quad(*reinterpret_cast<const float4 *>(rows + (kTok + i) * NP + 4 * q));
-                G = fmaq(Cv, dy[i], G);
-                gB[i] = dotq(G, Bv, gB[i]);
-                const Quad e = G * (d[i] * u[i]);
-                v[4 * i] = e.a.x;
-                v[4 * i + 1] = e.a.y;
-                v[4 * i + 2] = e.b.x;
-                v[4 * i + 3] = e.b.y;
-                G = a[i] * G;
-                const Quad wt = G * before[i];
-                wA[i] = dotq(wt, A, wA[i]);
-                dA = fmaq(wt, d[i], dA);
-            }
-            ring.sums[(w * Q + q) * kLanes + lane] = vec4(dA);
-            if (ch > 0) {
-                ring.slot[(w * Q + q) * kLanes + lane] = vec4(G);
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive(ring.bar + w * Q + q);
-            } else if (p.dh0 && live) {
-                store_quad(p.dh0 + state, 4 * q, p.N, vec4(G));
-            }
-            const float dB = sum_values(v);
-            if (row_in) {
-                out[4 * q] = dB;
-                out[NP + 4 * q] = dC;
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < kTok; ++i) {
-            if (!live || t0 + i >= p.T) break;
-            const int64_t at = (b * p.T + t0 + i) * p.C + c;
-            const float gb = gB[i].x + gB[i].y;
-            float ddt = fmaf(wA[i].x + wA[i].y, kLn2, u[i] * gb), du = d[i] * gb;
-            if (p.softplus) ddt *= logistic<float>(raw[i]);
-            if (p.D) du = fmaf(D, dy[i], du);
-            put(static_cast<T *>(p.du) + at, du);
-            put(static_cast<T *>(p.ddt) + at, ddt);
-            dbias += ddt;
-            dD = fmaf(dy[i], u[i], dD);
-            if (p.dz) {
-                float yy = y[i].x + y[i].y;
-                if (p.D) yy = fmaf(D, u[i], yy);
-                put(static_cast<T *>(p.dz) + at, go[i] * yy * act_grad<T>(z[i], 1));
-            }
-        }
-    }
-    chan[w][lane] = make_float2(dD, dbias);
-    __syncthreads();
-    if (!live) return;
-    float *to = parts.chan + (b * p.C + c) * (p.N + 2);
-    for (int n = w; n < p.N; n += W) {
-        float s = 0.f;
-        for (int i = 0; i < W; ++i)
-            s += reinterpret_cast<const float *>(ring.sums + (i * Q + n / 4) * kLanes + lane)[n % 4];
-        to[n] = s;
-    }
-    if (w == 0) {
-        for (int i = 1; i < W; ++i) {
-            dD += chan[i][lane].x;
-            dbias += chan[i][lane].y;
-        }
-        to[p.N] = dD;
-        to[p.N + 1] = dbias;
-    }
-}
-
-// dB and dC from the tiles' parts, each added in order.
-template <typename T>
-__global__ void __launch_bounds__(256)
-ssm_rows_kernel(const __grid_constant__ SsmProblem p, const Parts parts) {
-    const int NP = (p.N + 3) / 4 * 4;
-    const Tiles tl = tiles_of(p.C, p.G);
-    const int64_t rows = p.B * p.T, id = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int64_t n = id % NP, k = id / NP % 2, g = id / (2 * NP) % p.G, row = id / (2 * NP) / p.G;
-    if (row >= rows || n >= p.N) return;
-    float s = 0.f;
-    for (int i = 0; i < tl.per_group; ++i)
-        s += parts.rows[(((g * tl.per_group + i) * rows + row) * 2 + k) * NP + n];
-    put(static_cast<T *>(k ? p.dCm : p.dBm) + (row * p.G + g) * p.N + n, s);
-}
-// dA, dD and ddt_bias from the batch entries' parts.
-__global__ void __launch_bounds__(256)
-ssm_chan_kernel(const __grid_constant__ SsmProblem p, const Parts parts) {
-    const int64_t w = p.N + 2, id = (int64_t)blockIdx.x * 256 + threadIdx.x, c = id / w, n = id % w;
-    if (c >= p.C) return;
-    float s = 0.f;
-    for (int64_t b = 0; b < p.B; ++b) s += parts.chan[(b * p.C + c) * w + n];
-    if (n < p.N) p.dA[c * p.N + n] = s;
-    else if (n == p.N) { if (p.dD) p.dD[c] = s; }
-    else if (p.dbias) p.dbias[c] = s;
 }
 
 // One token of each row on the pages of a pool. kL lanes (a power of two) own a channel, four states
@@ -460,7 +844,7 @@ ssm_step_kernel(const __grid_constant__ SsmProblem p, int lanes, unsigned int *e
                 Cv[j] = n0 + j < p.N ? get(Cp + n0 + j) : 0.f;
             }
             const Quad x = Quad{make_float2(Bv[0], Bv[1]), make_float2(Bv[2], Bv[3])} * (d * u);
-            const Quad h = fmaq(exp2q(A * d), quad(load_quad(S, n0, p.N)), x);
+            const Quad h = fmaq(Quad{decay2(A.a, both(d)), decay2(A.b, both(d))}, quad(load_quad(S, n0, p.N)), x);
             store_quad(S, n0, p.N, vec4(h));
             s = dotq(h, Quad{make_float2(Cv[0], Cv[1]), make_float2(Cv[2], Cv[3])}, s);
         }
@@ -478,66 +862,94 @@ ssm_step_kernel(const __grid_constant__ SsmProblem p, int lanes, unsigned int *e
     put(static_cast<T *>(p.o) + r * p.C + c, y);
 }
 
-int quads(const SsmProblem &p) { return (p.N + 3) / 4; }
-
-// Warps of a ring: at most one for each chunk, and what shared memory holds.
-int ring_warps(const SsmProblem &p) {
+template <typename T, int kCh>
+int ring_warps(const SsmProblem &p, int in, bool backward, int most) {
     const int64_t chunks = (p.T + kTok - 1) / kTok;
-    return (int)std::min<int64_t>(quads(p) > 16 ? 4 : 8, chunks);
+    int W = most;
+    while (W > 1 && Ring<T, kCh>::bytes(W, in, p.N, backward) > 216 * 1024) W /= 2;
+    return (int)std::min<int64_t>(W, chunks);
 }
+
+// Whether the rows of all inputs, and the first channels and groups of the tiles, are on 16 bytes.
+bool vectors(const SsmProblem &p) {
+    const int es = p.io == 0 ? 2 : 4;
+    for (const SsmRows *r : {&p.u, &p.dt, &p.z, &p.go, &p.Bm, &p.Cm})
+        if (r->p && (reinterpret_cast<uintptr_t>(r->p) % 16 || r->b * es % 16 || r->t * es % 16)) return false;
+    return p.C / p.G * es % 16 == 0 && p.N * es % 16 == 0;
+}
+
+// Channels of a lane in the backward pass: two, which share the loads of B and C and the sums across
+// lanes, where the states of a step fit shared memory.
+int bwd_channels(const SsmProblem &p) { return p.N <= 64 ? 2 : 1; }
 
 struct BwdWorkspace {
     size_t marks, rows, chan, all;
 };
 BwdWorkspace bwd_workspace(const SsmProblem &p) {
     auto round = [](size_t n) { return (n + 255) & ~size_t(255); };
-    const Tiles tl = tiles_of(p.C, p.G);
-    const size_t chunks = (size_t)((p.T + kTok - 1) / kTok), Q = (size_t)quads(p);
+    const int ch = bwd_channels(p);
+    const Tiles tl = tiles_of(p.C, p.G, ch);
+    const size_t chunks = (size_t)((p.T + kTok - 1) / kTok), Q = (size_t)(p.N + 4 / ch - 1) / (4 / ch);
     BwdWorkspace w;
-    w.marks = round((size_t)p.B * chunks * tl.all * Q * kLanes * 16);
-    w.rows = round((size_t)tl.all * p.B * p.T * 2 * 4 * Q * 4);
+    w.marks = round((size_t)p.B * chunks * tl.all * Q * 32 * 16);
+    w.rows = round((size_t)tl.all * p.B * p.T * 2 * ((p.N + 3) / 4 * 4) * 4);
     w.chan = round((size_t)p.B * p.C * (p.N + 2) * 4);
     w.all = w.marks + w.rows + w.chan;
     return w;
 }
 
-template <typename T, int kQ, bool kOut>
-cudaError_t run_fwd(const SsmProblem &p, float4 *marks, unsigned int *err, cudaStream_t s) {
-    const int W = ring_warps(p);
-    const size_t smem = Ring::bytes(W, quads(p), false);
-    const cudaError_t e = cudaFuncSetAttribute(ssm_fwd_kernel<T, kQ, kOut>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+template <typename T, int kCh, int kN, bool kOut, bool kVec>
+cudaError_t run_fwd(const SsmProblem &p, int warps, float4 *marks, unsigned int *err, cudaStream_t s) {
+    constexpr int in = kOut ? 3 : 2;
+    const int W = ring_warps<T, kCh>(p, in, false, warps);
+    const size_t smem = Ring<T, kCh>::bytes(W, in, p.N, false);
+    const auto kernel = ssm_fwd_kernel<T, kCh, kN, kOut, kVec>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    ssm_fwd_kernel<T, kQ, kOut><<<(unsigned)(p.B * tiles_of(p.C, p.G).all), 32 * W, smem, s>>>(p, marks, err);
+    kernel<<<(unsigned)(p.B * tiles_of(p.C, p.G, kCh).all), 32 * W, smem, s>>>(p, marks, err);
     return cudaGetLastError();
 }
-template <bool kOut>
-cudaError_t fwd(const SsmProblem &p, float4 *marks, unsigned int *err, cudaStream_t s) {
+template <typename T, int kCh, bool kOut>
+cudaError_t fwd(const SsmProblem &p, int num_sms, float4 *marks, unsigned int *err, cudaStream_t s) {
+    // 16 warps to an SM: of one ring where there are no more rings than SMs
+    const int warps = p.B * tiles_of(p.C, p.G, kCh).all <= num_sms ? 16 : 8;
     cudaError_t e;
-    if (p.io == 0)
-        e = quads(p) == 4 ? run_fwd<__nv_bfloat16, 4, kOut>(p, marks, err, s)
-                          : run_fwd<__nv_bfloat16, 0, kOut>(p, marks, err, s);
-    else
-        e = quads(p) == 4 ? run_fwd<float, 4, kOut>(p, marks, err, s) : run_fwd<float, 0, kOut>(p, marks, err, s);
+    if (!vectors(p)) e = run_fwd<T, kCh, 0, kOut, false>(p, warps, marks, err, s);
+    else if (p.N == 16) e = run_fwd<T, kCh, 16, kOut, true>(p, warps, marks, err, s);
+    else e = run_fwd<T, kCh, 0, kOut, true>(p, warps, marks, err, s);
     if (e == cudaSuccess) count_launches(1);
     return e;
 }
 
-template <typename T, int kQ>
+template <typename T, int kCh, int kN, bool kVec>
 cudaError_t run_bwd(const SsmProblem &p, const float4 *marks, const Parts &parts, unsigned int *err, cudaStream_t s) {
-    const int W = ring_warps(p);
-    const size_t smem = Ring::bytes(W, quads(p), true);
-    cudaError_t e = cudaFuncSetAttribute(ssm_bwd_kernel<T, kQ>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)smem);
+    const int W = ring_warps<T, kCh>(p, 4, true, 8);
+    const size_t smem = Ring<T, kCh>::bytes(W, 4, p.N, true);
+    const auto kernel = ssm_bwd_kernel<T, kCh, kN, kVec>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    const Tiles tl = tiles_of(p.C, p.G);
-    ssm_bwd_kernel<T, kQ><<<(unsigned)(p.B * tl.all), 32 * W, smem, s>>>(p, marks, parts, err);
+    const Tiles tl = tiles_of(p.C, p.G, kCh);
+    kernel<<<(unsigned)(p.B * tl.all), 32 * W, smem, s>>>(p, marks, parts, err);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    const int64_t rows = p.B * p.T * p.G * 2 * 4 * quads(p), chan = p.C * (p.N + 2);
-    ssm_rows_kernel<T><<<(unsigned)((rows + 255) / 256), 256, 0, s>>>(p, parts);
+    const int64_t rows = p.B * p.T * p.G * 2 * ((p.N + 3) / 4 * 4), chan = p.C * (p.N + 2);
+    ssm_rows_kernel<T><<<(unsigned)((rows + 255) / 256), 256, 0, s>>>(p, parts, tl);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     ssm_chan_kernel<<<(unsigned)((chan + 255) / 256), 256, 0, s>>>(p, parts);
     return cudaGetLastError();
+}
+template <typename T, int kCh>
+cudaError_t bwd(const SsmProblem &p, int num_sms, void *ws, unsigned int *err, cudaStream_t s) {
+    const BwdWorkspace lay = bwd_workspace(p);
+    char *at = static_cast<char *>(ws);
+    float4 *marks = reinterpret_cast<float4 *>(at);
+    const Parts parts{reinterpret_cast<float *>(at + lay.marks), reinterpret_cast<float *>(at + lay.marks + lay.rows)};
+    cudaError_t e = fwd<T, kCh, false>(p, num_sms, marks, err, s);
+    if (e != cudaSuccess) return e;
+    if (!vectors(p)) e = run_bwd<T, kCh, 0, false>(p, marks, parts, err, s);
+    else if (p.N == 16) e = run_bwd<T, kCh, 16, true>(p, marks, parts, err, s);
+    else e = run_bwd<T, kCh, 0, true>(p, marks, parts, err, s);
+    if (e == cudaSuccess) count_launches(3);
+    return e;
 }
 
 }  // namespace
@@ -545,25 +957,15 @@ cudaError_t run_bwd(const SsmProblem &p, const float4 *marks, const Parts &parts
 size_t ssm_fwd_workspace_bytes(const SsmProblem &, int, int) { return 0; }
 size_t ssm_bwd_workspace_bytes(const SsmProblem &p, int, int) { return bwd_workspace(p).all; }
 
-cudaError_t launch_ssm_fwd(const SsmProblem &p, int, int, void *, unsigned int *dev_err, cudaStream_t s) {
-    return fwd<true>(p, nullptr, dev_err, s);
+cudaError_t launch_ssm_fwd(const SsmProblem &p, int, int num_sms, void *, unsigned int *dev_err, cudaStream_t s) {
+    return p.io == 0 ? fwd<__nv_bfloat16, 1, true>(p, num_sms, nullptr, dev_err, s)
+                     : fwd<float, 1, true>(p, num_sms, nullptr, dev_err, s);
 }
 
-cudaError_t launch_ssm_bwd(const SsmProblem &p, int, int, void *ws, unsigned int *dev_err, cudaStream_t s) {
-    const BwdWorkspace lay = bwd_workspace(p);
-    char *at = static_cast<char *>(ws);
-    float4 *marks = reinterpret_cast<float4 *>(at);
-    const Parts parts{reinterpret_cast<float *>(at + lay.marks), reinterpret_cast<float *>(at + lay.marks + lay.rows)};
-    cudaError_t e = fwd<false>(p, marks, dev_err, s);
-    if (e != cudaSuccess) return e;
-    if (p.io == 0)
-        e = quads(p) == 4 ? run_bwd<__nv_bfloat16, 4>(p, marks, parts, dev_err, s)
-                          : run_bwd<__nv_bfloat16, 0>(p, marks, parts, dev_err, s);
-    else
-        e = quads(p) == 4 ? run_bwd<float, 4>(p, marks, parts, dev_err, s)
-                          : run_bwd<float, 0>(p, marks, parts, dev_err, s);
-    if (e == cudaSuccess) count_launches(3);
-    return e;
+cudaError_t launch_ssm_bwd(const SsmProblem &p, int, int num_sms, void *ws, unsigned int *dev_err, cudaStream_t s) {
+    if (bwd_channels(p) == 2)
+        return p.io == 0 ? bwd<__nv_bfloat16, 2>(p, num_sms, ws, dev_err, s) : bwd<float, 2>(p, num_sms, ws, dev_err, s);
+    return p.io == 0 ? bwd<__nv_bfloat16, 1>(p, num_sms, ws, dev_err, s) : bwd<float, 1>(p, num_sms, ws, dev_err, s);
 }
 
 cudaError_t launch_ssm_step(const SsmProblem &p, int, unsigned int *dev_err, cudaStream_t s) {

@@ -78,6 +78,20 @@ def test_long_and_short_memories(steps):
     check(make(1, 200, 32, 1, 16, "f32", seed=4, steps=steps), "f32")
 
 
+def test_steps_of_zero_keep_the_state():
+    """Bit for bit, whatever A is."""
+    from chunkwise_recurrent_prefill_gb300 import ssm_fwd, ssm_step
+    t = {k: ref.gpu(v) for k, v in make(2, 50, 40, 1, 16, "f32", seed=3).items()}
+    dt = torch.zeros_like(t["dt"])
+    A = t["A"] * torch.logspace(-6, 6, 40, device="cuda")[:, None]
+    A[3, 2] = -3e38
+    hT = ssm_fwd(t["u"], dt, A, t["Bm"], t["Cm"], h0=t["h0"], softplus=False, return_state=True)[1]
+    assert torch.equal(hT, t["h0"])
+    S = t["h0"].clone()
+    ssm_step(t["u"][:, 0], dt[:, 0], A, t["Bm"][:, 0], t["Cm"][:, 0], S, softplus=False)
+    assert torch.equal(S, t["h0"])
+
+
 def test_no_tokens_and_no_channels():
     from chunkwise_recurrent_prefill_gb300 import ssm_bwd, ssm_fwd
     d = {n: ref.gpu(v) for n, v in make(2, 0, 8, 1, 16, "f32").items()}
