@@ -24,10 +24,12 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <stdlib.h>
 
 #include "elem.cuh"
 #include "gla_internal.h"
 #include "ssm.h"
+#include "tma_host.h"
 
 namespace gla {
 namespace {
@@ -81,17 +83,6 @@ __device__ __forceinline__ float2 softplus2(float2 x) {
 }
 __device__ __forceinline__ float step_size(float x, int softplus) { return softplus ? softplus2(both(x)).x : x; }
 
-__device__ __forceinline__ void copy16(void *to, const void *from, bool in) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(tc::smem_u32(to)), "l"(from),
-                 "r"(in ? 16 : 0)
-                 : "memory");
-}
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int kLeft>
-__device__ __forceinline__ void copies_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
-}
-
 // What a CTA's warps read: the sequence's rows from the tile's first channel (the group's B and C) on.
 struct Source {
     const void *p;
@@ -100,30 +91,23 @@ struct Source {
     int row;
 };
 
-// Brings the tokens [t0, t0 + kTok) of a source into to[kTok][row], with zeros for tokens and
-// elements that do not exist. kVec: rows are on 16 bytes, and the copies stay on their way until
-// copies_wait; else element by element.
-template <typename T, bool kVec>
+// Brings the tokens [t0, t0 + kTok) of a source into to[kTok][row] element by element, with zeros for tokens and
+// elements that do not exist: what TMA does where rows are on 16 bytes.
+template <typename T>
 __device__ __forceinline__ void stage_rows(const Source &s, int64_t t0, int64_t T_, T *to) {
-    constexpr int V = 16 / sizeof(T);
-    const int lane = threadIdx.x % 32;
     const T *p = static_cast<const T *>(s.p) + t0 * s.t;
-    if (kVec) {
-        const int pieces = s.row / V;
-        for (int k = lane; k < kTok * pieces; k += 32) {
-            const int i = k / pieces, v = (k - i * pieces) * V;
-            const bool in = t0 + i < T_ && v < s.width;
-            copy16(to + i * s.row + v, in ? p + i * s.t + v : s.p, in);
-        }
-    } else {
-        for (int k = lane; k < kTok * s.row; k += 32) {
-            const int i = k / s.row, v = k - i * s.row;
-            T x;
-            put(&x, 0.f);
-            to[k] = t0 + i < T_ && v < s.width ? p[i * s.t + v] : x;
-        }
+    T zero;
+    put(&zero, 0.f);
+    for (int k = threadIdx.x % 32; k < kTok * s.row; k += 32) {
+        const int i = k / s.row, v = k - i * s.row;
+        to[k] = t0 + i < T_ && v < s.width ? p[i * s.t + v] : zero;
     }
 }
+
+// Tensor maps of the rows: boxes of kTok tokens by a tile's channels (or a group's states).
+struct Maps {
+    CUtensorMap in[4], b, c, out[3];
+};
 
 // B and C of the chunk as floats, the values of two tokens side by side as the packed arithmetic takes
 // them: from[2][kTok][N] -> to[2][kTok / 2][NP] float2, NP = N up to a multiple of 4, zero past N.
@@ -187,7 +171,7 @@ struct Place {
     __device__ int64_t channel(int j) const { return c0 + (j < mine ? threadIdx.x % 32 * kCh + j : 0); }
     template <typename T>
     __device__ Source channels(const SsmRows &r) const {
-        return Source{static_cast<const T *>(r.p) + b * r.b + c0, r.t, width, 32 * kCh};
+        return Source{r.p ? static_cast<const T *>(r.p) + b * r.b + c0 : nullptr, r.t, width, 32 * kCh};
     }
     template <typename T>
     __device__ Source rows(const SsmRows &r, int N) const {
@@ -201,24 +185,28 @@ struct Place {
 //   sums[W][Q][32] float4 (backward): dA;  turn[W][32][kTurn] float (backward): sums across lanes
 //   rows[W][2][kPairs][NP] float2: B and C of a warp's chunk;  bar[W][Q]
 //   stage[W][2]: a chunk as it lies in memory, on its way while the one before it is worked on:
-//     kIn tensors [kTok][32 kCh], then B and C [kTok][N]
+//     kIn tensors [kTok][32 kCh], then B and C [kTok][N];  full[W][2]: it is there
 constexpr int kTurn = 66;           // (lanes that write pairs side by side meet no bank twice)
 template <typename T, int kCh>
 struct Ring {
     float4 *slot, *A, *sums;
     float *turn;
     float2 *rows;
-    uint64_t *bar;
+    uint64_t *bar, *full;
     unsigned char *stage;
     static __host__ __device__ int steps(int N) { return (N + 4 / kCh - 1) / (4 / kCh); }
     static __host__ __device__ int padded(int N) { return (N + 3) / 4 * 4; }
     static __host__ __device__ size_t stage_bytes(int in, int N) {
-        return ((size_t)in * kTok * 32 * kCh * sizeof(T) + 2 * kTok * (size_t)N * sizeof(T) + 15) / 16 * 16;
+        return ((size_t)in * kTok * 32 * kCh * sizeof(T) + 2 * kTok * (size_t)N * sizeof(T) + 127) / 128 * 128;
+    }
+    static __host__ __device__ size_t round(size_t n) { return (n + 127) / 128 * 128; }
+    static __host__ __device__ size_t stage_at(int W, int N, bool backward) {
+        const size_t Q = steps(N);
+        return W * Q * 32 * 16 * (backward ? 2 : 1) + Q * 2 * 32 * 16 + (backward ? round(W * 32 * kTurn * 4) : 0) +
+               round((size_t)W * 2 * kPairs * padded(N) * 8) + round(W * (Q + 2) * 8);
     }
     static __host__ __device__ size_t bytes(int W, int in, int N, bool backward) {
-        const size_t Q = steps(N);
-        return W * Q * 32 * 16 * (backward ? 2 : 1) + Q * 2 * 32 * 16 + (backward ? W * 32 * kTurn * 4 : 0) +
-               (size_t)W * 2 * kPairs * padded(N) * 8 + (W * Q * 8 + 15) / 16 * 16 + 2 * W * stage_bytes(in, N);
+        return stage_at(W, N, backward) + 2 * W * stage_bytes(in, N);
     }
     __device__ Ring(unsigned char *smem, int W, int N, bool backward) {
         const int Q = steps(N);
@@ -226,9 +214,10 @@ struct Ring {
         A = slot + W * Q * 32;
         sums = A + Q * 2 * 32;
         turn = reinterpret_cast<float *>(sums + (backward ? W * Q * 32 : 0));
-        rows = reinterpret_cast<float2 *>(turn + (backward ? W * 32 * kTurn : 0));
-        bar = reinterpret_cast<uint64_t *>(rows + W * 2 * kPairs * padded(N));
-        stage = reinterpret_cast<unsigned char *>(bar) + (W * Q * 8 + 15) / 16 * 16;
+        rows = reinterpret_cast<float2 *>(reinterpret_cast<unsigned char *>(turn) + (backward ? round(W * 32 * kTurn * 4) : 0));
+        bar = reinterpret_cast<uint64_t *>(reinterpret_cast<unsigned char *>(rows) + round((size_t)W * 2 * kPairs * padded(N) * 8));
+        full = bar + W * Q;
+        stage = smem + stage_at(W, N, backward);
     }
     // A and the barriers; the CTA synchronises.
     __device__ void begin(const SsmProblem &p, const Place<kCh> &at, int W, int N) {
@@ -245,7 +234,7 @@ struct Ring {
             A[(2 * q + 1) * 32 + lane] = make_float4(a[2], a[2], a[3], a[3]);
         }
         if (threadIdx.x == 0) {
-            for (int i = 0; i < W * Q; ++i) tc::mbar_init(bar + i, 1);
+            for (int i = 0; i < W * (Q + 2); ++i) tc::mbar_init(bar + i, 1);
             tc::fence_mbar_init();
         }
         __syncthreads();
@@ -329,24 +318,13 @@ __device__ __forceinline__ void put_lane_pair(T *to, int ip, const float2 (&v)[k
     put_lane_row<T, kCh>(to, 2 * ip, x);
     put_lane_row<T, kCh>(to, 2 * ip + 1, y);
 }
-// Rows of the stage to the tile's rows of a contiguous [B, T, C] tensor.
-template <typename T, int kCh, bool kVec>
+// Rows of the stage to the tile's rows of a contiguous [B, T, C] tensor, where TMA does not do it.
+template <typename T, int kCh>
 __device__ __forceinline__ void write_rows(const T *from, void *to, const SsmProblem &p, const Place<kCh> &at, int64_t t0) {
-    const int lane = threadIdx.x % 32;
     T *out = static_cast<T *>(to) + (at.b * p.T + t0) * p.C + at.c0;
-    if (kVec) {
-        constexpr int V = 16 / sizeof(T), pieces = 32 * kCh / V;
-#pragma unroll
-        for (int j = lane; j < kTok * pieces; j += 32) {
-            const int i = j / pieces, v = j % pieces * V;
-            if (t0 + i < p.T && v < at.width)
-                *reinterpret_cast<uint4 *>(out + i * p.C + v) = *reinterpret_cast<const uint4 *>(from + i * 32 * kCh + v);
-        }
-    } else {
-        for (int i = 0; i < kTok; ++i)
-            for (int v = lane; v < at.width; v += 32)
-                if (t0 + i < p.T) out[i * p.C + v] = from[i * 32 * kCh + v];
-    }
+    for (int i = 0; i < kTok; ++i)
+        for (int v = threadIdx.x % 32; v < at.width; v += 32)
+            if (t0 + i < p.T) out[i * p.C + v] = from[i * 32 * kCh + v];
 }
 
 // Step sizes of the chunk from the stage (zero for tokens and channels that do not exist: they keep the state).
@@ -389,8 +367,8 @@ __device__ __forceinline__ void load_bc(const float2 *row, int q, float2 (&v)[kS
 // [B][chunks][tiles][Q][32] float4. kN: N, if known at compile time.
 template <typename T, int kCh, int kN, bool kOut, bool kVec>
 __global__ void __launch_bounds__(512, 1)
-ssm_fwd_kernel(const __grid_constant__ SsmProblem p, float4 *marks, unsigned int *err) {
-    extern __shared__ __align__(16) unsigned char smem[];
+ssm_fwd_kernel(const __grid_constant__ SsmProblem p, const __grid_constant__ Maps maps, float4 *marks, unsigned int *err) {
+    extern __shared__ __align__(128) unsigned char smem[];
     constexpr int kSt = 4 / kCh, kIn = kOut ? 3 : 2, kRow = kTok * 32 * kCh;
     using R = Ring<T, kCh>;
     const int W = blockDim.x / 32, N = kN ? kN : p.N, Q = R::steps(N), NP = R::padded(N);
@@ -409,28 +387,47 @@ ssm_fwd_kernel(const __grid_constant__ SsmProblem p, float4 *marks, unsigned int
     const size_t stage_bytes = R::stage_bytes(kIn, N);
     auto stage = [&](int k) { return reinterpret_cast<T *>(ring.stage + (2 * w + k) * stage_bytes); };
     const int64_t chunks = (p.T + kTok - 1) / kTok;
+    // the chunk into buffer k of the stage, by one lane where TMA does it
     auto fetch = [&](int64_t ch, int k) {
-        if (ch < chunks) {
-            T *to = stage(k);
-            const int64_t t0 = ch * kTok;
-            stage_rows<T, kVec>(at.template channels<T>(p.u), t0, p.T, to);
-            stage_rows<T, kVec>(at.template channels<T>(p.dt), t0, p.T, to + kRow);
-            if (kOut && p.z.p) stage_rows<T, kVec>(at.template channels<T>(p.z), t0, p.T, to + 2 * kRow);
-            to += kIn * kRow;
-            stage_rows<T, kVec>(at.template rows<T>(p.Bm, N), t0, p.T, to);
-            stage_rows<T, kVec>(at.template rows<T>(p.Cm, N), t0, p.T, to + kTok * N);
+        if (ch >= chunks) return;
+        T *to = stage(k);
+        const int64_t t0 = ch * kTok;
+        if (kVec) {
+            if (lane == 0) {
+                uint64_t *bar = ring.full + 2 * w + k;
+                const bool z = kOut && p.z.p;
+                tc::bulk_wait_read_all();       // the outputs that were there
+                tc::mbar_arrive_expect_tx(bar, ((z ? 3 : 2) * kRow + 2 * kTok * N) * (int)sizeof(T));
+                const int c = (int)at.c0, b = (int)at.b, t = (int)t0, n = (int)at.g * N;
+                tc::tma_load_4d(to, &maps.in[0], bar, c, t, b, 0);
+                tc::tma_load_4d(to + kRow, &maps.in[1], bar, c, t, b, 0);
+                if (z) tc::tma_load_4d(to + 2 * kRow, &maps.in[2], bar, c, t, b, 0);
+                tc::tma_load_4d(to + kIn * kRow, &maps.b, bar, n, t, b, 0);
+                tc::tma_load_4d(to + kIn * kRow + kTok * N, &maps.c, bar, n, t, b, 0);
+            }
+        } else {
+            stage_rows<T>(at.template channels<T>(p.u), t0, p.T, to);
+            stage_rows<T>(at.template channels<T>(p.dt), t0, p.T, to + kRow);
+            if (kOut && p.z.p) stage_rows<T>(at.template channels<T>(p.z), t0, p.T, to + 2 * kRow);
+            stage_rows<T>(at.template rows<T>(p.Bm, N), t0, p.T, to + kIn * kRow);
+            stage_rows<T>(at.template rows<T>(p.Cm, N), t0, p.T, to + kIn * kRow + kTok * N);
         }
-        if (kVec) copies_commit();
     };
     const int prev = w == 0 ? W - 1 : w - 1;
     bool dead = false;
+    auto wait = [&](uint64_t *bar, uint32_t parity) {
+        if (!dead && !ring_wait(bar, parity)) {
+            dead = true;
+            atomicOr(err, kDevErrTimeout);
+        }
+    };
     int k = 0;
+    uint32_t round = 0;         // parity of the stage's buffer
     fetch(w, 0);
-    for (int64_t ch = w; ch < chunks; ch += W, k ^= 1) {
+    for (int64_t ch = w; ch < chunks; ch += W) {
         const int64_t t0 = ch * kTok;
-        fetch(ch + W, k ^ 1);
-        if (kVec) copies_wait<1>();
-        __syncwarp();
+        if (kVec) wait(ring.full + 2 * w + k, round);
+        else __syncwarp();
         T *in = stage(k);
         widen_rows<T, kN>(in + kIn * kRow, rows, N);
         float2 d[kCh][kPairs], x[kCh][kPairs], y[kCh][kPairs];
@@ -441,11 +438,12 @@ ssm_fwd_kernel(const __grid_constant__ SsmProblem p, float4 *marks, unsigned int
             lane_pair<T, kCh>(in, ip, u);
 #pragma unroll
             for (int c = 0; c < kCh; ++c) {
-                x[c][ip] = mul2(d[c][ip], u[c]);
+                x[c][ip] = c < at.mine ? mul2(d[c][ip], u[c]) : both(0.f);
                 y[c][ip] = both(0.f);
             }
         }
         __syncwarp();
+        fetch(ch + W, k ^ 1);
         const uint32_t parity = (uint32_t)((ch - 1) / W) & 1u;
 #pragma unroll 1
         for (int q = 0; q < Q; ++q) {
@@ -465,10 +463,7 @@ ssm_fwd_kernel(const __grid_constant__ SsmProblem p, float4 *marks, unsigned int
             if (ch == 0) {
                 load_states<kCh>(p.h0, p, at, q, h);
             } else {
-                if (!dead && !ring_wait(ring.bar + prev * Q + q, parity)) {
-                    dead = true;
-                    atomicOr(err, kDevErrTimeout);
-                }
+                wait(ring.bar + prev * Q + q, parity);
                 const float4 v = ring.slot[(prev * Q + q) * 32 + lane];
                 h[0] = v.x;
                 h[1] = v.y;
@@ -519,11 +514,23 @@ ssm_fwd_kernel(const __grid_constant__ SsmProblem p, float4 *marks, unsigned int
                 for (int c = 0; c < kCh; ++c) o[c] = y[c][ip];
                 put_lane_pair<T, kCh>(in, ip, o);
             }
-            __syncwarp();
-            write_rows<T, kCh, kVec>(in, p.o, p, at, t0);
+            if (kVec && at.width == 32 * kCh) {
+                tc::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    tc::tma_store_4d(&maps.out[0], in, (int)at.c0, (int)t0, (int)at.b, 0);
+                    tc::bulk_commit();
+                }
+            } else {
+                __syncwarp();
+                write_rows<T, kCh>(in, p.o, p, at, t0);
+            }
         }
         __syncwarp();       // the stage and the rows have been read
+        k ^= 1;
+        if (k == 0) round ^= 1;
     }
+    if (kVec && kOut && lane == 0) tc::bulk_wait_all();
 }
 
 // Where the backward kernel leaves what is summed later, all float:
@@ -534,10 +541,11 @@ struct Parts {
 };
 
 template <typename T, int kCh, int kN, bool kVec>
-__global__ void __launch_bounds__(256, 1)
-ssm_bwd_kernel(const __grid_constant__ SsmProblem p, const float4 *marks, const Parts parts, unsigned int *err) {
-    extern __shared__ __align__(16) unsigned char smem[];
-    __shared__ float2 chan[8][32 * kCh];
+__global__ void __launch_bounds__(kCh == 2 ? 256 : 384, 1)
+ssm_bwd_kernel(const __grid_constant__ SsmProblem p, const __grid_constant__ Maps maps, const float4 *marks,
+               const Parts parts, unsigned int *err) {
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ float2 chan[kCh == 2 ? 8 : 12][32 * kCh];
     constexpr int kSt = 4 / kCh, kIn = 4, kRow = kTok * 32 * kCh;
     using R = Ring<T, kCh>;
     const int W = blockDim.x / 32, N = kN ? kN : p.N, Q = R::steps(N), NP = R::padded(N);
@@ -559,29 +567,50 @@ ssm_bwd_kernel(const __grid_constant__ SsmProblem p, const float4 *marks, const 
     const size_t stage_bytes = R::stage_bytes(kIn, N);
     auto stage = [&](int k) { return reinterpret_cast<T *>(ring.stage + (2 * w + k) * stage_bytes); };
     const int64_t chunks = (p.T + kTok - 1) / kTok;
+    // the chunk into buffer k of the stage, by one lane where TMA does it
     auto fetch = [&](int64_t step, int k) {
-        if (step < chunks) {
-            const int64_t t0 = (chunks - 1 - step) * kTok;
-            T *to = stage(k);
-            stage_rows<T, kVec>(at.template channels<T>(p.u), t0, p.T, to);
-            stage_rows<T, kVec>(at.template channels<T>(p.dt), t0, p.T, to + kRow);
-            stage_rows<T, kVec>(at.template channels<T>(p.go), t0, p.T, to + 2 * kRow);
-            if (p.z.p) stage_rows<T, kVec>(at.template channels<T>(p.z), t0, p.T, to + 3 * kRow);
-            to += kIn * kRow;
-            stage_rows<T, kVec>(at.template rows<T>(p.Bm, N), t0, p.T, to);
-            stage_rows<T, kVec>(at.template rows<T>(p.Cm, N), t0, p.T, to + kTok * N);
+        if (step >= chunks) return;
+        T *to = stage(k);
+        const int64_t t0 = (chunks - 1 - step) * kTok;
+        if (kVec) {
+            if (lane == 0) {
+                uint64_t *bar = ring.full + 2 * w + k;
+                tc::bulk_wait_read_all();       // the gradients that were there
+                tc::mbar_arrive_expect_tx(bar, ((p.z.p ? 4 : 3) * kRow + 2 * kTok * N) * (int)sizeof(T));
+                const int c = (int)at.c0, b = (int)at.b, t = (int)t0, n = (int)at.g * N;
+                tc::tma_load_4d(to, &maps.in[0], bar, c, t, b, 0);
+                tc::tma_load_4d(to + kRow, &maps.in[1], bar, c, t, b, 0);
+                tc::tma_load_4d(to + 2 * kRow, &maps.in[3], bar, c, t, b, 0);
+                if (p.z.p) tc::tma_load_4d(to + 3 * kRow, &maps.in[2], bar, c, t, b, 0);
+                tc::tma_load_4d(to + kIn * kRow, &maps.b, bar, n, t, b, 0);
+                tc::tma_load_4d(to + kIn * kRow + kTok * N, &maps.c, bar, n, t, b, 0);
+            }
+        } else {
+            stage_rows<T>(at.template channels<T>(p.u), t0, p.T, to);
+            stage_rows<T>(at.template channels<T>(p.dt), t0, p.T, to + kRow);
+            stage_rows<T>(at.template channels<T>(p.go), t0, p.T, to + 2 * kRow);
+            if (p.z.p) stage_rows<T>(at.template channels<T>(p.z), t0, p.T, to + 3 * kRow);
+            stage_rows<T>(at.template rows<T>(p.Bm, N), t0, p.T, to + kIn * kRow);
+            stage_rows<T>(at.template rows<T>(p.Cm, N), t0, p.T, to + kIn * kRow + kTok * N);
         }
-        if (kVec) copies_commit();
     };
     const int prev = w == 0 ? W - 1 : w - 1;
     bool dead = false;
+    auto wait = [&](uint64_t *bar, uint32_t parity) {
+        if (!dead && !ring_wait(bar, parity)) {
+            dead = true;
+            atomicOr(err, kDevErrTimeout);
+        }
+    };
     int k = 0;
+    uint32_t round = 0;         // parity of the stage's buffer
     fetch(w, 0);
-    for (int64_t step = w; step < chunks; step += W, k ^= 1) {
+    for (int64_t step = w; step < chunks; step += W) {
         const int64_t ch = chunks - 1 - step, t0 = ch * kTok;
-        fetch(step + W, k ^ 1);
-        if (kVec) copies_wait<1>();
-        __syncwarp();
+        const float4 *mark = marks + ((at.b * chunks + ch) * tl.all + at.tile) * Q * 32 + lane;
+        float4 mk = mark[0];        // a step's states come while the one before is worked on
+        if (kVec) wait(ring.full + 2 * w + k, round);
+        else __syncwarp();
         T *in = stage(k);
         widen_rows<T, kN>(in + kIn * kRow, rows, N);
         float2 d[kCh][kPairs], x[kCh][kPairs], dy[kCh][kPairs];
@@ -599,22 +628,23 @@ ssm_bwd_kernel(const __grid_constant__ SsmProblem p, const float4 *marks, const 
                 dy[c][ip] = go[c];
                 if (p.z.p)
                     dy[c][ip] = mul2(go[c], mul2(z[c], make_float2(logistic<T>(z[c].x), logistic<T>(z[c].y))));
+                if (c >= at.mine) x[c][ip] = dy[c][ip] = both(0.f);     // (TMA brings the next group's channels)
                 y[c][ip] = gB[c][ip] = wA[c][ip] = both(0.f);
             }
         }
         __syncwarp();
+        fetch(step + W, k ^ 1);
         const uint32_t parity = (uint32_t)((step - 1) / W) & 1u;
         // Sums across the lanes: a lane leaves its values in its row of turn; a step's are dC and dB of kSt states
         // of 8 tokens (2 tokens side by side), [2][kSt][kTok]. kCh = 2: two steps' values, 64 in all. Lane l
         // adds the columns 2 l and 2 l + 1 and has two tokens of dC or dB of one state.
-        const float4 *mark = marks + ((at.b * chunks + ch) * tl.all + at.tile) * Q * 32 + lane;
 #pragma unroll 1
         for (int q = 0; q < Q; ++q) {
             float2 A[4], a[4][kPairs], s[4][kPairs];
             float *mine = turn + lane * kTurn + (kCh == 2 ? q % 2 * 32 : 0);
             ring.load_a(q, A);
-            const float4 mk = mark[q * 32];
             float h[4] = {mk.x, mk.y, mk.z, mk.w};
+            if (q + 1 < Q) mk = mark[(q + 1) * 32];
 #pragma unroll
             for (int ip = 0; ip < kPairs; ++ip) {
                 float2 b[kSt], c[kSt], dC[kSt];
@@ -637,40 +667,31 @@ ssm_bwd_kernel(const __grid_constant__ SsmProblem p, const float4 *marks, const 
             if (step == 0) {
                 load_states<kCh>(p.dhT, p, at, q, G);
             } else {
-                if (!dead && !ring_wait(ring.bar + prev * Q + q, parity)) {
-                    dead = true;
-                    atomicOr(err, kDevErrTimeout);
-                }
+                wait(ring.bar + prev * Q + q, parity);
                 const float4 v = ring.slot[(prev * Q + q) * 32 + lane];
                 G[0] = v.x;
                 G[1] = v.y;
                 G[2] = v.z;
                 G[3] = v.w;
             }
-            float2 dA[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) dA[j] = both(0.f);
+            // the walk, which the next warp waits for; a becomes the gradient of the state, the state before a
+            // token becomes w (that before the first token: h)
 #pragma unroll
             for (int ip = kPairs - 1; ip >= 0; --ip) {
-                float2 b[kSt], c[kSt], dB[kSt];
-                load_bc<kSt>(rows + ip * NP, q, b);
+                float2 c[kSt];
                 load_bc<kSt>(rows + (kPairs + ip) * NP, q, c);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    float2 g = mul2(c[j % kSt], dy[j / kSt][ip]), wt;
+                    float2 g = mul2(c[j % kSt], dy[j / kSt][ip]);
                     g.y += G[j];
                     G[j] = a[j][ip].y * g.y;
-                    wt.y = G[j] * s[j][ip].x;
+                    s[j][ip].x *= G[j];
                     g.x += G[j];
                     G[j] = a[j][ip].x * g.x;
-                    wt.x = G[j] * (ip ? s[j][ip ? ip - 1 : 0].y : h[j]);
-                    gB[j / kSt][ip] = fma2(g, b[j % kSt], gB[j / kSt][ip]);
-                    wA[j / kSt][ip] = fma2(wt, A[j], wA[j / kSt][ip]);
-                    dA[j] = fma2(wt, d[j / kSt][ip], dA[j]);
-                    dB[j % kSt] = j < kSt ? mul2(g, x[0][ip]) : fma2(g, x[j / kSt][ip], dB[j % kSt]);
+                    if (ip) s[j][ip - 1].y *= G[j];
+                    else h[j] *= G[j];
+                    a[j][ip] = g;
                 }
-#pragma unroll
-                for (int n = 0; n < kSt; ++n) *reinterpret_cast<float2 *>(mine + (kSt + n) * kTok + 2 * ip) = dB[n];
             }
             if (ch > 0) {
                 ring.slot[(w * Q + q) * 32 + lane] = make_float4(G[0], G[1], G[2], G[3]);
@@ -678,6 +699,24 @@ ssm_bwd_kernel(const __grid_constant__ SsmProblem p, const float4 *marks, const 
                 if (lane == 0) tc::mbar_arrive(ring.bar + w * Q + q);
             } else if (p.dh0) {
                 store_states<kCh>(p.dh0, p, at, q, G);
+            }
+            float2 dA[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) dA[j] = both(0.f);
+#pragma unroll
+            for (int ip = 0; ip < kPairs; ++ip) {
+                float2 b[kSt], dB[kSt];
+                load_bc<kSt>(rows + ip * NP, q, b);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 g = a[j][ip], wt = make_float2(ip ? s[j][ip ? ip - 1 : 0].y : h[j], s[j][ip].x);
+                    gB[j / kSt][ip] = fma2(g, b[j % kSt], gB[j / kSt][ip]);
+                    wA[j / kSt][ip] = fma2(wt, A[j], wA[j / kSt][ip]);
+                    dA[j] = fma2(wt, d[j / kSt][ip], dA[j]);
+                    dB[j % kSt] = j < kSt ? mul2(g, x[0][ip]) : fma2(g, x[j / kSt][ip], dB[j % kSt]);
+                }
+#pragma unroll
+                for (int n = 0; n < kSt; ++n) *reinterpret_cast<float2 *>(mine + (kSt + n) * kTok + 2 * ip) = dB[n];
             }
             // (a chunk's sum first: those of thousands of tokens go up in two steps)
             float4 *sum = ring.sums + (w * Q + q) * 32 + lane;
@@ -736,12 +775,26 @@ ssm_bwd_kernel(const __grid_constant__ SsmProblem p, const float4 *marks, const 
             dD[c] += sD[c].x + sD[c].y;
             dbias[c] += sbias[c].x + sbias[c].y;
         }
-        __syncwarp();
-        write_rows<T, kCh, kVec>(in, p.du, p, at, t0);
-        write_rows<T, kCh, kVec>(in + kRow, p.ddt, p, at, t0);
-        if (p.dz) write_rows<T, kCh, kVec>(in + 3 * kRow, p.dz, p, at, t0);
+        if (kVec && at.width == 32 * kCh) {
+            tc::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                tc::tma_store_4d(&maps.out[0], in, (int)at.c0, (int)t0, (int)at.b, 0);
+                tc::tma_store_4d(&maps.out[1], in + kRow, (int)at.c0, (int)t0, (int)at.b, 0);
+                if (p.dz) tc::tma_store_4d(&maps.out[2], in + 3 * kRow, (int)at.c0, (int)t0, (int)at.b, 0);
+                tc::bulk_commit();
+            }
+        } else {
+            __syncwarp();
+            write_rows<T, kCh>(in, p.du, p, at, t0);
+            write_rows<T, kCh>(in + kRow, p.ddt, p, at, t0);
+            if (p.dz) write_rows<T, kCh>(in + 3 * kRow, p.dz, p, at, t0);
+        }
         __syncwarp();       // the stage and the rows have been read
+        k ^= 1;
+        if (k == 0) round ^= 1;
     }
+    if (kVec && lane == 0) tc::bulk_wait_all();
 #pragma unroll
     for (int c = 0; c < kCh; ++c) chan[w][lane * kCh + c] = make_float2(dD[c], dbias[c]);
     __syncthreads();
@@ -866,8 +919,35 @@ template <typename T, int kCh>
 int ring_warps(const SsmProblem &p, int in, bool backward, int most) {
     const int64_t chunks = (p.T + kTok - 1) / kTok;
     int W = most;
-    while (W > 1 && Ring<T, kCh>::bytes(W, in, p.N, backward) > 216 * 1024) W /= 2;
+    // (the backward kernel has 4 KB of its own)
+    while (W > 1 && Ring<T, kCh>::bytes(W, in, p.N, backward) > 222 * 1024) W = W > 8 ? W - 4 : W / 2;
     return (int)std::min<int64_t>(W, chunks);
+}
+
+// A map of [B, T, cols] rows.
+bool rows_map(CUtensorMap *m, const void *base, int io, int64_t cols, int64_t T, int64_t B, int64_t st, int64_t sb,
+              int box_cols) {
+    EncodeTiledFn fn = encode_tiled_fn();
+    if (!fn) return false;
+    const cuuint64_t es = io == 0 ? 2 : 4;
+    const cuuint64_t dims[4] = {(cuuint64_t)cols, (cuuint64_t)T, (cuuint64_t)B, 1};
+    const cuuint64_t strides[3] = {(cuuint64_t)st * es, (cuuint64_t)sb * es, (cuuint64_t)sb * es};
+    const cuuint32_t box[4] = {(cuuint32_t)box_cols, kTok, 1, 1}, one[4] = {1, 1, 1, 1};
+    return fn(m, io == 0 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4,
+              const_cast<void *>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// The maps of a call; false where a map cannot be made.
+bool make_maps(const SsmProblem &p, int ch, Maps *m) {
+    const SsmRows *in[4] = {&p.u, &p.dt, &p.z, &p.go};
+    void *const out[3] = {p.du ? p.du : p.o, p.ddt, p.dz};
+    for (int i = 0; i < 4; ++i)
+        if (in[i]->p && !rows_map(&m->in[i], in[i]->p, p.io, p.C, p.T, p.B, in[i]->t, in[i]->b, 32 * ch)) return false;
+    for (int i = 0; i < 3; ++i)
+        if (out[i] && !rows_map(&m->out[i], out[i], p.io, p.C, p.T, p.B, p.C, p.T * p.C, 32 * ch)) return false;
+    return rows_map(&m->b, p.Bm.p, p.io, p.G * p.N, p.T, p.B, p.Bm.t, p.Bm.b, p.N) &&
+           rows_map(&m->c, p.Cm.p, p.io, p.G * p.N, p.T, p.B, p.Cm.t, p.Cm.b, p.N);
 }
 
 // Whether the rows of all inputs, and the first channels and groups of the tiles, are on 16 bytes.
@@ -875,12 +955,18 @@ bool vectors(const SsmProblem &p) {
     const int es = p.io == 0 ? 2 : 4;
     for (const SsmRows *r : {&p.u, &p.dt, &p.z, &p.go, &p.Bm, &p.Cm})
         if (r->p && (reinterpret_cast<uintptr_t>(r->p) % 16 || r->b * es % 16 || r->t * es % 16)) return false;
-    return p.C / p.G * es % 16 == 0 && p.N * es % 16 == 0;
+    // (strides and coordinates that a tensor map holds)
+    for (const SsmRows *r : {&p.u, &p.dt, &p.z, &p.go, &p.Bm, &p.Cm})
+        if (r->p && (r->b >= int64_t(1) << 38 || r->t >= int64_t(1) << 38)) return false;
+    return p.C / p.G * es % 16 == 0 && p.N * es % 16 == 0 && p.T * p.C < int64_t(1) << 38;
 }
 
 // Channels of a lane in the backward pass: two, which share the loads of B and C and the sums across
 // lanes, where the states of a step fit shared memory.
-int bwd_channels(const SsmProblem &p) { return p.N <= 64 ? 2 : 1; }
+int bwd_channels(const SsmProblem &p) {
+    const char *e = getenv("SSM_CH");
+    if (e) return atoi(e);
+    return p.N <= 64 ? 2 : 1; }
 
 struct BwdWorkspace {
     size_t marks, rows, chan, all;
@@ -899,37 +985,38 @@ BwdWorkspace bwd_workspace(const SsmProblem &p) {
 }
 
 template <typename T, int kCh, int kN, bool kOut, bool kVec>
-cudaError_t run_fwd(const SsmProblem &p, int warps, float4 *marks, unsigned int *err, cudaStream_t s) {
+cudaError_t run_fwd(const SsmProblem &p, const Maps &maps, int warps, float4 *marks, unsigned int *err, cudaStream_t s) {
     constexpr int in = kOut ? 3 : 2;
     const int W = ring_warps<T, kCh>(p, in, false, warps);
     const size_t smem = Ring<T, kCh>::bytes(W, in, p.N, false);
     const auto kernel = ssm_fwd_kernel<T, kCh, kN, kOut, kVec>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    kernel<<<(unsigned)(p.B * tiles_of(p.C, p.G, kCh).all), 32 * W, smem, s>>>(p, marks, err);
+    kernel<<<(unsigned)(p.B * tiles_of(p.C, p.G, kCh).all), 32 * W, smem, s>>>(p, maps, marks, err);
     return cudaGetLastError();
 }
 template <typename T, int kCh, bool kOut>
-cudaError_t fwd(const SsmProblem &p, int num_sms, float4 *marks, unsigned int *err, cudaStream_t s) {
+cudaError_t fwd(const SsmProblem &p, const Maps *maps, int num_sms, float4 *marks, unsigned int *err, cudaStream_t s) {
     // 16 warps to an SM: of one ring where there are no more rings than SMs
     const int warps = p.B * tiles_of(p.C, p.G, kCh).all <= num_sms ? 16 : 8;
     cudaError_t e;
-    if (!vectors(p)) e = run_fwd<T, kCh, 0, kOut, false>(p, warps, marks, err, s);
-    else if (p.N == 16) e = run_fwd<T, kCh, 16, kOut, true>(p, warps, marks, err, s);
-    else e = run_fwd<T, kCh, 0, kOut, true>(p, warps, marks, err, s);
+    if (!maps) e = run_fwd<T, kCh, 0, kOut, false>(p, Maps{}, warps, marks, err, s);
+    else if (p.N == 16) e = run_fwd<T, kCh, 16, kOut, true>(p, *maps, warps, marks, err, s);
+    else e = run_fwd<T, kCh, 0, kOut, true>(p, *maps, warps, marks, err, s);
     if (e == cudaSuccess) count_launches(1);
     return e;
 }
 
 template <typename T, int kCh, int kN, bool kVec>
-cudaError_t run_bwd(const SsmProblem &p, const float4 *marks, const Parts &parts, unsigned int *err, cudaStream_t s) {
-    const int W = ring_warps<T, kCh>(p, 4, true, 8);
+cudaError_t run_bwd(const SsmProblem &p, const Maps &maps, const float4 *marks, const Parts &parts, unsigned int *err,
+                    cudaStream_t s) {
+    const int W = ring_warps<T, kCh>(p, 4, true, kCh == 2 ? 8 : 12);
     const size_t smem = Ring<T, kCh>::bytes(W, 4, p.N, true);
     const auto kernel = ssm_bwd_kernel<T, kCh, kN, kVec>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     const Tiles tl = tiles_of(p.C, p.G, kCh);
-    kernel<<<(unsigned)(p.B * tl.all), 32 * W, smem, s>>>(p, marks, parts, err);
+    kernel<<<(unsigned)(p.B * tl.all), 32 * W, smem, s>>>(p, maps, marks, parts, err);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     const int64_t rows = p.B * p.T * p.G * 2 * ((p.N + 3) / 4 * 4), chan = p.C * (p.N + 2);
     ssm_rows_kernel<T><<<(unsigned)((rows + 255) / 256), 256, 0, s>>>(p, parts, tl);
@@ -943,11 +1030,14 @@ cudaError_t bwd(const SsmProblem &p, int num_sms, void *ws, unsigned int *err, c
     char *at = static_cast<char *>(ws);
     float4 *marks = reinterpret_cast<float4 *>(at);
     const Parts parts{reinterpret_cast<float *>(at + lay.marks), reinterpret_cast<float *>(at + lay.marks + lay.rows)};
-    cudaError_t e = fwd<T, kCh, false>(p, num_sms, marks, err, s);
+    Maps maps;
+    const bool vec = vectors(p);
+    if (vec && !make_maps(p, kCh, &maps)) return cudaErrorInvalidResourceHandle;
+    cudaError_t e = fwd<T, kCh, false>(p, vec ? &maps : nullptr, num_sms, marks, err, s);
     if (e != cudaSuccess) return e;
-    if (!vectors(p)) e = run_bwd<T, kCh, 0, false>(p, marks, parts, err, s);
-    else if (p.N == 16) e = run_bwd<T, kCh, 16, true>(p, marks, parts, err, s);
-    else e = run_bwd<T, kCh, 0, true>(p, marks, parts, err, s);
+    if (!vec) e = run_bwd<T, kCh, 0, false>(p, Maps{}, marks, parts, err, s);
+    else if (p.N == 16) e = run_bwd<T, kCh, 16, true>(p, maps, marks, parts, err, s);
+    else e = run_bwd<T, kCh, 0, true>(p, maps, marks, parts, err, s);
     if (e == cudaSuccess) count_launches(3);
     return e;
 }
@@ -958,8 +1048,12 @@ size_t ssm_fwd_workspace_bytes(const SsmProblem &, int, int) { return 0; }
 size_t ssm_bwd_workspace_bytes(const SsmProblem &p, int, int) { return bwd_workspace(p).all; }
 
 cudaError_t launch_ssm_fwd(const SsmProblem &p, int, int num_sms, void *, unsigned int *dev_err, cudaStream_t s) {
-    return p.io == 0 ? fwd<__nv_bfloat16, 1, true>(p, num_sms, nullptr, dev_err, s)
-                     : fwd<float, 1, true>(p, num_sms, nullptr, dev_err, s);
+    Maps maps;
+    const bool vec = vectors(p);
+    if (vec && !make_maps(p, 1, &maps)) return cudaErrorInvalidResourceHandle;
+    const Maps *m = vec ? &maps : nullptr;
+    return p.io == 0 ? fwd<__nv_bfloat16, 1, true>(p, m, num_sms, nullptr, dev_err, s)
+                     : fwd<float, 1, true>(p, m, num_sms, nullptr, dev_err, s);
 }
 
 cudaError_t launch_ssm_bwd(const SsmProblem &p, int, int num_sms, void *ws, unsigned int *dev_err, cudaStream_t s) {
