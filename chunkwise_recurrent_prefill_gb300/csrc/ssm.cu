@@ -63,25 +63,26 @@ __device__ __forceinline__ float scale_a(float a) {
     return isinf(x) ? copysignf(3.4028235e38f, x) : x;
 }
 
-// softplus(x) = max(x, 0) + log(1 + e), e = e^-|x|, of a pair. log(1 + e) is e times a polynomial
-// fitted to log(1 + e) / e on [0, 1] with the smallest relative error (5e-9, 1.4e-7 with the roundings of
-// fp32): the small steps that give a state its memory keep their digits, which log(1 + e) formed as
-// such would lose, and ten multiply-adds of pairs cost a third of the library's functions.
-__device__ __forceinline__ float2 softplus2(float2 x) {
-    const float2 e = make_float2(ex2(fabsf(x.x) * -kLog2e), ex2(fabsf(x.y) * -kLog2e));
-    float2 r = both(-0.003244024235755205f);
-    r = fma2(r, e, both(0.019851457327604294f));
-    r = fma2(r, e, both(-0.056959524750709534f));
-    r = fma2(r, e, both(0.10603654384613037f));
-    r = fma2(r, e, both(-0.15305592119693756f));
-    r = fma2(r, e, both(0.1967593878507614f));
-    r = fma2(r, e, both(-0.24954134225845337f));
-    r = fma2(r, e, both(0.3332996368408203f));
-    r = fma2(r, e, both(-0.4999990165233612f));
-    r = fma2(r, e, both(1.f));
-    return fma2(r, e, make_float2(fmaxf(x.x, 0.f), fmaxf(x.y, 0.f)));
+// softplus(x) = max(x, 0) + log(1 + e), e = e^-|x|. log(1 + e) is e times a polynomial fitted to
+// log(1 + e) / e on [0, 1] with the smallest relative error (5e-9, 1.4e-7 with the roundings of fp32): the
+// small steps that give a state its memory keep their digits, which log(1 + e) formed as such would lose, and
+// ten multiply-adds cost a third of the library's functions. (Scalar: packed ones would have to fetch
+// their constants into registers.)
+__device__ __forceinline__ float softplus(float x) {
+    const float e = ex2(fabsf(x) * -kLog2e);
+    float r = -0.003244024235755205f;
+    r = fmaf(r, e, 0.019851457327604294f);
+    r = fmaf(r, e, -0.056959524750709534f);
+    r = fmaf(r, e, 0.10603654384613037f);
+    r = fmaf(r, e, -0.15305592119693756f);
+    r = fmaf(r, e, 0.1967593878507614f);
+    r = fmaf(r, e, -0.24954134225845337f);
+    r = fmaf(r, e, 0.3332996368408203f);
+    r = fmaf(r, e, -0.4999990165233612f);
+    r = fmaf(r, e, 1.f);
+    return fmaf(r, e, fmaxf(x, 0.f));
 }
-__device__ __forceinline__ float step_size(float x, int softplus) { return softplus ? softplus2(both(x)).x : x; }
+__device__ __forceinline__ float step_size(float x, int on) { return on ? softplus(x) : x; }
 
 // What a CTA's warps read: the sequence's rows from the tile's first channel (the group's B and C) on.
 struct Source {
@@ -329,7 +330,7 @@ __device__ __forceinline__ void write_rows(const T *from, void *to, const SsmPro
 
 // Step sizes of the chunk from the stage (zero for tokens and channels that do not exist: they keep the state).
 template <typename T, int kCh>
-__device__ __forceinline__ void step_sizes(const T *in, const float (&bias)[kCh], int softplus, int64_t left, int mine,
+__device__ __forceinline__ void step_sizes(const T *in, const float (&bias)[kCh], int plus, int64_t left, int mine,
                                            float2 (&d)[kCh][kPairs]) {
 #pragma unroll
     for (int ip = 0; ip < kPairs; ++ip) {
@@ -338,8 +339,13 @@ __device__ __forceinline__ void step_sizes(const T *in, const float (&bias)[kCh]
 #pragma unroll
         for (int c = 0; c < kCh; ++c) {
             d[c][ip] = add2(r[c], both(bias[c]));
-            if (softplus) d[c][ip] = softplus2(d[c][ip]);
         }
+    }
+    if (plus) {
+#pragma unroll
+        for (int c = 0; c < kCh; ++c)
+#pragma unroll
+            for (int ip = 0; ip < kPairs; ++ip) d[c][ip] = make_float2(softplus(d[c][ip].x), softplus(d[c][ip].y));
     }
     if (left < kTok || mine < kCh) {
 #pragma unroll
@@ -423,6 +429,7 @@ ssm_fwd_kernel(const __grid_constant__ SsmProblem p, const __grid_constant__ Map
     };
     int k = 0;
     uint32_t round = 0;         // parity of the stage's buffer
+    uint32_t parity = w == 0;   // of the hand-over: the warp before is in the same round, or the last one in the one before
     fetch(w, 0);
     for (int64_t ch = w; ch < chunks; ch += W) {
         const int64_t t0 = ch * kTok;
@@ -444,7 +451,6 @@ ssm_fwd_kernel(const __grid_constant__ SsmProblem p, const __grid_constant__ Map
         }
         __syncwarp();
         fetch(ch + W, k ^ 1);
-        const uint32_t parity = (uint32_t)((ch - 1) / W) & 1u;
 #pragma unroll 1
         for (int q = 0; q < Q; ++q) {
             float2 A[4], a[4][kPairs], s[4][kPairs];      // [kCh][kSt]
@@ -528,7 +534,8 @@ ssm_fwd_kernel(const __grid_constant__ SsmProblem p, const __grid_constant__ Map
         }
         __syncwarp();       // the stage and the rows have been read
         k ^= 1;
-        if (k == 0) round ^= 1;
+        round ^= k == 0;
+        parity ^= 1;
     }
     if (kVec && kOut && lane == 0) tc::bulk_wait_all();
 }
@@ -604,6 +611,7 @@ ssm_bwd_kernel(const __grid_constant__ SsmProblem p, const __grid_constant__ Map
     };
     int k = 0;
     uint32_t round = 0;         // parity of the stage's buffer
+    uint32_t parity = w == 0;   // of the hand-over: the warp before is in the same round, or the last one in the one before
     fetch(w, 0);
     for (int64_t step = w; step < chunks; step += W) {
         const int64_t ch = chunks - 1 - step, t0 = ch * kTok;
@@ -634,7 +642,6 @@ ssm_bwd_kernel(const __grid_constant__ SsmProblem p, const __grid_constant__ Map
         }
         __syncwarp();
         fetch(step + W, k ^ 1);
-        const uint32_t parity = (uint32_t)((step - 1) / W) & 1u;
         // Sums across the lanes: a lane leaves its values in its row of turn; a step's are dC and dB of kSt states
         // of 8 tokens (2 tokens side by side), [2][kSt][kTok]. kCh = 2: two steps' values, 64 in all. Lane l
         // adds the columns 2 l and 2 l + 1 and has two tokens of dC or dB of one state.
@@ -792,7 +799,8 @@ ssm_bwd_kernel(const __grid_constant__ SsmProblem p, const __grid_constant__ Map
         }
         __syncwarp();       // the stage and the rows have been read
         k ^= 1;
-        if (k == 0) round ^= 1;
+        round ^= k == 0;
+        parity ^= 1;
     }
     if (kVec && lane == 0) tc::bulk_wait_all();
 #pragma unroll
