@@ -134,15 +134,55 @@ __device__ __forceinline__ void widen_rows(const T *from, float2 *to, int N) {
     }
 }
 
-// Waits for a hand-over. Most arrive while it polls; the clock that bounds the wait takes longer to read than
-// they do, so that it is left to mbar_wait.
-__device__ __forceinline__ bool ring_wait(uint64_t *bar, uint32_t parity) {
+// Hand-overs. Addresses are those of shared memory, so that a step's are immediate offsets of a chunk's.
+struct Link {
+    uint32_t bar, slot;             // step 0 of a warp (32 slots of 16 bytes and one barrier to a step)
+};
+__device__ __forceinline__ float4 load4(uint32_t at) {
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ void store4(uint32_t at, const float (&v)[4]) {
+    asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]) : "memory");
+}
+__device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+// Most hand-overs arrive while it polls; the clock that bounds the wait takes longer to read than they do. A warp that
+// gave up once (dead) does not wait again.
+__device__ __forceinline__ bool wait_on(uint32_t bar, uint32_t parity, bool dead, unsigned int *err) {
+    if (dead) return true;
 #pragma unroll 1
     for (int i = 0; i < 256; ++i)
-        if (tc::mbar_try_wait(bar, parity)) return true;
-    return tc::mbar_wait(bar, parity);
+        if (try_wait(bar, parity)) return false;
+    const uint64_t t0 = tc::global_ns();
+    for (;;) {
+#pragma unroll 1
+        for (int i = 0; i < 32; ++i)
+            if (try_wait(bar, parity)) return false;
+        if (tc::global_ns() - t0 > tc::kWaitLimitNs) break;
+    }
+    atomicOr(err, kDevErrTimeout);
+    return true;
 }
-
+// Lane 0 tells the next warp, once all lanes have written.
+__device__ __forceinline__ void hand_over(uint32_t bar, int lane) {
+    __syncwarp();
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 st;\n\t"
+        "setp.eq.s32 p, %1, 0;\n\t"
+        "@p mbarrier.arrive.release.cta.shared::cta.b64 st, [%0];\n\t}" ::"r"(bar), "r"(lane)
+        : "memory");
+}
 
 // The CTAs of a sequence: tiles of 32 kCh channels of one group.
 struct Tiles {
@@ -179,6 +219,28 @@ struct Place {
         return Source{static_cast<const T *>(r.p) + b * r.b + g * N, r.t, N, N};
     }
 };
+
+// States [kCh][kSt] of step q of the lane, from and to [B, C, N].
+template <int kCh>
+__device__ __forceinline__ void load_states(const float *from, const SsmProblem &p, const Place<kCh> &at, int q,
+                                            float (&h)[4]) {
+    constexpr int kSt = 4 / kCh;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int n = kSt * q + j % kSt;
+        h[j] = from && j / kSt < at.mine && n < p.N ? from[(at.b * p.C + at.channel(j / kSt)) * p.N + n] : 0.f;
+    }
+}
+template <int kCh>
+__device__ __forceinline__ void store_states(float *to, const SsmProblem &p, const Place<kCh> &at, int q,
+                                             const float (&h)[4]) {
+    constexpr int kSt = 4 / kCh;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int n = kSt * q + j % kSt;
+        if (j / kSt < at.mine && n < p.N) to[(at.b * p.C + at.channel(j / kSt)) * p.N + n] = h[j];
+    }
+}
 
 // A lane works on kSt = 4 / kCh states of its channels at a time, Q = N / kSt times. Shared memory of a
 // ring of W warps:
@@ -220,8 +282,8 @@ struct Ring {
         full = bar + W * Q;
         stage = smem + stage_at(W, N, backward);
     }
-    // A and the barriers; the CTA synchronises.
-    __device__ void begin(const SsmProblem &p, const Place<kCh> &at, int W, int N) {
+    // A, the barriers, and the states that the first chunk takes over, as if from the last warp; the CTA synchronises.
+    __device__ void begin(const SsmProblem &p, const Place<kCh> &at, int W, int N, const float *first) {
         constexpr int kSt = 4 / kCh;
         const int Q = steps(N), lane = threadIdx.x % 32;
         for (int q = threadIdx.x / 32; q < Q; q += W) {
@@ -233,12 +295,18 @@ struct Ring {
             }
             A[2 * q * 32 + lane] = make_float4(a[0], a[0], a[1], a[1]);
             A[(2 * q + 1) * 32 + lane] = make_float4(a[2], a[2], a[3], a[3]);
+            load_states<kCh>(first, p, at, q, a);
+            slot[((W - 1) * Q + q) * 32 + lane] = make_float4(a[0], a[1], a[2], a[3]);
         }
         if (threadIdx.x == 0) {
             for (int i = 0; i < W * (Q + 2); ++i) tc::mbar_init(bar + i, 1);
             tc::fence_mbar_init();
         }
         __syncthreads();
+        for (int q = threadIdx.x; q < Q; q += 32 * W) tc::mbar_arrive(bar + (W - 1) * Q + q);
+    }
+    __device__ Link link(int w, int Q) const {
+        return Link{tc::smem_u32(bar + w * Q), tc::smem_u32(slot + w * Q * 32 + threadIdx.x % 32)};
     }
     __device__ void load_a(int q, float2 (&a)[4]) const {
         const int lane = threadIdx.x % 32;
@@ -249,28 +317,6 @@ struct Ring {
         a[3] = make_float2(y.z, y.w);
     }
 };
-
-// States [kCh][kSt] of step q of the lane, from and to [B, C, N].
-template <int kCh>
-__device__ __forceinline__ void load_states(const float *from, const SsmProblem &p, const Place<kCh> &at, int q,
-                                            float (&h)[4]) {
-    constexpr int kSt = 4 / kCh;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const int n = kSt * q + j % kSt;
-        h[j] = from && j / kSt < at.mine && n < p.N ? from[(at.b * p.C + at.channel(j / kSt)) * p.N + n] : 0.f;
-    }
-}
-template <int kCh>
-__device__ __forceinline__ void store_states(float *to, const SsmProblem &p, const Place<kCh> &at, int q,
-                                             const float (&h)[4]) {
-    constexpr int kSt = 4 / kCh;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const int n = kSt * q + j % kSt;
-        if (j / kSt < at.mine && n < p.N) to[(at.b * p.C + at.channel(j / kSt)) * p.N + n] = h[j];
-    }
-}
 
 // The lane's channels of row i of a tensor in the stage.
 template <typename T, int kCh>
@@ -382,7 +428,7 @@ ssm_fwd_kernel(const __grid_constant__ SsmProblem p, const __grid_constant__ Map
     const int w = threadIdx.x / 32, lane = threadIdx.x % 32;
     const Tiles tl = tiles_of(p.C, p.G, kCh);
     const Place<kCh> at(p, tl);
-    ring.begin(p, at, W, N);
+    ring.begin(p, at, W, N, p.h0);
     float bias[kCh], D[kCh];
 #pragma unroll
     for (int c = 0; c < kCh; ++c) {
@@ -419,21 +465,18 @@ ssm_fwd_kernel(const __grid_constant__ SsmProblem p, const __grid_constant__ Map
             stage_rows<T>(at.template rows<T>(p.Cm, N), t0, p.T, to + kIn * kRow + kTok * N);
         }
     };
-    const int prev = w == 0 ? W - 1 : w - 1;
+    const Link from = ring.link(w == 0 ? W - 1 : w - 1, Q), to = ring.link(w, Q);
+    const uint32_t full = tc::smem_u32(ring.full + 2 * w);
     bool dead = false;
-    auto wait = [&](uint64_t *bar, uint32_t parity) {
-        if (!dead && !ring_wait(bar, parity)) {
-            dead = true;
-            atomicOr(err, kDevErrTimeout);
-        }
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+        if (!try_wait(bar, parity)) dead = wait_on(bar, parity, dead, err);
     };
     int k = 0;
-    uint32_t round = 0;         // parity of the stage's buffer
-    uint32_t parity = w == 0;   // of the hand-over: the warp before is in the same round, or the last one in the one before
+    uint32_t round = 0, parity = 0;     // of the stage's buffer, and of the hand-overs
     fetch(w, 0);
     for (int64_t ch = w; ch < chunks; ch += W) {
         const int64_t t0 = ch * kTok;
-        if (kVec) wait(ring.full + 2 * w + k, round);
+        if (kVec) wait(full + 8 * k, round);
         else __syncwarp();
         T *in = stage(k);
         widen_rows<T, kN>(in + kIn * kRow, rows, N);
@@ -465,17 +508,9 @@ ssm_fwd_kernel(const __grid_constant__ SsmProblem p, const __grid_constant__ Map
                     s[j][ip] = mul2(b[j % kSt], x[j / kSt][ip]);
                 }
             }
-            float h[4];
-            if (ch == 0) {
-                load_states<kCh>(p.h0, p, at, q, h);
-            } else {
-                wait(ring.bar + prev * Q + q, parity);
-                const float4 v = ring.slot[(prev * Q + q) * 32 + lane];
-                h[0] = v.x;
-                h[1] = v.y;
-                h[2] = v.z;
-                h[3] = v.w;
-            }
+            wait(from.bar + 8 * q, parity);
+            const float4 v = load4(from.slot + 512 * q);
+            float h[4] = {v.x, v.y, v.z, v.w};
             if (!kOut)
                 marks[(((at.b * chunks + ch) * tl.all + at.tile) * Q + q) * 32 + lane] = make_float4(h[0], h[1], h[2], h[3]);
 #pragma unroll
@@ -485,13 +520,8 @@ ssm_fwd_kernel(const __grid_constant__ SsmProblem p, const __grid_constant__ Map
                     s[j][ip].x = fmaf(a[j][ip].x, h[j], s[j][ip].x);
                     h[j] = s[j][ip].y = fmaf(a[j][ip].y, s[j][ip].x, s[j][ip].y);
                 }
-            if (ch + 1 < chunks) {
-                ring.slot[(w * Q + q) * 32 + lane] = make_float4(h[0], h[1], h[2], h[3]);
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive(ring.bar + w * Q + q);
-            } else if (kOut && p.hT) {
-                store_states<kCh>(p.hT, p, at, q, h);
-            }
+            store4(to.slot + 512 * q, h);
+            hand_over(to.bar + 8 * q, lane);
             if (kOut) {
 #pragma unroll
                 for (int ip = 0; ip < kPairs; ++ip) {
@@ -538,6 +568,13 @@ ssm_fwd_kernel(const __grid_constant__ SsmProblem p, const __grid_constant__ Map
         parity ^= 1;
     }
     if (kVec && kOut && lane == 0) tc::bulk_wait_all();
+    if (kOut && p.hT && w == (int)((chunks - 1) % W)) {     // what the last chunk handed on
+        for (int q = 0; q < Q; ++q) {
+            const float4 v = load4(to.slot + 512 * q);
+            const float h[4] = {v.x, v.y, v.z, v.w};
+            store_states<kCh>(p.hT, p, at, q, h);
+        }
+    }
 }
 
 // Where the backward kernel leaves what is summed later, all float:
@@ -561,7 +598,7 @@ ssm_bwd_kernel(const __grid_constant__ SsmProblem p, const __grid_constant__ Map
     const Tiles tl = tiles_of(p.C, p.G, kCh);
     const Place<kCh> at(p, tl);
     for (int q = 0; q < Q; ++q) ring.sums[(w * Q + q) * 32 + lane] = make_float4(0.f, 0.f, 0.f, 0.f);
-    ring.begin(p, at, W, N);
+    ring.begin(p, at, W, N, p.dhT);
     float bias[kCh], D[kCh], dD[kCh], dbias[kCh];
 #pragma unroll
     for (int c = 0; c < kCh; ++c) {
@@ -601,23 +638,20 @@ ssm_bwd_kernel(const __grid_constant__ SsmProblem p, const __grid_constant__ Map
             stage_rows<T>(at.template rows<T>(p.Cm, N), t0, p.T, to + kIn * kRow + kTok * N);
         }
     };
-    const int prev = w == 0 ? W - 1 : w - 1;
+    const Link from = ring.link(w == 0 ? W - 1 : w - 1, Q), to = ring.link(w, Q);
+    const uint32_t full = tc::smem_u32(ring.full + 2 * w);
     bool dead = false;
-    auto wait = [&](uint64_t *bar, uint32_t parity) {
-        if (!dead && !ring_wait(bar, parity)) {
-            dead = true;
-            atomicOr(err, kDevErrTimeout);
-        }
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+        if (!try_wait(bar, parity)) dead = wait_on(bar, parity, dead, err);
     };
     int k = 0;
-    uint32_t round = 0;         // parity of the stage's buffer
-    uint32_t parity = w == 0;   // of the hand-over: the warp before is in the same round, or the last one in the one before
+    uint32_t round = 0, parity = 0;     // of the stage's buffer, and of the hand-overs
     fetch(w, 0);
     for (int64_t step = w; step < chunks; step += W) {
         const int64_t ch = chunks - 1 - step, t0 = ch * kTok;
         const float4 *mark = marks + ((at.b * chunks + ch) * tl.all + at.tile) * Q * 32 + lane;
         float4 mk = mark[0];        // a step's states come while the one before is worked on
-        if (kVec) wait(ring.full + 2 * w + k, round);
+        if (kVec) wait(full + 8 * k, round);
         else __syncwarp();
         T *in = stage(k);
         widen_rows<T, kN>(in + kIn * kRow, rows, N);
@@ -670,17 +704,9 @@ ssm_bwd_kernel(const __grid_constant__ SsmProblem p, const __grid_constant__ Map
 #pragma unroll
                 for (int n = 0; n < kSt; ++n) *reinterpret_cast<float2 *>(mine + n * kTok + 2 * ip) = dC[n];
             }
-            float G[4];         // what comes from the tokens after
-            if (step == 0) {
-                load_states<kCh>(p.dhT, p, at, q, G);
-            } else {
-                wait(ring.bar + prev * Q + q, parity);
-                const float4 v = ring.slot[(prev * Q + q) * 32 + lane];
-                G[0] = v.x;
-                G[1] = v.y;
-                G[2] = v.z;
-                G[3] = v.w;
-            }
+            wait(from.bar + 8 * q, parity);
+            const float4 v = load4(from.slot + 512 * q);
+            float G[4] = {v.x, v.y, v.z, v.w};      // what comes from the tokens after
             // the walk, which the next warp waits for; a becomes the gradient of the state, the state before a
             // token becomes w (that before the first token: h)
 #pragma unroll
@@ -700,13 +726,8 @@ ssm_bwd_kernel(const __grid_constant__ SsmProblem p, const __grid_constant__ Map
                     a[j][ip] = g;
                 }
             }
-            if (ch > 0) {
-                ring.slot[(w * Q + q) * 32 + lane] = make_float4(G[0], G[1], G[2], G[3]);
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive(ring.bar + w * Q + q);
-            } else if (p.dh0) {
-                store_states<kCh>(p.dh0, p, at, q, G);
-            }
+            store4(to.slot + 512 * q, G);
+            hand_over(to.bar + 8 * q, lane);
             float2 dA[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) dA[j] = both(0.f);
@@ -803,6 +824,13 @@ ssm_bwd_kernel(const __grid_constant__ SsmProblem p, const __grid_constant__ Map
         parity ^= 1;
     }
     if (kVec && lane == 0) tc::bulk_wait_all();
+    if (p.dh0 && w == (int)((chunks - 1) % W)) {            // what the first token handed on
+        for (int q = 0; q < Q; ++q) {
+            const float4 v = load4(to.slot + 512 * q);
+            const float G[4] = {v.x, v.y, v.z, v.w};
+            store_states<kCh>(p.dh0, p, at, q, G);
+        }
+    }
 #pragma unroll
     for (int c = 0; c < kCh; ++c) chan[w][lane * kCh + c] = make_float2(dD[c], dbias[c]);
     __syncthreads();
