@@ -249,6 +249,7 @@ __device__ __forceinline__ void store_states(float *to, const SsmProblem &p, con
 //   rows[W][2][kPairs][NP] float2: B and C of a warp's chunk;  bar[W][Q]
 //   stage[W][2]: a chunk as it lies in memory, on its way while the one before it is worked on:
 //     kIn tensors [kTok][32 kCh], then B and C [kTok][N];  full[W][2]: it is there
+//   dx[W][kPairs][kCh][32] float4 (forward): d and d u of a warp's chunk
 constexpr int kTurn = 66;           // (lanes that write pairs side by side meet no bank twice)
 template <typename T, int kCh>
 struct Ring {
@@ -269,7 +270,7 @@ struct Ring {
                round((size_t)W * 2 * kPairs * padded(N) * 8) + round(W * (Q + 2) * 8);
     }
     static __host__ __device__ size_t bytes(int W, int in, int N, bool backward) {
-        return stage_at(W, N, backward) + 2 * W * stage_bytes(in, N);
+        return stage_at(W, N, backward) + 2 * W * stage_bytes(in, N) + (backward ? 0 : W * kPairs * kCh * 32 * 16);
     }
     __device__ Ring(unsigned char *smem, int W, int N, bool backward) {
         const int Q = steps(N);
@@ -438,6 +439,8 @@ ssm_fwd_kernel(const __grid_constant__ SsmProblem p, const __grid_constant__ Map
     float2 *rows = ring.rows + w * 2 * kPairs * NP;
     const size_t stage_bytes = R::stage_bytes(kIn, N);
     auto stage = [&](int k) { return reinterpret_cast<T *>(ring.stage + (2 * w + k) * stage_bytes); };
+    // d and d u of a chunk: in registers they would cost a tenth more instructions (moves; 128 registers are few)
+    float4 *dx = reinterpret_cast<float4 *>(ring.stage + 2 * W * stage_bytes) + w * kPairs * kCh * 32 + lane;
     const int64_t chunks = (p.T + kTok - 1) / kTok;
     // the chunk into buffer k of the stage, by one lane where TMA does it
     auto fetch = [&](int64_t ch, int k) {
@@ -480,7 +483,7 @@ ssm_fwd_kernel(const __grid_constant__ SsmProblem p, const __grid_constant__ Map
         else __syncwarp();
         T *in = stage(k);
         widen_rows<T, kN>(in + kIn * kRow, rows, N);
-        float2 d[kCh][kPairs], x[kCh][kPairs], y[kCh][kPairs];
+        float2 d[kCh][kPairs], y[kCh][kPairs];
         step_sizes<T, kCh>(in + kRow, bias, p.softplus, p.T - t0, at.mine, d);
 #pragma unroll
         for (int ip = 0; ip < kPairs; ++ip) {
@@ -488,7 +491,8 @@ ssm_fwd_kernel(const __grid_constant__ SsmProblem p, const __grid_constant__ Map
             lane_pair<T, kCh>(in, ip, u);
 #pragma unroll
             for (int c = 0; c < kCh; ++c) {
-                x[c][ip] = c < at.mine ? mul2(d[c][ip], u[c]) : both(0.f);
+                const float2 x = c < at.mine ? mul2(d[c][ip], u[c]) : both(0.f);
+                dx[(ip * kCh + c) * 32] = make_float4(d[c][ip].x, d[c][ip].y, x.x, x.y);
                 y[c][ip] = both(0.f);
             }
         }
@@ -502,10 +506,13 @@ ssm_fwd_kernel(const __grid_constant__ SsmProblem p, const __grid_constant__ Map
             for (int ip = 0; ip < kPairs; ++ip) {
                 float2 b[kSt];
                 load_bc<kSt>(rows + ip * NP, q, b);
+                float4 v[kCh];
+#pragma unroll
+                for (int c = 0; c < kCh; ++c) v[c] = dx[(ip * kCh + c) * 32];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    a[j][ip] = decay2(A[j], d[j / kSt][ip]);
-                    s[j][ip] = mul2(b[j % kSt], x[j / kSt][ip]);
+                    a[j][ip] = decay2(A[j], make_float2(v[j / kSt].x, v[j / kSt].y));
+                    s[j][ip] = mul2(b[j % kSt], make_float2(v[j / kSt].z, v[j / kSt].w));
                 }
             }
             wait(from.bar + 8 * q, parity);
