@@ -115,7 +115,7 @@ struct Maps {
 template <typename T, int kN>
 __device__ __forceinline__ void widen_rows(const T *from, float2 *to, int N) {
     const int lane = threadIdx.x % 32, NP = (N + 3) / 4 * 4;
-    if (kN) {        // four states at a time
+    if constexpr (kN > 0) {     // four states at a time
 #pragma unroll
         for (int k = lane; k < kTok * kN / 4; k += 32) {
             const int row = k / (kN / 4), q = k % (kN / 4);     // row: a pair of tokens of B, or of C
@@ -126,11 +126,11 @@ __device__ __forceinline__ void widen_rows(const T *from, float2 *to, int N) {
             t[0] = make_float4(x[0], y[0], x[1], y[1]);
             t[1] = make_float4(x[2], y[2], x[3], y[3]);
         }
-        return;
-    }
-    for (int k = lane; k < kTok * NP; k += 32) {
-        const int row = k / NP, n = k - row * NP;
-        to[k] = n < N ? make_float2(get(from + 2 * row * N + n), get(from + (2 * row + 1) * N + n)) : both(0.f);
+    } else {
+        for (int k = lane; k < kTok * NP; k += 32) {
+            const int row = k / NP, n = k - row * NP;
+            to[k] = n < N ? make_float2(get(from + 2 * row * N + n), get(from + (2 * row + 1) * N + n)) : both(0.f);
+        }
     }
 }
 
@@ -194,14 +194,31 @@ __host__ __device__ inline Tiles tiles_of(int64_t C, int64_t G, int ch) {
     return Tiles{(int)n, n * G};
 }
 
-// Where a CTA is: a sequence, a group of channels and 32 kCh of them.
+// Segments of a sequence: with few channels it is cut, so that all SMs have a part. The segments' states from zero come
+// first, then those that they start from (ssm_join_kernel), then the walk over all segments at once.
+struct Split {
+    int n;                          // segments of a sequence
+    int64_t chunks;                 // of each but the last
+    float *h, *g;                   // [B][n][C][N]: what a segment ends with if it starts from zero, then what it
+                                    // starts from (g: backwards)
+    float *sum;                     // [B][n][C]: the segment's step sizes
+};
+
+// Where a CTA is: a sequence (a segment of it), a group of channels and 32 kCh of them.
 template <int kCh>
 struct Place {
-    int64_t b, tile, g, c0;         // c0: the first channel
+    int64_t b, row, tile, g, c0;    // row: b n + the segment; c0: the first channel
+    int seg;
+    int64_t ch0, ch1;               // chunks
     int width, mine;                // channels of the tile, of the lane
-    __device__ Place(const SsmProblem &p, const Tiles &tl) {
-        b = blockIdx.x / tl.all;
+    __device__ Place(const SsmProblem &p, const Tiles &tl, const Split &sp, int segs) {
         tile = blockIdx.x % tl.all;
+        const int64_t i = blockIdx.x / tl.all;
+        b = i / segs;
+        seg = (int)(i - b * segs);
+        row = b * sp.n + seg;
+        ch0 = seg * sp.chunks;
+        ch1 = min(ch0 + sp.chunks, (p.T + kTok - 1) / kTok);
         g = tile / tl.per_group;
         const int64_t cg = p.C / p.G, first = (tile - g * tl.per_group) * 32 * kCh;
         width = (int)min((int64_t)32 * kCh, cg - first);
@@ -220,25 +237,25 @@ struct Place {
     }
 };
 
-// States [kCh][kSt] of step q of the lane, from and to [B, C, N].
+// States [kCh][kSt] of step q of the lane, from and to row `row` of [rows, C, N].
 template <int kCh>
-__device__ __forceinline__ void load_states(const float *from, const SsmProblem &p, const Place<kCh> &at, int q,
-                                            float (&h)[4]) {
+__device__ __forceinline__ void load_states(const float *from, int64_t row, const SsmProblem &p, const Place<kCh> &at,
+                                            int q, float (&h)[4]) {
     constexpr int kSt = 4 / kCh;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         const int n = kSt * q + j % kSt;
-        h[j] = from && j / kSt < at.mine && n < p.N ? from[(at.b * p.C + at.channel(j / kSt)) * p.N + n] : 0.f;
+        h[j] = from && j / kSt < at.mine && n < p.N ? from[(row * p.C + at.channel(j / kSt)) * p.N + n] : 0.f;
     }
 }
 template <int kCh>
-__device__ __forceinline__ void store_states(float *to, const SsmProblem &p, const Place<kCh> &at, int q,
-                                             const float (&h)[4]) {
+__device__ __forceinline__ void store_states(float *to, int64_t row, const SsmProblem &p, const Place<kCh> &at,
+                                             int q, const float (&h)[4]) {
     constexpr int kSt = 4 / kCh;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         const int n = kSt * q + j % kSt;
-        if (j / kSt < at.mine && n < p.N) to[(at.b * p.C + at.channel(j / kSt)) * p.N + n] = h[j];
+        if (j / kSt < at.mine && n < p.N) to[(row * p.C + at.channel(j / kSt)) * p.N + n] = h[j];
     }
 }
 
@@ -284,7 +301,7 @@ struct Ring {
         stage = smem + stage_at(W, N, backward);
     }
     // A, the barriers, and the states that the first chunk takes over, as if from the last warp; the CTA synchronises.
-    __device__ void begin(const SsmProblem &p, const Place<kCh> &at, int W, int N, const float *first) {
+    __device__ void begin(const SsmProblem &p, const Place<kCh> &at, int W, int N, const float *first, int64_t row) {
         constexpr int kSt = 4 / kCh;
         const int Q = steps(N), lane = threadIdx.x % 32;
         for (int q = threadIdx.x / 32; q < Q; q += W) {
@@ -296,7 +313,7 @@ struct Ring {
             }
             A[2 * q * 32 + lane] = make_float4(a[0], a[0], a[1], a[1]);
             A[(2 * q + 1) * 32 + lane] = make_float4(a[2], a[2], a[3], a[3]);
-            load_states<kCh>(first, p, at, q, a);
+            load_states<kCh>(first, row, p, at, q, a);
             slot[((W - 1) * Q + q) * 32 + lane] = make_float4(a[0], a[1], a[2], a[3]);
         }
         if (threadIdx.x == 0) {
@@ -416,20 +433,26 @@ __device__ __forceinline__ void load_bc(const float2 *row, int q, float2 (&v)[kS
     }
 }
 
-// kOut: outputs and the last state; else the states before each chunk go to marks
-// [B][chunks][tiles][Q][32] float4. kN: N, if known at compile time.
-template <typename T, int kCh, int kN, bool kOut, bool kVec>
+// What a forward walk leaves: outputs and the last state; the states before each chunk (marks
+// [B][chunks][tiles][Q][32] float4), which the backward walk needs; a segment's last state and step sizes (Split).
+enum { kOutputs = 0, kMarks = 1, kEnds = 2 };
+
+// kN: N, if known at compile time. segs: segments of a sequence that this call walks over.
+template <typename T, int kCh, int kN, int kMode, bool kVec>
 __global__ void __launch_bounds__(512, 1)
-ssm_fwd_kernel(const __grid_constant__ SsmProblem p, const __grid_constant__ Maps maps, float4 *marks, unsigned int *err) {
+ssm_fwd_kernel(const __grid_constant__ SsmProblem p, const __grid_constant__ Maps maps, const Split sp, int segs,
+               float4 *marks, unsigned int *err) {
     extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ float sums[kMode == kEnds ? 16 : 1][32 * kCh];
+    constexpr bool kOut = kMode == kOutputs;
     constexpr int kSt = 4 / kCh, kIn = kOut ? 3 : 2, kRow = kTok * 32 * kCh;
     using R = Ring<T, kCh>;
     const int W = blockDim.x / 32, N = kN ? kN : p.N, Q = R::steps(N), NP = R::padded(N);
     R ring(smem, W, N, false);
     const int w = threadIdx.x / 32, lane = threadIdx.x % 32;
     const Tiles tl = tiles_of(p.C, p.G, kCh);
-    const Place<kCh> at(p, tl);
-    ring.begin(p, at, W, N, p.h0);
+    const Place<kCh> at(p, tl, sp, segs);
+    ring.begin(p, at, W, N, kMode == kEnds ? nullptr : sp.n > 1 ? sp.h : p.h0, sp.n > 1 ? at.row : at.b);
     float bias[kCh], D[kCh];
 #pragma unroll
     for (int c = 0; c < kCh; ++c) {
@@ -444,7 +467,7 @@ ssm_fwd_kernel(const __grid_constant__ SsmProblem p, const __grid_constant__ Map
     const int64_t chunks = (p.T + kTok - 1) / kTok;
     // the chunk into buffer k of the stage, by one lane where TMA does it
     auto fetch = [&](int64_t ch, int k) {
-        if (ch >= chunks) return;
+        if (ch >= at.ch1) return;
         T *to = stage(k);
         const int64_t t0 = ch * kTok;
         if (kVec) {
@@ -476,8 +499,11 @@ ssm_fwd_kernel(const __grid_constant__ SsmProblem p, const __grid_constant__ Map
     };
     int k = 0;
     uint32_t round = 0, parity = 0;     // of the stage's buffer, and of the hand-overs
-    fetch(w, 0);
-    for (int64_t ch = w; ch < chunks; ch += W) {
+    float2 total[kCh];
+#pragma unroll
+    for (int c = 0; c < kCh; ++c) total[c] = both(0.f);
+    fetch(at.ch0 + w, 0);
+    for (int64_t ch = at.ch0 + w; ch < at.ch1; ch += W) {
         const int64_t t0 = ch * kTok;
         if (kVec) wait(full + 8 * k, round);
         else __syncwarp();
@@ -494,6 +520,7 @@ ssm_fwd_kernel(const __grid_constant__ SsmProblem p, const __grid_constant__ Map
                 const float2 x = c < at.mine ? mul2(d[c][ip], u[c]) : both(0.f);
                 dx[(ip * kCh + c) * 32] = make_float4(d[c][ip].x, d[c][ip].y, x.x, x.y);
                 y[c][ip] = both(0.f);
+                if (kMode == kEnds) total[c] = add2(total[c], d[c][ip]);
             }
         }
         __syncwarp();
@@ -518,7 +545,7 @@ ssm_fwd_kernel(const __grid_constant__ SsmProblem p, const __grid_constant__ Map
             wait(from.bar + 8 * q, parity);
             const float4 v = load4(from.slot + 512 * q);
             float h[4] = {v.x, v.y, v.z, v.w};
-            if (!kOut)
+            if (kMode == kMarks)
                 marks[(((at.b * chunks + ch) * tl.all + at.tile) * Q + q) * 32 + lane] = make_float4(h[0], h[1], h[2], h[3]);
 #pragma unroll
             for (int ip = 0; ip < kPairs; ++ip)
@@ -575,26 +602,38 @@ ssm_fwd_kernel(const __grid_constant__ SsmProblem p, const __grid_constant__ Map
         parity ^= 1;
     }
     if (kVec && kOut && lane == 0) tc::bulk_wait_all();
-    if (kOut && p.hT && w == (int)((chunks - 1) % W)) {     // what the last chunk handed on
+    float *last = kMode == kEnds ? sp.h : kOut && at.seg == sp.n - 1 ? p.hT : nullptr;
+    if (last && w == (int)((at.ch1 - at.ch0 - 1) % W)) {    // what the last chunk handed on
         for (int q = 0; q < Q; ++q) {
             const float4 v = load4(to.slot + 512 * q);
             const float h[4] = {v.x, v.y, v.z, v.w};
-            store_states<kCh>(p.hT, p, at, q, h);
+            store_states<kCh>(last, kMode == kEnds ? at.row : at.b, p, at, q, h);
+        }
+    }
+    if (kMode == kEnds) {
+#pragma unroll
+        for (int c = 0; c < kCh; ++c) sums[w][lane * kCh + c] = total[c].x + total[c].y;
+        __syncthreads();
+        for (int i = threadIdx.x; i < at.width; i += 32 * W) {
+            float t = 0.f;
+            for (int k2 = 0; k2 < W; ++k2) t += sums[k2][i];
+            sp.sum[at.row * p.C + at.c0 + i] = t;
         }
     }
 }
 
 // Where the backward kernel leaves what is summed later, all float:
 //   rows [tiles][B T][2][NP]: dB and dC of a tile's channels
-//   chan [B][C][N + 2]: dA, then dD and ddt_bias
+//   chan [B][n][C][N + 2]: dA, then dD and ddt_bias, of a segment
 struct Parts {
     float *rows, *chan;
 };
 
-template <typename T, int kCh, int kN, bool kVec>
+// kEnd: no gradients but that of the state before the segment if nothing comes from behind it (Split).
+template <typename T, int kCh, int kN, bool kEnd, bool kVec>
 __global__ void __launch_bounds__(kCh == 2 ? 256 : 384, 1)
-ssm_bwd_kernel(const __grid_constant__ SsmProblem p, const __grid_constant__ Maps maps, const float4 *marks,
-               const Parts parts, unsigned int *err) {
+ssm_bwd_kernel(const __grid_constant__ SsmProblem p, const __grid_constant__ Maps maps, const Split sp,
+               const float4 *marks, const Parts parts, unsigned int *err) {
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ float2 chan[kCh == 2 ? 8 : 12][32 * kCh];
     constexpr int kSt = 4 / kCh, kIn = 4, kRow = kTok * 32 * kCh;
@@ -603,9 +642,10 @@ ssm_bwd_kernel(const __grid_constant__ SsmProblem p, const __grid_constant__ Map
     R ring(smem, W, N, true);
     const int w = threadIdx.x / 32, lane = threadIdx.x % 32;
     const Tiles tl = tiles_of(p.C, p.G, kCh);
-    const Place<kCh> at(p, tl);
-    for (int q = 0; q < Q; ++q) ring.sums[(w * Q + q) * 32 + lane] = make_float4(0.f, 0.f, 0.f, 0.f);
-    ring.begin(p, at, W, N, p.dhT);
+    const Place<kCh> at(p, tl, sp, sp.n);
+    if (!kEnd)
+        for (int q = 0; q < Q; ++q) ring.sums[(w * Q + q) * 32 + lane] = make_float4(0.f, 0.f, 0.f, 0.f);
+    ring.begin(p, at, W, N, kEnd ? nullptr : sp.n > 1 ? sp.g : p.dhT, sp.n > 1 ? at.row : at.b);
     float bias[kCh], D[kCh], dD[kCh], dbias[kCh];
 #pragma unroll
     for (int c = 0; c < kCh; ++c) {
@@ -617,12 +657,12 @@ ssm_bwd_kernel(const __grid_constant__ SsmProblem p, const __grid_constant__ Map
     float *turn = ring.turn + w * 32 * kTurn;
     const size_t stage_bytes = R::stage_bytes(kIn, N);
     auto stage = [&](int k) { return reinterpret_cast<T *>(ring.stage + (2 * w + k) * stage_bytes); };
-    const int64_t chunks = (p.T + kTok - 1) / kTok;
+    const int64_t chunks = (p.T + kTok - 1) / kTok, steps = at.ch1 - at.ch0;
     // the chunk into buffer k of the stage, by one lane where TMA does it
     auto fetch = [&](int64_t step, int k) {
-        if (step >= chunks) return;
+        if (step >= steps) return;
         T *to = stage(k);
-        const int64_t t0 = (chunks - 1 - step) * kTok;
+        const int64_t t0 = (at.ch1 - 1 - step) * kTok;
         if (kVec) {
             if (lane == 0) {
                 uint64_t *bar = ring.full + 2 * w + k;
@@ -654,10 +694,11 @@ ssm_bwd_kernel(const __grid_constant__ SsmProblem p, const __grid_constant__ Map
     int k = 0;
     uint32_t round = 0, parity = 0;     // of the stage's buffer, and of the hand-overs
     fetch(w, 0);
-    for (int64_t step = w; step < chunks; step += W) {
-        const int64_t ch = chunks - 1 - step, t0 = ch * kTok;
+    for (int64_t step = w; step < steps; step += W) {
+        const int64_t ch = at.ch1 - 1 - step, t0 = ch * kTok;
         const float4 *mark = marks + ((at.b * chunks + ch) * tl.all + at.tile) * Q * 32 + lane;
-        float4 mk = mark[0];        // a step's states come while the one before is worked on
+        float4 mk;                  // a step's states come while the one before is worked on
+        if (!kEnd) mk = mark[0];
         if (kVec) wait(full + 8 * k, round);
         else __syncwarp();
         T *in = stage(k);
@@ -691,6 +732,29 @@ ssm_bwd_kernel(const __grid_constant__ SsmProblem p, const __grid_constant__ Map
             float2 A[4], a[4][kPairs], s[4][kPairs];
             float *mine = turn + lane * kTurn + (kCh == 2 ? q % 2 * 32 : 0);
             ring.load_a(q, A);
+            if (kEnd) {
+#pragma unroll
+                for (int ip = 0; ip < kPairs; ++ip)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) a[j][ip] = decay2(A[j], d[j / kSt][ip]);
+                wait(from.bar + 8 * q, parity);
+                const float4 v = load4(from.slot + 512 * q);
+                float G[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int ip = kPairs - 1; ip >= 0; --ip) {
+                    float2 c[kSt];
+                    load_bc<kSt>(rows + (kPairs + ip) * NP, q, c);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float2 g = mul2(c[j % kSt], dy[j / kSt][ip]);
+                        G[j] = a[j][ip].y * (g.y + G[j]);
+                        G[j] = a[j][ip].x * (g.x + G[j]);
+                    }
+                }
+                store4(to.slot + 512 * q, G);
+                hand_over(to.bar + 8 * q, lane);
+                continue;
+            }
             float h[4] = {mk.x, mk.y, mk.z, mk.w};
             if (q + 1 < Q) mk = mark[(q + 1) * 32];
 #pragma unroll
@@ -774,6 +838,13 @@ ssm_bwd_kernel(const __grid_constant__ SsmProblem p, const __grid_constant__ Map
                 }
             }
         }
+        if (kEnd) {
+            __syncwarp();       // the stage and the rows have been read
+            k ^= 1;
+            round ^= k == 0;
+            parity ^= 1;
+            continue;
+        }
         float2 sD[kCh], sbias[kCh];
 #pragma unroll
         for (int c = 0; c < kCh; ++c) sD[c] = sbias[c] = both(0.f);
@@ -831,13 +902,15 @@ ssm_bwd_kernel(const __grid_constant__ SsmProblem p, const __grid_constant__ Map
         parity ^= 1;
     }
     if (kVec && lane == 0) tc::bulk_wait_all();
-    if (p.dh0 && w == (int)((chunks - 1) % W)) {            // what the first token handed on
+    float *first = kEnd ? sp.g : at.seg == 0 ? p.dh0 : nullptr;
+    if (first && w == (int)((steps - 1) % W)) {             // what the first token handed on
         for (int q = 0; q < Q; ++q) {
             const float4 v = load4(to.slot + 512 * q);
             const float G[4] = {v.x, v.y, v.z, v.w};
-            store_states<kCh>(p.dh0, p, at, q, G);
+            store_states<kCh>(first, kEnd ? at.row : at.b, p, at, q, G);
         }
     }
+    if (kEnd) return;
 #pragma unroll
     for (int c = 0; c < kCh; ++c) chan[w][lane * kCh + c] = make_float2(dD[c], dbias[c]);
     __syncthreads();
@@ -849,7 +922,7 @@ ssm_bwd_kernel(const __grid_constant__ SsmProblem p, const __grid_constant__ Map
             if (n < N) s += reinterpret_cast<const float *>(ring.sums + (i * Q + n / kSt) * 32 + l)[j];
             else s += n == N ? chan[i][ci].x : chan[i][ci].y;
         }
-        parts.chan[(at.b * p.C + at.c0 + ci) * (N + 2) + n] = s;
+        parts.chan[(at.row * p.C + at.c0 + ci) * (N + 2) + n] = s;
     }
 }
 
@@ -866,13 +939,30 @@ ssm_rows_kernel(const __grid_constant__ SsmProblem p, const Parts parts, const T
         s += parts.rows[(((g * tl.per_group + i) * rows + row) * 2 + k) * NP + n];
     put(static_cast<T *>(k ? p.dCm : p.dBm) + (row * p.G + g) * p.N + n, s);
 }
-// dA, dD and ddt_bias from the batch entries' parts.
+// What the segments start from, from what they end with if they start from zero: in their order forward, or back.
 __global__ void __launch_bounds__(256)
-ssm_chan_kernel(const __grid_constant__ SsmProblem p, const Parts parts) {
+ssm_join_kernel(const __grid_constant__ SsmProblem p, const Split sp, int back) {
+    const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x, cn = p.C * p.N, b = id / cn, i = id - b * cn, c = i / p.N;
+    if (b >= p.B) return;
+    const float A = scale_a(p.A[i]), *from = back ? p.dhT : p.h0;
+    float v = from ? from[id] : 0.f, *x = (back ? sp.g : sp.h) + b * sp.n * cn + i;
+    const float *sum = sp.sum + b * sp.n * p.C + c;
+#pragma unroll 4
+    for (int k = 0; k < sp.n; ++k) {
+        const int seg = back ? sp.n - 1 - k : k;
+        const float end = x[seg * cn], a = exp2f(A * sum[seg * p.C]);
+        x[seg * cn] = v;
+        v = fmaf(a, v, end);
+    }
+}
+// dA, dD and ddt_bias from the segments' parts.
+__global__ void __launch_bounds__(256)
+ssm_chan_kernel(const __grid_constant__ SsmProblem p, const Parts parts, int64_t rows) {
     const int64_t w = p.N + 2, id = (int64_t)blockIdx.x * 256 + threadIdx.x, c = id / w, n = id % w;
     if (c >= p.C) return;
     float s = 0.f;
-    for (int64_t b = 0; b < p.B; ++b) s += parts.chan[(b * p.C + c) * w + n];
+#pragma unroll 4
+    for (int64_t b = 0; b < rows; ++b) s += parts.chan[(b * p.C + c) * w + n];
     if (n < p.N) p.dA[c * p.N + n] = s;
     else if (n == p.N) { if (p.dD) p.dD[c] = s; }
     else if (p.dbias) p.dbias[c] = s;
@@ -1011,98 +1101,167 @@ int bwd_channels(const SsmProblem &p) {
     if (e) return atoi(e);
     return p.N <= 64 ? 2 : 1; }
 
+// Segments of a sequence for CTAs of 32 ch channels. Cutting it costs two thirds of a walk more (and the join), so it is
+// done where the tiles leave almost half of the SMs idle; two CTAs to an SM then, of at least 8 chunks.
+// Measured: SPLIT_NOTE
+Split split_of(const SsmProblem &p, int ch, int splits, int num_sms) {
+    const int64_t chunks = (p.T + kTok - 1) / kTok, ctas = p.B * tiles_of(p.C, p.G, ch).all;
+    int64_t n = 1;
+    if (splits > 0) n = std::min({(int64_t)splits, chunks, std::max<int64_t>(1, (int64_t(1) << 30) / ctas)});
+    else if (9 * ctas <= 5 * num_sms) n = std::min<int64_t>(2 * num_sms / ctas, chunks / 8);
+    Split sp{};
+    sp.chunks = (chunks + std::max<int64_t>(n, 1) - 1) / std::max<int64_t>(n, 1);
+    sp.n = (int)((chunks + sp.chunks - 1) / sp.chunks);
+    return sp;
+}
+size_t round256(size_t n) { return (n + 255) & ~size_t(255); }
+// The segments' states of one direction, and their step sizes.
+size_t split_state_bytes(const SsmProblem &p, const Split &sp) {
+    return sp.n > 1 ? round256((size_t)p.B * sp.n * p.C * p.N * 4) : 0;
+}
+size_t split_sum_bytes(const SsmProblem &p, const Split &sp) {
+    return sp.n > 1 ? round256((size_t)p.B * sp.n * p.C * 4) : 0;
+}
+
 struct BwdWorkspace {
     size_t marks, rows, chan, all;
 };
-BwdWorkspace bwd_workspace(const SsmProblem &p) {
-    auto round = [](size_t n) { return (n + 255) & ~size_t(255); };
+BwdWorkspace bwd_workspace(const SsmProblem &p, const Split &sp) {
+    auto round = round256;
     const int ch = bwd_channels(p);
     const Tiles tl = tiles_of(p.C, p.G, ch);
     const size_t chunks = (size_t)((p.T + kTok - 1) / kTok), Q = (size_t)(p.N + 4 / ch - 1) / (4 / ch);
     BwdWorkspace w;
     w.marks = round((size_t)p.B * chunks * tl.all * Q * 32 * 16);
     w.rows = round((size_t)tl.all * p.B * p.T * 2 * ((p.N + 3) / 4 * 4) * 4);
-    w.chan = round((size_t)p.B * p.C * (p.N + 2) * 4);
-    w.all = w.marks + w.rows + w.chan;
+    w.chan = round((size_t)p.B * sp.n * p.C * (p.N + 2) * 4);
+    w.all = w.marks + w.rows + w.chan + 2 * split_state_bytes(p, sp) + split_sum_bytes(p, sp);
     return w;
 }
 
-template <typename T, int kCh, int kN, bool kOut, bool kVec>
-cudaError_t run_fwd(const SsmProblem &p, const Maps &maps, int warps, float4 *marks, unsigned int *err, cudaStream_t s) {
-    constexpr int in = kOut ? 3 : 2;
-    const int W = ring_warps<T, kCh>(p, in, false, warps);
+template <typename T, int kCh, int kN, int kMode, bool kVec>
+cudaError_t run_fwd(const SsmProblem &p, const Maps &maps, const Split &sp, int segs, int warps, float4 *marks,
+                    unsigned int *err, cudaStream_t s) {
+    constexpr int in = kMode == kOutputs ? 3 : 2;
+    const int W = (int)std::min<int64_t>(ring_warps<T, kCh>(p, in, false, warps), sp.chunks);
     const size_t smem = Ring<T, kCh>::bytes(W, in, p.N, false);
-    const auto kernel = ssm_fwd_kernel<T, kCh, kN, kOut, kVec>;
+    const auto kernel = ssm_fwd_kernel<T, kCh, kN, kMode, kVec>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    kernel<<<(unsigned)(p.B * tiles_of(p.C, p.G, kCh).all), 32 * W, smem, s>>>(p, maps, marks, err);
+    kernel<<<(unsigned)(p.B * segs * tiles_of(p.C, p.G, kCh).all), 32 * W, smem, s>>>(p, maps, sp, segs, marks, err);
     return cudaGetLastError();
 }
-template <typename T, int kCh, bool kOut>
-cudaError_t fwd(const SsmProblem &p, const Maps *maps, int num_sms, float4 *marks, unsigned int *err, cudaStream_t s) {
+template <typename T, int kCh, int kMode>
+cudaError_t fwd(const SsmProblem &p, const Maps *maps, const Split &sp, int segs, int num_sms, float4 *marks,
+                unsigned int *err, cudaStream_t s) {
     // 16 warps to an SM: of one ring where there are no more rings than SMs
-    const int warps = p.B * tiles_of(p.C, p.G, kCh).all <= num_sms ? 16 : 8;
+    const int warps = p.B * segs * tiles_of(p.C, p.G, kCh).all <= num_sms ? 16 : 8;
     cudaError_t e;
-    if (!maps) e = run_fwd<T, kCh, 0, kOut, false>(p, Maps{}, warps, marks, err, s);
-    else if (p.N == 16) e = run_fwd<T, kCh, 16, kOut, true>(p, *maps, warps, marks, err, s);
-    else e = run_fwd<T, kCh, 0, kOut, true>(p, *maps, warps, marks, err, s);
+    if (!maps) e = run_fwd<T, kCh, 0, kMode, false>(p, Maps{}, sp, segs, warps, marks, err, s);
+    else if (p.N == 16) e = run_fwd<T, kCh, 16, kMode, true>(p, *maps, sp, segs, warps, marks, err, s);
+    else e = run_fwd<T, kCh, 0, kMode, true>(p, *maps, sp, segs, warps, marks, err, s);
+    if (e == cudaSuccess) count_launches(1);
+    return e;
+}
+cudaError_t join(const SsmProblem &p, const Split &sp, bool back, cudaStream_t s) {
+    ssm_join_kernel<<<(unsigned)((p.B * p.C * p.N + 255) / 256), 256, 0, s>>>(p, sp, back);
+    const cudaError_t e = cudaGetLastError();
     if (e == cudaSuccess) count_launches(1);
     return e;
 }
 
-template <typename T, int kCh, int kN, bool kVec>
-cudaError_t run_bwd(const SsmProblem &p, const Maps &maps, const float4 *marks, const Parts &parts, unsigned int *err,
-                    cudaStream_t s) {
-    const int W = ring_warps<T, kCh>(p, 4, true, kCh == 2 ? 8 : 12);
+template <typename T, int kCh, int kN, bool kEnd, bool kVec>
+cudaError_t run_bwd(const SsmProblem &p, const Maps &maps, const Split &sp, const float4 *marks, const Parts &parts,
+                    unsigned int *err, cudaStream_t s) {
+    const int W = (int)std::min<int64_t>(ring_warps<T, kCh>(p, 4, true, kCh == 2 ? 8 : 12), sp.chunks);
     const size_t smem = Ring<T, kCh>::bytes(W, 4, p.N, true);
-    const auto kernel = ssm_bwd_kernel<T, kCh, kN, kVec>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const auto kernel = ssm_bwd_kernel<T, kCh, kN, kEnd, kVec>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    const Tiles tl = tiles_of(p.C, p.G, kCh);
-    kernel<<<(unsigned)(p.B * tl.all), 32 * W, smem, s>>>(p, maps, marks, parts, err);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    const int64_t rows = p.B * p.T * p.G * 2 * ((p.N + 3) / 4 * 4), chan = p.C * (p.N + 2);
-    ssm_rows_kernel<T><<<(unsigned)((rows + 255) / 256), 256, 0, s>>>(p, parts, tl);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    ssm_chan_kernel<<<(unsigned)((chan + 255) / 256), 256, 0, s>>>(p, parts);
+    kernel<<<(unsigned)(p.B * sp.n * tiles_of(p.C, p.G, kCh).all), 32 * W, smem, s>>>(p, maps, sp, marks, parts, err);
     return cudaGetLastError();
 }
+template <typename T, int kCh, bool kEnd>
+cudaError_t back(const SsmProblem &p, const Maps *maps, const Split &sp, const float4 *marks, const Parts &parts,
+                 unsigned int *err, cudaStream_t s) {
+    cudaError_t e;
+    if (!maps) e = run_bwd<T, kCh, 0, kEnd, false>(p, Maps{}, sp, marks, parts, err, s);
+    else if (p.N == 16) e = run_bwd<T, kCh, 16, kEnd, true>(p, *maps, sp, marks, parts, err, s);
+    else e = run_bwd<T, kCh, 0, kEnd, true>(p, *maps, sp, marks, parts, err, s);
+    if (e == cudaSuccess) count_launches(1);
+    return e;
+}
+
+template <typename T>
+cudaError_t whole_fwd(const SsmProblem &p, int splits, int num_sms, void *ws, unsigned int *err, cudaStream_t s) {
+    Maps store;
+    const bool vec = vectors(p);
+    if (vec && !make_maps(p, 1, &store)) return cudaErrorInvalidResourceHandle;
+    const Maps *maps = vec ? &store : nullptr;
+    Split sp = split_of(p, 1, splits, num_sms);
+    cudaError_t e = cudaSuccess;
+    if (sp.n > 1) {
+        sp.h = static_cast<float *>(ws);
+        sp.sum = reinterpret_cast<float *>(static_cast<char *>(ws) + split_state_bytes(p, sp));
+        e = fwd<T, 1, kEnds>(p, maps, sp, sp.n - 1, num_sms, nullptr, err, s);      // (nothing starts from the last one's end)
+        if (e == cudaSuccess) e = join(p, sp, false, s);
+    }
+    return e == cudaSuccess ? fwd<T, 1, kOutputs>(p, maps, sp, sp.n, num_sms, nullptr, err, s) : e;
+}
 template <typename T, int kCh>
-cudaError_t bwd(const SsmProblem &p, int num_sms, void *ws, unsigned int *err, cudaStream_t s) {
-    const BwdWorkspace lay = bwd_workspace(p);
+cudaError_t whole_bwd(const SsmProblem &p, int splits, int num_sms, void *ws, unsigned int *err, cudaStream_t s) {
+    Maps store;
+    const bool vec = vectors(p);
+    if (vec && !make_maps(p, kCh, &store)) return cudaErrorInvalidResourceHandle;
+    const Maps *maps = vec ? &store : nullptr;
+    Split sp = split_of(p, kCh, splits, num_sms);
+    const BwdWorkspace lay = bwd_workspace(p, sp);
     char *at = static_cast<char *>(ws);
     float4 *marks = reinterpret_cast<float4 *>(at);
     const Parts parts{reinterpret_cast<float *>(at + lay.marks), reinterpret_cast<float *>(at + lay.marks + lay.rows)};
-    Maps maps;
-    const bool vec = vectors(p);
-    if (vec && !make_maps(p, kCh, &maps)) return cudaErrorInvalidResourceHandle;
-    cudaError_t e = fwd<T, kCh, false>(p, vec ? &maps : nullptr, num_sms, marks, err, s);
+    cudaError_t e = cudaSuccess;
+    if (sp.n > 1) {
+        at += lay.marks + lay.rows + lay.chan;
+        sp.h = reinterpret_cast<float *>(at);
+        sp.g = reinterpret_cast<float *>(at + split_state_bytes(p, sp));
+        sp.sum = reinterpret_cast<float *>(at + 2 * split_state_bytes(p, sp));
+        e = fwd<T, kCh, kEnds>(p, maps, sp, sp.n, num_sms, nullptr, err, s);
+        if (e == cudaSuccess) e = back<T, kCh, true>(p, maps, sp, nullptr, parts, err, s);
+        if (e == cudaSuccess) e = join(p, sp, false, s);
+        if (e == cudaSuccess) e = join(p, sp, true, s);
+    }
+    if (e == cudaSuccess) e = fwd<T, kCh, kMarks>(p, maps, sp, sp.n, num_sms, marks, err, s);
+    if (e == cudaSuccess) e = back<T, kCh, false>(p, maps, sp, marks, parts, err, s);
     if (e != cudaSuccess) return e;
-    if (!vec) e = run_bwd<T, kCh, 0, false>(p, Maps{}, marks, parts, err, s);
-    else if (p.N == 16) e = run_bwd<T, kCh, 16, true>(p, maps, marks, parts, err, s);
-    else e = run_bwd<T, kCh, 0, true>(p, maps, marks, parts, err, s);
-    if (e == cudaSuccess) count_launches(3);
+    const int64_t rows = p.B * p.T * p.G * 2 * ((p.N + 3) / 4 * 4), chan = p.C * (p.N + 2);
+    ssm_rows_kernel<T><<<(unsigned)((rows + 255) / 256), 256, 0, s>>>(p, parts, tiles_of(p.C, p.G, kCh));
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    ssm_chan_kernel<<<(unsigned)((chan + 255) / 256), 256, 0, s>>>(p, parts, p.B * sp.n);
+    if ((e = cudaGetLastError()) == cudaSuccess) count_launches(2);
     return e;
 }
 
 }  // namespace
 
-size_t ssm_fwd_workspace_bytes(const SsmProblem &, int, int) { return 0; }
-size_t ssm_bwd_workspace_bytes(const SsmProblem &p, int, int) { return bwd_workspace(p).all; }
-
-cudaError_t launch_ssm_fwd(const SsmProblem &p, int, int num_sms, void *, unsigned int *dev_err, cudaStream_t s) {
-    Maps maps;
-    const bool vec = vectors(p);
-    if (vec && !make_maps(p, 1, &maps)) return cudaErrorInvalidResourceHandle;
-    const Maps *m = vec ? &maps : nullptr;
-    return p.io == 0 ? fwd<__nv_bfloat16, 1, true>(p, m, num_sms, nullptr, dev_err, s)
-                     : fwd<float, 1, true>(p, m, num_sms, nullptr, dev_err, s);
+size_t ssm_fwd_workspace_bytes(const SsmProblem &p, int splits, int num_sms) {
+    const Split sp = split_of(p, 1, splits, num_sms);
+    return split_state_bytes(p, sp) + split_sum_bytes(p, sp);
+}
+size_t ssm_bwd_workspace_bytes(const SsmProblem &p, int splits, int num_sms) {
+    return bwd_workspace(p, split_of(p, bwd_channels(p), splits, num_sms)).all;
 }
 
-cudaError_t launch_ssm_bwd(const SsmProblem &p, int, int num_sms, void *ws, unsigned int *dev_err, cudaStream_t s) {
+cudaError_t launch_ssm_fwd(const SsmProblem &p, int splits, int num_sms, void *ws, unsigned int *dev_err, cudaStream_t s) {
+    return p.io == 0 ? whole_fwd<__nv_bfloat16>(p, splits, num_sms, ws, dev_err, s)
+                     : whole_fwd<float>(p, splits, num_sms, ws, dev_err, s);
+}
+
+cudaError_t launch_ssm_bwd(const SsmProblem &p, int splits, int num_sms, void *ws, unsigned int *dev_err, cudaStream_t s) {
     if (bwd_channels(p) == 2)
-        return p.io == 0 ? bwd<__nv_bfloat16, 2>(p, num_sms, ws, dev_err, s) : bwd<float, 2>(p, num_sms, ws, dev_err, s);
-    return p.io == 0 ? bwd<__nv_bfloat16, 1>(p, num_sms, ws, dev_err, s) : bwd<float, 1>(p, num_sms, ws, dev_err, s);
+        return p.io == 0 ? whole_bwd<__nv_bfloat16, 2>(p, splits, num_sms, ws, dev_err, s)
+                         : whole_bwd<float, 2>(p, splits, num_sms, ws, dev_err, s);
+    return p.io == 0 ? whole_bwd<__nv_bfloat16, 1>(p, splits, num_sms, ws, dev_err, s)
+                     : whole_bwd<float, 1>(p, splits, num_sms, ws, dev_err, s);
 }
 
 cudaError_t launch_ssm_step(const SsmProblem &p, int, unsigned int *dev_err, cudaStream_t s) {

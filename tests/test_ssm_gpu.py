@@ -78,6 +78,24 @@ def test_long_and_short_memories(steps):
     check(make(1, 200, 32, 1, 16, "f32", seed=4, steps=steps), "f32")
 
 
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("splits", [1, 2, 3, 7, 1000])
+def test_sequences_in_segments(splits, io):
+    """The join of segments adds a few roundings to a state for each of them; the bounds count several for each token."""
+    check(make(2, 203, 40, 2, 16, io, seed=splits, steps=(1e-3, 0.5)), io, seq_splits=splits)
+    check(make(1, 90, 70, 1, 16, io, seed=splits + 1, state=False), io, seq_splits=splits)
+    check(make(1, 65, 9, 1, 11, io, seed=splits + 2, strided=True), io, seq_splits=splits)
+
+
+@pytest.mark.parametrize("B,T,C,G,N", [(1, 1500, 32, 1, 16), (2, 700, 19, 1, 16), (1, 900, 16, 2, 8), (1, 520, 6, 1, 96)])
+def test_few_channels(B, T, C, G, N):
+    """What is cut by the rule."""
+    from chunkwise_recurrent_prefill_gb300 import ssm_workspace_size
+    d = make(B, T, C, G, N, "f32", seed=T, state=False)
+    assert ssm_workspace_size(*(d[n] for n in ("u", "dt", "A", "Bm", "Cm")), z=d["z"]) > 0
+    check(d, "f32")
+
+
 def test_steps_of_zero_keep_the_state():
     """Bit for bit, whatever A is."""
     from chunkwise_recurrent_prefill_gb300 import ssm_fwd, ssm_step
