@@ -159,7 +159,7 @@ size_t ssm_workspace(const ssm_shape *shape, const gla_options *opt, bool backwa
     unsigned *err;
     gla::device_info(&sms, &err);
     const int splits = opt ? opt->seq_splits : 0;
-    return backward ? gla::ssm_bwd_workspace_bytes(p, splits, sms) : gla::ssm_fwd_workspace_bytes(p, splits, sms);
+    return backward ? gla::ssm_bwd_workspace_bytes(p, splits, sms, true) : gla::ssm_fwd_workspace_bytes(p, splits, sms, true);
 }
 
 // A state after no tokens: the one before them, or zero.
@@ -371,7 +371,7 @@ gla_status ssm_fwd(const void *u, const void *dt, const float *A, const void *Bm
     const int splits = opt ? opt->seq_splits : 0;
     void *ws;
     rc = get_workspace(opt ? opt->workspace : nullptr, opt ? opt->workspace_bytes : 0,
-                       gla::ssm_fwd_workspace_bytes(p, splits, sms), s, used, 11, &ws);
+                       gla::ssm_fwd_workspace_bytes(p, splits, sms, false), s, used, 11, &ws);
     if (rc != GLA_OK) return rc;
     return done("scan launch", gla::launch_ssm_fwd(p, splits, sms, ws, err, s));
 }
@@ -439,7 +439,7 @@ gla_status ssm_bwd(const void *d_o, const void *u, const void *dt, const float *
     const int splits = opt ? opt->seq_splits : 0;
     void *ws;
     rc = get_workspace(opt ? opt->workspace : nullptr, opt ? opt->workspace_bytes : 0,
-                       gla::ssm_bwd_workspace_bytes(p, splits, sms), s, used, 20, &ws);
+                       gla::ssm_bwd_workspace_bytes(p, splits, sms, false), s, used, 20, &ws);
     if (rc != GLA_OK) return rc;
     return done("scan gradient launch", gla::launch_ssm_bwd(p, splits, sms, ws, err, s));
 }

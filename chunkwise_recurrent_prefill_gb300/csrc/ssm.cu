@@ -24,7 +24,6 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
-#include <stdlib.h>
 
 #include "elem.cuh"
 #include "gla_internal.h"
@@ -84,52 +83,31 @@ __device__ __forceinline__ float softplus(float x) {
 }
 __device__ __forceinline__ float step_size(float x, int on) { return on ? softplus(x) : x; }
 
-// What a CTA's warps read: the sequence's rows from the tile's first channel (the group's B and C) on.
-struct Source {
-    const void *p;
-    int64_t t;          // element stride of a token
-    int width;          // elements that exist, of a row of `row` in the stage
-    int row;
-};
-
-// Brings the tokens [t0, t0 + kTok) of a source into to[kTok][row] element by element, with zeros for tokens and
-// elements that do not exist: what TMA does where rows are on 16 bytes.
-template <typename T>
-__device__ __forceinline__ void stage_rows(const Source &s, int64_t t0, int64_t T_, T *to) {
-    const T *p = static_cast<const T *>(s.p) + t0 * s.t;
-    T zero;
-    put(&zero, 0.f);
-    for (int k = threadIdx.x % 32; k < kTok * s.row; k += 32) {
-        const int i = k / s.row, v = k - i * s.row;
-        to[k] = t0 + i < T_ && v < s.width ? p[i * s.t + v] : zero;
-    }
-}
-
 // Tensor maps of the rows: boxes of kTok tokens by a tile's channels (or a group's states).
 struct Maps {
     CUtensorMap in[4], b, c, out[3];
 };
 
 // B and C of the chunk as floats, the values of two tokens side by side as the packed arithmetic takes
-// them: from[2][kTok][N] -> to[2][kTok / 2][NP] float2, NP = N up to a multiple of 4, zero past N.
+// them: from[2][kTok][row] -> to[2][kTok / 2][NP] float2, NP = N up to a multiple of 4, zero past N.
 template <typename T, int kN>
-__device__ __forceinline__ void widen_rows(const T *from, float2 *to, int N) {
+__device__ __forceinline__ void widen_rows(const T *from, float2 *to, int N, int row) {
     const int lane = threadIdx.x % 32, NP = (N + 3) / 4 * 4;
     if constexpr (kN > 0) {     // four states at a time
 #pragma unroll
         for (int k = lane; k < kTok * kN / 4; k += 32) {
-            const int row = k / (kN / 4), q = k % (kN / 4);     // row: a pair of tokens of B, or of C
+            const int i = k / (kN / 4), q = k % (kN / 4);       // i: a pair of tokens of B, or of C
             float x[4], y[4];
-            Pack<T, 4>::unpack(*reinterpret_cast<const typename Pack<T, 4>::raw *>(from + 2 * row * N + 4 * q), x);
-            Pack<T, 4>::unpack(*reinterpret_cast<const typename Pack<T, 4>::raw *>(from + (2 * row + 1) * N + 4 * q), y);
-            float4 *t = reinterpret_cast<float4 *>(to + row * NP + 4 * q);
+            Pack<T, 4>::unpack(*reinterpret_cast<const typename Pack<T, 4>::raw *>(from + 2 * i * kN + 4 * q), x);
+            Pack<T, 4>::unpack(*reinterpret_cast<const typename Pack<T, 4>::raw *>(from + (2 * i + 1) * kN + 4 * q), y);
+            float4 *t = reinterpret_cast<float4 *>(to + i * NP + 4 * q);
             t[0] = make_float4(x[0], y[0], x[1], y[1]);
             t[1] = make_float4(x[2], y[2], x[3], y[3]);
         }
     } else {
         for (int k = lane; k < kTok * NP; k += 32) {
-            const int row = k / NP, n = k - row * NP;
-            to[k] = n < N ? make_float2(get(from + 2 * row * N + n), get(from + (2 * row + 1) * N + n)) : both(0.f);
+            const int i = k / NP, n = k - i * NP;
+            to[k] = n < N ? make_float2(get(from + 2 * i * row + n), get(from + (2 * i + 1) * row + n)) : both(0.f);
         }
     }
 }
@@ -208,6 +186,7 @@ struct Split {
 template <int kCh>
 struct Place {
     int64_t b, row, tile, g, c0;    // row: b n + the segment; c0: the first channel
+    int in;                         // where it is in the inputs
     int seg;
     int64_t ch0, ch1;               // chunks
     int width, mine;                // channels of the tile, of the lane
@@ -223,18 +202,11 @@ struct Place {
         const int64_t cg = p.C / p.G, first = (tile - g * tl.per_group) * 32 * kCh;
         width = (int)min((int64_t)32 * kCh, cg - first);
         c0 = g * cg + first;
+        in = (int)(g * p.group + first);
         mine = max(0, min(kCh, width - kCh * (int)(threadIdx.x % 32)));
     }
     // Channel j of the lane; the tile's first one where there is none.
     __device__ int64_t channel(int j) const { return c0 + (j < mine ? threadIdx.x % 32 * kCh + j : 0); }
-    template <typename T>
-    __device__ Source channels(const SsmRows &r) const {
-        return Source{r.p ? static_cast<const T *>(r.p) + b * r.b + c0 : nullptr, r.t, width, 32 * kCh};
-    }
-    template <typename T>
-    __device__ Source rows(const SsmRows &r, int N) const {
-        return Source{static_cast<const T *>(r.p) + b * r.b + g * N, r.t, N, N};
-    }
 };
 
 // States [kCh][kSt] of step q of the lane, from and to row `row` of [rows, C, N].
@@ -265,7 +237,7 @@ __device__ __forceinline__ void store_states(float *to, int64_t row, const SsmPr
 //   sums[W][Q][32] float4 (backward): dA;  turn[W][32][kTurn] float (backward): sums across lanes
 //   rows[W][2][kPairs][NP] float2: B and C of a warp's chunk;  bar[W][Q]
 //   stage[W][2]: a chunk as it lies in memory, on its way while the one before it is worked on:
-//     kIn tensors [kTok][32 kCh], then B and C [kTok][N];  full[W][2]: it is there
+//     kIn tensors [kTok][32 kCh], then B and C [kTok][row];  full[W][2]: it is there
 //   dx[W][kPairs][kCh][32] float4 (forward): d and d u of a warp's chunk
 constexpr int kTurn = 66;           // (lanes that write pairs side by side meet no bank twice)
 template <typename T, int kCh>
@@ -277,8 +249,8 @@ struct Ring {
     unsigned char *stage;
     static __host__ __device__ int steps(int N) { return (N + 4 / kCh - 1) / (4 / kCh); }
     static __host__ __device__ int padded(int N) { return (N + 3) / 4 * 4; }
-    static __host__ __device__ size_t stage_bytes(int in, int N) {
-        return ((size_t)in * kTok * 32 * kCh * sizeof(T) + 2 * kTok * (size_t)N * sizeof(T) + 127) / 128 * 128;
+    static __host__ __device__ size_t stage_bytes(int in, int row) {
+        return ((size_t)in * kTok * 32 * kCh * sizeof(T) + 2 * kTok * (size_t)row * sizeof(T) + 127) / 128 * 128;
     }
     static __host__ __device__ size_t round(size_t n) { return (n + 127) / 128 * 128; }
     static __host__ __device__ size_t stage_at(int W, int N, bool backward) {
@@ -286,8 +258,8 @@ struct Ring {
         return W * Q * 32 * 16 * (backward ? 2 : 1) + Q * 2 * 32 * 16 + (backward ? round(W * 32 * kTurn * 4) : 0) +
                round((size_t)W * 2 * kPairs * padded(N) * 8) + round(W * (Q + 2) * 8);
     }
-    static __host__ __device__ size_t bytes(int W, int in, int N, bool backward) {
-        return stage_at(W, N, backward) + 2 * W * stage_bytes(in, N) + (backward ? 0 : W * kPairs * kCh * 32 * 16);
+    static __host__ __device__ size_t bytes(int W, int in, int N, int row, bool backward) {
+        return stage_at(W, N, backward) + 2 * W * stage_bytes(in, row) + (backward ? 0 : W * kPairs * kCh * 32 * 16);
     }
     __device__ Ring(unsigned char *smem, int W, int N, bool backward) {
         const int Q = steps(N);
@@ -438,7 +410,7 @@ __device__ __forceinline__ void load_bc(const float2 *row, int q, float2 (&v)[kS
 enum { kOutputs = 0, kMarks = 1, kEnds = 2 };
 
 // kN: N, if known at compile time. segs: segments of a sequence that this call walks over.
-template <typename T, int kCh, int kN, int kMode, bool kVec>
+template <typename T, int kCh, int kN, int kMode>
 __global__ void __launch_bounds__(512, 1)
 ssm_fwd_kernel(const __grid_constant__ SsmProblem p, const __grid_constant__ Maps maps, const Split sp, int segs,
                float4 *marks, unsigned int *err) {
@@ -447,7 +419,7 @@ ssm_fwd_kernel(const __grid_constant__ SsmProblem p, const __grid_constant__ Map
     constexpr bool kOut = kMode == kOutputs;
     constexpr int kSt = 4 / kCh, kIn = kOut ? 3 : 2, kRow = kTok * 32 * kCh;
     using R = Ring<T, kCh>;
-    const int W = blockDim.x / 32, N = kN ? kN : p.N, Q = R::steps(N), NP = R::padded(N);
+    const int W = blockDim.x / 32, N = kN ? kN : p.N, row = kN ? kN : p.row, Q = R::steps(N), NP = R::padded(N);
     R ring(smem, W, N, false);
     const int w = threadIdx.x / 32, lane = threadIdx.x % 32;
     const Tiles tl = tiles_of(p.C, p.G, kCh);
@@ -460,35 +432,27 @@ ssm_fwd_kernel(const __grid_constant__ SsmProblem p, const __grid_constant__ Map
         D[c] = p.D ? p.D[at.channel(c)] : 0.f;
     }
     float2 *rows = ring.rows + w * 2 * kPairs * NP;
-    const size_t stage_bytes = R::stage_bytes(kIn, N);
+    const size_t stage_bytes = R::stage_bytes(kIn, row);
     auto stage = [&](int k) { return reinterpret_cast<T *>(ring.stage + (2 * w + k) * stage_bytes); };
     // d and d u of a chunk: in registers they would cost a tenth more instructions (moves; 128 registers are few)
     float4 *dx = reinterpret_cast<float4 *>(ring.stage + 2 * W * stage_bytes) + w * kPairs * kCh * 32 + lane;
     const int64_t chunks = (p.T + kTok - 1) / kTok;
-    // the chunk into buffer k of the stage, by one lane where TMA does it
+    // the chunk into buffer k of the stage
     auto fetch = [&](int64_t ch, int k) {
         if (ch >= at.ch1) return;
         T *to = stage(k);
         const int64_t t0 = ch * kTok;
-        if (kVec) {
-            if (lane == 0) {
-                uint64_t *bar = ring.full + 2 * w + k;
-                const bool z = kOut && p.z.p;
-                tc::bulk_wait_read_all();       // the outputs that were there
-                tc::mbar_arrive_expect_tx(bar, ((z ? 3 : 2) * kRow + 2 * kTok * N) * (int)sizeof(T));
-                const int c = (int)at.c0, b = (int)at.b, t = (int)t0, n = (int)at.g * N;
-                tc::tma_load_4d(to, &maps.in[0], bar, c, t, b, 0);
-                tc::tma_load_4d(to + kRow, &maps.in[1], bar, c, t, b, 0);
-                if (z) tc::tma_load_4d(to + 2 * kRow, &maps.in[2], bar, c, t, b, 0);
-                tc::tma_load_4d(to + kIn * kRow, &maps.b, bar, n, t, b, 0);
-                tc::tma_load_4d(to + kIn * kRow + kTok * N, &maps.c, bar, n, t, b, 0);
-            }
-        } else {
-            stage_rows<T>(at.template channels<T>(p.u), t0, p.T, to);
-            stage_rows<T>(at.template channels<T>(p.dt), t0, p.T, to + kRow);
-            if (kOut && p.z.p) stage_rows<T>(at.template channels<T>(p.z), t0, p.T, to + 2 * kRow);
-            stage_rows<T>(at.template rows<T>(p.Bm, N), t0, p.T, to + kIn * kRow);
-            stage_rows<T>(at.template rows<T>(p.Cm, N), t0, p.T, to + kIn * kRow + kTok * N);
+        if (lane == 0) {
+            uint64_t *bar = ring.full + 2 * w + k;
+            const bool z = kOut && p.z.p;
+            tc::bulk_wait_read_all();       // the outputs that were there
+            tc::mbar_arrive_expect_tx(bar, ((z ? 3 : 2) * kRow + 2 * kTok * row) * (int)sizeof(T));
+            const int c = at.in, b = (int)at.b, t = (int)t0, n = (int)at.g * row;
+            tc::tma_load_4d(to, &maps.in[0], bar, c, t, b, 0);
+            tc::tma_load_4d(to + kRow, &maps.in[1], bar, c, t, b, 0);
+            if (z) tc::tma_load_4d(to + 2 * kRow, &maps.in[2], bar, c, t, b, 0);
+            tc::tma_load_4d(to + kIn * kRow, &maps.b, bar, n, t, b, 0);
+            tc::tma_load_4d(to + kIn * kRow + kTok * row, &maps.c, bar, n, t, b, 0);
         }
     };
     const Link from = ring.link(w == 0 ? W - 1 : w - 1, Q), to = ring.link(w, Q);
@@ -505,10 +469,9 @@ ssm_fwd_kernel(const __grid_constant__ SsmProblem p, const __grid_constant__ Map
     fetch(at.ch0 + w, 0);
     for (int64_t ch = at.ch0 + w; ch < at.ch1; ch += W) {
         const int64_t t0 = ch * kTok;
-        if (kVec) wait(full + 8 * k, round);
-        else __syncwarp();
+        wait(full + 8 * k, round);
         T *in = stage(k);
-        widen_rows<T, kN>(in + kIn * kRow, rows, N);
+        widen_rows<T, kN>(in + kIn * kRow, rows, N, row);
         float2 d[kCh][kPairs], y[kCh][kPairs];
         step_sizes<T, kCh>(in + kRow, bias, p.softplus, p.T - t0, at.mine, d);
 #pragma unroll
@@ -584,15 +547,14 @@ ssm_fwd_kernel(const __grid_constant__ SsmProblem p, const __grid_constant__ Map
                 for (int c = 0; c < kCh; ++c) o[c] = y[c][ip];
                 put_lane_pair<T, kCh>(in, ip, o);
             }
-            if (kVec && at.width == 32 * kCh) {
-                tc::fence_proxy_async_smem();
-                __syncwarp();
+            tc::fence_proxy_async_smem();       // (TMA reads the outputs, and writes the next chunk over them)
+            __syncwarp();
+            if (p.tma_out && at.width == 32 * kCh) {
                 if (lane == 0) {
                     tc::tma_store_4d(&maps.out[0], in, (int)at.c0, (int)t0, (int)at.b, 0);
                     tc::bulk_commit();
                 }
             } else {
-                __syncwarp();
                 write_rows<T, kCh>(in, p.o, p, at, t0);
             }
         }
@@ -601,7 +563,7 @@ ssm_fwd_kernel(const __grid_constant__ SsmProblem p, const __grid_constant__ Map
         round ^= k == 0;
         parity ^= 1;
     }
-    if (kVec && kOut && lane == 0) tc::bulk_wait_all();
+    if (kOut && lane == 0) tc::bulk_wait_all();
     float *last = kMode == kEnds ? sp.h : kOut && at.seg == sp.n - 1 ? p.hT : nullptr;
     if (last && w == (int)((at.ch1 - at.ch0 - 1) % W)) {    // what the last chunk handed on
         for (int q = 0; q < Q; ++q) {
@@ -630,7 +592,7 @@ struct Parts {
 };
 
 // kEnd: no gradients but that of the state before the segment if nothing comes from behind it (Split).
-template <typename T, int kCh, int kN, bool kEnd, bool kVec>
+template <typename T, int kCh, int kN, bool kEnd>
 __global__ void __launch_bounds__(kCh == 2 ? 256 : 384, 1)
 ssm_bwd_kernel(const __grid_constant__ SsmProblem p, const __grid_constant__ Maps maps, const Split sp,
                const float4 *marks, const Parts parts, unsigned int *err) {
@@ -638,7 +600,7 @@ ssm_bwd_kernel(const __grid_constant__ SsmProblem p, const __grid_constant__ Map
     __shared__ float2 chan[kCh == 2 ? 8 : 12][32 * kCh];
     constexpr int kSt = 4 / kCh, kIn = 4, kRow = kTok * 32 * kCh;
     using R = Ring<T, kCh>;
-    const int W = blockDim.x / 32, N = kN ? kN : p.N, Q = R::steps(N), NP = R::padded(N);
+    const int W = blockDim.x / 32, N = kN ? kN : p.N, row = kN ? kN : p.row, Q = R::steps(N), NP = R::padded(N);
     R ring(smem, W, N, true);
     const int w = threadIdx.x / 32, lane = threadIdx.x % 32;
     const Tiles tl = tiles_of(p.C, p.G, kCh);
@@ -655,34 +617,25 @@ ssm_bwd_kernel(const __grid_constant__ SsmProblem p, const __grid_constant__ Map
     }
     float2 *rows = ring.rows + w * 2 * kPairs * NP;
     float *turn = ring.turn + w * 32 * kTurn;
-    const size_t stage_bytes = R::stage_bytes(kIn, N);
+    const size_t stage_bytes = R::stage_bytes(kIn, row);
     auto stage = [&](int k) { return reinterpret_cast<T *>(ring.stage + (2 * w + k) * stage_bytes); };
     const int64_t chunks = (p.T + kTok - 1) / kTok, steps = at.ch1 - at.ch0;
-    // the chunk into buffer k of the stage, by one lane where TMA does it
+    // the chunk into buffer k of the stage
     auto fetch = [&](int64_t step, int k) {
         if (step >= steps) return;
         T *to = stage(k);
         const int64_t t0 = (at.ch1 - 1 - step) * kTok;
-        if (kVec) {
-            if (lane == 0) {
-                uint64_t *bar = ring.full + 2 * w + k;
-                tc::bulk_wait_read_all();       // the gradients that were there
-                tc::mbar_arrive_expect_tx(bar, ((p.z.p ? 4 : 3) * kRow + 2 * kTok * N) * (int)sizeof(T));
-                const int c = (int)at.c0, b = (int)at.b, t = (int)t0, n = (int)at.g * N;
-                tc::tma_load_4d(to, &maps.in[0], bar, c, t, b, 0);
-                tc::tma_load_4d(to + kRow, &maps.in[1], bar, c, t, b, 0);
-                tc::tma_load_4d(to + 2 * kRow, &maps.in[3], bar, c, t, b, 0);
-                if (p.z.p) tc::tma_load_4d(to + 3 * kRow, &maps.in[2], bar, c, t, b, 0);
-                tc::tma_load_4d(to + kIn * kRow, &maps.b, bar, n, t, b, 0);
-                tc::tma_load_4d(to + kIn * kRow + kTok * N, &maps.c, bar, n, t, b, 0);
-            }
-        } else {
-            stage_rows<T>(at.template channels<T>(p.u), t0, p.T, to);
-            stage_rows<T>(at.template channels<T>(p.dt), t0, p.T, to + kRow);
-            stage_rows<T>(at.template channels<T>(p.go), t0, p.T, to + 2 * kRow);
-            if (p.z.p) stage_rows<T>(at.template channels<T>(p.z), t0, p.T, to + 3 * kRow);
-            stage_rows<T>(at.template rows<T>(p.Bm, N), t0, p.T, to + kIn * kRow);
-            stage_rows<T>(at.template rows<T>(p.Cm, N), t0, p.T, to + kIn * kRow + kTok * N);
+        if (lane == 0) {
+            uint64_t *bar = ring.full + 2 * w + k;
+            tc::bulk_wait_read_all();       // the gradients that were there
+            tc::mbar_arrive_expect_tx(bar, ((p.z.p ? 4 : 3) * kRow + 2 * kTok * row) * (int)sizeof(T));
+            const int c = at.in, b = (int)at.b, t = (int)t0, n = (int)at.g * row;
+            tc::tma_load_4d(to, &maps.in[0], bar, c, t, b, 0);
+            tc::tma_load_4d(to + kRow, &maps.in[1], bar, c, t, b, 0);
+            tc::tma_load_4d(to + 2 * kRow, &maps.in[3], bar, c, t, b, 0);
+            if (p.z.p) tc::tma_load_4d(to + 3 * kRow, &maps.in[2], bar, c, t, b, 0);
+            tc::tma_load_4d(to + kIn * kRow, &maps.b, bar, n, t, b, 0);
+            tc::tma_load_4d(to + kIn * kRow + kTok * row, &maps.c, bar, n, t, b, 0);
         }
     };
     const Link from = ring.link(w == 0 ? W - 1 : w - 1, Q), to = ring.link(w, Q);
@@ -699,10 +652,9 @@ ssm_bwd_kernel(const __grid_constant__ SsmProblem p, const __grid_constant__ Map
         const float4 *mark = marks + ((at.b * chunks + ch) * tl.all + at.tile) * Q * 32 + lane;
         float4 mk;                  // a step's states come while the one before is worked on
         if (!kEnd) mk = mark[0];
-        if (kVec) wait(full + 8 * k, round);
-        else __syncwarp();
+        wait(full + 8 * k, round);
         T *in = stage(k);
-        widen_rows<T, kN>(in + kIn * kRow, rows, N);
+        widen_rows<T, kN>(in + kIn * kRow, rows, N, row);
         float2 d[kCh][kPairs], x[kCh][kPairs], dy[kCh][kPairs];
         float2 y[kCh][kPairs], gB[kCh][kPairs], wA[kCh][kPairs];
         step_sizes<T, kCh>(in + kRow, bias, p.softplus, p.T - t0, at.mine, d);
@@ -732,7 +684,7 @@ ssm_bwd_kernel(const __grid_constant__ SsmProblem p, const __grid_constant__ Map
             float2 A[4], a[4][kPairs], s[4][kPairs];
             float *mine = turn + lane * kTurn + (kCh == 2 ? q % 2 * 32 : 0);
             ring.load_a(q, A);
-            if (kEnd) {
+            if constexpr (kEnd) {
 #pragma unroll
                 for (int ip = 0; ip < kPairs; ++ip)
 #pragma unroll
@@ -753,155 +705,149 @@ ssm_bwd_kernel(const __grid_constant__ SsmProblem p, const __grid_constant__ Map
                 }
                 store4(to.slot + 512 * q, G);
                 hand_over(to.bar + 8 * q, lane);
-                continue;
-            }
-            float h[4] = {mk.x, mk.y, mk.z, mk.w};
-            if (q + 1 < Q) mk = mark[(q + 1) * 32];
+            } else {
+                float h[4] = {mk.x, mk.y, mk.z, mk.w};
+                if (q + 1 < Q) mk = mark[(q + 1) * 32];
 #pragma unroll
-            for (int ip = 0; ip < kPairs; ++ip) {
-                float2 b[kSt], c[kSt], dC[kSt];
-                load_bc<kSt>(rows + ip * NP, q, b);
-                load_bc<kSt>(rows + (kPairs + ip) * NP, q, c);
+                for (int ip = 0; ip < kPairs; ++ip) {
+                    float2 b[kSt], c[kSt], dC[kSt];
+                    load_bc<kSt>(rows + ip * NP, q, b);
+                    load_bc<kSt>(rows + (kPairs + ip) * NP, q, c);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    a[j][ip] = decay2(A[j], d[j / kSt][ip]);
-                    s[j][ip] = mul2(b[j % kSt], x[j / kSt][ip]);
-                    // s: the states after the tokens
-                    s[j][ip].x = fmaf(a[j][ip].x, ip ? s[j][ip ? ip - 1 : 0].y : h[j], s[j][ip].x);
-                    s[j][ip].y = fmaf(a[j][ip].y, s[j][ip].x, s[j][ip].y);
-                    y[j / kSt][ip] = fma2(c[j % kSt], s[j][ip], y[j / kSt][ip]);
-                    dC[j % kSt] = j < kSt ? mul2(s[j][ip], dy[0][ip]) : fma2(s[j][ip], dy[j / kSt][ip], dC[j % kSt]);
+                    for (int j = 0; j < 4; ++j) {
+                        a[j][ip] = decay2(A[j], d[j / kSt][ip]);
+                        s[j][ip] = mul2(b[j % kSt], x[j / kSt][ip]);
+                        // s: the states after the tokens
+                        s[j][ip].x = fmaf(a[j][ip].x, ip ? s[j][ip ? ip - 1 : 0].y : h[j], s[j][ip].x);
+                        s[j][ip].y = fmaf(a[j][ip].y, s[j][ip].x, s[j][ip].y);
+                        y[j / kSt][ip] = fma2(c[j % kSt], s[j][ip], y[j / kSt][ip]);
+                        dC[j % kSt] = j < kSt ? mul2(s[j][ip], dy[0][ip]) : fma2(s[j][ip], dy[j / kSt][ip], dC[j % kSt]);
+                    }
+#pragma unroll
+                    for (int n = 0; n < kSt; ++n) *reinterpret_cast<float2 *>(mine + n * kTok + 2 * ip) = dC[n];
                 }
+                wait(from.bar + 8 * q, parity);
+                const float4 v = load4(from.slot + 512 * q);
+                float G[4] = {v.x, v.y, v.z, v.w};      // what comes from the tokens after
+                // the walk, which the next warp waits for; a becomes the gradient of the state, the state before a
+                // token becomes w (that before the first token: h)
 #pragma unroll
-                for (int n = 0; n < kSt; ++n) *reinterpret_cast<float2 *>(mine + n * kTok + 2 * ip) = dC[n];
-            }
-            wait(from.bar + 8 * q, parity);
-            const float4 v = load4(from.slot + 512 * q);
-            float G[4] = {v.x, v.y, v.z, v.w};      // what comes from the tokens after
-            // the walk, which the next warp waits for; a becomes the gradient of the state, the state before a
-            // token becomes w (that before the first token: h)
+                for (int ip = kPairs - 1; ip >= 0; --ip) {
+                    float2 c[kSt];
+                    load_bc<kSt>(rows + (kPairs + ip) * NP, q, c);
 #pragma unroll
-            for (int ip = kPairs - 1; ip >= 0; --ip) {
-                float2 c[kSt];
-                load_bc<kSt>(rows + (kPairs + ip) * NP, q, c);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    float2 g = mul2(c[j % kSt], dy[j / kSt][ip]);
-                    g.y += G[j];
-                    G[j] = a[j][ip].y * g.y;
-                    s[j][ip].x *= G[j];
-                    g.x += G[j];
-                    G[j] = a[j][ip].x * g.x;
-                    if (ip) s[j][ip - 1].y *= G[j];
-                    else h[j] *= G[j];
-                    a[j][ip] = g;
+                    for (int j = 0; j < 4; ++j) {
+                        float2 g = mul2(c[j % kSt], dy[j / kSt][ip]);
+                        g.y += G[j];
+                        G[j] = a[j][ip].y * g.y;
+                        s[j][ip].x *= G[j];
+                        g.x += G[j];
+                        G[j] = a[j][ip].x * g.x;
+                        if (ip) s[j][ip - 1].y *= G[j];
+                        else h[j] *= G[j];
+                        a[j][ip] = g;
+                    }
                 }
-            }
-            store4(to.slot + 512 * q, G);
-            hand_over(to.bar + 8 * q, lane);
-            float2 dA[4];
+                store4(to.slot + 512 * q, G);
+                hand_over(to.bar + 8 * q, lane);
+                float2 dA[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) dA[j] = both(0.f);
+                for (int j = 0; j < 4; ++j) dA[j] = both(0.f);
 #pragma unroll
-            for (int ip = 0; ip < kPairs; ++ip) {
-                float2 b[kSt], dB[kSt];
-                load_bc<kSt>(rows + ip * NP, q, b);
+                for (int ip = 0; ip < kPairs; ++ip) {
+                    float2 b[kSt], dB[kSt];
+                    load_bc<kSt>(rows + ip * NP, q, b);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float2 g = a[j][ip], wt = make_float2(ip ? s[j][ip ? ip - 1 : 0].y : h[j], s[j][ip].x);
-                    gB[j / kSt][ip] = fma2(g, b[j % kSt], gB[j / kSt][ip]);
-                    wA[j / kSt][ip] = fma2(wt, A[j], wA[j / kSt][ip]);
-                    dA[j] = fma2(wt, d[j / kSt][ip], dA[j]);
-                    dB[j % kSt] = j < kSt ? mul2(g, x[0][ip]) : fma2(g, x[j / kSt][ip], dB[j % kSt]);
+                    for (int j = 0; j < 4; ++j) {
+                        const float2 g = a[j][ip], wt = make_float2(ip ? s[j][ip ? ip - 1 : 0].y : h[j], s[j][ip].x);
+                        gB[j / kSt][ip] = fma2(g, b[j % kSt], gB[j / kSt][ip]);
+                        wA[j / kSt][ip] = fma2(wt, A[j], wA[j / kSt][ip]);
+                        dA[j] = fma2(wt, d[j / kSt][ip], dA[j]);
+                        dB[j % kSt] = j < kSt ? mul2(g, x[0][ip]) : fma2(g, x[j / kSt][ip], dB[j % kSt]);
+                    }
+#pragma unroll
+                    for (int n = 0; n < kSt; ++n) *reinterpret_cast<float2 *>(mine + (kSt + n) * kTok + 2 * ip) = dB[n];
                 }
+                // (a chunk's sum first: those of thousands of tokens go up in two steps)
+                float4 *sum = ring.sums + (w * Q + q) * 32 + lane;
+                const float4 all = *sum;
+                *sum = make_float4(all.x + (dA[0].x + dA[0].y), all.y + (dA[1].x + dA[1].y), all.z + (dA[2].x + dA[2].y),
+                                   all.w + (dA[3].x + dA[3].y));
+                if (kCh == 1 || q % 2 == 1 || q == Q - 1) {
+                    __syncwarp();
+                    float2 v = both(0.f);
 #pragma unroll
-                for (int n = 0; n < kSt; ++n) *reinterpret_cast<float2 *>(mine + (kSt + n) * kTok + 2 * ip) = dB[n];
-            }
-            // (a chunk's sum first: those of thousands of tokens go up in two steps)
-            float4 *sum = ring.sums + (w * Q + q) * 32 + lane;
-            const float4 all = *sum;
-            *sum = make_float4(all.x + (dA[0].x + dA[0].y), all.y + (dA[1].x + dA[1].y), all.z + (dA[2].x + dA[2].y),
-                               all.w + (dA[3].x + dA[3].y));
-            if (kCh == 1 || q % 2 == 1 || q == Q - 1) {
-                __syncwarp();
-                float2 v = both(0.f);
-#pragma unroll
-                for (int l = 0; l < 32; ++l) v = add2(v, *reinterpret_cast<const float2 *>(turn + l * kTurn + 2 * lane));
-                __syncwarp();
-                const int at_q = kCh == 2 ? q / 2 * 2 + lane / 16 : q;              // the step,
-                const int col = 2 * (kCh == 2 ? lane % 16 : lane);                  // [2][kSt][kTok]
-                const int n = kSt * at_q + col / kTok % kSt, i = col % kTok, dB_ = col / (kSt * kTok);
-                if (n < N && at_q <= q) {
-                    float *out = parts.rows + (((at.tile * p.B + at.b) * p.T + t0 + i) * 2 + (1 - dB_)) * NP + n;
-                    if (t0 + i < p.T) out[0] = v.x;
-                    if (t0 + i + 1 < p.T) out[2 * NP] = v.y;
+                    for (int l = 0; l < 32; ++l) v = add2(v, *reinterpret_cast<const float2 *>(turn + l * kTurn + 2 * lane));
+                    __syncwarp();
+                    const int at_q = kCh == 2 ? q / 2 * 2 + lane / 16 : q;              // the step,
+                    const int col = 2 * (kCh == 2 ? lane % 16 : lane);                  // [2][kSt][kTok]
+                    const int n = kSt * at_q + col / kTok % kSt, i = col % kTok, dB_ = col / (kSt * kTok);
+                    if (n < N && at_q <= q) {
+                        float *out = parts.rows + (((at.tile * p.B + at.b) * p.T + t0 + i) * 2 + (1 - dB_)) * NP + n;
+                        if (t0 + i < p.T) out[0] = v.x;
+                        if (t0 + i + 1 < p.T) out[2 * NP] = v.y;
+                    }
                 }
             }
         }
-        if (kEnd) {
-            __syncwarp();       // the stage and the rows have been read
-            k ^= 1;
-            round ^= k == 0;
-            parity ^= 1;
-            continue;
-        }
-        float2 sD[kCh], sbias[kCh];
+        if constexpr (!kEnd) {
+            float2 sD[kCh], sbias[kCh];
 #pragma unroll
-        for (int c = 0; c < kCh; ++c) sD[c] = sbias[c] = both(0.f);
+            for (int c = 0; c < kCh; ++c) sD[c] = sbias[c] = both(0.f);
 #pragma unroll
-        for (int ip = 0; ip < kPairs; ++ip) {
-            float2 u[kCh], raw[kCh], go[kCh], z[kCh], du[kCh], ddt[kCh], dz[kCh];
-            lane_pair<T, kCh>(in, ip, u);
-            lane_pair<T, kCh>(in + kRow, ip, raw);
-            lane_pair<T, kCh>(in + 2 * kRow, ip, go);
-            if (p.z.p) lane_pair<T, kCh>(in + 3 * kRow, ip, z);
+            for (int ip = 0; ip < kPairs; ++ip) {
+                float2 u[kCh], raw[kCh], go[kCh], z[kCh], du[kCh], ddt[kCh], dz[kCh];
+                lane_pair<T, kCh>(in, ip, u);
+                lane_pair<T, kCh>(in + kRow, ip, raw);
+                lane_pair<T, kCh>(in + 2 * kRow, ip, go);
+                if (p.z.p) lane_pair<T, kCh>(in + 3 * kRow, ip, z);
+#pragma unroll
+                for (int c = 0; c < kCh; ++c) {
+                    ddt[c] = fma2(wA[c][ip], both(kLn2), mul2(u[c], gB[c][ip]));
+                    if (p.softplus) {
+                        const float2 r = add2(raw[c], both(bias[c]));
+                        ddt[c] = mul2(ddt[c], make_float2(logistic<float>(r.x), logistic<float>(r.y)));
+                    }
+                    if (2 * ip >= p.T - t0) ddt[c].x = 0.f;         // tokens that do not exist
+                    if (2 * ip + 1 >= p.T - t0) ddt[c].y = 0.f;
+                    du[c] = fma2(both(D[c]), dy[c][ip], mul2(d[c][ip], gB[c][ip]));
+                    sbias[c] = add2(sbias[c], ddt[c]);
+                    sD[c] = fma2(dy[c][ip], u[c], sD[c]);
+                    if (p.z.p) {
+                        const float2 yy = fma2(both(D[c]), u[c], y[c][ip]);
+                        dz[c] = mul2(mul2(go[c], yy), make_float2(act_grad<T>(z[c].x, 1), act_grad<T>(z[c].y, 1)));
+                    }
+                }
+                put_lane_pair<T, kCh>(in, ip, du);
+                put_lane_pair<T, kCh>(in + kRow, ip, ddt);
+                if (p.dz) put_lane_pair<T, kCh>(in + 3 * kRow, ip, dz);
+            }
 #pragma unroll
             for (int c = 0; c < kCh; ++c) {
-                ddt[c] = fma2(wA[c][ip], both(kLn2), mul2(u[c], gB[c][ip]));
-                if (p.softplus) {
-                    const float2 r = add2(raw[c], both(bias[c]));
-                    ddt[c] = mul2(ddt[c], make_float2(logistic<float>(r.x), logistic<float>(r.y)));
-                }
-                if (2 * ip >= p.T - t0) ddt[c].x = 0.f;         // tokens that do not exist
-                if (2 * ip + 1 >= p.T - t0) ddt[c].y = 0.f;
-                du[c] = fma2(both(D[c]), dy[c][ip], mul2(d[c][ip], gB[c][ip]));
-                sbias[c] = add2(sbias[c], ddt[c]);
-                sD[c] = fma2(dy[c][ip], u[c], sD[c]);
-                if (p.z.p) {
-                    const float2 yy = fma2(both(D[c]), u[c], y[c][ip]);
-                    dz[c] = mul2(mul2(go[c], yy), make_float2(act_grad<T>(z[c].x, 1), act_grad<T>(z[c].y, 1)));
-                }
+                dD[c] += sD[c].x + sD[c].y;
+                dbias[c] += sbias[c].x + sbias[c].y;
             }
-            put_lane_pair<T, kCh>(in, ip, du);
-            put_lane_pair<T, kCh>(in + kRow, ip, ddt);
-            if (p.dz) put_lane_pair<T, kCh>(in + 3 * kRow, ip, dz);
-        }
-#pragma unroll
-        for (int c = 0; c < kCh; ++c) {
-            dD[c] += sD[c].x + sD[c].y;
-            dbias[c] += sbias[c].x + sbias[c].y;
-        }
-        if (kVec && at.width == 32 * kCh) {
-            tc::fence_proxy_async_smem();
+            tc::fence_proxy_async_smem();           // (TMA reads the gradients, and writes the next chunk over them)
             __syncwarp();
-            if (lane == 0) {
-                tc::tma_store_4d(&maps.out[0], in, (int)at.c0, (int)t0, (int)at.b, 0);
-                tc::tma_store_4d(&maps.out[1], in + kRow, (int)at.c0, (int)t0, (int)at.b, 0);
-                if (p.dz) tc::tma_store_4d(&maps.out[2], in + 3 * kRow, (int)at.c0, (int)t0, (int)at.b, 0);
-                tc::bulk_commit();
+            if (p.tma_out && at.width == 32 * kCh) {
+                if (lane == 0) {
+                    tc::tma_store_4d(&maps.out[0], in, (int)at.c0, (int)t0, (int)at.b, 0);
+                    tc::tma_store_4d(&maps.out[1], in + kRow, (int)at.c0, (int)t0, (int)at.b, 0);
+                    if (p.dz) tc::tma_store_4d(&maps.out[2], in + 3 * kRow, (int)at.c0, (int)t0, (int)at.b, 0);
+                    tc::bulk_commit();
+                }
+            } else {
+                write_rows<T, kCh>(in, p.du, p, at, t0);
+                write_rows<T, kCh>(in + kRow, p.ddt, p, at, t0);
+                if (p.dz) write_rows<T, kCh>(in + 3 * kRow, p.dz, p, at, t0);
             }
-        } else {
-            __syncwarp();
-            write_rows<T, kCh>(in, p.du, p, at, t0);
-            write_rows<T, kCh>(in + kRow, p.ddt, p, at, t0);
-            if (p.dz) write_rows<T, kCh>(in + 3 * kRow, p.dz, p, at, t0);
         }
         __syncwarp();       // the stage and the rows have been read
         k ^= 1;
         round ^= k == 0;
         parity ^= 1;
     }
-    if (kVec && lane == 0) tc::bulk_wait_all();
+    if (lane == 0) tc::bulk_wait_all();
     float *first = kEnd ? sp.g : at.seg == 0 ? p.dh0 : nullptr;
     if (first && w == (int)((steps - 1) % W)) {             // what the first token handed on
         for (int q = 0; q < Q; ++q) {
@@ -910,19 +856,20 @@ ssm_bwd_kernel(const __grid_constant__ SsmProblem p, const __grid_constant__ Map
             store_states<kCh>(first, kEnd ? at.row : at.b, p, at, q, G);
         }
     }
-    if (kEnd) return;
+    if constexpr (!kEnd) {
 #pragma unroll
-    for (int c = 0; c < kCh; ++c) chan[w][lane * kCh + c] = make_float2(dD[c], dbias[c]);
-    __syncthreads();
-    // the warps' sums in order: a thread for each channel and state (state fastest)
-    for (int k2 = threadIdx.x; k2 < at.width * (N + 2); k2 += blockDim.x) {
-        const int ci = k2 / (N + 2), n = k2 % (N + 2), l = ci / kCh, j = ci % kCh * kSt + n % kSt;
-        float s = 0.f;
-        for (int i = 0; i < W; ++i) {
-            if (n < N) s += reinterpret_cast<const float *>(ring.sums + (i * Q + n / kSt) * 32 + l)[j];
-            else s += n == N ? chan[i][ci].x : chan[i][ci].y;
+        for (int c = 0; c < kCh; ++c) chan[w][lane * kCh + c] = make_float2(dD[c], dbias[c]);
+        __syncthreads();
+        // the warps' sums in order: a thread for each channel and state (state fastest)
+        for (int k2 = threadIdx.x; k2 < at.width * (N + 2); k2 += blockDim.x) {
+            const int ci = k2 / (N + 2), n = k2 % (N + 2), l = ci / kCh, j = ci % kCh * kSt + n % kSt;
+            float s = 0.f;
+            for (int i = 0; i < W; ++i) {
+                if (n < N) s += reinterpret_cast<const float *>(ring.sums + (i * Q + n / kSt) * 32 + l)[j];
+                else s += n == N ? chan[i][ci].x : chan[i][ci].y;
+            }
+            parts.chan[(at.row * p.C + at.c0 + ci) * (N + 2) + n] = s;
         }
-        parts.chan[(at.row * p.C + at.c0 + ci) * (N + 2) + n] = s;
     }
 }
 
@@ -968,94 +915,134 @@ ssm_chan_kernel(const __grid_constant__ SsmProblem p, const Parts parts, int64_t
     else if (p.dbias) p.dbias[c] = s;
 }
 
-struct Quad {                       // four states of a channel
-    float2 a, b;
-};
-__device__ __forceinline__ Quad quad(float4 v) { return Quad{make_float2(v.x, v.y), make_float2(v.z, v.w)}; }
-__device__ __forceinline__ float4 vec4(const Quad &q) { return make_float4(q.a.x, q.a.y, q.b.x, q.b.y); }
-__device__ __forceinline__ Quad operator*(const Quad &x, float y) { return Quad{mul2(x.a, both(y)), mul2(x.b, both(y))}; }
-__device__ __forceinline__ Quad fmaq(const Quad &x, const Quad &y, const Quad &z) {
-    return Quad{fma2(x.a, y.a, z.a), fma2(x.b, y.b, z.b)};
-}
-// x . y added to a pair of sums
-__device__ __forceinline__ float2 dotq(const Quad &x, const Quad &y, float2 s) { return fma2(x.b, y.b, fma2(x.a, y.a, s)); }
-
-// Four consecutive values of a row of N from value n0 on (zero past the end).
-__device__ __forceinline__ float4 load_quad(const float *row, int n0, int N) {
-    if (N % 4 == 0 && (reinterpret_cast<uintptr_t>(row) & 15) == 0)
-        return *reinterpret_cast<const float4 *>(row + n0);
-    return make_float4(n0 < N ? row[n0] : 0.f, n0 + 1 < N ? row[n0 + 1] : 0.f, n0 + 2 < N ? row[n0 + 2] : 0.f,
-                       n0 + 3 < N ? row[n0 + 3] : 0.f);
-}
-__device__ __forceinline__ void store_quad(float *row, int n0, int N, float4 v) {
-    if (N % 4 == 0) {
-        *reinterpret_cast<float4 *>(row + n0) = v;
-        return;
-    }
-    if (n0 < N) row[n0] = v.x;
-    if (n0 + 1 < N) row[n0 + 1] = v.y;
-    if (n0 + 2 < N) row[n0 + 2] = v.z;
-    if (n0 + 3 < N) row[n0 + 3] = v.w;
-}
-
-// One token of each row on the pages of a pool. kL lanes (a power of two) own a channel, four states
-// each (more where N > 4 kL); their outputs are added by shuffles.
-template <typename T>
-__global__ void __launch_bounds__(256)
-ssm_step_kernel(const __grid_constant__ SsmProblem p, int lanes, unsigned int *err) {
-    const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int l = (int)(id % lanes);
-    const int64_t c = id / lanes % p.C, r = id / lanes / p.C;
-    const bool in = r < p.B;
-    const int64_t slot = !in ? -1 : p.slots ? p.slots[r] : r;
-    const bool live = slot >= 0 && slot < p.P;
-    if (in && slot >= p.P && c == 0 && l == 0) atomicOr(err, kDevErrPages);
-    float y = 0.f, u = 0.f;
-    if (live) {
-        const int64_t g = c / (p.C / p.G);
-        u = get(static_cast<const T *>(p.u.p) + r * p.u.b + c);
-        const float d = step_size(get(static_cast<const T *>(p.dt.p) + r * p.dt.b + c) + (p.dt_bias ? p.dt_bias[c] : 0.f),
-                                  p.softplus);
-        float *S = p.S + (slot * p.C + c) * p.N;
-        const T *Bp = static_cast<const T *>(p.Bm.p) + r * p.Bm.b + g * p.N;
-        const T *Cp = static_cast<const T *>(p.Cm.p) + r * p.Cm.b + g * p.N;
-        float2 s = both(0.f);
-        for (int n0 = 4 * l; n0 < p.N; n0 += 4 * lanes) {
-            const float4 a = load_quad(p.A + c * p.N, n0, p.N);
-            const Quad A{make_float2(scale_a(a.x), scale_a(a.y)), make_float2(scale_a(a.z), scale_a(a.w))};
-            float Bv[4], Cv[4];
+// One token of each row on the pages of a pool. kLanes lanes (4 kLanes >= N) own a channel, four states each, and keep
+// its row of A while they go through rows of the batch, kRows at a time: all that these need is on its way
+// together, and the page numbers of the next ones. A row's step size and output are made by one of the lanes. The
+// states are read and written once: HBM bandwidth bounds a batch. Measured: STEP_NOTE
+template <typename T, int kLanes>
+__global__ void __launch_bounds__(256, 3)
+ssm_step_kernel(const __grid_constant__ SsmProblem p, int vec, unsigned int *err) {
+    constexpr int kRows = 4, kOwn = kLanes < kRows ? kRows / kLanes : 1;     // rows of a lane: l, l + kLanes, ...
+    using Raw = typename Pack<T, 4>::raw;
+    const int l = threadIdx.x % kLanes, n0 = 4 * l;
+    const int64_t c = (int64_t)blockIdx.x * (256 / kLanes) + threadIdx.x / kLanes;
+    const bool live = c < p.C;
+    const int64_t cc = live ? c : 0, g = cc / (p.C / p.G);
+    const bool whole = p.N % 4 == 0, mine = live && n0 < p.N;
+    float A[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                Bv[j] = n0 + j < p.N ? get(Bp + n0 + j) : 0.f;
-                Cv[j] = n0 + j < p.N ? get(Cp + n0 + j) : 0.f;
+    for (int j = 0; j < 4; ++j) A[j] = live && n0 + j < p.N ? scale_a(p.A[cc * p.N + n0 + j]) : 0.f;
+    const float D = p.D ? p.D[cc] : 0.f, bias = p.dt_bias ? p.dt_bias[cc] : 0.f;
+    const int rows = (int)p.B, P = (int)p.P;        // (at most 2^30)
+    auto page_of = [&](int r) { return r >= rows ? -1 : p.slots ? p.slots[r] : r; };
+    auto quad = [&](const SsmRows &m, int r) {              // four values of a row of B or C
+        const T *q = static_cast<const T *>(m.p) + r * m.b + g * p.N + n0;
+        if (vec) return *reinterpret_cast<const Raw *>(q);
+        float f[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) f[j] = n0 + j < p.N ? get(q + j) : 0.f;
+        return Pack<T, 4>::pack(f);                         // (they are T's values: nothing is rounded)
+    };
+    const int step = (int)gridDim.y * kRows;
+    int next[kRows];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) next[i] = page_of((int)blockIdx.y * kRows + i);
+    // (the whole warp walks together: rows past the last one do nothing)
+    for (int r0 = (int)blockIdx.y * kRows; r0 < rows; r0 += step) {
+        float4 h[kRows];
+        Raw Br[kRows], Cr[kRows];
+        float u[kOwn], d[kOwn], z[kOwn];
+        int page[kRows];
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            if (next[i] >= P && c == 0 && l == 0) atomicOr(err, kDevErrPages);
+            page[i] = next[i] < P ? next[i] : -1;
+            h[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            Br[i] = Cr[i] = Raw{};
+            if (page[i] >= 0 && mine) {
+                const float *S = p.S + ((int64_t)page[i] * p.C + cc) * p.N + n0;
+                if (whole) {
+                    h[i] = *reinterpret_cast<const float4 *>(S);
+                } else {
+                    h[i].x = S[0];
+                    if (n0 + 1 < p.N) h[i].y = S[1];
+                    if (n0 + 2 < p.N) h[i].z = S[2];
+                    if (n0 + 3 < p.N) h[i].w = S[3];
+                }
+                Br[i] = quad(p.Bm, r0 + i);
+                Cr[i] = quad(p.Cm, r0 + i);
             }
-            const Quad x = Quad{make_float2(Bv[0], Bv[1]), make_float2(Bv[2], Bv[3])} * (d * u);
-            const Quad h = fmaq(Quad{decay2(A.a, both(d)), decay2(A.b, both(d))}, quad(load_quad(S, n0, p.N)), x);
-            store_quad(S, n0, p.N, vec4(h));
-            s = dotq(h, Quad{make_float2(Cv[0], Cv[1]), make_float2(Cv[2], Cv[3])}, s);
         }
-        y = s.x + s.y;
-    }
-    for (int o = lanes / 2; o > 0; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
-    if (!in || l != 0) return;
-    if (live) {
-        if (p.D) y = fmaf(p.D[c], u, y);
-        if (p.z.p) {
-            const float z = get(static_cast<const T *>(p.z.p) + r * p.z.b + c);
-            y *= z * logistic<T>(z);
+#pragma unroll
+        for (int k = 0; k < kOwn; ++k) {
+            const int i = l + k * kLanes;
+            u[k] = d[k] = z[k] = 0.f;
+            if (i < kRows && live && r0 + i < rows) {
+                u[k] = get(static_cast<const T *>(p.u.p) + (r0 + i) * p.u.b + c);
+                d[k] = get(static_cast<const T *>(p.dt.p) + (r0 + i) * p.dt.b + c);
+                if (p.z.p) z[k] = get(static_cast<const T *>(p.z.p) + (r0 + i) * p.z.b + c);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) next[i] = page_of(r0 + step + i);
+#pragma unroll
+        for (int k = 0; k < kOwn; ++k) d[k] = step_size(d[k] + bias, p.softplus);
+        float y[kRows];
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            const float di = __shfl_sync(0xffffffffu, d[i / kLanes], i % kLanes, kLanes);
+            const float x = di * __shfl_sync(0xffffffffu, u[i / kLanes], i % kLanes, kLanes);
+            float4 v;
+            float Bv[4], Cv[4];
+            Pack<T, 4>::unpack(Br[i], Bv);
+            Pack<T, 4>::unpack(Cr[i], Cv);
+            v.x = fmaf(ex2(fmaf(A[0], di, 2e-8f)), h[i].x, x * Bv[0]);
+            v.y = fmaf(ex2(fmaf(A[1], di, 2e-8f)), h[i].y, x * Bv[1]);
+            v.z = fmaf(ex2(fmaf(A[2], di, 2e-8f)), h[i].z, x * Bv[2]);
+            v.w = fmaf(ex2(fmaf(A[3], di, 2e-8f)), h[i].w, x * Bv[3]);
+            y[i] = fmaf(v.x, Cv[0], v.y * Cv[1]) + fmaf(v.z, Cv[2], v.w * Cv[3]);
+            if (page[i] >= 0 && mine) {
+                float *S = p.S + ((int64_t)page[i] * p.C + cc) * p.N + n0;
+                if (whole) {
+                    *reinterpret_cast<float4 *>(S) = v;
+                } else {
+                    S[0] = v.x;
+                    if (n0 + 1 < p.N) S[1] = v.y;
+                    if (n0 + 2 < p.N) S[2] = v.z;
+                    if (n0 + 3 < p.N) S[3] = v.w;
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kRows; ++i)
+#pragma unroll
+            for (int o = kLanes / 2; o > 0; o >>= 1) y[i] += __shfl_xor_sync(0xffffffffu, y[i], o);
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            if (i % kLanes != l || !live || r0 + i >= rows) continue;
+            float o = 0.f;
+            if (page[i] >= 0) {
+                o = y[i];
+                if (p.D) o = fmaf(D, u[i / kLanes], o);
+                if (p.z.p) o *= z[i / kLanes] * logistic<T>(z[i / kLanes]);
+            }
+            put(static_cast<T *>(p.o) + (int64_t)(r0 + i) * p.C + c, o);
         }
     }
-    put(static_cast<T *>(p.o) + r * p.C + c, y);
 }
+
+// Shared memory of a ring (the kernels have up to 4 KB of their own).
+constexpr size_t kRingBytes = 222 * 1024;
 
 template <typename T, int kCh>
 int ring_warps(const SsmProblem &p, int in, bool backward, int most) {
     const int64_t chunks = (p.T + kTok - 1) / kTok;
     int W = most;
-    // (the backward kernel has 4 KB of its own)
-    while (W > 1 && Ring<T, kCh>::bytes(W, in, p.N, backward) > 222 * 1024) W = W > 8 ? W - 4 : W / 2;
+    while (W > 1 && Ring<T, kCh>::bytes(W, in, p.N, p.row, backward) > kRingBytes) W = W > 8 ? W - 4 : W / 2;
     return (int)std::min<int64_t>(W, chunks);
 }
+
+size_t round256(size_t n) { return (n + 255) & ~size_t(255); }
 
 // A map of [B, T, cols] rows.
 bool rows_map(CUtensorMap *m, const void *base, int io, int64_t cols, int64_t T, int64_t B, int64_t st, int64_t sb,
@@ -1071,50 +1058,126 @@ bool rows_map(CUtensorMap *m, const void *base, int io, int64_t cols, int64_t T,
               CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
-// The maps of a call; false where a map cannot be made.
+// The maps of a call (of its packed inputs); false where a map cannot be made.
 bool make_maps(const SsmProblem &p, int ch, Maps *m) {
     const SsmRows *in[4] = {&p.u, &p.dt, &p.z, &p.go};
     void *const out[3] = {p.du ? p.du : p.o, p.ddt, p.dz};
     for (int i = 0; i < 4; ++i)
-        if (in[i]->p && !rows_map(&m->in[i], in[i]->p, p.io, p.C, p.T, p.B, in[i]->t, in[i]->b, 32 * ch)) return false;
-    for (int i = 0; i < 3; ++i)
+        if (in[i]->p && !rows_map(&m->in[i], in[i]->p, p.io, p.G * p.group, p.T, p.B, in[i]->t, in[i]->b, 32 * ch))
+            return false;
+    for (int i = 0; i < 3 && p.tma_out; ++i)
         if (out[i] && !rows_map(&m->out[i], out[i], p.io, p.C, p.T, p.B, p.C, p.T * p.C, 32 * ch)) return false;
-    return rows_map(&m->b, p.Bm.p, p.io, p.G * p.N, p.T, p.B, p.Bm.t, p.Bm.b, p.N) &&
-           rows_map(&m->c, p.Cm.p, p.io, p.G * p.N, p.T, p.B, p.Cm.t, p.Cm.b, p.N);
+    return rows_map(&m->b, p.Bm.p, p.io, p.G * p.row, p.T, p.B, p.Bm.t, p.Bm.b, p.row) &&
+           rows_map(&m->c, p.Cm.p, p.io, p.G * p.row, p.T, p.B, p.Cm.t, p.Cm.b, p.row);
 }
 
-// Whether the rows of all inputs, and the first channels and groups of the tiles, are on 16 bytes.
-bool vectors(const SsmProblem &p) {
-    const int es = p.io == 0 ? 2 : 4;
-    for (const SsmRows *r : {&p.u, &p.dt, &p.z, &p.go, &p.Bm, &p.Cm})
-        if (r->p && (reinterpret_cast<uintptr_t>(r->p) % 16 || r->b * es % 16 || r->t * es % 16)) return false;
-    // (strides and coordinates that a tensor map holds)
-    for (const SsmRows *r : {&p.u, &p.dt, &p.z, &p.go, &p.Bm, &p.Cm})
-        if (r->p && (r->b >= int64_t(1) << 38 || r->t >= int64_t(1) << 38)) return false;
-    return p.C / p.G * es % 16 == 0 && p.N * es % 16 == 0 && p.T * p.C < int64_t(1) << 38;
+// TMA wants rows and tiles on 16 bytes. Inputs that are not (odd numbers of channels or states, slices that start
+// anywhere) are first copied to rows that are: a copy costs a fraction of what reading them element by
+// element did (16384 tokens of 3000 channels, B and C from an odd column on: 1190 us, PACK_NOTE with the copy).
+struct Packing {
+    size_t bytes;               // of the copies
+    bool copy[6];               // u, dt, z, go, B, C
+};
+// any: the most that pointers of any alignment need (of a forward call, or a backward one).
+Packing packing_of(const SsmProblem &p, bool any, bool backward) {
+    const int es = p.io == 0 ? 2 : 4, unit = 16 / es;
+    const SsmRows *t[6] = {&p.u, &p.dt, &p.z, &p.go, &p.Bm, &p.Cm};
+    const int64_t cg = p.C / p.G;
+    Packing k{};
+    for (int i = 0; i < 6; ++i) {
+        const int64_t w = i < 4 ? cg : p.N;
+        if (any ? i == 3 && !backward : !t[i]->p) continue;
+        k.copy[i] = any || w % unit || reinterpret_cast<uintptr_t>(t[i]->p) % 16 || t[i]->b % unit || t[i]->t % unit ||
+                    t[i]->b >= int64_t(1) << 38 || t[i]->t >= int64_t(1) << 38;     // (what a tensor map holds)
+    }
+    for (int i = 0; i < 6; ++i) {
+        const int64_t w = i < 4 ? cg : p.N;
+        if (k.copy[i]) k.bytes += round256((size_t)(p.B * p.T * p.G * ((w + unit - 1) / unit * unit)) * es);
+    }
+    return k;
+}
+struct PackJob {
+    const void *from;
+    int64_t b, t;               // element strides
+    void *to;                   // [B, T, G, padded]
+    int64_t width, padded;
+};
+struct PackJobs {
+    PackJob job[6];
+    int64_t T, rows;            // rows: B T G
+    int G;
+};
+template <typename T>
+__global__ void __launch_bounds__(256)
+ssm_pack_kernel(const __grid_constant__ PackJobs jobs) {
+    const PackJob &j = jobs.job[blockIdx.y];
+    if (!j.to) return;
+    T zero;
+    put(&zero, 0.f);
+    // a warp for a group of a token
+    for (int64_t row = (int64_t)blockIdx.x * 8 + threadIdx.x / 32; row < jobs.rows; row += (int64_t)gridDim.x * 8) {
+        const int64_t token = row / jobs.G, g = row - token * jobs.G, b = token / jobs.T, t = token - b * jobs.T;
+        const T *from = static_cast<const T *>(j.from) + b * j.b + t * j.t + g * j.width;
+        T *to = static_cast<T *>(j.to) + row * j.padded;
+        for (int64_t i = threadIdx.x % 32; i < j.padded; i += 32) to[i] = i < j.width ? from[i] : zero;
+    }
+}
+// Copies what has to be, and leaves the problem with inputs that TMA reads.
+cudaError_t pack(SsmProblem *p, char *at, int num_sms, cudaStream_t s) {
+    const Packing k = packing_of(*p, false, false);
+    const int es = p->io == 0 ? 2 : 4, unit = 16 / es;
+    const int64_t cg = p->C / p->G;
+    SsmRows *t[6] = {&p->u, &p->dt, &p->z, &p->go, &p->Bm, &p->Cm};
+    PackJobs jobs{};
+    jobs.T = p->T;
+    jobs.G = (int)p->G;
+    jobs.rows = p->B * p->T * p->G;
+    bool any = false;
+    p->group = (cg + unit - 1) / unit * unit;
+    p->row = (p->N + unit - 1) / unit * unit;
+    p->tma_out = cg % unit == 0 && p->T * p->C < int64_t(1) << 38;
+    for (int i = 0; i < 6; ++i) {
+        if (!k.copy[i]) continue;
+        any = true;
+        const int64_t padded = i < 4 ? p->group : p->row;
+        jobs.job[i] = PackJob{t[i]->p, t[i]->b, t[i]->t, at, i < 4 ? cg : p->N, padded};
+        t[i]->p = at;
+        t[i]->t = p->G * padded;
+        t[i]->b = p->T * p->G * padded;
+        at += round256((size_t)(jobs.rows * padded) * es);
+    }
+    if (!any) return cudaSuccess;
+    const dim3 grid((unsigned)std::min<int64_t>((jobs.rows + 7) / 8, 8 * num_sms), 6);
+    if (p->io == 0) ssm_pack_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(jobs);
+    else ssm_pack_kernel<float><<<grid, 256, 0, s>>>(jobs);
+    const cudaError_t e = cudaGetLastError();
+    if (e == cudaSuccess) count_launches(1);
+    return e;
 }
 
-// Channels of a lane in the backward pass: two, which share the loads of B and C and the sums across
-// lanes, where the states of a step fit shared memory.
+// Channels of a lane in the backward pass: two share the loads of B and C and the sums across lanes (4 x 2047 tokens
+// of 2048 channels, 16 states, bf16: 460 us against 585 with one), if a ring of eight warps still fits
+// shared memory (2 x 358 tokens of 481 channels, 64 states: 672 us with two warps, 272 with one channel to a lane).
 int bwd_channels(const SsmProblem &p) {
-    const char *e = getenv("SSM_CH");
-    if (e) return atoi(e);
-    return p.N <= 64 ? 2 : 1; }
+    const int unit = p.io == 0 ? 8 : 4, row = (p.N + unit - 1) / unit * unit;
+    const size_t bytes = p.io == 0 ? Ring<__nv_bfloat16, 2>::bytes(8, 4, p.N, row, true)
+                                   : Ring<float, 2>::bytes(8, 4, p.N, row, true);
+    return bytes <= kRingBytes ? 2 : 1;
+}
 
 // Segments of a sequence for CTAs of 32 ch channels. Cutting it costs two thirds of a walk more (and the join), so it is
 // done where the tiles leave almost half of the SMs idle; two CTAs to an SM then, of at least 8 chunks.
 // Measured: SPLIT_NOTE
-Split split_of(const SsmProblem &p, int ch, int splits, int num_sms) {
+Split split_of(const SsmProblem &p, int ch, bool backward, int splits, int num_sms) {
     const int64_t chunks = (p.T + kTok - 1) / kTok, ctas = p.B * tiles_of(p.C, p.G, ch).all;
     int64_t n = 1;
     if (splits > 0) n = std::min({(int64_t)splits, chunks, std::max<int64_t>(1, (int64_t(1) << 30) / ctas)});
-    else if (9 * ctas <= 5 * num_sms) n = std::min<int64_t>(2 * num_sms / ctas, chunks / 8);
+    else if (9 * ctas <= 5 * num_sms) n = std::min<int64_t>((backward ? 1 : 2) * num_sms / ctas, chunks / (backward ? 16 : 8));
     Split sp{};
     sp.chunks = (chunks + std::max<int64_t>(n, 1) - 1) / std::max<int64_t>(n, 1);
     sp.n = (int)((chunks + sp.chunks - 1) / sp.chunks);
     return sp;
 }
-size_t round256(size_t n) { return (n + 255) & ~size_t(255); }
 // The segments' states of one direction, and their step sizes.
 size_t split_state_bytes(const SsmProblem &p, const Split &sp) {
     return sp.n > 1 ? round256((size_t)p.B * sp.n * p.C * p.N * 4) : 0;
@@ -1139,27 +1202,26 @@ BwdWorkspace bwd_workspace(const SsmProblem &p, const Split &sp) {
     return w;
 }
 
-template <typename T, int kCh, int kN, int kMode, bool kVec>
+template <typename T, int kCh, int kN, int kMode>
 cudaError_t run_fwd(const SsmProblem &p, const Maps &maps, const Split &sp, int segs, int warps, float4 *marks,
                     unsigned int *err, cudaStream_t s) {
     constexpr int in = kMode == kOutputs ? 3 : 2;
     const int W = (int)std::min<int64_t>(ring_warps<T, kCh>(p, in, false, warps), sp.chunks);
-    const size_t smem = Ring<T, kCh>::bytes(W, in, p.N, false);
-    const auto kernel = ssm_fwd_kernel<T, kCh, kN, kMode, kVec>;
+    const size_t smem = Ring<T, kCh>::bytes(W, in, p.N, p.row, false);
+    const auto kernel = ssm_fwd_kernel<T, kCh, kN, kMode>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     kernel<<<(unsigned)(p.B * segs * tiles_of(p.C, p.G, kCh).all), 32 * W, smem, s>>>(p, maps, sp, segs, marks, err);
     return cudaGetLastError();
 }
 template <typename T, int kCh, int kMode>
-cudaError_t fwd(const SsmProblem &p, const Maps *maps, const Split &sp, int segs, int num_sms, float4 *marks,
+cudaError_t fwd(const SsmProblem &p, const Maps &maps, const Split &sp, int segs, int num_sms, float4 *marks,
                 unsigned int *err, cudaStream_t s) {
     // 16 warps to an SM: of one ring where there are no more rings than SMs
     const int warps = p.B * segs * tiles_of(p.C, p.G, kCh).all <= num_sms ? 16 : 8;
     cudaError_t e;
-    if (!maps) e = run_fwd<T, kCh, 0, kMode, false>(p, Maps{}, sp, segs, warps, marks, err, s);
-    else if (p.N == 16) e = run_fwd<T, kCh, 16, kMode, true>(p, *maps, sp, segs, warps, marks, err, s);
-    else e = run_fwd<T, kCh, 0, kMode, true>(p, *maps, sp, segs, warps, marks, err, s);
+    if (p.N == 16) e = run_fwd<T, kCh, 16, kMode>(p, maps, sp, segs, warps, marks, err, s);
+    else e = run_fwd<T, kCh, 0, kMode>(p, maps, sp, segs, warps, marks, err, s);
     if (e == cudaSuccess) count_launches(1);
     return e;
 }
@@ -1170,57 +1232,57 @@ cudaError_t join(const SsmProblem &p, const Split &sp, bool back, cudaStream_t s
     return e;
 }
 
-template <typename T, int kCh, int kN, bool kEnd, bool kVec>
+template <typename T, int kCh, int kN, bool kEnd>
 cudaError_t run_bwd(const SsmProblem &p, const Maps &maps, const Split &sp, const float4 *marks, const Parts &parts,
                     unsigned int *err, cudaStream_t s) {
     const int W = (int)std::min<int64_t>(ring_warps<T, kCh>(p, 4, true, kCh == 2 ? 8 : 12), sp.chunks);
-    const size_t smem = Ring<T, kCh>::bytes(W, 4, p.N, true);
-    const auto kernel = ssm_bwd_kernel<T, kCh, kN, kEnd, kVec>;
+    const size_t smem = Ring<T, kCh>::bytes(W, 4, p.N, p.row, true);
+    const auto kernel = ssm_bwd_kernel<T, kCh, kN, kEnd>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     kernel<<<(unsigned)(p.B * sp.n * tiles_of(p.C, p.G, kCh).all), 32 * W, smem, s>>>(p, maps, sp, marks, parts, err);
     return cudaGetLastError();
 }
 template <typename T, int kCh, bool kEnd>
-cudaError_t back(const SsmProblem &p, const Maps *maps, const Split &sp, const float4 *marks, const Parts &parts,
+cudaError_t back(const SsmProblem &p, const Maps &maps, const Split &sp, const float4 *marks, const Parts &parts,
                  unsigned int *err, cudaStream_t s) {
     cudaError_t e;
-    if (!maps) e = run_bwd<T, kCh, 0, kEnd, false>(p, Maps{}, sp, marks, parts, err, s);
-    else if (p.N == 16) e = run_bwd<T, kCh, 16, kEnd, true>(p, *maps, sp, marks, parts, err, s);
-    else e = run_bwd<T, kCh, 0, kEnd, true>(p, *maps, sp, marks, parts, err, s);
+    if (p.N == 16) e = run_bwd<T, kCh, 16, kEnd>(p, maps, sp, marks, parts, err, s);
+    else e = run_bwd<T, kCh, 0, kEnd>(p, maps, sp, marks, parts, err, s);
     if (e == cudaSuccess) count_launches(1);
     return e;
 }
 
 template <typename T>
-cudaError_t whole_fwd(const SsmProblem &p, int splits, int num_sms, void *ws, unsigned int *err, cudaStream_t s) {
-    Maps store;
-    const bool vec = vectors(p);
-    if (vec && !make_maps(p, 1, &store)) return cudaErrorInvalidResourceHandle;
-    const Maps *maps = vec ? &store : nullptr;
-    Split sp = split_of(p, 1, splits, num_sms);
-    cudaError_t e = cudaSuccess;
-    if (sp.n > 1) {
-        sp.h = static_cast<float *>(ws);
-        sp.sum = reinterpret_cast<float *>(static_cast<char *>(ws) + split_state_bytes(p, sp));
+cudaError_t whole_fwd(SsmProblem p, int splits, int num_sms, void *ws, unsigned int *err, cudaStream_t s) {
+    Maps maps;
+    Split sp = split_of(p, 1, false, splits, num_sms);
+    char *at = static_cast<char *>(ws);
+    const size_t copies = packing_of(p, false, false).bytes;
+    cudaError_t e = pack(&p, at, num_sms, s);
+    if (e == cudaSuccess && !make_maps(p, 1, &maps)) e = cudaErrorInvalidResourceHandle;
+    if (e == cudaSuccess && sp.n > 1) {
+        at += copies;
+        sp.h = reinterpret_cast<float *>(at);
+        sp.sum = reinterpret_cast<float *>(at + split_state_bytes(p, sp));
         e = fwd<T, 1, kEnds>(p, maps, sp, sp.n - 1, num_sms, nullptr, err, s);      // (nothing starts from the last one's end)
         if (e == cudaSuccess) e = join(p, sp, false, s);
     }
     return e == cudaSuccess ? fwd<T, 1, kOutputs>(p, maps, sp, sp.n, num_sms, nullptr, err, s) : e;
 }
 template <typename T, int kCh>
-cudaError_t whole_bwd(const SsmProblem &p, int splits, int num_sms, void *ws, unsigned int *err, cudaStream_t s) {
-    Maps store;
-    const bool vec = vectors(p);
-    if (vec && !make_maps(p, kCh, &store)) return cudaErrorInvalidResourceHandle;
-    const Maps *maps = vec ? &store : nullptr;
-    Split sp = split_of(p, kCh, splits, num_sms);
+cudaError_t whole_bwd(SsmProblem p, int splits, int num_sms, void *ws, unsigned int *err, cudaStream_t s) {
+    Maps maps;
+    Split sp = split_of(p, kCh, true, splits, num_sms);
     const BwdWorkspace lay = bwd_workspace(p, sp);
     char *at = static_cast<char *>(ws);
+    const size_t copies = packing_of(p, false, false).bytes;
+    cudaError_t e = pack(&p, at, num_sms, s);
+    if (e == cudaSuccess && !make_maps(p, kCh, &maps)) e = cudaErrorInvalidResourceHandle;
+    at += copies;
     float4 *marks = reinterpret_cast<float4 *>(at);
     const Parts parts{reinterpret_cast<float *>(at + lay.marks), reinterpret_cast<float *>(at + lay.marks + lay.rows)};
-    cudaError_t e = cudaSuccess;
-    if (sp.n > 1) {
+    if (e == cudaSuccess && sp.n > 1) {
         at += lay.marks + lay.rows + lay.chan;
         sp.h = reinterpret_cast<float *>(at);
         sp.g = reinterpret_cast<float *>(at + split_state_bytes(p, sp));
@@ -1243,12 +1305,12 @@ cudaError_t whole_bwd(const SsmProblem &p, int splits, int num_sms, void *ws, un
 
 }  // namespace
 
-size_t ssm_fwd_workspace_bytes(const SsmProblem &p, int splits, int num_sms) {
-    const Split sp = split_of(p, 1, splits, num_sms);
-    return split_state_bytes(p, sp) + split_sum_bytes(p, sp);
+size_t ssm_fwd_workspace_bytes(const SsmProblem &p, int splits, int num_sms, bool any) {
+    const Split sp = split_of(p, 1, false, splits, num_sms);
+    return packing_of(p, any, false).bytes + split_state_bytes(p, sp) + split_sum_bytes(p, sp);
 }
-size_t ssm_bwd_workspace_bytes(const SsmProblem &p, int splits, int num_sms) {
-    return bwd_workspace(p, split_of(p, bwd_channels(p), splits, num_sms)).all;
+size_t ssm_bwd_workspace_bytes(const SsmProblem &p, int splits, int num_sms, bool any) {
+    return packing_of(p, any, true).bytes + bwd_workspace(p, split_of(p, bwd_channels(p), true, splits, num_sms)).all;
 }
 
 cudaError_t launch_ssm_fwd(const SsmProblem &p, int splits, int num_sms, void *ws, unsigned int *dev_err, cudaStream_t s) {
@@ -1264,13 +1326,28 @@ cudaError_t launch_ssm_bwd(const SsmProblem &p, int splits, int num_sms, void *w
                      : whole_bwd<float, 1>(p, splits, num_sms, ws, dev_err, s);
 }
 
-cudaError_t launch_ssm_step(const SsmProblem &p, int, unsigned int *dev_err, cudaStream_t s) {
-    int lanes = 1;
-    while (lanes < 32 && 4 * lanes < p.N) lanes *= 2;
-    const int64_t n = p.B * p.C * lanes;
-    const unsigned grid = (unsigned)((n + 255) / 256);
-    if (p.io == 0) ssm_step_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(p, lanes, dev_err);
-    else ssm_step_kernel<float><<<grid, 256, 0, s>>>(p, lanes, dev_err);
+template <typename T, int kLanes>
+static void run_step(const SsmProblem &p, int num_sms, unsigned int *err, cudaStream_t s) {
+    const int64_t tiles = (p.C * kLanes + 255) / 256, rows = (p.B + 3) / 4;
+    // two rounds of resident CTAs, each with as many rows of its channels as that leaves
+    const dim3 grid((unsigned)tiles, (unsigned)std::min<int64_t>(rows, std::max<int64_t>(1, 6 * num_sms / tiles)));
+    const int vec = p.N % 4 == 0 && p.Bm.b % 4 == 0 && p.Cm.b % 4 == 0 &&
+                    (reinterpret_cast<uintptr_t>(p.Bm.p) | reinterpret_cast<uintptr_t>(p.Cm.p)) % (4 * sizeof(T)) == 0;
+    ssm_step_kernel<T, kLanes><<<grid, 256, 0, s>>>(p, vec, err);
+}
+template <typename T>
+static void step_of(const SsmProblem &p, int num_sms, unsigned int *err, cudaStream_t s) {
+    if (p.N <= 4) run_step<T, 1>(p, num_sms, err, s);
+    else if (p.N <= 8) run_step<T, 2>(p, num_sms, err, s);
+    else if (p.N <= 16) run_step<T, 4>(p, num_sms, err, s);
+    else if (p.N <= 32) run_step<T, 8>(p, num_sms, err, s);
+    else if (p.N <= 64) run_step<T, 16>(p, num_sms, err, s);
+    else run_step<T, 32>(p, num_sms, err, s);
+}
+
+cudaError_t launch_ssm_step(const SsmProblem &p, int num_sms, unsigned int *dev_err, cudaStream_t s) {
+    if (p.io == 0) step_of<__nv_bfloat16>(p, num_sms, dev_err, s);
+    else step_of<float>(p, num_sms, dev_err, s);
     const cudaError_t e = cudaGetLastError();
     if (e == cudaSuccess) count_launches(1);
     return e;

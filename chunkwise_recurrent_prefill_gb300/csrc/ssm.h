@@ -23,14 +23,19 @@ struct SsmProblem {
     float *dA, *dD, *dbias, *dh0;       // dD, dbias, dh0 may be null
     int64_t B, T, C, G;
     int N, softplus, io;
+    // Set by the launchers, whose kernels read by TMA: rows of B and C, and the groups of the other inputs, are this
+    // many elements apart (N and C / G, or those brought to 16 bytes by a copy), and whether TMA writes.
+    int64_t group;
+    int row, tma_out;
     // one token
     float *S;                           // [P, C, N]
     const int *slots;
     int64_t P;
 };
 
-size_t ssm_fwd_workspace_bytes(const SsmProblem &p, int splits, int num_sms);
-size_t ssm_bwd_workspace_bytes(const SsmProblem &p, int splits, int num_sms);
+// any: whatever the alignment of the inputs' pointers (which inputs are copied first depends on it).
+size_t ssm_fwd_workspace_bytes(const SsmProblem &p, int splits, int num_sms, bool any);
+size_t ssm_bwd_workspace_bytes(const SsmProblem &p, int splits, int num_sms, bool any);
 cudaError_t launch_ssm_fwd(const SsmProblem &p, int splits, int num_sms, void *ws, unsigned int *dev_err,
                            cudaStream_t s);
 cudaError_t launch_ssm_bwd(const SsmProblem &p, int splits, int num_sms, void *ws, unsigned int *dev_err,

@@ -92,7 +92,8 @@ def _state(t, name, sh, dev):
 
 
 def ssm_workspace_size(u, dt, A, Bm, Cm, z=None, backward: bool = False, seq_splits: int = 0) -> int:
-    """Bytes of workspace ``ssm_fwd`` (or ``ssm_bwd``) needs for these tensors' shapes."""
+    """Bytes of workspace that are enough for ``ssm_fwd`` (or ``ssm_bwd``) with tensors of these shapes, whatever
+    their alignment."""
     lib = load_library()
     f = lib.ssm_bwd_workspace_size if backward else lib.ssm_fwd_workspace_size
     return int(f(ctypes.byref(_shape(u, dt, A, Bm, Cm, z, False)),

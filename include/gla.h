@@ -559,7 +559,8 @@ gla_status ssm_step(const void *u, const void *dt, const float *A, const void *B
                     const float *D, const void *z, const float *dt_bias, float *S,
                     const int32_t *slots, void *o, int64_t P, const ssm_shape *shape,
                     gla_stream_t stream);
-/* Bytes of workspace ssm_fwd / ssm_bwd need (0 if none, or if they would reject the shape). */
+/* Bytes of workspace that are enough for ssm_fwd / ssm_bwd (0 if they would reject the shape). Inputs that are not on
+ * 16 bytes (pointer, strides, C / G or N) are copied into it first: this counts all of them. */
 size_t ssm_fwd_workspace_size(const ssm_shape *shape, const gla_options *opt);
 size_t ssm_bwd_workspace_size(const ssm_shape *shape, const gla_options *opt);
 
