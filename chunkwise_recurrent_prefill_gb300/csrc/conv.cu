@@ -10,6 +10,7 @@
 #include "conv.h"
 #include "elem.cuh"
 #include "gla_internal.h"
+#include "launch.h"
 
 namespace gla {
 namespace {
@@ -158,6 +159,7 @@ conv_fwd_kernel(const __grid_constant__ ConvProblem p, const ConvPlan pl) {
 template <typename T, int kV, int W, bool kSilu>
 __global__ void __launch_bounds__(kThreads, kBwdCtas)
 conv_bwd_kernel(const __grid_constant__ ConvProblem p, const ConvPlan pl, float *part) {
+    tc::pdl_launch_dependents();
     constexpr int kBatch = 4, kP = (kV + 1) / 2;
     using R = typename Pack<T, kV>::raw;
     __shared__ float sums[kThreads][kV];
@@ -292,6 +294,8 @@ conv_sums_kernel(const float *part, int64_t parts, int64_t C, int W, float *dw, 
     if (id >= C * (W + 1)) return;
     const int64_t j = id / C, c = id - j * C;
     float s = 0.f;
+    tc::pdl_wait_prerequisites();
+#pragma unroll 8
     for (int64_t i = 0; i < parts; ++i) s += part[(i * (W + 1) + j) * C + c];
     if (j < W) {
         if (dw) dw[c * W + j] = s;
@@ -463,17 +467,13 @@ cudaError_t launch_conv_bwd(const ConvProblem &p, void *ws, int num_sms, cudaStr
     int64_t parts = 0;
     float *part = p.dw || p.dbias ? static_cast<float *>(ws) : nullptr;
     dispatch<4, 4>(p, Bwd{p, num_sms, part, &parts, s});
-    cudaError_t e = cudaGetLastError();
+    const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     count_launches(1);
-    if (part) {
-        const int64_t n = p.C * (p.W + 1);
-        conv_sums_kernel<<<(unsigned)((n + kThreads - 1) / kThreads), kThreads, 0, s>>>(part, parts, p.C, p.W, p.dw,
-                                                                                     p.dbias);
-        e = cudaGetLastError();
-        if (e == cudaSuccess) count_launches(1);
-    }
-    return e;
+    if (!part) return e;
+    const int64_t n = p.C * (p.W + 1);
+    return launch(conv_sums_kernel, dim3((unsigned)((n + kThreads - 1) / kThreads)), kThreads, 0, true, s, part, parts, p.C,
+                  p.W, p.dw, p.dbias);
 }
 
 cudaError_t launch_conv_step(const ConvProblem &p, unsigned int *dev_err, cudaStream_t s) {

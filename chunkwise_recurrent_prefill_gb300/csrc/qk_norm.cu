@@ -8,6 +8,7 @@
 
 #include "elem.cuh"
 #include "gla_internal.h"
+#include "launch.h"
 #include "qk_norm.h"
 
 namespace gla {
@@ -102,6 +103,7 @@ qk_plain_fwd(const __grid_constant__ QkProblem p, unsigned int *err) {
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
 qk_plain_bwd(const __grid_constant__ QkProblem p, float *part, unsigned int *err) {
+    tc::pdl_launch_dependents();
     extern __shared__ float sums[];         // [2][kWarps][D]
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     for (int i = threadIdx.x; i < 2 * kWarps * p.D; i += kThreads) sums[i] = 0.f;
@@ -334,6 +336,7 @@ qk_rows_fwd(const __grid_constant__ QkProblem p, const QkPlan pl, unsigned int *
 template <typename T, int V, int kHeads>
 __global__ void __launch_bounds__(kThreads)
 qk_rows_bwd(const __grid_constant__ QkProblem p, const QkPlan pl, float *part, unsigned int *err) {
+    tc::pdl_launch_dependents();
     using P = Pack<T, V>;
     using R = typename P::raw;
     __shared__ float sums[kThreads][V + 1];
@@ -434,26 +437,30 @@ qk_rows_bwd(const __grid_constant__ QkProblem p, const QkPlan pl, float *part, u
     }
 }
 
-// dwq and dwk from parts, each added in a fixed order: 8 rows of threads take every 8th part, then are added.
+// dwq and dwk from parts, each added in a fixed order: 32 rows of threads take every 32nd part, then are added.
 struct QkSums {
     const float *part[2];
     int64_t n[2], stride[2];
 };
-__global__ void __launch_bounds__(kThreads)
-qk_sums_kernel(const __grid_constant__ QkProblem p, const QkSums q) {
-    __shared__ float rows[8][32];
+__global__ void __launch_bounds__(1024)
+qk_sums_kernel(const __grid_constant__ QkProblem p, const __grid_constant__ QkSums q) {
+    __shared__ float rows[32][33];
     const int which = blockIdx.y, col = threadIdx.x % 32, row = threadIdx.x / 32, i = blockIdx.x * 32 + col;
     float s = 0.f;
+    tc::pdl_wait_prerequisites();
     if (i < p.D) {
         const float *at = q.part[which] + i;
-#pragma unroll 4
-        for (int64_t k = row; k < q.n[which]; k += 8) s += at[k * q.stride[which]];
+#pragma unroll 8
+        for (int64_t k = row; k < q.n[which]; k += 32) s += at[k * q.stride[which]];
     }
     rows[row][col] = s;
     __syncthreads();
-    if (row != 0 || i >= p.D || !p.t[which].dw) return;
-    for (int r = 1; r < 8; ++r) s += rows[r][col];
-    p.t[which].dw[i] = s;
+    // a warp adds the rows of one column
+    s = rows[col][row];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    const int c = blockIdx.x * 32 + row;
+    if (col == 0 && c < p.D && p.t[which].dw) p.t[which].dw[c] = s;
 }
 
 int64_t rows_of(const QkProblem &p) { return p.B * p.T * (p.t[0].heads + p.t[1].heads); }
@@ -545,15 +552,10 @@ static cudaError_t run_bwd(const QkProblem &p, float *part, int num_sms, unsigne
             sums.stride[i] = 2 * p.D;
         }
     }
-    cudaError_t e = cudaGetLastError();
+    const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     count_launches(1);
-    if (part) {
-        qk_sums_kernel<<<dim3((p.D + 31) / 32, 2), kThreads, 0, s>>>(p, sums);
-        e = cudaGetLastError();
-        if (e == cudaSuccess) count_launches(1);
-    }
-    return e;
+    return part ? launch(qk_sums_kernel, dim3((p.D + 31) / 32, 2), 1024, 0, true, s, p, sums) : e;
 }
 
 cudaError_t launch_qk_bwd(const QkProblem &p, void *ws, int num_sms, unsigned int *dev_err, cudaStream_t s) {

@@ -27,6 +27,7 @@
 
 #include "elem.cuh"
 #include "gla_internal.h"
+#include "launch.h"
 #include "ssm.h"
 #include "tma_host.h"
 
@@ -414,6 +415,7 @@ template <typename T, int kCh, int kN, int kMode>
 __global__ void __launch_bounds__(512, 1)
 ssm_fwd_kernel(const __grid_constant__ SsmProblem p, const __grid_constant__ Maps maps, const Split sp, int segs,
                float4 *marks, unsigned int *err) {
+    tc::pdl_launch_dependents();
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ float sums[kMode == kEnds ? 16 : 1][32 * kCh];
     constexpr bool kOut = kMode == kOutputs;
@@ -424,6 +426,7 @@ ssm_fwd_kernel(const __grid_constant__ SsmProblem p, const __grid_constant__ Map
     const int w = threadIdx.x / 32, lane = threadIdx.x % 32;
     const Tiles tl = tiles_of(p.C, p.G, kCh);
     const Place<kCh> at(p, tl, sp, segs);
+    tc::pdl_wait_prerequisites();
     ring.begin(p, at, W, N, kMode == kEnds ? nullptr : sp.n > 1 ? sp.h : p.h0, sp.n > 1 ? at.row : at.b);
     float bias[kCh], D[kCh];
 #pragma unroll
@@ -596,6 +599,7 @@ template <typename T, int kCh, int kN, bool kEnd>
 __global__ void __launch_bounds__(kCh == 2 ? 256 : 384, 1)
 ssm_bwd_kernel(const __grid_constant__ SsmProblem p, const __grid_constant__ Maps maps, const Split sp,
                const float4 *marks, const Parts parts, unsigned int *err) {
+    tc::pdl_launch_dependents();
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ float2 chan[kCh == 2 ? 8 : 12][32 * kCh];
     constexpr int kSt = 4 / kCh, kIn = 4, kRow = kTok * 32 * kCh;
@@ -607,6 +611,7 @@ ssm_bwd_kernel(const __grid_constant__ SsmProblem p, const __grid_constant__ Map
     const Place<kCh> at(p, tl, sp, sp.n);
     if (!kEnd)
         for (int q = 0; q < Q; ++q) ring.sums[(w * Q + q) * 32 + lane] = make_float4(0.f, 0.f, 0.f, 0.f);
+    tc::pdl_wait_prerequisites();
     ring.begin(p, at, W, N, kEnd ? nullptr : sp.n > 1 ? sp.g : p.dhT, sp.n > 1 ? at.row : at.b);
     float bias[kCh], D[kCh], dD[kCh], dbias[kCh];
 #pragma unroll
@@ -873,46 +878,66 @@ ssm_bwd_kernel(const __grid_constant__ SsmProblem p, const __grid_constant__ Map
     }
 }
 
-// dB and dC from the tiles' parts, each added in order.
-template <typename T>
+// What the segments start from, from what they end with if they start from zero: in their order forward, or back
+// (blockIdx.y).
 __global__ void __launch_bounds__(256)
-ssm_rows_kernel(const __grid_constant__ SsmProblem p, const Parts parts, const Tiles tl) {
-    const int NP = (p.N + 3) / 4 * 4;
-    const int64_t rows = p.B * p.T, id = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int64_t n = id % NP, k = id / NP % 2, g = id / (2 * NP) % p.G, row = id / (2 * NP) / p.G;
-    if (row >= rows || n >= p.N) return;
-    float s = 0.f;
-    for (int i = 0; i < tl.per_group; ++i)
-        s += parts.rows[(((g * tl.per_group + i) * rows + row) * 2 + k) * NP + n];
-    put(static_cast<T *>(k ? p.dCm : p.dBm) + (row * p.G + g) * p.N + n, s);
-}
-// What the segments start from, from what they end with if they start from zero: in their order forward, or back.
-__global__ void __launch_bounds__(256)
-ssm_join_kernel(const __grid_constant__ SsmProblem p, const Split sp, int back) {
-    const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x, cn = p.C * p.N, b = id / cn, i = id - b * cn, c = i / p.N;
-    if (b >= p.B) return;
+ssm_join_kernel(const __grid_constant__ SsmProblem p, const Split sp) {
+    constexpr int kAhead = 8;       // segments whose values are on their way together
+    tc::pdl_launch_dependents();
+    const bool back = blockIdx.y == 1;
+    const int cn = (int)(p.C * p.N), i = (int)(blockIdx.x * 256 + threadIdx.x);
+    const int64_t b = blockIdx.z;
+    if (i >= cn) return;
     const float A = scale_a(p.A[i]), *from = back ? p.dhT : p.h0;
-    float v = from ? from[id] : 0.f, *x = (back ? sp.g : sp.h) + b * sp.n * cn + i;
-    const float *sum = sp.sum + b * sp.n * p.C + c;
-#pragma unroll 4
-    for (int k = 0; k < sp.n; ++k) {
-        const int seg = back ? sp.n - 1 - k : k;
-        const float end = x[seg * cn], a = exp2f(A * sum[seg * p.C]);
-        x[seg * cn] = v;
-        v = fmaf(a, v, end);
+    float v = from ? from[b * cn + i] : 0.f, *x = (back ? sp.g : sp.h) + b * sp.n * cn + i;
+    const float *sum = sp.sum + b * sp.n * p.C + i / p.N;
+    tc::pdl_wait_prerequisites();
+    for (int k = 0; k < sp.n; k += kAhead) {
+        float end[kAhead], a[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            const int seg = back ? sp.n - 1 - k - j : k + j;
+            const bool in = k + j < sp.n;
+            end[j] = in ? x[(int64_t)seg * cn] : 0.f;
+            a[j] = in ? sum[(int64_t)seg * p.C] : 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            if (k + j >= sp.n) break;
+            x[(int64_t)(back ? sp.n - 1 - k - j : k + j) * cn] = v;
+            v = fmaf(exp2f(A * a[j]), v, end[j]);
+        }
     }
 }
-// dA, dD and ddt_bias from the segments' parts.
+
+// The sums of the backward pass, each added in a fixed order. The first row_ctas CTAs: dB and dC from the tiles'
+// parts; the others: dA, dD and ddt_bias from the segments'.
+template <typename T>
 __global__ void __launch_bounds__(256)
-ssm_chan_kernel(const __grid_constant__ SsmProblem p, const Parts parts, int64_t rows) {
-    const int64_t w = p.N + 2, id = (int64_t)blockIdx.x * 256 + threadIdx.x, c = id / w, n = id % w;
-    if (c >= p.C) return;
+ssm_sums_kernel(const __grid_constant__ SsmProblem p, const Parts parts, const Tiles tl, int segs, unsigned row_ctas) {
     float s = 0.f;
-#pragma unroll 4
-    for (int64_t b = 0; b < rows; ++b) s += parts.chan[(b * p.C + c) * w + n];
-    if (n < p.N) p.dA[c * p.N + n] = s;
-    else if (n == p.N) { if (p.dD) p.dD[c] = s; }
-    else if (p.dbias) p.dbias[c] = s;
+    if (blockIdx.x < row_ctas) {
+        const int NP = (p.N + 3) / 4 * 4, wide = 2 * NP;
+        const int64_t rows = p.B * p.T, id = (int64_t)blockIdx.x * 256 + threadIdx.x, k = id / wide;
+        const int j = (int)(id - k * wide), n = j % NP;
+        const int64_t row = k / p.G, g = k - row * p.G;
+        if (row >= rows || n >= p.N) return;
+        const float *at = parts.rows + (g * tl.per_group * rows + row) * wide + j;
+        tc::pdl_wait_prerequisites();
+#pragma unroll 8
+        for (int i = 0; i < tl.per_group; ++i) s += at[i * rows * wide];
+        put(static_cast<T *>(j < NP ? p.dBm : p.dCm) + (row * p.G + g) * p.N + n, s);
+    } else {
+        const int64_t w = p.N + 2, id = (int64_t)(blockIdx.x - row_ctas) * 256 + threadIdx.x, c = id / w, n = id - c * w;
+        if (c >= p.C) return;
+        const float *at = parts.chan + id;
+        tc::pdl_wait_prerequisites();
+#pragma unroll 8
+        for (int64_t b = 0; b < p.B * segs; ++b) s += at[b * p.C * w];
+        if (n < p.N) p.dA[c * p.N + n] = s;
+        else if (n == p.N) { if (p.dD) p.dD[c] = s; }
+        else if (p.dbias) p.dbias[c] = s;
+    }
 }
 
 // One token of each row on the pages of a pool. kLanes lanes (4 kLanes >= N) own a channel, four states each, and keep
@@ -1110,6 +1135,7 @@ struct PackJobs {
 template <typename T>
 __global__ void __launch_bounds__(256)
 ssm_pack_kernel(const __grid_constant__ PackJobs jobs) {
+    tc::pdl_launch_dependents();
     const PackJob &j = jobs.job[blockIdx.y];
     if (!j.to) return;
     T zero;
@@ -1148,11 +1174,7 @@ cudaError_t pack(SsmProblem *p, char *at, int num_sms, cudaStream_t s) {
     }
     if (!any) return cudaSuccess;
     const dim3 grid((unsigned)std::min<int64_t>((jobs.rows + 7) / 8, 8 * num_sms), 6);
-    if (p->io == 0) ssm_pack_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(jobs);
-    else ssm_pack_kernel<float><<<grid, 256, 0, s>>>(jobs);
-    const cudaError_t e = cudaGetLastError();
-    if (e == cudaSuccess) count_launches(1);
-    return e;
+    return launch(p->io == 0 ? ssm_pack_kernel<__nv_bfloat16> : ssm_pack_kernel<float>, grid, 256, 0, false, s, jobs);
 }
 
 // Channels of a lane in the backward pass: two share the loads of B and C and the sums across lanes (4 x 2047 tokens
@@ -1173,6 +1195,7 @@ Split split_of(const SsmProblem &p, int ch, bool backward, int splits, int num_s
     int64_t n = 1;
     if (splits > 0) n = std::min({(int64_t)splits, chunks, std::max<int64_t>(1, (int64_t(1) << 30) / ctas)});
     else if (9 * ctas <= 5 * num_sms) n = std::min<int64_t>((backward ? 1 : 2) * num_sms / ctas, chunks / (backward ? 16 : 8));
+    if (p.B > 65535 || p.C * p.N > int64_t(1) << 30) n = 1;        // (the join's grid and indices)
     Split sp{};
     sp.chunks = (chunks + std::max<int64_t>(n, 1) - 1) / std::max<int64_t>(n, 1);
     sp.n = (int)((chunks + sp.chunks - 1) / sp.chunks);
@@ -1203,7 +1226,7 @@ BwdWorkspace bwd_workspace(const SsmProblem &p, const Split &sp) {
 }
 
 template <typename T, int kCh, int kN, int kMode>
-cudaError_t run_fwd(const SsmProblem &p, const Maps &maps, const Split &sp, int segs, int warps, float4 *marks,
+cudaError_t run_fwd(const SsmProblem &p, const Maps &maps, const Split &sp, int segs, int warps, float4 *marks, bool after,
                     unsigned int *err, cudaStream_t s) {
     constexpr int in = kMode == kOutputs ? 3 : 2;
     const int W = (int)std::min<int64_t>(ring_warps<T, kCh>(p, in, false, warps), sp.chunks);
@@ -1211,25 +1234,20 @@ cudaError_t run_fwd(const SsmProblem &p, const Maps &maps, const Split &sp, int 
     const auto kernel = ssm_fwd_kernel<T, kCh, kN, kMode>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    kernel<<<(unsigned)(p.B * segs * tiles_of(p.C, p.G, kCh).all), 32 * W, smem, s>>>(p, maps, sp, segs, marks, err);
-    return cudaGetLastError();
+    return launch(kernel, dim3((unsigned)(p.B * segs * tiles_of(p.C, p.G, kCh).all)), 32 * W, smem, after, s, p, maps, sp,
+                  segs, marks, err);
 }
 template <typename T, int kCh, int kMode>
-cudaError_t fwd(const SsmProblem &p, const Maps &maps, const Split &sp, int segs, int num_sms, float4 *marks,
+cudaError_t fwd(const SsmProblem &p, const Maps &maps, const Split &sp, int segs, int num_sms, float4 *marks, bool after,
                 unsigned int *err, cudaStream_t s) {
     // 16 warps to an SM: of one ring where there are no more rings than SMs
     const int warps = p.B * segs * tiles_of(p.C, p.G, kCh).all <= num_sms ? 16 : 8;
-    cudaError_t e;
-    if (p.N == 16) e = run_fwd<T, kCh, 16, kMode>(p, maps, sp, segs, warps, marks, err, s);
-    else e = run_fwd<T, kCh, 0, kMode>(p, maps, sp, segs, warps, marks, err, s);
-    if (e == cudaSuccess) count_launches(1);
-    return e;
+    if (p.N == 16) return run_fwd<T, kCh, 16, kMode>(p, maps, sp, segs, warps, marks, after, err, s);
+    return run_fwd<T, kCh, 0, kMode>(p, maps, sp, segs, warps, marks, after, err, s);
 }
-cudaError_t join(const SsmProblem &p, const Split &sp, bool back, cudaStream_t s) {
-    ssm_join_kernel<<<(unsigned)((p.B * p.C * p.N + 255) / 256), 256, 0, s>>>(p, sp, back);
-    const cudaError_t e = cudaGetLastError();
-    if (e == cudaSuccess) count_launches(1);
-    return e;
+cudaError_t join(const SsmProblem &p, const Split &sp, int directions, cudaStream_t s) {
+    return launch(ssm_join_kernel, dim3((unsigned)((p.C * p.N + 255) / 256), directions, (unsigned)p.B), 256, 0, true, s, p,
+                  sp);
 }
 
 template <typename T, int kCh, int kN, bool kEnd>
@@ -1240,17 +1258,14 @@ cudaError_t run_bwd(const SsmProblem &p, const Maps &maps, const Split &sp, cons
     const auto kernel = ssm_bwd_kernel<T, kCh, kN, kEnd>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    kernel<<<(unsigned)(p.B * sp.n * tiles_of(p.C, p.G, kCh).all), 32 * W, smem, s>>>(p, maps, sp, marks, parts, err);
-    return cudaGetLastError();
+    return launch(kernel, dim3((unsigned)(p.B * sp.n * tiles_of(p.C, p.G, kCh).all)), 32 * W, smem, true, s, p, maps, sp,
+                  marks, parts, err);
 }
 template <typename T, int kCh, bool kEnd>
 cudaError_t back(const SsmProblem &p, const Maps &maps, const Split &sp, const float4 *marks, const Parts &parts,
                  unsigned int *err, cudaStream_t s) {
-    cudaError_t e;
-    if (p.N == 16) e = run_bwd<T, kCh, 16, kEnd>(p, maps, sp, marks, parts, err, s);
-    else e = run_bwd<T, kCh, 0, kEnd>(p, maps, sp, marks, parts, err, s);
-    if (e == cudaSuccess) count_launches(1);
-    return e;
+    if (p.N == 16) return run_bwd<T, kCh, 16, kEnd>(p, maps, sp, marks, parts, err, s);
+    return run_bwd<T, kCh, 0, kEnd>(p, maps, sp, marks, parts, err, s);
 }
 
 template <typename T>
@@ -1265,10 +1280,12 @@ cudaError_t whole_fwd(SsmProblem p, int splits, int num_sms, void *ws, unsigned 
         at += copies;
         sp.h = reinterpret_cast<float *>(at);
         sp.sum = reinterpret_cast<float *>(at + split_state_bytes(p, sp));
-        e = fwd<T, 1, kEnds>(p, maps, sp, sp.n - 1, num_sms, nullptr, err, s);      // (nothing starts from the last one's end)
-        if (e == cudaSuccess) e = join(p, sp, false, s);
+        // (nothing starts from the last one's end)
+        e = fwd<T, 1, kEnds>(p, maps, sp, sp.n - 1, num_sms, nullptr, copies > 0, err, s);
+        if (e == cudaSuccess) e = join(p, sp, 1, s);
     }
-    return e == cudaSuccess ? fwd<T, 1, kOutputs>(p, maps, sp, sp.n, num_sms, nullptr, err, s) : e;
+    if (e != cudaSuccess) return e;
+    return fwd<T, 1, kOutputs>(p, maps, sp, sp.n, num_sms, nullptr, copies > 0 || sp.n > 1, err, s);
 }
 template <typename T, int kCh>
 cudaError_t whole_bwd(SsmProblem p, int splits, int num_sms, void *ws, unsigned int *err, cudaStream_t s) {
@@ -1287,20 +1304,16 @@ cudaError_t whole_bwd(SsmProblem p, int splits, int num_sms, void *ws, unsigned 
         sp.h = reinterpret_cast<float *>(at);
         sp.g = reinterpret_cast<float *>(at + split_state_bytes(p, sp));
         sp.sum = reinterpret_cast<float *>(at + 2 * split_state_bytes(p, sp));
-        e = fwd<T, kCh, kEnds>(p, maps, sp, sp.n, num_sms, nullptr, err, s);
+        e = fwd<T, kCh, kEnds>(p, maps, sp, sp.n, num_sms, nullptr, copies > 0, err, s);
         if (e == cudaSuccess) e = back<T, kCh, true>(p, maps, sp, nullptr, parts, err, s);
-        if (e == cudaSuccess) e = join(p, sp, false, s);
-        if (e == cudaSuccess) e = join(p, sp, true, s);
+        if (e == cudaSuccess) e = join(p, sp, 2, s);
     }
-    if (e == cudaSuccess) e = fwd<T, kCh, kMarks>(p, maps, sp, sp.n, num_sms, marks, err, s);
+    if (e == cudaSuccess) e = fwd<T, kCh, kMarks>(p, maps, sp, sp.n, num_sms, marks, copies > 0 || sp.n > 1, err, s);
     if (e == cudaSuccess) e = back<T, kCh, false>(p, maps, sp, marks, parts, err, s);
     if (e != cudaSuccess) return e;
     const int64_t rows = p.B * p.T * p.G * 2 * ((p.N + 3) / 4 * 4), chan = p.C * (p.N + 2);
-    ssm_rows_kernel<T><<<(unsigned)((rows + 255) / 256), 256, 0, s>>>(p, parts, tiles_of(p.C, p.G, kCh));
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    ssm_chan_kernel<<<(unsigned)((chan + 255) / 256), 256, 0, s>>>(p, parts, p.B * sp.n);
-    if ((e = cudaGetLastError()) == cudaSuccess) count_launches(2);
-    return e;
+    const unsigned row_ctas = (unsigned)((rows + 255) / 256), ctas = row_ctas + (unsigned)((chan + 255) / 256);
+    return launch(ssm_sums_kernel<T>, dim3(ctas), 256, 0, true, s, p, parts, tiles_of(p.C, p.G, kCh), sp.n, row_ctas);
 }
 
 }  // namespace
