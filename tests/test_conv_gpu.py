@@ -158,6 +158,37 @@ def test_gradient_against_differences():
         assert abs(got - want) <= 2e-5 * (g.cpu().double() * v).abs().sum().item() + 1e-6
 
 
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("C", [64, 19])
+def test_time_major_inputs(C, io):
+    d = make(3, 37, C, 4, io, seed=C)
+    for n in ("x", "dy"):
+        d[n] = d[n].transpose(0, 1).contiguous().transpose(0, 1)
+    check(d, "silu", io)
+
+
+def test_more_than_32_bits_of_elements():
+    from chunkwise_recurrent_prefill_gb300 import conv_bwd, conv_fwd, conv_step
+    T, C = (1 << 20) + 11, 2080
+    g = torch.Generator("cuda").manual_seed(1)
+    x = torch.empty(1, T, C, device="cuda", dtype=torch.bfloat16).normal_(generator=g)
+    w = torch.randn(C, 4, device="cuda", generator=g)
+    y = conv_fwd(x, w, act="silu")[0]
+    cut = T - 1000
+    s0 = x[:, cut - 3:cut].contiguous()
+    assert torch.equal(y[:, cut:], conv_fwd(x[:, cut:].contiguous(), w, None, s0, act="silu")[0])
+    dx = conv_bwd(y, x, w, act="silu")[0]
+    dx2 = conv_bwd(y[:, cut:].contiguous(), x[:, cut:].contiguous(), w, None, s0, act="silu")[0]
+    assert torch.equal(dx[:, cut:], dx2)
+    del x, y, dx
+    S = torch.empty(200000, 3, 4096, device="cuda", dtype=torch.bfloat16)
+    few = torch.randn(2, 3, 4096, device="cuda", generator=g).bfloat16()
+    S[199999], S[180000] = few[0], few[1]
+    x, w = torch.randn(2, 4096, device="cuda", generator=g).bfloat16(), torch.randn(4096, 4, device="cuda", generator=g)
+    y = conv_step(x, w, S, torch.tensor([199999, 180000], dtype=torch.int32, device="cuda"))
+    assert torch.equal(y, conv_step(x, w, few)) and torch.equal(S[199999], few[0]) and torch.equal(S[180000], few[1])
+
+
 def test_streams_and_graphs():
     """On a stream of its own, with the library's workspace and one of the caller's, and replayed."""
     from chunkwise_recurrent_prefill_gb300 import conv_bwd, conv_fwd, conv_step, conv_workspace_size

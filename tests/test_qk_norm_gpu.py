@@ -153,6 +153,36 @@ def test_gradient_against_differences():
         assert abs(terms.sum().item() - want) <= 2e-5 * terms.abs().sum().item() + 1e-6
 
 
+@pytest.mark.parametrize("D", [64, 20])
+def test_time_major_inputs(D):
+    """[T, B, heads, D], and [B, heads, T, D]."""
+    d = make(3, 17, 4, 2, D, D, seed=D)
+    for a, b in ((0, 1), (1, 2)):
+        for n in ("q", "k", "dqo", "dko"):
+            d[n] = d[n].transpose(a, b).contiguous().transpose(a, b)
+        check(d, "rms", "halves")
+
+
+def test_more_than_32_bits_of_elements():
+    from chunkwise_recurrent_prefill_gb300 import qk_norm_bwd, qk_norm_fwd
+    T = (1 << 20) + 11
+    g = torch.Generator("cuda").manual_seed(1)
+    q = torch.empty(1, T, 16, 136, device="cuda", dtype=torch.bfloat16).normal_(generator=g)
+    k = torch.randn(1, T, 1, 136, device="cuda", generator=g).bfloat16()
+    w, cut = torch.randn(136, device="cuda", generator=g), T - 1000
+    c = torch.randn(T, 32, device="cuda", generator=g)
+    pos = torch.arange(T, dtype=torch.int32, device="cuda")[None]
+    out = qk_norm_fwd(q, k, w, w, cos=c, sin=c, positions=pos)
+    last = [t[:, cut:].contiguous() for t in (q, k)]
+    out2 = qk_norm_fwd(*last, w, w, cos=c, sin=c, positions=pos[:, cut:].contiguous())
+    for a, b in zip(out, out2):
+        assert torch.equal(a[:, cut:], b)
+    rq, rk = out[2:]
+    dq = qk_norm_bwd(q, k, q, k, rq, rk, w, w, cos=c, sin=c, positions=pos)[0]
+    dq2 = qk_norm_bwd(*last, *last, out2[2], out2[3], w, w, cos=c, sin=c, positions=pos[:, cut:].contiguous())[0]
+    assert torch.equal(dq[:, cut:], dq2)
+
+
 def test_streams_and_graphs():
     from chunkwise_recurrent_prefill_gb300 import qk_norm_workspace_size
     d = {n: ref.gpu(v) for n, v in make(2, 100, 8, 2, 128, 128, "bf16", seed=9).items()}

@@ -106,6 +106,55 @@ def test_alignment(C, G, N, io):
             check({**d, n: rows[..., lo:lo + t.shape[2]].unflatten(-1, d[n].shape[2:])}, io)
 
 
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("C,N", [(64, 16), (19, 16)])
+def test_time_major_inputs(C, N, io):
+    """Tensors laid out [T, B, C], and batch entries whose distance is no multiple of a token's."""
+    d = make(3, 37, C, 1, N, io, seed=C)
+    for n in ("u", "dt", "z", "Bm", "Cm", "do"):
+        d[n] = d[n].transpose(0, 1).contiguous().transpose(0, 1)
+    check(d, io)
+    for n in ("u", "z", "Bm", "do"):
+        t = d[n]
+        w = t[0, 0].numel()
+        flat = torch.zeros(3 * (37 * w + 8), dtype=t.dtype)
+        v = flat.as_strided((3, 37, w), (37 * w + 8, w, 1))
+        v.copy_(t.flatten(2))
+        d[n] = v.unflatten(-1, t.shape[2:])
+    check(d, io)
+
+
+def test_more_than_32_bits_of_elements():
+    """Outputs and pages past 2^31 elements, against the same on their own."""
+    from chunkwise_recurrent_prefill_gb300 import last_device_status, ssm_fwd, ssm_step
+    T, C, N = (1 << 20) + 11, 2080, 8
+    g = torch.Generator("cuda").manual_seed(1)
+    u = torch.empty(1, T, C, device="cuda", dtype=torch.bfloat16).normal_(generator=g)
+    dt = torch.empty_like(u).normal_(generator=g)
+    Bm, Cm = (torch.randn(1, T, 1, N, device="cuda", generator=g).bfloat16() for _ in range(2))
+    A = -torch.rand(C, N, device="cuda", generator=g) - 0.5
+    o, hT = ssm_fwd(u, dt, A, Bm, Cm, return_state=True)
+    cut = T - 1000
+    part = [t[:, :cut] for t in (u, dt)] + [A] + [t[:, :cut] for t in (Bm, Cm)]
+    h = ssm_fwd(*part, return_state=True)[1]
+    part = [t[:, cut:].contiguous() for t in (u, dt)] + [A] + [t[:, cut:].contiguous() for t in (Bm, Cm)]
+    o2, h2 = ssm_fwd(*part, h0=h, return_state=True)
+    # the same operations in the same order, but for where a chunk ends
+    assert torch.allclose(o[:, cut:].float(), o2.float(), rtol=2.0 ** -7, atol=1e-4)
+    assert torch.allclose(hT, h2, rtol=1e-5, atol=1e-6)
+    del o, u, dt
+    S = torch.empty(40000, 4096, 16, device="cuda")
+    few = torch.randn(2, 4096, 16, device="cuda", generator=g)
+    S[39999], S[35000] = few[0], few[1]
+    x = torch.randn(2, 4096, device="cuda", generator=g)
+    b = torch.randn(2, 1, 16, device="cuda", generator=g)
+    A = -torch.rand(4096, 16, device="cuda", generator=g)
+    o = ssm_step(x, x, A, b, b, S, torch.tensor([39999, 35000], dtype=torch.int32, device="cuda"))
+    o2 = ssm_step(x, x, A, b, b, few)
+    assert torch.equal(o, o2) and torch.equal(S[39999], few[0]) and torch.equal(S[35000], few[1])
+    assert last_device_status() == 0
+
+
 def test_steps_of_zero_keep_the_state():
     """Bit for bit, whatever A is."""
     from chunkwise_recurrent_prefill_gb300 import ssm_fwd, ssm_step
