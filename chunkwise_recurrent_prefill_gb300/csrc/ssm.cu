@@ -943,7 +943,8 @@ ssm_sums_kernel(const __grid_constant__ SsmProblem p, const Parts parts, const T
 // One token of each row on the pages of a pool. kLanes lanes (4 kLanes >= N) own a channel, four states each, and keep
 // its row of A while they go through rows of the batch, kRows at a time: all that these need is on its way
 // together, and the page numbers of the next ones. A row's step size and output are made by one of the lanes. The
-// states are read and written once: HBM bandwidth bounds a batch. Measured: STEP_NOTE
+// states are read and written once: HBM bandwidth bounds a batch. Measured: 240 rows of 4096 channels of 16 states
+// (134 MB) 29 us a call, 4.6 TB/s; with the loads of a row behind those of the row before, 61.
 template <typename T, int kLanes>
 __global__ void __launch_bounds__(256, 3)
 ssm_step_kernel(const __grid_constant__ SsmProblem p, int vec, unsigned int *err) {
@@ -1098,7 +1099,7 @@ bool make_maps(const SsmProblem &p, int ch, Maps *m) {
 
 // TMA wants rows and tiles on 16 bytes. Inputs that are not (odd numbers of channels or states, slices that start
 // anywhere) are first copied to rows that are: a copy costs a fraction of what reading them element by
-// element did (16384 tokens of 3000 channels, B and C from an odd column on: 1190 us, PACK_NOTE with the copy).
+// element did (16384 tokens of 3000 channels, B and C from an odd column on: 1190 us, 554 with the copy).
 struct Packing {
     size_t bytes;               // of the copies
     bool copy[6];               // u, dt, z, go, B, C
@@ -1188,13 +1189,20 @@ int bwd_channels(const SsmProblem &p) {
 }
 
 // Segments of a sequence for CTAs of 32 ch channels. Cutting it costs two thirds of a walk more (and the join), so it is
-// done where the tiles leave almost half of the SMs idle; two CTAs to an SM then, of at least 8 chunks.
-// Measured: SPLIT_NOTE
+// done where the tiles leave more than half of the SMs idle; the segments then make one round of resident CTAs (two to
+// an SM forward, one backward), or two rounds if those are better filled. Measured, 16384 tokens: forward, 512
+// channels 104 us against 449 uncut, 2048 channels 368 against 450, 2560 channels 450 uncut against 473 at best;
+// gradients, 1024 channels 599 us against 3376, 4864 channels of 8192 tokens 1281 against 1733.
 Split split_of(const SsmProblem &p, int ch, bool backward, int splits, int num_sms) {
     const int64_t chunks = (p.T + kTok - 1) / kTok, ctas = p.B * tiles_of(p.C, p.G, ch).all;
+    const int64_t round = backward ? num_sms : 2 * num_sms, most = chunks / (backward ? 16 : 8);
     int64_t n = 1;
-    if (splits > 0) n = std::min({(int64_t)splits, chunks, std::max<int64_t>(1, (int64_t(1) << 30) / ctas)});
-    else if (9 * ctas <= 5 * num_sms) n = std::min<int64_t>((backward ? 1 : 2) * num_sms / ctas, chunks / (backward ? 16 : 8));
+    if (splits > 0) {
+        n = std::min({(int64_t)splits, chunks, std::max<int64_t>(1, (int64_t(1) << 30) / ctas)});
+    } else if (backward ? 2 * ctas <= num_sms : 9 * ctas <= 4 * num_sms) {
+        const int64_t one = round / ctas, two = 2 * round / ctas;
+        n = std::min(40 * two * ctas > 42 * 2 * one * ctas ? two : one, most);
+    }
     if (p.B > 65535 || p.C * p.N > int64_t(1) << 30) n = 1;        // (the join's grid and indices)
     Split sp{};
     sp.chunks = (chunks + std::max<int64_t>(n, 1) - 1) / std::max<int64_t>(n, 1);
