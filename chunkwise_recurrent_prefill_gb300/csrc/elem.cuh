@@ -60,26 +60,6 @@ struct Pack<__nv_bfloat16, 8> {
     }
 };
 template <>
-struct Pack<__nv_bfloat16, 2> {
-    using raw = uint32_t;
-    static __device__ __forceinline__ void unpack(raw v, float (&f)[2]) {
-        f[0] = __uint_as_float(v << 16);
-        f[1] = __uint_as_float(v & 0xffff0000u);
-    }
-    static __device__ __forceinline__ raw pack(const float (&f)[2]) { return tc::pack_bf16(f[0], f[1]); }
-};
-template <>
-struct Pack<float, 2> {
-    using raw = uint2;
-    static __device__ __forceinline__ void unpack(raw v, float (&f)[2]) {
-        f[0] = __uint_as_float(v.x);
-        f[1] = __uint_as_float(v.y);
-    }
-    static __device__ __forceinline__ raw pack(const float (&f)[2]) {
-        return make_uint2(__float_as_uint(f[0]), __float_as_uint(f[1]));
-    }
-};
-template <>
 struct Pack<__nv_bfloat16, 4> {
     using raw = uint2;
     static __device__ __forceinline__ void unpack(raw v, float (&f)[4]) {

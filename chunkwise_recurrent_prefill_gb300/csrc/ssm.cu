@@ -119,11 +119,13 @@ struct Link {
 };
 __device__ __forceinline__ float4 load4(uint32_t at) {
     float4 v;
-    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at) : "memory");
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(at) : "memory");
     return v;
 }
 __device__ __forceinline__ void store4(uint32_t at, const float (&v)[4]) {
-    asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]) : "memory");
+    asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3])
+                 : "memory");
 }
 __device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
     uint32_t ok;
@@ -268,8 +270,9 @@ struct Ring {
         A = slot + W * Q * 32;
         sums = A + Q * 2 * 32;
         turn = reinterpret_cast<float *>(sums + (backward ? W * Q * 32 : 0));
-        rows = reinterpret_cast<float2 *>(reinterpret_cast<unsigned char *>(turn) + (backward ? round(W * 32 * kTurn * 4) : 0));
-        bar = reinterpret_cast<uint64_t *>(reinterpret_cast<unsigned char *>(rows) + round((size_t)W * 2 * kPairs * padded(N) * 8));
+        unsigned char *after = reinterpret_cast<unsigned char *>(turn) + (backward ? round(W * 32 * kTurn * 4) : 0);
+        rows = reinterpret_cast<float2 *>(after);
+        bar = reinterpret_cast<uint64_t *>(after + round((size_t)W * 2 * kPairs * padded(N) * 8));
         full = bar + W * Q;
         stage = smem + stage_at(W, N, backward);
     }
@@ -512,7 +515,8 @@ ssm_fwd_kernel(const __grid_constant__ SsmProblem p, const __grid_constant__ Map
             const float4 v = load4(from.slot + 512 * q);
             float h[4] = {v.x, v.y, v.z, v.w};
             if (kMode == kMarks)
-                marks[(((at.b * chunks + ch) * tl.all + at.tile) * Q + q) * 32 + lane] = make_float4(h[0], h[1], h[2], h[3]);
+                marks[(((at.b * chunks + ch) * tl.all + at.tile) * Q + q) * 32 + lane] =
+                    make_float4(h[0], h[1], h[2], h[3]);
 #pragma unroll
             for (int ip = 0; ip < kPairs; ++ip)
 #pragma unroll
@@ -782,7 +786,8 @@ ssm_bwd_kernel(const __grid_constant__ SsmProblem p, const __grid_constant__ Map
                     __syncwarp();
                     float2 v = both(0.f);
 #pragma unroll
-                    for (int l = 0; l < 32; ++l) v = add2(v, *reinterpret_cast<const float2 *>(turn + l * kTurn + 2 * lane));
+                    for (int l = 0; l < 32; ++l)
+                        v = add2(v, *reinterpret_cast<const float2 *>(turn + l * kTurn + 2 * lane));
                     __syncwarp();
                     const int at_q = kCh == 2 ? q / 2 * 2 + lane / 16 : q;              // the step,
                     const int col = 2 * (kCh == 2 ? lane % 16 : lane);                  // [2][kSt][kTok]

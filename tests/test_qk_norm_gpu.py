@@ -202,3 +202,25 @@ def test_streams_and_graphs():
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("B,T,Hq,Hk,D,R", [
+    (3, 1700, 6, 2, 128, 128),      # several rounds of a warp, a batch entry ending inside of one
+    (4999, 1, 3, 5, 64, 32), (700, 7, 1, 9, 24, 16), (1, 5000, 40, 1, 8, 0),
+    (2, 700, 3, 2, 384, 384), (2, 300, 3, 2, 512, 128), (2, 40, 3, 2, 320, 320)])
+def test_many_tokens(B, T, Hq, Hk, D, R, io):
+    check(make(B, T, Hq, Hk, D, R, io, seed=D + 1), "rms", "halves")
+    check(make(B, T, Hq, Hk, D, R, io, seed=D + 2), "l2", "pairs")
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_heads_side_by_side(D):
+    """Queries and keys as parts of one projection's rows, heads before tokens in memory, one head of many."""
+    d = make(2, 1300, 4, 2, D, D, "bf16", seed=5)
+    g = torch.Generator().manual_seed(6)
+    both = ref.draw(g, 2, 1300, 8 * D, io="bf16")
+    d["q"], d["k"] = both[..., :4 * D].unflatten(-1, (4, D)), both[..., 5 * D:7 * D].unflatten(-1, (2, D))
+    d["dqo"] = d["dqo"].transpose(1, 2).contiguous().transpose(1, 2)
+    d["dko"] = ref.draw(g, 2, 1300, 9, D, io="bf16")[:, :, 3:5]
+    check(d, "rms", "halves")
