@@ -102,6 +102,8 @@ __device__ __forceinline__ float2 grad2(float2 a, int act) {
 template <typename T, int kV, int W, bool kSilu>
 __global__ void __launch_bounds__(kThreads)
 conv_fwd_kernel(const __grid_constant__ ConvProblem p, const ConvPlan pl) {
+    tc::pdl_launch_dependents();
+    tc::pdl_wait_prerequisites();
     // Tokens loaded at a time, while those before them are worked on: what is on its way bounds the rate (16 loads
     // of 8 bytes to a thread, 64 KB to an SM: 16384 x 4096 channels in 52 us, 5.2 TB/s; with 8 of them 59).
     constexpr int kBatch = kV * sizeof(T) > 8 ? 8 : 16;
@@ -160,6 +162,7 @@ template <typename T, int kV, int W, bool kSilu>
 __global__ void __launch_bounds__(kThreads, kBwdCtas)
 conv_bwd_kernel(const __grid_constant__ ConvProblem p, const ConvPlan pl, float *part) {
     tc::pdl_launch_dependents();
+    tc::pdl_wait_prerequisites();
     constexpr int kBatch = 4, kP = (kV + 1) / 2;
     using R = typename Pack<T, kV>::raw;
     __shared__ float sums[kThreads][kV];
@@ -290,11 +293,12 @@ conv_bwd_kernel(const __grid_constant__ ConvProblem p, const ConvPlan pl, float 
 // dw and dbias from the parts, added in their order.
 __global__ void __launch_bounds__(kThreads)
 conv_sums_kernel(const float *part, int64_t parts, int64_t C, int W, float *dw, float *db) {
+    tc::pdl_launch_dependents();
+    tc::pdl_wait_prerequisites();
     const int64_t id = (int64_t)blockIdx.x * kThreads + threadIdx.x;
     if (id >= C * (W + 1)) return;
     const int64_t j = id / C, c = id - j * C;
     float s = 0.f;
-    tc::pdl_wait_prerequisites();
 #pragma unroll 8
     for (int64_t i = 0; i < parts; ++i) s += part[(i * (W + 1) + j) * C + c];
     if (j < W) {
@@ -308,6 +312,8 @@ conv_sums_kernel(const float *part, int64_t parts, int64_t C, int W, float *dw, 
 template <typename T, int kV, int W>
 __global__ void __launch_bounds__(128)
 conv_step_kernel(const __grid_constant__ ConvProblem p, unsigned int *err) {
+    tc::pdl_launch_dependents();
+    tc::pdl_wait_prerequisites();
     using R = typename Pack<T, kV>::raw;
     const int64_t nv = p.C / kV, id = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
     const int64_t r = id / nv, c = (id - r * nv) * kV;
@@ -375,27 +381,23 @@ dim3 conv_grid(const ConvProblem &p, int v, const ConvPlan &pl) {
 
 // f.template run<T, kV, W>() for the problem's type, width and vectors.
 template <typename T, int kV, typename F>
-void by_width(int W, const F &f) {
+cudaError_t by_width(int W, const F &f) {
     switch (W) {
-        case 1: f.template run<T, kV, 1>(); break;
-        case 2: f.template run<T, kV, 2>(); break;
-        case 3: f.template run<T, kV, 3>(); break;
-        case 4: f.template run<T, kV, 4>(); break;
-        case 5: f.template run<T, kV, 5>(); break;
-        case 6: f.template run<T, kV, 6>(); break;
-        case 7: f.template run<T, kV, 7>(); break;
-        default: f.template run<T, kV, 8>(); break;
+        case 1: return f.template run<T, kV, 1>();
+        case 2: return f.template run<T, kV, 2>();
+        case 3: return f.template run<T, kV, 3>();
+        case 4: return f.template run<T, kV, 4>();
+        case 5: return f.template run<T, kV, 5>();
+        case 6: return f.template run<T, kV, 6>();
+        case 7: return f.template run<T, kV, 7>();
+        default: return f.template run<T, kV, 8>();
     }
 }
 template <int kBf16, int kF32, typename F>
-void dispatch(const ConvProblem &p, const F &f) {
-    if (p.io == 0) {
-        if (vectors(p, kBf16)) by_width<__nv_bfloat16, kBf16>(p.W, f);
-        else by_width<__nv_bfloat16, 1>(p.W, f);
-    } else {
-        if (vectors(p, kF32)) by_width<float, kF32>(p.W, f);
-        else by_width<float, 1>(p.W, f);
-    }
+cudaError_t dispatch(const ConvProblem &p, const F &f) {
+    if (p.io == 0)
+        return vectors(p, kBf16) ? by_width<__nv_bfloat16, kBf16>(p.W, f) : by_width<__nv_bfloat16, 1>(p.W, f);
+    return vectors(p, kF32) ? by_width<float, kF32>(p.W, f) : by_width<float, 1>(p.W, f);
 }
 
 struct Fwd {
@@ -403,14 +405,13 @@ struct Fwd {
     int sms;
     cudaStream_t s;
     template <typename T, int kV, int W, bool kSilu>
-    void go() const {
+    cudaError_t go() const {
         const ConvPlan pl = conv_plan(p, kV, sms, false);
-        conv_fwd_kernel<T, kV, W, kSilu><<<conv_grid(p, kV, pl), kThreads, 0, s>>>(p, pl);
+        return launch(conv_fwd_kernel<T, kV, W, kSilu>, conv_grid(p, kV, pl), kThreads, 0, s, p, pl);
     }
     template <typename T, int kV, int W>
-    void run() const {
-        if (p.act == 1) go<T, kV, W, true>();
-        else go<T, kV, W, false>();
+    cudaError_t run() const {
+        return p.act == 1 ? go<T, kV, W, true>() : go<T, kV, W, false>();
     }
 };
 struct Bwd {
@@ -420,16 +421,15 @@ struct Bwd {
     int64_t *parts;
     cudaStream_t s;
     template <typename T, int kV, int W, bool kSilu>
-    void go() const {
+    cudaError_t go() const {
         const ConvPlan pl = conv_plan(p, kV, sms, true);
         const dim3 grid = conv_grid(p, kV, pl);
         *parts = grid.x;
-        conv_bwd_kernel<T, kV, W, kSilu><<<grid, kThreads, 0, s>>>(p, pl, part);
+        return launch(conv_bwd_kernel<T, kV, W, kSilu>, grid, kThreads, 0, s, p, pl, part);
     }
     template <typename T, int kV, int W>
-    void run() const {
-        if (p.act == 1) go<T, kV, W, true>();
-        else go<T, kV, W, false>();
+    cudaError_t run() const {
+        return p.act == 1 ? go<T, kV, W, true>() : go<T, kV, W, false>();
     }
 };
 struct Step {
@@ -437,19 +437,16 @@ struct Step {
     unsigned int *err;
     cudaStream_t s;
     template <typename T, int kV, int W>
-    void run() const {
+    cudaError_t run() const {
         const int64_t n = p.B * (p.C / kV);
-        conv_step_kernel<T, kV, W><<<(unsigned)((n + 127) / 128), 128, 0, s>>>(p, err);
+        return launch(conv_step_kernel<T, kV, W>, dim3((unsigned)((n + 127) / 128)), 128, 0, s, p, err);
     }
 };
 
 }  // namespace
 
 cudaError_t launch_conv_fwd(const ConvProblem &p, int num_sms, cudaStream_t s) {
-    dispatch<4, 4>(p, Fwd{p, num_sms, s});
-    const cudaError_t e = cudaGetLastError();
-    if (e == cudaSuccess) count_launches(1);
-    return e;
+    return dispatch<4, 4>(p, Fwd{p, num_sms, s});
 }
 
 size_t conv_bwd_workspace_bytes(const ConvProblem &p, int num_sms) {
@@ -466,21 +463,15 @@ size_t conv_bwd_workspace_bytes(const ConvProblem &p, int num_sms) {
 cudaError_t launch_conv_bwd(const ConvProblem &p, void *ws, int num_sms, cudaStream_t s) {
     int64_t parts = 0;
     float *part = p.dw || p.dbias ? static_cast<float *>(ws) : nullptr;
-    dispatch<4, 4>(p, Bwd{p, num_sms, part, &parts, s});
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    count_launches(1);
-    if (!part) return e;
+    const cudaError_t e = dispatch<4, 4>(p, Bwd{p, num_sms, part, &parts, s});
+    if (e != cudaSuccess || !part) return e;
     const int64_t n = p.C * (p.W + 1);
-    return launch(conv_sums_kernel, dim3((unsigned)((n + kThreads - 1) / kThreads)), kThreads, 0, true, s, part, parts, p.C,
+    return launch(conv_sums_kernel, dim3((unsigned)((n + kThreads - 1) / kThreads)), kThreads, 0, s, part, parts, p.C,
                   p.W, p.dw, p.dbias);
 }
 
 cudaError_t launch_conv_step(const ConvProblem &p, unsigned int *dev_err, cudaStream_t s) {
-    dispatch<8, 4>(p, Step{p, dev_err, s});
-    const cudaError_t e = cudaGetLastError();
-    if (e == cudaSuccess) count_launches(1);
-    return e;
+    return dispatch<8, 4>(p, Step{p, dev_err, s});
 }
 
 }  // namespace gla

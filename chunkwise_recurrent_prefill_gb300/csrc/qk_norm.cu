@@ -62,6 +62,8 @@ __device__ __forceinline__ int64_t position(const QkProblem &p, const Row &r, un
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
 qk_plain_fwd(const __grid_constant__ QkProblem p, unsigned int *err) {
+    tc::pdl_launch_dependents();
+    tc::pdl_wait_prerequisites();
     const int lane = threadIdx.x % 32;
     const int64_t id = (int64_t)blockIdx.x * kWarps + threadIdx.x / 32;
     const Row r = row_of(p, id);
@@ -105,6 +107,7 @@ template <typename T>
 __global__ void __launch_bounds__(kThreads)
 qk_plain_bwd(const __grid_constant__ QkProblem p, float *part, unsigned int *err) {
     tc::pdl_launch_dependents();
+    tc::pdl_wait_prerequisites();
     extern __shared__ float sums[];         // [2][kWarps][D]
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     for (int i = threadIdx.x; i < 2 * kWarps * p.D; i += kThreads) sums[i] = 0.f;
@@ -373,6 +376,8 @@ template <typename T, int V, int kHeads, bool kPairs>
 __global__ void __launch_bounds__(kThreads, 2)
 qk_rows_fwd(const __grid_constant__ QkProblem p, const __grid_constant__ QkMaps maps, const QkPlan pl,
             unsigned int *err) {
+    tc::pdl_launch_dependents();
+    tc::pdl_wait_prerequisites();
     using R = typename Pack<T, V>::raw;
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ uint64_t bars[kWarps][kAhead];
@@ -451,6 +456,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 qk_rows_bwd(const __grid_constant__ QkProblem p, const __grid_constant__ QkMaps maps, const QkPlan pl, float *part,
             unsigned int *err) {
     tc::pdl_launch_dependents();
+    tc::pdl_wait_prerequisites();
     using R = typename Pack<T, V>::raw;
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ uint64_t bars[kWarps][kAhead];
@@ -547,10 +553,11 @@ struct QkSums {
 };
 __global__ void __launch_bounds__(1024)
 qk_sums_kernel(const __grid_constant__ QkProblem p, const __grid_constant__ QkSums q) {
+    tc::pdl_launch_dependents();
+    tc::pdl_wait_prerequisites();
     __shared__ float rows[32][33];
     const int which = blockIdx.y, col = threadIdx.x % 32, row = threadIdx.x / 32, i = blockIdx.x * 32 + col;
     float s = 0.f;
-    tc::pdl_wait_prerequisites();
     if (i < p.D) {
         const float *at = q.part[which] + i;
 #pragma unroll 8
@@ -652,7 +659,7 @@ bool make_maps(const QkProblem &p, const QkPlan &pl, QkMaps *m) {
 template <typename T>
 cudaError_t run_fwd(const QkProblem &in, int num_sms, unsigned int *err, cudaStream_t s) {
     if (!vectors(in))
-        return launch(qk_plain_fwd<T>, dim3((unsigned)((rows_of(in) + kWarps - 1) / kWarps)), kThreads, 0, false, s, in,
+        return launch(qk_plain_fwd<T>, dim3((unsigned)((rows_of(in) + kWarps - 1) / kWarps)), kThreads, 0, s, in,
                       err);
     const QkProblem p = joined(in);
     const QkPlan pl = plan_of(p, kFwdHeads);
@@ -663,7 +670,7 @@ cudaError_t run_fwd(const QkProblem &in, int num_sms, unsigned int *err, cudaStr
     const size_t smem = kWarps * Items<T, 1, kFwdHeads>::warp_bytes(p.D, pl.W);
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    return launch(kernel, dim3(item_ctas(p, pl, num_sms), pl.chunks[0] + pl.chunks[1]), kThreads, smem, false, s, p, maps,
+    return launch(kernel, dim3(item_ctas(p, pl, num_sms), pl.chunks[0] + pl.chunks[1]), kThreads, smem, s, p, maps,
                   pl, err);
 }
 
@@ -682,7 +689,7 @@ cudaError_t run_bwd(const QkProblem &in, float *part, int num_sms, unsigned int 
         const size_t smem = kWarps * Items<T, 2, kBwdHeads>::warp_bytes(p.D, pl.W);
         e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
-        e = launch(kernel, grid, kThreads, smem, false, s, p, maps, pl, part, err);
+        e = launch(kernel, grid, kThreads, smem, s, p, maps, pl, part, err);
         for (int i = 0; i < 2; ++i) {
             sums.part[i] = part + (i ? (size_t)pl.chunks[0] * grid.x * p.D : 0);
             sums.n[i] = (int64_t)pl.chunks[i] * grid.x;
@@ -693,7 +700,7 @@ cudaError_t run_bwd(const QkProblem &in, float *part, int num_sms, unsigned int 
         const size_t smem = 2 * kWarps * (size_t)p.D * sizeof(float);
         e = cudaFuncSetAttribute(qk_plain_bwd<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
-        e = launch(qk_plain_bwd<T>, dim3(parts), kThreads, smem, false, s, p, part, err);
+        e = launch(qk_plain_bwd<T>, dim3(parts), kThreads, smem, s, p, part, err);
         for (int i = 0; i < 2; ++i) {
             sums.part[i] = part + (i ? p.D : 0);
             sums.n[i] = parts;
@@ -701,7 +708,7 @@ cudaError_t run_bwd(const QkProblem &in, float *part, int num_sms, unsigned int 
         }
     }
     if (e != cudaSuccess || !part) return e;
-    return launch(qk_sums_kernel, dim3((p.D + 31) / 32, 2), 1024, 0, true, s, p, sums);
+    return launch(qk_sums_kernel, dim3((p.D + 31) / 32, 2), 1024, 0, s, p, sums);
 }
 
 }  // namespace

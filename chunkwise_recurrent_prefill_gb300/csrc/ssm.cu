@@ -889,6 +889,7 @@ __global__ void __launch_bounds__(256)
 ssm_join_kernel(const __grid_constant__ SsmProblem p, const Split sp) {
     constexpr int kAhead = 8;       // segments whose values are on their way together
     tc::pdl_launch_dependents();
+    tc::pdl_wait_prerequisites();
     const bool back = blockIdx.y == 1;
     const int cn = (int)(p.C * p.N), i = (int)(blockIdx.x * 256 + threadIdx.x);
     const int64_t b = blockIdx.z;
@@ -896,7 +897,6 @@ ssm_join_kernel(const __grid_constant__ SsmProblem p, const Split sp) {
     const float A = scale_a(p.A[i]), *from = back ? p.dhT : p.h0;
     float v = from ? from[b * cn + i] : 0.f, *x = (back ? sp.g : sp.h) + b * sp.n * cn + i;
     const float *sum = sp.sum + b * sp.n * p.C + i / p.N;
-    tc::pdl_wait_prerequisites();
     for (int k = 0; k < sp.n; k += kAhead) {
         float end[kAhead], a[kAhead];
 #pragma unroll
@@ -920,6 +920,8 @@ ssm_join_kernel(const __grid_constant__ SsmProblem p, const Split sp) {
 template <typename T>
 __global__ void __launch_bounds__(256)
 ssm_sums_kernel(const __grid_constant__ SsmProblem p, const Parts parts, const Tiles tl, int segs, unsigned row_ctas) {
+    tc::pdl_launch_dependents();
+    tc::pdl_wait_prerequisites();
     float s = 0.f;
     if (blockIdx.x < row_ctas) {
         const int NP = (p.N + 3) / 4 * 4, wide = 2 * NP;
@@ -928,7 +930,6 @@ ssm_sums_kernel(const __grid_constant__ SsmProblem p, const Parts parts, const T
         const int64_t row = k / p.G, g = k - row * p.G;
         if (row >= rows || n >= p.N) return;
         const float *at = parts.rows + (g * tl.per_group * rows + row) * wide + j;
-        tc::pdl_wait_prerequisites();
 #pragma unroll 8
         for (int i = 0; i < tl.per_group; ++i) s += at[i * rows * wide];
         put(static_cast<T *>(j < NP ? p.dBm : p.dCm) + (row * p.G + g) * p.N + n, s);
@@ -936,7 +937,6 @@ ssm_sums_kernel(const __grid_constant__ SsmProblem p, const Parts parts, const T
         const int64_t w = p.N + 2, id = (int64_t)(blockIdx.x - row_ctas) * 256 + threadIdx.x, c = id / w, n = id - c * w;
         if (c >= p.C) return;
         const float *at = parts.chan + id;
-        tc::pdl_wait_prerequisites();
 #pragma unroll 8
         for (int64_t b = 0; b < p.B * segs; ++b) s += at[b * p.C * w];
         if (n < p.N) p.dA[c * p.N + n] = s;
@@ -953,6 +953,8 @@ ssm_sums_kernel(const __grid_constant__ SsmProblem p, const Parts parts, const T
 template <typename T, int kLanes>
 __global__ void __launch_bounds__(256, 3)
 ssm_step_kernel(const __grid_constant__ SsmProblem p, int vec, unsigned int *err) {
+    tc::pdl_launch_dependents();
+    tc::pdl_wait_prerequisites();
     constexpr int kRows = 4, kOwn = kLanes < kRows ? kRows / kLanes : 1;     // rows of a lane: l, l + kLanes, ...
     using Raw = typename Pack<T, 4>::raw;
     const int l = threadIdx.x % kLanes, n0 = 4 * l;
@@ -1142,6 +1144,7 @@ template <typename T>
 __global__ void __launch_bounds__(256)
 ssm_pack_kernel(const __grid_constant__ PackJobs jobs) {
     tc::pdl_launch_dependents();
+    tc::pdl_wait_prerequisites();
     const PackJob &j = jobs.job[blockIdx.y];
     if (!j.to) return;
     T zero;
@@ -1180,7 +1183,7 @@ cudaError_t pack(SsmProblem *p, char *at, int num_sms, cudaStream_t s) {
     }
     if (!any) return cudaSuccess;
     const dim3 grid((unsigned)std::min<int64_t>((jobs.rows + 7) / 8, 8 * num_sms), 6);
-    return launch(p->io == 0 ? ssm_pack_kernel<__nv_bfloat16> : ssm_pack_kernel<float>, grid, 256, 0, false, s, jobs);
+    return launch(p->io == 0 ? ssm_pack_kernel<__nv_bfloat16> : ssm_pack_kernel<float>, grid, 256, 0, s, jobs);
 }
 
 // Channels of a lane in the backward pass: two share the loads of B and C and the sums across lanes (4 x 2047 tokens
@@ -1239,7 +1242,7 @@ BwdWorkspace bwd_workspace(const SsmProblem &p, const Split &sp) {
 }
 
 template <typename T, int kCh, int kN, int kMode>
-cudaError_t run_fwd(const SsmProblem &p, const Maps &maps, const Split &sp, int segs, int warps, float4 *marks, bool after,
+cudaError_t run_fwd(const SsmProblem &p, const Maps &maps, const Split &sp, int segs, int warps, float4 *marks,
                     unsigned int *err, cudaStream_t s) {
     constexpr int in = kMode == kOutputs ? 3 : 2;
     const int W = (int)std::min<int64_t>(ring_warps<T, kCh>(p, in, false, warps), sp.chunks);
@@ -1247,19 +1250,19 @@ cudaError_t run_fwd(const SsmProblem &p, const Maps &maps, const Split &sp, int 
     const auto kernel = ssm_fwd_kernel<T, kCh, kN, kMode>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    return launch(kernel, dim3((unsigned)(p.B * segs * tiles_of(p.C, p.G, kCh).all)), 32 * W, smem, after, s, p, maps, sp,
+    return launch(kernel, dim3((unsigned)(p.B * segs * tiles_of(p.C, p.G, kCh).all)), 32 * W, smem, s, p, maps, sp,
                   segs, marks, err);
 }
 template <typename T, int kCh, int kMode>
-cudaError_t fwd(const SsmProblem &p, const Maps &maps, const Split &sp, int segs, int num_sms, float4 *marks, bool after,
+cudaError_t fwd(const SsmProblem &p, const Maps &maps, const Split &sp, int segs, int num_sms, float4 *marks,
                 unsigned int *err, cudaStream_t s) {
     // 16 warps to an SM: of one ring where there are no more rings than SMs
     const int warps = p.B * segs * tiles_of(p.C, p.G, kCh).all <= num_sms ? 16 : 8;
-    if (p.N == 16) return run_fwd<T, kCh, 16, kMode>(p, maps, sp, segs, warps, marks, after, err, s);
-    return run_fwd<T, kCh, 0, kMode>(p, maps, sp, segs, warps, marks, after, err, s);
+    if (p.N == 16) return run_fwd<T, kCh, 16, kMode>(p, maps, sp, segs, warps, marks, err, s);
+    return run_fwd<T, kCh, 0, kMode>(p, maps, sp, segs, warps, marks, err, s);
 }
 cudaError_t join(const SsmProblem &p, const Split &sp, int directions, cudaStream_t s) {
-    return launch(ssm_join_kernel, dim3((unsigned)((p.C * p.N + 255) / 256), directions, (unsigned)p.B), 256, 0, true, s, p,
+    return launch(ssm_join_kernel, dim3((unsigned)((p.C * p.N + 255) / 256), directions, (unsigned)p.B), 256, 0, s, p,
                   sp);
 }
 
@@ -1271,7 +1274,7 @@ cudaError_t run_bwd(const SsmProblem &p, const Maps &maps, const Split &sp, cons
     const auto kernel = ssm_bwd_kernel<T, kCh, kN, kEnd>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    return launch(kernel, dim3((unsigned)(p.B * sp.n * tiles_of(p.C, p.G, kCh).all)), 32 * W, smem, true, s, p, maps, sp,
+    return launch(kernel, dim3((unsigned)(p.B * sp.n * tiles_of(p.C, p.G, kCh).all)), 32 * W, smem, s, p, maps, sp,
                   marks, parts, err);
 }
 template <typename T, int kCh, bool kEnd>
@@ -1294,11 +1297,11 @@ cudaError_t whole_fwd(SsmProblem p, int splits, int num_sms, void *ws, unsigned 
         sp.h = reinterpret_cast<float *>(at);
         sp.sum = reinterpret_cast<float *>(at + split_state_bytes(p, sp));
         // (nothing starts from the last one's end)
-        e = fwd<T, 1, kEnds>(p, maps, sp, sp.n - 1, num_sms, nullptr, copies > 0, err, s);
+        e = fwd<T, 1, kEnds>(p, maps, sp, sp.n - 1, num_sms, nullptr, err, s);
         if (e == cudaSuccess) e = join(p, sp, 1, s);
     }
     if (e != cudaSuccess) return e;
-    return fwd<T, 1, kOutputs>(p, maps, sp, sp.n, num_sms, nullptr, copies > 0 || sp.n > 1, err, s);
+    return fwd<T, 1, kOutputs>(p, maps, sp, sp.n, num_sms, nullptr, err, s);
 }
 template <typename T, int kCh>
 cudaError_t whole_bwd(SsmProblem p, int splits, int num_sms, void *ws, unsigned int *err, cudaStream_t s) {
@@ -1317,16 +1320,16 @@ cudaError_t whole_bwd(SsmProblem p, int splits, int num_sms, void *ws, unsigned 
         sp.h = reinterpret_cast<float *>(at);
         sp.g = reinterpret_cast<float *>(at + split_state_bytes(p, sp));
         sp.sum = reinterpret_cast<float *>(at + 2 * split_state_bytes(p, sp));
-        e = fwd<T, kCh, kEnds>(p, maps, sp, sp.n, num_sms, nullptr, copies > 0, err, s);
+        e = fwd<T, kCh, kEnds>(p, maps, sp, sp.n, num_sms, nullptr, err, s);
         if (e == cudaSuccess) e = back<T, kCh, true>(p, maps, sp, nullptr, parts, err, s);
         if (e == cudaSuccess) e = join(p, sp, 2, s);
     }
-    if (e == cudaSuccess) e = fwd<T, kCh, kMarks>(p, maps, sp, sp.n, num_sms, marks, copies > 0 || sp.n > 1, err, s);
+    if (e == cudaSuccess) e = fwd<T, kCh, kMarks>(p, maps, sp, sp.n, num_sms, marks, err, s);
     if (e == cudaSuccess) e = back<T, kCh, false>(p, maps, sp, marks, parts, err, s);
     if (e != cudaSuccess) return e;
     const int64_t rows = p.B * p.T * p.G * 2 * ((p.N + 3) / 4 * 4), chan = p.C * (p.N + 2);
     const unsigned row_ctas = (unsigned)((rows + 255) / 256), ctas = row_ctas + (unsigned)((chan + 255) / 256);
-    return launch(ssm_sums_kernel<T>, dim3(ctas), 256, 0, true, s, p, parts, tiles_of(p.C, p.G, kCh), sp.n, row_ctas);
+    return launch(ssm_sums_kernel<T>, dim3(ctas), 256, 0, s, p, parts, tiles_of(p.C, p.G, kCh), sp.n, row_ctas);
 }
 
 }  // namespace
@@ -1353,30 +1356,26 @@ cudaError_t launch_ssm_bwd(const SsmProblem &p, int splits, int num_sms, void *w
 }
 
 template <typename T, int kLanes>
-static void run_step(const SsmProblem &p, int num_sms, unsigned int *err, cudaStream_t s) {
+static cudaError_t run_step(const SsmProblem &p, int num_sms, unsigned int *err, cudaStream_t s) {
     const int64_t tiles = (p.C * kLanes + 255) / 256, rows = (p.B + 3) / 4;
     // two rounds of resident CTAs, each with as many rows of its channels as that leaves
     const dim3 grid((unsigned)tiles, (unsigned)std::min<int64_t>(rows, std::max<int64_t>(1, 6 * num_sms / tiles)));
     const int vec = p.N % 4 == 0 && p.Bm.b % 4 == 0 && p.Cm.b % 4 == 0 &&
                     (reinterpret_cast<uintptr_t>(p.Bm.p) | reinterpret_cast<uintptr_t>(p.Cm.p)) % (4 * sizeof(T)) == 0;
-    ssm_step_kernel<T, kLanes><<<grid, 256, 0, s>>>(p, vec, err);
+    return launch(ssm_step_kernel<T, kLanes>, grid, 256, 0, s, p, vec, err);
 }
 template <typename T>
-static void step_of(const SsmProblem &p, int num_sms, unsigned int *err, cudaStream_t s) {
-    if (p.N <= 4) run_step<T, 1>(p, num_sms, err, s);
-    else if (p.N <= 8) run_step<T, 2>(p, num_sms, err, s);
-    else if (p.N <= 16) run_step<T, 4>(p, num_sms, err, s);
-    else if (p.N <= 32) run_step<T, 8>(p, num_sms, err, s);
-    else if (p.N <= 64) run_step<T, 16>(p, num_sms, err, s);
-    else run_step<T, 32>(p, num_sms, err, s);
+static cudaError_t step_of(const SsmProblem &p, int num_sms, unsigned int *err, cudaStream_t s) {
+    if (p.N <= 4) return run_step<T, 1>(p, num_sms, err, s);
+    if (p.N <= 8) return run_step<T, 2>(p, num_sms, err, s);
+    if (p.N <= 16) return run_step<T, 4>(p, num_sms, err, s);
+    if (p.N <= 32) return run_step<T, 8>(p, num_sms, err, s);
+    if (p.N <= 64) return run_step<T, 16>(p, num_sms, err, s);
+    return run_step<T, 32>(p, num_sms, err, s);
 }
 
 cudaError_t launch_ssm_step(const SsmProblem &p, int num_sms, unsigned int *dev_err, cudaStream_t s) {
-    if (p.io == 0) step_of<__nv_bfloat16>(p, num_sms, dev_err, s);
-    else step_of<float>(p, num_sms, dev_err, s);
-    const cudaError_t e = cudaGetLastError();
-    if (e == cudaSuccess) count_launches(1);
-    return e;
+    return p.io == 0 ? step_of<__nv_bfloat16>(p, num_sms, dev_err, s) : step_of<float>(p, num_sms, dev_err, s);
 }
 
 }  // namespace gla

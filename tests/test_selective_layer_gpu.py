@@ -203,3 +203,71 @@ def test_two_graphs_at_once():
         torch.cuda.synchronize()
         for got, want in zip(outs, wants):
             assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def _chain(x, wait, d):
+    """Each call reads what the one before it wrote, into memory that others have just given back."""
+    from chunkwise_recurrent_prefill_gb300 import conv_bwd, conv_fwd, hda_fwd, qk_norm_bwd, qk_norm_fwd, ssm_bwd, ssm_fwd
+    for _ in range(3):
+        y = wait(conv_fwd(x, d["w"], act="silu"))[0]
+        o = wait(ssm_fwd(y, d["dt"], d["A"], d["B"], d["C"]))[0]
+        q = o.unflatten(-1, (4, 64))
+        qo, ko, rq, rk = wait(qk_norm_fwd(q, q[:, :, :2], d["wq"], None, cos=d["cos"], sin=d["sin"]))
+        a = wait(hda_fwd(qo, ko, q, d["decay"], 0.1))[0]
+        dq, _, dw, _ = wait(qk_norm_bwd(a, ko, q, q[:, :, :2], rq, rk, d["wq"], None, cos=d["cos"], sin=d["sin"]))
+        g = wait(ssm_bwd(dq.flatten(2), y, d["dt"], d["A"], d["B"], d["C"]))
+        dx, dcw = wait(conv_bwd(g[0], x, d["w"], act="silu"))[:2]
+        x = wait((x + dx * 0.1,))[0]
+    return x, a, dw, dcw, g[2], g[3]
+
+
+def _chain_inputs(T=3000):
+    g = torch.Generator().manual_seed(7)
+    r = lambda *s: ref.gpu(ref.draw(g, *s, io="bf16"))      # noqa: E731
+    f = lambda *s: ref.gpu(ref.draw(g, *s))                 # noqa: E731
+    ang = torch.arange(T)[:, None] * 0.01 * torch.arange(32)
+    return r(2, T, 256), dict(w=f(256, 4), dt=r(2, T, 256).abs() * 0.1, A=-f(256, 16).abs(), B=r(2, T, 1, 16), C=r(2, T, 1, 16),
+                              wq=f(64), cos=ref.gpu(torch.cos(ang)), sin=ref.gpu(torch.sin(ang)), decay=-f(4).abs() * 0.1)
+
+
+def test_calls_behind_each_other():
+    """Kernels are scheduled before those ahead of them in the stream are done: nothing may be read or written early."""
+    x, d = _chain_inputs()
+
+    def sync(r):
+        torch.cuda.synchronize()
+        return r
+
+    want = _chain(x, sync, d)
+    for _ in range(10):
+        assert all(torch.equal(a, b) for a, b in zip(_chain(x, lambda r: r, d), want))
+
+
+def test_a_capture_of_two_streams():
+    """A capture that forks and joins: the kernel behind the join waits for both."""
+    from chunkwise_recurrent_prefill_gb300 import conv_fwd, qk_norm_fwd, ssm_fwd
+    x, d = _chain_inputs(1000)
+
+    def run(main, other):
+        y, _ = conv_fwd(x, d["w"], act="silu")
+        other.wait_stream(main)
+        with torch.cuda.stream(other):
+            dt = conv_fwd(d["dt"], d["w"].abs() * 0.1)[0].abs()
+            q = qk_norm_fwd(x.unflatten(-1, (4, 64)), y.unflatten(-1, (4, 64)))[1].flatten(2)
+        z = conv_fwd(y, d["w"])[0]
+        main.wait_stream(other)
+        return ssm_fwd(q, dt, d["A"], d["B"], d["C"], z=z)[0]
+
+    other = torch.cuda.Stream()
+    want = run(torch.cuda.current_stream(), other)
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.stream(side):
+        run(side, other)                # (its workspace; a call that is captured makes none)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        got = run(side, other)
+    for _ in range(10):
+        got.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
