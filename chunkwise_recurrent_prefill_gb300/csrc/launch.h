@@ -3,6 +3,8 @@
 
 #include <cuda_runtime.h>
 
+#include <atomic>
+
 #include "gla_internal.h"
 
 namespace gla {
@@ -25,6 +27,25 @@ cudaError_t launch(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cu
     cfg.numAttrs = 1;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, P(args)...);
     if (e == cudaSuccess) count_launches(1);
+    return e;
+}
+
+// Lets a kernel have all of a CTA's shared memory, once for each device. (Not what a call needs: another thread's call of
+// the kernel could set a lower limit before the launch.)
+template <auto kKernel>
+cudaError_t allow_shared() {
+    static std::atomic<uint64_t> done{0};
+    int dev = 0, most = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+    if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+    cudaFuncAttributes attr{};
+    e = cudaFuncGetAttributes(&attr, kKernel);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most - (int)attr.sharedSizeBytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
     return e;
 }
 

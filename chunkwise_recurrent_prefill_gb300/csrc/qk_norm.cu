@@ -656,59 +656,67 @@ bool make_maps(const QkProblem &p, const QkPlan &pl, QkMaps *m) {
     return true;
 }
 
+template <typename T, bool kPairs>
+cudaError_t rows_fwd(const QkProblem &p, int num_sms, unsigned int *err, cudaStream_t s) {
+    constexpr auto kernel = qk_rows_fwd<T, 16 / sizeof(T), kFwdHeads, kPairs>;
+    const QkPlan pl = plan_of(p, kFwdHeads);
+    QkMaps maps;
+    if (!make_maps(p, pl, &maps)) return cudaErrorInvalidResourceHandle;
+    const size_t smem = kWarps * Items<T, 1, kFwdHeads>::warp_bytes(p.D, pl.W);
+    const cudaError_t e = allow_shared<kernel>();
+    if (e != cudaSuccess) return e;
+    return launch(kernel, dim3(item_ctas(p, pl, num_sms), pl.chunks[0] + pl.chunks[1]), kThreads, smem, s, p, maps, pl,
+                  err);
+}
+template <typename T, bool kPairs>
+cudaError_t rows_bwd(const QkProblem &p, float *part, int num_sms, unsigned int *err, cudaStream_t s, QkSums *sums) {
+    constexpr auto kernel = qk_rows_bwd<T, 16 / sizeof(T), kBwdHeads, kPairs>;
+    const QkPlan pl = plan_of(p, kBwdHeads);
+    QkMaps maps;
+    if (!make_maps(p, pl, &maps)) return cudaErrorInvalidResourceHandle;
+    const dim3 grid(item_ctas(p, pl, num_sms), pl.chunks[0] + pl.chunks[1]);
+    const size_t smem = kWarps * Items<T, 2, kBwdHeads>::warp_bytes(p.D, pl.W);
+    for (int i = 0; i < 2; ++i) {
+        sums->part[i] = part + (i ? (size_t)pl.chunks[0] * grid.x * p.D : 0);
+        sums->n[i] = (int64_t)pl.chunks[i] * grid.x;
+        sums->stride[i] = p.D;
+    }
+    const cudaError_t e = allow_shared<kernel>();
+    if (e != cudaSuccess) return e;
+    return launch(kernel, grid, kThreads, smem, s, p, maps, pl, part, err);
+}
+
 template <typename T>
 cudaError_t run_fwd(const QkProblem &in, int num_sms, unsigned int *err, cudaStream_t s) {
     if (!vectors(in))
         return launch(qk_plain_fwd<T>, dim3((unsigned)((rows_of(in) + kWarps - 1) / kWarps)), kThreads, 0, s, in,
                       err);
     const QkProblem p = joined(in);
-    const QkPlan pl = plan_of(p, kFwdHeads);
-    QkMaps maps;
-    if (!make_maps(p, pl, &maps)) return cudaErrorInvalidResourceHandle;
-    const auto kernel =
-        p.pairs ? qk_rows_fwd<T, 16 / sizeof(T), kFwdHeads, true> : qk_rows_fwd<T, 16 / sizeof(T), kFwdHeads, false>;
-    const size_t smem = kWarps * Items<T, 1, kFwdHeads>::warp_bytes(p.D, pl.W);
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-    return launch(kernel, dim3(item_ctas(p, pl, num_sms), pl.chunks[0] + pl.chunks[1]), kThreads, smem, s, p, maps,
-                  pl, err);
+    return p.pairs ? rows_fwd<T, true>(p, num_sms, err, s) : rows_fwd<T, false>(p, num_sms, err, s);
 }
 
 template <typename T>
 cudaError_t run_bwd(const QkProblem &in, float *part, int num_sms, unsigned int *err, cudaStream_t s) {
-    const QkProblem p = vectors(in) ? joined(in) : in;
     QkSums sums{};
     cudaError_t e;
     if (vectors(in)) {
-        const QkPlan pl = plan_of(p, kBwdHeads);
-        QkMaps maps;
-        if (!make_maps(p, pl, &maps)) return cudaErrorInvalidResourceHandle;
-        const dim3 grid(item_ctas(p, pl, num_sms), pl.chunks[0] + pl.chunks[1]);
-        const auto kernel =
-            p.pairs ? qk_rows_bwd<T, 16 / sizeof(T), kBwdHeads, true> : qk_rows_bwd<T, 16 / sizeof(T), kBwdHeads, false>;
-        const size_t smem = kWarps * Items<T, 2, kBwdHeads>::warp_bytes(p.D, pl.W);
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
-        e = launch(kernel, grid, kThreads, smem, s, p, maps, pl, part, err);
-        for (int i = 0; i < 2; ++i) {
-            sums.part[i] = part + (i ? (size_t)pl.chunks[0] * grid.x * p.D : 0);
-            sums.n[i] = (int64_t)pl.chunks[i] * grid.x;
-            sums.stride[i] = p.D;
-        }
+        const QkProblem p = joined(in);
+        e = p.pairs ? rows_bwd<T, true>(p, part, num_sms, err, s, &sums) : rows_bwd<T, false>(p, part, num_sms, err, s, &sums);
     } else {
-        const int parts = bwd_parts(p, num_sms);
-        const size_t smem = 2 * kWarps * (size_t)p.D * sizeof(float);
-        e = cudaFuncSetAttribute(qk_plain_bwd<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
-        e = launch(qk_plain_bwd<T>, dim3(parts), kThreads, smem, s, p, part, err);
+        constexpr auto kernel = qk_plain_bwd<T>;
+        const int parts = bwd_parts(in, num_sms);
+        const size_t smem = 2 * kWarps * (size_t)in.D * sizeof(float);
         for (int i = 0; i < 2; ++i) {
-            sums.part[i] = part + (i ? p.D : 0);
+            sums.part[i] = part + (i ? in.D : 0);
             sums.n[i] = parts;
-            sums.stride[i] = 2 * p.D;
+            sums.stride[i] = 2 * in.D;
         }
+        e = allow_shared<kernel>();
+        if (e != cudaSuccess) return e;
+        e = launch(kernel, dim3(parts), kThreads, smem, s, in, part, err);
     }
     if (e != cudaSuccess || !part) return e;
-    return launch(qk_sums_kernel, dim3((p.D + 31) / 32, 2), 1024, 0, s, p, sums);
+    return launch(qk_sums_kernel, dim3((in.D + 31) / 32, 2), 1024, 0, s, in, sums);
 }
 
 }  // namespace

@@ -1247,8 +1247,8 @@ cudaError_t run_fwd(const SsmProblem &p, const Maps &maps, const Split &sp, int 
     constexpr int in = kMode == kOutputs ? 3 : 2;
     const int W = (int)std::min<int64_t>(ring_warps<T, kCh>(p, in, false, warps), sp.chunks);
     const size_t smem = Ring<T, kCh>::bytes(W, in, p.N, p.row, false);
-    const auto kernel = ssm_fwd_kernel<T, kCh, kN, kMode>;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    constexpr auto kernel = ssm_fwd_kernel<T, kCh, kN, kMode>;
+    const cudaError_t e = allow_shared<kernel>();
     if (e != cudaSuccess) return e;
     return launch(kernel, dim3((unsigned)(p.B * segs * tiles_of(p.C, p.G, kCh).all)), 32 * W, smem, s, p, maps, sp,
                   segs, marks, err);
@@ -1271,8 +1271,8 @@ cudaError_t run_bwd(const SsmProblem &p, const Maps &maps, const Split &sp, cons
                     unsigned int *err, cudaStream_t s) {
     const int W = (int)std::min<int64_t>(ring_warps<T, kCh>(p, 4, true, kCh == 2 ? 8 : 12), sp.chunks);
     const size_t smem = Ring<T, kCh>::bytes(W, 4, p.N, p.row, true);
-    const auto kernel = ssm_bwd_kernel<T, kCh, kN, kEnd>;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    constexpr auto kernel = ssm_bwd_kernel<T, kCh, kN, kEnd>;
+    const cudaError_t e = allow_shared<kernel>();
     if (e != cudaSuccess) return e;
     return launch(kernel, dim3((unsigned)(p.B * sp.n * tiles_of(p.C, p.G, kCh).all)), 32 * W, smem, s, p, maps, sp,
                   marks, parts, err);

@@ -271,3 +271,42 @@ def test_a_capture_of_two_streams():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(got, want)
+
+
+def test_calls_of_two_threads():
+    """Calls of one kernel that need different amounts of shared memory, from threads with a stream each."""
+    import threading
+    from chunkwise_recurrent_prefill_gb300 import qk_norm_bwd, qk_norm_fwd, ssm_bwd, ssm_fwd
+    g = torch.Generator().manual_seed(9)
+    f = lambda *s: ref.gpu(ref.draw(g, *s))                 # noqa: E731
+
+    def inputs(T, N, D):
+        return dict(u=f(1, T, 64), dt=f(1, T, 64), A=-f(64, N).abs(), B=f(1, T, 1, N), C=f(1, T, 1, N), q=f(1, T, 2, D), w=f(D))
+
+    def run(d):
+        o = ssm_fwd(d["u"], d["dt"], d["A"], d["B"], d["C"])[0]
+        du = ssm_bwd(o, d["u"], d["dt"], d["A"], d["B"], d["C"])[:5]
+        qo, ko, rq, rk = qk_norm_fwd(d["q"], d["q"], d["w"], d["w"])
+        return (o, *du, qo, *qk_norm_bwd(qo, ko, d["q"], d["q"], rq, rk, d["w"], d["w"]))
+
+    sets = [inputs(9, 20, 24), inputs(300, 128, 300), inputs(40, 40, 999)]
+    wants = [run(d) for d in sets]
+    torch.cuda.synchronize()
+    failed = []
+
+    def work(d, want):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(100):
+                    got = run(d)
+                torch.cuda.current_stream().synchronize()
+                assert all(torch.equal(a, b) for a, b in zip(got, want))
+        except Exception as e:      # noqa: BLE001 (reported by the test's own thread)
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=a) for a in zip(sets, wants)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed
