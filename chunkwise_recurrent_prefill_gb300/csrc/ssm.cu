@@ -106,10 +106,28 @@ __device__ __forceinline__ void widen_rows(const T *from, float2 *to, int N, int
             t[1] = make_float4(x[2], y[2], x[3], y[3]);
         }
     } else {
-        for (int k = lane; k < kTok * NP; k += 32) {
-            const int i = k / NP, n = k - i * NP;
-            to[k] = n < N ? make_float2(get(from + 2 * i * row + n), get(from + (2 * i + 1) * row + n)) : both(0.f);
+        for (int n = lane; n < NP; n += 32)
+#pragma unroll
+            for (int i = 0; i < kTok; ++i)      // (pairs of tokens of B, then of C)
+                to[i * NP + n] = n < N ? make_float2(get(from + 2 * i * row + n), get(from + (2 * i + 1) * row + n)) : both(0.f);
+    }
+}
+
+// The same for the forward walk, as they are: from[2][kTok][row] -> to[2][kTok][NP] floats.
+template <typename T, int kN>
+__device__ __forceinline__ void widen_tokens(const T *from, float *to, int N, int row) {
+    const int lane = threadIdx.x % 32, NP = (N + 3) / 4 * 4;
+    if (kN > 0 || row == NP) {          // (what is past N in a row is zero)
+#pragma unroll
+        for (int k = lane; k < 2 * kTok * (kN > 0 ? kN : NP) / 4; k += 32) {
+            float x[4];
+            Pack<T, 4>::unpack(*reinterpret_cast<const typename Pack<T, 4>::raw *>(from + 4 * k), x);
+            *reinterpret_cast<float4 *>(to + 4 * k) = make_float4(x[0], x[1], x[2], x[3]);
         }
+    } else {
+        for (int n = lane; n < NP; n += 32)
+#pragma unroll
+            for (int i = 0; i < 2 * kTok; ++i) to[i * NP + n] = n < N ? get(from + i * row + n) : 0.f;
     }
 }
 
@@ -236,9 +254,9 @@ __device__ __forceinline__ void store_states(float *to, int64_t row, const SsmPr
 
 // A lane works on kSt = 4 / kCh states of its channels at a time, Q = N / kSt times. Shared memory of a
 // ring of W warps:
-//   slot[W][Q][32] float4: what a warp hands on, [kCh][kSt];  A[Q][2][32] float4: A log2 e, twice each
+//   slot[W][Q][32] float4: what a warp hands on, [kCh][kSt];  A[Q][32] float4: A log2 e (backward [Q][2][32]: twice each)
 //   sums[W][Q][32] float4 (backward): dA;  turn[W][32][kTurn] float (backward): sums across lanes
-//   rows[W][2][kPairs][NP] float2: B and C of a warp's chunk;  bar[W][Q]
+//   rows[W][2][kPairs][NP] float2: B and C of a warp's chunk (forward [W][2][kTok][NP] float);  bar[W][Q]
 //   stage[W][2]: a chunk as it lies in memory, on its way while the one before it is worked on:
 //     kIn tensors [kTok][32 kCh], then B and C [kTok][row];  full[W][2]: it is there
 //   dx[W][kPairs][kCh][32] float4 (forward): d and d u of a warp's chunk
@@ -258,7 +276,7 @@ struct Ring {
     static __host__ __device__ size_t round(size_t n) { return (n + 127) / 128 * 128; }
     static __host__ __device__ size_t stage_at(int W, int N, bool backward) {
         const size_t Q = steps(N);
-        return W * Q * 32 * 16 * (backward ? 2 : 1) + Q * 2 * 32 * 16 + (backward ? round(W * 32 * kTurn * 4) : 0) +
+        return W * Q * 32 * 16 * (backward ? 2 : 1) + Q * (backward ? 2 : 1) * 32 * 16 + (backward ? round(W * 32 * kTurn * 4) : 0) +
                round((size_t)W * 2 * kPairs * padded(N) * 8) + round(W * (Q + 2) * 8);
     }
     static __host__ __device__ size_t bytes(int W, int in, int N, int row, bool backward) {
@@ -268,7 +286,7 @@ struct Ring {
         const int Q = steps(N);
         slot = reinterpret_cast<float4 *>(smem);
         A = slot + W * Q * 32;
-        sums = A + Q * 2 * 32;
+        sums = A + Q * (backward ? 2 : 1) * 32;
         turn = reinterpret_cast<float *>(sums + (backward ? W * Q * 32 : 0));
         unsigned char *after = reinterpret_cast<unsigned char *>(turn) + (backward ? round(W * 32 * kTurn * 4) : 0);
         rows = reinterpret_cast<float2 *>(after);
@@ -277,6 +295,7 @@ struct Ring {
         stage = smem + stage_at(W, N, backward);
     }
     // A, the barriers, and the states that the first chunk takes over, as if from the last warp; the CTA synchronises.
+    template <bool kBack>
     __device__ void begin(const SsmProblem &p, const Place<kCh> &at, int W, int N, const float *first, int64_t row) {
         constexpr int kSt = 4 / kCh;
         const int Q = steps(N), lane = threadIdx.x % 32;
@@ -287,8 +306,12 @@ struct Ring {
                 const int n = kSt * q + j % kSt;
                 a[j] = n < N && j / kSt < at.mine ? scale_a(p.A[at.channel(j / kSt) * N + n]) : 0.f;
             }
-            A[2 * q * 32 + lane] = make_float4(a[0], a[0], a[1], a[1]);
-            A[(2 * q + 1) * 32 + lane] = make_float4(a[2], a[2], a[3], a[3]);
+            if (kBack) {
+                A[2 * q * 32 + lane] = make_float4(a[0], a[0], a[1], a[1]);
+                A[(2 * q + 1) * 32 + lane] = make_float4(a[2], a[2], a[3], a[3]);
+            } else {
+                A[q * 32 + lane] = make_float4(a[0], a[1], a[2], a[3]);
+            }
             load_states<kCh>(first, row, p, at, q, a);
             slot[((W - 1) * Q + q) * 32 + lane] = make_float4(a[0], a[1], a[2], a[3]);
         }
@@ -409,6 +432,18 @@ __device__ __forceinline__ void load_bc(const float2 *row, int q, float2 (&v)[kS
     }
 }
 
+// The step's states of a token's row of B (or C), in pairs.
+template <int kSt>
+__device__ __forceinline__ void load_states_row(const float *row, int q, float2 (&v)[2]) {
+    if constexpr (kSt == 4) {
+        const float4 x = *reinterpret_cast<const float4 *>(row + 4 * q);
+        v[0] = make_float2(x.x, x.y);
+        v[1] = make_float2(x.z, x.w);
+    } else {
+        v[0] = v[1] = *reinterpret_cast<const float2 *>(row + 2 * q);
+    }
+}
+
 // What a forward walk leaves: outputs and the last state; the states before each chunk (marks
 // [B][chunks][tiles][Q][32] float4), which the backward walk needs; a segment's last state and step sizes (Split).
 enum { kOutputs = 0, kMarks = 1, kEnds = 2 };
@@ -430,14 +465,14 @@ ssm_fwd_kernel(const __grid_constant__ SsmProblem p, const __grid_constant__ Map
     const Tiles tl = tiles_of(p.C, p.G, kCh);
     const Place<kCh> at(p, tl, sp, segs);
     tc::pdl_wait_prerequisites();
-    ring.begin(p, at, W, N, kMode == kEnds ? nullptr : sp.n > 1 ? sp.h : p.h0, sp.n > 1 ? at.row : at.b);
+    ring.template begin<false>(p, at, W, N, kMode == kEnds ? nullptr : sp.n > 1 ? sp.h : p.h0, sp.n > 1 ? at.row : at.b);
     float bias[kCh], D[kCh];
 #pragma unroll
     for (int c = 0; c < kCh; ++c) {
         bias[c] = p.dt_bias ? p.dt_bias[at.channel(c)] : 0.f;
         D[c] = p.D ? p.D[at.channel(c)] : 0.f;
     }
-    float2 *rows = ring.rows + w * 2 * kPairs * NP;
+    float *rows = reinterpret_cast<float *>(ring.rows) + w * 2 * kTok * NP;
     const size_t stage_bytes = R::stage_bytes(kIn, row);
     auto stage = [&](int k) { return reinterpret_cast<T *>(ring.stage + (2 * w + k) * stage_bytes); };
     // d and d u of a chunk: in registers they would cost a tenth more instructions (moves; 128 registers are few)
@@ -477,8 +512,8 @@ ssm_fwd_kernel(const __grid_constant__ SsmProblem p, const __grid_constant__ Map
         const int64_t t0 = ch * kTok;
         wait(full + 8 * k, round);
         T *in = stage(k);
-        widen_rows<T, kN>(in + kIn * kRow, rows, N, row);
-        float2 d[kCh][kPairs], y[kCh][kPairs];
+        widen_tokens<T, kN>(in + kIn * kRow, rows, N, row);
+        float2 d[kCh][kPairs], y[kCh][kTok];        // y: of even and odd states
         step_sizes<T, kCh>(in + kRow, bias, p.softplus, p.T - t0, at.mine, d);
 #pragma unroll
         for (int ip = 0; ip < kPairs; ++ip) {
@@ -488,7 +523,7 @@ ssm_fwd_kernel(const __grid_constant__ SsmProblem p, const __grid_constant__ Map
             for (int c = 0; c < kCh; ++c) {
                 const float2 x = c < at.mine ? mul2(d[c][ip], u[c]) : both(0.f);
                 dx[(ip * kCh + c) * 32] = make_float4(d[c][ip].x, d[c][ip].y, x.x, x.y);
-                y[c][ip] = both(0.f);
+                y[c][2 * ip] = y[c][2 * ip + 1] = both(0.f);
                 if (kMode == kEnds) total[c] = add2(total[c], d[c][ip]);
             }
         }
@@ -496,43 +531,50 @@ ssm_fwd_kernel(const __grid_constant__ SsmProblem p, const __grid_constant__ Map
         fetch(ch + W, k ^ 1);
 #pragma unroll 1
         for (int q = 0; q < Q; ++q) {
-            float2 A[4], a[4][kPairs], s[4][kPairs];      // [kCh][kSt]
-            ring.load_a(q, A);
+            // pairs of states: (0, 1), (2, 3) of [kCh][kSt]
+            const float4 av = ring.A[q * 32 + lane];
+            const float2 A[2] = {make_float2(av.x, av.y), make_float2(av.z, av.w)};
+            float2 a[kTok][2], s[kTok][2];
 #pragma unroll
             for (int ip = 0; ip < kPairs; ++ip) {
-                float2 b[kSt];
-                load_bc<kSt>(rows + ip * NP, q, b);
                 float4 v[kCh];
 #pragma unroll
                 for (int c = 0; c < kCh; ++c) v[c] = dx[(ip * kCh + c) * 32];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    a[j][ip] = decay2(A[j], make_float2(v[j / kSt].x, v[j / kSt].y));
-                    s[j][ip] = mul2(b[j % kSt], make_float2(v[j / kSt].z, v[j / kSt].w));
+                for (int i = 2 * ip; i < 2 * ip + 2; ++i) {
+                    float2 b[2];
+                    load_states_row<kSt>(rows + i * NP, q, b);
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const float4 &of = v[kCh == 1 ? 0 : j];
+                        a[i][j] = decay2(A[j], both(i % 2 ? of.y : of.x));
+                        s[i][j] = mul2(b[j], both(i % 2 ? of.w : of.z));
+                    }
                 }
             }
             wait(from.bar + 8 * q, parity);
             const float4 v = load4(from.slot + 512 * q);
-            float h[4] = {v.x, v.y, v.z, v.w};
+            float2 h[2] = {make_float2(v.x, v.y), make_float2(v.z, v.w)};
             if (kMode == kMarks)
-                marks[(((at.b * chunks + ch) * tl.all + at.tile) * Q + q) * 32 + lane] =
-                    make_float4(h[0], h[1], h[2], h[3]);
+                marks[(((at.b * chunks + ch) * tl.all + at.tile) * Q + q) * 32 + lane] = v;
+            // the walk, which the next warp waits for
 #pragma unroll
-            for (int ip = 0; ip < kPairs; ++ip)
+            for (int i = 0; i < kTok; ++i)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    s[j][ip].x = fmaf(a[j][ip].x, h[j], s[j][ip].x);
-                    h[j] = s[j][ip].y = fmaf(a[j][ip].y, s[j][ip].x, s[j][ip].y);
-                }
-            store4(to.slot + 512 * q, h);
+                for (int j = 0; j < 2; ++j) h[j] = s[i][j] = fma2(a[i][j], h[j], s[i][j]);
+            const float last[4] = {h[0].x, h[0].y, h[1].x, h[1].y};
+            store4(to.slot + 512 * q, last);
             hand_over(to.bar + 8 * q, lane);
             if (kOut) {
 #pragma unroll
-                for (int ip = 0; ip < kPairs; ++ip) {
-                    float2 c[kSt];
-                    load_bc<kSt>(rows + (kPairs + ip) * NP, q, c);
+                for (int i = 0; i < kTok; ++i) {
+                    float2 c[2];
+                    load_states_row<kSt>(rows + (kTok + i) * NP, q, c);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) y[j / kSt][ip] = fma2(c[j % kSt], s[j][ip], y[j / kSt][ip]);
+                    for (int j = 0; j < 2; ++j) {
+                        float2 &to_y = y[kCh == 1 ? 0 : j][i];
+                        to_y = fma2(c[j], s[i][j], to_y);
+                    }
                 }
             }
         }
@@ -540,18 +582,16 @@ ssm_fwd_kernel(const __grid_constant__ SsmProblem p, const __grid_constant__ Map
             // outputs take the place of u in the stage, then leave in whole rows
 #pragma unroll
             for (int ip = 0; ip < kPairs; ++ip) {
-                float2 u[kCh], z[kCh];
+                float2 u[kCh], z[kCh], o[kCh];
                 if (p.D) lane_pair<T, kCh>(in, ip, u);
                 if (p.z.p) lane_pair<T, kCh>(in + 2 * kRow, ip, z);
 #pragma unroll
                 for (int c = 0; c < kCh; ++c) {
-                    if (p.D) y[c][ip] = fma2(both(D[c]), u[c], y[c][ip]);
-                    if (p.z.p)
-                        y[c][ip] = mul2(y[c][ip], mul2(z[c], make_float2(logistic<T>(z[c].x), logistic<T>(z[c].y))));
+                    const float2 even = y[c][2 * ip], odd = y[c][2 * ip + 1];
+                    o[c] = make_float2(even.x + even.y, odd.x + odd.y);
+                    if (p.D) o[c] = fma2(both(D[c]), u[c], o[c]);
+                    if (p.z.p) o[c] = mul2(o[c], mul2(z[c], make_float2(logistic<T>(z[c].x), logistic<T>(z[c].y))));
                 }
-                float2 o[kCh];
-#pragma unroll
-                for (int c = 0; c < kCh; ++c) o[c] = y[c][ip];
                 put_lane_pair<T, kCh>(in, ip, o);
             }
             tc::fence_proxy_async_smem();       // (TMA reads the outputs, and writes the next chunk over them)
@@ -616,7 +656,7 @@ ssm_bwd_kernel(const __grid_constant__ SsmProblem p, const __grid_constant__ Map
     if (!kEnd)
         for (int q = 0; q < Q; ++q) ring.sums[(w * Q + q) * 32 + lane] = make_float4(0.f, 0.f, 0.f, 0.f);
     tc::pdl_wait_prerequisites();
-    ring.begin(p, at, W, N, kEnd ? nullptr : sp.n > 1 ? sp.g : p.dhT, sp.n > 1 ? at.row : at.b);
+    ring.template begin<true>(p, at, W, N, kEnd ? nullptr : sp.n > 1 ? sp.g : p.dhT, sp.n > 1 ? at.row : at.b);
     float bias[kCh], D[kCh], dD[kCh], dbias[kCh];
 #pragma unroll
     for (int c = 0; c < kCh; ++c) {
@@ -1071,7 +1111,7 @@ template <typename T, int kCh>
 int ring_warps(const SsmProblem &p, int in, bool backward, int most) {
     const int64_t chunks = (p.T + kTok - 1) / kTok;
     int W = most;
-    while (W > 1 && Ring<T, kCh>::bytes(W, in, p.N, p.row, backward) > kRingBytes) W = W > 8 ? W - 4 : W / 2;
+    while (W > 1 && Ring<T, kCh>::bytes(W, in, p.N, p.row, backward) > kRingBytes) W -= W > 8 ? 4 : 1;
     return (int)std::min<int64_t>(W, chunks);
 }
 
