@@ -14,13 +14,17 @@
 // although all warps work at the same time. Backwards the ring turns the other way, on the states
 // that a forward walk left at the start of each chunk.
 //
-// Pairs of packed arithmetic are two tokens of one state: step sizes, inputs, B, C and sums of outputs
-// then are pairs as they come, and only the walk itself is scalar. (Pairs of two states need each
-// token's d and d u twice, which cost more moves than the walk saved: 191 instructions for a
-// token and channel of 16 states.)
+// Forward, pairs of packed arithmetic are two states of a token. What a warp does between the state's arrival
+// and its hand-over sets the ring's rate, and so it is 16 instructions for 4 states of 8 tokens; each token's d and d u are
+// needed twice side by side, which costs the moves that the walk saves (16384 tokens of 4096 channels, bf16, 16 states,
+// inputs and outputs 539 MB: 423 us, 448 with pairs of tokens). Backward, where registers are few, pairs are two
+// tokens of a state: step sizes, inputs, B, C and sums are pairs as they come, and only the walk is scalar.
 //
 // Bound: 16 exponentials of a token and channel take 64 cycles of a scheduler's share of the special function
-// units, the four multiply-adds of each state 64 of its FP32 pipe; in the backward pass thirteen of them 208.
+// units, the four multiply-adds of each state 64 of its FP32 pipe; in the backward pass thirteen of them 208. Forward
+// that is 172 us of the 423: a chunk comes every 400 cycles, of which its instructions take 280 and the rest is the
+// hand-over. Gradients (4 x 2047 tokens of 2048 channels) take 447 us, 343 of them in the backward kernel, whose two
+// warps to a scheduler (255 registers) issue half of the time.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -989,7 +993,7 @@ ssm_sums_kernel(const __grid_constant__ SsmProblem p, const Parts parts, const T
 // its row of A while they go through rows of the batch, kRows at a time: all that these need is on its way
 // together, and the page numbers of the next ones. A row's step size and output are made by one of the lanes. The
 // states are read and written once: HBM bandwidth bounds a batch. Measured: 240 rows of 4096 channels of 16 states
-// (134 MB) 29 us a call, 4.6 TB/s; with the loads of a row behind those of the row before, 61.
+// (134 MB) 28 us a call, 4.8 TB/s; with the loads of a row behind those of the row before, 61.
 template <typename T, int kLanes>
 __global__ void __launch_bounds__(256, 3)
 ssm_step_kernel(const __grid_constant__ SsmProblem p, int vec, unsigned int *err) {
@@ -1239,8 +1243,8 @@ int bwd_channels(const SsmProblem &p) {
 // Segments of a sequence for CTAs of 32 ch channels. Cutting it costs two thirds of a walk more (and the join), so it is
 // done where the tiles leave more than half of the SMs idle; the segments then make one round of resident CTAs (two to
 // an SM forward, one backward), or two rounds if those are better filled. Measured, 16384 tokens: forward, 512
-// channels 104 us against 449 uncut, 2048 channels 368 against 450, 2560 channels 450 uncut against 473 at best;
-// gradients, 1024 channels 599 us against 3376, 4864 channels of 8192 tokens 1281 against 1733.
+// channels 98 us against 421 uncut, 2048 channels 348 against 423, 2560 channels 424 uncut against 446 at best;
+// gradients, 1024 channels 606 us against 3364, 4864 channels of 8192 tokens 1272 against 1723.
 Split split_of(const SsmProblem &p, int ch, bool backward, int splits, int num_sms) {
     const int64_t chunks = (p.T + kTok - 1) / kTok, ctas = p.B * tiles_of(p.C, p.G, ch).all;
     const int64_t round = backward ? num_sms : 2 * num_sms, most = chunks / (backward ? 16 : 8);
