@@ -28,6 +28,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "elem.cuh"
 #include "gla_internal.h"
@@ -263,7 +264,7 @@ __device__ __forceinline__ void store_states(float *to, int64_t row, const SsmPr
 //   rows[W][2][kPairs][NP] float2: B and C of a warp's chunk (forward [W][2][kTok][NP] float);  bar[W][Q]
 //   stage[W][2]: a chunk as it lies in memory, on its way while the one before it is worked on:
 //     kIn tensors [kTok][32 kCh], then B and C [kTok][row];  full[W][2]: it is there
-//   dx[W][kPairs][kCh][32] float4 (forward): d and d u of a warp's chunk
+//   dx[W][kPairs][kCh][32] float4 (forward): d u and d of a warp's chunk
 constexpr int kTurn = 66;           // (lanes that write pairs side by side meet no bank twice)
 template <typename T, int kCh>
 struct Ring {
@@ -479,8 +480,10 @@ ssm_fwd_kernel(const __grid_constant__ SsmProblem p, const __grid_constant__ Map
     float *rows = reinterpret_cast<float *>(ring.rows) + w * 2 * kTok * NP;
     const size_t stage_bytes = R::stage_bytes(kIn, row);
     auto stage = [&](int k) { return reinterpret_cast<T *>(ring.stage + (2 * w + k) * stage_bytes); };
-    // d and d u of a chunk: in registers they would cost a tenth more instructions (moves; 128 registers are few)
-    float4 *dx = reinterpret_cast<float4 *>(ring.stage + 2 * W * stage_bytes) + w * kPairs * kCh * 32 + lane;
+    // d u of a chunk, and with outputs d: in registers d costs moves, as 128 are few (walks of no outputs have some left:
+    // the marks of 4 x 2047 tokens of 2048 channels 92 us, 83 with d in registers; outputs of 16384 x 4096 419, 549)
+    using DX = std::conditional_t<kOut, float4, float2>;
+    DX *dx = reinterpret_cast<DX *>(ring.stage + 2 * W * stage_bytes) + w * kPairs * kCh * 32 + lane;
     const int64_t chunks = (p.T + kTok - 1) / kTok;
     // the chunk into buffer k of the stage
     auto fetch = [&](int64_t ch, int k) {
@@ -526,7 +529,9 @@ ssm_fwd_kernel(const __grid_constant__ SsmProblem p, const __grid_constant__ Map
 #pragma unroll
             for (int c = 0; c < kCh; ++c) {
                 const float2 x = c < at.mine ? mul2(d[c][ip], u[c]) : both(0.f);
-                dx[(ip * kCh + c) * 32] = make_float4(d[c][ip].x, d[c][ip].y, x.x, x.y);
+                DX *at_dx = dx + (ip * kCh + c) * 32;
+                if constexpr (kOut) *at_dx = make_float4(x.x, x.y, d[c][ip].x, d[c][ip].y);
+                else *at_dx = x;
                 y[c][2 * ip] = y[c][2 * ip + 1] = both(0.f);
                 if (kMode == kEnds) total[c] = add2(total[c], d[c][ip]);
             }
@@ -541,18 +546,23 @@ ssm_fwd_kernel(const __grid_constant__ SsmProblem p, const __grid_constant__ Map
             float2 a[kTok][2], s[kTok][2];
 #pragma unroll
             for (int ip = 0; ip < kPairs; ++ip) {
-                float4 v[kCh];
+                DX v[kCh];
+                float2 of_d[kCh];
 #pragma unroll
-                for (int c = 0; c < kCh; ++c) v[c] = dx[(ip * kCh + c) * 32];
+                for (int c = 0; c < kCh; ++c) {
+                    v[c] = dx[(ip * kCh + c) * 32];
+                    if constexpr (kOut) of_d[c] = make_float2(v[c].z, v[c].w);
+                    else of_d[c] = d[c][ip];
+                }
 #pragma unroll
                 for (int i = 2 * ip; i < 2 * ip + 2; ++i) {
                     float2 b[2];
                     load_states_row<kSt>(rows + i * NP, q, b);
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        const float4 &of = v[kCh == 1 ? 0 : j];
-                        a[i][j] = decay2(A[j], both(i % 2 ? of.y : of.x));
-                        s[i][j] = mul2(b[j], both(i % 2 ? of.w : of.z));
+                        const int c = kCh == 1 ? 0 : j;
+                        a[i][j] = decay2(A[j], both(i % 2 ? of_d[c].y : of_d[c].x));
+                        s[i][j] = mul2(b[j], both(i % 2 ? v[c].y : v[c].x));
                     }
                 }
             }
