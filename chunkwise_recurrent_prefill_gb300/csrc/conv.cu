@@ -165,7 +165,7 @@ conv_bwd_kernel(const __grid_constant__ ConvProblem p, const ConvPlan pl, float 
     tc::pdl_wait_prerequisites();
     constexpr int kBatch = 4, kP = (kV + 1) / 2;
     using R = typename Pack<T, kV>::raw;
-    __shared__ float sums[kThreads][kV];
+    __shared__ float sums[W + 1][kThreads][kV];
     const int lane = threadIdx.x % pl.lanes, row = threadIdx.x / pl.lanes, rows = kThreads / pl.lanes;
     const int64_t c = ((int64_t)blockIdx.y * pl.lanes + lane) * kV;
     const int64_t id = (int64_t)blockIdx.x * rows + row;
@@ -272,21 +272,21 @@ conv_bwd_kernel(const __grid_constant__ ConvProblem p, const ConvPlan pl, float 
     if (!part) return;
     // the runs of the CTA are added in their order
 #pragma unroll
-    for (int j = 0; j <= W; ++j) {
-        __syncthreads();
+    for (int j = 0; j <= W; ++j)
 #pragma unroll
         for (int v = 0; v < kV; ++v) {
             const float2 s = j < W ? dw[j < W ? j : 0][v / 2] : db[v / 2];
-            sums[threadIdx.x][v] = v % 2 ? s.y : s.x;
+            sums[j][threadIdx.x][v] = v % 2 ? s.y : s.x;
         }
-        __syncthreads();
-        for (int k = threadIdx.x; k < pl.lanes * kV; k += kThreads) {
-            const int64_t ch = (int64_t)blockIdx.y * pl.lanes * kV + k;
-            if (ch >= p.C) continue;
-            float s = 0.f;
-            for (int r = 0; r < rows; ++r) s += sums[r * pl.lanes + k / kV][k % kV];
-            part[((int64_t)blockIdx.x * (W + 1) + j) * p.C + ch] = s;
-        }
+    __syncthreads();
+    const int tile = pl.lanes * kV;
+    for (int k = threadIdx.x; k < tile * (W + 1); k += kThreads) {
+        const int j = k / tile, i = k - j * tile;
+        const int64_t ch = (int64_t)blockIdx.y * tile + i;
+        if (ch >= p.C) continue;
+        float s = 0.f;
+        for (int r = 0; r < rows; ++r) s += sums[j][r * pl.lanes + i / kV][i % kV];
+        part[((int64_t)blockIdx.x * (W + 1) + j) * p.C + ch] = s;
     }
 }
 

@@ -22,8 +22,8 @@
 //
 // Bound: 16 exponentials of a token and channel take 64 cycles of a scheduler's share of the special function
 // units, the four multiply-adds of each state 64 of its FP32 pipe; in the backward pass thirteen of them 208. Forward
-// that is 172 us of the 423: a chunk comes every 400 cycles, of which its instructions take 280 and the rest is the
-// hand-over. Gradients (4 x 2047 tokens of 2048 channels) take 447 us, 343 of them in the backward kernel, whose two
+// that is 172 us of the 423: a chunk comes every 400 cycles, of which its instructions take 250 and the rest is the
+// hand-over. Gradients (4 x 2047 tokens of 2048 channels) take 437 us, 343 of them in the backward kernel, whose two
 // warps to a scheduler (255 registers) issue half of the time.
 #include <cuda_bf16.h>
 
