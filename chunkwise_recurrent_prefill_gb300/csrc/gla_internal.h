@@ -57,6 +57,12 @@ int launch_failed(const char *where, cudaError_t e);
 // Host-side count of kernel launches issued by the library (gla_launch_counter).
 void count_launches(unsigned n);
 
+// Test hook of the bounded waits. The environment is read once per process: with
+// GLA_TEST_STALL_ONE_LOAD set, the first call of the process whose kernel asks leaves out the
+// load of one chunk (later calls run normally), so its waits run out and the call reports
+// GLA_ERR_DEVICE_TIMEOUT with the context intact.
+bool take_stall_hook();
+
 // Sets the text gla_last_error_detail() returns on this host thread.
 void set_error_detail(const char *text);
 

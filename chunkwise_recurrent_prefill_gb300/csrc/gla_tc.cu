@@ -1491,25 +1491,6 @@ cudaError_t set_attrs() {
     return cudaSuccess;
 }
 
-// Test hook of the bounded waits. The environment is read once per process: with
-// GLA_TEST_STALL_ONE_LOAD set, the first tensor-core launch of the process skips the q/k/v
-// load of one chunk in every output CTA (later launches run normally), so its waits run out
-// and the call reports GLA_ERR_DEVICE_TIMEOUT with the context intact.
-std::atomic<int> g_stall_left{-1};   // -1: environment not read yet
-
-bool take_stall_hook() {
-    int left = g_stall_left.load(std::memory_order_relaxed);
-    if (left < 0) {
-        int init = std::getenv("GLA_TEST_STALL_ONE_LOAD") ? 1 : 0, expect = -1;
-        g_stall_left.compare_exchange_strong(expect, init);
-        left = g_stall_left.load(std::memory_order_relaxed);
-    }
-    while (left > 0) {
-        if (g_stall_left.compare_exchange_weak(left, left - 1)) return true;
-    }
-    return false;
-}
-
 int clamp_splits(const Problem &p, int splits) {
     const int64_t nchunks = (p.T + kC - 1) / kC;
     int64_t s = std::max<int64_t>(1, std::min<int64_t>(splits, nchunks));
@@ -1532,6 +1513,21 @@ Problem tc_view(const Problem &p) {
 }
 
 }  // namespace
+
+// (see gla_internal.h; here the call leaves out the q/k/v load of one chunk in every output CTA)
+bool take_stall_hook() {
+    static std::atomic<int> calls_left{-1};     // -1: environment not read yet
+    int left = calls_left.load(std::memory_order_relaxed);
+    if (left < 0) {
+        int init = std::getenv("GLA_TEST_STALL_ONE_LOAD") ? 1 : 0, expect = -1;
+        calls_left.compare_exchange_strong(expect, init);
+        left = calls_left.load(std::memory_order_relaxed);
+    }
+    while (left > 0) {
+        if (calls_left.compare_exchange_weak(left, left - 1)) return true;
+    }
+    return false;
+}
 
 bool tc_supported(const Problem &p) {
     // head dims 64 run on the 128-wide kernels: the tensor copies read zeros past the

@@ -162,8 +162,11 @@ __device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
     return ok != 0;
 }
 // Most hand-overs arrive while it polls; the clock that bounds the wait takes longer to read than they do. A warp that
-// gave up once (dead) does not wait again.
-__device__ __forceinline__ bool wait_on(uint32_t bar, uint32_t parity, bool dead, unsigned int *err) {
+// gives up lets what it has asked for land (bounded, too, as the shared memory of a CTA that ends is another's): the
+// chunk in buffer k of its stage, and the next one. From then on it asks for nothing, waits for nothing and goes on
+// with what is there.
+__device__ __forceinline__ bool wait_on(uint32_t bar, uint32_t parity, bool dead, uint64_t *full, int k, uint32_t round,
+                                        unsigned int *err) {
     if (dead) return true;
 #pragma unroll 1
     for (int i = 0; i < 256; ++i)
@@ -176,6 +179,8 @@ __device__ __forceinline__ bool wait_on(uint32_t bar, uint32_t parity, bool dead
         if (tc::global_ns() - t0 > tc::kWaitLimitNs) break;
     }
     atomicOr(err, kDevErrTimeout);
+    tc::mbar_wait(full + k, round);
+    tc::mbar_wait(full + (k ^ 1), round ^ k);
     return true;
 }
 // Lane 0 tells the next warp, once all lanes have written.
@@ -485,9 +490,10 @@ ssm_fwd_kernel(const __grid_constant__ SsmProblem p, const __grid_constant__ Map
     using DX = std::conditional_t<kOut, float4, float2>;
     DX *dx = reinterpret_cast<DX *>(ring.stage + 2 * W * stage_bytes) + w * kPairs * kCh * 32 + lane;
     const int64_t chunks = (p.T + kTok - 1) / kTok;
+    bool dead = false;                  // the warp has given up
     // the chunk into buffer k of the stage
     auto fetch = [&](int64_t ch, int k) {
-        if (ch >= at.ch1) return;
+        if (ch >= at.ch1 || dead) return;
         T *to = stage(k);
         const int64_t t0 = ch * kTok;
         if (lane == 0) {
@@ -505,16 +511,15 @@ ssm_fwd_kernel(const __grid_constant__ SsmProblem p, const __grid_constant__ Map
     };
     const Link from = ring.link(w == 0 ? W - 1 : w - 1, Q), to = ring.link(w, Q);
     const uint32_t full = tc::smem_u32(ring.full + 2 * w);
-    bool dead = false;
-    auto wait = [&](uint32_t bar, uint32_t parity) {
-        if (!try_wait(bar, parity)) dead = wait_on(bar, parity, dead, err);
-    };
     int k = 0;
     uint32_t round = 0, parity = 0;     // of the stage's buffer, and of the hand-overs
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+        if (!try_wait(bar, parity) && wait_on(bar, parity, dead, ring.full + 2 * w, k, round, err)) dead = true;
+    };
     float2 total[kCh];
 #pragma unroll
     for (int c = 0; c < kCh; ++c) total[c] = both(0.f);
-    fetch(at.ch0 + w, 0);
+    if (w != p.stall) fetch(at.ch0 + w, 0);
     for (int64_t ch = at.ch0 + w; ch < at.ch1; ch += W) {
         const int64_t t0 = ch * kTok;
         wait(full + 8 * k, round);
@@ -683,9 +688,10 @@ ssm_bwd_kernel(const __grid_constant__ SsmProblem p, const __grid_constant__ Map
     const size_t stage_bytes = R::stage_bytes(kIn, row);
     auto stage = [&](int k) { return reinterpret_cast<T *>(ring.stage + (2 * w + k) * stage_bytes); };
     const int64_t chunks = (p.T + kTok - 1) / kTok, steps = at.ch1 - at.ch0;
+    bool dead = false;                  // the warp has given up
     // the chunk into buffer k of the stage
     auto fetch = [&](int64_t step, int k) {
-        if (step >= steps) return;
+        if (step >= steps || dead) return;
         T *to = stage(k);
         const int64_t t0 = (at.ch1 - 1 - step) * kTok;
         if (lane == 0) {
@@ -703,13 +709,12 @@ ssm_bwd_kernel(const __grid_constant__ SsmProblem p, const __grid_constant__ Map
     };
     const Link from = ring.link(w == 0 ? W - 1 : w - 1, Q), to = ring.link(w, Q);
     const uint32_t full = tc::smem_u32(ring.full + 2 * w);
-    bool dead = false;
-    auto wait = [&](uint32_t bar, uint32_t parity) {
-        if (!try_wait(bar, parity)) dead = wait_on(bar, parity, dead, err);
-    };
     int k = 0;
     uint32_t round = 0, parity = 0;     // of the stage's buffer, and of the hand-overs
-    fetch(w, 0);
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+        if (!try_wait(bar, parity) && wait_on(bar, parity, dead, ring.full + 2 * w, k, round, err)) dead = true;
+    };
+    if (w != p.stall) fetch(w, 0);
     for (int64_t step = w; step < steps; step += W) {
         const int64_t ch = at.ch1 - 1 - step, t0 = ch * kTok;
         const float4 *mark = marks + ((at.b * chunks + ch) * tl.all + at.tile) * Q * 32 + lane;
@@ -1342,6 +1347,7 @@ template <typename T>
 cudaError_t whole_fwd(SsmProblem p, int splits, int num_sms, void *ws, unsigned int *err, cudaStream_t s) {
     Maps maps;
     Split sp = split_of(p, 1, false, splits, num_sms);
+    p.stall = take_stall_hook() ? 1 : -1;
     char *at = static_cast<char *>(ws);
     const size_t copies = packing_of(p, false, false).bytes;
     cudaError_t e = pack(&p, at, num_sms, s);
@@ -1361,6 +1367,7 @@ template <typename T, int kCh>
 cudaError_t whole_bwd(SsmProblem p, int splits, int num_sms, void *ws, unsigned int *err, cudaStream_t s) {
     Maps maps;
     Split sp = split_of(p, kCh, true, splits, num_sms);
+    p.stall = take_stall_hook() ? 1 : -1;
     const BwdWorkspace lay = bwd_workspace(p, sp);
     char *at = static_cast<char *>(ws);
     const size_t copies = packing_of(p, false, false).bytes;

@@ -27,6 +27,7 @@ struct SsmProblem {
     // many elements apart (N and C / G, or those brought to 16 bytes by a copy), and whether TMA writes.
     int64_t group;
     int row, tma_out;
+    int stall;                          // test hook: warp of each ring whose first load is never issued (-1: none)
     // one token
     float *S;                           // [P, C, N]
     const int *slots;
