@@ -323,10 +323,10 @@ struct Items {
         x.at += step, x.b += step_b, x.tile += step_tile;
         if (x.tile >= pl.tiles) x.tile -= pl.tiles, ++x.b;
     }
-    // The next item, into buffer k.
+    // The next item, into buffer k (skip: a test's that never comes).
     __device__ __forceinline__ void fetch(const QkProblem &p, const QkPlan &pl, const CUtensorMap *const (&maps)[kTensors],
-                                          int h0) {
-        if (threadIdx.x % 32 == 0 && next.at < all) {
+                                          int h0, bool skip = false) {
+        if (threadIdx.x % 32 == 0 && next.at < all && !skip) {
             const int t = next.tile * (32 / pl.W);
             int n = 0;
             for (int i = 0; i < kTensors; ++i) n += maps[i] ? 32 / pl.W * kHeads * p.D * (int)sizeof(T) : 0;
@@ -338,11 +338,12 @@ struct Items {
         }
         move(next, pl);
     }
-    // Waits for buffer k; if it never comes, says so and waits for the others that may be on their way.
+    // Waits for buffer k; if it never comes, says so and waits (bounded, too) for all that may be on its way: the shared
+    // memory of a CTA that ends is another's.
     __device__ __forceinline__ bool arrived(unsigned int *err) const {
         if (tc::mbar_wait(full + k, parity)) return true;
         atomicOr(err, kDevErrTimeout);
-        for (int i = 1; i < kAhead; ++i) tc::mbar_wait(full + (k + i) % kAhead, parity ^ (k + i >= kAhead));
+        for (int i = 0; i < kAhead; ++i) tc::mbar_wait(full + (k + i) % kAhead, parity ^ (k + i >= kAhead));
         return false;
     }
     // Done with buffer k: it takes another item, and the warp goes on to its next.
@@ -387,7 +388,7 @@ qk_rows_fwd(const __grid_constant__ QkProblem p, const __grid_constant__ QkMaps 
     const Unit<V, kPairs> u(p, l);
     const CUtensorMap *const from[1] = {&maps.x[which]};
     Items<T, 1, kHeads> items(p, pl, smem, bars);
-    for (int k = 0; k < kAhead; ++k, ++items.k) items.fetch(p, pl, from, h0);
+    for (int k = 0; k < kAhead; ++k, ++items.k) items.fetch(p, pl, from, h0, p.stall && k == 0);
     items.k = 0;
     Pairs<V> w[2];
 #pragma unroll
@@ -467,7 +468,7 @@ qk_rows_bwd(const __grid_constant__ QkProblem p, const __grid_constant__ QkMaps 
     const Unit<V, kPairs> u(p, l);
     const CUtensorMap *const from[2] = {&maps.go[which], p.norm ? &maps.x[which] : nullptr};
     Items<T, 2, kHeads> items(p, pl, smem, bars);
-    for (int k = 0; k < kAhead; ++k, ++items.k) items.fetch(p, pl, from, h0);
+    for (int k = 0; k < kAhead; ++k, ++items.k) items.fetch(p, pl, from, h0, p.stall && k == 0);
     items.k = 0;
     Pairs<V> w[2], dw[2] = {};
 #pragma unroll
@@ -691,7 +692,8 @@ cudaError_t run_fwd(const QkProblem &in, int num_sms, unsigned int *err, cudaStr
     if (!vectors(in))
         return launch(qk_plain_fwd<T>, dim3((unsigned)((rows_of(in) + kWarps - 1) / kWarps)), kThreads, 0, s, in,
                       err);
-    const QkProblem p = joined(in);
+    QkProblem p = joined(in);
+    p.stall = take_stall_hook();
     return p.pairs ? rows_fwd<T, true>(p, num_sms, err, s) : rows_fwd<T, false>(p, num_sms, err, s);
 }
 
@@ -700,7 +702,8 @@ cudaError_t run_bwd(const QkProblem &in, float *part, int num_sms, unsigned int 
     QkSums sums{};
     cudaError_t e;
     if (vectors(in)) {
-        const QkProblem p = joined(in);
+        QkProblem p = joined(in);
+        p.stall = take_stall_hook();
         e = p.pairs ? rows_bwd<T, true>(p, part, num_sms, err, s, &sums) : rows_bwd<T, false>(p, part, num_sms, err, s, &sums);
     } else {
         constexpr auto kernel = qk_plain_bwd<T>;

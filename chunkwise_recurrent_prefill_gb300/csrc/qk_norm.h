@@ -25,6 +25,7 @@ struct QkProblem {
     int64_t B, T, P;
     int D, R, norm, pairs, io;
     float eps;
+    int stall;                  // test hook: the first load of each warp is never issued
 };
 
 cudaError_t launch_qk_fwd(const QkProblem &p, int num_sms, unsigned int *dev_err, cudaStream_t s);

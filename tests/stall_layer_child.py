@@ -13,6 +13,8 @@ ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 sys.path.insert(0, ROOT)
 sys.path.insert(0, os.path.join(ROOT, "tests"))
 
+import torch  # noqa: E402
+
 import layer_ref as ref  # noqa: E402
 
 
@@ -33,11 +35,38 @@ def scan(backward, splits):
     return run, ref.scan(d, back=backward)
 
 
-CALLS = {"scan": lambda: scan(False, 1), "scan in segments": lambda: scan(False, 2), "scan gradients": lambda: scan(True, 1)}
+def qk(backward):
+    from chunkwise_recurrent_prefill_gb300 import qk_norm_bwd, qk_norm_fwd
+    g = torch.Generator().manual_seed(7)
+    B, T, D = 2, 50, 64
+    q, dq = ref.draw(g, B, T, 4, D), ref.draw(g, B, T, 4, D)
+    k, dk = ref.draw(g, B, T, 2, D), ref.draw(g, B, T, 2, D)
+    wq, wk = ref.draw(g, D), ref.draw(g, D)
+    angle = torch.rand(T, D // 2, generator=g) * 6
+    cos, sin, positions = torch.cos(angle), torch.sin(angle), torch.arange(T).expand(B, T)
+    t = [ref.gpu(x) for x in (q, k, wq, wk)]
+    kw = dict(cos=cos.cuda(), sin=sin.cuda())
+    # the forward's factors to 2^-24, which the gradients take as they are
+    r = [(x.double().square().mean(-1) + 1e-6).pow(-0.5).float() for x in (q, k)]
+
+    def run():
+        if backward:
+            out = qk_norm_bwd(dq.cuda(), dk.cuda(), *t[:2], r[0].cuda(), r[1].cuda(), *t[2:], **kw)
+            return dict(zip(("dx0", "dx1", "dw0", "dw1"), out))
+        return dict(zip(("out0", "out1", "r0", "r1"), qk_norm_fwd(*t, **kw)))
+
+    want = {}
+    for i, (x, w, go) in enumerate(((q, wq, dq), (k, wk, dk))):
+        for n, v in ref.qk(x, w, cos, sin, positions, "rms", False, 1e-6, go, r[i]).items():
+            want[f"{n}{i}"] = v
+    return run, want
+
+
+CALLS = {"scan": lambda: scan(False, 1), "scan in segments": lambda: scan(False, 2), "scan gradients": lambda: scan(True, 1),
+         "norm": lambda: qk(False), "norm gradients": lambda: qk(True)}
 
 
 def main():
-    import torch
     from chunkwise_recurrent_prefill_gb300 import last_device_status
     assert os.environ.get("GLA_TEST_STALL_ONE_LOAD")
     run, want = CALLS[sys.argv[1]]()

@@ -23,9 +23,9 @@ def _built():
     __graft_entry__.build()
 
 
-# A warp waits 2 s until it gives up, and as long for each of the two loads that may be on their way; each of these calls
-# has two kernels that load, the first one.
-@pytest.mark.parametrize("call", ["scan", "scan in segments", "scan gradients"])
+# A warp waits 2 s until it gives up, and as long for each of the two loads that may be on their way; a call has up to two
+# kernels that load.
+@pytest.mark.parametrize("call", ["scan", "scan in segments", "scan gradients", "norm", "norm gradients"])
 def test_a_wait_that_runs_out(call):
     env = dict(os.environ, GLA_TEST_STALL_ONE_LOAD="1")
     r = subprocess.run([sys.executable, os.path.join(HERE, "stall_layer_child.py"), call], env=env, capture_output=True,
