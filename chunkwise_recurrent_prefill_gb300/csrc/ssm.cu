@@ -969,7 +969,10 @@ ssm_join_kernel(const __grid_constant__ SsmProblem p, const Split sp) {
         for (int j = 0; j < kAhead; ++j) {
             if (k + j >= sp.n) break;
             x[(int64_t)(back ? sp.n - 1 - k - j : k + j) * cn] = v;
-            v = fmaf(exp2f(A * a[j]), v, end[j]);
+            // (in two halves: where states grow, a segment's factor may pass the range although its product with a small
+            // state does not; and nothing stays nothing, whatever the factor)
+            const float half = exp2f(0.5f * A * a[j]);
+            v = v == 0.f ? end[j] : fmaf(half * v, half, end[j]);
         }
     }
 }

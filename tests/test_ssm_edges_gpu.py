@@ -1,4 +1,4 @@
-"""Edges of the selective state space scan: small steps, the last token, states that fill lanes, segments that grow."""
+"""Edges of the selective state space scan."""
 import pytest
 import torch
 
@@ -12,60 +12,6 @@ pytestmark = pytest.mark.gpu
 def _built():
     import __graft_entry__
     __graft_entry__.build()
-
-
-@pytest.mark.parametrize("lo,hi", [(-80.0, -20.0), (-20.0, -5.0), (-5.0, 0.0), (0.0, 20.0)])
-def test_small_steps_keep_their_digits(lo, hi):
-    """Step sizes on their own: with A = 0, u = B = C = do = 1 the state after one token, and du, are the step. Whatever
-    the size of x, softplus(x) is off by the hardware's 2^x (2^-22 of the value, four U), by a rounding each of what the
-    argument's rounding left out, of the last two sums and of the polynomial's terms before (less than one U
-    together), and by its fit (a tenth of a U): eight U. (What the argument's rounding leaves out has an error of its own
-    of 2^-24 of 2^-19.)"""
-    from chunkwise_recurrent_prefill_gb300 import ssm_bwd, ssm_fwd, ssm_step
-    C = 4096
-    x = torch.linspace(lo, hi, C)
-    want = torch.logaddexp(x.double(), torch.zeros(C).double())
-    dt, one, A, b = x.cuda()[None, None], torch.ones(1, 1, C, device="cuda"), torch.zeros(C, 1, device="cuda"), \
-        torch.ones(1, 1, 1, 1, device="cuda")
-    hT = ssm_fwd(one, dt, A, b, b, return_state=True)[1]
-    S = torch.zeros(1, C, 1, device="cuda")
-    ssm_step(one[:, 0], dt[:, 0], A, b[:, 0], b[:, 0], S)
-    du = ssm_bwd(one, one, dt, A, b, b)[0]
-    for n, got in (("hT", hT), ("S", S), ("du", du)):
-        ref.close(n, got.view(C), want, 8 * ref.U * want)
-
-
-@pytest.mark.parametrize("value", [float("nan"), float("inf")])
-@pytest.mark.parametrize("T,C,N,splits", [(100, 40, 16, 0), (104, 40, 16, 0), (97, 64, 16, 3), (99, 7, 64, 0),
-                                          (102, 33, 12, 2), (1, 5, 16, 0)])
-def test_a_last_token_that_is_not_finite_leaves_dA(T, C, N, splits, value):
-    """dA is made of the states before the tokens: that after the last one has no part in it."""
-    t = {k: ref.gpu(v) for k, v in make(2, T, C, 1, N, "f32", seed=T).items()}
-    clean = call(t, seq_splits=splits)
-    t["u"][1, T - 1, 3] = value
-    got = call(t, seq_splits=splits)
-    assert got["o"][1, T - 1, 3].isfinite().logical_not() and got["hT"][1, 3].isfinite().logical_not().all()
-    assert torch.equal(got["dA"], clean["dA"])
-
-
-@pytest.mark.parametrize("io", ["bf16", "f32"])
-@pytest.mark.parametrize("N", [12, 20, 24, 36, 100])
-def test_steps_of_an_infinite_input(N, io):
-    """N is a multiple of 4 and no power of two: positive B and C make an infinity of an infinite u, not a NaN."""
-    from chunkwise_recurrent_prefill_gb300 import ssm_fwd, ssm_step
-    g = torch.Generator().manual_seed(N)
-    R, C = 3, 32
-    u, dt = ref.draw(g, R, 1, C, io=io).cuda(), ref.draw(g, R, 1, C, io=io).cuda()
-    b, c = (ref.draw(g, R, 1, 1, N, io=io).abs().cuda() + 1 for _ in range(2))
-    A = -torch.rand(C, N, generator=g).cuda()
-    u[1, 0, 5] = float("inf")
-    want, h = ssm_fwd(u, dt, A, b, c, return_state=True)
-    S = torch.zeros(R, C, N, device="cuda")
-    o = ssm_step(u[:, 0], dt[:, 0], A, b[:, 0], c[:, 0], S)
-    assert want[1, 0, 5] == float("inf") and o[1, 5] == float("inf")
-    assert (S[1, 5] == float("inf")).all() and (h[1, 5] == float("inf")).all()
-    o[1, 5] = want[1, 0, 5] = 0
-    assert o.isfinite().all() and want.isfinite().all()
 
 
 @pytest.mark.parametrize("N", [16, 7])
@@ -89,3 +35,19 @@ def test_growing_segments_of_nothing(N):
     for n, v in got.items():
         if v is not None:
             ref.close(n, v, *want[n])
+
+
+def test_segments_that_grow_and_shrink():
+    """A small state that grows by more than the range in a segment, and shrinks in the next: it is never large."""
+    from chunkwise_recurrent_prefill_gb300 import ssm_fwd
+    T = 256
+    d = make(2, T, 40, 1, 16, "f32", seed=3, params=False)
+    d["A"], d["u"], d["h0"] = torch.full_like(d["A"], 0.71), 0 * d["u"], 1e-37 * d["h0"]
+    d["dt"] = torch.ones_like(d["dt"])
+    d["dt"][:, T // 2:] = -1
+    t = {k: ref.gpu(v) for k, v in d.items()}
+    o, hT = ssm_fwd(t["u"], t["dt"], t["A"], t["Bm"], t["Cm"], z=t["z"], h0=t["h0"], softplus=False, return_state=True,
+                    seq_splits=2)
+    want = ref.scan(d, softplus=False, back=False)
+    ref.close("o", o, *want["o"])
+    ref.close("hT", hT, *want["hT"])
