@@ -51,3 +51,16 @@ def test_segments_that_grow_and_shrink():
     want = ref.scan(d, softplus=False, back=False)
     ref.close("o", o, *want["o"])
     ref.close("hT", hT, *want["hT"])
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("T,C,N,splits", [(100, 40, 16, 0), (104, 40, 16, 0), (97, 64, 16, 3), (99, 7, 64, 0),
+                                          (102, 33, 12, 2), (1, 5, 16, 0)])
+def test_a_last_token_that_is_not_finite_leaves_dA(T, C, N, splits, value):
+    """dA is made of the states before the tokens: that after the last one has no part in it."""
+    t = {k: ref.gpu(v) for k, v in make(2, T, C, 1, N, "f32", seed=T).items()}
+    clean = call(t, seq_splits=splits)
+    t["u"][1, T - 1, 3] = value
+    got = call(t, seq_splits=splits)
+    assert got["o"][1, T - 1, 3].isfinite().logical_not() and got["hT"][1, 3].isfinite().logical_not().all()
+    assert torch.equal(got["dA"], clean["dA"])
