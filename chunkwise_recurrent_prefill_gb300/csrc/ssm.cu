@@ -1106,6 +1106,7 @@ ssm_step_kernel(const __grid_constant__ SsmProblem p, int vec, unsigned int *err
             v.z = fmaf(ex2(fmaf(A[2], di, 2e-8f)), h[i].z, x * Bv[2]);
             v.w = fmaf(ex2(fmaf(A[3], di, 2e-8f)), h[i].w, x * Bv[3]);
             y[i] = fmaf(v.x, Cv[0], v.y * Cv[1]) + fmaf(v.z, Cv[2], v.w * Cv[3]);
+            if (page[i] < 0 || !mine) y[i] = 0.f;       // (0 times an infinite d u is NaN)
             if (page[i] >= 0 && mine) {
                 float *S = p.S + ((int64_t)page[i] * p.C + cc) * p.N + n0;
                 if (whole) {

@@ -64,3 +64,23 @@ def test_a_last_token_that_is_not_finite_leaves_dA(T, C, N, splits, value):
     got = call(t, seq_splits=splits)
     assert got["o"][1, T - 1, 3].isfinite().logical_not() and got["hT"][1, 3].isfinite().logical_not().all()
     assert torch.equal(got["dA"], clean["dA"])
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("N", [12, 20, 24, 36, 100])
+def test_steps_of_an_infinite_input(N, io):
+    """N is a multiple of 4 and no power of two: positive B and C make an infinity of an infinite u, not a NaN."""
+    from chunkwise_recurrent_prefill_gb300 import ssm_fwd, ssm_step
+    g = torch.Generator().manual_seed(N)
+    R, C = 3, 32
+    u, dt = ref.draw(g, R, 1, C, io=io).cuda(), ref.draw(g, R, 1, C, io=io).cuda()
+    b, c = (ref.draw(g, R, 1, 1, N, io=io).abs().cuda() + 1 for _ in range(2))
+    A = -torch.rand(C, N, generator=g).cuda()
+    u[1, 0, 5] = float("inf")
+    want, h = ssm_fwd(u, dt, A, b, c, return_state=True)
+    S = torch.zeros(R, C, N, device="cuda")
+    o = ssm_step(u[:, 0], dt[:, 0], A, b[:, 0], c[:, 0], S)
+    assert want[1, 0, 5] == float("inf") and o[1, 5] == float("inf")
+    assert (S[1, 5] == float("inf")).all() and (h[1, 5] == float("inf")).all()
+    o[1, 5] = want[1, 0, 5] = 0
+    assert o.isfinite().all() and want.isfinite().all()
