@@ -74,7 +74,8 @@ struct Pack<__nv_bfloat16, 4> {
 };
 
 // The logistic function 1 / (1 + 2^(-u log2 e)). Results that are rounded to bf16 take the hardware's
-// approximate exponential and reciprocal (a few 2^-22 of the value), flushing denormals.
+// approximate exponential and reciprocal, flushing denormals: good to a few 2^-22 of the value, and where u < 0 to
+// another 2^-23 |u|, from the rounding of u log2 e.
 template <typename T>
 __device__ __forceinline__ float logistic(float u) {
     if (sizeof(T) == 4) return 1.f / (1.f + expf(-u));

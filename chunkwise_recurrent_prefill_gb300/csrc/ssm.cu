@@ -73,8 +73,18 @@ __device__ __forceinline__ float scale_a(float a) {
 // small steps that give a state its memory keep their digits, which log(1 + e) formed as such would lose, and
 // ten multiply-adds cost a third of the library's functions. (Scalar: packed ones would have to fetch
 // their constants into registers.)
+// e takes its error from 2^x (2^-22) and from the rounding of x log2 e, which is |x| 2^-24 of the value (6e-7 of the step at
+// x = -7, 1e-6 at -12, 4e-6 at -60). fp32 calls put back what the rounding left out, to first order: their steps are good to
+// 8 2^-24 whatever x is. bf16 calls, whose dt has 2^-9 |x| of the step to itself, do not pay for that.
+template <typename T>
 __device__ __forceinline__ float softplus(float x) {
-    const float e = ex2(fabsf(x) * -kLog2e);
+    const float t = fabsf(x) * -kLog2e;
+    float e = ex2(t);
+    if (sizeof(T) == 4) {
+        constexpr float kLog2eLow = 1.4426950408889634 - (double)kLog2e;
+        const float left = fmaf(fabsf(x), -kLog2eLow, fmaf(fabsf(x), -kLog2e, -t));
+        e = fmaf(e, fminf(left, 1.f) * kLn2, e);        // (infinite or NaN where x log2 e is not finite: e is 0)
+    }
     float r = -0.003244024235755205f;
     r = fmaf(r, e, 0.019851457327604294f);
     r = fmaf(r, e, -0.056959524750709534f);
@@ -87,7 +97,8 @@ __device__ __forceinline__ float softplus(float x) {
     r = fmaf(r, e, 1.f);
     return fmaf(r, e, fmaxf(x, 0.f));
 }
-__device__ __forceinline__ float step_size(float x, int on) { return on ? softplus(x) : x; }
+template <typename T>
+__device__ __forceinline__ float step_size(float x, int on) { return on ? softplus<T>(x) : x; }
 
 // Tensor maps of the rows: boxes of kTok tokens by a tile's channels (or a group's states).
 struct Maps {
@@ -419,7 +430,7 @@ __device__ __forceinline__ void step_sizes(const T *in, const float (&bias)[kCh]
 #pragma unroll
         for (int c = 0; c < kCh; ++c)
 #pragma unroll
-            for (int ip = 0; ip < kPairs; ++ip) d[c][ip] = make_float2(softplus(d[c][ip].x), softplus(d[c][ip].y));
+            for (int ip = 0; ip < kPairs; ++ip) d[c][ip] = make_float2(softplus<T>(d[c][ip].x), softplus<T>(d[c][ip].y));
     }
     if (left < kTok || mine < kCh) {
 #pragma unroll
@@ -1091,7 +1102,7 @@ ssm_step_kernel(const __grid_constant__ SsmProblem p, int vec, unsigned int *err
 #pragma unroll
         for (int i = 0; i < kRows; ++i) next[i] = page_of(r0 + step + i);
 #pragma unroll
-        for (int k = 0; k < kOwn; ++k) d[k] = step_size(d[k] + bias, p.softplus);
+        for (int k = 0; k < kOwn; ++k) d[k] = step_size<T>(d[k] + bias, p.softplus);
         float y[kRows];
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {

@@ -84,3 +84,61 @@ def test_steps_of_an_infinite_input(N, io):
     assert (S[1, 5] == float("inf")).all() and (h[1, 5] == float("inf")).all()
     o[1, 5] = want[1, 0, 5] = 0
     assert o.isfinite().all() and want.isfinite().all()
+
+
+@pytest.mark.parametrize("lo,hi", [(-80.0, -20.0), (-20.0, -5.0), (-5.0, 0.0), (0.0, 20.0)])
+def test_small_steps_keep_their_digits(lo, hi):
+    """Step sizes on their own: with A = 0, u = B = C = do = 1 the state after one token, and du, are the step. Whatever
+    the size of x, softplus(x) is off by the hardware's 2^x (2^-22 of the value, four U), by a rounding each of what the
+    argument's rounding left out, of the last two sums and of the polynomial's terms before (less than one U
+    together), and by its fit (a tenth of a U): eight U. (What the argument's rounding leaves out has an error of its own
+    of 2^-24 of 2^-19.)"""
+    from chunkwise_recurrent_prefill_gb300 import ssm_bwd, ssm_fwd, ssm_step
+    C = 4096
+    x = torch.linspace(lo, hi, C)
+    want = torch.logaddexp(x.double(), torch.zeros(C).double())
+    dt, one, A, b = x.cuda()[None, None], torch.ones(1, 1, C, device="cuda"), torch.zeros(C, 1, device="cuda"), \
+        torch.ones(1, 1, 1, 1, device="cuda")
+    hT = ssm_fwd(one, dt, A, b, b, return_state=True)[1]
+    S = torch.zeros(1, C, 1, device="cuda")
+    ssm_step(one[:, 0], dt[:, 0], A, b[:, 0], b[:, 0], S)
+    du = ssm_bwd(one, one, dt, A, b, b)[0]
+    for n, got in (("hT", hT), ("S", S), ("du", du)):
+        ref.close(n, got.view(C), want, 8 * ref.U * want)
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("off", [-float("inf"), torch.finfo(torch.bfloat16).min, -1e30])
+def test_tokens_that_a_mask_takes_out(off, io):
+    """dt of minus infinity, or the type's lowest value: steps of zero, which leave the state and have no gradient."""
+    from chunkwise_recurrent_prefill_gb300 import ssm_step
+    d = make(2, 29, 40, 1, 16, io, seed=2)
+    d["dt"][:, 5:] = off
+    t = {k: ref.gpu(v) for k, v in d.items()}
+    got = call(t)
+    want = ref.scan({**{k: v if k in ("A", "D", "dt_bias", "h0") else v[:, :5] for k, v in d.items() if k != "dhT"}}, io=io,
+                    back=False)
+    ref.close("hT", got["hT"], *want["hT"])
+    S = got["hT"].clone()
+    o = ssm_step(t["u"][:, 9], t["dt"][:, 9], t["A"], t["Bm"][:, 9], t["Cm"][:, 9], S, D=t["D"], z=t["z"][:, 9],
+                 dt_bias=t["dt_bias"])
+    assert torch.equal(S, got["hT"]) and not got["ddt"][:, 5:].any() and not got["dB"][:, 5:].any()
+    # (sums of N products in another order, of values below 100)
+    assert torch.allclose(o.float(), got["o"][:, 9].float(), rtol=2.0 ** -7 if io == "bf16" else 1e-5, atol=1e-4)
+    for n, v in got.items():
+        assert v.isfinite().all(), n
+
+
+def test_steps_that_are_not_finite():
+    """softplus of an infinity is one, and that of a NaN a NaN."""
+    from chunkwise_recurrent_prefill_gb300 import ssm_fwd, ssm_step
+    for io in ("bf16", "f32"):
+        T = torch.bfloat16 if io == "bf16" else torch.float32
+        one = torch.ones(1, 1, 3, device="cuda", dtype=T)
+        dt = torch.tensor([[[float("inf"), float("nan"), 3e38]]], device="cuda").to(T)
+        A, b = torch.zeros(3, 1, device="cuda"), torch.ones(1, 1, 1, 1, device="cuda", dtype=T)
+        A[0] = -1
+        S = torch.zeros(1, 3, 1, device="cuda")
+        ssm_step(one[:, 0], dt[:, 0], A, b[:, 0], b[:, 0], S)
+        for h in (ssm_fwd(one, dt, A, b, b, return_state=True)[1], S):
+            assert h[0, 0] == float("inf") and h[0, 1].isnan() and h[0, 2] == dt[0, 0, 2].float()
