@@ -79,7 +79,8 @@ def _shape(x, groups, eps, act, gate, dy=None) -> _NormShape:
         if t is not None and t.device != x.device:
             raise ValueError(f"{n}: on {t.device}, expected {x.device}")
         key.append(None if t is None else (t.shape, t.stride(), t.dtype))
-    return _plan(operator.index(groups), eps, act, *key)
+    # (eps by its value: a plan is not kept for a tensor that may change)
+    return _plan(operator.index(groups), ctypes.c_float(eps).value, act, *key)
 
 
 def _affine(x, weight, bias):

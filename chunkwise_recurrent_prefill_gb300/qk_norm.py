@@ -61,7 +61,8 @@ def _shape(q, k, norm, layout, eps, cos, *grads) -> _QkShape:
         _tensor(cos, "cos")
         if cos.dim() != 2:
             raise ValueError("cos must be [P, R / 2]")
-    return _plan(norm, layout, eps, None if cos is None else tuple(cos.shape), tuple(key))
+    # (eps by its value: a plan is not kept for a tensor that may change)
+    return _plan(norm, layout, ctypes.c_float(eps).value, None if cos is None else tuple(cos.shape), tuple(key))
 
 
 def _check_inputs(sh, q, k, wq, wk, cos, sin, positions):
