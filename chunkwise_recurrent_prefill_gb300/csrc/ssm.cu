@@ -78,12 +78,11 @@ __device__ __forceinline__ float scale_a(float a) {
 // 8 2^-24 whatever x is. bf16 calls, whose dt has 2^-9 |x| of the step to itself, do not pay for that.
 template <typename T>
 __device__ __forceinline__ float softplus(float x) {
-    const float t = fabsf(x) * -kLog2e;
+    const float a = fabsf(x), t = a * -kLog2e;
     float e = ex2(t);
-    if (sizeof(T) == 4) {
-        constexpr float kLog2eLow = 1.4426950408889634 - (double)kLog2e;
-        const float left = fmaf(fabsf(x), -kLog2eLow, fmaf(fabsf(x), -kLog2e, -t));
-        e = fmaf(e, fminf(left, 1.f) * kLn2, e);        // (infinite or NaN where x log2 e is not finite: e is 0)
+    if (sizeof(T) == 4) {       // e^(-a - t ln 2); where t is not finite that is infinite or NaN, and e is 0
+        constexpr float kLn2Low = 0.6931471805599453 - (double)kLn2;
+        e = fmaf(e, fminf(fmaf(t, -kLn2Low, -fmaf(t, kLn2, a)), 1.f), e);
     }
     float r = -0.003244024235755205f;
     r = fmaf(r, e, 0.019851457327604294f);
@@ -729,7 +728,7 @@ ssm_bwd_kernel(const __grid_constant__ SsmProblem p, const __grid_constant__ Map
     };
     if (w != p.stall) fetch(w, 0);
     for (int step = w; step < steps; step += W) {
-        const int ch = last - step, t0 = ch * kTok;
+        const int ch = last - step, t0 = ch * kTok, left = (int)p.T - t0;
         const float4 *mark = marks + ((at.b * chunks + ch) * tl.all + at.tile) * Q * 32 + lane;
         float4 mk;                  // a step's states come while the one before is worked on
         if (!kEnd) mk = mark[0];
@@ -832,12 +831,12 @@ ssm_bwd_kernel(const __grid_constant__ SsmProblem p, const __grid_constant__ Map
                 store4(to.slot + 512 * q, G);
                 hand_over(to.bar + 8 * q, lane);
                 // (tokens that do not exist have no part in dA: a last state that is not finite times their d of 0 is NaN)
-                if (p.T - t0 < kTok) {
+                if (left < kTok) {
 #pragma unroll
                     for (int i = 1; i < kTok; ++i)
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
-                            if (i >= p.T - t0) (i % 2 ? s[j][i / 2].x : s[j][i / 2 - 1].y) = 0.f;
+                            if (i >= left) (i % 2 ? s[j][i / 2].x : s[j][i / 2 - 1].y) = 0.f;
                 }
                 float2 dA[4];
 #pragma unroll
