@@ -142,3 +142,26 @@ def test_steps_that_are_not_finite():
         ssm_step(one[:, 0], dt[:, 0], A, b[:, 0], b[:, 0], S)
         for h in (ssm_fwd(one, dt, A, b, b, return_state=True)[1], S):
             assert h[0, 0] == float("inf") and h[0, 1].isnan() and h[0, 2] == dt[0, 0, 2].float()
+
+
+def test_gradients_of_more_than_32_bits_of_elements():
+    """The last tokens' gradients, of inputs past 2^31 elements, against those of the same tokens on their own."""
+    from chunkwise_recurrent_prefill_gb300 import last_device_status, ssm_bwd, ssm_fwd
+    T, C, N = (1 << 20) + 11, 2080, 8
+    g = torch.Generator("cuda").manual_seed(2)
+    u, dt, z, do = (torch.empty(1, T, C, device="cuda", dtype=torch.bfloat16).normal_(generator=g) for _ in range(4))
+    Bm, Cm = (torch.randn(1, T, 1, N, device="cuda", generator=g).bfloat16() for _ in range(2))
+    A = -torch.rand(C, N, device="cuda", generator=g) - 0.5
+    cut = T - 1000
+    du, ddt, _, dBm, dCm, _, dz, _, _ = ssm_bwd(do, u, dt, A, Bm, Cm, z=z)
+    whole = [x[:, cut:].clone() for x in (du, ddt, dBm, dCm, dz)]
+    del du, ddt, dz
+    head = [x[:, :cut] for x in (u, dt)] + [A] + [x[:, :cut] for x in (Bm, Cm)]
+    h = ssm_fwd(*head, return_state=True)[1]
+    part = [x[:, cut:].contiguous() for x in (u, dt)] + [A] + [x[:, cut:].contiguous() for x in (Bm, Cm)]
+    own = ssm_bwd(do[:, cut:].contiguous(), *part, z=z[:, cut:].contiguous(), h0=h)
+    assert last_device_status() == 0
+    # the same operations but for where a chunk ends, each rounded to bf16
+    for n, a, b in zip(("du", "ddt", "dB", "dC", "dz"), whole, (own[0], own[1], own[3], own[4], own[6])):
+        a, b = a.float(), b.float()
+        assert ((a - b).abs() <= 2.0 ** -7 * b.abs() + 1e-3 * b.square().mean().sqrt()).all(), n
