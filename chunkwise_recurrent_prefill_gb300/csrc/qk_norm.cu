@@ -182,7 +182,7 @@ qk_plain_bwd(const __grid_constant__ QkProblem p, float *part, unsigned int *err
 // kHeads heads of 32 / W tokens (at most 4 KB), which TMA brings while the items before it are worked on: what is on its
 // way does not cost registers. The heads of a token share its angles, in registers; a CTA keeps to the same heads, so
 // that weights are loaded once.
-// Measured: 16384 tokens of 16 + 4 heads of 128, bf16 (177 MB): 34.6 us, 5.1 TB/s; gradients of 8 x 1023 tokens of 16 + 16
+// Measured: 16384 tokens of 16 + 4 heads of 128, bf16 (177 MB): 34.6 us, 5.1 TB/s (fp32 58 us, 5.9); gradients of 8 x 1023 tokens of 16 + 16
 // heads of 64 (102 MB): 22.4 us with the sums. Items in registers instead, without packed arithmetic: 37.8 and 27.4.
 // Heads of an item: 2 forward 40.4, 8 50.2; backward 1 26.9, 4 29.6. Three items ahead 35.5, three CTAs to an SM
 // 37.2; all heads of a token to warps side by side 35.2 and 26.8 (more addresses, and sums of both weights in each CTA).

@@ -17,14 +17,15 @@
 // Forward, pairs of packed arithmetic are two states of a token. What a warp does between the state's arrival
 // and its hand-over sets the ring's rate, and so it is 16 instructions for 4 states of 8 tokens; each token's d and d u are
 // needed twice side by side, which costs the moves that the walk saves (16384 tokens of 4096 channels, bf16, 16 states,
-// inputs and outputs 539 MB: 423 us, 448 with pairs of tokens). Backward, where registers are few, pairs are two
+// inputs and outputs 539 MB: 411 us; when it was built 423, and 448 with pairs of tokens). Backward, where registers are few, pairs are two
 // tokens of a state: step sizes, inputs, B, C and sums are pairs as they come, and only the walk is scalar.
 //
-// Bound: 16 exponentials of a token and channel take 64 cycles of a scheduler's share of the special function
-// units, the four multiply-adds of each state 64 of its FP32 pipe; in the backward pass thirteen of them 208. Forward
-// that is 172 us of the 423: a chunk comes every 400 cycles, of which its instructions take 250 and the rest is the
-// hand-over. Gradients (4 x 2047 tokens of 2048 channels) take 437 us, 343 of them in the backward kernel, whose two
-// warps to a scheduler (255 registers) issue half of the time.
+// Bound: 16 exponentials of a token of 32 channels take 64 cycles of a scheduler's share of the special function
+// units, the four multiply-adds of each state 64 of its FP32 pipe; in the backward pass thirteen of them 208. Forward, on
+// all 608 schedulers at 2.07 GHz, that is 107 us of the 411. What bounds it is the shared-memory data pipe: on its SM a
+// chunk comes every 415 cycles, in 337 of which (82 %) that pipe moves a wavefront, most of them the reads of B, C, d u
+// and d in each of the four steps. Gradients (4 x 2047 tokens of 2048 channels) have 87 us of multiply-adds and take 437, 345 of
+// them in the backward kernel, whose two warps to a scheduler (255 registers) issue half of the time.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -497,7 +498,7 @@ ssm_fwd_kernel(const __grid_constant__ SsmProblem p, const __grid_constant__ Map
     const size_t stage_bytes = R::stage_bytes(kIn, row);
     auto stage = [&](int k) { return reinterpret_cast<T *>(ring.stage + (2 * w + k) * stage_bytes); };
     // d u of a chunk, and with outputs d: in registers d costs moves, as 128 are few (walks of no outputs have some left:
-    // the marks of 4 x 2047 tokens of 2048 channels 92 us, 83 with d in registers; outputs of 16384 x 4096 419, 549)
+    // the marks of 4 x 2047 tokens of 2048 channels 92 us, 83 with d in registers; outputs of 16384 x 4096 411, 549 when they were)
     using DX = std::conditional_t<kOut, float4, float2>;
     DX *dx = reinterpret_cast<DX *>(ring.stage + 2 * W * stage_bytes) + w * kPairs * kCh * 32 + lane;
     const int64_t chunks = (p.T + kTok - 1) / kTok;
@@ -1030,8 +1031,10 @@ ssm_sums_kernel(const __grid_constant__ SsmProblem p, const Parts parts, const T
 // One token of each row on the pages of a pool. kLanes lanes (4 kLanes >= N) own a channel, four states each, and keep
 // its row of A while they go through rows of the batch, kRows at a time: all that these need is on its way
 // together, and the page numbers of the next ones. A row's step size and output are made by one of the lanes. The
-// states are read and written once: HBM bandwidth bounds a batch. Measured: 240 rows of 4096 channels of 16 states
-// (134 MB) 28 us a call, 4.8 TB/s; with the loads of a row behind those of the row before, 61.
+// states are read and written once. Measured: 240 rows of 4096 channels of 16 states (134 MB) 32 us a call, 26 in a graph
+// where the pool (75 MB) stays in L2, and 30, 4.5 TB/s, on pages anywhere in 2 GB; with the loads of a row behind
+// those of the row before, 61 a call. A CTA loads, computes and stores in turn, so its loads pause while it
+// computes: latency bounds it before HBM does.
 template <typename T, int kLanes>
 __global__ void __launch_bounds__(256, 3)
 ssm_step_kernel(const __grid_constant__ SsmProblem p, int vec, unsigned int *err) {
@@ -1282,8 +1285,8 @@ int bwd_channels(const SsmProblem &p) {
 // Segments of a sequence for CTAs of 32 ch channels. Cutting it costs two thirds of a walk more (and the join), so it is
 // done where the tiles leave more than half of the SMs idle; the segments then make one round of resident CTAs (two to
 // an SM forward, one backward), or two rounds if those are better filled. Measured, 16384 tokens: forward, 512
-// channels 98 us against 421 uncut, 2048 channels 348 against 423, 2560 channels 424 uncut against 446 at best;
-// gradients, 1024 channels 606 us against 3364, 4864 channels of 8192 tokens 1272 against 1723.
+// channels 88 us against 406 uncut, 2048 channels 330 against 408, 2560 channels 408 uncut against 481 in three;
+// gradients, 1024 channels 575 us against 3266, 4864 channels of 8192 tokens 1216 against 1681.
 Split split_of(const SsmProblem &p, int ch, bool backward, int splits, int num_sms) {
     const int64_t chunks = (p.T + kTok - 1) / kTok, ctas = p.B * tiles_of(p.C, p.G, ch).all;
     const int64_t round = backward ? num_sms : 2 * num_sms, most = chunks / (backward ? 16 : 8);

@@ -480,7 +480,8 @@ size_t gla_pages_workspace_size(int64_t P, int64_t R, int64_t M, int64_t n);
  * arithmetic and sums in fp32. All of it is deterministic: no atomics. A NaN or an infinity reaches
  * what the formulas let it reach, and nothing else; but an infinity of a channel of ssm_* may become
  * a NaN of the same channel (of that token and, through the state, of those after it) where N is not
- * a multiple of 4 or the sequence is cut into parts.
+ * a multiple of 4 or the sequence is cut into parts, and an infinity of B or C a NaN of dB and dC, whose
+ * sums over channels may take in channels that do not exist.
  */
 typedef struct {
     int64_t b, t;           /* element strides of the batch and token dimension; both zero = contiguous */
