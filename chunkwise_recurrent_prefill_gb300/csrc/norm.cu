@@ -112,7 +112,7 @@ using tc::mul2;
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
 // The logistic function 1 / (1 + 2^(-u log2 e)). Results that are rounded to bf16 take the hardware's
-// approximate exponential and reciprocal (a few 2^-22 of the value), flushing denormals: the exact
+// approximate exponential and reciprocal (a few 2^-22 of the value, where u < 0 another 2^-23 |u|), flushing denormals: the exact
 // functions, and even the fast ones with their care for denormals, made the kernels bound by issue.
 template <typename T>
 __device__ __forceinline__ float logistic(float u) {

@@ -15,7 +15,7 @@
 // that a forward walk left at the start of each chunk.
 //
 // Forward, pairs of packed arithmetic are two states of a token. What a warp does between the state's arrival
-// and its hand-over sets the ring's rate, and so it is 16 instructions for 4 states of 8 tokens; each token's d and d u are
+// and its hand-over is all that is serial, and so it is 16 instructions for 4 states of 8 tokens; each token's d and d u are
 // needed twice side by side, which costs the moves that the walk saves (16384 tokens of 4096 channels, bf16, 16 states,
 // inputs and outputs 539 MB: 411 us; when it was built 423, and 448 with pairs of tokens). Backward, where registers are few, pairs are two
 // tokens of a state: step sizes, inputs, B, C and sums are pairs as they come, and only the walk is scalar.
@@ -76,7 +76,7 @@ __device__ __forceinline__ float scale_a(float a) {
 // their constants into registers.)
 // e takes its error from 2^x (2^-22) and from the rounding of x log2 e, which is |x| 2^-24 of the value (6e-7 of the step at
 // x = -7, 1e-6 at -12, 4e-6 at -60). fp32 calls put back what the rounding left out, to first order: their steps are good to
-// 8 2^-24 whatever x is. bf16 calls, whose dt has 2^-9 |x| of the step to itself, do not pay for that.
+// 8 2^-24 whatever x is (16384 tokens of 4096 channels 464 us, 458 without). bf16 calls, whose dt has 2^-9 |x| of the step to itself, do not pay for that.
 template <typename T>
 __device__ __forceinline__ float softplus(float x) {
     const float a = fabsf(x), t = a * -kLog2e;
